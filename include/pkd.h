@@ -145,6 +145,18 @@ typedef struct pkd_config {
  * page size a multiple of 16; combinable with PKD_FLAG_HND and
  * PKD_FLAG_MMA_CONSUMER only. */
 #define PKD_FLAG_CASCADE 256u
+/* Latent cache: kv is bf16 [num_pages][P][576], one row per token shared by
+ * every query head -- 512 latent columns, then 64 columns of the rotary key --
+ * and q is bf16 [batch][Hq][576], the queries with the key up-projection
+ * absorbed.  pkd_run returns, for every head,
+ *     out [batch][Hq][512] = softmax(k_scale * q . row) x the rows' latent columns
+ * (the value up-projection is the caller's, after it) and the lse of those
+ * scores; the softmax scale is k_scale itself, since 576 is not the width the
+ * heads were trained with (pkd_run's is 1: use pkd_run_scaled).  head_dim 512,
+ * num_kv_heads 1, 1 <= Hq <= 128, page size a multiple of 16; combinable with
+ * PKD_FLAG_CHUNK_SEARCH only.  Plans are pkd_plan's; a work item covers up to
+ * 64 heads.  Graphs replay with the batch they were captured with. */
+#define PKD_FLAG_LATENT 1024u
 
 typedef struct pkd_ctx pkd_ctx;
 typedef struct pkd_graph pkd_graph;
@@ -357,6 +369,24 @@ int pkd_append_kv_layers(int32_t layers, const void *const *k_new, const void *c
                          const int32_t *indices, const int32_t *last_page_len, int32_t batch,
                          int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
                          int32_t head_dim, uint32_t flags, int32_t *err, void *stream);
+
+/* Write n new tokens' rows into a latent cache (PKD_FLAG_LATENT): token i's
+ * row is latent_new[i] (512 bf16) then rope_new[i] (64 bf16), the slot rule
+ * and the table are pkd_append_kv's.  Rows of latent_new / rope_new start
+ * latent_stride / rope_stride ELEMENTS apart (multiples of 8, at least the
+ * row's width, or anything when n is 1): both may be column ranges of one
+ * projection's output.  The inputs must not overlap the cache.
+ *   latent_new, rope_new : device bf16, 16-byte aligned
+ *   cache                : device bf16 [num_pages][P][576], 16-byte aligned
+ * Two tokens with the same slot leave one of the two rows there.  Tokens
+ * outside the table are skipped and flagged in *err as by pkd_append_kv.
+ * Errors: INVALID_ARG, CUDA. */
+int pkd_append_latent(const void *latent_new, int64_t latent_stride, const void *rope_new,
+                      int64_t rope_stride, const int32_t *batch_indices,
+                      const int32_t *positions, int32_t n, const int32_t *indptr,
+                      const int32_t *indices, const int32_t *last_page_len, int32_t batch,
+                      void *cache, int32_t num_pages, int32_t page_size, int32_t *err,
+                      void *stream);
 
 /* Self-test of the device-side bounded waits (failure detection without a
  * GPU fault; FlashInfer, in depth, "Failure modes in production": errors come

@@ -17,6 +17,8 @@ API (names follow the pages' plan / run / merge_states):
 * :func:`merge_states` -- exact LSE merge of two attention states.
 * :func:`append_kv` -- write a step's new K / V rows into their page slots.
 * :func:`plan_host` -- the scheduler alone on the host (no GPU), for tests.
+* :class:`BatchLatentDecodeWithPagedCache`, :func:`append_latent` -- the same
+  plan / run / append over a cache of one latent vector per token.
 * ``cascade=True`` contexts: ``plan_cascade(group_indptr, prefix, suffix)``
   plans a shared prefix and every request's own suffix together; ``run``
   returns attention over both, merged.
@@ -30,8 +32,9 @@ import os
 import numpy as np
 
 __all__ = [
-    "build", "load", "PkdError", "BatchDecodeWithPagedKVCache", "merge_states", "append_kv",
-    "append_kv_layers", "plan_host", "plan_host_shared", "plan_host_cascade", "advise_format",
+    "build", "load", "PkdError", "BatchDecodeWithPagedKVCache",
+    "BatchLatentDecodeWithPagedCache", "merge_states", "append_kv",
+    "append_kv_layers", "append_latent", "plan_host", "plan_host_shared", "plan_host_cascade", "advise_format",
     "schedule_layout",
     "selftest_bounded_wait", "Graph",
     "STATUS",
@@ -59,8 +62,12 @@ EXPORTS = (
     "pkd_graph_destroy", "pkd_status_str", "pkd_version", "pkd_run_static_scratch",
     "pkd_append_kv", "pkd_append_kv_ex", "pkd_plan_shared", "pkd_plan_host_shared", "pkd_run_scaled",
     "pkd_selftest_bounded_wait", "pkd_append_kv_layers", "pkd_static_scratch_last_error",
-    "pkd_plan_cascade", "pkd_plan_host_cascade", "pkd_advise_format",
+    "pkd_plan_cascade", "pkd_plan_host_cascade", "pkd_advise_format", "pkd_append_latent",
 )
+
+
+LATENT_DIM = 512   # columns of a latent row that are key and value
+LATENT_ROPE = 64   # rotary key columns behind them
 
 
 class PkdError(RuntimeError):
@@ -163,6 +170,9 @@ def load():
         "pkd_append_kv_layers": (ctypes.c_int, [i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32,
                                                 i32, i32, i32, i32, ctypes.c_uint32, vp, vp]),
     }
+    i64 = ctypes.c_int64
+    sig["pkd_append_latent"] = (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i32, vp, vp, vp, i32, vp,
+                                               i32, i32, vp, vp])
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
         f.restype = res
@@ -207,6 +217,7 @@ FLAG_ROW_COPIES = 16    # force one KV copy per token row (no page-tile tensor m
 FLAG_CHUNK_SEARCH = 64  # chunk = largest page multiple still giving >= N_CTA items
 FLAG_HND = 32           # cache layout [pages, 2, Hkv, P, D] instead of NHD [pages, 2, P, Hkv, D]
 FLAG_DENSE_PREFIX = 128  # shared prefix on tcgen05 tensor cores: 128-row tiles, one KV head per item
+FLAG_LATENT = 1024      # latent cache [pages, P, 576] shared by every query head
 FLAG_CASCADE = 256      # both levels of a shared-prefix step in one plan, one launch, one merge
 
 
@@ -434,8 +445,14 @@ class BatchDecodeWithPagedKVCache:
             raise ValueError("chunk_rule must be 'closed' or 'search'")
         if chunk_rule == "search":
             flags |= FLAG_CHUNK_SEARCH
-        self.cfg = make_config(num_qo_heads, num_kv_heads, head_dim, page_size, max_batch,
-                               max_num_pages, num_pages, alpha, min_chunk_tokens, num_ctas, flags)
+        self._create(make_config(num_qo_heads, num_kv_heads, head_dim, page_size, max_batch,
+                                 max_num_pages, num_pages, alpha, min_chunk_tokens, num_ctas,
+                                 flags))
+
+    def _create(self, cfg):
+        import torch
+        self.cfg = cfg
+        lib = load()
         with torch.cuda.device(self.device):
             nbytes = lib.pkd_workspace_bytes(ctypes.byref(self.cfg))
             if nbytes == 0:
@@ -701,6 +718,83 @@ class BatchDecodeWithPagedKVCache:
             pass
 
 
+class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
+    """Decode attention over a paged cache of latent vectors: one row of
+    ``latent_dim + rope_dim`` values per token, shared by every query head
+    (the key up-projection absorbed into the queries, the value up-projection
+    left to the caller).
+
+    ``run(q, cache)`` with q ``[batch, heads, 576]`` and cache ``[pages, P,
+    576]``, both bf16, returns out ``[batch, heads, 512]`` = softmax(scale *
+    q . row) x the rows' first 512 columns, and the lse.  ``scale`` is the
+    softmax scale of the heads before absorption, e.g. 1 / sqrt(their width).
+    1 to 128 heads, latent_dim 512, rope_dim 64, page size a multiple of 16.
+    plan / capture / device_error as in :class:`BatchDecodeWithPagedKVCache`;
+    a captured graph replays with the batch it was captured with.
+    """
+
+    def __init__(self, num_heads, latent_dim, rope_dim, page_size, *, scale, max_batch,
+                 max_num_pages, num_pages, alpha=-1, min_chunk_tokens=-1, num_ctas=0,
+                 chunk_rule="closed", device=None):
+        import math
+        import torch
+        if (latent_dim, rope_dim) != (LATENT_DIM, LATENT_ROPE):
+            raise PkdError(-3, f"latent_dim {LATENT_DIM} and rope_dim {LATENT_ROPE} are supported")
+        if not math.isfinite(scale):
+            raise ValueError("scale must be finite")
+        if chunk_rule not in ("closed", "search"):
+            raise ValueError("chunk_rule must be 'closed' or 'search'")
+        self.device = torch.device("cuda" if device is None else device)
+        self.hq, self.hkv, self.d, self.p = num_heads, 1, latent_dim, page_size
+        self.num_pages, self.scale = num_pages, float(scale)
+        self.kv_dtype, self.kv_layout = "bf16", "latent"
+        self._create(make_config(num_heads, 1, latent_dim, page_size, max_batch, max_num_pages,
+                                 num_pages, alpha, min_chunk_tokens, num_ctas,
+                                 FLAG_LATENT | (FLAG_CHUNK_SEARCH if chunk_rule == "search" else 0)))
+
+    def _check_run_args(self, q, kv_cache, out, lse):
+        import torch
+        if self.batch is None:
+            raise PkdError(-5, "run before plan")
+        B, row = self.batch, LATENT_DIM + LATENT_ROPE
+        dev = q.device
+        for name, t, dt, shape in (("q", q, torch.bfloat16, (B, self.hq, row)),
+                                   ("cache", kv_cache, torch.bfloat16,
+                                    (self.num_pages, self.p, row)),
+                                   ("out", out, torch.bfloat16, (B, self.hq, self.d)),
+                                   ("lse", lse, torch.float32, (B, self.hq))):
+            if t is None:
+                continue
+            if t.dtype != dt:
+                raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} shape {tuple(t.shape)} != {shape}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if not t.is_cuda or t.device != dev or self.device.index not in (None, dev.index):
+                raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
+
+    def run(self, q, cache, out=None, lse=None, return_lse=True, expect_epoch=0, stream=None):
+        """Attention for one layer.  Returns (out, lse) or out."""
+        import torch
+        if out is None:
+            out = torch.empty(*q.shape[:-1], self.d, dtype=torch.bfloat16, device=q.device)
+        return super().run(q, cache, out=out, lse=lse, return_lse=return_lse,
+                           expect_epoch=expect_epoch, stream=stream, k_scale=self.scale)
+
+    def capture(self, qs, caches, outs, lses=None, timing=False, host_qs=None, host_outs=None,
+                host_lses=None) -> Graph:
+        """Capture one decode step over all layers in a graph."""
+        return super().capture(qs, caches, outs, lses, timing=timing,
+                               kv_scales=[(self.scale, 1.0)] * len(qs), host_qs=host_qs,
+                               host_outs=host_outs, host_lses=host_lses)
+
+    def plan_shared(self, *args, **kwargs):
+        raise PkdError(-1, "a latent context plans requests of their own (plan)")
+
+    plan_cascade = plan_shared
+
+
 def selftest_bounded_wait(mode=0, device=None):
     """Run the device-side bounded-wait self-test (see pkd_selftest_bounded_wait)
     and wait for it.  Returns (error bits, [wait 0 ns, wait 1 ns])."""
@@ -843,3 +937,60 @@ def append_kv_layers(k_news, v_news, batch_indices, positions, indptr, indices, 
         flags, ctypes.c_void_p(err.data_ptr() if err is not None else 0), _stream_ptr(stream))
     _check(st, "pkd_append_kv_layers")
     return kv_caches
+
+
+def append_latent(latent_new, rope_new, batch_indices, positions, indptr, indices, last_page_len,
+                  cache, err=None, stream=None):
+    """Write new tokens' latent rows into their page slots: token i's row is
+    latent_new[i] then rope_new[i].
+
+    latent_new [n, 512], rope_new [n, 64]: bf16, last dimension contiguous,
+    rows of any stride that is a multiple of 8 elements (they may be column
+    ranges of one projection's output); cache: bf16 [pages, P, 576], written
+    in place, not overlapping the inputs.  The table arguments and err are
+    append_kv's."""
+    import torch
+    bf = torch.bfloat16
+    for name, t, dt in (("cache", cache, bf), ("batch_indices", batch_indices, torch.int32),
+                        ("positions", positions, torch.int32), ("indptr", indptr, torch.int32),
+                        ("indices", indices, torch.int32),
+                        ("last_page_len", last_page_len, torch.int32)):
+        if t.dtype != dt or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous CUDA {dt} tensor")
+    if cache.dim() != 3 or cache.shape[2] != LATENT_DIM + LATENT_ROPE:
+        raise ValueError(f"cache must be [pages, P, {LATENT_DIM + LATENT_ROPE}]")
+    n = int(batch_indices.numel())
+    for name, t, width in (("latent_new", latent_new, LATENT_DIM),
+                           ("rope_new", rope_new, LATENT_ROPE)):
+        if t.dtype != bf or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA {bf} tensor")
+        if tuple(t.shape) != (n, width):
+            raise ValueError(f"{name} must be [{n}, {width}]")
+        if n and (t.stride(1) != 1 or (n > 1 and (t.stride(0) < width or t.stride(0) % 8))
+                  or t.data_ptr() % 16):
+            raise ValueError(f"{name}: contiguous rows on 16-byte boundaries are needed")
+    if positions.numel() != n:
+        raise ValueError("batch_indices and positions need one entry per new token")
+    batch = int(last_page_len.numel())
+    if indptr.numel() != batch + 1:
+        raise ValueError("indptr must have batch + 1 entries")
+    if err is not None and (err.dtype != torch.int32 or not err.is_cuda):
+        raise TypeError("err must be an int32 CUDA tensor")
+    _one_device(cache, latent_new, rope_new, batch_indices, positions, indptr, indices,
+                last_page_len, err)
+    with torch.cuda.device(cache.device):
+        st = load().pkd_append_latent(
+            latent_new.data_ptr(), latent_new.stride(0), rope_new.data_ptr(), rope_new.stride(0),
+            batch_indices.data_ptr(), positions.data_ptr(), n, indptr.data_ptr(),
+            indices.data_ptr(), last_page_len.data_ptr(), batch, cache.data_ptr(),
+            int(cache.shape[0]), int(cache.shape[1]), err.data_ptr() if err is not None else 0,
+            _stream_ptr(stream))
+    _check(st, "pkd_append_latent")
+    return cache
+
+
+def _one_device(*tensors):
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")

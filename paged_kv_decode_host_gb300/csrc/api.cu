@@ -67,8 +67,11 @@ bool valid_group(int g) { return g == 1 || g == 2 || g == 4 || g == 8; }
 bool valid_flags(uint32_t f) {
   const uint32_t known = PKD_FLAG_FMA_CONSUMER | PKD_FLAG_MMA_CONSUMER | PKD_FLAG_SHARED_PREFIX |
                          PKD_FLAG_KV_FP8 | PKD_FLAG_ROW_COPIES | PKD_FLAG_CHUNK_SEARCH |
-                         PKD_FLAG_HND | PKD_FLAG_DENSE_PREFIX | PKD_FLAG_CASCADE;
+                         PKD_FLAG_HND | PKD_FLAG_DENSE_PREFIX | PKD_FLAG_CASCADE |
+                         PKD_FLAG_LATENT;
   if (f & ~known) return false;
+  // a latent cache has one layout, one type and a kernel of its own
+  if ((f & PKD_FLAG_LATENT) && (f & ~(PKD_FLAG_LATENT | PKD_FLAG_CHUNK_SEARCH))) return false;
   // a cascade context runs both of its levels itself: bf16 page tiles,
   // tensor cores, either layout
   if ((f & PKD_FLAG_CASCADE) && (f & ~(PKD_FLAG_CASCADE | PKD_FLAG_MMA_CONSUMER | PKD_FLAG_HND)))
@@ -91,6 +94,13 @@ int check_config(const pkd_config* c) {
   if (c->max_batch < 0 || c->max_num_pages < 0 || c->num_pages < 1 || c->page_size < 1 ||
       c->num_ctas < 0)
     return PKD_E_INVALID_ARG;
+  if (c->flags & PKD_FLAG_LATENT) {
+    // every head reads the same rows; pages are read in 16-token tiles
+    if (c->head_dim != kLatentDim || c->num_kv_heads != 1 || c->num_qo_heads < 1 ||
+        c->num_qo_heads > kLatentMaxHeads || c->page_size % 16 != 0 || c->page_size > 1 << 20)
+      return PKD_E_UNSUPPORTED_SHAPE;
+    return PKD_OK;
+  }
   if (c->head_dim != kHeadDim) return PKD_E_UNSUPPORTED_SHAPE;
   if (c->num_kv_heads < 1 || c->num_kv_heads > kMaxKvHeads) return PKD_E_UNSUPPORTED_SHAPE;
   if (c->num_qo_heads < 1 || c->num_qo_heads % c->num_kv_heads != 0)
@@ -112,6 +122,13 @@ int check_config(const pkd_config* c) {
 // shape; with a null probe the check is skipped).
 DecodeKind kind_for(const pkd_config* c, const void* probe_address) {
   DecodeKind k;
+  if (c->flags & PKD_FLAG_LATENT) {
+    k.latent = true;
+    CUtensorMap m;
+    k.tmap = probe_address == nullptr ||
+             encode_latent_map(probe_address, c->num_pages, c->page_size, &m) == cudaSuccess;
+    return k;
+  }
   k.group = c->num_qo_heads / c->num_kv_heads;
   k.mma = use_mma_consumer(k.group, c->flags);
   k.block = (c->flags & PKD_FLAG_SHARED_PREFIX) != 0;
@@ -132,7 +149,8 @@ DecodeKind kind_for(const pkd_config* c, const void* probe_address) {
 }
 
 int resolve_ctas(const pkd_config* c, const DecodeKind& k, int32_t* n_cta, int* smem_bytes) {
-  *smem_bytes = decode_smem_bytes(c->num_kv_heads, k);
+  *smem_bytes = k.latent ? latent_smem_bytes(c->num_qo_heads)
+                         : decode_smem_bytes(c->num_kv_heads, k);
   if (c->num_ctas > 0) {
     *n_cta = c->num_ctas;
     return PKD_OK;
@@ -141,8 +159,10 @@ int resolve_ctas(const pkd_config* c, const DecodeKind& k, int32_t* n_cta, int* 
   if (cudaGetDevice(&dev) != cudaSuccess) return PKD_E_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PKD_E_CUDA;
-  if (decode_prepare(k, *smem_bytes) != cudaSuccess) return PKD_E_CUDA;
-  if (decode_occupancy(k, c->num_kv_heads, *smem_bytes, &per_sm) != cudaSuccess)
+  if ((k.latent ? latent_prepare(c->num_qo_heads) : decode_prepare(k, *smem_bytes)) != cudaSuccess)
+    return PKD_E_CUDA;
+  if ((k.latent ? latent_occupancy(c->num_qo_heads, &per_sm)
+                : decode_occupancy(k, c->num_kv_heads, *smem_bytes, &per_sm)) != cudaSuccess)
     return PKD_E_CUDA;
   if (per_sm < 1) return PKD_E_UNSUPPORTED_SHAPE;
   *n_cta = sms * per_sm;
@@ -163,8 +183,10 @@ int kv_map_for(pkd_ctx* ctx, const void* kv, CUtensorMap* out, CUtensorMap* out_
   e.kv = kv;
   const pkd_config& c = ctx->cfg;
   const bool hnd = (c.flags & PKD_FLAG_HND) != 0;
-  if (encode_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads, ctx->kind.fp8, hnd,
-                    ctx->kind.dense, &e.map) != cudaSuccess)
+  if ((ctx->kind.latent ? encode_latent_map(kv, c.num_pages, c.page_size, &e.map)
+                        : encode_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads,
+                                        ctx->kind.fp8, hnd, ctx->kind.dense, &e.map)) !=
+      cudaSuccess)
     return PKD_E_CUDA;
   if (ctx->kind.cascade &&
       encode_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads, false, hnd, true,
@@ -182,9 +204,54 @@ int kv_map_for(pkd_ctx* ctx, const void* kv, CUtensorMap* out, CUtensorMap* out_
   return PKD_OK;
 }
 
+// pkd_run of a latent context.
+int launch_latent_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, float* lse,
+                      float scale, float v_scale, cudaStream_t stream, cudaEvent_t ev_before,
+                      cudaEvent_t ev_after, int32_t wait_epoch) {
+  const pkd_config& c = ctx->cfg;
+  LatentArgs a{};
+  a.sched = reinterpret_cast<const int32_t*>(ctx->ws);
+  a.o_part = reinterpret_cast<float*>(ctx->ws + ctx->layout.o_part_byte);
+  a.l_part = reinterpret_cast<float*>(ctx->ws + ctx->layout.l_part_byte);
+  a.err = reinterpret_cast<int32_t*>(ctx->ws + ctx->layout.err_byte);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.off_cta = ctx->layout.cta_indptr;
+  a.off_items = ctx->layout.items;
+  a.off_pages = ctx->layout.page_list;
+  a.off_units = ctx->layout.units;
+  a.off_merge = ctx->layout.merge_indptr;
+  a.heads = c.num_qo_heads;
+  a.blocks = latent_blocks(c.num_qo_heads);
+  a.page_size = c.page_size;
+  a.num_pages = c.num_pages;
+  a.scale_log2 = (float)(1.4426950408889634 * (double)scale);
+  a.v_scale = v_scale;
+  a.wait_epoch = wait_epoch;
+  if (ctx->info.batch > 0) {
+    const int st = kv_map_for(ctx, kv, &a.kv_map);
+    if (st != PKD_OK) return st;
+    if (encode_latent_q_map(q, ctx->info.batch, c.num_qo_heads, &a.q_map) != cudaSuccess)
+      return PKD_E_CUDA;
+  }
+  if (ev_before && cudaEventRecordWithFlags(ev_before, stream, cudaEventRecordExternal) != cudaSuccess)
+    return PKD_E_CUDA;
+  // the merge has nothing to do when no request is split; a captured launch
+  // must follow later plans, whose splits are not known yet
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PKD_E_CUDA;
+  const bool merge = ctx->info.num_units > 0 || cap != cudaStreamCaptureStatusNone;
+  return launch_latent(a, ctx->n_cta, ctx->merge_grid, merge, ev_after, stream) == cudaSuccess
+             ? PKD_OK
+             : PKD_E_CUDA;
+}
+
 int launch_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, float* lse,
                float k_scale, float v_scale, cudaStream_t stream, cudaEvent_t ev_before,
                cudaEvent_t ev_after, int32_t wait_epoch = 0) {
+  if (ctx->kind.latent)
+    return launch_latent_run(ctx, q, kv, out, lse, k_scale, v_scale, stream, ev_before, ev_after,
+                             wait_epoch);
   const pkd_config& c = ctx->cfg;
   DecodeArgs a{};
   a.wait_epoch = wait_epoch;
@@ -366,7 +433,7 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
   if (!ctx) return PKD_E_INVALID_ARG;
   ctx->cfg = *cfg;
   ctx->kind = kind_for(cfg, d_workspace);
-  if ((ctx->kind.dense || ctx->kind.cascade) && !ctx->kind.tmap) {   // the driver refused a map
+  if ((ctx->kind.dense || ctx->kind.cascade || ctx->kind.latent) && !ctx->kind.tmap) {   // the driver refused a map
     delete ctx;
     return PKD_E_UNSUPPORTED_SHAPE;
   }
@@ -375,7 +442,8 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
     delete ctx;
     return st;
   }
-  if (decode_prepare(ctx->kind, ctx->smem_bytes) != cudaSuccess) {
+  if ((ctx->kind.latent ? latent_prepare(cfg->num_qo_heads)
+                        : decode_prepare(ctx->kind, ctx->smem_bytes)) != cudaSuccess) {
     delete ctx;
     return PKD_E_CUDA;
   }
@@ -622,6 +690,30 @@ int pkd_append_kv_layers(int32_t layers, const void* const* k_new, const void* c
   return PKD_OK;
 }
 
+int pkd_append_latent(const void* latent_new, int64_t latent_stride, const void* rope_new,
+                      int64_t rope_stride, const int32_t* batch_indices, const int32_t* positions,
+                      int32_t n, const int32_t* indptr, const int32_t* indices,
+                      const int32_t* last_page_len, int32_t batch, void* cache, int32_t num_pages,
+                      int32_t page_size, int32_t* err, void* stream) {
+  if (n < 0 || batch < 0 || num_pages < 1 || page_size < 1) return PKD_E_INVALID_ARG;
+  if (n == 0) return PKD_OK;
+  if (!latent_new || !rope_new || !batch_indices || !positions || !indptr || !indices ||
+      !last_page_len || !cache)
+    return PKD_E_INVALID_ARG;
+  if (!aligned(latent_new, 16) || !aligned(rope_new, 16) || !aligned(cache, 16) || !aligned(err, 4))
+    return PKD_E_INVALID_ARG;
+  if (n > 1 && (latent_stride < kLatentDim || rope_stride < kLatentRope || latent_stride % 8 != 0 ||
+                rope_stride % 8 != 0 || latent_stride > ((int64_t)1 << 40) ||
+                rope_stride > ((int64_t)1 << 40)))
+    return PKD_E_INVALID_ARG;
+  if (launch_latent_append(latent_new, n > 1 ? latent_stride * 2 : 0, rope_new,
+                           n > 1 ? rope_stride * 2 : 0, batch_indices, positions, n, indptr,
+                           indices, last_page_len, batch, cache, num_pages, page_size, err,
+                           static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return PKD_E_CUDA;
+  return PKD_OK;
+}
+
 int pkd_last_device_error(pkd_ctx* ctx, void* stream, int32_t* dev_err) {
   if (ctx == nullptr || dev_err == nullptr) return PKD_E_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -674,7 +766,8 @@ int pkd_graph_capture_io(pkd_ctx* ctx, int32_t layers, const void* const* q,
   }
   const pkd_config& c = ctx->cfg;
   const size_t rows = (size_t)ctx->info.batch * c.num_qo_heads;
-  const size_t q_bytes = rows * c.head_dim * 2, lse_bytes = rows * 4;
+  const size_t q_bytes = rows * (ctx->kind.latent ? kLatentRow : c.head_dim) * 2;
+  const size_t out_bytes = rows * c.head_dim * 2, lse_bytes = rows * 4;
   const bool copy_in = q_host != nullptr && rows > 0;
   const bool copy_out = (out_host != nullptr || lse_host != nullptr) && rows > 0;
   pkd_graph* g = new (std::nothrow) pkd_graph();
@@ -752,7 +845,7 @@ int pkd_graph_capture_io(pkd_ctx* ctx, int32_t layers, const void* const* q,
       }
       if (copy_out && ok(cudaEventRecord(done[l], cs)) &&
           ok(cudaStreamWaitEvent(cout, done[l], 0))) {
-        if (out_host) ok(cudaMemcpyAsync(out_host[l], out[l], q_bytes, cudaMemcpyDeviceToHost, cout));
+        if (out_host) ok(cudaMemcpyAsync(out_host[l], out[l], out_bytes, cudaMemcpyDeviceToHost, cout));
         if (lse_host)
           ok(cudaMemcpyAsync(lse_host[l], lse[l], lse_bytes, cudaMemcpyDeviceToHost, cout));
       }
@@ -779,9 +872,10 @@ int pkd_graph_capture_io(pkd_ctx* ctx, int32_t layers, const void* const* q,
 
 int pkd_graph_launch(pkd_graph* g, void* stream) {
   if (g == nullptr || g->exec == nullptr) return PKD_E_INVALID_ARG;
-  // a dense-prefix (or cascade) graph's query maps cover the batch it was
-  // captured with
-  if ((g->ctx->kind.dense || g->ctx->kind.cascade) && g->ctx->info.batch != g->batch)
+  // a dense-prefix (or cascade, or latent) graph's query maps cover the batch
+  // it was captured with
+  if ((g->ctx->kind.dense || g->ctx->kind.cascade || g->ctx->kind.latent) &&
+      g->ctx->info.batch != g->batch)
     return PKD_E_STALE_PLAN;
   if (cudaGraphLaunch(g->exec, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return PKD_E_CUDA;

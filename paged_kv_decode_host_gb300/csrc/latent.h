@@ -1,0 +1,60 @@
+// The latent cache's decode and append (latent_kernel.cu): sizes, arguments
+// and launchers.
+#pragma once
+
+#include <stdint.h>
+
+#include <cuda.h>
+#include <cuda_runtime_api.h>
+
+namespace pkd {
+
+constexpr int kLatentDim = 512;   // latent columns: the output's width
+constexpr int kLatentRope = 64;   // rotary key columns behind them
+constexpr int kLatentRow = kLatentDim + kLatentRope;
+constexpr int kLatentMaxHeads = 128;
+
+// Query heads that one work item covers: the products' columns, 16, 32 or
+// 64 (the output of 64 heads, 512 dims each, fills half of tensor memory).
+// More heads make ceil(heads / 64) blocks, each an item of its own.
+__host__ __device__ constexpr int32_t latent_block_heads(int32_t heads) {
+  return heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
+}
+__host__ __device__ constexpr int32_t latent_blocks(int32_t heads) {
+  return (heads + latent_block_heads(heads) - 1) / latent_block_heads(heads);
+}
+
+struct LatentArgs {
+  const int32_t* sched;
+  float* o_part;         // fp32 [slot][heads][512]
+  float* l_part;         // fp32 [slot][heads] (natural log)
+  int32_t* err;
+  uint16_t* out;         // bf16 [batch][heads][512]
+  float* lse;            // fp32 [batch][heads] or null
+  int64_t off_cta, off_items, off_pages, off_units, off_merge;
+  int32_t heads, blocks, page_size, num_pages;
+  float scale_log2, v_scale;
+  int32_t wait_epoch;
+  CUtensorMap kv_map;    // the cache, 16-token boxes of 64 columns
+  CUtensorMap q_map;     // the queries, a block's heads of 64 columns
+};
+
+int latent_smem_bytes(int32_t heads);
+cudaError_t latent_prepare(int32_t heads);
+cudaError_t latent_occupancy(int32_t heads, int* blocks_per_sm);
+// The decode kernel and, with merge, the merge of split requests (its grid
+// follows the plan on the device).  decode_done (or null) is recorded
+// between the two.
+cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool merge,
+                          cudaEvent_t decode_done, cudaStream_t stream);
+cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page_size,
+                              CUtensorMap* map);
+cudaError_t encode_latent_q_map(const void* q, int32_t batch, int32_t heads, CUtensorMap* map);
+cudaError_t launch_latent_append(const void* latent, int64_t latent_stride, const void* rope,
+                                 int64_t rope_stride, const int32_t* batch_indices,
+                                 const int32_t* positions, int32_t n, const int32_t* indptr,
+                                 const int32_t* indices, const int32_t* last_page_len,
+                                 int32_t batch, void* cache, int32_t num_pages, int32_t page_size,
+                                 int32_t* err, cudaStream_t stream);
+
+}  // namespace pkd

@@ -1,0 +1,869 @@
+// Decode attention over a paged cache of latent vectors (contexts with
+// PKD_FLAG_LATENT), the merge of its split requests, and the append of new
+// latent rows, for sm_103a.
+//
+// The cache holds one row per token, shared by every query head: kLatentDim
+// latent columns and kLatentRope columns of the rotary key.  With the
+// up-projections absorbed into the queries and the output projection, head h
+// of request i computes
+//     s_t   = scale * q[i][h] . c_t                 (all 576 columns)
+//     out   = sum_t softmax(s)_t * c_t[0 .. 511]    (the latent columns)
+// so one read of a row serves as key and value of up to 128 heads: 4 * 544
+// flop per head and 1,152 bytes per token.
+//
+// GB300 design: one CTA per SM walks its queue of (request, 64-head block,
+// token range) items from the planner's schedule.  Both products put the
+// long axis on the tensor core's 128 rows and the heads on its columns, so a
+// CTA's tensor-memory use follows the number of heads (the transposed
+// orientation would need all 512 columns for the 512-wide output alone) and
+// short head counts cost narrow instructions:
+//     S^T [tokens x heads]  = C [tokens x 576]  Q^T    A = C, B = Q, K-major
+//     O^T [dims x heads]   += C^T [dims x tokens] P^T  A = C, B = P, MN-major
+// The same shared-memory tile of C feeds both: 64-column chunks of T token
+// rows of 128 bytes (128-byte swizzle), two adjacent chunks being the 128
+// rows of one O^T product.
+//  * warp 8 streams C: per chunk, one TMA tensor copy per 16-token page tile;
+//    a chunk's slot is refilled as soon as the products that read it are done
+//    (the rotary chunk after the scores, latent chunk pairs one by one while
+//    P.V walks over them);
+//  * warp 9 issues the score products as the chunks land, warp 10 the P.V
+//    products; the whole warp runs the loop and one elected lane issues, with
+//    unrolled constant descriptor steps: 46 / 56 cycles per 128 x 16 / 64 x 16
+//    product, where a lone thread that forms descriptors in the loop takes
+//    135;
+//  * warps 0-7 are the softmax: a thread holds one token (a tensor-memory
+//    lane) and half of the block's heads.  The maxima run over tokens, that
+//    is, across lanes and warps, so they are not formed per tile: every tile
+//    is only compared with the running base, and the exact maxima are taken
+//    when some score exceeds its head's base by more than 2^8 (always in an
+//    item's first tile).  P is written as bf16 (rounded to nearest; the sums
+//    that divide it are kept unrounded in fp32) into shared memory.
+// Every wait is bounded; on timeout the kernel sets the device error word,
+// stops, waits (bounded) for its copies and products, frees tensor memory
+// and returns.
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "latent.h"
+#include "pkd_internal.h"
+#include "prefix_tc_body.cuh"
+#include "sm103_ptx.cuh"
+#include "tensor_map.h"
+
+namespace pkd {
+namespace {
+
+using namespace dev;
+using tc::fast_exp2;
+using tc::mma_commit;
+using tc::mma_ss;
+using tc::pack_bf16;
+using tc::smem_desc;
+using tc::tc_fence_after;
+using tc::tc_fence_before;
+using tc::tc_wait;
+
+constexpr int kChunks = kLatentRow / 64;        // 9: eight latent chunks, then the rotary one
+constexpr int kRopeChunk = kChunks - 1;
+constexpr int kPairs = kLatentDim / 128;        // 4 O^T products of 128 dims
+constexpr int kSoftWarps = 8;
+constexpr int kWarpLoad = 8, kWarpScore = 9, kWarpOut = 10;
+constexpr int kLatThreads = 11 * 32;
+constexpr float kRaiseLog2 = 8.f;
+constexpr float kLowest = -3.0e38f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
+
+// NH: heads (instruction columns) of a block; T: tokens of a tile, a multiple
+// of 16 up to 128 (the products always have 128 rows: rows past T read
+// whatever follows in shared memory and are ignored); ST: tiles in flight.
+template <int NH_, int T_, int ST_>
+struct LatentShape {
+  static constexpr int NH = NH_, T = T_, ST = ST_, HH = NH_ / 2;
+  static constexpr int kBoxes = T / 16;
+  static constexpr int kSlot = T * 128;             // one chunk of a tile
+  static constexpr int kStage = kChunks * kSlot;
+  static constexpr int kQChunk = NH * 128;
+  static constexpr int kQ = kChunks * kQChunk;
+  static constexpr int kP = T * 128;                // [token][64 heads] bf16, 128-byte rows
+  static constexpr uint32_t kColO = 0, kColS = kPairs * NH;
+  static_assert(T % 16 == 0 && T <= 128 && NH % 16 == 0 && NH <= 64, "shape");
+  static_assert(kColS + 2 * NH <= 512, "tensor-memory columns");
+  // score products read 128 rows from the last slot on: Q and P lie behind
+  static_assert(kQ + kP >= (128 - T) * 128, "rows past the tile stay inside the allocation");
+};
+
+template <class C>
+struct LatentSmem {
+  uint64_t full[C::ST][kChunks];     // chunk landed
+  uint64_t epair[C::ST][kPairs];     // a pair's P.V products done
+  uint64_t erope[C::ST];             // the tile's rotary products done
+  uint64_t qfull, qfree;
+  uint64_t sfull[2], sfree[2];
+  uint64_t pfull, pvdone, ofree;
+  uint64_t xch[2];                   // per half of the heads: the four warps' exchanges
+  uint64_t fin;
+  uint32_t tmem_base;
+  int abort_flag;
+  int raise[2][2][4];                // [phase parity][half][quadrant]
+  float top[2][2][4][C::HH];         // column maxima / sums, [phase parity][half][quadrant]
+};
+
+template <class C>
+constexpr int latent_smem() {
+  return 1024 + C::ST * C::kStage + C::kQ + C::kP + (int)sizeof(LatentSmem<C>);
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+__device__ __forceinline__ void tensor_copy3_g2s(void* dst, const CUtensorMap* map, int c0, int c1,
+                                                 int c2, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)),
+      "l"(policy)
+      : "memory");
+}
+
+// N columns of this warp's 32 lanes
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t t, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns");
+  if constexpr (N == 32) {
+    tc::tmem_ld32(t, r);
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(t)
+                 : "memory");
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_stn(uint32_t t, const uint32_t (&r)[N]) {
+  if constexpr (N == 32) {
+    tc::tmem_st32(t, r);
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16};" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+  }
+}
+
+// fp32 order as signed integer order (NaN above +inf)
+__device__ __forceinline__ int order_of(float x) {
+  const int b = __float_as_int(x);
+  return b >= 0 ? b : b ^ 0x7fffffff;
+}
+__device__ __forceinline__ float from_order(int o) {
+  return __int_as_float(o >= 0 ? o : o ^ 0x7fffffff);
+}
+
+struct LatentItem {
+  int req, tb, te, dst, page0, block;
+};
+__device__ __forceinline__ LatentItem item_at(const LatentArgs& a, int it) {
+  const int32_t* w = a.sched + a.off_items + (int64_t)it * kItemWords;
+  return LatentItem{w[0], w[1], w[2], w[3], w[4], w[7]};
+}
+
+template <class C>
+__global__ void __launch_bounds__(kLatThreads, 1)
+    latent_decode_kernel(const __grid_constant__ LatentArgs a) {
+  extern __shared__ uint8_t raw[];
+  if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
+  // the 128-byte swizzle repeats every 1024 bytes
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t* sC = smem;
+  uint8_t* sQ = sC + C::ST * C::kStage;
+  uint8_t* sP = sQ + C::kQ;
+  LatentSmem<C>* sh = reinterpret_cast<LatentSmem<C>*>(sP + C::kP);
+  volatile int* abort_flag = &sh->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  const int it0 = a.sched[a.off_cta + blockIdx.x];
+  const int it1 = a.sched[a.off_cta + blockIdx.x + 1];
+  if (it0 >= it1) {
+    pdl_wait();
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) {
+      for (int c = 0; c < kChunks; ++c) mbar_init(&sh->full[s][c], 1);
+      for (int p = 0; p < kPairs; ++p) mbar_init(&sh->epair[s][p], 1);
+      mbar_init(&sh->erope[s], 1);
+    }
+    mbar_init(&sh->qfull, 1);
+    mbar_init(&sh->qfree, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh->sfull[b], 1);
+      mbar_init(&sh->sfree[b], kSoftWarps);
+      mbar_init(&sh->xch[b], 4);
+    }
+    mbar_init(&sh->pfull, kSoftWarps);
+    mbar_init(&sh->pvdone, 1);
+    mbar_init(&sh->ofree, kSoftWarps);
+    mbar_init(&sh->fin, 2);
+    sh->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sh->tmem_base)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(kFull, sh->tmem_base, 0);
+
+  if (warp == kWarpLoad) {
+    // ------------------------------------------------------------ producer
+    // q and the cache are read before the previous kernel is waited for, as
+    // the decode kernel does (the contract of pkd_run)
+    const uint64_t policy = a.blocks > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
+    const int P = a.page_size;
+    int r = 0, nq = 0;
+    int extra = 0;   // chunks issued of a tile that a timeout cut short
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+      const LatentItem w = item_at(a, it);
+      if (it > it0 && !tc_wait(&sh->qfree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        ++nq;
+        mbar_arrive_expect_tx(&sh->qfull, (uint32_t)C::kQ);
+        for (int c = 0; c < kChunks; ++c)
+          tensor_copy3_g2s(sQ + c * C::kQChunk, &a.q_map, 64 * c, C::NH * w.block, w.req, &sh->qfull,
+                           policy);
+      }
+      __syncwarp();
+      // page ids of 32 consecutive 16-token boxes, one per lane (items start
+      // on page boundaries)
+      const int boxes = (w.te - w.tb + 15) >> 4;
+      int base = -32, my_page = 0;
+      for (int t = w.tb, k = 0; t < w.te; t += C::T, ++k, ++r) {
+        const int nbox = min(C::kBoxes, (w.te - t + 15) >> 4);
+        const int box0 = C::kBoxes * k;
+        if (box0 + C::kBoxes > base + 32) {
+          base = box0;
+          my_page = 0;
+          if (base + lane < boxes) {
+            my_page = a.sched[a.off_pages + w.page0 + (16 * (base + lane)) / P];
+            if ((unsigned)my_page >= (unsigned)a.num_pages) {
+              atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+              my_page = 0;
+            }
+          }
+        }
+        const int st = r % C::ST;
+        const uint32_t use = (uint32_t)(r / C::ST);
+        uint8_t* stage = sC + st * C::kStage;
+        // lane 8 c + j copies box j of chunk c of the pair (lanes 0-15); the
+        // rotary chunk (lanes 0-7) goes first, as its slot is free first
+        const int j = lane & 7, cc = lane >> 3;
+        const int page = __shfl_sync(kFull, my_page, (box0 + j - base) & 31);
+        const int tok = (t + 16 * j) % P;
+        const uint32_t bytes = (uint32_t)nbox * 2048u;
+        if (use > 0 && !tc_wait(&sh->erope[st], (use - 1) & 1u, abort_flag, a.err, lane)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][kRopeChunk], bytes);
+        __syncwarp();
+        if (cc == 0 && j < nbox)
+          tensor_copy3_g2s(stage + kRopeChunk * C::kSlot + j * 2048, &a.kv_map, 64 * kRopeChunk, tok,
+                           page, &sh->full[st][kRopeChunk], policy);
+        extra = 1;
+        for (int p = 0; p < kPairs; ++p) {
+          if (use > 0 && !tc_wait(&sh->epair[st][p], (use - 1) & 1u, abort_flag, a.err, lane)) {
+            ok = false;
+            break;
+          }
+          if (lane < 2) mbar_arrive_expect_tx(&sh->full[st][2 * p + lane], bytes);
+          __syncwarp();
+          if (cc < 2 && j < nbox) {
+            const int c = 2 * p + cc;
+            tensor_copy3_g2s(stage + c * C::kSlot + j * 2048, &a.kv_map, 64 * c, tok, page,
+                             &sh->full[st][c], policy);
+          }
+          extra += 2;
+        }
+        if (!ok) break;
+        extra = 0;
+      }
+    }
+    // drain: no copy may be in flight when the block ends.  Chunk c of stage
+    // s was copied once per whole tile of the stage, and once more when it
+    // was among the first chunks of a tile cut short.
+    if (lane == 0) {
+      for (int s = 0; s < C::ST; ++s)
+        for (int c = 0; c < kChunks; ++c) {
+          int uses = r > s ? (r - 1 - s) / C::ST + 1 : 0;
+          if (s == r % C::ST && (c == kRopeChunk ? 0 : c + 1) < extra) ++uses;
+          if (uses > 0 && !mbar_wait(&sh->full[s][c], (uint32_t)((uses - 1) & 1), nullptr))
+            atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+        }
+      if (nq > 0 && !mbar_wait(&sh->qfull, (uint32_t)((nq - 1) & 1), nullptr))
+        atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp == kWarpScore) {
+    // -------------------------------------------------------- S^T products
+    const bool me = elect_one();
+    const uint32_t idesc = tc::mma_idesc(128, C::NH, 0);
+    const uint64_t c0 = smem_desc(smem_u32(sC), 16, 1024);
+    const uint64_t q0 = smem_desc(smem_u32(sQ), 16, 1024);
+    int r = 0;
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+      const LatentItem w = item_at(a, it);
+      if (!tc_wait(&sh->qfull, (uint32_t)((it - it0) & 1), abort_flag, a.err, lane)) break;
+      for (int t = w.tb; t < w.te && ok; t += C::T, ++r) {
+        const int st = r % C::ST, b = r & 1;
+        const uint32_t use = (uint32_t)(r / C::ST);
+        if (r >= 2 && !tc_wait(&sh->sfree[b], (uint32_t)(((r >> 1) - 1) & 1), abort_flag, a.err, lane)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d = tmem + C::kColS + C::NH * b;
+        const uint64_t cs = c0 + (uint64_t)(st * (C::kStage >> 4));
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = i == 0 ? kRopeChunk : i - 1;
+          if (ok && !tc_wait(&sh->full[st][c], use & 1u, abort_flag, a.err, lane)) ok = false;
+          if (ok && me) {
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss(d, cs + (uint64_t)(c * (C::kSlot >> 4) + 2 * kk),
+                     q0 + (uint64_t)(c * (C::kQChunk >> 4) + 2 * kk), idesc, i > 0 || kk > 0);
+            if (i == 0) mma_commit(&sh->erope[st]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (me) {
+          mma_commit(&sh->sfull[b]);
+          if (t + C::T >= w.te) mma_commit(&sh->qfree);
+        }
+        __syncwarp();
+      }
+    }
+    if (me) {
+      mma_commit(&sh->fin);
+      if (!mbar_wait(&sh->fin, 0, nullptr)) atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp == kWarpOut) {
+    // -------------------------------------------------------- O^T products
+    const bool me = elect_one();
+    const uint32_t idesc = tc::mma_idesc(128, C::NH, 1) | (1u << 15);   // A and B MN-major
+    const uint64_t c0 = smem_desc(smem_u32(sC), C::kSlot, 1024);
+    const uint64_t p0 = smem_desc(smem_u32(sP), 16, 1024);
+    int r = 0;
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+      const LatentItem w = item_at(a, it);
+      for (int t = w.tb; t < w.te; t += C::T, ++r) {
+        const int st = r % C::ST;
+        if (!tc_wait(&sh->pfull, (uint32_t)(r & 1), abort_flag, a.err, lane) ||
+            (t == w.tb && it > it0 &&
+             !tc_wait(&sh->ofree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane))) {
+          ok = false;
+          break;
+        }
+        const int n = min(C::T, w.te - t);
+        const int nbox = (n + 15) >> 4;
+        if (n & 15) {
+          // rows past the last token: their P is 0, but 0 x NaN would stay
+          const int rows = 16 * nbox - n;
+          for (int i = lane; i < 2 * kPairs * rows * 8; i += 32) {
+            const int c = i / (rows * 8), rem = i % (rows * 8);
+            *reinterpret_cast<uint4*>(sC + st * C::kStage + c * C::kSlot + (n + rem / 8) * 128 +
+                                      (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (me) {
+          tc_fence_after();
+          const uint64_t cs = c0 + (uint64_t)(st * (C::kStage >> 4));
+#pragma unroll
+          for (int p = 0; p < kPairs; ++p) {
+#pragma unroll
+            for (int kk = 0; kk < C::kBoxes; ++kk)
+              if (kk < nbox)
+                mma_ss(tmem + C::kColO + C::NH * p, cs + (uint64_t)(p * (C::kSlot >> 3) + 128 * kk),
+                       p0 + (uint64_t)(128 * kk), idesc, t > w.tb || kk > 0);
+            mma_commit(&sh->epair[st][p]);
+          }
+          mma_commit(&sh->pvdone);
+        }
+        __syncwarp();
+      }
+    }
+    if (me) {
+      mma_commit(&sh->fin);
+      if (!mbar_wait(&sh->fin, 0, nullptr)) atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------- softmax + epilogue
+    constexpr int HH = C::HH;
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = 32 * quad + lane;                           // token of the tile
+    const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16);   // this quadrant's lanes
+    uint32_t xc = 0;                                            // exchanges so far
+    int r = 0;
+    bool ok = true, waited = false;
+    // the four warps of this half meet (bounded): what each wrote into the
+    // exchange arrays of this phase's parity is visible to all afterwards;
+    // the other parity's arrays may be rewritten from here on
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->xch[half]);
+      if (!tc_wait(&sh->xch[half], xc & 1u, abort_flag, a.err, lane)) return false;
+      ++xc;
+      return true;
+    };
+    for (int it = it0; it < it1 && ok; ++it) {
+      const LatentItem w = item_at(a, it);
+      float m[HH], l[HH];   // base (log2 units) of this half's heads; this token lane's sums
+#pragma unroll
+      for (int j = 0; j < HH; ++j) {
+        m[j] = -CUDART_INF_F;
+        l[j] = 0.f;
+      }
+      for (int t = w.tb; t < w.te && ok; t += C::T, ++r) {
+        const int b = r & 1;
+        if (!tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sv[HH];
+        tmem_ldn<HH>(tq + C::kColS + C::NH * b + HH * half, sv);
+        tc::tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->sfree[b]);
+        const bool live = row < min(C::T, w.te - t);
+        float x[HH];
+        float over = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < HH; ++j) {
+          x[j] = live ? __uint_as_float(sv[j]) * a.scale_log2 : -CUDART_INF_F;
+          over = fmaxf(over, x[j] - m[j]);   // NaN (-inf - -inf) is ignored
+        }
+        const bool first = t == w.tb;
+        const int par = (int)(xc & 1u);
+        const bool want = __any_sync(kFull, over > kRaiseLog2) || first;
+        if (lane == 0) sh->raise[par][half][quad] = want ? 1 : 0;
+        if (!meet()) {
+          ok = false;
+          break;
+        }
+        const bool up = (sh->raise[par][half][0] | sh->raise[par][half][1] |
+                         sh->raise[par][half][2] | sh->raise[par][half][3]) != 0;
+        // P of the tile before is read (its buffer is written below, and a
+        // raised base rescales O)
+        if (r > 0 && !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) {
+          ok = false;
+          break;
+        }
+        if (up) {
+          const int par2 = (int)(xc & 1u);
+#pragma unroll
+          for (int j = 0; j < HH; ++j) {
+            const int top = __reduce_max_sync(kFull, order_of(x[j]));
+            if (lane == 0) sh->top[par2][half][quad][j] = from_order(top);
+          }
+          if (!meet()) {
+            ok = false;
+            break;
+          }
+          float f[HH];
+#pragma unroll
+          for (int j = 0; j < HH; ++j) {
+            int top = order_of(m[j]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top = max(top, order_of(sh->top[par2][half][q][j]));
+            // finite, so that scores of -inf weigh 0 (not -inf - -inf)
+            const float nm = top < order_of(kLowest) ? kLowest : from_order(top);
+            f[j] = first ? 0.f : exp2f(m[j] - nm);
+            m[j] = nm;
+            l[j] = first ? 0.f : l[j] * f[j];
+          }
+          if (!first) {
+            tc_fence_after();
+            constexpr int kPart = HH < 16 ? HH : 16;   // columns at a time: the registers
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+              for (int c = 0; c < HH; c += kPart) {
+                uint32_t o[kPart];
+                const uint32_t col = tq + C::kColO + C::NH * p + HH * half + c;
+                tmem_ldn<kPart>(col, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < kPart; ++j)
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * f[c + j]);
+                tmem_stn<kPart>(col, o);
+              }
+            tc::tmem_wait_st();
+          }
+        }
+        // weights 2^(x - m); this thread's row of P: 16-byte pieces of 8
+        // heads, swizzled as the products read them
+        uint32_t pw[HH / 2];
+#pragma unroll
+        for (int j = 0; j < HH; j += 2) {
+          const float p0 = live ? fast_exp2(x[j] - m[j]) : 0.f;
+          const float p1 = live ? fast_exp2(x[j + 1] - m[j + 1]) : 0.f;
+          l[j] += p0;
+          l[j + 1] += p1;
+          pw[j / 2] = pack_bf16(p0, p1);
+        }
+        if (row < C::T) {
+#pragma unroll
+          for (int i = 0; i < HH / 8; ++i)
+            *reinterpret_cast<uint4*>(sP + row * 128 + (((half * (HH / 8) + i) ^ (row & 7)) << 4)) =
+                make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->pfull);
+      }
+      if (!ok) break;
+      // ---- epilogue: sums over the 128 token lanes in a fixed order
+      const int par = (int)(xc & 1u);
+#pragma unroll
+      for (int j = 0; j < HH; ++j) {
+        float z = l[j];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+        if (lane == 0) sh->top[par][half][quad][j] = z;
+      }
+      if (!meet() || !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (!waited) {
+        pdl_wait();   // outputs and partial states may be in use by the previous kernel
+        waited = true;
+      }
+      const int h0 = C::NH * w.block + HH * half;
+      float inv[HH];
+#pragma unroll
+      for (int j = 0; j < HH; ++j) {
+        const float z = (sh->top[par][half][0][j] + sh->top[par][half][1][j]) +
+                        (sh->top[par][half][2][j] + sh->top[par][half][3][j]);
+        inv[j] = z == 0.f ? 0.f : a.v_scale / z;   // every score -inf: an empty state
+        if (quad == 0 && lane == 0 && h0 + j < a.heads) {
+          const float lse = (m[j] + log2f(z)) * kLn2;
+          if (w.dst >= 0)
+            a.l_part[(int64_t)w.dst * a.heads + h0 + j] = lse;
+          else if (a.lse != nullptr)
+            a.lse[(int64_t)w.req * a.heads + h0 + j] = lse;
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        uint32_t o[HH];
+        tmem_ldn<HH>(tq + C::kColO + C::NH * p + HH * half, o);
+        tc::tmem_wait_ld();
+        const int dim = 128 * p + row;
+        if (w.dst >= 0) {
+          float* to = a.o_part + ((int64_t)w.dst * a.heads + h0) * kLatentDim + dim;
+#pragma unroll
+          for (int j = 0; j < HH; ++j)
+            if (h0 + j < a.heads) to[(int64_t)j * kLatentDim] = __uint_as_float(o[j]) * inv[j];
+        } else {
+          uint16_t* to = a.out + ((int64_t)w.req * a.heads + h0) * kLatentDim + dim;
+#pragma unroll
+          for (int j = 0; j < HH; ++j)
+            if (h0 + j < a.heads)
+              to[(int64_t)j * kLatentDim] =
+                  (uint16_t)(pack_bf16(__uint_as_float(o[j]) * inv[j], 0.f) & 0xffffu);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->ofree);
+    }
+    if (!waited) pdl_wait();
+  }
+  pdl_wait();   // complete only after the previous kernel
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+// Merge of split requests: out = sum_i w_i o_i / sum_i w_i, w_i = exp(L_i -
+// max L), over a request's partial states in slot order.  A block takes 128
+// dims of one (request, head): four warps each fold every fourth slot (a
+// lane four dims, so a slot is one 512-byte read) with several slots' loads
+// in flight, then add up in warp order.
+constexpr int kMergeDims = 128;
+__global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant__ LatentArgs a) {
+  __shared__ float4 acc_s[4][32];
+  __shared__ float z_s[4];
+  pdl_launch_dependents();
+  if (a.wait_epoch != 0) pdl_wait();   // the schedule came from another stream
+  const int units = a.sched[H_NUNITS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kParts = kLatentDim / kMergeDims;
+  const int64_t tasks = (int64_t)units * a.heads * kParts;
+  pdl_wait();   // the partial states belong to the decode kernel
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int part = (int)(task % kParts);
+    const int h = (int)(task / kParts % a.heads);
+    const int u = (int)(task / ((int64_t)kParts * a.heads));
+    const int s0 = a.sched[a.off_merge + u], s1 = a.sched[a.off_merge + u + 1];
+    const int req = a.sched[a.off_units + 2 * u];
+    float top = -CUDART_INF_F;
+    for (int s = s0 + lane; s < s1; s += 32)
+      top = fmaxf(top, a.l_part[(int64_t)s * a.heads + h]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    const float base = top == -CUDART_INF_F ? 0.f : top;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float z = 0.f;
+#pragma unroll 4
+    for (int s = s0 + warp; s < s1; s += 4) {
+      const float wgt = exp2f((a.l_part[(int64_t)s * a.heads + h] - base) * kLog2e);
+      const float4 o = *reinterpret_cast<const float4*>(
+          a.o_part + ((int64_t)s * a.heads + h) * kLatentDim + kMergeDims * part + 4 * lane);
+      z += wgt;
+      acc.x = fmaf(wgt, o.x, acc.x);
+      acc.y = fmaf(wgt, o.y, acc.y);
+      acc.z = fmaf(wgt, o.z, acc.z);
+      acc.w = fmaf(wgt, o.w, acc.w);
+    }
+    acc_s[warp][lane] = acc;
+    if (lane == 0) z_s[warp] = z;
+    __syncthreads();
+    if (warp == 0) {
+      float4 t = acc_s[0][lane];
+      float zt = z_s[0];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float4 v = acc_s[w][lane];
+        t.x += v.x;
+        t.y += v.y;
+        t.z += v.z;
+        t.w += v.w;
+        zt += z_s[w];
+      }
+      const float inv = zt == 0.f ? 0.f : 1.f / zt;
+      const int64_t qrow = (int64_t)req * a.heads + h;
+      *reinterpret_cast<uint2*>(a.out + qrow * kLatentDim + kMergeDims * part + 4 * lane) =
+          make_uint2(pack_bf16(t.x * inv, t.y * inv), pack_bf16(t.z * inv, t.w * inv));
+      if (part == 0 && lane == 0 && a.lse != nullptr) a.lse[qrow] = base + log2f(zt) * kLn2;
+    }
+    __syncthreads();
+  }
+}
+
+using Shape16 = LatentShape<16, 64, 2>;
+using Shape32 = LatentShape<32, 64, 2>;
+using Shape64 = LatentShape<64, 112, 1>;
+static_assert(latent_smem<Shape16>() <= 227 * 1024 && latent_smem<Shape32>() <= 227 * 1024 &&
+                  latent_smem<Shape64>() <= 227 * 1024,
+              "dynamic shared memory of one CTA");
+
+const void* kernel_of(int32_t block_heads) {
+  switch (block_heads) {
+    case 16: return reinterpret_cast<const void*>(&latent_decode_kernel<Shape16>);
+    case 32: return reinterpret_cast<const void*>(&latent_decode_kernel<Shape32>);
+    default: return reinterpret_cast<const void*>(&latent_decode_kernel<Shape64>);
+  }
+}
+
+// ---------------------------------------------------------------- append
+// One warp per new token: its latent and rotary parts, read from rows of any
+// stride (they are often column ranges of one projection's output), become
+// one cache row.  Bytes: a row read and written per token.
+constexpr int kAppendWarps = 8;
+__global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(
+    const uint8_t* __restrict__ latent, int64_t latent_stride, const uint8_t* __restrict__ rope,
+    int64_t rope_stride, const int32_t* __restrict__ batch_indices,
+    const int32_t* __restrict__ positions, int32_t n, const int32_t* __restrict__ indptr,
+    const int32_t* __restrict__ indices, const int32_t* __restrict__ last_page_len, int32_t batch,
+    uint8_t* __restrict__ cache, int32_t num_pages, int32_t page_size, int32_t* err) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  if (i >= n) return;
+  constexpr int kLat16 = kLatentDim * 2 / 16, kRope16 = kLatentRope * 2 / 16;
+  // the row does not depend on the table: fetch it while the table is read
+  const uint4* src = reinterpret_cast<const uint4*>(latent + i * latent_stride);
+  uint4 v[2];
+#pragma unroll
+  for (int k = 0; k < kLat16 / 32; ++k) v[k] = src[32 * k + lane];
+  uint4 vr = make_uint4(0, 0, 0, 0);
+  if (lane < kRope16) vr = reinterpret_cast<const uint4*>(rope + i * rope_stride)[lane];
+  int page = -1, slot = 0;
+  const int b = batch_indices[i], pos = positions[i];
+  if (b >= 0 && b < batch) {
+    const int p0 = indptr[b], p1 = indptr[b + 1], last = last_page_len[b];
+    const int64_t len = (int64_t)page_size * (p1 - p0 - 1) + last;
+    if (p1 > p0 && last >= 1 && last <= page_size && pos >= 0 && pos < len) {
+      const int pg = indices[p0 + pos / page_size];
+      if (pg >= 0 && pg < num_pages) {
+        page = pg;
+        slot = pos % page_size;
+      }
+    }
+  }
+  if (page < 0) {
+    if (lane == 0 && err != nullptr) atomicOr(err, PKD_DEV_ERR_BOUNDS);
+    return;
+  }
+  uint4* dst = reinterpret_cast<uint4*>(cache + ((int64_t)page * page_size + slot) * kLatentRow * 2);
+#pragma unroll
+  for (int k = 0; k < kLat16 / 32; ++k) dst[32 * k + lane] = v[k];
+  if (lane < kRope16) dst[kLat16 + lane] = vr;
+}
+static_assert(kLatentDim * 2 / 16 == 64 && kLatentRope * 2 / 16 <= 32, "two pieces per lane");
+
+}  // namespace
+
+int latent_smem_bytes(int32_t heads) {
+  switch (latent_block_heads(heads)) {
+    case 16: return latent_smem<Shape16>();
+    case 32: return latent_smem<Shape32>();
+    default: return latent_smem<Shape64>();
+  }
+}
+
+cudaError_t latent_prepare(int32_t heads) {
+  return cudaFuncSetAttribute(kernel_of(latent_block_heads(heads)),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              latent_smem_bytes(heads));
+}
+
+cudaError_t latent_occupancy(int32_t heads, int* blocks_per_sm) {
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+      blocks_per_sm, kernel_of(latent_block_heads(heads)), kLatThreads,
+      (size_t)latent_smem_bytes(heads));
+}
+
+cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool merge,
+                          cudaEvent_t decode_done, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kLatThreads);
+  cfg.dynamicSmemBytes = (size_t)latent_smem_bytes(a.heads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {const_cast<LatentArgs*>(&a)};
+  cudaError_t e = cudaLaunchKernelExC(&cfg, kernel_of(latent_block_heads(a.heads)), args);
+  if (e != cudaSuccess) return e;
+  if (decode_done && (e = cudaEventRecordWithFlags(decode_done, stream, cudaEventRecordExternal)) !=
+                         cudaSuccess)
+    return e;
+  if (!merge) return cudaSuccess;
+  cfg.gridDim = dim3(merge_grid);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&latent_merge_kernel), args);
+}
+
+// The cache map: {576 columns, token slot, page}, box {64 columns, 16 slots,
+// 1 page}: 2 KB, 16 rows of 128 bytes with the 128-byte swizzle.
+cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page_size,
+                              CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  if (cache == nullptr || (uintptr_t)cache % 16 != 0 || page_size % 16 != 0 || num_pages < 1)
+    return cudaErrorInvalidValue;
+  const cuuint64_t row = (cuuint64_t)kLatentRow * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)kLatentRow, (cuuint64_t)page_size, (cuuint64_t)num_pages};
+  const cuuint64_t strides[2] = {row, row * (cuuint64_t)page_size};
+  const cuuint32_t box[3] = {64, 16, 1};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(cache), dims, strides,
+                box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+// The query map: {576 columns, head, request}, box {64 columns, a block's
+// heads, 1 request}; heads past the last read as zeros.
+cudaError_t encode_latent_q_map(const void* q, int32_t batch, int32_t heads, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  if (q == nullptr || (uintptr_t)q % 16 != 0 || batch < 1 || heads < 1) return cudaErrorInvalidValue;
+  const cuuint64_t row = (cuuint64_t)kLatentRow * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)kLatentRow, (cuuint64_t)heads, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {row, row * (cuuint64_t)heads};
+  const cuuint32_t box[3] = {64, (cuuint32_t)latent_block_heads(heads), 1};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+                elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_latent_append(const void* latent, int64_t latent_stride, const void* rope,
+                                 int64_t rope_stride, const int32_t* batch_indices,
+                                 const int32_t* positions, int32_t n, const int32_t* indptr,
+                                 const int32_t* indices, const int32_t* last_page_len,
+                                 int32_t batch, void* cache, int32_t num_pages, int32_t page_size,
+                                 int32_t* err, cudaStream_t stream) {
+  const int64_t blocks = ((int64_t)n + kAppendWarps - 1) / kAppendWarps;
+  latent_append_kernel<<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(
+      static_cast<const uint8_t*>(latent), latent_stride, static_cast<const uint8_t*>(rope),
+      rope_stride, batch_indices, positions, n, indptr, indices, last_page_len, batch,
+      static_cast<uint8_t*>(cache), num_pages, page_size, err);
+  return cudaGetLastError();
+}
+
+}  // namespace pkd

@@ -8,6 +8,7 @@
 #include <cuda.h>   // CUtensorMap (encoded through the runtime's driver entry point)
 #include <cuda_runtime_api.h>
 
+#include "latent.h"
 #include "pkd.h"
 
 namespace pkd {
@@ -28,6 +29,10 @@ __host__ __device__ constexpr int ring_depth(bool mma, bool block, bool fp8) {
 constexpr int kDefaultAlpha = 32;
 constexpr int kDefaultMinChunk = 256;
 constexpr int kMergeThreads = 256;
+// Latent contexts: an item's fixed cost (its queries, its epilogue and its
+// partial state of 64 heads x 512 dims) in tokens, and the split floor.
+constexpr int kLatentAlpha = 128;
+constexpr int kLatentMinChunk = 256;
 
 // Schedule header words (first 32 int32 of the workspace; 19..31 are 0).
 enum HeaderWord {
@@ -138,6 +143,9 @@ inline Layout make_layout(const pkd_config& c, int64_t n_cta) {
   // items <= Hkv * blocks + 4 n_cta
   if (c.flags & PKD_FLAG_DENSE_PREFIX)
     L.max_items = (int64_t)c.num_kv_heads * c.max_batch + 4 * n_cta + 8;
+  // latent plans: an item per block of heads; a request's blocks share slots
+  if (c.flags & PKD_FLAG_LATENT)
+    L.max_items = (int64_t)latent_blocks(c.num_qo_heads) * c.max_batch + 4 * n_cta + 8;
   if (c.flags & PKD_FLAG_CASCADE) {
     // prefix items <= Hkv * blocks + 2 n_pre, suffix items <= batch + 2 n_suf
     // (chunks at least half the level's work bound); every request is a
@@ -228,6 +236,7 @@ struct DecodeKind {
                        // (P % 16 == 0, tensor-core consumers); else one copy per token row
   bool dense = false;  // dense shared-prefix kernel (tcgen05, one KV head per item)
   bool cascade = false;  // cascade kernel: dense prefix role + decode role (page tiles)
+  bool latent = false;   // latent cache (latent.h)
 };
 int decode_smem_bytes(int hkv, const DecodeKind& k);
 int decode_threads(int hkv, const DecodeKind& k);

@@ -217,7 +217,9 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   const int64_t P = cfg.page_size;
   const int32_t group = cfg.num_qo_heads / cfg.num_kv_heads;
   const int32_t rows = group_indptr ? block_rows(cfg) : 1;
-  const int32_t heads = (group_indptr && (cfg.flags & PKD_FLAG_DENSE_PREFIX))
+  const bool latent = (cfg.flags & PKD_FLAG_LATENT) != 0;
+  const int32_t heads = latent ? latent_blocks(cfg.num_qo_heads)
+                        : (group_indptr && (cfg.flags & PKD_FLAG_DENSE_PREFIX))
                             ? cfg.num_kv_heads : 1;   // units per block
   (void)group;
 
@@ -281,8 +283,9 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   for (int64_t l : ulens) total += l;
 
   // ---- P1 + P2 + P3: chunk candidates, split, LPT; keep the best
-  const int64_t alpha = cfg.alpha < 0 ? kDefaultAlpha : cfg.alpha;
-  const int64_t min_chunk = cfg.min_chunk_tokens < 0 ? kDefaultMinChunk : cfg.min_chunk_tokens;
+  const int64_t alpha = cfg.alpha >= 0 ? cfg.alpha : latent ? kLatentAlpha : kDefaultAlpha;
+  const int64_t min_chunk = cfg.min_chunk_tokens >= 0 ? cfg.min_chunk_tokens
+                            : latent ? kLatentMinChunk : kDefaultMinChunk;
   const int64_t floor_c = ceil_div(std::max<int64_t>(min_chunk, 1), P) * P;
   const int64_t work_bound = ceil_div(total, n_cta);
   std::vector<int64_t>& cands = sc.cands;
@@ -380,7 +383,7 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     w[4] = (int32_t)(indptr[bk.table_row] + it.tok_begin / P);  // index of the first page
     w[5] = bk.n_req;
     w[6] = first_slot[b] >= 0 ? n_chunks[b] : 0;     // slot stride per request
-    w[7] = it.req % heads;                           // KV head (dense prefix), else 0
+    w[7] = it.req % heads;   // KV head (dense prefix), block of heads (latent), else 0
   }
   int32_t* unit_words = words + L.units;
   int32_t* merge_indptr = words + L.merge_indptr;

@@ -1,0 +1,219 @@
+"""Decode over the latent cache and its append, against the formulas in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_decode_host_gb300 as pkd
+
+pytestmark = pytest.mark.gpu
+ROW, DIM = 576, 512
+SCALE = 1.0 / math.sqrt(192.0)
+
+
+def table(lens, page, seed=0, spare=3):
+    """(indptr, indices, last, pool pages): pages scattered over the pool."""
+    counts = [-(-n // page) for n in lens]
+    indptr = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    pool = int(indptr[-1]) + spare
+    where = np.random.default_rng(seed).permutation(pool)[: indptr[-1]].astype(np.int32)
+    last = np.array([n - page * (c - 1) for n, c in zip(lens, counts)], np.int32)
+    return indptr, where, last, pool
+
+
+def reference(q, cache, lens, t, page, scale=SCALE):
+    indptr, indices = t[0], t[1]
+    outs, lses = [], []
+    for i, n in enumerate(lens):
+        mine = torch.from_numpy(indices[indptr[i]:indptr[i + 1]]).long().to(cache.device)
+        c = cache[mine].reshape(-1, ROW)[:n].double()
+        x = q[i].double() @ c.T * scale
+        lse = torch.logsumexp(x, 1)
+        outs.append(torch.exp(x - lse[:, None]) @ c[:, :DIM])
+        lses.append(lse)
+    return torch.stack(outs), torch.stack(lses)
+
+
+def make(heads, lens, page, seed=0, **kw):
+    t = table(lens, page, seed)
+    g = torch.Generator("cuda").manual_seed(seed)
+    q = torch.randn(len(lens), heads, ROW, generator=g, device="cuda").bfloat16()
+    cache = torch.randn(t[3], page, ROW, generator=g, device="cuda").bfloat16()
+    dec = pkd.BatchLatentDecodeWithPagedCache(heads, DIM, 64, page, scale=SCALE,
+                                              max_batch=max(1, len(lens)),
+                                              max_num_pages=len(t[1]), num_pages=t[3], **kw)
+    return t, q, cache, dec
+
+
+def close(got, ref, top):
+    """P and the result are rounded to bf16 (half a step: 2^-8 relative).  A result is a weighted
+    mean of cached values of magnitude at most `top`: the rounding of P moves it by at most 2^-8
+    top, its own by 2^-8 |out|; the fp32 sums (2^-24 per step, under 2^14 steps) by under 2^-10 of
+    that, which 1 % covers.  lse: fp32 sums of 576 products, each at most 6 x 6 x scale < 2.6 in
+    these inputs: 576 x 2^-24 x 576 x 2.6 would be the worst case, rounding errors of random sign
+    grow with the root, under 2^-24 x 24 x 24 x 2.6 < 1e-4."""
+    (out, lse), (ro, rl) = got, ref
+    assert (out.double() - ro).abs().max() <= 1.01 * 2 ** -8 * (top + ro.abs().max())
+    assert (lse.double() - rl).abs().max() <= 2e-4
+
+
+@pytest.mark.parametrize("heads", [1, 5, 16, 17, 32, 33, 64, 65, 128])
+@pytest.mark.parametrize("page", [16, 64])
+def test_heads_and_lengths(heads, page):
+    lens = [1, 15, 16, 17, 63, 64, 65, 111, 112, 113, 127, 128, 129, 250, 700]
+    t, q, cache, dec = make(heads, lens, page, seed=heads)
+    dec.plan(*t[:3])
+    out, lse = dec.run(q, cache)
+    close((out, lse), reference(q, cache, lens, t, page), cache.abs().max().double())
+    assert dec.device_error() == 0
+
+
+@pytest.mark.parametrize("heads", [16, 32, 64, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(num_ctas=3), dict(chunk_rule="search")])
+def test_split_requests(heads, kw):
+    lens = [9001, 3, 1500]
+    t, q, cache, dec = make(heads, lens, 16, seed=1, **kw)
+    dec.plan(*t[:3])
+    out, lse = dec.run(q, cache)
+    close((out, lse), reference(q, cache, lens, t, 16), cache.abs().max().double())
+    out2, lse2 = dec.run(q, cache)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert dec.device_error() == 0
+
+
+def test_rising_scores_rescale():
+    """Scores that grow along the sequence raise the softmax base in every tile."""
+    lens = [1000]
+    t, q, cache, dec = make(64, lens, 16, seed=2, min_chunk_tokens=4096)
+    ramp = torch.linspace(0.0, 8.0, 1008, device="cuda")
+    at = torch.from_numpy(t[1]).long().cuda()
+    flat = cache[at].reshape(-1, ROW)
+    flat[:, 512:] = ramp[:, None].bfloat16()
+    cache[at] = flat.view(-1, 16, ROW)
+    q[:, :, 512:] = 1.0 / 4
+    dec.plan(*t[:3])
+    out, lse = dec.run(q, cache)
+    close((out, lse), reference(q, cache, lens, t, 16), cache.abs().max().double())
+
+
+def test_stale_slots_are_not_read():
+    """NaN and infinities behind the last token, and in pages of the pool that are not the request's."""
+    lens = [5, 130, 64]
+    t, q, cache, dec = make(40, lens, 16, seed=3)
+    ref = reference(q, cache, lens, t, 16)
+    dirty = torch.full_like(cache, float("nan"))
+    dirty[::2] = float("inf")
+    for i, n in enumerate(lens):
+        for k in range(n):
+            pg, sl = int(t[1][t[0][i] + k // 16]), k % 16
+            dirty[pg, sl] = cache[pg, sl]
+    dec.plan(*t[:3])
+    out, lse = dec.run(q, dirty)
+    close((out, lse), ref, cache.abs().max().double())
+
+
+def test_infinite_scores_in_one_place():
+    """A score of -inf weighs nothing; a head whose scores are all -inf is an empty state."""
+    lens = [40]
+    t, q, cache, dec = make(16, lens, 16, seed=4)
+    cache[:, :, 575] = 0.0
+    first = int(t[1][0])
+    cache[first, 3, 575] = float("inf")
+    q[:, :, 575] = -1.0
+    dec.plan(*t[:3])
+    out, lse = dec.run(q, cache)
+    ref = reference(q, cache, lens, t, 16)
+    close((out, lse), ref, 6.0)
+    cache[:, :, 575] = float("inf")
+    out, lse = dec.run(q, cache)
+    assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+def test_v_scale_and_no_lse():
+    lens = [77, 200]
+    t, q, cache, dec = make(20, lens, 16, seed=5)
+    dec.plan(*t[:3])
+    out = dec.run(q, cache, return_lse=False)
+    assert torch.equal(out, dec.run(q, cache)[0])
+
+
+def test_append_then_decode_in_a_graph():
+    """Two steps of a serving loop: append, plan, replayed decode, against the formulas."""
+    page, lens, heads = 16, [31, 64, 1], 16
+    t = table([n + 2 for n in lens], page, 7)
+    cache = torch.randn(t[3], page, ROW, device="cuda").bfloat16()
+    q = torch.empty(len(lens), heads, ROW, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(len(lens), heads, DIM, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(len(lens), heads, device="cuda")
+    dec = pkd.BatchLatentDecodeWithPagedCache(heads, DIM, 64, page, scale=SCALE, max_batch=3,
+                                              max_num_pages=len(t[1]), num_pages=t[3])
+    graph = None
+    for step in range(2):
+        now = [n + step + 1 for n in lens]
+        counts = [-(-n // page) for n in now]
+        indptr = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        indices = np.concatenate([t[1][t[0][i]:t[0][i] + c] for i, c in enumerate(counts)])
+        last = np.array([n - page * (c - 1) for n, c in zip(now, counts)], np.int32)
+        both = torch.randn(3, 600, device="cuda").bfloat16()
+        before = cache.clone()
+        pkd.append_latent(both[:, :512], both[:, 512:576], torch.arange(3, device="cuda").int(),
+                          torch.tensor([n - 1 for n in now], device="cuda").int(),
+                          torch.from_numpy(indptr).cuda(), torch.from_numpy(indices).cuda(),
+                          torch.from_numpy(last).cuda(), cache)
+        for i, n in enumerate(now):
+            before[int(indices[indptr[i] + (n - 1) // page]), (n - 1) % page] = both[i, :576]
+        assert torch.equal(before, cache)
+        q.copy_(torch.randn_like(q))
+        dec.plan(indptr, indices, last)
+        if graph is None:
+            graph = dec.capture([q], [cache], [out], [lse])
+        graph.launch()
+        ref = reference(q, cache, now, (indptr, indices), page)
+        close((out, lse), ref, cache.abs().max().double())
+
+
+def test_append_skips_and_flags():
+    page = 16
+    t = table([20, 5], page)
+    d = [torch.from_numpy(x).cuda() for x in t[:3]]
+    cache = torch.zeros(t[3], page, ROW, dtype=torch.bfloat16, device="cuda")
+    new = torch.ones(5, ROW, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rows = torch.tensor([0, 0, 1, 2, -1], device="cuda").int()
+    at = torch.tensor([19, 20, 4, 0, 0], device="cuda").int()   # 20 and requests 2, -1: outside
+    pkd.append_latent(new[:, :512], new[:, 512:], rows, at, *d, cache, err=err)
+    assert err.item() == pkd.DEV_ERR_BOUNDS
+    assert int((cache != 0).any(-1).sum()) == 2
+    assert cache[int(t[1][1]), 3].all() and cache[int(t[1][2]), 4].all()
+    pkd.append_latent(new[:0, :512], new[:0, 512:], rows[:0], at[:0], *d, cache)
+
+
+def test_other_stream_and_refusals():
+    lens = [100]
+    t, q, cache, dec = make(16, lens, 16, seed=8)
+    with pytest.raises(pkd.PkdError):
+        dec.run(q, cache)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        dec.plan(*t[:3])
+        got = dec.run(q, cache)
+    s.synchronize()
+    close(got, reference(q, cache, lens, t, 16), cache.abs().max().double())
+    for bad in (q.float(), q[:, :8], q[:, :, :512].contiguous()):
+        with pytest.raises((TypeError, ValueError)):
+            dec.run(bad, cache)
+    with pytest.raises(ValueError):
+        dec.run(q, cache[:, :, :512])
+    with pytest.raises(pkd.PkdError):
+        dec.plan_cascade(None, None, None)
+    for kw in (dict(num_heads=129), dict(num_heads=0), dict(page_size=8), dict(latent_dim=256)):
+        args = dict(num_heads=16, latent_dim=512, rope_dim=64, page_size=16)
+        args.update(kw)
+        with pytest.raises(pkd.PkdError):
+            pkd.BatchLatentDecodeWithPagedCache(**args, scale=1.0, max_batch=1, max_num_pages=4,
+                                                num_pages=4)
+    with pytest.raises(ValueError):
+        pkd.append_latent(q[0, :, :512].t(), q[0, :, 512:], *[torch.zeros(16, device="cuda").int()] * 4,
+                          torch.zeros(15, device="cuda").int(), cache)
