@@ -370,6 +370,70 @@ int pkd_append_kv_layers(int32_t layers, const void *const *k_new, const void *c
                          int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
                          int32_t head_dim, uint32_t flags, int32_t *err, void *stream);
 
+/* Add the attention weight of every cached token in this step to its running
+ * sum.  For the current plan (pkd_plan; contexts without PKD_FLAG_
+ * SHARED_PREFIX, CASCADE and LATENT), request b, KV head h and token t in
+ * page p at slot s:
+ *     w = sum over the g query heads j of h of
+ *         exp(k_scale * q[b][j] . k_t / sqrt(D) - lse[b][j])
+ *     weights[p][h][s] = (t is new ? 0 : weights[p][h][s]) + w
+ * lse is what pkd_run returned for the same q, cache and k_scale; a head whose
+ * lse is -inf adds nothing.  The last new_tokens[b] tokens of request b are
+ * new: their sums start from zero, whatever the slot held, and with positions
+ * their slots get positions[p][h][s] = seen[b] - l_b + t, t counted from 0 in
+ * the request's present length l_b (seen: tokens the request has had in all,
+ * evicted ones included).
+ *   q, kv               : as for pkd_run
+ *   lse                 : device fp32 [batch][Hq]
+ *   weights             : device fp32 [num_pages][Hkv][P], updated in place
+ *   positions           : device int32 [num_pages][Hkv][P], or NULL
+ *   new_tokens, seen    : device int32 [batch]; new_tokens may be NULL (no new
+ *                         token), positions needs both
+ * Slots behind a request's end and pages of no request keep their values.
+ * A page has one owner: a plan that names a page twice is BAD_TABLE (a graph
+ * replayed under a later plan relies on that plan being free of repeats).
+ * expect_epoch as in pkd_run.  One kernel, stream-ordered, capturable, the
+ * same bits every run.
+ * Errors: INVALID_ARG, NO_PLAN, STALE_PLAN, BAD_TABLE, CAPACITY (no host
+ * memory for the check), CUDA. */
+int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const float *lse,
+                           float *weights, int32_t *positions, const int32_t *new_tokens,
+                           const int32_t *seen, float k_scale, uint64_t expect_epoch,
+                           void *stream);
+
+/* Cut every request of more than `budget` tokens to `budget`, in place, by
+ * its tokens' accumulated weights -- for 1 to 128 layers in one launch, each
+ * with its own cache, weights and positions.
+ * Per layer, request and KV head (per_head 1), or per layer and request by
+ * the sum of the heads' weights (per_head 0; positions of head 0 count), the
+ * `budget` tokens of largest weight stay; tokens with position < sinks or
+ * >= seen[b] - recent stay before all others (sinks + recent <= budget);
+ * equal weights: the lower slot first; NaN counts as the lowest.  Slots are
+ * closed up without keeping an order (attention does not depend on it): the
+ * i-th slot below `budget` whose token goes takes the i-th kept token from
+ * the slots behind, its K and V rows, weight and position.  A request's first
+ * `budget` slots then are its cache; what lies behind is left as it was, and
+ * the caller's next table ends there (requests of at most `budget` tokens are
+ * not touched).
+ *   kv, weights, positions : HOST arrays of `layers` device pointers, read
+ *       before the call returns, all different: bf16 or (PKD_FLAG_KV_FP8)
+ *       E4M3 [num_pages][2][P][Hkv][D] or (PKD_FLAG_HND)
+ *       [num_pages][2][Hkv][P][D]; fp32 and int32 [num_pages][Hkv][P]
+ *   indptr [batch + 1], indices, last_page_len [batch], seen [batch] : device
+ *       int32, the table before the eviction; a page may stand in it once
+ *   max_len : at least the longest request's tokens, at most 262,144
+ *   err     : device int32 word or NULL
+ * A request whose table row is wrong, is longer than max_len or names a page
+ * outside the pool is left as it is and PKD_DEV_ERR_BOUNDS is OR-ed into *err.
+ * One kernel, stream-ordered, capturable, the same bits every run.
+ * Errors: INVALID_ARG, CAPACITY (max_len), CUDA. */
+int pkd_evict_kv(int32_t layers, void *const *kv, float *const *weights,
+                 int32_t *const *positions, const int32_t *indptr, const int32_t *indices,
+                 const int32_t *last_page_len, const int32_t *seen, int32_t batch,
+                 int32_t max_len, int32_t budget, int32_t sinks, int32_t recent,
+                 int32_t per_head, int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                 int32_t head_dim, uint32_t flags, int32_t *err, void *stream);
+
 /* Write n new tokens' rows into a latent cache (PKD_FLAG_LATENT): token i's
  * row is latent_new[i] (512 bf16) then rope_new[i] (64 bf16), the slot rule
  * and the table are pkd_append_kv's.  Rows of latent_new / rope_new start
@@ -455,7 +519,8 @@ int pkd_plan_host_cascade(const pkd_config *cfg, const int32_t *group_indptr,
  *   off[2] units[num_units][2] = {req, num_chunks}
  *   off[3] merge_indptr[num_units + 1]
  *   off[4] page_list[nnz]    (the CSR indices, unchanged)
- *   off[5] total words
+ *   off[5] total words (the page list's capacity, then max_batch words: plain
+ *          plans put the requests' lengths behind the page list's nnz words)
  * Header words 0..31 hold: magic, batch, Hq, Hkv, D, P, num_ctas,
  * num_items, num_units, num_slots, chunk, alpha, nnz, makespan (clamped to
  * int32), split floor, requests per block, the most chunks of any split

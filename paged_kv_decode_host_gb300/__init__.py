@@ -19,6 +19,9 @@ API (names follow the pages' plan / run / merge_states):
 * :func:`plan_host` -- the scheduler alone on the host (no GPU), for tests.
 * :class:`BatchLatentDecodeWithPagedCache`, :func:`append_latent` -- the same
   plan / run / append over a cache of one latent vector per token.
+* :meth:`BatchDecodeWithPagedKVCache.accumulate_weights`, :func:`evict_kv`,
+  :func:`evicted_table` -- a cache cut to a budget of tokens by the attention
+  weight they have received.
 * ``cascade=True`` contexts: ``plan_cascade(group_indptr, prefix, suffix)``
   plans a shared prefix and every request's own suffix together; ``run``
   returns attention over both, merged.
@@ -34,7 +37,7 @@ import numpy as np
 __all__ = [
     "build", "load", "PkdError", "BatchDecodeWithPagedKVCache",
     "BatchLatentDecodeWithPagedCache", "merge_states", "append_kv",
-    "append_kv_layers", "append_latent", "plan_host", "plan_host_shared", "plan_host_cascade", "advise_format",
+    "append_kv_layers", "append_latent", "evict_kv", "evicted_table", "plan_host", "plan_host_shared", "plan_host_cascade", "advise_format",
     "schedule_layout",
     "selftest_bounded_wait", "Graph",
     "STATUS",
@@ -63,6 +66,7 @@ EXPORTS = (
     "pkd_append_kv", "pkd_append_kv_ex", "pkd_plan_shared", "pkd_plan_host_shared", "pkd_run_scaled",
     "pkd_selftest_bounded_wait", "pkd_append_kv_layers", "pkd_static_scratch_last_error",
     "pkd_plan_cascade", "pkd_plan_host_cascade", "pkd_advise_format", "pkd_append_latent",
+    "pkd_accumulate_weights", "pkd_evict_kv",
 )
 
 
@@ -173,6 +177,10 @@ def load():
     i64 = ctypes.c_int64
     sig["pkd_append_latent"] = (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i32, vp, vp, vp, i32, vp,
                                                i32, i32, vp, vp])
+    sig["pkd_accumulate_weights"] = (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp,
+                                                    ctypes.c_float, u64, vp])
+    sig["pkd_evict_kv"] = (ctypes.c_int, [i32, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                          i32, i32, i32, i32, i32, u32, vp, vp])
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
         f.restype = res
@@ -659,6 +667,45 @@ class BatchDecodeWithPagedKVCache:
         _check(st, "pkd_run")
         return (out, lse) if return_lse else out
 
+    def accumulate_weights(self, q, kv_cache, lse, weights, *, positions=None, new_tokens=None,
+                           seen=None, k_scale=1.0, expect_epoch=0, stream=None):
+        """Add every cached token's attention weight in this step to its
+        running sum, for the current plan (of :meth:`plan`).
+
+        weights [pages, Hkv, P] float32, updated in place: += the sum over the
+        KV head's query heads of exp(k_scale q . k / sqrt(D) - lse), with q,
+        kv_cache, k_scale as given to :meth:`run` and the lse it returned.
+        new_tokens [batch] int32: that many tokens at a request's end are new,
+        their sums start from zero; with positions [pages, Hkv, P] int32 and
+        seen [batch] int32 (tokens the request has had in all) the new tokens'
+        positions in the request are written there.  A page may stand in the
+        plan once.  Returns weights."""
+        import torch
+        if self.batch is None:
+            raise PkdError(-5, "accumulate_weights before plan")
+        B, f32, i32 = self.batch, torch.float32, torch.int32
+        per_slot = (self.num_pages, self.hkv, self.p)
+        if positions is not None and (new_tokens is None or seen is None):
+            raise ValueError("positions needs new_tokens and seen")
+        self._check_run_args(q, kv_cache, q, lse)
+        for name, t, dt, shape in (("lse", lse, f32, (B, self.hq)),
+                                   ("weights", weights, f32, per_slot),
+                                   ("positions", positions, i32, per_slot),
+                                   ("new_tokens", new_tokens, i32, (B,)),
+                                   ("seen", seen, i32, (B,))):
+            if t is None and name != "lse":
+                continue
+            if t is None or t.dtype != dt or t.shape != shape or not t.is_contiguous() \
+                    or t.device != q.device:
+                raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)} on "
+                                 f"{q.device}")
+        ptr = lambda t: t.data_ptr() if t is not None else 0
+        _check(self._lib.pkd_accumulate_weights(
+            self._h, q.data_ptr(), kv_cache.data_ptr(), lse.data_ptr(), weights.data_ptr(),
+            ptr(positions), ptr(new_tokens), ptr(seen), float(k_scale), int(expect_epoch),
+            _stream_ptr(stream)), "pkd_accumulate_weights")
+        return weights
+
     def capture(self, qs, kvs, outs, lses=None, timing=False, kv_scales=None, host_qs=None,
                 host_outs=None, host_lses=None) -> Graph:
         """Capture len(qs) runs (one decode step over all layers) in a graph.
@@ -793,6 +840,9 @@ class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
         raise PkdError(-1, "a latent context plans requests of their own (plan)")
 
     plan_cascade = plan_shared
+
+    def accumulate_weights(self, *args, **kwargs):
+        raise PkdError(-1, "weights are accumulated for K / V caches")
 
 
 def selftest_bounded_wait(mode=0, device=None):
@@ -987,6 +1037,96 @@ def append_latent(latent_new, rope_new, batch_indices, positions, indptr, indice
             _stream_ptr(stream))
     _check(st, "pkd_append_latent")
     return cache
+
+
+def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen, budget, *,
+             max_len, sinks=0, recent=0, per_head=True, kv_layout="NHD", err=None, stream=None):
+    """Cut every request of more than ``budget`` tokens to ``budget``, in
+    place, keeping the tokens of largest accumulated weight; all layers in one
+    launch.
+
+    kv_caches, weights, positions: one tensor per layer (lists of 1 to 128):
+    caches as for :func:`append_kv`, weights float32 and positions int32
+    [pages, Hkv, P] as :meth:`BatchDecodeWithPagedKVCache.accumulate_weights`
+    keeps them.  indptr / indices / last_page_len / seen: int32 CUDA tensors,
+    the table and the tokens seen; max_len: at least the longest request's
+    tokens (at most 262,144).  Tokens at positions below ``sinks`` and among
+    the last ``recent`` always stay.  per_head: every KV head keeps its own
+    tokens; else all keep the same, by the sum of their weights.  Slots are
+    closed up without keeping their order: afterwards the request's first
+    ``budget`` slots are its cache (:func:`evicted_table` gives the table).
+    err: optional int32 CUDA tensor of one element, flagged for requests whose
+    table is wrong (they are left as they are)."""
+    import torch
+    layers = len(kv_caches)
+    if not 1 <= layers <= 128 or len(weights) != layers or len(positions) != layers:
+        raise ValueError("one cache, weights and positions tensor per layer, 1 to 128 layers")
+    if kv_layout not in ("NHD", "HND"):
+        raise ValueError("kv_layout must be 'NHD' or 'HND'")
+    c0 = kv_caches[0]
+    fp8 = c0.dtype in (torch.float8_e4m3fn, torch.uint8)
+    if not fp8 and c0.dtype != torch.bfloat16:
+        raise TypeError("caches must be bfloat16 or e4m3")
+    if c0.dim() != 5 or c0.shape[1] != 2:
+        raise ValueError("caches must be [pages, 2, P, Hkv, D] or [pages, 2, Hkv, P, D]")
+    pages, _, P, hkv, D = c0.shape
+    if kv_layout == "HND":
+        P, hkv = hkv, P
+    per_slot = (pages, hkv, P)
+    for l in range(layers):
+        for name, t, dt, shape in (("kv_caches", kv_caches[l], c0.dtype, c0.shape),
+                                   ("weights", weights[l], torch.float32, per_slot),
+                                   ("positions", positions[l], torch.int32, per_slot)):
+            if t.dtype != dt or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name}[{l}] must be a contiguous CUDA {dt} tensor {list(shape)}")
+    for name, t in (("indptr", indptr), ("indices", indices), ("last_page_len", last_page_len),
+                    ("seen", seen)):
+        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous CUDA int32 tensor")
+    batch = int(last_page_len.numel())
+    if indptr.numel() != batch + 1 or seen.numel() != batch:
+        raise ValueError("indptr needs batch + 1 entries, seen batch")
+    if err is not None and (err.dtype != torch.int32 or not err.is_cuda):
+        raise TypeError("err must be an int32 CUDA tensor")
+    _one_device(*kv_caches, *weights, *positions, indptr, indices, last_page_len, seen, err)
+
+    def ptrs(ts):
+        return (ctypes.c_void_p * layers)(*[t.data_ptr() for t in ts])
+
+    with torch.cuda.device(c0.device):
+        st = load().pkd_evict_kv(
+            layers, ptrs(kv_caches), ptrs(weights), ptrs(positions), indptr.data_ptr(),
+            indices.data_ptr(), last_page_len.data_ptr(), seen.data_ptr(), batch, int(max_len),
+            int(budget), int(sinks), int(recent), 1 if per_head else 0, int(pages), int(P),
+            int(hkv), int(D), (FLAG_HND if kv_layout == "HND" else 0) | (FLAG_KV_FP8 if fp8 else 0),
+            err.data_ptr() if err is not None else 0, _stream_ptr(stream))
+    _check(st, "pkd_evict_kv")
+
+
+def evicted_table(indptr, indices, last_page_len, page_size, budget):
+    """The page table after :func:`evict_kv` with this budget, on the host:
+    (indptr, indices, last_page_len, freed page ids), int32 arrays.  Raises
+    PkdError (PKD_E_BAD_TABLE) for a wrong table and for one that names a page
+    twice, which an eviction must not."""
+    indptr, indices, last = _host_i32(indptr), _host_i32(indices), _host_i32(last_page_len)
+    if budget < 1 or page_size < 1:
+        raise ValueError("budget and page_size must be at least 1")
+    batch = last.shape[0]
+    if indptr.shape[0] != batch + 1 or (batch and indptr[0] != 0):
+        raise PkdError(-2, "indptr must start at 0 and have batch + 1 entries")
+    counts = np.diff(indptr.astype(np.int64))
+    used = int(indptr[-1]) if batch else 0
+    if (counts < 1).any() or (last < 1).any() or (last > page_size).any() or used > indices.shape[0]:
+        raise PkdError(-2, "wrong page table")
+    if np.unique(indices[:used]).size != used:
+        raise PkdError(-2, "a page stands in the table twice")
+    lens = page_size * (counts - 1) + last
+    now = np.minimum(lens, budget)
+    left = -(-now // page_size)
+    keep = np.arange(used) - np.repeat(indptr[:-1], counts) < np.repeat(left, counts)
+    ids = indices[:used]
+    return (np.concatenate([[0], np.cumsum(left)]).astype(np.int32), np.ascontiguousarray(ids[keep]),
+            (now - page_size * (left - 1)).astype(np.int32), np.ascontiguousarray(ids[~keep]))
 
 
 def _one_device(*tensors):

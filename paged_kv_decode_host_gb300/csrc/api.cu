@@ -11,11 +11,13 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <new>
 #include <vector>
 
 #include "append_layers.h"
+#include "evict.h"
 #include "pkd_internal.h"
 
 using namespace pkd;
@@ -48,6 +50,9 @@ struct pkd_ctx {
   uint64_t epoch = 0;
   pkd_plan_info info{};
   int32_t max_chunks = 0;   // header word H_MAXCHUNKS of the published plan
+  // whether the current plan names a page twice, looked up when first asked
+  uint64_t pages_epoch = 0;
+  bool pages_twice = false;
 };
 
 struct pkd_graph {
@@ -516,7 +521,7 @@ static int plan_and_publish(pkd_ctx* ctx, PlanFn plan_fn, void* stream, uint64_t
   // sees the whole schedule
   words[H_EPOCH] = epoch_word(ctx->epoch + 1);
   if (cudaMemcpyAsync(ctx->ws + (size_t)H_WORDS * 4, words + H_WORDS,
-                      ((size_t)L.page_list + (size_t)info.nnz - H_WORDS) * 4,
+                      ((size_t)L.page_list + (size_t)info.nnz + (size_t)info.batch - H_WORDS) * 4,
                       cudaMemcpyHostToDevice, s) != cudaSuccess ||
       cudaMemcpyAsync(ctx->ws, words, (size_t)H_WORDS * 4, cudaMemcpyHostToDevice, s) !=
           cudaSuccess)
@@ -712,6 +717,126 @@ int pkd_append_latent(const void* latent_new, int64_t latent_stride, const void*
                            static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return PKD_E_CUDA;
   return PKD_OK;
+}
+
+int pkd_accumulate_weights(pkd_ctx* ctx, const void* q, const void* kv, const float* lse,
+                           float* weights, int32_t* positions, const int32_t* new_tokens,
+                           const int32_t* seen, float k_scale, uint64_t expect_epoch,
+                           void* stream) {
+  if (ctx == nullptr || !std::isfinite(k_scale)) return PKD_E_INVALID_ARG;
+  if (ctx->kind.block || ctx->kind.cascade || ctx->kind.latent) return PKD_E_INVALID_ARG;
+  if (ctx->epoch == 0) return PKD_E_NO_PLAN;
+  if (expect_epoch != 0 && expect_epoch != ctx->epoch) return PKD_E_STALE_PLAN;
+  if (ctx->info.batch == 0) return PKD_OK;
+  if (!q || !kv || !lse || !weights || (positions && (!new_tokens || !seen)))
+    return PKD_E_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(lse, 4) || !aligned(weights, 4) ||
+      !aligned(positions, 4) || !aligned(new_tokens, 4) || !aligned(seen, 4))
+    return PKD_E_INVALID_ARG;
+  const pkd_config& c = ctx->cfg;
+  if (ctx->pages_epoch != ctx->epoch) {
+    // every slot's sum has one owner: a page may stand in the table once
+    const int32_t* pages = ctx->staging[ctx->next_staging ^ 1] + ctx->layout.page_list;
+    uint64_t* seen_pages = static_cast<uint64_t*>(std::calloc(((size_t)c.num_pages + 63) / 64, 8));
+    if (seen_pages == nullptr) return PKD_E_CAPACITY;
+    bool twice = false;
+    for (int32_t i = 0; i < ctx->info.nnz; ++i) {
+      uint64_t& w = seen_pages[pages[i] / 64];
+      const uint64_t bit = (uint64_t)1 << (pages[i] % 64);
+      twice |= (w & bit) != 0;
+      w |= bit;
+    }
+    std::free(seen_pages);
+    ctx->pages_twice = twice;
+    ctx->pages_epoch = ctx->epoch;
+  }
+  if (ctx->pages_twice) return PKD_E_BAD_TABLE;
+  const int elem = ctx->kind.fp8 ? 1 : 2;
+  const bool hnd = (c.flags & PKD_FLAG_HND) != 0;
+  WeightsArgs a{};
+  a.sched = reinterpret_cast<const int32_t*>(ctx->ws);
+  a.err = reinterpret_cast<int32_t*>(ctx->ws + ctx->layout.err_byte);
+  a.q = static_cast<const uint16_t*>(q);
+  a.kv = static_cast<const uint8_t*>(kv);
+  a.lse = lse;
+  a.weights = weights;
+  a.positions = positions;
+  a.new_tokens = new_tokens;
+  a.seen = seen;
+  a.off_cta = ctx->layout.cta_indptr;
+  a.off_items = ctx->layout.items;
+  a.off_pages = ctx->layout.page_list;
+  const int64_t head = (int64_t)kHeadDim * elem;
+  a.page_bytes = 2 * (int64_t)c.page_size * c.num_kv_heads * head;
+  a.token_bytes = hnd ? head : head * c.num_kv_heads;
+  a.head_bytes = hnd ? head * c.page_size : head;
+  a.hq = c.num_qo_heads;
+  a.hkv = c.num_kv_heads;
+  a.page_size = c.page_size;
+  a.num_pages = c.num_pages;
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kHeadDim) * (double)k_scale);
+  a.wait_epoch = expect_epoch != 0 ? epoch_word(expect_epoch) : 0;
+  return launch_weights(a, ctx->kind.fp8, ctx->n_cta, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? PKD_OK
+             : PKD_E_CUDA;
+}
+
+int pkd_evict_kv(int32_t layers, void* const* kv, float* const* weights,
+                 int32_t* const* positions, const int32_t* indptr, const int32_t* indices,
+                 const int32_t* last_page_len, const int32_t* seen, int32_t batch,
+                 int32_t max_len, int32_t budget, int32_t sinks, int32_t recent, int32_t per_head,
+                 int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                 uint32_t flags, int32_t* err, void* stream) {
+  if ((flags & ~(PKD_FLAG_HND | PKD_FLAG_KV_FP8)) != 0) return PKD_E_INVALID_ARG;
+  if (layers < 1 || layers > kMaxEvictLayers || !kv || !weights || !positions)
+    return PKD_E_INVALID_ARG;
+  const int elem = (flags & PKD_FLAG_KV_FP8) ? 1 : 2;
+  if (batch < 0 || max_len < 0 || budget < 1 || sinks < 0 || recent < 0 ||
+      (int64_t)sinks + recent > budget || (per_head != 0 && per_head != 1) || num_pages < 1 ||
+      page_size < 1 || num_kv_heads < 1 || head_dim < 1 || ((int64_t)head_dim * elem) % 16 != 0)
+    return PKD_E_INVALID_ARG;
+  if (max_len > kEvictMaxTokens) return PKD_E_CAPACITY;
+  const int64_t head = (int64_t)head_dim * elem;
+  if (head * num_kv_heads > (1 << 20) ||
+      (int64_t)layers * batch * num_kv_heads * 8 > 0x7fffffffLL)
+    return PKD_E_INVALID_ARG;
+  if (batch == 0 || max_len <= budget) return PKD_OK;   // nothing is over the budget
+  if (!indptr || !indices || !last_page_len || !seen || !aligned(err, 4)) return PKD_E_INVALID_ARG;
+  const bool hnd = (flags & PKD_FLAG_HND) != 0;
+  EvictArgs a{};
+  for (int32_t l = 0; l < layers; ++l) {
+    if (!kv[l] || !weights[l] || !positions[l] || !aligned(kv[l], 16) || !aligned(weights[l], 4) ||
+        !aligned(positions[l], 4))
+      return PKD_E_INVALID_ARG;
+    for (int32_t m = 0; m < l; ++m)   // two layers on one cache would race
+      if (kv[m] == kv[l] || weights[m] == weights[l] || positions[m] == positions[l])
+        return PKD_E_INVALID_ARG;
+    a.kv[l] = kv[l];
+    a.weights[l] = weights[l];
+    a.positions[l] = positions[l];
+  }
+  a.indptr = indptr;
+  a.indices = indices;
+  a.last = last_page_len;
+  a.seen = seen;
+  a.err = err;
+  a.layers = layers;
+  a.batch = batch;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.hkv = num_kv_heads;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.per_head = per_head;
+  a.max_len = max_len;
+  a.v_bytes = (int64_t)page_size * num_kv_heads * head;
+  a.page_bytes = 2 * a.v_bytes;
+  a.token_bytes = hnd ? head : head * num_kv_heads;
+  a.head_bytes = hnd ? head * page_size : head;
+  a.pieces = (int32_t)(head / 16);
+  return launch_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKD_OK : PKD_E_CUDA;
 }
 
 int pkd_last_device_error(pkd_ctx* ctx, void* stream, int32_t* dev_err) {

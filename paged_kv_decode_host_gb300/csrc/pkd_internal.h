@@ -104,7 +104,7 @@ struct Layout {
   int64_t units;         // [max_items][2]
   int64_t merge_indptr;  // [max_items + 1]
   int64_t page_list;     // [max_num_pages]
-  int64_t words;         // schedule words (end of page_list)
+  int64_t words;         // schedule words (end of page_list and the lengths behind it)
   int64_t max_items;
   int64_t max_slots;     // partial-state slots
   // byte offsets inside the device workspace
@@ -160,7 +160,8 @@ inline Layout make_layout(const pkd_config& c, int64_t n_cta) {
   L.units = L.items + L.max_items * kItemWords;
   L.merge_indptr = L.units + L.max_items * 2;
   L.page_list = align_up(L.merge_indptr + L.max_items + 1, 4);
-  L.words = L.page_list + c.max_num_pages;
+  // behind the page list: plain plans' request lengths, from word nnz on
+  L.words = L.page_list + c.max_num_pages + c.max_batch;
   size_t sched_bytes = (size_t)L.words * 4;
   L.err_byte = (size_t)align_up((int64_t)sched_bytes, 256);
   L.o_part_byte = L.err_byte + 256;

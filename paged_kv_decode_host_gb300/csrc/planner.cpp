@@ -253,6 +253,8 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     // page ids go into the schedule verbatim (the kernel reads a table row's
     // pages at indptr[row] + t / P), range-checked in the same pass
     if (!copy_checked(indices, words + L.page_list, nnz, cfg.num_pages)) return PKD_E_BAD_TABLE;
+    if (!group_indptr)   // the requests' lengths, for kernels that ask where a request ends
+      for (int32_t i = 0; i < n_rows; ++i) words[L.page_list + nnz + i] = (int32_t)row_len[i];
   }
 
   // ---- row blocks
