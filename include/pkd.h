@@ -422,17 +422,27 @@ int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const fl
  *   indptr [batch + 1], indices, last_page_len [batch], seen [batch] : device
  *       int32, the table before the eviction; a page may stand in it once
  *   max_len : at least the longest request's tokens, at most 262,144
+ *   d_workspace : pkd_evict_workspace_bytes(...) bytes, 16-byte aligned, the
+ *       call's own until its kernels are done (NULL when that is 0)
+ *   D * element bytes: a multiple of 16; Hkv * D * element bytes <= 32,768
  *   err     : device int32 word or NULL
  * A request whose table row is wrong, is longer than max_len or names a page
  * outside the pool is left as it is and PKD_DEV_ERR_BOUNDS is OR-ed into *err.
- * One kernel, stream-ordered, capturable, the same bits every run.
- * Errors: INVALID_ARG, CAPACITY (max_len), CUDA. */
+ * One or two kernels, stream-ordered, capturable, the same bits every run.
+ * Errors: INVALID_ARG, CAPACITY (max_len), WORKSPACE_TOO_SMALL, CUDA. */
 int pkd_evict_kv(int32_t layers, void *const *kv, float *const *weights,
                  int32_t *const *positions, const int32_t *indptr, const int32_t *indices,
                  const int32_t *last_page_len, const int32_t *seen, int32_t batch,
                  int32_t max_len, int32_t budget, int32_t sinks, int32_t recent,
                  int32_t per_head, int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
-                 int32_t head_dim, uint32_t flags, int32_t *err, void *stream);
+                 int32_t head_dim, uint32_t flags, void *d_workspace, size_t workspace_bytes,
+                 int32_t *err, void *stream);
+
+/* Device workspace of pkd_evict_kv for these arguments: a bit per token and
+ * job where few long requests are cut, else 0 (also for arguments that
+ * pkd_evict_kv refuses). */
+size_t pkd_evict_workspace_bytes(int32_t layers, int32_t batch, int32_t max_len, int32_t budget,
+                                 int32_t per_head, int32_t num_kv_heads);
 
 /* Write n new tokens' rows into a latent cache (PKD_FLAG_LATENT): token i's
  * row is latent_new[i] (512 bf16) then rope_new[i] (64 bf16), the slot rule

@@ -66,7 +66,7 @@ EXPORTS = (
     "pkd_append_kv", "pkd_append_kv_ex", "pkd_plan_shared", "pkd_plan_host_shared", "pkd_run_scaled",
     "pkd_selftest_bounded_wait", "pkd_append_kv_layers", "pkd_static_scratch_last_error",
     "pkd_plan_cascade", "pkd_plan_host_cascade", "pkd_advise_format", "pkd_append_latent",
-    "pkd_accumulate_weights", "pkd_evict_kv",
+    "pkd_accumulate_weights", "pkd_evict_kv", "pkd_evict_workspace_bytes",
 )
 
 
@@ -180,7 +180,8 @@ def load():
     sig["pkd_accumulate_weights"] = (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp,
                                                     ctypes.c_float, u64, vp])
     sig["pkd_evict_kv"] = (ctypes.c_int, [i32, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
-                                          i32, i32, i32, i32, i32, u32, vp, vp])
+                                          i32, i32, i32, i32, i32, u32, vp, sz, vp, vp])
+    sig["pkd_evict_workspace_bytes"] = (sz, [i32] * 6)
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
         f.restype = res
@@ -371,6 +372,52 @@ def _stream_ptr(stream=None):
         else:
             _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream
     return _current_raw_stream()
+
+
+class _On:
+    """Makes a tensor's device the current one for a call, when it is not."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, dev):
+        import torch
+        get = getattr(torch._C, "_cuda_getDevice", None)
+        self.guard = None if get is not None and get() == dev else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _table_args(dev, indptr, indices, last_page_len, **per_row):
+    """Checks of a device table (int32, contiguous, on device `dev`) and of
+    int32 tensors with one entry per request; returns the batch."""
+    import torch
+    i32 = torch.int32
+    for name, t in (("indptr", indptr), ("indices", indices), ("last_page_len", last_page_len),
+                    *per_row.items()):
+        if t.dtype is not i32 or not t.is_contiguous() or t.get_device() != dev:
+            raise TypeError(f"{name} must be a contiguous int32 tensor on cuda:{dev}")
+    batch = last_page_len.numel()
+    if indptr.numel() != batch + 1:
+        raise ValueError("indptr must have batch + 1 entries")
+    for name, t in per_row.items():
+        if t.numel() != batch:
+            raise ValueError(f"{name} must have one entry per request")
+    return batch
+
+
+def _err_arg(err, dev):
+    import torch
+    if err is None:
+        return 0
+    if err.dtype is not torch.int32 or err.get_device() != dev or err.numel() < 1:
+        raise TypeError(f"err must be an int32 tensor on cuda:{dev}")
+    return err.data_ptr()
 
 
 class Graph:
@@ -687,7 +734,8 @@ class BatchDecodeWithPagedKVCache:
         per_slot = (self.num_pages, self.hkv, self.p)
         if positions is not None and (new_tokens is None or seen is None):
             raise ValueError("positions needs new_tokens and seen")
-        self._check_run_args(q, kv_cache, q, lse)
+        self._check_run_args(q, kv_cache, q, None)
+        dev = q.get_device()
         for name, t, dt, shape in (("lse", lse, f32, (B, self.hq)),
                                    ("weights", weights, f32, per_slot),
                                    ("positions", positions, i32, per_slot),
@@ -695,15 +743,18 @@ class BatchDecodeWithPagedKVCache:
                                    ("seen", seen, i32, (B,))):
             if t is None and name != "lse":
                 continue
-            if t is None or t.dtype != dt or t.shape != shape or not t.is_contiguous() \
-                    or t.device != q.device:
+            if t is None or t.dtype is not dt or t.shape != shape or not t.is_contiguous() \
+                    or t.get_device() != dev:
                 raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)} on "
                                  f"{q.device}")
         ptr = lambda t: t.data_ptr() if t is not None else 0
-        _check(self._lib.pkd_accumulate_weights(
-            self._h, q.data_ptr(), kv_cache.data_ptr(), lse.data_ptr(), weights.data_ptr(),
-            ptr(positions), ptr(new_tokens), ptr(seen), float(k_scale), int(expect_epoch),
-            _stream_ptr(stream)), "pkd_accumulate_weights")
+        with _On(dev):
+            st = self._lib.pkd_accumulate_weights(
+                self._h, q.data_ptr(), kv_cache.data_ptr(), lse.data_ptr(), weights.data_ptr(),
+                ptr(positions), ptr(new_tokens), ptr(seen), k_scale, expect_epoch,
+                _stream_ptr(stream))
+        if st:
+            _check(st, "pkd_accumulate_weights")
         return weights
 
     def capture(self, qs, kvs, outs, lses=None, timing=False, kv_scales=None, host_qs=None,
@@ -801,33 +852,53 @@ class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
 
     def _check_run_args(self, q, kv_cache, out, lse):
         import torch
-        if self.batch is None:
+        B = self.batch
+        if B is None:
             raise PkdError(-5, "run before plan")
-        B, row = self.batch, LATENT_DIM + LATENT_ROPE
-        dev = q.device
-        for name, t, dt, shape in (("q", q, torch.bfloat16, (B, self.hq, row)),
-                                   ("cache", kv_cache, torch.bfloat16,
-                                    (self.num_pages, self.p, row)),
-                                   ("out", out, torch.bfloat16, (B, self.hq, self.d)),
-                                   ("lse", lse, torch.float32, (B, self.hq))):
+        if self._run_shapes is None or self._run_shapes[0] != B:
+            row = LATENT_DIM + LATENT_ROPE
+            self._run_shapes = (B, torch.Size((B, self.hq, row)),
+                                torch.Size((self.num_pages, self.p, row)),
+                                torch.Size((B, self.hq, self.d)), torch.Size((B, self.hq)))
+        _, qs, cs, os_, ls = self._run_shapes
+        bf, dev = torch.bfloat16, q.get_device()
+        if dev < 0 or self.device.index not in (None, dev):
+            raise ValueError(f"q is on {q.device}, the plan on {self.device}")
+        for name, t, dt, shape in (("q", q, bf, qs), ("cache", kv_cache, bf, cs),
+                                   ("out", out, bf, os_), ("lse", lse, torch.float32, ls)):
             if t is None:
                 continue
-            if t.dtype != dt:
+            if t.dtype is not dt:
                 raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name} shape {tuple(t.shape)} != {shape}")
+            if t.shape != shape:
+                raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-            if not t.is_cuda or t.device != dev or self.device.index not in (None, dev.index):
-                raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, q on {q.device}")
 
     def run(self, q, cache, out=None, lse=None, return_lse=True, expect_epoch=0, stream=None):
         """Attention for one layer.  Returns (out, lse) or out."""
         import torch
+        if self.batch is None:
+            raise PkdError(-5, "run before plan")
         if out is None:
-            out = torch.empty(*q.shape[:-1], self.d, dtype=torch.bfloat16, device=q.device)
-        return super().run(q, cache, out=out, lse=lse, return_lse=return_lse,
-                           expect_epoch=expect_epoch, stream=stream, k_scale=self.scale)
+            out = q.new_empty((q.shape[0], self.hq, self.d), dtype=torch.bfloat16)
+        if lse is None and return_lse:
+            lse = q.new_empty((q.shape[0], self.hq), dtype=torch.float32)
+        self._check_run_args(q, cache, out, lse)
+        fast, lp = _fast(), lse.data_ptr() if lse is not None else 0
+        with _On(q.get_device()):
+            s = _stream_ptr(stream)
+            st = _NOT_HANDLED if fast is None else fast.run(
+                self._hv, q.data_ptr(), cache.data_ptr(), out.data_ptr(), lp, self.scale, 1.0,
+                expect_epoch, s)
+            if st == _NOT_HANDLED:
+                st = self._lib.pkd_run_scaled(self._h, q.data_ptr(), cache.data_ptr(),
+                                              out.data_ptr(), lp, self.scale, 1.0, expect_epoch, s)
+        if st:
+            _check(st, "pkd_run")
+        return (out, lse) if return_lse else out
 
     def capture(self, qs, caches, outs, lses=None, timing=False, host_qs=None, host_outs=None,
                 host_lses=None) -> Graph:
@@ -1000,42 +1071,38 @@ def append_latent(latent_new, rope_new, batch_indices, positions, indptr, indice
     in place, not overlapping the inputs.  The table arguments and err are
     append_kv's."""
     import torch
-    bf = torch.bfloat16
-    for name, t, dt in (("cache", cache, bf), ("batch_indices", batch_indices, torch.int32),
-                        ("positions", positions, torch.int32), ("indptr", indptr, torch.int32),
-                        ("indices", indices, torch.int32),
-                        ("last_page_len", last_page_len, torch.int32)):
-        if t.dtype != dt or not t.is_cuda or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous CUDA {dt} tensor")
+    bf, i32 = torch.bfloat16, torch.int32
+    dev = cache.get_device()
+    if cache.dtype is not bf or dev < 0 or not cache.is_contiguous():
+        raise TypeError("cache must be a contiguous CUDA bfloat16 tensor")
     if cache.dim() != 3 or cache.shape[2] != LATENT_DIM + LATENT_ROPE:
         raise ValueError(f"cache must be [pages, P, {LATENT_DIM + LATENT_ROPE}]")
-    n = int(batch_indices.numel())
+    n = batch_indices.numel()
+    strides = []
     for name, t, width in (("latent_new", latent_new, LATENT_DIM),
                            ("rope_new", rope_new, LATENT_ROPE)):
-        if t.dtype != bf or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA {bf} tensor")
-        if tuple(t.shape) != (n, width):
+        if t.dtype is not bf or t.get_device() != dev:
+            raise TypeError(f"{name} must be a bfloat16 tensor on cuda:{dev}")
+        if t.shape != (n, width):
             raise ValueError(f"{name} must be [{n}, {width}]")
-        if n and (t.stride(1) != 1 or (n > 1 and (t.stride(0) < width or t.stride(0) % 8))
-                  or t.data_ptr() % 16):
+        row, col = t.stride()
+        if n and (col != 1 or (n > 1 and (row < width or row % 8)) or t.data_ptr() % 16):
             raise ValueError(f"{name}: contiguous rows on 16-byte boundaries are needed")
+        strides.append(row)
+    for name, t in (("batch_indices", batch_indices), ("positions", positions)):
+        if t.dtype is not i32 or not t.is_contiguous() or t.get_device() != dev:
+            raise TypeError(f"{name} must be a contiguous int32 tensor on cuda:{dev}")
     if positions.numel() != n:
         raise ValueError("batch_indices and positions need one entry per new token")
-    batch = int(last_page_len.numel())
-    if indptr.numel() != batch + 1:
-        raise ValueError("indptr must have batch + 1 entries")
-    if err is not None and (err.dtype != torch.int32 or not err.is_cuda):
-        raise TypeError("err must be an int32 CUDA tensor")
-    _one_device(cache, latent_new, rope_new, batch_indices, positions, indptr, indices,
-                last_page_len, err)
-    with torch.cuda.device(cache.device):
+    batch = _table_args(dev, indptr, indices, last_page_len)
+    with _On(dev):
         st = load().pkd_append_latent(
-            latent_new.data_ptr(), latent_new.stride(0), rope_new.data_ptr(), rope_new.stride(0),
+            latent_new.data_ptr(), strides[0], rope_new.data_ptr(), strides[1],
             batch_indices.data_ptr(), positions.data_ptr(), n, indptr.data_ptr(),
             indices.data_ptr(), last_page_len.data_ptr(), batch, cache.data_ptr(),
-            int(cache.shape[0]), int(cache.shape[1]), err.data_ptr() if err is not None else 0,
-            _stream_ptr(stream))
-    _check(st, "pkd_append_latent")
+            cache.shape[0], cache.shape[1], _err_arg(err, dev), _stream_ptr(stream))
+    if st:
+        _check(st, "pkd_append_latent")
     return cache
 
 
@@ -1069,38 +1136,40 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
         raise TypeError("caches must be bfloat16 or e4m3")
     if c0.dim() != 5 or c0.shape[1] != 2:
         raise ValueError("caches must be [pages, 2, P, Hkv, D] or [pages, 2, Hkv, P, D]")
-    pages, _, P, hkv, D = c0.shape
+    pages, _, P, hkv, D = shape = c0.shape
     if kv_layout == "HND":
         P, hkv = hkv, P
-    per_slot = (pages, hkv, P)
-    for l in range(layers):
-        for name, t, dt, shape in (("kv_caches", kv_caches[l], c0.dtype, c0.shape),
-                                   ("weights", weights[l], torch.float32, per_slot),
-                                   ("positions", positions[l], torch.int32, per_slot)):
-            if t.dtype != dt or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name}[{l}] must be a contiguous CUDA {dt} tensor {list(shape)}")
-    for name, t in (("indptr", indptr), ("indices", indices), ("last_page_len", last_page_len),
-                    ("seen", seen)):
-        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous CUDA int32 tensor")
-    batch = int(last_page_len.numel())
-    if indptr.numel() != batch + 1 or seen.numel() != batch:
-        raise ValueError("indptr needs batch + 1 entries, seen batch")
-    if err is not None and (err.dtype != torch.int32 or not err.is_cuda):
-        raise TypeError("err must be an int32 CUDA tensor")
-    _one_device(*kv_caches, *weights, *positions, indptr, indices, last_page_len, seen, err)
-
-    def ptrs(ts):
-        return (ctypes.c_void_p * layers)(*[t.data_ptr() for t in ts])
-
-    with torch.cuda.device(c0.device):
-        st = load().pkd_evict_kv(
-            layers, ptrs(kv_caches), ptrs(weights), ptrs(positions), indptr.data_ptr(),
-            indices.data_ptr(), last_page_len.data_ptr(), seen.data_ptr(), batch, int(max_len),
-            int(budget), int(sinks), int(recent), 1 if per_head else 0, int(pages), int(P),
-            int(hkv), int(D), (FLAG_HND if kv_layout == "HND" else 0) | (FLAG_KV_FP8 if fp8 else 0),
-            err.data_ptr() if err is not None else 0, _stream_ptr(stream))
-    _check(st, "pkd_evict_kv")
+    dev, dtype, f32, i32 = c0.get_device(), c0.dtype, torch.float32, torch.int32
+    per_slot = torch.Size((pages, hkv, P))
+    if dev < 0:
+        raise TypeError("caches must be on the GPU")
+    for name, ts, dt, size in (("kv_caches", kv_caches, dtype, shape),
+                               ("weights", weights, f32, per_slot),
+                               ("positions", positions, i32, per_slot)):
+        for l, t in enumerate(ts):
+            if t.dtype is not dt or t.shape != size or t.get_device() != dev or \
+                    not t.is_contiguous():
+                raise ValueError(f"{name}[{l}] must be a contiguous {dt} tensor {list(size)} on "
+                                 f"cuda:{dev}")
+    batch = _table_args(dev, indptr, indices, last_page_len, seen=seen)
+    ptrs = ctypes.c_void_p * layers
+    per_head = 1 if per_head else 0
+    lib = load()
+    with _On(dev):
+        # raises for sizes out of range only in the call itself
+        need = lib.pkd_evict_workspace_bytes(layers, batch, max_len, budget, per_head, hkv)
+        ws = torch.empty(need, dtype=torch.uint8, device=c0.device) if need else None
+        if need and stream is not None:
+            ws.record_stream(stream)
+        st = lib.pkd_evict_kv(
+            layers, ptrs(*[t.data_ptr() for t in kv_caches]),
+            ptrs(*[t.data_ptr() for t in weights]), ptrs(*[t.data_ptr() for t in positions]),
+            indptr.data_ptr(), indices.data_ptr(), last_page_len.data_ptr(), seen.data_ptr(), batch,
+            max_len, budget, sinks, recent, per_head, pages, P, hkv, D,
+            (FLAG_HND if kv_layout == "HND" else 0) | (FLAG_KV_FP8 if fp8 else 0),
+            ws.data_ptr() if need else 0, need, _err_arg(err, dev), _stream_ptr(stream))
+    if st:
+        _check(st, "pkd_evict_kv")
 
 
 def evicted_table(indptr, indices, last_page_len, page_size, budget):
@@ -1127,10 +1196,3 @@ def evicted_table(indptr, indices, last_page_len, page_size, budget):
     ids = indices[:used]
     return (np.concatenate([[0], np.cumsum(left)]).astype(np.int32), np.ascontiguousarray(ids[keep]),
             (now - page_size * (left - 1)).astype(np.int32), np.ascontiguousarray(ids[~keep]))
-
-
-def _one_device(*tensors):
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")

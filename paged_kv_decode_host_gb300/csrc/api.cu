@@ -782,27 +782,45 @@ int pkd_accumulate_weights(pkd_ctx* ctx, const void* q, const void* kv, const fl
              : PKD_E_CUDA;
 }
 
+// The sizes of an eviction; PKD_OK when they can be run.
+static int check_evict(int32_t layers, int32_t batch, int32_t max_len, int32_t budget,
+                       int32_t per_head, int32_t num_kv_heads) {
+  if (layers < 1 || layers > kMaxEvictLayers || batch < 0 || max_len < 0 || budget < 1 ||
+      (per_head != 0 && per_head != 1) || num_kv_heads < 1 || num_kv_heads > 1024 ||
+      (int64_t)layers * batch * num_kv_heads * 8 > 0x7fffffffLL)
+    return PKD_E_INVALID_ARG;
+  return max_len > kEvictMaxTokens ? PKD_E_CAPACITY : PKD_OK;
+}
+
+size_t pkd_evict_workspace_bytes(int32_t layers, int32_t batch, int32_t max_len, int32_t budget,
+                                 int32_t per_head, int32_t num_kv_heads) {
+  if (check_evict(layers, batch, max_len, budget, per_head, num_kv_heads) != PKD_OK || batch == 0 ||
+      max_len <= budget)
+    return 0;
+  return evict_workspace_bytes(layers, batch, num_kv_heads, per_head, max_len, budget);
+}
+
 int pkd_evict_kv(int32_t layers, void* const* kv, float* const* weights,
                  int32_t* const* positions, const int32_t* indptr, const int32_t* indices,
                  const int32_t* last_page_len, const int32_t* seen, int32_t batch,
                  int32_t max_len, int32_t budget, int32_t sinks, int32_t recent, int32_t per_head,
                  int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
-                 uint32_t flags, int32_t* err, void* stream) {
+                 uint32_t flags, void* d_workspace, size_t workspace_bytes, int32_t* err,
+                 void* stream) {
   if ((flags & ~(PKD_FLAG_HND | PKD_FLAG_KV_FP8)) != 0) return PKD_E_INVALID_ARG;
-  if (layers < 1 || layers > kMaxEvictLayers || !kv || !weights || !positions)
-    return PKD_E_INVALID_ARG;
+  const int st = check_evict(layers, batch, max_len, budget, per_head, num_kv_heads);
+  if (st != PKD_OK) return st;
   const int elem = (flags & PKD_FLAG_KV_FP8) ? 1 : 2;
-  if (batch < 0 || max_len < 0 || budget < 1 || sinks < 0 || recent < 0 ||
-      (int64_t)sinks + recent > budget || (per_head != 0 && per_head != 1) || num_pages < 1 ||
-      page_size < 1 || num_kv_heads < 1 || head_dim < 1 || ((int64_t)head_dim * elem) % 16 != 0)
-    return PKD_E_INVALID_ARG;
-  if (max_len > kEvictMaxTokens) return PKD_E_CAPACITY;
-  const int64_t head = (int64_t)head_dim * elem;
-  if (head * num_kv_heads > (1 << 20) ||
-      (int64_t)layers * batch * num_kv_heads * 8 > 0x7fffffffLL)
+  if (!kv || !weights || !positions || sinks < 0 || recent < 0 ||
+      (int64_t)sinks + recent > budget || num_pages < 1 || page_size < 1 || head_dim < 1 ||
+      ((int64_t)head_dim * elem) % 16 != 0 || (int64_t)head_dim * elem > 16384 ||
+      (int64_t)head_dim * elem * num_kv_heads > 32768)
     return PKD_E_INVALID_ARG;
   if (batch == 0 || max_len <= budget) return PKD_OK;   // nothing is over the budget
   if (!indptr || !indices || !last_page_len || !seen || !aligned(err, 4)) return PKD_E_INVALID_ARG;
+  const size_t need = evict_workspace_bytes(layers, batch, num_kv_heads, per_head, max_len, budget);
+  if (need > 0 && (d_workspace == nullptr || !aligned(d_workspace, 16))) return PKD_E_INVALID_ARG;
+  if (workspace_bytes < need) return PKD_E_WORKSPACE_TOO_SMALL;
   const bool hnd = (flags & PKD_FLAG_HND) != 0;
   EvictArgs a{};
   for (int32_t l = 0; l < layers; ++l) {
@@ -831,6 +849,8 @@ int pkd_evict_kv(int32_t layers, void* const* kv, float* const* weights,
   a.recent = recent;
   a.per_head = per_head;
   a.max_len = max_len;
+  a.bitmaps = static_cast<uint32_t*>(d_workspace);
+  const int64_t head = (int64_t)head_dim * elem;
   a.v_bytes = (int64_t)page_size * num_kv_heads * head;
   a.page_bytes = 2 * a.v_bytes;
   a.token_bytes = hnd ? head : head * num_kv_heads;

@@ -2,6 +2,7 @@
 // (evict_kernel.cu): arguments and launchers.
 #pragma once
 
+#include <stddef.h>
 #include <stdint.h>
 
 #include <cuda_runtime_api.h>
@@ -40,10 +41,14 @@ struct EvictArgs {
   int64_t page_bytes, token_bytes, head_bytes;   // strides in the cache
   int64_t v_bytes;                               // from a page's K block to its V block
   int32_t pieces;                                // 16-byte pieces of one head's row
+  int32_t splits;                                // blocks of the moving kernel per job
+  uint32_t* bitmaps;                             // workspace: kept tokens per job
   void* kv[kMaxEvictLayers];
   float* weights[kMaxEvictLayers];
   int32_t* positions[kMaxEvictLayers];
 };
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+// Workspace of a call: 0 when its blocks choose and move in one kernel.
+size_t evict_workspace_bytes(int layers, int batch, int hkv, int per_head, int max_len, int budget);
+cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream);
 
 }  // namespace pkd

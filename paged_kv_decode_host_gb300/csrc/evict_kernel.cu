@@ -11,14 +11,17 @@
 // rows, weight and position).  Slots behind the budget keep what they held.
 // Sources and destinations are disjoint, so the moves need no order.
 //
-// HBM bound where many rows move, latency bound where one does.  A cluster
-// of 1 to 8 blocks takes one (layer, request, head): each block keeps the
-// ordered keys of its share of the tokens in shared memory (weights and
-// positions are read once), the budget-th largest key is found by a radix
-// search of four 8-bit digits whose histograms the blocks add up through
-// distributed shared memory, the bitmap of kept tokens is gathered by every
-// block, and the blocks then move disjoint windows of the pairs.  The moves
-// begin only after every block of the cluster has read its weights.
+// Choosing is latency bound (weights and positions are read once: 8 bytes a
+// token), moving is HBM bound.  A block takes one job (layer, request, head)
+// and keeps its tokens' ordered keys in shared memory.  The budget-th largest
+// key is found by a radix search of four 8-bit digits; when at most kFew
+// tokens go (each step of steady decoding evicts one), by as many block-wide
+// minima instead.  The kept tokens become a bitmap, whose running counts pair
+// holes and movers.  Jobs with more than 32,768 tokens, and calls of few jobs
+// with long requests, take a cluster of up to 8 blocks a job, whose digit
+// counts and bitmaps meet through distributed shared memory; calls of few
+// jobs also leave the moves to a second kernel over the whole GPU, which
+// reads the bitmaps.  A job's moves begin only when all its weights are read.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -26,16 +29,18 @@
 
 #include "evict.h"
 #include "pkd.h"
+#include "sm103_ptx.cuh"
 
 namespace pkd {
 namespace {
 
 namespace cg = cooperative_groups;
+using dev::kFull;
+using dev::pdl_launch_dependents;
+using dev::pdl_wait;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kWindow = 512;   // pairs whose slots are listed at a time
-constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kWindow = 256;   // pairs listed at a time
+constexpr int kFew = 8;        // evictions taken by block-wide minima
 
 // fp32 order as unsigned order: NaN lowest, -0 equal to 0; kept-always above all
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -45,19 +50,36 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 }
 constexpr uint32_t kAlways = 0xffffffffu;
 
+// x / d for x < 2^20 and d <= 2^11 by a multiplication: m = ceil(2^32 / d)
+// gives x m / 2^32 = x / d + x e / (d 2^32) with e < d, an error below
+// 2^20 / 2^32 < 1 / d
+struct Div {
+  uint32_t d, m;
+  __device__ explicit Div(uint32_t v) : d(v), m(v == 1 ? 0 : 0xffffffffu / v + 1) {}
+  __device__ uint32_t div(uint32_t x) const { return d == 1 ? x : __umulhi(x, m); }
+};
+
+template <int kThreads>
 struct Shared {
   // a pass's digits; three in turn, as a block may still read the last pass's
   // from here while this one zeroes the next
   int hist[3][256];
-  int sums[kWarps + 1];
+  int sums[kThreads / 32 + 1];
+  unsigned long long low[2][kThreads / 32];
   uint32_t prefix;       // digits found so far
   int need;              // keys still to take among those with the prefix
   int equal;             // this block's keys equal to the threshold
   int eq_before;
+  // the pairs of a window: where to and from, as bytes of head 0's K row and
+  // as slots of head 0
+  int64_t to[kWindow], from[kWindow];
+  int64_t slot_to[kWindow], slot_from[kWindow];
 };
 
-// exclusive prefix sum over the block's threads; total in sh.sums[kWarps]
-__device__ __forceinline__ int block_scan(Shared& sh, int v) {
+// exclusive prefix sum over the block's threads; total in sh.sums[warps]
+template <int kThreads>
+__device__ __forceinline__ int block_scan(Shared<kThreads>& sh, int v) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -84,8 +106,7 @@ __device__ __forceinline__ int block_scan(Shared& sh, int v) {
   return sh.sums[warp] + x - v;
 }
 
-// Dynamic shared memory: Shared, keys [share], bitmap [words], before
-// [words], lists [2][kWindow].
+// Dynamic shared memory: Shared, bitmap [words], before [words], keys [share].
 struct Sizes {
   int share;   // tokens of a block (a multiple of 32)
   int words;   // bitmap words of the longest request
@@ -94,190 +115,74 @@ __host__ __device__ inline Sizes sizes_for(int max_len, int blocks) {
   const int words = (max_len + 31) / 32;
   return Sizes{(words + blocks - 1) / blocks * 32, words};
 }
-inline size_t smem_for(const Sizes& z) {
-  return sizeof(Shared) + 16 + ((size_t)z.share + 2 * (size_t)z.words + 2 * kWindow) * 4;
+template <int kThreads>
+__host__ __device__ constexpr size_t shared_bytes() {
+  return (sizeof(Shared<kThreads>) + 15) & ~(size_t)15;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const Sizes z = sizes_for(a.max_len, blocks);
-  Shared& sh = *reinterpret_cast<Shared*>(raw);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(raw + ((sizeof(Shared) + 15) & ~(size_t)15));
-  uint32_t* kept = keys + z.share;
-  int* before = reinterpret_cast<int*>(kept + z.words);
-  int* holes = before + z.words;
-  int* movers = holes + kWindow;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
+struct Job {
+  int layer, req, head, n;
+  const int32_t* pages;
+};
+// false when the job has nothing to do: the table row is wrong (flagged by
+// `tell`), or the request is not over the budget
+__device__ __forceinline__ bool job_of(const EvictArgs& a, int job, bool tell, Job* j) {
   const int groups = a.per_head ? a.hkv : 1;
-  int job = (int)(blockIdx.x / blocks);
-  const int head = job % groups;
+  j->head = job % groups;
   job /= groups;
-  const int req = job % a.batch, layer = job / a.batch;
+  j->req = job % a.batch;
+  j->layer = job / a.batch;
+  const int p0 = a.indptr[j->req], p1 = a.indptr[j->req + 1], last = a.last[j->req];
+  const int64_t len = p1 > p0 ? (int64_t)a.page_size * (p1 - p0 - 1) + last : 0;
+  const bool wrong = p0 < 0 || p1 <= p0 || last < 1 || last > a.page_size || len > a.max_len;
+  if (wrong && tell && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+  j->n = (int)len;
+  j->pages = a.indices + p0;
+  return !wrong && len > a.budget;
+}
+
+// Running counts of the bitmap, then the moves: windows of pairs `first`,
+// `first` + `step`, ...
+template <int kThreads>
+__device__ __forceinline__ void move_pairs(const EvictArgs& a, Shared<kThreads>& sh, const Job& j,
+                                           const uint32_t* kept, int* before, int first, int step) {
+  const int tid = threadIdx.x;
   const int P = a.page_size, keep = a.budget;
-  const int p0 = a.indptr[req], p1 = a.indptr[req + 1], last = a.last[req];
-  const int64_t len = p1 > p0 ? (int64_t)P * (p1 - p0 - 1) + last : 0;
-  const bool wrong = p0 < 0 || p1 <= p0 || last < 1 || last > P || len > a.max_len;
-  if (wrong || len <= keep) {   // the same for every block of the cluster
-    if (wrong && tid == 0 && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
-    return;
-  }
-  const int n = (int)len;
-  const int32_t* pages = a.indices + p0;
-  // a page outside the pool: the request is left as it is
-  int bad = 0;
-  for (int i = tid; i < p1 - p0; i += kThreads)
-    bad |= (unsigned)pages[i] >= (unsigned)a.num_pages ? 1 : 0;
-  if (__syncthreads_or(bad)) {
-    if (tid == 0 && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
-    return;   // every block of the cluster saw the same pages
-  }
-  float* weights = a.weights[layer];
-  int32_t* positions = a.positions[layer];
-  const int seen = a.seen[req];
-  const int words = (n + 31) / 32;
-  const int w0 = min(words, rank * (z.share / 32)), w1 = min(words, w0 + z.share / 32);
-  const int t0 = 32 * w0, t1 = min(n, 32 * w1);
-
-  // ---- keys of this block's tokens
-  for (int t = t0 + tid; t < t1; t += kThreads) {
-    const int64_t at = (int64_t)pages[t / P] * a.hkv * P + t % P;
-    float w;
-    int pos;
-    if (a.per_head) {
-      w = weights[at + (int64_t)head * P];
-      pos = positions[at + (int64_t)head * P];
-    } else {
-      // the heads' sum in head order, 64 bits, rounded once
-      double s = 0.0;
-      for (int h = 0; h < a.hkv; ++h) s += (double)weights[at + (int64_t)h * P];
-      w = (float)s;
-      pos = positions[at];
-    }
-    keys[t - t0] = (pos < a.sinks || pos >= seen - a.recent) ? kAlways : key_of(w);
-  }
-  if (tid < 256) sh.hist[0][tid] = 0;
-  if (tid == 0) {
-    sh.prefix = 0;
-    sh.need = keep;
-  }
-  __syncthreads();
-
-  // ---- the keep-th largest key, digit by digit
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass, cur = pass % 3;
-    const uint32_t prefix = sh.prefix;
-    const int need = sh.need;
-    for (int i = tid; i < t1 - t0; i += kThreads) {
-      const uint32_t k = keys[i];
-      if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&sh.hist[cur][(k >> shift) & 255], 1);
-    }
-    if (tid < 256) sh.hist[(pass + 1) % 3][tid] = 0;
-    cluster.sync();
-    // thread i holds bin 255 - i, so the scan counts from the largest down
-    int c = 0;
-    if (tid < 256)
-      for (int r = 0; r < blocks; ++r)
-        c += cluster.map_shared_rank(&sh.hist[cur][0], r)[255 - tid];
-    const int above = block_scan(sh, c);
-    if (tid < 256 && above < need && above + c >= need) {
-      sh.prefix = prefix | ((uint32_t)(255 - tid) << shift);
-      sh.need = need - above;
-    }
-    __syncthreads();
-  }
-  const uint32_t limit = sh.prefix;
-  const int need = sh.need;   // keys equal to the limit that stay, lowest slots first
-
-  // ---- kept bits of this block's words: above the limit, then the first
-  // `need` equal ones of the whole request
-  int mine = 0;
-  for (int i = tid; i < t1 - t0; i += kThreads) mine += keys[i] == limit ? 1 : 0;
-  mine = __reduce_add_sync(kFull, mine);
-  __syncthreads();
-  if (tid == 0) sh.equal = 0;
-  __syncthreads();
-  if (lane == 0) atomicAdd(&sh.equal, mine);
-  cluster.sync();
-  if (tid == 0) {
-    int b = 0;
-    for (int r = 0; r < rank; ++r) b += *cluster.map_shared_rank(&sh.equal, r);
-    sh.eq_before = b;
-  }
-  __syncthreads();
-  int eq_before = sh.eq_before;
-  for (int wb = w0; wb < w1; wb += kThreads) {   // a chunk of up to 512 words, a thread each
-    const int w = wb + tid;
-    uint32_t gt = 0, eq = 0;
-    // warps form the words' masks: word wb + 32 warp + i from 32 lanes
-    for (int i = 0; i < 32; ++i) {
-      const int ww = wb + 32 * warp + i;
-      if (ww >= w1) break;
-      const int t = 32 * ww + lane;
-      const uint32_t k = t < t1 ? keys[t - t0] : 0u;
-      const uint32_t g = __ballot_sync(kFull, t < t1 && k > limit);
-      const uint32_t e = __ballot_sync(kFull, t < t1 && k == limit);
-      if (lane == i) {
-        gt = g;
-        eq = e;
-      }
-    }
-    const int first = eq_before + block_scan(sh, __popc(eq));
-    if (w < w1) {
-      int left = need - first;
-      uint32_t take = 0;
-      if (left >= __popc(eq)) {
-        take = eq;
-      } else {
-        for (; left > 0; --left) {
-          take |= eq & (0u - eq);
-          eq &= eq - 1;
-        }
-      }
-      kept[w] = gt | take;
-    }
-    eq_before += sh.sums[kWarps];
-  }
-  cluster.sync();
-  // ---- every block gathers the whole bitmap and its running counts
-  for (int w = tid; w < words; w += kThreads) {
-    const int owner = w / (z.share / 32);
-    if (owner != rank) kept[w] = cluster.map_shared_rank(kept, owner)[w];
-  }
-  cluster.sync();   // no block's shared memory is read by others from here on
+  const int words = (j.n + 31) / 32;
   int run = 0;
   for (int wb = 0; wb < words; wb += kThreads) {
     const int w = wb + tid;
-    const int c = w < words ? __popc(kept[w]) : 0;
-    const int ex = block_scan(sh, c);
+    const int ex = block_scan(sh, w < words ? __popc(kept[w]) : 0);
     if (w < words) before[w] = run + ex;
-    run += sh.sums[kWarps];
+    run += sh.sums[kThreads / 32];
   }
   __syncthreads();
   // kept tokens below the budget, and so the number of holes there
   const int kw = keep / 32, kb = keep % 32;
   const int below = before[kw] + __popc(kept[kw] & ((1u << kb) - 1u));   // keep < n: kw < words
   const int moves = keep - below;
-
-  // ---- the moves, a window of pairs at a time; windows go round the blocks
   const int nh = a.per_head ? 1 : a.hkv;
-  uint8_t* kv = static_cast<uint8_t*>(a.kv[layer]);
-  const int pieces = 2 * a.pieces;   // K and V
-  for (int m0 = rank * kWindow; m0 < moves; m0 += blocks * kWindow) {
+  uint8_t* kv = static_cast<uint8_t*>(a.kv[j.layer]);
+  float* weights = a.weights[j.layer];
+  int32_t* positions = a.positions[j.layer];
+  const Div by_row((uint32_t)(2 * a.pieces)), by_heads((uint32_t)nh);
+  for (int m0 = first * kWindow; m0 < moves; m0 += step * kWindow) {
     const int m1 = min(moves, m0 + kWindow);
     __syncthreads();
+    auto note = [&](int t, int64_t& row, int64_t& slot) {
+      const int64_t page = j.pages[t / P];
+      row = page * a.page_bytes + (t % P) * a.token_bytes;
+      slot = page * a.hkv * P + t % P;
+    };
     for (int w = tid; w < words; w += kThreads) {
       const int tw = 32 * w;
       if (tw < keep) {   // holes: tokens below the budget that go
         const uint32_t in = tw + 32 <= keep ? kFull : (1u << kb) - 1u;
-        uint32_t free_bits = ~kept[w] & in;
+        uint32_t bits = ~kept[w] & in;
         int r = tw - before[w];
-        if (r < m1 && r + __popc(free_bits) > m0)
-          for (; free_bits; free_bits &= free_bits - 1, ++r)
-            if (r >= m0 && r < m1) holes[r - m0] = tw + __ffs(free_bits) - 1;
+        if (r < m1 && r + __popc(bits) > m0)
+          for (; bits; bits &= bits - 1, ++r)
+            if (r >= m0 && r < m1) note(tw + __ffs(bits) - 1, sh.to[r - m0], sh.slot_to[r - m0]);
       }
       if (tw + 32 > keep) {   // movers: kept tokens behind it
         const uint32_t in = tw >= keep ? kFull : ~((1u << kb) - 1u);
@@ -285,12 +190,14 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
         int r = tw >= keep ? before[w] - below : 0;
         if (r < m1 && r + __popc(bits) > m0)
           for (; bits; bits &= bits - 1, ++r)
-            if (r >= m0 && r < m1) movers[r - m0] = tw + __ffs(bits) - 1;
+            if (r >= m0 && r < m1)
+              note(tw + __ffs(bits) - 1, sh.from[r - m0], sh.slot_from[r - m0]);
       }
     }
     __syncthreads();
+    // 16 bytes of a row a thread, four in flight
     const int rows = (m1 - m0) * nh;
-    const int total = rows * pieces;
+    const int total = rows * 2 * a.pieces;
     constexpr int kUnroll = 4;
     for (int p = tid; p < total; p += kUnroll * kThreads) {
       uint4 v[kUnroll];
@@ -300,14 +207,14 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
         const int q = p + u * kThreads;
         to[u] = nullptr;
         if (q < total) {
-          const int row = q / pieces, piece = q % pieces;
-          const int pair = row / nh, h = a.per_head ? head : row % nh;
-          const int64_t in_row = (int64_t)h * a.head_bytes +
-                                 (piece >= a.pieces ? a.v_bytes + 16 * (piece - a.pieces) : 16 * piece);
-          const int src = movers[pair], dst = holes[pair];
-          v[u] = *reinterpret_cast<const uint4*>(kv + pages[src / P] * a.page_bytes +
-                                                 (src % P) * a.token_bytes + in_row);
-          to[u] = kv + pages[dst / P] * a.page_bytes + (dst % P) * a.token_bytes + in_row;
+          const int row = (int)by_row.div((uint32_t)q), piece = q - row * 2 * a.pieces;
+          const int pair = (int)by_heads.div((uint32_t)row);
+          const int h = a.per_head ? j.head : row - pair * nh;
+          const int64_t in_row = h * a.head_bytes + (piece >= a.pieces
+                                                         ? a.v_bytes + 16 * (piece - a.pieces)
+                                                         : 16 * piece);
+          v[u] = *reinterpret_cast<const uint4*>(kv + sh.from[pair] + in_row);
+          to[u] = kv + sh.to[pair] + in_row;
         }
       }
 #pragma unroll
@@ -315,48 +222,340 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
         if (to[u] != nullptr) *reinterpret_cast<uint4*>(to[u]) = v[u];
     }
     for (int row = tid; row < rows; row += kThreads) {
-      const int pair = row / nh, h = a.per_head ? head : row % nh;
-      const int src = movers[pair], dst = holes[pair];
-      const int64_t from = ((int64_t)pages[src / P] * a.hkv + h) * P + src % P;
-      const int64_t to = ((int64_t)pages[dst / P] * a.hkv + h) * P + dst % P;
-      const float w = weights[from];
-      const int32_t pos = positions[from];
-      weights[to] = w;
-      positions[to] = pos;
+      const int pair = (int)by_heads.div((uint32_t)row);
+      const int64_t h = (int64_t)(a.per_head ? j.head : row - pair * nh) * P;
+      const float w = weights[sh.slot_from[pair] + h];
+      const int32_t pos = positions[sh.slot_from[pair] + h];
+      weights[sh.slot_to[pair] + h] = w;
+      positions[sh.slot_to[pair] + h] = pos;
     }
   }
 }
 
-}  // namespace
+// kCluster: a cluster per job (of one block or more); kMove: the job's moves
+// follow, else the bitmap is left in the workspace for evict_move_kernel.
+template <int kThreads, bool kCluster, bool kMove>
+__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  constexpr int kWarps = kThreads / 32;
+  if (!kMove) pdl_launch_dependents();
+  int blocks = 1, rank = 0;
+  if constexpr (kCluster) {
+    blocks = (int)cg::this_cluster().num_blocks();
+    rank = (int)cg::this_cluster().block_rank();
+  }
+  auto meet = [&] {   // every block of the job
+    if constexpr (kCluster)
+      cg::this_cluster().sync();
+    else
+      __syncthreads();
+  };
+  auto theirs = [&](auto* p, int r) {
+    if constexpr (kCluster)
+      return cg::this_cluster().map_shared_rank(p, r);
+    else
+      return p;
+  };
+  const Sizes z = sizes_for(a.max_len, blocks);
+  Shared<kThreads>& sh = *reinterpret_cast<Shared<kThreads>*>(raw);
+  uint32_t* kept = reinterpret_cast<uint32_t*>(raw + shared_bytes<kThreads>());
+  int* before = reinterpret_cast<int*>(kept + z.words);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(before + z.words);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-  const int groups = a.per_head ? a.hkv : 1;
-  const int64_t jobs = (int64_t)a.layers * a.batch * groups;
-  // blocks per job: enough for the longest request's keys, then more while
-  // the grid leaves SMs idle and a block keeps 512 tokens or more
-  int blocks = 1;
-  while (blocks < 8 && (a.max_len > blocks * kEvictBlockTokens ||
-                        (jobs * blocks * 2 <= 304 && a.max_len >= blocks * 1024)))
-    blocks *= 2;
-  const size_t smem = smem_for(sizes_for(a.max_len, blocks));
+  Job j;
+  const int job = (int)blockIdx.x / blocks;
+  if (!job_of(a, job, tid == 0, &j)) return;   // the same for every block of the cluster
+  const int P = a.page_size, keep = a.budget, n = j.n;
+  // a page outside the pool: the request is left as it is (every block of
+  // the cluster sees the same pages)
+  int bad = 0;
+  for (int i = tid; i * P < n; i += kThreads)
+    bad |= (unsigned)j.pages[i] >= (unsigned)a.num_pages ? 1 : 0;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0 && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+    return;
+  }
+  const float* weights = a.weights[j.layer];
+  const int32_t* positions = a.positions[j.layer];
+  const int seen = a.seen[j.req];
+  const int words = (n + 31) / 32;
+  const int w0 = min(words, rank * (z.share / 32)), w1 = min(words, w0 + z.share / 32);
+  const int t0 = 32 * w0, t1 = min(n, 32 * w1);
+
+  // ---- keys of this block's tokens
+#pragma unroll 4
+  for (int t = t0 + tid; t < t1; t += kThreads) {
+    const int64_t at = (int64_t)j.pages[t / P] * a.hkv * P + t % P;
+    float w;
+    int pos;
+    if (a.per_head) {
+      w = weights[at + (int64_t)j.head * P];
+      pos = positions[at + (int64_t)j.head * P];
+    } else {
+      // the heads' sum in head order, 64 bits, rounded once
+      double s = 0.0;
+      for (int h = 0; h < a.hkv; ++h) s += (double)weights[at + (int64_t)h * P];
+      w = (float)s;
+      pos = positions[at];
+    }
+    keys[t - t0] = (pos < a.sinks || pos >= seen - a.recent) ? kAlways : key_of(w);
+  }
+
+  if (!kCluster && n - keep <= kFew) {
+    // ---- few go: the lowest key, of equal ones the highest slot, so often
+    for (int w = tid; w < words; w += kThreads)
+      kept[w] = n - 32 * w >= 32 ? kFull : (1u << (n - 32 * w)) - 1u;
+    auto lowest = [&] {   // of this thread's tokens that are still kept
+      unsigned long long low = ~0ull;
+      for (int t = tid; t < n; t += kThreads)
+        if (kept[t >> 5] >> (t & 31) & 1u) {
+          const unsigned long long k = (unsigned long long)keys[t] << 32 | (0xffffffffu - (uint32_t)t);
+          low = k < low ? k : low;
+        }
+      return low;
+    };
+    __syncthreads();
+    unsigned long long mine = lowest();
+    for (int e = 0; e < n - keep; ++e) {
+      unsigned long long low = mine;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long x = __shfl_xor_sync(kFull, low, o);
+        low = x < low ? x : low;
+      }
+      if (lane == 0) sh.low[e & 1][warp] = low;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) low = sh.low[e & 1][w] < low ? sh.low[e & 1][w] : low;
+      const int t = (int)(0xffffffffu - (uint32_t)low);
+      if (mine == low) {   // the token's owner; others of its word wait for the next barrier
+        atomicAnd(&kept[t >> 5], ~(1u << (t & 31)));
+        mine = lowest();
+      }
+    }
+    __syncthreads();
+  } else {
+    for (int i = tid; i < 256; i += kThreads) sh.hist[0][i] = 0;
+    if (tid == 0) {
+      sh.prefix = 0;
+      sh.need = keep;
+      sh.equal = 0;
+    }
+    __syncthreads();
+    // ---- the keep-th largest key, digit by digit
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass, cur = pass % 3;
+      const uint32_t prefix = sh.prefix;
+      const int need = sh.need;
+      for (int i = tid; i < t1 - t0; i += kThreads) {
+        const uint32_t k = keys[i];
+        if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
+          atomicAdd(&sh.hist[cur][(k >> shift) & 255], 1);
+      }
+      for (int i = tid; i < 256; i += kThreads) sh.hist[(pass + 1) % 3][i] = 0;
+      meet();
+      // bins from the largest down, 256 / kThreads or one to a thread
+      constexpr int kBins = kThreads >= 256 ? 1 : 256 / kThreads;
+      int c[kBins], all = 0;
+#pragma unroll
+      for (int b = 0; b < kBins; ++b) {
+        c[b] = 0;
+        const int bin = 255 - (tid * kBins + b);
+        if (bin >= 0)
+          for (int r = 0; r < blocks; ++r) c[b] += theirs(&sh.hist[cur][0], r)[bin];
+        all += c[b];
+      }
+      int above = block_scan(sh, all);
+#pragma unroll
+      for (int b = 0; b < kBins; ++b) {
+        if (above < need && above + c[b] >= need) {
+          sh.prefix = prefix | ((uint32_t)(255 - (tid * kBins + b)) << shift);
+          sh.need = need - above;
+        }
+        above += c[b];
+      }
+      __syncthreads();
+    }
+    const uint32_t limit = sh.prefix;
+    const int need = sh.need;   // keys equal to the limit that stay, lowest slots first
+
+    // ---- kept bits of this block's words: above the limit, then the first
+    // `need` equal ones of the whole request
+    int eq_before = 0;
+    if constexpr (kCluster) {
+      int mine = 0;
+      for (int i = tid; i < t1 - t0; i += kThreads) mine += keys[i] == limit ? 1 : 0;
+      mine = __reduce_add_sync(kFull, mine);
+      if (lane == 0) atomicAdd(&sh.equal, mine);
+      meet();
+      if (tid == 0) {
+        int b = 0;
+        for (int r = 0; r < rank; ++r) b += *theirs(&sh.equal, r);
+        sh.eq_before = b;
+      }
+      __syncthreads();
+      eq_before = sh.eq_before;
+    }
+    for (int wb = w0; wb < w1; wb += kThreads) {   // a word a thread
+      uint32_t gt = 0, eq = 0;
+      // a warp's 32 words, whose masks come from 32 lanes at a time
+      const int wn = min(32, w1 - wb - 32 * warp);
+      for (int i = 0; i < wn; ++i) {
+        const int t = 32 * (wb + 32 * warp + i) + lane;
+        const uint32_t k = t < t1 ? keys[t - t0] : 0u;
+        const uint32_t g = __ballot_sync(kFull, t < t1 && k > limit);
+        const uint32_t e = __ballot_sync(kFull, t < t1 && k == limit);
+        if (lane == i) {
+          gt = g;
+          eq = e;
+        }
+      }
+      const int first = eq_before + block_scan(sh, __popc(eq));
+      if (wb + tid < w1) {
+        int left = need - first;
+        uint32_t take = 0;
+        if (left >= __popc(eq)) {
+          take = eq;
+        } else {
+          for (; left > 0; --left) {
+            take |= eq & (0u - eq);
+            eq &= eq - 1;
+          }
+        }
+        kept[wb + tid] = gt | take;
+      }
+      eq_before += sh.sums[kWarps];
+    }
+  }
+  if constexpr (!kMove) {
+    // the words of this block; a job that has nothing to do leaves none
+    __syncthreads();
+    uint32_t* out = a.bitmaps + (int64_t)job * z.words;
+    for (int w = w0 + tid; w < w1; w += kThreads) out[w] = kept[w];
+    meet();   // no block ends while others read its shared memory
+    return;
+  }
+  meet();
+  if constexpr (kCluster) {
+    // ---- every block gathers the whole bitmap
+    for (int w = tid; w < words; w += kThreads) {
+      const int owner = w / (z.share / 32);
+      if (owner != rank) kept[w] = theirs(kept, owner)[w];
+    }
+    meet();   // no block's shared memory is read by others from here on
+  }
+  move_pairs(a, sh, j, kept, before, rank, blocks);
+}
+
+// The moves of a call with few jobs: a.splits blocks per job.
+constexpr int kMoveThreads = 512;
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  const Sizes z = sizes_for(a.max_len, 1);
+  Shared<kMoveThreads>& sh = *reinterpret_cast<Shared<kMoveThreads>*>(raw);
+  uint32_t* kept = reinterpret_cast<uint32_t*>(raw + shared_bytes<kMoveThreads>());
+  int* before = reinterpret_cast<int*>(kept + z.words);
+  const int job = (int)blockIdx.x / a.splits;
+  pdl_wait();   // the bitmaps, and whatever came before them
+  Job j;
+  if (!job_of(a, job, false, &j)) return;
+  int bad = 0;
+  for (int i = threadIdx.x; i * a.page_size < j.n; i += kMoveThreads)
+    bad |= (unsigned)j.pages[i] >= (unsigned)a.num_pages ? 1 : 0;
+  if (__syncthreads_or(bad)) return;   // flagged by the kernel before
+  const uint32_t* in = a.bitmaps + (int64_t)job * z.words;
+  for (int w = threadIdx.x; 32 * w < j.n; w += kMoveThreads) kept[w] = in[w];
+  __syncthreads();
+  move_pairs(a, sh, j, kept, before, (int)blockIdx.x % a.splits, a.splits);
+}
+
+constexpr int kSms = 152;
+
+struct EvictPlan {
+  int64_t jobs;
+  int blocks;    // of a job
+  bool cluster, split;
+  int threads, splits;
+};
+
+EvictPlan plan_for(int layers, int batch, int hkv, int per_head, int max_len, int budget) {
+  EvictPlan p{};
+  p.jobs = (int64_t)layers * batch * (per_head ? hkv : 1);
+  // Few jobs whose moves may be many: choose with a cluster per job (while a
+  // block keeps 4,096 tokens or more), move with the whole GPU.
+  p.split = p.jobs < kSms && max_len - budget >= 2 * kWindow;
+  p.blocks = 1;
+  while (p.blocks < 8 && (max_len > p.blocks * kEvictBlockTokens ||
+                          (p.split && p.jobs * p.blocks * 2 <= kSms && max_len > p.blocks * 4096)))
+    p.blocks *= 2;
+  p.cluster = p.split || p.blocks > 1;
+  // a block per 2,048 tokens of four warps: more blocks per SM hide each
+  // other's barriers
+  const int share = (max_len + p.blocks - 1) / p.blocks;
+  p.threads = p.cluster ? 512 : share <= 2048 ? 128 : share <= 8192 ? 256 : 512;
+  p.splits = p.split ? (int)((2 * kSms + p.jobs - 1) / p.jobs) : 0;
+  return p;
+}
+
+template <int kThreads, bool kCluster, bool kMove>
+cudaError_t launch_choose(const EvictArgs& a, const EvictPlan& p, cudaStream_t stream) {
+  const Sizes z = sizes_for(a.max_len, p.blocks);
+  const size_t smem = shared_bytes<kThreads>() + ((size_t)z.share + 2 * (size_t)z.words) * 4;
+  auto f = &evict_kernel<kThreads, kCluster, kMove>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(jobs * blocks));
+  cfg.gridDim = dim3((unsigned)(p.jobs * p.blocks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)blocks;
+  attr[0].val.clusterDim.x = (unsigned)p.blocks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, f, a);
+}
+
+}  // namespace
+
+size_t evict_workspace_bytes(int layers, int batch, int hkv, int per_head, int max_len, int budget) {
+  const EvictPlan p = plan_for(layers, batch, hkv, per_head, max_len, budget);
+  return p.split ? (size_t)p.jobs * (size_t)sizes_for(max_len, 1).words * 4 : 0;
+}
+
+cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
+  const EvictPlan p = plan_for(a.layers, a.batch, a.hkv, a.per_head, a.max_len, a.budget);
+  a.splits = p.splits;
+  if (!p.split) {
+    if (p.cluster) return launch_choose<512, true, true>(a, p, stream);
+    if (p.threads == 128) return launch_choose<128, false, true>(a, p, stream);
+    if (p.threads == 256) return launch_choose<256, false, true>(a, p, stream);
+    return launch_choose<512, false, true>(a, p, stream);
+  }
+  cudaError_t e = launch_choose<512, true, false>(a, p, stream);
+  if (e != cudaSuccess) return e;
+  const size_t smem = shared_bytes<kMoveThreads>() + 2 * (size_t)sizes_for(a.max_len, 1).words * 4;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.jobs * p.splits));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_kernel, a);
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a);
 }
 
 }  // namespace pkd
