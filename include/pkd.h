@@ -405,7 +405,8 @@ int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const fl
  * its tokens' accumulated weights -- for 1 to 128 layers in one launch, each
  * with its own cache, weights and positions.
  * Per layer, request and KV head (per_head 1), or per layer and request by
- * the sum of the heads' weights (per_head 0; positions of head 0 count), the
+ * the sum of the heads' weights, rounded to fp32 once (per_head 0; positions of
+ * head 0 count), the
  * `budget` tokens of largest weight stay; tokens with position < sinks or
  * >= seen[b] - recent stay before all others (sinks + recent <= budget);
  * equal weights: the lower slot first; NaN counts as the lowest.  Slots are

@@ -41,6 +41,7 @@ struct EvictArgs {
   int64_t page_bytes, token_bytes, head_bytes;   // strides in the cache
   int64_t v_bytes;                               // from a page's K block to its V block
   int32_t pieces;                                // 16-byte pieces of one head's row
+  int32_t page_shift;                            // log2 of the page size, -1 if it has none
   int32_t splits;                                // blocks of the moving kernel per job
   uint32_t* bitmaps;                             // workspace: kept tokens per job
   void* kv[kMaxEvictLayers];

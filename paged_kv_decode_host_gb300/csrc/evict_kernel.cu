@@ -59,6 +59,26 @@ struct Div {
   __device__ uint32_t div(uint32_t x) const { return d == 1 ? x : __umulhi(x, m); }
 };
 
+// Tokens of a page: most sizes are powers of two.
+struct PageSize {
+  int size, shift;
+  __device__ explicit PageSize(const EvictArgs& a) : size(a.page_size), shift(a.page_shift) {}
+  __device__ int div(int t) const { return shift >= 0 ? t >> shift : t / size; }
+};
+
+// The sum of up to a few fp32 values, each addition's rounding error carried
+// along (a + b = s + e exactly) and added at the end: as exact as 64-bit
+// additions, whose rate here is 1/64 of fp32's.
+struct Sum2 {
+  float s = 0.f, e = 0.f;
+  __device__ void add(float x) {
+    const float t = s + x, z = t - s;
+    e += (s - (t - z)) + (x - z);
+    s = t;
+  }
+  __device__ float value() const { return fabsf(s) < CUDART_INF_F ? s + e : s; }
+};
+
 template <int kThreads>
 struct Shared {
   // a pass's digits; three in turn, as a block may still read the last pass's
@@ -70,10 +90,10 @@ struct Shared {
   int need;              // keys still to take among those with the prefix
   int equal;             // this block's keys equal to the threshold
   int eq_before;
-  // the pairs of a window: where to and from, as bytes of head 0's K row and
-  // as slots of head 0
-  int64_t to[kWindow], from[kWindow];
-  int64_t slot_to[kWindow], slot_from[kWindow];
+  // the tokens of a window's pairs (where to, from), then the same as bytes of
+  // head 0's K row and as slots of head 0
+  int token[2 * kWindow];
+  int64_t row[2 * kWindow], slot[2 * kWindow];
 };
 
 // exclusive prefix sum over the block's threads; total in sh.sums[warps]
@@ -147,7 +167,8 @@ template <int kThreads>
 __device__ __forceinline__ void move_pairs(const EvictArgs& a, Shared<kThreads>& sh, const Job& j,
                                            const uint32_t* kept, int* before, int first, int step) {
   const int tid = threadIdx.x;
-  const int P = a.page_size, keep = a.budget;
+  const PageSize P(a);
+  const int keep = a.budget;
   const int words = (j.n + 31) / 32;
   int run = 0;
   for (int wb = 0; wb < words; wb += kThreads) {
@@ -169,11 +190,6 @@ __device__ __forceinline__ void move_pairs(const EvictArgs& a, Shared<kThreads>&
   for (int m0 = first * kWindow; m0 < moves; m0 += step * kWindow) {
     const int m1 = min(moves, m0 + kWindow);
     __syncthreads();
-    auto note = [&](int t, int64_t& row, int64_t& slot) {
-      const int64_t page = j.pages[t / P];
-      row = page * a.page_bytes + (t % P) * a.token_bytes;
-      slot = page * a.hkv * P + t % P;
-    };
     for (int w = tid; w < words; w += kThreads) {
       const int tw = 32 * w;
       if (tw < keep) {   // holes: tokens below the budget that go
@@ -182,7 +198,7 @@ __device__ __forceinline__ void move_pairs(const EvictArgs& a, Shared<kThreads>&
         int r = tw - before[w];
         if (r < m1 && r + __popc(bits) > m0)
           for (; bits; bits &= bits - 1, ++r)
-            if (r >= m0 && r < m1) note(tw + __ffs(bits) - 1, sh.to[r - m0], sh.slot_to[r - m0]);
+            if (r >= m0 && r < m1) sh.token[r - m0] = tw + __ffs(bits) - 1;
       }
       if (tw + 32 > keep) {   // movers: kept tokens behind it
         const uint32_t in = tw >= keep ? kFull : ~((1u << kb) - 1u);
@@ -190,15 +206,22 @@ __device__ __forceinline__ void move_pairs(const EvictArgs& a, Shared<kThreads>&
         int r = tw >= keep ? before[w] - below : 0;
         if (r < m1 && r + __popc(bits) > m0)
           for (; bits; bits &= bits - 1, ++r)
-            if (r >= m0 && r < m1)
-              note(tw + __ffs(bits) - 1, sh.from[r - m0], sh.slot_from[r - m0]);
+            if (r >= m0 && r < m1) sh.token[kWindow + r - m0] = tw + __ffs(bits) - 1;
       }
     }
     __syncthreads();
-    // 16 bytes of a row a thread, four in flight
+    for (int i = tid; i < 2 * kWindow; i += kThreads)
+      if ((i & (kWindow - 1)) < m1 - m0) {
+        const int t = sh.token[i], pi = P.div(t), ps = t - pi * P.size;
+        const int64_t page = j.pages[pi];
+        sh.row[i] = page * a.page_bytes + ps * a.token_bytes;
+        sh.slot[i] = page * a.hkv * P.size + ps;
+      }
+    __syncthreads();
+    // 16 bytes of a row a thread, eight in flight
     const int rows = (m1 - m0) * nh;
     const int total = rows * 2 * a.pieces;
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = 8;
     for (int p = tid; p < total; p += kUnroll * kThreads) {
       uint4 v[kUnroll];
       uint8_t* to[kUnroll];
@@ -213,8 +236,8 @@ __device__ __forceinline__ void move_pairs(const EvictArgs& a, Shared<kThreads>&
           const int64_t in_row = h * a.head_bytes + (piece >= a.pieces
                                                          ? a.v_bytes + 16 * (piece - a.pieces)
                                                          : 16 * piece);
-          v[u] = *reinterpret_cast<const uint4*>(kv + sh.from[pair] + in_row);
-          to[u] = kv + sh.to[pair] + in_row;
+          v[u] = *reinterpret_cast<const uint4*>(kv + sh.row[kWindow + pair] + in_row);
+          to[u] = kv + sh.row[pair] + in_row;
         }
       }
 #pragma unroll
@@ -223,11 +246,11 @@ __device__ __forceinline__ void move_pairs(const EvictArgs& a, Shared<kThreads>&
     }
     for (int row = tid; row < rows; row += kThreads) {
       const int pair = (int)by_heads.div((uint32_t)row);
-      const int64_t h = (int64_t)(a.per_head ? j.head : row - pair * nh) * P;
-      const float w = weights[sh.slot_from[pair] + h];
-      const int32_t pos = positions[sh.slot_from[pair] + h];
-      weights[sh.slot_to[pair] + h] = w;
-      positions[sh.slot_to[pair] + h] = pos;
+      const int64_t h = (int64_t)(a.per_head ? j.head : row - pair * nh) * P.size;
+      const float w = weights[sh.slot[kWindow + pair] + h];
+      const int32_t pos = positions[sh.slot[kWindow + pair] + h];
+      weights[sh.slot[pair] + h] = w;
+      positions[sh.slot[pair] + h] = pos;
     }
   }
 }
@@ -266,11 +289,12 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   Job j;
   const int job = (int)blockIdx.x / blocks;
   if (!job_of(a, job, tid == 0, &j)) return;   // the same for every block of the cluster
-  const int P = a.page_size, keep = a.budget, n = j.n;
+  const PageSize P(a);
+  const int keep = a.budget, n = j.n;
   // a page outside the pool: the request is left as it is (every block of
   // the cluster sees the same pages)
   int bad = 0;
-  for (int i = tid; i * P < n; i += kThreads)
+  for (int i = tid; i <= P.div(n - 1); i += kThreads)
     bad |= (unsigned)j.pages[i] >= (unsigned)a.num_pages ? 1 : 0;
   if (__syncthreads_or(bad)) {
     if (tid == 0 && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
@@ -283,23 +307,56 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   const int w0 = min(words, rank * (z.share / 32)), w1 = min(words, w0 + z.share / 32);
   const int t0 = 32 * w0, t1 = min(n, 32 * w1);
 
-  // ---- keys of this block's tokens
-#pragma unroll 4
-  for (int t = t0 + tid; t < t1; t += kThreads) {
-    const int64_t at = (int64_t)j.pages[t / P] * a.hkv * P + t % P;
-    float w;
-    int pos;
-    if (a.per_head) {
-      w = weights[at + (int64_t)j.head * P];
-      pos = positions[at + (int64_t)j.head * P];
-    } else {
-      // the heads' sum in head order, 64 bits, rounded once
-      double s = 0.0;
-      for (int h = 0; h < a.hkv; ++h) s += (double)weights[at + (int64_t)h * P];
-      w = (float)s;
-      pos = positions[at];
+  // ---- keys of this block's tokens, several tokens' loads in flight
+  auto key_with = [&](float w, int pos) {
+    return (pos < a.sinks || pos >= seen - a.recent) ? kAlways : key_of(w);
+  };
+  if (a.per_head) {
+    constexpr int kAtOnce = 8;
+    for (int tb = t0 + tid; tb < t1; tb += kAtOnce * kThreads) {
+      float w[kAtOnce];
+      int pos[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int t = min(tb + i * kThreads, t1 - 1), pi = P.div(t);
+        const int64_t at = ((int64_t)j.pages[pi] * a.hkv + j.head) * P.size + (t - pi * P.size);
+        w[i] = weights[at];
+        pos[i] = positions[at];
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (tb + i * kThreads < t1) keys[tb + i * kThreads - t0] = key_with(w[i], pos[i]);
     }
-    keys[t - t0] = (pos < a.sinks || pos >= seen - a.recent) ? kAlways : key_of(w);
+  } else {
+    // by the heads' sum, in head order
+    constexpr int kAtOnce = 4, kHeads = 4;
+    for (int tb = t0 + tid; tb < t1; tb += kAtOnce * kThreads) {
+      Sum2 sum[kAtOnce];
+      int64_t at[kAtOnce];
+      int pos[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int t = min(tb + i * kThreads, t1 - 1), pi = P.div(t);
+        at[i] = (int64_t)j.pages[pi] * a.hkv * P.size + (t - pi * P.size);
+        pos[i] = positions[at[i]];
+      }
+      for (int h = 0; h < a.hkv; h += kHeads) {
+        float w[kAtOnce][kHeads];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+          for (int k = 0; k < kHeads; ++k)
+            w[i][k] = h + k < a.hkv ? weights[at[i] + (int64_t)(h + k) * P.size] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+          for (int k = 0; k < kHeads; ++k)
+            if (h + k < a.hkv) sum[i].add(w[i][k]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (tb + i * kThreads < t1) keys[tb + i * kThreads - t0] = key_with(sum[i].value(), pos[i]);
+    }
   }
 
   if (!kCluster && n - keep <= kFew) {
@@ -456,18 +513,22 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   Shared<kMoveThreads>& sh = *reinterpret_cast<Shared<kMoveThreads>*>(raw);
   uint32_t* kept = reinterpret_cast<uint32_t*>(raw + shared_bytes<kMoveThreads>());
   int* before = reinterpret_cast<int*>(kept + z.words);
-  const int job = (int)blockIdx.x / a.splits;
+  // neighbouring blocks: the heads of a request in the same window, whose
+  // rows lie near each other
+  const int groups = a.per_head ? a.hkv : 1;
+  const int split = (int)blockIdx.x / groups % a.splits;
+  const int job = (int)blockIdx.x / (groups * a.splits) * groups + (int)blockIdx.x % groups;
   pdl_wait();   // the bitmaps, and whatever came before them
   Job j;
   if (!job_of(a, job, false, &j)) return;
   int bad = 0;
-  for (int i = threadIdx.x; i * a.page_size < j.n; i += kMoveThreads)
+  for (int i = threadIdx.x; i <= (j.n - 1) / a.page_size; i += kMoveThreads)
     bad |= (unsigned)j.pages[i] >= (unsigned)a.num_pages ? 1 : 0;
   if (__syncthreads_or(bad)) return;   // flagged by the kernel before
   const uint32_t* in = a.bitmaps + (int64_t)job * z.words;
   for (int w = threadIdx.x; 32 * w < j.n; w += kMoveThreads) kept[w] = in[w];
   __syncthreads();
-  move_pairs(a, sh, j, kept, before, (int)blockIdx.x % a.splits, a.splits);
+  move_pairs(a, sh, j, kept, before, split, a.splits);
 }
 
 constexpr int kSms = 152;
@@ -482,19 +543,23 @@ struct EvictPlan {
 EvictPlan plan_for(int layers, int batch, int hkv, int per_head, int max_len, int budget) {
   EvictPlan p{};
   p.jobs = (int64_t)layers * batch * (per_head ? hkv : 1);
-  // Few jobs whose moves may be many: choose with a cluster per job (while a
-  // block keeps 4,096 tokens or more), move with the whole GPU.
-  p.split = p.jobs < kSms && max_len - budget >= 2 * kWindow;
+  // Where a job may move more than two windows, a kernel of its own moves
+  // them, in blocks of a window or a few: within the choosing blocks the
+  // longest jobs' moves would run alone at the end.  Few jobs choose with a
+  // cluster each (while a block keeps 4,096 tokens or more).
+  const int most = (max_len - budget < budget ? max_len - budget : budget);
+  p.split = most >= 2 * kWindow;
   p.blocks = 1;
   while (p.blocks < 8 && (max_len > p.blocks * kEvictBlockTokens ||
                           (p.split && p.jobs * p.blocks * 2 <= kSms && max_len > p.blocks * 4096)))
     p.blocks *= 2;
-  p.cluster = p.split || p.blocks > 1;
+  p.cluster = p.blocks > 1;
   // a block per 2,048 tokens of four warps: more blocks per SM hide each
   // other's barriers
   const int share = (max_len + p.blocks - 1) / p.blocks;
   p.threads = p.cluster ? 512 : share <= 2048 ? 128 : share <= 8192 ? 256 : 512;
-  p.splits = p.split ? (int)((2 * kSms + p.jobs - 1) / p.jobs) : 0;
+  const int64_t windows = (most + kWindow - 1) / kWindow, want = (8 * kSms + p.jobs - 1) / p.jobs;
+  p.splits = (int)(windows < 4 ? windows : want < 4 ? 4 : want < windows ? want : windows);
   return p;
 }
 
@@ -532,13 +597,19 @@ size_t evict_workspace_bytes(int layers, int batch, int hkv, int per_head, int m
 cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
   const EvictPlan p = plan_for(a.layers, a.batch, a.hkv, a.per_head, a.max_len, a.budget);
   a.splits = p.splits;
+  a.page_shift = -1;
+  for (int k = 0; k < 31; ++k)
+    if (a.page_size == 1 << k) a.page_shift = k;
   if (!p.split) {
     if (p.cluster) return launch_choose<512, true, true>(a, p, stream);
     if (p.threads == 128) return launch_choose<128, false, true>(a, p, stream);
     if (p.threads == 256) return launch_choose<256, false, true>(a, p, stream);
     return launch_choose<512, false, true>(a, p, stream);
   }
-  cudaError_t e = launch_choose<512, true, false>(a, p, stream);
+  cudaError_t e = p.cluster          ? launch_choose<512, true, false>(a, p, stream)
+                  : p.threads == 128 ? launch_choose<128, false, false>(a, p, stream)
+                  : p.threads == 256 ? launch_choose<256, false, false>(a, p, stream)
+                                     : launch_choose<512, false, false>(a, p, stream);
   if (e != cudaSuccess) return e;
   const size_t smem = shared_bytes<kMoveThreads>() + 2 * (size_t)sizes_for(a.max_len, 1).words * 4;
   if (smem > 48 * 1024) {
