@@ -25,7 +25,8 @@ using namespace pkd;
 struct KvMapEntry {
   const void* kv = nullptr;
   CUtensorMap map{};
-  CUtensorMap map_dense{};   // cascade contexts: the dense role's per-head map too
+  CUtensorMap map_dense{};   // cascade contexts: the dense role's per-head map too; latent
+                             // contexts: the second column region's
 };
 
 struct pkd_ctx {
@@ -131,7 +132,7 @@ DecodeKind kind_for(const pkd_config* c, const void* probe_address) {
     k.latent = true;
     CUtensorMap m;
     k.tmap = probe_address == nullptr ||
-             encode_latent_map(probe_address, c->num_pages, c->page_size, &m) == cudaSuccess;
+             encode_latent_map(probe_address, c->num_pages, c->page_size, 0, &m) == cudaSuccess;
     return k;
   }
   k.group = c->num_qo_heads / c->num_kv_heads;
@@ -188,7 +189,10 @@ int kv_map_for(pkd_ctx* ctx, const void* kv, CUtensorMap* out, CUtensorMap* out_
   e.kv = kv;
   const pkd_config& c = ctx->cfg;
   const bool hnd = (c.flags & PKD_FLAG_HND) != 0;
-  if ((ctx->kind.latent ? encode_latent_map(kv, c.num_pages, c.page_size, &e.map)
+  if (ctx->kind.latent &&
+      encode_latent_map(kv, c.num_pages, c.page_size, 1, &e.map_dense) != cudaSuccess)
+    return PKD_E_CUDA;
+  if ((ctx->kind.latent ? encode_latent_map(kv, c.num_pages, c.page_size, 0, &e.map)
                         : encode_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads,
                                         ctx->kind.fp8, hnd, ctx->kind.dense, &e.map)) !=
       cudaSuccess)
@@ -234,7 +238,7 @@ int launch_latent_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, fl
   a.v_scale = v_scale;
   a.wait_epoch = wait_epoch;
   if (ctx->info.batch > 0) {
-    const int st = kv_map_for(ctx, kv, &a.kv_map);
+    const int st = kv_map_for(ctx, kv, &a.kv_map[0], &a.kv_map[1]);
     if (st != PKD_OK) return st;
     if (encode_latent_q_map(q, ctx->info.batch, c.num_qo_heads, &a.q_map) != cudaSuccess)
       return PKD_E_CUDA;

@@ -35,7 +35,7 @@ struct LatentArgs {
   int32_t heads, blocks, page_size, num_pages;
   float scale_log2, v_scale;
   int32_t wait_epoch;
-  CUtensorMap kv_map;    // the cache, 16-token boxes of 64 columns
+  CUtensorMap kv_map[2]; // the cache, 16-token boxes of either column region
   CUtensorMap q_map;     // the queries, a block's heads of 64 columns
 };
 
@@ -47,7 +47,7 @@ cudaError_t latent_occupancy(int32_t heads, int* blocks_per_sm);
 // between the two.
 cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool merge,
                           cudaEvent_t decode_done, cudaStream_t stream);
-cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page_size,
+cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page_size, int region,
                               CUtensorMap* map);
 cudaError_t encode_latent_q_map(const void* q, int32_t batch, int32_t heads, CUtensorMap* map);
 cudaError_t launch_latent_append(const void* latent, int64_t latent_stride, const void* rope,

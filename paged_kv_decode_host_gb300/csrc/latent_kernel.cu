@@ -19,18 +19,18 @@
 // short head counts cost narrow instructions:
 //     S^T [tokens x heads]  = C [tokens x 576]  Q^T    A = C, B = Q, K-major
 //     O^T [dims x heads]   += C^T [dims x tokens] P^T  A = C, B = P, MN-major
-// The same shared-memory tile of C feeds both: 64-column chunks of T token
-// rows of 128 bytes (128-byte swizzle), two adjacent chunks being the 128
-// rows of one O^T product.
-//  * warp 8 streams C: per chunk, one TMA tensor copy per 16-token page tile;
-//    a chunk's slot is refilled as soon as the products that read it are done
-//    (the rotary chunk after the scores, latent chunk pairs one by one while
-//    P.V walks over them);
-//  * warp 9 issues the score products as the chunks land, warp 10 the P.V
-//    products; the whole warp runs the loop and one elected lane issues, with
-//    unrolled constant descriptor steps: 46 / 56 cycles per 128 x 16 / 64 x 16
-//    product, where a lone thread that forms descriptors in the loop takes
-//    135;
+// The same shared-memory tile of C feeds both: blocks of 8 tokens x 64 columns
+// (1 KB, 128-byte swizzle), the 9 column chunks of 8 tokens in two regions:
+// chunks 4-8 (with the rotary key) and chunks 0-3.
+//  * warp 8 streams C: one TMA tensor copy per region and 16 tokens (10 and 8
+//    KB; a 5-D map of the cache gives the blocked order, so page tiles join
+//    to one operand however the pages are scattered; copies of 2 KB each were
+//    bound by their issue, about 110 cycles a copy);
+//  * warp 9 issues the score products of a region as it lands, warp 10 the P.V
+//    products, whose regions are refilled one after the other; the whole warp
+//    runs the loop and one elected lane issues, with unrolled constant
+//    descriptor steps: 47 / 56 cycles per 128 x 16 / 128 x 64 product, where a
+//    lone thread that forms descriptors in the loop takes 135;
 //  * warps 0-7 are the softmax: a thread holds one token (a tensor-memory
 //    lane) and half of the block's heads.  The maxima run over tokens, that
 //    is, across lanes and warps, so they are not formed per tile: every tile
@@ -64,9 +64,13 @@ using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::tc_wait;
 
-constexpr int kChunks = kLatentRow / 64;        // 9: eight latent chunks, then the rotary one
-constexpr int kRopeChunk = kChunks - 1;
+constexpr int kChunks = kLatentRow / 64;        // 9 column chunks: 8 latent, 1 rotary
+constexpr int kRegions = 2;
 constexpr int kPairs = kLatentDim / 128;        // 4 O^T products of 128 dims
+// first chunk and chunks of a region; the pairs (128 dims) whose values it holds
+__host__ __device__ constexpr int region_first(int g) { return g == 0 ? 4 : 0; }
+__host__ __device__ constexpr int region_chunks(int g) { return g == 0 ? 5 : 4; }
+constexpr int kRegionPairs = 2;
 constexpr int kSoftWarps = 8;
 constexpr int kWarpLoad = 8, kWarpScore = 9, kWarpOut = 10;
 constexpr int kLatThreads = 11 * 32;
@@ -75,29 +79,34 @@ constexpr float kLowest = -3.0e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
 
 // NH: heads (instruction columns) of a block; T: tokens of a tile, a multiple
-// of 16 up to 128 (the products always have 128 rows: rows past T read
+// of 16 up to 128 (the score products always have 128 rows: rows past T read
 // whatever follows in shared memory and are ignored); ST: tiles in flight.
 template <int NH_, int T_, int ST_>
 struct LatentShape {
   static constexpr int NH = NH_, T = T_, ST = ST_, HH = NH_ / 2;
   static constexpr int kBoxes = T / 16;
-  static constexpr int kSlot = T * 128;             // one chunk of a tile
-  static constexpr int kStage = kChunks * kSlot;
+  static constexpr int kQuads = (T + 31) / 32;      // lane quadrants that hold tokens
+  // 8 tokens of a region: the stride of the products' 8-row groups
+  __host__ __device__ static constexpr int group(int g) { return region_chunks(g) * 1024; }
+  __host__ __device__ static constexpr int region(int g) { return g == 0 ? 0 : T / 8 * group(0); }
+  static constexpr int kStage = T / 8 * kChunks * 1024;
   static constexpr int kQChunk = NH * 128;
   static constexpr int kQ = kChunks * kQChunk;
   static constexpr int kP = T * 128;                // [token][64 heads] bf16, 128-byte rows
   static constexpr uint32_t kColO = 0, kColS = kPairs * NH;
   static_assert(T % 16 == 0 && T <= 128 && NH % 16 == 0 && NH <= 64, "shape");
   static_assert(kColS + 2 * NH <= 512, "tensor-memory columns");
-  // score products read 128 rows from the last slot on: Q and P lie behind
-  static_assert(kQ + kP >= (128 - T) * 128, "rows past the tile stay inside the allocation");
+  // bytes behind the last stage that the score products' 128 rows reach: the
+  // allocation goes at least that far
+  static constexpr int kTail = region(1) + 16 * group(1) - kStage > 16 * group(0) - kStage
+                                   ? region(1) + 16 * group(1) - kStage
+                                   : 16 * group(0) - kStage;
 };
 
 template <class C>
 struct LatentSmem {
-  uint64_t full[C::ST][kChunks];     // chunk landed
-  uint64_t epair[C::ST][kPairs];     // a pair's P.V products done
-  uint64_t erope[C::ST];             // the tile's rotary products done
+  uint64_t full[C::ST][kRegions];    // region landed
+  uint64_t empty[C::ST][kRegions];   // its P.V products done
   uint64_t qfull, qfree;
   uint64_t sfull[2], sfree[2];
   uint64_t pfull, pvdone, ofree;
@@ -105,13 +114,15 @@ struct LatentSmem {
   uint64_t fin;
   uint32_t tmem_base;
   int abort_flag;
-  int raise[2][2][4];                // [phase parity][half][quadrant]
-  float top[2][2][4][C::HH];         // column maxima / sums, [phase parity][half][quadrant]
+  int raise[2][2][C::kQuads];                      // [phase parity][half][quadrant]
+  float top[2][2][C::kQuads][C::HH];               // column maxima / sums, likewise
+  float base[kSoftWarps][C::HH];                   // a warp's copy of its heads' bases
 };
 
 template <class C>
 constexpr int latent_smem() {
-  return 1024 + C::ST * C::kStage + C::kQ + C::kP + (int)sizeof(LatentSmem<C>);
+  const int used = C::kQ + C::kP + (int)sizeof(LatentSmem<C>);
+  return C::ST * C::kStage + (used > C::kTail ? used : C::kTail);
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -200,11 +211,13 @@ __device__ __forceinline__ LatentItem item_at(const LatentArgs& a, int it) {
 template <class C>
 __global__ void __launch_bounds__(kLatThreads, 1)
     latent_decode_kernel(const __grid_constant__ LatentArgs a) {
-  extern __shared__ uint8_t raw[];
+  extern __shared__ __align__(1024) uint8_t sC[];   // the swizzle repeats every 1024 bytes
   if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
-  // the 128-byte swizzle repeats every 1024 bytes
-  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint8_t* sC = smem;
+  if ((smem_u32(sC) & 1023u) != 0) {   // the compiler's alignment was not honoured
+    if (threadIdx.x == 0) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+    pdl_wait();
+    return;
+  }
   uint8_t* sQ = sC + C::ST * C::kStage;
   uint8_t* sP = sQ + C::kQ;
   LatentSmem<C>* sh = reinterpret_cast<LatentSmem<C>*>(sP + C::kP);
@@ -218,11 +231,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::ST; ++s) {
-      for (int c = 0; c < kChunks; ++c) mbar_init(&sh->full[s][c], 1);
-      for (int p = 0; p < kPairs; ++p) mbar_init(&sh->epair[s][p], 1);
-      mbar_init(&sh->erope[s], 1);
-    }
+    for (int s = 0; s < C::ST; ++s)
+      for (int g = 0; g < kRegions; ++g) {
+        mbar_init(&sh->full[s][g], 1);
+        mbar_init(&sh->empty[s][g], 1);
+      }
     mbar_init(&sh->qfull, 1);
     mbar_init(&sh->qfree, 1);
     for (int b = 0; b < 2; ++b) {
@@ -256,7 +269,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     const uint64_t policy = a.blocks > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
     const int P = a.page_size;
     int r = 0, nq = 0;
-    int extra = 0;   // chunks issued of a tile that a timeout cut short
+    int extra = 0;   // regions issued of a tile that a timeout cut short
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
       const LatentItem w = item_at(a, it);
@@ -267,75 +280,62 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       if (lane == 0) {
         ++nq;
         mbar_arrive_expect_tx(&sh->qfull, (uint32_t)C::kQ);
-        for (int c = 0; c < kChunks; ++c)
-          tensor_copy3_g2s(sQ + c * C::kQChunk, &a.q_map, 64 * c, C::NH * w.block, w.req, &sh->qfull,
-                           policy);
       }
       __syncwarp();
+      if (lane < kChunks)
+        tensor_copy3_g2s(sQ + lane * C::kQChunk, &a.q_map, 64 * lane, C::NH * w.block, w.req,
+                         &sh->qfull, policy);
       // page ids of 32 consecutive 16-token boxes, one per lane (items start
-      // on page boundaries)
+      // on page boundaries); the next 32 are fetched while these are copied
       const int boxes = (w.te - w.tb + 15) >> 4;
-      int base = -32, my_page = 0;
+      const int32_t* pages = a.sched + a.off_pages + w.page0;
+      auto page_of = [&](int box) { return box < boxes ? pages[16 * box / P] : 0; };
+      int base = 0, my_page = page_of(lane), next_page = page_of(32 + lane);
       for (int t = w.tb, k = 0; t < w.te; t += C::T, ++k, ++r) {
         const int nbox = min(C::kBoxes, (w.te - t + 15) >> 4);
-        const int box0 = C::kBoxes * k;
-        if (box0 + C::kBoxes > base + 32) {
-          base = box0;
-          my_page = 0;
-          if (base + lane < boxes) {
-            my_page = a.sched[a.off_pages + w.page0 + (16 * (base + lane)) / P];
-            if ((unsigned)my_page >= (unsigned)a.num_pages) {
-              atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
-              my_page = 0;
-            }
-          }
-        }
         const int st = r % C::ST;
         const uint32_t use = (uint32_t)(r / C::ST);
-        uint8_t* stage = sC + st * C::kStage;
-        // lane 8 c + j copies box j of chunk c of the pair (lanes 0-15); the
-        // rotary chunk (lanes 0-7) goes first, as its slot is free first
-        const int j = lane & 7, cc = lane >> 3;
-        const int page = __shfl_sync(kFull, my_page, (box0 + j - base) & 31);
-        const int tok = (t + 16 * j) % P;
-        const uint32_t bytes = (uint32_t)nbox * 2048u;
-        if (use > 0 && !tc_wait(&sh->erope[st], (use - 1) & 1u, abort_flag, a.err, lane)) {
-          ok = false;
-          break;
+        // lane j copies box j of the tile
+        const int box = C::kBoxes * k + lane % C::kBoxes;
+        const int late = __shfl_sync(kFull, next_page, box & 31);
+        int page = __shfl_sync(kFull, my_page, box & 31);
+        if (box >= base + 32) page = late;
+        if (C::kBoxes * (k + 1) >= base + 32) {
+          base += 32;
+          my_page = next_page;
+          next_page = page_of(base + 32 + lane);
         }
-        if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][kRopeChunk], bytes);
-        __syncwarp();
-        if (cc == 0 && j < nbox)
-          tensor_copy3_g2s(stage + kRopeChunk * C::kSlot + j * 2048, &a.kv_map, 64 * kRopeChunk, tok,
-                           page, &sh->full[st][kRopeChunk], policy);
-        extra = 1;
-        for (int p = 0; p < kPairs; ++p) {
-          if (use > 0 && !tc_wait(&sh->epair[st][p], (use - 1) & 1u, abort_flag, a.err, lane)) {
+        if ((unsigned)page >= (unsigned)a.num_pages) {
+          atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+          page = 0;
+        }
+        const int tok = (t + 16 * lane) % P;
+#pragma unroll
+        for (int g = 0; g < kRegions; ++g) {
+          if (ok && use > 0 && !tc_wait(&sh->empty[st][g], (use - 1) & 1u, abort_flag, a.err, lane))
             ok = false;
-            break;
-          }
-          if (lane < 2) mbar_arrive_expect_tx(&sh->full[st][2 * p + lane], bytes);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][g], (uint32_t)(nbox * 2 * C::group(g)));
           __syncwarp();
-          if (cc < 2 && j < nbox) {
-            const int c = 2 * p + cc;
-            tensor_copy3_g2s(stage + c * C::kSlot + j * 2048, &a.kv_map, 64 * c, tok, page,
-                             &sh->full[st][c], policy);
-          }
-          extra += 2;
+          if (lane < nbox)
+            tensor_copy_g2s(sC + st * C::kStage + C::region(g) + lane * 2 * C::group(g),
+                            &a.kv_map[g], 0, 0, region_first(g), tok / 8, page, &sh->full[st][g],
+                            policy);
+          ++extra;
         }
         if (!ok) break;
         extra = 0;
       }
     }
-    // drain: no copy may be in flight when the block ends.  Chunk c of stage
+    // drain: no copy may be in flight when the block ends.  Region g of stage
     // s was copied once per whole tile of the stage, and once more when it
-    // was among the first chunks of a tile cut short.
+    // was among the first of a tile cut short.
     if (lane == 0) {
       for (int s = 0; s < C::ST; ++s)
-        for (int c = 0; c < kChunks; ++c) {
+        for (int g = 0; g < kRegions; ++g) {
           int uses = r > s ? (r - 1 - s) / C::ST + 1 : 0;
-          if (s == r % C::ST && (c == kRopeChunk ? 0 : c + 1) < extra) ++uses;
-          if (uses > 0 && !mbar_wait(&sh->full[s][c], (uint32_t)((uses - 1) & 1), nullptr))
+          if (s == r % C::ST && g < extra) ++uses;
+          if (uses > 0 && !mbar_wait(&sh->full[s][g], (uint32_t)((uses - 1) & 1), nullptr))
             atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
         }
       if (nq > 0 && !mbar_wait(&sh->qfull, (uint32_t)((nq - 1) & 1), nullptr))
@@ -346,7 +346,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     // -------------------------------------------------------- S^T products
     const bool me = elect_one();
     const uint32_t idesc = tc::mma_idesc(128, C::NH, 0);
-    const uint64_t c0 = smem_desc(smem_u32(sC), 16, 1024);
+    uint64_t c0[kRegions];
+#pragma unroll
+    for (int g = 0; g < kRegions; ++g)
+      c0[g] = smem_desc(smem_u32(sC) + C::region(g), 16, C::group(g));
     const uint64_t q0 = smem_desc(smem_u32(sQ), 16, 1024);
     int r = 0;
     bool ok = true;
@@ -361,18 +364,20 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           break;
         }
         const uint32_t d = tmem + C::kColS + C::NH * b;
-        const uint64_t cs = c0 + (uint64_t)(st * (C::kStage >> 4));
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int c = i == 0 ? kRopeChunk : i - 1;
-          if (ok && !tc_wait(&sh->full[st][c], use & 1u, abort_flag, a.err, lane)) ok = false;
+        for (int g = 0; g < kRegions; ++g) {
+          if (ok && !tc_wait(&sh->full[st][g], use & 1u, abort_flag, a.err, lane)) ok = false;
           if (ok && me) {
             tc_fence_after();
+            const uint64_t cs = c0[g] + (uint64_t)(st * (C::kStage >> 4));
+            const uint64_t qs = q0 + (uint64_t)(region_first(g) * (C::kQChunk >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss(d, cs + (uint64_t)(c * (C::kSlot >> 4) + 2 * kk),
-                     q0 + (uint64_t)(c * (C::kQChunk >> 4) + 2 * kk), idesc, i > 0 || kk > 0);
-            if (i == 0) mma_commit(&sh->erope[st]);
+            for (int i = 0; i < region_chunks(g); ++i)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss(d, cs + (uint64_t)(64 * i + 2 * kk),
+                       qs + (uint64_t)(i * (C::kQChunk >> 4) + 2 * kk), idesc,
+                       g > 0 || i > 0 || kk > 0);
           }
           __syncwarp();
         }
@@ -393,7 +398,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     // -------------------------------------------------------- O^T products
     const bool me = elect_one();
     const uint32_t idesc = tc::mma_idesc(128, C::NH, 1) | (1u << 15);   // A and B MN-major
-    const uint64_t c0 = smem_desc(smem_u32(sC), C::kSlot, 1024);
+    uint64_t c0[kRegions];   // 64-dim blocks 1 KB apart, 8-token groups a group apart
+#pragma unroll
+    for (int g = 0; g < kRegions; ++g)
+      c0[g] = smem_desc(smem_u32(sC) + C::region(g), 1024, C::group(g));
     const uint64_t p0 = smem_desc(smem_u32(sP), 16, 1024);
     int r = 0;
     bool ok = true;
@@ -413,8 +421,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           // rows past the last token: their P is 0, but 0 x NaN would stay
           const int rows = 16 * nbox - n;
           for (int i = lane; i < 2 * kPairs * rows * 8; i += 32) {
-            const int c = i / (rows * 8), rem = i % (rows * 8);
-            *reinterpret_cast<uint4*>(sC + st * C::kStage + c * C::kSlot + (n + rem / 8) * 128 +
+            const int c = i / (rows * 8), rem = i % (rows * 8), row = n + rem / 8;
+            const int g = c >= region_first(0) ? 0 : 1;
+            *reinterpret_cast<uint4*>(sC + st * C::kStage + C::region(g) + (row >> 3) * C::group(g) +
+                                      (c - region_first(g)) * 1024 + (row & 7) * 128 +
                                       (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -422,15 +432,18 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         }
         if (me) {
           tc_fence_after();
-          const uint64_t cs = c0 + (uint64_t)(st * (C::kStage >> 4));
 #pragma unroll
-          for (int p = 0; p < kPairs; ++p) {
+          for (int g = 0; g < kRegions; ++g) {
+            const uint64_t cs = c0[g] + (uint64_t)(st * (C::kStage >> 4));
 #pragma unroll
-            for (int kk = 0; kk < C::kBoxes; ++kk)
-              if (kk < nbox)
-                mma_ss(tmem + C::kColO + C::NH * p, cs + (uint64_t)(p * (C::kSlot >> 3) + 128 * kk),
-                       p0 + (uint64_t)(128 * kk), idesc, t > w.tb || kk > 0);
-            mma_commit(&sh->epair[st][p]);
+            for (int p = 0; p < kRegionPairs; ++p)
+#pragma unroll
+              for (int kk = 0; kk < C::kBoxes; ++kk)
+                if (kk < nbox)
+                  mma_ss(tmem + C::kColO + C::NH * (region_first(g) / 2 + p),
+                         cs + (uint64_t)(128 * p + kk * (C::group(g) >> 3)),
+                         p0 + (uint64_t)(128 * kk), idesc, t > w.tb || kk > 0);
+            mma_commit(&sh->empty[st][g]);
           }
           mma_commit(&sh->pvdone);
         }
@@ -463,43 +476,54 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     };
     for (int it = it0; it < it1 && ok; ++it) {
       const LatentItem w = item_at(a, it);
-      float m[HH], l[HH];   // base (log2 units) of this half's heads; this token lane's sums
+      // base[j] (log2 units) of this half's heads, a copy per warp in shared
+      // memory; l: this token lane's sums
+      float l[HH];
+      float sum_base = 0.f;   // of lane's head: base[lane] outside the raise below
+      float* base = sh->base[warp];
 #pragma unroll
-      for (int j = 0; j < HH; ++j) {
-        m[j] = -CUDART_INF_F;
-        l[j] = 0.f;
-      }
+      for (int j = 0; j < HH; ++j) l[j] = 0.f;
+      __syncwarp();
+      if (lane < HH) base[lane] = 0.f;
+      __syncwarp();
       for (int t = w.tb; t < w.te && ok; t += C::T, ++r) {
         const int b = r & 1;
         if (!tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        uint32_t sv[HH];
-        tmem_ldn<HH>(tq + C::kColS + C::NH * b + HH * half, sv);
-        tc::tmem_wait_ld();
-        tc_fence_before();
+        const bool first = t == w.tb;
+        const bool live = row < min(C::T, w.te - t);
+        float y[HH];   // scores over the base
+        if (quad < C::kQuads) {
+          tc_fence_after();
+          uint32_t sv[HH];
+          tmem_ldn<HH>(tq + C::kColS + C::NH * b + HH * half, sv);
+          tc::tmem_wait_ld();
+          tc_fence_before();
+          float over = -CUDART_INF_F;
+#pragma unroll
+          for (int j = 0; j < HH; j += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(base + j);
+            y[j] = live ? fmaf(__uint_as_float(sv[j]), a.scale_log2, -m.x) : -CUDART_INF_F;
+            y[j + 1] = live ? fmaf(__uint_as_float(sv[j + 1]), a.scale_log2, -m.y) : -CUDART_INF_F;
+            y[j + 2] = live ? fmaf(__uint_as_float(sv[j + 2]), a.scale_log2, -m.z) : -CUDART_INF_F;
+            y[j + 3] = live ? fmaf(__uint_as_float(sv[j + 3]), a.scale_log2, -m.w) : -CUDART_INF_F;
+            over = fmaxf(fmaxf(fmaxf(over, y[j]), fmaxf(y[j + 1], y[j + 2])), y[j + 3]);
+          }
+          const bool want = __any_sync(kFull, over > kRaiseLog2) || first;
+          if (lane == 0) sh->raise[xc & 1u][half][quad] = want ? 1 : 0;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->sfree[b]);
-        const bool live = row < min(C::T, w.te - t);
-        float x[HH];
-        float over = -CUDART_INF_F;
-#pragma unroll
-        for (int j = 0; j < HH; ++j) {
-          x[j] = live ? __uint_as_float(sv[j]) * a.scale_log2 : -CUDART_INF_F;
-          over = fmaxf(over, x[j] - m[j]);   // NaN (-inf - -inf) is ignored
-        }
-        const bool first = t == w.tb;
         const int par = (int)(xc & 1u);
-        const bool want = __any_sync(kFull, over > kRaiseLog2) || first;
-        if (lane == 0) sh->raise[par][half][quad] = want ? 1 : 0;
         if (!meet()) {
           ok = false;
           break;
         }
-        const bool up = (sh->raise[par][half][0] | sh->raise[par][half][1] |
-                         sh->raise[par][half][2] | sh->raise[par][half][3]) != 0;
+        int up = 0;
+#pragma unroll
+        for (int q = 0; q < C::kQuads; ++q) up |= sh->raise[par][half][q];
         // P of the tile before is read (its buffer is written below, and a
         // raised base rescales O)
         if (r > 0 && !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) {
@@ -508,28 +532,30 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         }
         if (up) {
           const int par2 = (int)(xc & 1u);
+          if (quad < C::kQuads) {
 #pragma unroll
-          for (int j = 0; j < HH; ++j) {
-            const int top = __reduce_max_sync(kFull, order_of(x[j]));
-            if (lane == 0) sh->top[par2][half][quad][j] = from_order(top);
+            for (int j = 0; j < HH; ++j) {
+              const int top = __reduce_max_sync(kFull, order_of(y[j]));
+              if (lane == 0) sh->top[par2][half][quad][j] = from_order(top);
+            }
           }
           if (!meet()) {
             ok = false;
             break;
           }
-          float f[HH];
+          // how far each base rises; it stays finite, so that scores of -inf
+          // weigh 0 (not -inf - -inf).  A lane per head, then all read.
+          if (lane < HH) {
+            int top = order_of(sh->top[par2][half][0][lane]);
 #pragma unroll
-          for (int j = 0; j < HH; ++j) {
-            int top = order_of(m[j]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) top = max(top, order_of(sh->top[par2][half][q][j]));
-            // finite, so that scores of -inf weigh 0 (not -inf - -inf)
-            const float nm = top < order_of(kLowest) ? kLowest : from_order(top);
-            f[j] = first ? 0.f : exp2f(m[j] - nm);
-            m[j] = nm;
-            l[j] = first ? 0.f : l[j] * f[j];
+            for (int q = 1; q < C::kQuads; ++q)
+              top = max(top, order_of(sh->top[par2][half][q][lane]));
+            if (!first) top = max(top, 0);
+            base[lane] = top < order_of(kLowest) ? kLowest : from_order(top);
           }
+          __syncwarp();
           if (!first) {
+            // O shrinks by 2^-rise
             tc_fence_after();
             constexpr int kPart = HH < 16 ? HH : 16;   // columns at a time: the registers
 #pragma unroll
@@ -542,43 +568,59 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < kPart; ++j)
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) * f[c + j]);
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * exp2f(-base[c + j]));
                 tmem_stn<kPart>(col, o);
               }
             tc::tmem_wait_st();
           }
-        }
-        // weights 2^(x - m); this thread's row of P: 16-byte pieces of 8
-        // heads, swizzled as the products read them
-        uint32_t pw[HH / 2];
 #pragma unroll
-        for (int j = 0; j < HH; j += 2) {
-          const float p0 = live ? fast_exp2(x[j] - m[j]) : 0.f;
-          const float p1 = live ? fast_exp2(x[j + 1] - m[j + 1]) : 0.f;
-          l[j] += p0;
-          l[j + 1] += p1;
-          pw[j / 2] = pack_bf16(p0, p1);
+          for (int j = 0; j < HH; ++j) {
+            const float rise = base[j];
+            l[j] = first ? 0.f : l[j] * exp2f(-rise);
+            if (quad < C::kQuads) y[j] -= rise;
+          }
+          __syncwarp();
+          if (lane < HH) {
+            sum_base += base[lane];
+            base[lane] = sum_base;
+          }
+          __syncwarp();
         }
-        if (row < C::T) {
+        // weights 2^y; this thread's row of P: 16-byte pieces of 8 heads,
+        // swizzled as the products read them
+        if (quad < C::kQuads) {
+          uint32_t pw[HH / 2];
 #pragma unroll
-          for (int i = 0; i < HH / 8; ++i)
-            *reinterpret_cast<uint4*>(sP + row * 128 + (((half * (HH / 8) + i) ^ (row & 7)) << 4)) =
-                make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
+          for (int j = 0; j < HH; j += 2) {
+            const float p0 = live ? fast_exp2(y[j]) : 0.f;
+            const float p1 = live ? fast_exp2(y[j + 1]) : 0.f;
+            l[j] += p0;
+            l[j + 1] += p1;
+            pw[j / 2] = pack_bf16(p0, p1);
+          }
+          if (row < C::T) {
+#pragma unroll
+            for (int i = 0; i < HH / 8; ++i)
+              *reinterpret_cast<uint4*>(sP + row * 128 + (((half * (HH / 8) + i) ^ (row & 7)) << 4)) =
+                  make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
+          }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->pfull);
       }
       if (!ok) break;
-      // ---- epilogue: sums over the 128 token lanes in a fixed order
+      // ---- epilogue: sums over the token lanes in a fixed order
       const int par = (int)(xc & 1u);
+      if (quad < C::kQuads) {
 #pragma unroll
-      for (int j = 0; j < HH; ++j) {
-        float z = l[j];
+        for (int j = 0; j < HH; ++j) {
+          float z = l[j];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-        if (lane == 0) sh->top[par][half][quad][j] = z;
+          for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+          if (lane == 0) sh->top[par][half][quad][j] = z;
+        }
       }
       if (!meet() || !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) {
         ok = false;
@@ -590,20 +632,23 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         waited = true;
       }
       const int h0 = C::NH * w.block + HH * half;
-      float inv[HH];
+      if (lane < HH) {
+        float z = sh->top[par][half][0][lane];
 #pragma unroll
-      for (int j = 0; j < HH; ++j) {
-        const float z = (sh->top[par][half][0][j] + sh->top[par][half][1][j]) +
-                        (sh->top[par][half][2][j] + sh->top[par][half][3][j]);
-        inv[j] = z == 0.f ? 0.f : a.v_scale / z;   // every score -inf: an empty state
-        if (quad == 0 && lane == 0 && h0 + j < a.heads) {
-          const float lse = (m[j] + log2f(z)) * kLn2;
+        for (int q = 1; q < C::kQuads; ++q) z += sh->top[par][half][q][lane];
+        base[lane] = z == 0.f ? 0.f : a.v_scale / z;   // 0: every score -inf, an empty state
+        if (quad == 0 && h0 + lane < a.heads) {
+          const float lse = (sum_base + log2f(z)) * kLn2;
           if (w.dst >= 0)
-            a.l_part[(int64_t)w.dst * a.heads + h0 + j] = lse;
+            a.l_part[(int64_t)w.dst * a.heads + h0 + lane] = lse;
           else if (a.lse != nullptr)
-            a.lse[(int64_t)w.req * a.heads + h0 + j] = lse;
+            a.lse[(int64_t)w.req * a.heads + h0 + lane] = lse;
         }
       }
+      __syncwarp();
+      float inv[HH];
+#pragma unroll
+      for (int j = 0; j < HH; ++j) inv[j] = base[j];
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         uint32_t o[HH];
@@ -706,7 +751,7 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant
 
 using Shape16 = LatentShape<16, 64, 2>;
 using Shape32 = LatentShape<32, 64, 2>;
-using Shape64 = LatentShape<64, 112, 1>;
+using Shape64 = LatentShape<64, 64, 2>;
 static_assert(latent_smem<Shape16>() <= 227 * 1024 && latent_smem<Shape32>() <= 227 * 1024 &&
                   latent_smem<Shape64>() <= 227 * 1024,
               "dynamic shared memory of one CTA");
@@ -812,20 +857,23 @@ cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool me
   return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&latent_merge_kernel), args);
 }
 
-// The cache map: {576 columns, token slot, page}, box {64 columns, 16 slots,
-// 1 page}: 2 KB, 16 rows of 128 bytes with the 128-byte swizzle.
-cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page_size,
+// The cache maps, one per region: {64 columns, token of 8, column chunk, group
+// of 8 tokens, page} with byte strides {row, 128, 8 rows, page}; box {64, 8,
+// the region's chunks, 2 groups, 1 page}, which lands as [group][chunk][8
+// tokens][128 bytes] with the 128-byte swizzle.
+cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page_size, int region,
                               CUtensorMap* map) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   if (cache == nullptr || (uintptr_t)cache % 16 != 0 || page_size % 16 != 0 || num_pages < 1)
     return cudaErrorInvalidValue;
   const cuuint64_t row = (cuuint64_t)kLatentRow * 2;
-  const cuuint64_t dims[3] = {(cuuint64_t)kLatentRow, (cuuint64_t)page_size, (cuuint64_t)num_pages};
-  const cuuint64_t strides[2] = {row, row * (cuuint64_t)page_size};
-  const cuuint32_t box[3] = {64, 16, 1};
-  const cuuint32_t elem[3] = {1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(cache), dims, strides,
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)kChunks, (cuuint64_t)(page_size / 8),
+                              (cuuint64_t)num_pages};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, row * (cuuint64_t)page_size};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)region_chunks(region), 2, 1};
+  const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(cache), dims, strides,
                 box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
