@@ -153,9 +153,11 @@ typedef struct pkd_config {
  * (the value up-projection is the caller's, after it) and the lse of those
  * scores; the softmax scale is k_scale itself, since 576 is not the width the
  * heads were trained with (pkd_run's is 1: use pkd_run_scaled).  head_dim 512,
- * num_kv_heads 1, 1 <= Hq <= 128, page size a multiple of 16; combinable with
- * PKD_FLAG_CHUNK_SEARCH only.  Plans are pkd_plan's; a work item covers up to
- * 64 heads.  Graphs replay with the batch they were captured with. */
+ * num_kv_heads 1, 1 <= Hq <= 128, page size a multiple of 16; no other flag.
+ * Plans (pkd_plan) cut the requests' tokens, laid end to end, into equal
+ * stretches, one per CTA -- per CTA pair above 64 heads, a work item covering
+ * up to 64; alpha < 0 selects 128 and min_chunk_tokens < 0 128.  Graphs replay
+ * with the batch they were captured with. */
 #define PKD_FLAG_LATENT 1024u
 
 typedef struct pkd_ctx pkd_ctx;

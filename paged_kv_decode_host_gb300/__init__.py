@@ -833,22 +833,19 @@ class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
 
     def __init__(self, num_heads, latent_dim, rope_dim, page_size, *, scale, max_batch,
                  max_num_pages, num_pages, alpha=-1, min_chunk_tokens=-1, num_ctas=0,
-                 chunk_rule="closed", device=None):
+                 device=None):
         import math
         import torch
         if (latent_dim, rope_dim) != (LATENT_DIM, LATENT_ROPE):
             raise PkdError(-3, f"latent_dim {LATENT_DIM} and rope_dim {LATENT_ROPE} are supported")
         if not math.isfinite(scale):
             raise ValueError("scale must be finite")
-        if chunk_rule not in ("closed", "search"):
-            raise ValueError("chunk_rule must be 'closed' or 'search'")
         self.device = torch.device("cuda" if device is None else device)
         self.hq, self.hkv, self.d, self.p = num_heads, 1, latent_dim, page_size
         self.num_pages, self.scale = num_pages, float(scale)
         self.kv_dtype, self.kv_layout = "bf16", "latent"
         self._create(make_config(num_heads, 1, latent_dim, page_size, max_batch, max_num_pages,
-                                 num_pages, alpha, min_chunk_tokens, num_ctas,
-                                 FLAG_LATENT | (FLAG_CHUNK_SEARCH if chunk_rule == "search" else 0)))
+                                 num_pages, alpha, min_chunk_tokens, num_ctas, FLAG_LATENT))
 
     def _check_run_args(self, q, kv_cache, out, lse):
         import torch

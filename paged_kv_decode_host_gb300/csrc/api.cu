@@ -76,8 +76,8 @@ bool valid_flags(uint32_t f) {
                          PKD_FLAG_HND | PKD_FLAG_DENSE_PREFIX | PKD_FLAG_CASCADE |
                          PKD_FLAG_LATENT;
   if (f & ~known) return false;
-  // a latent cache has one layout, one type and a kernel of its own
-  if ((f & PKD_FLAG_LATENT) && (f & ~(PKD_FLAG_LATENT | PKD_FLAG_CHUNK_SEARCH))) return false;
+  // a latent cache has one layout, one type, a planner and a kernel of its own
+  if ((f & PKD_FLAG_LATENT) && f != PKD_FLAG_LATENT) return false;
   // a cascade context runs both of its levels itself: bf16 page tiles,
   // tensor cores, either layout
   if ((f & PKD_FLAG_CASCADE) && (f & ~(PKD_FLAG_CASCADE | PKD_FLAG_MMA_CONSUMER | PKD_FLAG_HND)))
@@ -515,7 +515,12 @@ static int plan_and_publish(pkd_ctx* ctx, PlanFn plan_fn, void* stream, uint64_t
   }
   int32_t* words = ctx->staging[k];
   pkd_plan_info info{};
-  int st = plan_fn(words, &info);
+  int st = PKD_OK;
+  try {
+    st = plan_fn(words, &info);
+  } catch (...) {   // the planner's working arrays found no memory
+    st = PKD_E_CAPACITY;
+  }
   if (st != PKD_OK) return st;
   const Layout& L = ctx->layout;
   // two copies in stream order: first the body (cta queues, items, units,

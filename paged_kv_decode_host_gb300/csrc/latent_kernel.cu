@@ -29,10 +29,11 @@
 //  * warp 9 issues the score products of a region as it lands, warp 10 the P.V
 //    products, whose regions are refilled one after the other; the whole warp
 //    runs the loop and one elected lane issues, with unrolled constant
-//    descriptor steps: 47 / 56 cycles per 128 x 16 / 128 x 64 product, where a
-//    lone thread that forms descriptors in the loop takes 135;
-//  * warps 0-7 are the softmax: a thread holds one token (a tensor-memory
-//    lane) and half of the block's heads.  The maxima run over tokens, that
+//    descriptor steps: 29 / 38 cycles per 64 x 16 / 64 x 64 product and 45 /
+//    54 with 128 rows, where a lone thread that forms descriptors in the loop
+//    takes 135 for any;
+//  * warps 0-7 are the softmax: a thread holds one token and a quarter of the
+//    block's heads.  The maxima run over tokens, that
 //    is, across lanes and warps, so they are not formed per tile: every tile
 //    is only compared with the running base, and the exact maxima are taken
 //    when some score exceeds its head's base by more than 2^8 (always in an
@@ -78,35 +79,32 @@ constexpr float kRaiseLog2 = 8.f;
 constexpr float kLowest = -3.0e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
 
-// NH: heads (instruction columns) of a block; T: tokens of a tile, a multiple
-// of 16 up to 128 (the score products always have 128 rows: rows past T read
-// whatever follows in shared memory and are ignored); ST: tiles in flight.
-template <int NH_, int T_, int ST_>
+// Tokens of a tile: the 64 rows of a score product.  (128-row products take
+// 45 to 54 cycles against 28 to 38, and two tiles of 128 tokens do not fit
+// shared memory beside the queries.)
+constexpr int kTile = 64, kBoxes = kTile / 16;
+constexpr int kStages = 2;
+// 8 tokens of a region: the stride of the products' 8-row groups
+__host__ __device__ constexpr int group_bytes(int g) { return region_chunks(g) * 1024; }
+__host__ __device__ constexpr int region_at(int g) { return g == 0 ? 0 : kTile / 8 * group_bytes(0); }
+constexpr int kStage = kTile / 8 * kChunks * 1024;
+constexpr int kP = kTile * 128;   // [token][64 heads] bf16, 128-byte rows
+
+// NH: heads (instruction columns) of a block.
+template <int NH_>
 struct LatentShape {
-  static constexpr int NH = NH_, T = T_, ST = ST_, HH = NH_ / 2;
-  static constexpr int kBoxes = T / 16;
-  static constexpr int kQuads = (T + 31) / 32;      // lane quadrants that hold tokens
-  // 8 tokens of a region: the stride of the products' 8-row groups
-  __host__ __device__ static constexpr int group(int g) { return region_chunks(g) * 1024; }
-  __host__ __device__ static constexpr int region(int g) { return g == 0 ? 0 : T / 8 * group(0); }
-  static constexpr int kStage = T / 8 * kChunks * 1024;
+  static constexpr int NH = NH_;
+  static constexpr int HH = NH / 2, QH = NH / 4;   // heads of a softmax warp, of a thread
   static constexpr int kQChunk = NH * 128;
   static constexpr int kQ = kChunks * kQChunk;
-  static constexpr int kP = T * 128;                // [token][64 heads] bf16, 128-byte rows
   static constexpr uint32_t kColO = 0, kColS = kPairs * NH;
-  static_assert(T % 16 == 0 && T <= 128 && NH % 16 == 0 && NH <= 64, "shape");
-  static_assert(kColS + 2 * NH <= 512, "tensor-memory columns");
-  // bytes behind the last stage that the score products' 128 rows reach: the
-  // allocation goes at least that far
-  static constexpr int kTail = region(1) + 16 * group(1) - kStage > 16 * group(0) - kStage
-                                   ? region(1) + 16 * group(1) - kStage
-                                   : 16 * group(0) - kStage;
+  static_assert(NH % 16 == 0 && NH <= 64 && kColS + 2 * NH <= 512, "shape");
 };
 
 template <class C>
 struct LatentSmem {
-  uint64_t full[C::ST][kRegions];    // region landed
-  uint64_t empty[C::ST][kRegions];   // its P.V products done
+  uint64_t full[kStages][kRegions];    // region landed
+  uint64_t empty[kStages][kRegions];   // its P.V products done
   uint64_t qfull, qfree;
   uint64_t sfull[2], sfree[2];
   uint64_t pfull, pvdone, ofree;
@@ -114,15 +112,13 @@ struct LatentSmem {
   uint64_t fin;
   uint32_t tmem_base;
   int abort_flag;
-  int raise[2][2][C::kQuads];                      // [phase parity][half][quadrant]
-  float top[2][2][C::kQuads][C::HH];               // column maxima / sums, likewise
-  float base[kSoftWarps][C::HH];                   // a warp's copy of its heads' bases
+  int raise[2][2][4];                              // [phase parity][half][quadrant]
+  float top[2][2][4][C::HH];                       // column maxima / sums, likewise
 };
 
 template <class C>
 constexpr int latent_smem() {
-  const int used = C::kQ + C::kP + (int)sizeof(LatentSmem<C>);
-  return C::ST * C::kStage + (used > C::kTail ? used : C::kTail);
+  return kStages * kStage + C::kQ + kP + (int)sizeof(LatentSmem<C>);
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -146,6 +142,36 @@ __device__ __forceinline__ void tensor_copy3_g2s(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)),
       "l"(policy)
       : "memory");
+}
+
+// A 64-row product keeps row 16 q + i in lane 32 q + i, i < 16.  Lanes 0-15
+// of the warp get N columns of the quadrant's 16 rows from column t on, lanes
+// 16-31 the same rows' N columns from t + N on.
+template <int N>
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t t, uint32_t (&r)[N]) {
+  static_assert(N == 4 || N == 8 || N == 16, "columns");
+  if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16], 16;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(t)
+        : "memory");
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0,%1,%2,%3}, [%4], 4;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(t)
+                 : "memory");
+  }
 }
 
 // N columns of this warp's 32 lanes
@@ -191,13 +217,35 @@ __device__ __forceinline__ void tmem_stn(uint32_t t, const uint32_t (&r)[N]) {
   }
 }
 
-// fp32 order as signed integer order (NaN above +inf)
-__device__ __forceinline__ int order_of(float x) {
-  const int b = __float_as_int(x);
-  return b >= 0 ? b : b ^ 0x7fffffff;
+// Column-wise reduction over 16 lanes (both halves of the warp at once) of N
+// <= 16 values per lane: a butterfly that halves the columns a lane still
+// holds with every exchange (N - 1 shuffles and the rest of the log; a
+// reduction per column would take 4 N).  Lane j (mod N) of a half returns its
+// column j.
+template <int N, class Op>
+__device__ __forceinline__ float columns_over_lanes(const float (&x)[N], int lane, Op op) {
+  float v[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = x[j];
+#pragma unroll
+  for (int w = N / 2; w >= 1; w >>= 1) {   // lanes with bit w keep the upper w columns
+    const bool upper = (lane & w) != 0;
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const float send = upper ? v[j] : v[j + w];
+      const float keep = upper ? v[j + w] : v[j];
+      v[j] = op(keep, __shfl_xor_sync(kFull, send, w));
+    }
+  }
+#pragma unroll
+  for (int w = N; w < 16; w <<= 1) v[0] = op(v[0], __shfl_xor_sync(kFull, v[0], w));
+  return v[0];
 }
-__device__ __forceinline__ float from_order(int o) {
-  return __int_as_float(o >= 0 ? o : o ^ 0x7fffffff);
+// the larger, NaN above all
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
 }
 
 struct LatentItem {
@@ -218,9 +266,9 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     pdl_wait();
     return;
   }
-  uint8_t* sQ = sC + C::ST * C::kStage;
+  uint8_t* sQ = sC + kStages * kStage;
   uint8_t* sP = sQ + C::kQ;
-  LatentSmem<C>* sh = reinterpret_cast<LatentSmem<C>*>(sP + C::kP);
+  LatentSmem<C>* sh = reinterpret_cast<LatentSmem<C>*>(sP + kP);
   volatile int* abort_flag = &sh->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -230,8 +278,12 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     pdl_wait();
     return;
   }
+  if (warp == kWarpLoad && lane < 3) {   // the first copies would wait for their maps
+    const CUtensorMap* map = lane < 2 ? &a.kv_map[lane] : &a.q_map;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+  }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::ST; ++s)
+    for (int s = 0; s < kStages; ++s)
       for (int g = 0; g < kRegions; ++g) {
         mbar_init(&sh->full[s][g], 1);
         mbar_init(&sh->empty[s][g], 1);
@@ -257,6 +309,17 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // the producer's first item and its page ids, on their way while the block
+  // sets itself up
+  LatentItem item0{};
+  int page_a = 0, page_b = 0;
+  if (warp == kWarpLoad) {
+    item0 = item_at(a, it0);
+    const int boxes = (item0.te - item0.tb + 15) >> 4;
+    const int32_t* pages = a.sched + a.off_pages + item0.page0;
+    if (lane < boxes) page_a = pages[16 * lane / a.page_size];
+    if (32 + lane < boxes) page_b = pages[16 * (32 + lane) / a.page_size];
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -272,7 +335,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     int extra = 0;   // regions issued of a tile that a timeout cut short
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
-      const LatentItem w = item_at(a, it);
+      const LatentItem w = it == it0 ? item0 : item_at(a, it);
       if (it > it0 && !tc_wait(&sh->qfree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane)) {
         ok = false;
         break;
@@ -290,17 +353,21 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       const int boxes = (w.te - w.tb + 15) >> 4;
       const int32_t* pages = a.sched + a.off_pages + w.page0;
       auto page_of = [&](int box) { return box < boxes ? pages[16 * box / P] : 0; };
-      int base = 0, my_page = page_of(lane), next_page = page_of(32 + lane);
-      for (int t = w.tb, k = 0; t < w.te; t += C::T, ++k, ++r) {
-        const int nbox = min(C::kBoxes, (w.te - t + 15) >> 4);
-        const int st = r % C::ST;
-        const uint32_t use = (uint32_t)(r / C::ST);
+      int base = 0, my_page = page_a, next_page = page_b;
+      if (it > it0) {
+        my_page = page_of(lane);
+        next_page = page_of(32 + lane);
+      }
+      for (int t = w.tb, k = 0; t < w.te; t += kTile, ++k, ++r) {
+        const int nbox = min(kBoxes, (w.te - t + 15) >> 4);
+        const int st = r % kStages;
+        const uint32_t use = (uint32_t)(r / kStages);
         // lane j copies box j of the tile
-        const int box = C::kBoxes * k + lane % C::kBoxes;
+        const int box = kBoxes * k + lane % kBoxes;
         const int late = __shfl_sync(kFull, next_page, box & 31);
         int page = __shfl_sync(kFull, my_page, box & 31);
         if (box >= base + 32) page = late;
-        if (C::kBoxes * (k + 1) >= base + 32) {
+        if (kBoxes * (k + 1) >= base + 32) {
           base += 32;
           my_page = next_page;
           next_page = page_of(base + 32 + lane);
@@ -315,10 +382,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           if (ok && use > 0 && !tc_wait(&sh->empty[st][g], (use - 1) & 1u, abort_flag, a.err, lane))
             ok = false;
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][g], (uint32_t)(nbox * 2 * C::group(g)));
+          if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][g], (uint32_t)(nbox * 2 * group_bytes(g)));
           __syncwarp();
           if (lane < nbox)
-            tensor_copy_g2s(sC + st * C::kStage + C::region(g) + lane * 2 * C::group(g),
+            tensor_copy_g2s(sC + st * kStage + region_at(g) + lane * 2 * group_bytes(g),
                             &a.kv_map[g], 0, 0, region_first(g), tok / 8, page, &sh->full[st][g],
                             policy);
           ++extra;
@@ -331,10 +398,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     // s was copied once per whole tile of the stage, and once more when it
     // was among the first of a tile cut short.
     if (lane == 0) {
-      for (int s = 0; s < C::ST; ++s)
+      for (int s = 0; s < kStages; ++s)
         for (int g = 0; g < kRegions; ++g) {
-          int uses = r > s ? (r - 1 - s) / C::ST + 1 : 0;
-          if (s == r % C::ST && g < extra) ++uses;
+          int uses = r > s ? (r - 1 - s) / kStages + 1 : 0;
+          if (s == r % kStages && g < extra) ++uses;
           if (uses > 0 && !mbar_wait(&sh->full[s][g], (uint32_t)((uses - 1) & 1), nullptr))
             atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
         }
@@ -345,20 +412,20 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   } else if (warp == kWarpScore) {
     // -------------------------------------------------------- S^T products
     const bool me = elect_one();
-    const uint32_t idesc = tc::mma_idesc(128, C::NH, 0);
+    const uint32_t idesc = tc::mma_idesc(kTile, C::NH, 0);
     uint64_t c0[kRegions];
 #pragma unroll
     for (int g = 0; g < kRegions; ++g)
-      c0[g] = smem_desc(smem_u32(sC) + C::region(g), 16, C::group(g));
+      c0[g] = smem_desc(smem_u32(sC) + region_at(g), 16, group_bytes(g));
     const uint64_t q0 = smem_desc(smem_u32(sQ), 16, 1024);
     int r = 0;
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
       const LatentItem w = item_at(a, it);
       if (!tc_wait(&sh->qfull, (uint32_t)((it - it0) & 1), abort_flag, a.err, lane)) break;
-      for (int t = w.tb; t < w.te && ok; t += C::T, ++r) {
-        const int st = r % C::ST, b = r & 1;
-        const uint32_t use = (uint32_t)(r / C::ST);
+      for (int t = w.tb; t < w.te && ok; t += kTile, ++r) {
+        const int st = r % kStages, b = r & 1;
+        const uint32_t use = (uint32_t)(r / kStages);
         if (r >= 2 && !tc_wait(&sh->sfree[b], (uint32_t)(((r >> 1) - 1) & 1), abort_flag, a.err, lane)) {
           ok = false;
           break;
@@ -369,7 +436,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           if (ok && !tc_wait(&sh->full[st][g], use & 1u, abort_flag, a.err, lane)) ok = false;
           if (ok && me) {
             tc_fence_after();
-            const uint64_t cs = c0[g] + (uint64_t)(st * (C::kStage >> 4));
+            const uint64_t cs = c0[g] + (uint64_t)(st * (kStage >> 4));
             const uint64_t qs = q0 + (uint64_t)(region_first(g) * (C::kQChunk >> 4));
 #pragma unroll
             for (int i = 0; i < region_chunks(g); ++i)
@@ -384,7 +451,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         if (!ok) break;
         if (me) {
           mma_commit(&sh->sfull[b]);
-          if (t + C::T >= w.te) mma_commit(&sh->qfree);
+          if (t + kTile >= w.te) mma_commit(&sh->qfree);
         }
         __syncwarp();
       }
@@ -401,21 +468,21 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     uint64_t c0[kRegions];   // 64-dim blocks 1 KB apart, 8-token groups a group apart
 #pragma unroll
     for (int g = 0; g < kRegions; ++g)
-      c0[g] = smem_desc(smem_u32(sC) + C::region(g), 1024, C::group(g));
+      c0[g] = smem_desc(smem_u32(sC) + region_at(g), 1024, group_bytes(g));
     const uint64_t p0 = smem_desc(smem_u32(sP), 16, 1024);
     int r = 0;
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
       const LatentItem w = item_at(a, it);
-      for (int t = w.tb; t < w.te; t += C::T, ++r) {
-        const int st = r % C::ST;
+      for (int t = w.tb; t < w.te; t += kTile, ++r) {
+        const int st = r % kStages;
         if (!tc_wait(&sh->pfull, (uint32_t)(r & 1), abort_flag, a.err, lane) ||
             (t == w.tb && it > it0 &&
              !tc_wait(&sh->ofree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane))) {
           ok = false;
           break;
         }
-        const int n = min(C::T, w.te - t);
+        const int n = min(kTile, w.te - t);
         const int nbox = (n + 15) >> 4;
         if (n & 15) {
           // rows past the last token: their P is 0, but 0 x NaN would stay
@@ -423,7 +490,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           for (int i = lane; i < 2 * kPairs * rows * 8; i += 32) {
             const int c = i / (rows * 8), rem = i % (rows * 8), row = n + rem / 8;
             const int g = c >= region_first(0) ? 0 : 1;
-            *reinterpret_cast<uint4*>(sC + st * C::kStage + C::region(g) + (row >> 3) * C::group(g) +
+            *reinterpret_cast<uint4*>(sC + st * kStage + region_at(g) + (row >> 3) * group_bytes(g) +
                                       (c - region_first(g)) * 1024 + (row & 7) * 128 +
                                       (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -434,14 +501,14 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int g = 0; g < kRegions; ++g) {
-            const uint64_t cs = c0[g] + (uint64_t)(st * (C::kStage >> 4));
+            const uint64_t cs = c0[g] + (uint64_t)(st * (kStage >> 4));
 #pragma unroll
             for (int p = 0; p < kRegionPairs; ++p)
 #pragma unroll
-              for (int kk = 0; kk < C::kBoxes; ++kk)
+              for (int kk = 0; kk < kBoxes; ++kk)
                 if (kk < nbox)
                   mma_ss(tmem + C::kColO + C::NH * (region_first(g) / 2 + p),
-                         cs + (uint64_t)(128 * p + kk * (C::group(g) >> 3)),
+                         cs + (uint64_t)(128 * p + kk * (group_bytes(g) >> 3)),
                          p0 + (uint64_t)(128 * kk), idesc, t > w.tb || kk > 0);
             mma_commit(&sh->empty[st][g]);
           }
@@ -457,10 +524,15 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     __syncwarp();
   } else {
     // -------------------------------------------------- softmax + epilogue
-    constexpr int HH = C::HH;
+    constexpr int HH = C::HH, QH = C::QH;
     const int quad = warp & 3, half = warp >> 2;
-    const int row = 32 * quad + lane;                           // token of the tile
+    // scores: this thread's token of the tile and its heads of the half
+    const int row = 16 * quad + (lane & 15), hq = (lane >> 4) * QH;
     const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16);   // this quadrant's lanes
+    // the column that a column-wise reduction leaves here, and whether this
+    // lane speaks for it
+    const int col = hq + (lane & (QH - 1));
+    const bool speaks = (lane & 15) < QH;
     uint32_t xc = 0;                                            // exchanges so far
     int r = 0;
     bool ok = true, waited = false;
@@ -476,54 +548,50 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     };
     for (int it = it0; it < it1 && ok; ++it) {
       const LatentItem w = item_at(a, it);
-      // base[j] (log2 units) of this half's heads, a copy per warp in shared
-      // memory; l: this token lane's sums
-      float l[HH];
-      float sum_base = 0.f;   // of lane's head: base[lane] outside the raise below
-      float* base = sh->base[warp];
+      // l: this token's sums.  base: lane j holds the base (log2 units) of the
+      // half's head j; every warp keeps its own copy
+      float l[QH], base = 0.f;
 #pragma unroll
-      for (int j = 0; j < HH; ++j) l[j] = 0.f;
-      __syncwarp();
-      if (lane < HH) base[lane] = 0.f;
-      __syncwarp();
-      for (int t = w.tb; t < w.te && ok; t += C::T, ++r) {
+      for (int j = 0; j < QH; ++j) l[j] = 0.f;
+      for (int t = w.tb; t < w.te && ok; t += kTile, ++r) {
         const int b = r & 1;
         if (!tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
           ok = false;
           break;
         }
         const bool first = t == w.tb;
-        const bool live = row < min(C::T, w.te - t);
-        float y[HH];   // scores over the base
-        if (quad < C::kQuads) {
-          tc_fence_after();
-          uint32_t sv[HH];
-          tmem_ldn<HH>(tq + C::kColS + C::NH * b + HH * half, sv);
-          tc::tmem_wait_ld();
-          tc_fence_before();
-          float over = -CUDART_INF_F;
-#pragma unroll
-          for (int j = 0; j < HH; j += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(base + j);
-            y[j] = live ? fmaf(__uint_as_float(sv[j]), a.scale_log2, -m.x) : -CUDART_INF_F;
-            y[j + 1] = live ? fmaf(__uint_as_float(sv[j + 1]), a.scale_log2, -m.y) : -CUDART_INF_F;
-            y[j + 2] = live ? fmaf(__uint_as_float(sv[j + 2]), a.scale_log2, -m.z) : -CUDART_INF_F;
-            y[j + 3] = live ? fmaf(__uint_as_float(sv[j + 3]), a.scale_log2, -m.w) : -CUDART_INF_F;
-            over = fmaxf(fmaxf(fmaxf(over, y[j]), fmaxf(y[j + 1], y[j + 2])), y[j + 3]);
-          }
-          const bool want = __any_sync(kFull, over > kRaiseLog2) || first;
-          if (lane == 0) sh->raise[xc & 1u][half][quad] = want ? 1 : 0;
-        }
+        const bool live = row < w.te - t;
+        tc_fence_after();
+        uint32_t sv[QH];
+        tmem_ld_rows16<QH>(tq + C::kColS + C::NH * b + HH * half, sv);
+        tc::tmem_wait_ld();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->sfree[b]);
+        float y[QH];   // scores over the base
+        float over = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < QH; ++j) {
+          const float m = __shfl_sync(kFull, base, hq + j);
+          y[j] = live ? fmaf(__uint_as_float(sv[j]), a.scale_log2, -m) : -CUDART_INF_F;
+          over = fmaxf(over, y[j]);
+        }
+        // the four warps of this half agree whether to raise their bases; an
+        // item's first tile always does, and brings its maxima along
         const int par = (int)(xc & 1u);
+        if (first) {
+          const float top = columns_over_lanes<QH>(y, lane, max_nan);
+          if (speaks) sh->top[par][half][quad][col] = top;
+        } else {
+          const bool want = __any_sync(kFull, over > kRaiseLog2);
+          if (lane == 0) sh->raise[par][half][quad] = want ? 1 : 0;
+        }
         if (!meet()) {
           ok = false;
           break;
         }
-        int up = 0;
-#pragma unroll
-        for (int q = 0; q < C::kQuads; ++q) up |= sh->raise[par][half][q];
+        const bool up = first || (sh->raise[par][half][0] | sh->raise[par][half][1] |
+                                  sh->raise[par][half][2] | sh->raise[par][half][3]) != 0;
         // P of the tile before is read (its buffer is written below, and a
         // raised base rescales O)
         if (r > 0 && !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) {
@@ -531,27 +599,24 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           break;
         }
         if (up) {
-          const int par2 = (int)(xc & 1u);
-          if (quad < C::kQuads) {
-#pragma unroll
-            for (int j = 0; j < HH; ++j) {
-              const int top = __reduce_max_sync(kFull, order_of(y[j]));
-              if (lane == 0) sh->top[par2][half][quad][j] = from_order(top);
+          int at = par;
+          if (!first) {
+            at = (int)(xc & 1u);
+            const float top = columns_over_lanes<QH>(y, lane, max_nan);
+            if (speaks) sh->top[at][half][quad][col] = top;
+            if (!meet()) {
+              ok = false;
+              break;
             }
-          }
-          if (!meet()) {
-            ok = false;
-            break;
           }
           // how far each base rises; it stays finite, so that scores of -inf
           // weigh 0 (not -inf - -inf).  A lane per head, then all read.
+          float rise = 0.f;
           if (lane < HH) {
-            int top = order_of(sh->top[par2][half][0][lane]);
-#pragma unroll
-            for (int q = 1; q < C::kQuads; ++q)
-              top = max(top, order_of(sh->top[par2][half][q][lane]));
-            if (!first) top = max(top, 0);
-            base[lane] = top < order_of(kLowest) ? kLowest : from_order(top);
+            const float top = max_nan(max_nan(sh->top[at][half][0][lane], sh->top[at][half][1][lane]),
+                                      max_nan(sh->top[at][half][2][lane], sh->top[at][half][3][lane]));
+            rise = max_nan(top, first ? kLowest : 0.f);
+            base += rise;
           }
           __syncwarp();
           if (!first) {
@@ -563,64 +628,57 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 #pragma unroll
               for (int c = 0; c < HH; c += kPart) {
                 uint32_t o[kPart];
-                const uint32_t col = tq + C::kColO + C::NH * p + HH * half + c;
-                tmem_ldn<kPart>(col, o);
+                const uint32_t at_o = tq + C::kColO + C::NH * p + HH * half + c;
+                tmem_ldn<kPart>(at_o, o);
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < kPart; ++j)
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) * exp2f(-base[c + j]));
-                tmem_stn<kPart>(col, o);
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) *
+                                         exp2f(-__shfl_sync(kFull, rise, c + j)));
+                tmem_stn<kPart>(at_o, o);
               }
             tc::tmem_wait_st();
           }
 #pragma unroll
-          for (int j = 0; j < HH; ++j) {
-            const float rise = base[j];
-            l[j] = first ? 0.f : l[j] * exp2f(-rise);
-            if (quad < C::kQuads) y[j] -= rise;
+          for (int j = 0; j < QH; ++j) {
+            const float up_j = __shfl_sync(kFull, rise, hq + j);
+            if (!first) l[j] *= exp2f(-up_j);
+            y[j] -= up_j;
           }
-          __syncwarp();
-          if (lane < HH) {
-            sum_base += base[lane];
-            base[lane] = sum_base;
-          }
-          __syncwarp();
         }
-        // weights 2^y; this thread's row of P: 16-byte pieces of 8 heads,
-        // swizzled as the products read them
-        if (quad < C::kQuads) {
-          uint32_t pw[HH / 2];
+        // weights 2^y; this thread's part of a row of P, 16-byte pieces of 8
+        // heads swizzled as the products read them
+        uint32_t pw[QH / 2];
 #pragma unroll
-          for (int j = 0; j < HH; j += 2) {
-            const float p0 = live ? fast_exp2(y[j]) : 0.f;
-            const float p1 = live ? fast_exp2(y[j + 1]) : 0.f;
-            l[j] += p0;
-            l[j + 1] += p1;
-            pw[j / 2] = pack_bf16(p0, p1);
-          }
-          if (row < C::T) {
-#pragma unroll
-            for (int i = 0; i < HH / 8; ++i)
-              *reinterpret_cast<uint4*>(sP + row * 128 + (((half * (HH / 8) + i) ^ (row & 7)) << 4)) =
-                  make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
-          }
-          fence_proxy_async_smem();
+        for (int j = 0; j < QH; j += 2) {
+          const float p0 = live ? fast_exp2(y[j]) : 0.f;
+          const float p1 = live ? fast_exp2(y[j + 1]) : 0.f;
+          l[j] += p0;
+          l[j + 1] += p1;
+          pw[j / 2] = pack_bf16(p0, p1);
         }
+        const int h8 = HH * half + hq;   // the block's head, a multiple of 4
+        uint8_t* prow = sP + row * 128;
+        if constexpr (QH == 4) {
+          *reinterpret_cast<uint2*>(prow + (((h8 >> 3) ^ (row & 7)) << 4) + (h8 & 4) * 2) =
+              make_uint2(pw[0], pw[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < QH / 8; ++i)
+            *reinterpret_cast<uint4*>(prow + ((((h8 >> 3) + i) ^ (row & 7)) << 4)) =
+                make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
+        }
+        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->pfull);
       }
       if (!ok) break;
-      // ---- epilogue: sums over the token lanes in a fixed order
+      // ---- epilogue: sums over the tokens in a fixed order
       const int par = (int)(xc & 1u);
-      if (quad < C::kQuads) {
-#pragma unroll
-        for (int j = 0; j < HH; ++j) {
-          float z = l[j];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-          if (lane == 0) sh->top[par][half][quad][j] = z;
-        }
+      {
+        const float z = columns_over_lanes<QH>(l, lane, [](float x, float y) { return x + y; });
+        if (speaks) sh->top[par][half][quad][col] = z;
       }
       if (!meet() || !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) {
         ok = false;
@@ -632,13 +690,13 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         waited = true;
       }
       const int h0 = C::NH * w.block + HH * half;
+      float inv_mine = 0.f;
       if (lane < HH) {
-        float z = sh->top[par][half][0][lane];
-#pragma unroll
-        for (int q = 1; q < C::kQuads; ++q) z += sh->top[par][half][q][lane];
-        base[lane] = z == 0.f ? 0.f : a.v_scale / z;   // 0: every score -inf, an empty state
+        const float z = (sh->top[par][half][0][lane] + sh->top[par][half][1][lane]) +
+                        (sh->top[par][half][2][lane] + sh->top[par][half][3][lane]);
+        inv_mine = z == 0.f ? 0.f : a.v_scale / z;   // 0: every score -inf, an empty state
         if (quad == 0 && h0 + lane < a.heads) {
-          const float lse = (sum_base + log2f(z)) * kLn2;
+          const float lse = (base + log2f(z)) * kLn2;
           if (w.dst >= 0)
             a.l_part[(int64_t)w.dst * a.heads + h0 + lane] = lse;
           else if (a.lse != nullptr)
@@ -648,13 +706,13 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       __syncwarp();
       float inv[HH];
 #pragma unroll
-      for (int j = 0; j < HH; ++j) inv[j] = base[j];
+      for (int j = 0; j < HH; ++j) inv[j] = __shfl_sync(kFull, inv_mine, j);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         uint32_t o[HH];
         tmem_ldn<HH>(tq + C::kColO + C::NH * p + HH * half, o);
         tc::tmem_wait_ld();
-        const int dim = 128 * p + row;
+        const int dim = 128 * p + 32 * quad + lane;
         if (w.dst >= 0) {
           float* to = a.o_part + ((int64_t)w.dst * a.heads + h0) * kLatentDim + dim;
 #pragma unroll
@@ -684,74 +742,109 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 }
 
 // Merge of split requests: out = sum_i w_i o_i / sum_i w_i, w_i = exp(L_i -
-// max L), over a request's partial states in slot order.  A block takes 128
-// dims of one (request, head): four warps each fold every fourth slot (a
-// lane four dims, so a slot is one 512-byte read) with several slots' loads
-// in flight, then add up in warp order.
-constexpr int kMergeDims = 128;
-__global__ void __launch_bounds__(128) latent_merge_kernel(const __grid_constant__ LatentArgs a) {
-  __shared__ float4 acc_s[4][32];
-  __shared__ float z_s[4];
-  pdl_launch_dependents();
-  if (a.wait_epoch != 0) pdl_wait();   // the schedule came from another stream
-  const int units = a.sched[H_NUNITS];
+// max L), over a request's partial states.  A task is 128 dims of one
+// (request, head); a lane holds four of them, so a slot is one 512-byte read
+// of a warp.  1, 2 or 8 warps share a task, by the longest request's slots
+// (one warp reads a task's few slots in one round trip; a long request's 150
+// would take it twenty): warp w takes slots w, w + warps, ... eight loads at
+// a time, and the warps' sums are added in warp order.
+constexpr int kMergeDims = 128, kMergeWarps = 8;
+template <int kTeam>
+__device__ __forceinline__ void merge_tasks(const LatentArgs& a, int units, float4 (&acc_s)[kMergeWarps][32],
+                                            float (&z_s)[kMergeWarps]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kParts = kLatentDim / kMergeDims;
+  constexpr int kParts = kLatentDim / kMergeDims, kTeams = kMergeWarps / kTeam;
+  const int sub = warp % kTeam;
   const int64_t tasks = (int64_t)units * a.heads * kParts;
-  pdl_wait();   // the partial states belong to the decode kernel
-  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int part = (int)(task % kParts);
-    const int h = (int)(task / kParts % a.heads);
-    const int u = (int)(task / ((int64_t)kParts * a.heads));
-    const int s0 = a.sched[a.off_merge + u], s1 = a.sched[a.off_merge + u + 1];
-    const int req = a.sched[a.off_units + 2 * u];
-    float top = -CUDART_INF_F;
-    for (int s = s0 + lane; s < s1; s += 32)
-      top = fmaxf(top, a.l_part[(int64_t)s * a.heads + h]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    const float base = top == -CUDART_INF_F ? 0.f : top;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTeams; t0 < tasks; t0 += (int64_t)gridDim.x * kTeams) {
+    const int64_t task = t0 + warp / kTeam;
+    const bool on = task < tasks;
+    int part = 0, h = 0, req = 0;
+    float base = 0.f, z = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float z = 0.f;
-#pragma unroll 4
-    for (int s = s0 + warp; s < s1; s += 4) {
-      const float wgt = exp2f((a.l_part[(int64_t)s * a.heads + h] - base) * kLog2e);
-      const float4 o = *reinterpret_cast<const float4*>(
-          a.o_part + ((int64_t)s * a.heads + h) * kLatentDim + kMergeDims * part + 4 * lane);
-      z += wgt;
-      acc.x = fmaf(wgt, o.x, acc.x);
-      acc.y = fmaf(wgt, o.y, acc.y);
-      acc.z = fmaf(wgt, o.z, acc.z);
-      acc.w = fmaf(wgt, o.w, acc.w);
-    }
-    acc_s[warp][lane] = acc;
-    if (lane == 0) z_s[warp] = z;
-    __syncthreads();
-    if (warp == 0) {
-      float4 t = acc_s[0][lane];
-      float zt = z_s[0];
+    if (on) {
+      part = (int)(task % kParts);
+      h = (int)(task / kParts % a.heads);
+      const int u = (int)(task / ((int64_t)kParts * a.heads));
+      const int s0 = a.sched[a.off_merge + u], s1 = a.sched[a.off_merge + u + 1];
+      req = a.sched[a.off_units + 2 * u];
+      const float* lp = a.l_part + h;
+      const float* op = a.o_part + (int64_t)h * kLatentDim + kMergeDims * part + 4 * lane;
+      float top = -CUDART_INF_F;
+      for (int s = s0 + lane; s < s1; s += 32) top = fmaxf(top, lp[(int64_t)s * a.heads]);
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const float4 v = acc_s[w][lane];
-        t.x += v.x;
-        t.y += v.y;
-        t.z += v.z;
-        t.w += v.w;
-        zt += z_s[w];
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      base = top == -CUDART_INF_F ? 0.f : top;
+      constexpr int kAtOnce = 8;
+      for (int s = s0 + sub; s < s1; s += kAtOnce * kTeam) {
+        float4 o[kAtOnce];
+        float lv[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int64_t si = min(s + i * kTeam, s1 - 1);
+          lv[i] = lp[si * a.heads];
+          // volatile: all eight leave before the first is used
+          asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(o[i].x), "=f"(o[i].y), "=f"(o[i].z), "=f"(o[i].w)
+                       : "l"(op + si * a.heads * kLatentDim));
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          if (s + i * kTeam >= s1) break;
+          const float w = exp2f((lv[i] - base) * kLog2e);
+          z += w;
+          acc.x = fmaf(w, o[i].x, acc.x);
+          acc.y = fmaf(w, o[i].y, acc.y);
+          acc.z = fmaf(w, o[i].z, acc.z);
+          acc.w = fmaf(w, o[i].w, acc.w);
+        }
       }
-      const float inv = zt == 0.f ? 0.f : 1.f / zt;
+    }
+    if constexpr (kTeam > 1) {
+      acc_s[warp][lane] = acc;
+      if (lane == 0) z_s[warp] = z;
+      __syncthreads();
+      if (sub == 0) {
+#pragma unroll
+        for (int w = 1; w < kTeam; ++w) {
+          const float4 v = acc_s[warp + w][lane];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+          z += z_s[warp + w];
+        }
+      }
+      __syncthreads();
+    }
+    if (on && sub == 0) {
+      const float inv = z == 0.f ? 0.f : 1.f / z;
       const int64_t qrow = (int64_t)req * a.heads + h;
       *reinterpret_cast<uint2*>(a.out + qrow * kLatentDim + kMergeDims * part + 4 * lane) =
-          make_uint2(pack_bf16(t.x * inv, t.y * inv), pack_bf16(t.z * inv, t.w * inv));
-      if (part == 0 && lane == 0 && a.lse != nullptr) a.lse[qrow] = base + log2f(zt) * kLn2;
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      if (part == 0 && lane == 0 && a.lse != nullptr) a.lse[qrow] = base + log2f(z) * kLn2;
     }
-    __syncthreads();
   }
 }
 
-using Shape16 = LatentShape<16, 64, 2>;
-using Shape32 = LatentShape<32, 64, 2>;
-using Shape64 = LatentShape<64, 64, 2>;
+__global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const __grid_constant__ LatentArgs a) {
+  __shared__ float4 acc_s[kMergeWarps][32];
+  __shared__ float z_s[kMergeWarps];
+  pdl_launch_dependents();
+  if (a.wait_epoch != 0) pdl_wait();   // the schedule came from another stream
+  const int units = a.sched[H_NUNITS], most = a.sched[H_MAXCHUNKS];
+  pdl_wait();   // the partial states belong to the decode kernel
+  if (most <= 8)
+    merge_tasks<1>(a, units, acc_s, z_s);
+  else if (most <= 32)
+    merge_tasks<2>(a, units, acc_s, z_s);
+  else
+    merge_tasks<8>(a, units, acc_s, z_s);
+}
+
+using Shape16 = LatentShape<16>;
+using Shape32 = LatentShape<32>;
+using Shape64 = LatentShape<64>;
 static_assert(latent_smem<Shape16>() <= 227 * 1024 && latent_smem<Shape32>() <= 227 * 1024 &&
                   latent_smem<Shape64>() <= 227 * 1024,
               "dynamic shared memory of one CTA");
@@ -852,7 +945,7 @@ cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool me
     return e;
   if (!merge) return cudaSuccess;
   cfg.gridDim = dim3(merge_grid);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&latent_merge_kernel), args);
 }

@@ -32,7 +32,7 @@ constexpr int kMergeThreads = 256;
 // Latent contexts: an item's fixed cost (its queries, its epilogue and its
 // partial state of 64 heads x 512 dims) in tokens, and the split floor.
 constexpr int kLatentAlpha = 128;
-constexpr int kLatentMinChunk = 256;
+constexpr int kLatentMinChunk = 128;
 
 // Schedule header words (first 32 int32 of the workspace; 19..31 are 0).
 enum HeaderWord {
@@ -293,6 +293,10 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
                           const int32_t* group_indptr, int32_t n_rows, const int32_t* indptr,
                           const int32_t* indices, const int32_t* last, int32_t* words,
                           pkd_plan_info* info);
+// Plans of latent contexts (PKD_FLAG_LATENT); plan_schedule(_grouped) calls it.
+int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
+                         const int32_t* indptr, const int32_t* indices, const int32_t* last,
+                         int32_t batch, int32_t* words, pkd_plan_info* info);
 // Which format a shared-prefix step should take (pkd_advise_format).
 int advise_format(const pkd_config& cfg, int32_t n_cta, const int32_t* group_indptr,
                   int32_t n_groups, const int32_t* p_indptr, const int32_t* p_last,

@@ -211,15 +211,17 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
                           const int32_t* group_indptr, int32_t n_rows, const int32_t* indptr,
                           const int32_t* indices, const int32_t* last, int32_t* words,
                           pkd_plan_info* info) {
+  if (cfg.flags & PKD_FLAG_LATENT)
+    return group_indptr ? PKD_E_INVALID_ARG
+                        : plan_schedule_latent(cfg, n_cta, L, indptr, indices, last, n_rows, words,
+                                               info);
   // n_rows: table rows (= requests without grouping, = groups with it)
   if (n_rows < 0 || n_cta < 1 || words == nullptr) return PKD_E_INVALID_ARG;
   if (n_rows > 0 && (indptr == nullptr || last == nullptr)) return PKD_E_INVALID_ARG;
   const int64_t P = cfg.page_size;
   const int32_t group = cfg.num_qo_heads / cfg.num_kv_heads;
   const int32_t rows = group_indptr ? block_rows(cfg) : 1;
-  const bool latent = (cfg.flags & PKD_FLAG_LATENT) != 0;
-  const int32_t heads = latent ? latent_blocks(cfg.num_qo_heads)
-                        : (group_indptr && (cfg.flags & PKD_FLAG_DENSE_PREFIX))
+  const int32_t heads = (group_indptr && (cfg.flags & PKD_FLAG_DENSE_PREFIX))
                             ? cfg.num_kv_heads : 1;   // units per block
   (void)group;
 
@@ -285,9 +287,8 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   for (int64_t l : ulens) total += l;
 
   // ---- P1 + P2 + P3: chunk candidates, split, LPT; keep the best
-  const int64_t alpha = cfg.alpha >= 0 ? cfg.alpha : latent ? kLatentAlpha : kDefaultAlpha;
-  const int64_t min_chunk = cfg.min_chunk_tokens >= 0 ? cfg.min_chunk_tokens
-                            : latent ? kLatentMinChunk : kDefaultMinChunk;
+  const int64_t alpha = cfg.alpha < 0 ? kDefaultAlpha : cfg.alpha;
+  const int64_t min_chunk = cfg.min_chunk_tokens < 0 ? kDefaultMinChunk : cfg.min_chunk_tokens;
   const int64_t floor_c = ceil_div(std::max<int64_t>(min_chunk, 1), P) * P;
   const int64_t work_bound = ceil_div(total, n_cta);
   std::vector<int64_t>& cands = sc.cands;
@@ -385,7 +386,7 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     w[4] = (int32_t)(indptr[bk.table_row] + it.tok_begin / P);  // index of the first page
     w[5] = bk.n_req;
     w[6] = first_slot[b] >= 0 ? n_chunks[b] : 0;     // slot stride per request
-    w[7] = it.req % heads;   // KV head (dense prefix), block of heads (latent), else 0
+    w[7] = it.req % heads;                           // KV head (dense prefix), else 0
   }
   int32_t* unit_words = words + L.units;
   int32_t* merge_indptr = words + L.merge_indptr;
@@ -431,6 +432,192 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     for (int64_t l : lens) tokens += l;
     info->total_tokens = tokens;
     info->makespan = best_span;
+    info->nnz = (int32_t)nnz;
+    info->schedule_words = (int32_t)(L.page_list + nnz);
+  }
+  return PKD_OK;
+}
+
+// ---------------------------------------------------------------- latent
+//
+// Plans of latent contexts.  Their kernel's time is its tokens (about 27 ns
+// each) plus a fixed cost per item, whatever the heads, and every request has
+// items for each block of heads.  So the tokens of all requests are laid end
+// to end and cut into as many equal stretches as there are CTAs (CTA pairs
+// when a request has two blocks of heads: both walk the same tokens at the
+// same time, and the second read of a row hits in L2): a CTA's queue is the
+// requests, or parts of them, that its stretch covers.  At most one cut per
+// CTA, so at most batch + N_CTA items, and loads equal within a page; equal
+// chunks per request (plan_schedule_grouped) left CTAs idle for up to a
+// quarter of the time (32 requests of 4,096 tokens).  A cut leaves at least
+// the split floor on both sides where it can; the stretch is the shortest of
+// a few per cent steps that fits.
+namespace {
+
+struct LatentPart {
+  int32_t req, tok_begin, tok_end, cta;   // cta: of the first block of heads
+};
+
+// Cut the requests into stretches of cost `span` for nv CTAs; false when they
+// do not fit.
+bool cut_even(const std::vector<int64_t>& lens, int64_t span, int64_t alpha, int64_t P,
+              int64_t floor_c, int32_t nv, std::vector<LatentPart>* parts) {
+  parts->clear();
+  int32_t v = 0;
+  int64_t cap = span;
+  for (size_t i = 0; i < lens.size(); ++i) {
+    int64_t pos = 0;
+    while (pos < lens[i]) {
+      if (v >= nv) return false;
+      const int64_t rem = lens[i] - pos;
+      int64_t take = 0;
+      if (rem + alpha <= cap) {
+        take = rem;
+      } else if (cap == span) {   // an empty CTA: as much as fits, but no short rest
+        take = (span - alpha) / P * P;
+        if (rem - take < floor_c) take = std::min(take, ceil_div(ceil_div(rem, 2), P) * P);
+      } else {
+        take = std::min((cap - alpha) / P * P, (rem - floor_c) / P * P);
+        if (take < floor_c) take = 0;
+      }
+      if (take > 0) parts->push_back(LatentPart{(int32_t)i, (int32_t)pos, (int32_t)(pos + take), v});
+      pos += take;
+      cap -= take + alpha;
+      if (pos < lens[i]) {   // this CTA is full
+        ++v;
+        cap = span;
+      }
+    }
+  }
+  return true;
+}
+
+}  // namespace
+
+int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
+                         const int32_t* indptr, const int32_t* indices, const int32_t* last,
+                         int32_t batch, int32_t* words, pkd_plan_info* info) {
+  if (batch < 0 || n_cta < 1 || words == nullptr) return PKD_E_INVALID_ARG;
+  if (batch > 0 && (indptr == nullptr || last == nullptr)) return PKD_E_INVALID_ARG;
+  if (batch > cfg.max_batch) return PKD_E_CAPACITY;
+  const int64_t P = cfg.page_size;
+  thread_local std::vector<int64_t> lens;
+  thread_local std::vector<LatentPart> parts;
+  thread_local std::vector<int32_t> first_slot, n_chunks, order;
+  lens.resize((size_t)batch);
+  int64_t nnz = 0, total = 0;
+  if (batch > 0) {
+    if (indptr[0] != 0) return PKD_E_BAD_TABLE;
+    for (int32_t i = 0; i < batch; ++i) {
+      const int64_t n = (int64_t)indptr[i + 1] - indptr[i];
+      if (n < 1 || last[i] < 1 || last[i] > P) return PKD_E_BAD_TABLE;
+      lens[i] = P * (n - 1) + last[i];
+      if (lens[i] > 0x7fffffffLL) return PKD_E_CAPACITY;
+      total += lens[i];
+    }
+    nnz = indptr[batch];
+    if (nnz > cfg.max_num_pages) return PKD_E_CAPACITY;
+    if (indices == nullptr) return PKD_E_INVALID_ARG;
+    if (!copy_checked(indices, words + L.page_list, nnz, cfg.num_pages)) return PKD_E_BAD_TABLE;
+    for (int32_t i = 0; i < batch; ++i) words[L.page_list + nnz + i] = (int32_t)lens[i];
+  }
+  const int32_t blocks = latent_blocks(cfg.num_qo_heads);
+  const int32_t nv = std::max(1, n_cta / blocks);
+  const int64_t alpha = cfg.alpha < 0 ? kLatentAlpha : cfg.alpha;
+  const int64_t min_chunk = cfg.min_chunk_tokens < 0 ? kLatentMinChunk : cfg.min_chunk_tokens;
+  const int64_t floor_c = ceil_div(std::max<int64_t>(min_chunk, 1), P) * P;
+  int64_t span = std::max(alpha + floor_c, ceil_div(total + alpha * batch, nv));
+  while (!cut_even(lens, span, alpha, P, floor_c, nv, &parts)) span += std::max<int64_t>(P, span / 64);
+
+  // reduction map: a request in several parts is a unit with a slot per part
+  // (all its blocks of heads share it); most parts first, as elsewhere
+  n_chunks.assign((size_t)batch, 0);
+  first_slot.assign((size_t)batch, -1);
+  for (const LatentPart& p : parts) ++n_chunks[p.req];
+  order.clear();
+  for (int32_t i = 0; i < batch; ++i)
+    if (n_chunks[i] > 1) order.push_back(i);
+  std::stable_sort(order.begin(), order.end(),
+                   [&](int32_t x, int32_t y) { return n_chunks[x] > n_chunks[y]; });
+  const int64_t n_items = (int64_t)parts.size() * blocks;
+  int64_t n_slots = 0;
+  int32_t* unit_words = words + L.units;
+  int32_t* merge_indptr = words + L.merge_indptr;
+  for (int32_t i : order) n_slots += n_chunks[i];
+  if (n_items > L.max_items || n_slots > L.max_slots) return PKD_E_CAPACITY;
+  merge_indptr[0] = 0;
+  for (size_t u = 0; u < order.size(); ++u) {
+    const int32_t i = order[u];
+    first_slot[i] = merge_indptr[u];
+    unit_words[2 * u] = i;
+    unit_words[2 * u + 1] = n_chunks[i];
+    merge_indptr[u + 1] = merge_indptr[u] + n_chunks[i];
+  }
+
+  // queues: the parts of virtual CTA v, once per block of heads, on CTAs
+  // v * blocks + block (all on one CTA when there are fewer CTAs than blocks)
+  int32_t* cta_indptr = words + L.cta_indptr;
+  int32_t* item_words = words + L.items;
+  int64_t at = 0, p0 = 0;
+  int32_t cta = 0;
+  cta_indptr[0] = 0;
+  while (p0 < (int64_t)parts.size()) {
+    int64_t p1 = p0;
+    while (p1 < (int64_t)parts.size() && parts[p1].cta == parts[p0].cta) ++p1;
+    const int32_t v = parts[p0].cta;
+    for (int32_t b = 0; b < blocks; ++b) {
+      const int32_t c = n_cta >= blocks ? v * blocks + b : 0;
+      while (cta < c) cta_indptr[++cta] = (int32_t)at;
+      for (int64_t k = p0; k < p1; ++k, ++at) {
+        const LatentPart& p = parts[k];
+        int32_t* w = item_words + at * kItemWords;
+        int32_t chunk = 0;   // parts of one request follow one another
+        for (int64_t q = k; q > 0 && parts[q - 1].req == p.req; --q) ++chunk;
+        w[0] = p.req;
+        w[1] = p.tok_begin;
+        w[2] = p.tok_end;
+        w[3] = first_slot[p.req] >= 0 ? first_slot[p.req] + chunk : -1;
+        w[4] = (int32_t)(indptr[p.req] + p.tok_begin / P);
+        w[5] = 1;
+        w[6] = first_slot[p.req] >= 0 ? n_chunks[p.req] : 0;
+        w[7] = b;
+      }
+    }
+    p0 = p1;
+  }
+  while (cta < n_cta) cta_indptr[++cta] = (int32_t)at;
+
+  int32_t* h = words;
+  std::memset(h, 0, sizeof(int32_t) * H_WORDS);
+  h[H_MAGIC] = kMagic;
+  h[H_BATCH] = batch;
+  h[H_HQ] = cfg.num_qo_heads;
+  h[H_HKV] = cfg.num_kv_heads;
+  h[H_D] = cfg.head_dim;
+  h[H_P] = cfg.page_size;
+  h[H_NCTA] = n_cta;
+  h[H_NITEMS] = (int32_t)n_items;
+  h[H_NUNITS] = (int32_t)order.size();
+  h[H_NSLOTS] = (int32_t)n_slots;
+  h[H_CHUNK] = (int32_t)std::min<int64_t>(span - alpha, 0x7fffffff);
+  h[H_ALPHA] = (int32_t)alpha;
+  h[H_NNZ] = (int32_t)nnz;
+  h[H_MAKESPAN] = (int32_t)std::min<int64_t>(span, 0x7fffffff);
+  h[H_MINCHUNK] = (int32_t)floor_c;
+  h[H_BLOCK] = 1;
+  h[H_MAXCHUNKS] = order.empty() ? 0 : n_chunks[order[0]];
+  h[H_MAXBATCH] = cfg.max_batch;
+  h[H_MAXPAGES] = cfg.max_num_pages;
+  if (info) {
+    *info = pkd_plan_info{};
+    info->batch = batch;
+    info->num_ctas = n_cta;
+    info->chunk_tokens = h[H_CHUNK];
+    info->num_items = (int32_t)n_items;
+    info->num_units = (int32_t)order.size();
+    info->num_slots = (int32_t)n_slots;
+    info->total_tokens = total;
+    info->makespan = span;
     info->nnz = (int32_t)nnz;
     info->schedule_words = (int32_t)(L.page_list + nnz);
   }

@@ -7,7 +7,7 @@ import torch
 
 import paged_kv_decode_host_gb300 as pkd
 
-pytestmark = pytest.mark.gpu
+gpu = pytest.mark.gpu
 ROW, DIM = 576, 512
 SCALE = 1.0 / math.sqrt(192.0)
 
@@ -58,6 +58,7 @@ def close(got, ref, top):
     assert (lse.double() - rl).abs().max() <= 2e-4
 
 
+@gpu
 @pytest.mark.parametrize("heads", [1, 5, 16, 17, 32, 33, 64, 65, 128])
 @pytest.mark.parametrize("page", [16, 64])
 def test_heads_and_lengths(heads, page):
@@ -69,8 +70,9 @@ def test_heads_and_lengths(heads, page):
     assert dec.device_error() == 0
 
 
+@gpu
 @pytest.mark.parametrize("heads", [16, 32, 64, 128])
-@pytest.mark.parametrize("kw", [dict(), dict(num_ctas=3), dict(chunk_rule="search")])
+@pytest.mark.parametrize("kw", [dict(), dict(num_ctas=3), dict(num_ctas=1)])
 def test_split_requests(heads, kw):
     lens = [9001, 3, 1500]
     t, q, cache, dec = make(heads, lens, 16, seed=1, **kw)
@@ -82,6 +84,7 @@ def test_split_requests(heads, kw):
     assert dec.device_error() == 0
 
 
+@gpu
 def test_rising_scores_rescale():
     """Scores that grow along the sequence raise the softmax base in every tile."""
     lens = [1000]
@@ -97,6 +100,7 @@ def test_rising_scores_rescale():
     close((out, lse), reference(q, cache, lens, t, 16), cache.abs().max().double())
 
 
+@gpu
 def test_stale_slots_are_not_read():
     """NaN and infinities behind the last token, and in pages of the pool that are not the request's."""
     lens = [5, 130, 64]
@@ -113,6 +117,7 @@ def test_stale_slots_are_not_read():
     close((out, lse), ref, cache.abs().max().double())
 
 
+@gpu
 def test_infinite_scores_in_one_place():
     """A score of -inf weighs nothing; a head whose scores are all -inf is an empty state."""
     lens = [40]
@@ -130,6 +135,7 @@ def test_infinite_scores_in_one_place():
     assert (out == 0).all() and (lse == -float("inf")).all()
 
 
+@gpu
 def test_v_scale_and_no_lse():
     lens = [77, 200]
     t, q, cache, dec = make(20, lens, 16, seed=5)
@@ -138,6 +144,7 @@ def test_v_scale_and_no_lse():
     assert torch.equal(out, dec.run(q, cache)[0])
 
 
+@gpu
 def test_append_then_decode_in_a_graph():
     """Two steps of a serving loop: append, plan, replayed decode, against the formulas."""
     page, lens, heads = 16, [31, 64, 1], 16
@@ -173,6 +180,7 @@ def test_append_then_decode_in_a_graph():
         close((out, lse), ref, cache.abs().max().double())
 
 
+@gpu
 def test_append_skips_and_flags():
     page = 16
     t = table([20, 5], page)
@@ -189,6 +197,7 @@ def test_append_skips_and_flags():
     pkd.append_latent(new[:0, :512], new[:0, 512:], rows[:0], at[:0], *d, cache)
 
 
+@gpu
 def test_other_stream_and_refusals():
     lens = [100]
     t, q, cache, dec = make(16, lens, 16, seed=8)
@@ -217,3 +226,36 @@ def test_other_stream_and_refusals():
     with pytest.raises(ValueError):
         pkd.append_latent(q[0, :, :512].t(), q[0, :, 512:], *[torch.zeros(16, device="cuda").int()] * 4,
                           torch.zeros(15, device="cuda").int(), cache)
+
+
+@pytest.mark.parametrize("heads", [16, 64, 128])
+@pytest.mark.parametrize("lens", [[1], [517], [4096] * 32, [100_000] + [300] * 8, list(range(1, 200)),
+                                  [], [129, 128, 127, 255, 256, 257] * 7])
+@pytest.mark.parametrize("n_cta,page", [(152, 16), (152, 64), (7, 16), (1, 16), (2, 128)])
+def test_plan_covers_every_token_once(heads, lens, n_cta, page):
+    """Host only: every (request, token, block of heads) in one item, slots as the reduction map
+    has them, and no CTA's cost above the plan's."""
+    t = table(lens, page) if lens else (np.zeros(1, np.int32), np.zeros(0, np.int32), np.zeros(0, np.int32), 1)
+    cfg = pkd.make_config(heads, 1, DIM, page, max(1, len(lens)), max(1, len(t[1])), max(1, t[3]),
+                          num_ctas=n_cta, flags=pkd.FLAG_LATENT)
+    words, info, off = pkd.plan_host(cfg, *t[:3])
+    s = pkd.decode_schedule(words, off, info)
+    blocks = -(-heads // 64)
+    seen = {}
+    for (req, tb, te, dst, page0, n_req, stride), b in zip(s["items"], s["heads"]):
+        assert n_req == 1 and 0 <= b < blocks and tb % page == 0 and te > tb
+        assert page0 == t[0][req] + tb // page
+        seen.setdefault((req, b), []).append((tb, te, dst))
+    slots = {req: list(range(s["merge_indptr"][u], s["merge_indptr"][u + 1]))
+             for u, (req, _) in enumerate(s["units"])}
+    for i, n in enumerate(lens):
+        for b in range(blocks):
+            parts = sorted(seen.pop((i, b)))
+            assert [p[0] for p in parts] == [0] + [p[1] for p in parts[:-1]] and parts[-1][1] == n
+            assert [p[2] for p in parts] == (slots[i] if len(parts) > 1 else [-1])
+    assert not seen and info["num_slots"] == sum(len(x) for x in slots.values())
+    cost = [sum(128 + te - tb for _, tb, te, *_ in s["items"][a:z])
+            for a, z in zip(s["cta_indptr"], s["cta_indptr"][1:])]
+    assert max(cost, default=0) <= info["makespan"] * (blocks if n_cta < blocks else 1)
+    even = (sum(lens) + 128 * len(lens)) / max(1, n_cta // blocks)
+    assert info["makespan"] <= max(1.35 * even, even + 2 * (256 + page)) + 256
