@@ -350,6 +350,8 @@ def _fast():
                    ctypes.cast(lib.pkd_plan_shared, ctypes.c_void_p).value,
                    ctypes.cast(lib.pkd_plan_cascade, ctypes.c_void_p).value,
                    ctypes.cast(lib.pkd_run_scaled, ctypes.c_void_p).value)
+            m.init_ops(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.pkd_accumulate_weights, lib.pkd_append_latent, lib.pkd_evict_kv)])
             _fast_plan = m
         except ImportError:
             _fast_plan = False
@@ -747,11 +749,13 @@ class BatchDecodeWithPagedKVCache:
                     or t.get_device() != dev:
                 raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)} on "
                                  f"{q.device}")
-        ptr = lambda t: t.data_ptr() if t is not None else 0
+        fast = _fast()
         with _On(dev):
-            st = self._lib.pkd_accumulate_weights(
-                self._h, q.data_ptr(), kv_cache.data_ptr(), lse.data_ptr(), weights.data_ptr(),
-                ptr(positions), ptr(new_tokens), ptr(seen), k_scale, expect_epoch,
+            st = (self._lib.pkd_accumulate_weights if fast is None else fast.accumulate)(
+                self._hv, q.data_ptr(), kv_cache.data_ptr(), lse.data_ptr(), weights.data_ptr(),
+                positions.data_ptr() if positions is not None else 0,
+                new_tokens.data_ptr() if new_tokens is not None else 0,
+                seen.data_ptr() if seen is not None else 0, k_scale, expect_epoch,
                 _stream_ptr(stream))
         if st:
             _check(st, "pkd_accumulate_weights")
@@ -880,9 +884,9 @@ class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
         if self.batch is None:
             raise PkdError(-5, "run before plan")
         if out is None:
-            out = q.new_empty((q.shape[0], self.hq, self.d), dtype=torch.bfloat16)
+            out = torch.empty((q.shape[0], self.hq, self.d), dtype=torch.bfloat16, device=q.device)
         if lse is None and return_lse:
-            lse = q.new_empty((q.shape[0], self.hq), dtype=torch.float32)
+            lse = torch.empty((q.shape[0], self.hq), dtype=torch.float32, device=q.device)
         self._check_run_args(q, cache, out, lse)
         fast, lp = _fast(), lse.data_ptr() if lse is not None else 0
         with _On(q.get_device()):
@@ -1092,8 +1096,9 @@ def append_latent(latent_new, rope_new, batch_indices, positions, indptr, indice
     if positions.numel() != n:
         raise ValueError("batch_indices and positions need one entry per new token")
     batch = _table_args(dev, indptr, indices, last_page_len)
+    fast = _fast()
     with _On(dev):
-        st = load().pkd_append_latent(
+        st = (load().pkd_append_latent if fast is None else fast.append_latent)(
             latent_new.data_ptr(), strides[0], rope_new.data_ptr(), strides[1],
             batch_indices.data_ptr(), positions.data_ptr(), n, indptr.data_ptr(),
             indices.data_ptr(), last_page_len.data_ptr(), batch, cache.data_ptr(),
@@ -1149,22 +1154,28 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
                 raise ValueError(f"{name}[{l}] must be a contiguous {dt} tensor {list(size)} on "
                                  f"cuda:{dev}")
     batch = _table_args(dev, indptr, indices, last_page_len, seen=seen)
-    ptrs = ctypes.c_void_p * layers
     per_head = 1 if per_head else 0
-    lib = load()
+    for name, v in (("max_len", max_len), ("budget", budget), ("sinks", sinks), ("recent", recent)):
+        if not -2**31 <= v < 2**31:
+            raise OverflowError(f"{name} must fit 32 bits")
+    lib, fast = load(), _fast()
     with _On(dev):
-        # raises for sizes out of range only in the call itself
-        need = lib.pkd_evict_workspace_bytes(layers, batch, max_len, budget, per_head, hkv)
+        # (sizes out of range: 0 here, refused in the call itself)
+        need = 0 if max_len <= budget else lib.pkd_evict_workspace_bytes(
+            layers, batch, max_len, budget, per_head, hkv)
         ws = torch.empty(need, dtype=torch.uint8, device=c0.device) if need else None
         if need and stream is not None:
             ws.record_stream(stream)
-        st = lib.pkd_evict_kv(
-            layers, ptrs(*[t.data_ptr() for t in kv_caches]),
-            ptrs(*[t.data_ptr() for t in weights]), ptrs(*[t.data_ptr() for t in positions]),
-            indptr.data_ptr(), indices.data_ptr(), last_page_len.data_ptr(), seen.data_ptr(), batch,
-            max_len, budget, sinks, recent, per_head, pages, P, hkv, D,
-            (FLAG_HND if kv_layout == "HND" else 0) | (FLAG_KV_FP8 if fp8 else 0),
-            ws.data_ptr() if need else 0, need, _err_arg(err, dev), _stream_ptr(stream))
+        args = [[t.data_ptr() for t in ts] for ts in (kv_caches, weights, positions)]
+        rest = (indptr.data_ptr(), indices.data_ptr(), last_page_len.data_ptr(), seen.data_ptr(),
+                batch, max_len, budget, sinks, recent, per_head, pages, P, hkv, D,
+                (FLAG_HND if kv_layout == "HND" else 0) | (FLAG_KV_FP8 if fp8 else 0),
+                ws.data_ptr() if need else 0, need, _err_arg(err, dev), _stream_ptr(stream))
+        if fast is not None:
+            st = fast.evict(*args, *rest)
+        else:
+            ptrs = ctypes.c_void_p * layers
+            st = lib.pkd_evict_kv(layers, *[ptrs(*a) for a in args], *rest)
     if st:
         _check(st, "pkd_evict_kv")
 

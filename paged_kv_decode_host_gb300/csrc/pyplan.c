@@ -11,6 +11,11 @@
  *              stream) -> (status, epoch)
  * run(ctx, q, kv, out, lse, k_scale, v_scale, expect_epoch, stream) -> status
  *
+ * accumulate, append_latent, evict: pkd_accumulate_weights, pkd_append_latent and
+ * pkd_evict_kv with their addresses as integers (evict: one sequence of them per
+ * layer array), after init_ops; an integer that does not fit its C type raises
+ * OverflowError.
+ *
  * status is the C ABI's return value, or NOT_HANDLED (1000) when an argument
  * is not a 1-D C-contiguous int32 buffer: the caller then takes its general
  * path, which converts or rejects the input with a proper message. */
@@ -181,7 +186,112 @@ static PyObject *plan_cascade(PyObject *self, PyObject *args) {
   return Py_BuildValue("iK", st, (unsigned long long)epoch);
 }
 
+typedef int (*accumulate_fn)(void *ctx, const void *q, const void *kv, const float *lse,
+                             float *weights, int32_t *positions, const int32_t *new_tokens,
+                             const int32_t *seen, float k_scale, uint64_t expect_epoch,
+                             void *stream);
+typedef int (*append_latent_fn)(const void *latent, int64_t latent_stride, const void *rope,
+                                int64_t rope_stride, const int32_t *batch_indices,
+                                const int32_t *positions, int32_t n, const int32_t *indptr,
+                                const int32_t *indices, const int32_t *last, int32_t batch,
+                                void *cache, int32_t num_pages, int32_t page_size, int32_t *err,
+                                void *stream);
+typedef int (*evict_fn)(int32_t layers, void *const *kv, float *const *weights,
+                        int32_t *const *positions, const int32_t *indptr, const int32_t *indices,
+                        const int32_t *last, const int32_t *seen, int32_t batch, int32_t max_len,
+                        int32_t budget, int32_t sinks, int32_t recent, int32_t per_head,
+                        int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                        int32_t head_dim, uint32_t flags, void *workspace, size_t workspace_bytes,
+                        int32_t *err, void *stream);
+static accumulate_fn g_accumulate = NULL;
+static append_latent_fn g_append_latent = NULL;
+static evict_fn g_evict = NULL;
+
+static PyObject *init_ops(PyObject *self, PyObject *args) {
+  unsigned long long a, b, c;
+  (void)self;
+  if (!PyArg_ParseTuple(args, "KKK", &a, &b, &c)) return NULL;
+  g_accumulate = (accumulate_fn)(uintptr_t)a;
+  g_append_latent = (append_latent_fn)(uintptr_t)b;
+  g_evict = (evict_fn)(uintptr_t)c;
+  Py_RETURN_NONE;
+}
+
+#define ADDR(x) ((void *)(uintptr_t)(x))
+
+static PyObject *accumulate(PyObject *self, PyObject *args) {
+  unsigned long long ctx, q, kv, lse, w, pos, nt, seen, epoch, stream;
+  float ks;
+  (void)self;
+  if (!PyArg_ParseTuple(args, "KKKKKKKKfKK", &ctx, &q, &kv, &lse, &w, &pos, &nt, &seen, &ks, &epoch,
+                        &stream))
+    return NULL;
+  if (g_accumulate == NULL) return PyLong_FromLong(NOT_HANDLED);
+  return PyLong_FromLong(g_accumulate(ADDR(ctx), ADDR(q), ADDR(kv), (const float *)ADDR(lse),
+                                      (float *)ADDR(w), (int32_t *)ADDR(pos),
+                                      (const int32_t *)ADDR(nt), (const int32_t *)ADDR(seen), ks,
+                                      (uint64_t)epoch, ADDR(stream)));
+}
+
+static PyObject *append_latent(PyObject *self, PyObject *args) {
+  unsigned long long lat, rope, bi, pos, ip, ix, la, cache, err, stream;
+  long long ls, rs;
+  int n, batch, pages, page;
+  (void)self;
+  if (!PyArg_ParseTuple(args, "KLKLKKiKKKiKiiKK", &lat, &ls, &rope, &rs, &bi, &pos, &n, &ip, &ix,
+                        &la, &batch, &cache, &pages, &page, &err, &stream))
+    return NULL;
+  if (g_append_latent == NULL) return PyLong_FromLong(NOT_HANDLED);
+  return PyLong_FromLong(g_append_latent(
+      ADDR(lat), (int64_t)ls, ADDR(rope), (int64_t)rs, (const int32_t *)ADDR(bi),
+      (const int32_t *)ADDR(pos), n, (const int32_t *)ADDR(ip), (const int32_t *)ADDR(ix),
+      (const int32_t *)ADDR(la), batch, ADDR(cache), pages, page, (int32_t *)ADDR(err),
+      ADDR(stream)));
+}
+
+#define MAX_LAYERS 128
+/* n addresses of a sequence into out; 0 when it is not a list of n integers */
+static int addresses(PyObject *list, Py_ssize_t n, void **out) {
+  if (!PyList_Check(list) || PyList_GET_SIZE(list) != n) return 0;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const unsigned long long v = PyLong_AsUnsignedLongLong(PyList_GET_ITEM(list, i));
+    if (v == (unsigned long long)-1 && PyErr_Occurred()) {
+      PyErr_Clear();
+      return 0;
+    }
+    out[i] = ADDR(v);
+  }
+  return 1;
+}
+
+static PyObject *evict(PyObject *self, PyObject *args) {
+  PyObject *kv, *w, *p;
+  unsigned long long ip, ix, la, seen, ws, err, stream, ws_bytes;
+  int batch, max_len, budget, sinks, recent, per_head, pages, page, hkv, dim;
+  unsigned int flags;
+  void *kvs[MAX_LAYERS], *ws_[MAX_LAYERS], *ps[MAX_LAYERS];
+  (void)self;
+  if (!PyArg_ParseTuple(args, "OOOKKKKiiiiiiiiiiIKKKK", &kv, &w, &p, &ip, &ix, &la, &seen, &batch,
+                        &max_len, &budget, &sinks, &recent, &per_head, &pages, &page, &hkv, &dim,
+                        &flags, &ws, &ws_bytes, &err, &stream))
+    return NULL;
+  const Py_ssize_t layers = PyList_Check(kv) ? PyList_GET_SIZE(kv) : 0;
+  if (g_evict == NULL || layers < 1 || layers > MAX_LAYERS || !addresses(kv, layers, kvs) ||
+      !addresses(w, layers, ws_) || !addresses(p, layers, ps))
+    return PyLong_FromLong(NOT_HANDLED);
+  return PyLong_FromLong(g_evict(
+      (int32_t)layers, kvs, (float *const *)ws_, (int32_t *const *)ps, (const int32_t *)ADDR(ip),
+      (const int32_t *)ADDR(ix), (const int32_t *)ADDR(la), (const int32_t *)ADDR(seen), batch,
+      max_len, budget, sinks, recent, per_head, pages, page, hkv, dim, (uint32_t)flags, ADDR(ws),
+      (size_t)ws_bytes, (int32_t *)ADDR(err), ADDR(stream)));
+}
+
 static PyMethodDef methods[] = {
+    {"init_ops", init_ops, METH_VARARGS,
+     "init_ops(accumulate_weights_address, append_latent_address, evict_address)"},
+    {"accumulate", accumulate, METH_VARARGS, "pkd_accumulate_weights -> status"},
+    {"append_latent", append_latent, METH_VARARGS, "pkd_append_latent -> status"},
+    {"evict", evict, METH_VARARGS, "pkd_evict_kv (lists of addresses per layer) -> status"},
     {"plan_cascade", plan_cascade, METH_VARARGS,
      "plan_cascade(ctx, group_indptr, p_indptr, p_indices, p_last, s_indptr, s_indices, "
      "s_last, stream) -> (status, epoch)"},
