@@ -37,8 +37,9 @@
 //    is, across lanes and warps, so they are not formed per tile: every tile
 //    is only compared with the running base, and the exact maxima are taken
 //    when some score exceeds its head's base by more than 2^8 (always in an
-//    item's first tile).  P is written as bf16 (rounded to nearest; the sums
-//    that divide it are kept unrounded in fp32) into shared memory.
+//    item's first tile).  P is written as bf16, for up to 32 heads with the
+//    rounding's rest beside it, into shared memory; the sums that divide it
+//    are kept unrounded in fp32.
 // Every wait is bounded; on timeout the kernel sets the device error word,
 // stops, waits (bounded) for its copies and products, frees tensor memory
 // and returns.
@@ -97,7 +98,15 @@ struct LatentShape {
   static constexpr int HH = NH / 2, QH = NH / 4;   // heads of a softmax warp, of a thread
   static constexpr int kQChunk = NH * 128;
   static constexpr int kQ = kChunks * kQChunk;
-  static constexpr uint32_t kColO = 0, kColS = kPairs * NH;
+  // P is kept as two bf16 values, the rounded weight and what the rounding
+  // left (16 bits in all), where that is free: their products share the
+  // instruction, as columns h and NH + h, and 32 columns take the time of 16,
+  // 64 of 32 nearly so (45, 46 and 54 cycles).  For 64 heads the second half
+  // fits neither tensor memory nor shared memory: there P is one bf16, and a
+  // result's error that of two roundings instead of one.
+  static constexpr bool kSplit = NH <= 32;
+  static constexpr int NP = kSplit ? 2 * NH : NH;   // columns of an O^T product
+  static constexpr uint32_t kColO = 0, kColS = kPairs * NP;
   static_assert(NH % 16 == 0 && NH <= 64 && kColS + 2 * NH <= 512, "shape");
 };
 
@@ -252,8 +261,10 @@ struct LatentItem {
   int req, tb, te, dst, page0, block;
 };
 __device__ __forceinline__ LatentItem item_at(const LatentArgs& a, int it) {
-  const int32_t* w = a.sched + a.off_items + (int64_t)it * kItemWords;
-  return LatentItem{w[0], w[1], w[2], w[3], w[4], w[7]};
+  const int4* w = reinterpret_cast<const int4*>(a.sched + a.off_items + (int64_t)it * kItemWords);
+  const int4 x = w[0], y = w[1];
+  auto same = [](int v) { return __shfl_sync(kFull, v, 0); };
+  return LatentItem{same(x.x), same(x.y), same(x.z), same(x.w), same(y.x), same(y.w)};
 }
 
 template <class C>
@@ -270,10 +281,13 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   uint8_t* sP = sQ + C::kQ;
   LatentSmem<C>* sh = reinterpret_cast<LatentSmem<C>*>(sP + kP);
   volatile int* abort_flag = &sh->abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (shuffled from lane 0 so that the compiler knows these as the same in the
+  // whole warp: the issuing loops then keep their descriptors in uniform
+  // registers)
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   pdl_launch_dependents();
-  const int it0 = a.sched[a.off_cta + blockIdx.x];
-  const int it1 = a.sched[a.off_cta + blockIdx.x + 1];
+  const int it0 = __shfl_sync(kFull, a.sched[a.off_cta + blockIdx.x], 0);
+  const int it1 = __shfl_sync(kFull, a.sched[a.off_cta + blockIdx.x + 1], 0);
   if (it0 >= it1) {
     pdl_wait();
     return;
@@ -464,7 +478,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   } else if (warp == kWarpOut) {
     // -------------------------------------------------------- O^T products
     const bool me = elect_one();
-    const uint32_t idesc = tc::mma_idesc(128, C::NH, 1) | (1u << 15);   // A and B MN-major
+    const uint32_t idesc = tc::mma_idesc(128, C::NP, 1) | (1u << 15);   // A and B MN-major
     uint64_t c0[kRegions];   // 64-dim blocks 1 KB apart, 8-token groups a group apart
 #pragma unroll
     for (int g = 0; g < kRegions; ++g)
@@ -507,7 +521,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < kBoxes; ++kk)
                 if (kk < nbox)
-                  mma_ss(tmem + C::kColO + C::NH * (region_first(g) / 2 + p),
+                  mma_ss(tmem + C::kColO + C::NP * (region_first(g) / 2 + p),
                          cs + (uint64_t)(128 * p + kk * (group_bytes(g) >> 3)),
                          p0 + (uint64_t)(128 * kk), idesc, t > w.tb || kk > 0);
             mma_commit(&sh->empty[st][g]);
@@ -624,7 +638,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             tc_fence_after();
             constexpr int kPart = HH < 16 ? HH : 16;   // columns at a time: the registers
 #pragma unroll
-            for (int p = 0; p < kPairs; ++p)
+            for (int p = 0; p < kPairs * (C::kSplit ? 2 : 1); ++p)
 #pragma unroll
               for (int c = 0; c < HH; c += kPart) {
                 uint32_t o[kPart];
@@ -648,26 +662,32 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         }
         // weights 2^y; this thread's part of a row of P, 16-byte pieces of 8
         // heads swizzled as the products read them
-        uint32_t pw[QH / 2];
+        uint32_t pw[QH / 2], pl[QH / 2];
 #pragma unroll
         for (int j = 0; j < QH; j += 2) {
           const float p0 = live ? fast_exp2(y[j]) : 0.f;
           const float p1 = live ? fast_exp2(y[j + 1]) : 0.f;
           l[j] += p0;
           l[j + 1] += p1;
-          pw[j / 2] = pack_bf16(p0, p1);
+          const uint32_t hi = pack_bf16(p0, p1);
+          pw[j / 2] = hi;
+          pl[j / 2] = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
         }
-        const int h8 = HH * half + hq;   // the block's head, a multiple of 4
+        const int h8 = HH * half + hq;   // the block's head, a multiple of QH
         uint8_t* prow = sP + row * 128;
-        if constexpr (QH == 4) {
-          *reinterpret_cast<uint2*>(prow + (((h8 >> 3) ^ (row & 7)) << 4) + (h8 & 4) * 2) =
-              make_uint2(pw[0], pw[1]);
-        } else {
+        auto put = [&](int h, const uint32_t (&w)[QH / 2]) {
+          if constexpr (QH == 4) {
+            *reinterpret_cast<uint2*>(prow + (((h >> 3) ^ (row & 7)) << 4) + (h & 4) * 2) =
+                make_uint2(w[0], w[1]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < QH / 8; ++i)
-            *reinterpret_cast<uint4*>(prow + ((((h8 >> 3) + i) ^ (row & 7)) << 4)) =
-                make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
-        }
+            for (int i = 0; i < QH / 8; ++i)
+              *reinterpret_cast<uint4*>(prow + ((((h >> 3) + i) ^ (row & 7)) << 4)) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        };
+        put(h8, pw);
+        if constexpr (C::kSplit) put(C::NH + h8, pl);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -710,8 +730,17 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         uint32_t o[HH];
-        tmem_ldn<HH>(tq + C::kColO + C::NH * p + HH * half, o);
-        tc::tmem_wait_ld();
+        tmem_ldn<HH>(tq + C::kColO + C::NP * p + HH * half, o);
+        if constexpr (C::kSplit) {
+          uint32_t o2[HH];
+          tmem_ldn<HH>(tq + C::kColO + C::NP * p + C::NH + HH * half, o2);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < HH; ++j)
+            o[j] = __float_as_uint(__uint_as_float(o[j]) + __uint_as_float(o2[j]));
+        } else {
+          tc::tmem_wait_ld();
+        }
         const int dim = 128 * p + 32 * quad + lane;
         if (w.dst >= 0) {
           float* to = a.o_part + ((int64_t)w.dst * a.heads + h0) * kLatentDim + dim;
