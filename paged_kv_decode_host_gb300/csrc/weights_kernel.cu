@@ -62,17 +62,18 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t* p, uint64_t policy) 
   return v;
 }
 
-// two E4M3 bytes to an f16 pair (exact)
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
-  uint32_t r;
-  asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(two));
-  return r;
+// four E4M3 bytes to two f16 pairs (exact)
+__device__ __forceinline__ void e4m3x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-template <bool kFp8>
+// kTiles: the page size is a multiple of 16, so that a tile lies in one page.
+template <bool kFp8, bool kTiles>
 __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(const __grid_constant__ WeightsArgs a) {
   if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
   constexpr int kPieces = kFp8 ? 2 : 4;      // 16-byte pieces of a row per lane
@@ -157,51 +158,74 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(const __grid_co
       if (j >= g || l == -CUDART_INF_F) base[e] = CUDART_INF_F;
     }
     const int tiles = (n + 15) >> 4;
-    auto page_of = [&](int t) -> int {
-      const int page = t < n ? pages[t / P] : 0;
-      return page;
-    };
-    int pg[2];
-    pg[0] = page_of(16 * sub + r8);
-    pg[1] = page_of(16 * sub + r8 + 8);
-    for (int tile = sub; tile < tiles; tile += per) {
-      uint4 k[2][kPieces];
-      float old = 0.f;
-      int64_t slot_at[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 16 * tile + r8 + 8 * i;
-        int page = pg[i];
-        const bool in = t < n && (unsigned)page < (unsigned)a.num_pages;
-        if (t < n && !in) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
-        if (!in) page = 0;
-        const int slot = t % P;
-        slot_at[i] = in ? ((int64_t)page * a.hkv + h) * P + slot : -1;
-        const uint8_t* row = a.kv + page * a.page_bytes + slot * a.token_bytes + h * a.head_bytes + 16 * c4;
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p)
-          k[i][p] = in ? load_stream(row + 64 * p, policy) : make_uint4(0, 0, 0, 0);
+    // a tile's pages, looked up a tile before they are used: one with kTiles,
+    // else the lane's two tokens'
+    int pg[2] = {0, 0};
+    auto look_up = [&](int tile) {
+      const int t = 16 * tile;
+      if constexpr (kTiles) {
+        pg[0] = t < n ? pages[t / P] : 0;
+      } else {
+        pg[0] = t + r8 < n ? pages[(t + r8) / P] : 0;
+        pg[1] = t + r8 + 8 < n ? pages[(t + r8 + 8) / P] : 0;
       }
-      // lanes 0 and 1 of a quad own its two tokens' sums
-      const int64_t at = c4 == 0 ? slot_at[0] : c4 == 1 ? slot_at[1] : -1;
-      const int mine = 16 * tile + r8 + 8 * c4;
-      if (at >= 0 && mine < fresh) old = a.weights[at];
-      // the next tile's pages while K is on its way
-      pg[0] = page_of(16 * (tile + per) + r8);
-      pg[1] = page_of(16 * (tile + per) + r8 + 8);
+    };
+    // one tile on its way: K, the lane's own sum (lanes 0 and 1 of a quad own
+    // its two tokens), and where that lies
+    struct Tile {
+      uint4 k[2][kPieces];
+      float old;
+      int64_t at;
+    };
+    const int64_t lane_at = h * a.head_bytes + 16 * c4;
+    auto fetch = [&](int tile, Tile& x) {
+      int64_t slot_at[2];
+      if constexpr (kTiles) {
+        const bool in = (unsigned)pg[0] < (unsigned)a.num_pages;   // (the tile has a token)
+        if (!in && lane == 0) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+        const int64_t page = in ? pg[0] : 0;
+        const int slot = 16 * tile % P, left = in ? n - 16 * tile : 0;
+        const uint8_t* row = a.kv + page * a.page_bytes + (slot + r8) * a.token_bytes + lane_at;
+        const int64_t first = (page * a.hkv + h) * P + slot + r8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool live = r8 + 8 * i < left;
+          slot_at[i] = live ? first + 8 * i : -1;
+#pragma unroll
+          for (int p = 0; p < kPieces; ++p)
+            x.k[i][p] = live ? load_stream(row + 8 * i * a.token_bytes + 64 * p, policy)
+                             : make_uint4(0, 0, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = 16 * tile + r8 + 8 * i;
+          const bool in = t < n && (unsigned)pg[i] < (unsigned)a.num_pages;
+          if (t < n && !in) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+          const int64_t page = in ? pg[i] : 0;
+          const int slot = t % P;
+          slot_at[i] = in ? (page * a.hkv + h) * P + slot : -1;
+          const uint8_t* row = a.kv + page * a.page_bytes + slot * a.token_bytes + lane_at;
+#pragma unroll
+          for (int p = 0; p < kPieces; ++p)
+            x.k[i][p] = in ? load_stream(row + 64 * p, policy) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      x.at = c4 == 0 ? slot_at[0] : c4 == 1 ? slot_at[1] : -1;
+      x.old = x.at >= 0 && 16 * tile + r8 + 8 * c4 < fresh ? a.weights[x.at] : 0.f;
+    };
+    auto finish = [&](int tile, const Tile& x) {
       float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        const uint32_t lo[4] = {k[0][p].x, k[0][p].y, k[0][p].z, k[0][p].w};
-        const uint32_t hi[4] = {k[1][p].x, k[1][p].y, k[1][p].z, k[1][p].w};
+        const uint32_t lo[4] = {x.k[0][p].x, x.k[0][p].y, x.k[0][p].z, x.k[0][p].w};
+        const uint32_t hi[4] = {x.k[1][p].x, x.k[1][p].y, x.k[1][p].z, x.k[1][p].w};
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           uint32_t af[4];
           if constexpr (kFp8) {
-            af[0] = e4m3x2(lo[s] & 0xffffu);
-            af[1] = e4m3x2(hi[s] & 0xffffu);
-            af[2] = e4m3x2(lo[s] >> 16);
-            af[3] = e4m3x2(hi[s] >> 16);
+            e4m3x4(lo[s], af[0], af[2]);
+            e4m3x4(hi[s], af[1], af[3]);
             mma_f16(c[s & 1], af, qf[p][s][0], qf[p][s][1]);
           } else {
             af[0] = lo[2 * s];
@@ -219,15 +243,46 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(const __grid_co
         w[i] = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x = fmaf(c[0][2 * i + e] + c[1][2 * i + e], sc[e], -base[e]);
-          w[i] += base[e] == CUDART_INF_F ? 0.f : exp2f(x);
+          const float z = fmaf(c[0][2 * i + e] + c[1][2 * i + e], sc[e], -base[e]);
+          w[i] += base[e] == CUDART_INF_F ? 0.f : exp2f(z);
         }
         w[i] += __shfl_xor_sync(kFull, w[i], 1);
         w[i] += __shfl_xor_sync(kFull, w[i], 2);
       }
-      if (at >= 0) {
-        a.weights[at] = old + (c4 == 0 ? w[0] : w[1]);
-        if (a.positions && mine >= fresh) a.positions[at] = age0 + mine;
+      if (x.at >= 0) {
+        const int mine = 16 * tile + r8 + 8 * c4;
+        a.weights[x.at] = x.old + (c4 == 0 ? w[0] : w[1]);
+        if (a.positions && mine >= fresh) a.positions[x.at] = age0 + mine;
+      }
+    };
+    // Two E4M3 tiles are on their way per warp (a bf16 tile has twice the
+    // bytes; two of them do not fit the registers of 24 warps).
+    int tile = sub;
+    look_up(tile);
+    if constexpr (kFp8) {
+      Tile x[2];
+      if (tile < tiles) {
+        fetch(tile, x[0]);
+        look_up(tile + per);
+      }
+      while (tile < tiles) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (tile >= tiles) break;
+          if (tile + per < tiles) {
+            fetch(tile + per, x[i ^ 1]);
+            look_up(tile + 2 * per);
+          }
+          finish(tile, x[i]);
+          tile += per;
+        }
+      }
+    } else {
+      for (; tile < tiles; tile += per) {
+        Tile x;
+        fetch(tile, x);
+        look_up(tile + per);
+        finish(tile, x);
       }
     }
   }
@@ -236,10 +291,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(const __grid_co
 }  // namespace
 
 cudaError_t launch_weights(const WeightsArgs& a, bool fp8, int grid, cudaStream_t stream) {
+  const bool tiles = a.page_size % 16 == 0;
   if (fp8)
-    weights_kernel<true><<<grid, kWarps * 32, 0, stream>>>(a);
+    (tiles ? weights_kernel<true, true> : weights_kernel<true, false>)<<<grid, kWarps * 32, 0, stream>>>(a);
   else
-    weights_kernel<false><<<grid, kWarps * 32, 0, stream>>>(a);
+    (tiles ? weights_kernel<false, true> : weights_kernel<false, false>)<<<grid, kWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
