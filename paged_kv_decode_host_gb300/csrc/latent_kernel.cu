@@ -20,12 +20,13 @@
 //     S^T [tokens x heads]  = C [tokens x 576]  Q^T    A = C, B = Q, K-major
 //     O^T [dims x heads]   += C^T [dims x tokens] P^T  A = C, B = P, MN-major
 // The same shared-memory tile of C feeds both: blocks of 8 tokens x 64 columns
-// (1 KB, 128-byte swizzle), the 9 column chunks of 8 tokens in two regions:
-// chunks 4-8 (with the rotary key) and chunks 0-3.
+// (1 KB, 128-byte swizzle), the 9 column chunks in two regions: 4-8 (with the
+// rotary key) and 0-3.  (Four regions shorten the wait for the last scores but
+// lengthen the producer's way more: 78 -> 79 us for 128 heads.)
 //  * warp 8 streams C: one TMA tensor copy per region and 16 tokens (10 and 8
 //    KB; a 5-D map of the cache gives the blocked order, so page tiles join
-//    to one operand however the pages are scattered; copies of 2 KB each were
-//    bound by their issue, about 110 cycles a copy);
+//    to one operand however the pages are scattered; 36 copies of 2 KB a tile
+//    were bound by their issue, about 110 cycles a copy);
 //  * warp 9 issues the score products of a region as it lands, warp 10 the P.V
 //    products, whose regions are refilled one after the other; the whole warp
 //    runs the loop and one elected lane issues, with unrolled constant
@@ -67,12 +68,13 @@ using tc::tc_fence_before;
 using tc::tc_wait;
 
 constexpr int kChunks = kLatentRow / 64;        // 9 column chunks: 8 latent, 1 rotary
-constexpr int kRegions = 2;
 constexpr int kPairs = kLatentDim / 128;        // 4 O^T products of 128 dims
-// first chunk and chunks of a region; the pairs (128 dims) whose values it holds
+constexpr int kRegions = 2;
+// first chunk and chunks of a region; the products (128 dims) whose values it
+// holds
 __host__ __device__ constexpr int region_first(int g) { return g == 0 ? 4 : 0; }
 __host__ __device__ constexpr int region_chunks(int g) { return g == 0 ? 5 : 4; }
-constexpr int kRegionPairs = 2;
+constexpr int kRegionPairs = kPairs / kRegions;
 constexpr int kSoftWarps = 8;
 constexpr int kWarpLoad = 8, kWarpScore = 9, kWarpOut = 10;
 constexpr int kLatThreads = 11 * 32;
@@ -143,12 +145,13 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
   return pol;
 }
 
-__device__ __forceinline__ void tensor_copy3_g2s(void* dst, const CUtensorMap* map, int c0, int c1,
-                                                 int c2, uint64_t* bar, uint64_t policy) {
+// 4-D tensor-map copy global -> shared, as tensor_copy_g2s.
+__device__ __forceinline__ void tensor_copy4_g2s(void* dst, const CUtensorMap* map, int c0, int c1,
+                                                 int c2, int c3, uint64_t* bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)),
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)),
       "l"(policy)
       : "memory");
 }
@@ -343,6 +346,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     // ------------------------------------------------------------ producer
     // q and the cache are read before the previous kernel is waited for, as
     // the decode kernel does (the contract of pkd_run)
+    // a second block of heads reads the rows from L2
     const uint64_t policy = a.blocks > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
     const int P = a.page_size;
     int r = 0, nq = 0;
@@ -357,11 +361,9 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       if (lane == 0) {
         ++nq;
         mbar_arrive_expect_tx(&sh->qfull, (uint32_t)C::kQ);
+        tensor_copy4_g2s(sQ, &a.q_map, 0, C::NH * w.block, 0, w.req, &sh->qfull, policy);
       }
       __syncwarp();
-      if (lane < kChunks)
-        tensor_copy3_g2s(sQ + lane * C::kQChunk, &a.q_map, 64 * lane, C::NH * w.block, w.req,
-                         &sh->qfull, policy);
       // page ids of 32 consecutive 16-token boxes, one per lane (items start
       // on page boundaries); the next 32 are fetched while these are copied
       const int boxes = (w.te - w.tb + 15) >> 4;
@@ -569,7 +571,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       for (int j = 0; j < QH; ++j) l[j] = 0.f;
       for (int t = w.tb; t < w.te && ok; t += kTile, ++r) {
         const int b = r & 1;
-        if (!tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
+        // P of the tile before has been read (its buffer is written below,
+        // and a raised base rescales O): long so when the scores arrive
+        if ((r > 0 && !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) ||
+            !tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
           ok = false;
           break;
         }
@@ -606,12 +611,6 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         }
         const bool up = first || (sh->raise[par][half][0] | sh->raise[par][half][1] |
                                   sh->raise[par][half][2] | sh->raise[par][half][3]) != 0;
-        // P of the tile before is read (its buffer is written below, and a
-        // raised base rescales O)
-        if (r > 0 && !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) {
-          ok = false;
-          break;
-        }
         if (up) {
           int at = par;
           if (!first) {
@@ -878,8 +877,8 @@ static_assert(latent_smem<Shape16>() <= 227 * 1024 && latent_smem<Shape32>() <= 
                   latent_smem<Shape64>() <= 227 * 1024,
               "dynamic shared memory of one CTA");
 
-const void* kernel_of(int32_t block_heads) {
-  switch (block_heads) {
+const void* kernel_of(int32_t heads) {
+  switch (latent_block_heads(heads)) {
     case 16: return reinterpret_cast<const void*>(&latent_decode_kernel<Shape16>);
     case 32: return reinterpret_cast<const void*>(&latent_decode_kernel<Shape32>);
     default: return reinterpret_cast<const void*>(&latent_decode_kernel<Shape64>);
@@ -943,15 +942,13 @@ int latent_smem_bytes(int32_t heads) {
 }
 
 cudaError_t latent_prepare(int32_t heads) {
-  return cudaFuncSetAttribute(kernel_of(latent_block_heads(heads)),
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(kernel_of(heads), cudaFuncAttributeMaxDynamicSharedMemorySize,
                               latent_smem_bytes(heads));
 }
 
 cudaError_t latent_occupancy(int32_t heads, int* blocks_per_sm) {
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-      blocks_per_sm, kernel_of(latent_block_heads(heads)), kLatThreads,
-      (size_t)latent_smem_bytes(heads));
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of(heads), kLatThreads,
+                                                       (size_t)latent_smem_bytes(heads));
 }
 
 cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool merge,
@@ -967,7 +964,7 @@ cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool me
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void* args[] = {const_cast<LatentArgs*>(&a)};
-  cudaError_t e = cudaLaunchKernelExC(&cfg, kernel_of(latent_block_heads(a.heads)), args);
+  cudaError_t e = cudaLaunchKernelExC(&cfg, kernel_of(a.heads), args);
   if (e != cudaSuccess) return e;
   if (decode_done && (e = cudaEventRecordWithFlags(decode_done, stream, cudaEventRecordExternal)) !=
                          cudaSuccess)
@@ -1003,18 +1000,19 @@ cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page
              : cudaErrorInvalidValue;
 }
 
-// The query map: {576 columns, head, request}, box {64 columns, a block's
-// heads, 1 request}; heads past the last read as zeros.
+// The query map: {64 columns, head, column chunk, request}, box {64, a block's
+// heads, every chunk, 1}, which lands as [chunk][head][128 bytes] with the
+// 128-byte swizzle; heads past the last read as zeros.
 cudaError_t encode_latent_q_map(const void* q, int32_t batch, int32_t heads, CUtensorMap* map) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   if (q == nullptr || (uintptr_t)q % 16 != 0 || batch < 1 || heads < 1) return cudaErrorInvalidValue;
   const cuuint64_t row = (cuuint64_t)kLatentRow * 2;
-  const cuuint64_t dims[3] = {(cuuint64_t)kLatentRow, (cuuint64_t)heads, (cuuint64_t)batch};
-  const cuuint64_t strides[2] = {row, row * (cuuint64_t)heads};
-  const cuuint32_t box[3] = {64, (cuuint32_t)latent_block_heads(heads), 1};
-  const cuuint32_t elem[3] = {1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+  const cuuint64_t dims[4] = {64, (cuuint64_t)heads, (cuuint64_t)kChunks, (cuuint64_t)batch};
+  const cuuint64_t strides[3] = {row, 128, row * (cuuint64_t)heads};
+  const cuuint32_t box[4] = {64, (cuuint32_t)latent_block_heads(heads), (cuuint32_t)kChunks, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box,
                 elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
