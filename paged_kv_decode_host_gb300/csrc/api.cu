@@ -245,14 +245,15 @@ int launch_latent_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, fl
   }
   if (ev_before && cudaEventRecordWithFlags(ev_before, stream, cudaEventRecordExternal) != cudaSuccess)
     return PKD_E_CUDA;
-  // the merge has nothing to do when no request is split; a captured launch
-  // must follow later plans, whose splits are not known yet
+  // the merge's grid follows the plan (0: no request is split); a captured
+  // launch must do for later plans, whose splits are not known yet
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PKD_E_CUDA;
-  const bool merge = ctx->info.num_units > 0 || cap != cudaStreamCaptureStatusNone;
-  return launch_latent(a, ctx->n_cta, ctx->merge_grid, merge, ev_after, stream) == cudaSuccess
-             ? PKD_OK
-             : PKD_E_CUDA;
+  const int merge = cap != cudaStreamCaptureStatusNone
+                        ? ctx->merge_grid
+                        : latent_merge_blocks(c.num_qo_heads, ctx->info.num_units,
+                                              ctx->max_chunks, ctx->merge_grid);
+  return launch_latent(a, ctx->n_cta, merge, ev_after, stream) == cudaSuccess ? PKD_OK : PKD_E_CUDA;
 }
 
 int launch_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, float* lse,

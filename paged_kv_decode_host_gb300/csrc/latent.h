@@ -42,11 +42,14 @@ struct LatentArgs {
 int latent_smem_bytes(int32_t heads);
 cudaError_t latent_prepare(int32_t heads);
 cudaError_t latent_occupancy(int32_t heads, int* blocks_per_sm);
-// The decode kernel and, with merge, the merge of split requests (its grid
-// follows the plan on the device).  decode_done (or null) is recorded
-// between the two.
-cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool merge,
-                          cudaEvent_t decode_done, cudaStream_t stream);
+// Merge blocks for a plan of `units` split requests, at most `most`: blocks
+// without a task would only keep the next kernel off their SMs.
+int latent_merge_blocks(int32_t heads, int32_t units, int32_t most_slots, int most);
+// The decode kernel and, with a merge grid, the merge of split requests (its
+// tasks are the plan's, read on the device; any grid does them all).
+// decode_done (or null) is recorded between the two.
+cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, cudaEvent_t decode_done,
+                          cudaStream_t stream);
 cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page_size, int region,
                               CUtensorMap* map);
 cudaError_t encode_latent_q_map(const void* q, int32_t batch, int32_t heads, CUtensorMap* map);

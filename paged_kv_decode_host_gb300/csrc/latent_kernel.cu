@@ -776,46 +776,62 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 // (one warp reads a task's few slots in one round trip; a long request's 150
 // would take it twenty): warp w takes slots w, w + warps, ... eight loads at
 // a time, and the warps' sums are added in warp order.
-constexpr int kMergeDims = 128, kMergeWarps = 8;
+constexpr int kMergeDims = 128, kMergeWarps = 8, kMergeParts = kLatentDim / kMergeDims;
+__host__ __device__ constexpr int merge_team(int most_slots) {
+  return most_slots <= 8 ? 1 : most_slots <= 32 ? 2 : 8;
+}
 template <int kTeam>
-__device__ __forceinline__ void merge_tasks(const LatentArgs& a, int units, float4 (&acc_s)[kMergeWarps][32],
+__device__ __forceinline__ void merge_tasks(const LatentArgs& a, int units,
+                                            float4 (&acc_s)[kMergeWarps][32],
                                             float (&z_s)[kMergeWarps]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kParts = kLatentDim / kMergeDims, kTeams = kMergeWarps / kTeam;
+  constexpr int kTeams = kMergeWarps / kTeam;
   const int sub = warp % kTeam;
-  const int64_t tasks = (int64_t)units * a.heads * kParts;
+  const int64_t tasks = (int64_t)units * a.heads * kMergeParts;
+  bool waited = false;
   for (int64_t t0 = (int64_t)blockIdx.x * kTeams; t0 < tasks; t0 += (int64_t)gridDim.x * kTeams) {
     const int64_t task = t0 + warp / kTeam;
     const bool on = task < tasks;
-    int part = 0, h = 0, req = 0;
+    int part = 0, h = 0, req = 0, s0 = 0, s1 = 0;
+    if (on) {
+      part = (int)(task % kMergeParts);
+      h = (int)(task / kMergeParts % a.heads);
+      const int u = (int)(task / ((int64_t)kMergeParts * a.heads));
+      s0 = a.sched[a.off_merge + u];
+      s1 = a.sched[a.off_merge + u + 1];
+      req = a.sched[a.off_units + 2 * u];
+    }
+    if (!waited) {
+      pdl_wait();   // the partial states belong to the decode kernel
+      waited = true;
+    }
     float base = 0.f, z = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
-      part = (int)(task % kParts);
-      h = (int)(task / kParts % a.heads);
-      const int u = (int)(task / ((int64_t)kParts * a.heads));
-      const int s0 = a.sched[a.off_merge + u], s1 = a.sched[a.off_merge + u + 1];
-      req = a.sched[a.off_units + 2 * u];
       const float* lp = a.l_part + h;
       const float* op = a.o_part + (int64_t)h * kLatentDim + kMergeDims * part + 4 * lane;
-      float top = -CUDART_INF_F;
-      for (int s = s0 + lane; s < s1; s += 32) top = fmaxf(top, lp[(int64_t)s * a.heads]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-      base = top == -CUDART_INF_F ? 0.f : top;
       constexpr int kAtOnce = 8;
-      for (int s = s0 + sub; s < s1; s += kAtOnce * kTeam) {
-        float4 o[kAtOnce];
-        float lv[kAtOnce];
+      float4 o[kAtOnce];
+      float lv[kAtOnce];
+      auto load = [&](int s) {
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
           const int64_t si = min(s + i * kTeam, s1 - 1);
-          lv[i] = lp[si * a.heads];
           // volatile: all eight leave before the first is used
           asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
                        : "=f"(o[i].x), "=f"(o[i].y), "=f"(o[i].z), "=f"(o[i].w)
                        : "l"(op + si * a.heads * kLatentDim));
+          lv[i] = lp[si * a.heads];
         }
+      };
+      load(s0 + sub);   // the first eight travel with the maxima
+      float top = -CUDART_INF_F;
+      for (int s = s0 + lane; s < s1; s += 32) top = fmaxf(top, lp[(int64_t)s * a.heads]);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+      base = top == -CUDART_INF_F ? 0.f : top;
+      for (int s = s0 + sub; s < s1; s += kAtOnce * kTeam) {
+        if (s > s0 + sub) load(s);
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
           if (s + i * kTeam >= s1) break;
@@ -853,6 +869,7 @@ __device__ __forceinline__ void merge_tasks(const LatentArgs& a, int units, floa
       if (part == 0 && lane == 0 && a.lse != nullptr) a.lse[qrow] = base + log2f(z) * kLn2;
     }
   }
+  if (!waited) pdl_wait();   // complete only after the decode kernel
 }
 
 __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const __grid_constant__ LatentArgs a) {
@@ -860,11 +877,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const __
   __shared__ float z_s[kMergeWarps];
   pdl_launch_dependents();
   if (a.wait_epoch != 0) pdl_wait();   // the schedule came from another stream
-  const int units = a.sched[H_NUNITS], most = a.sched[H_MAXCHUNKS];
-  pdl_wait();   // the partial states belong to the decode kernel
-  if (most <= 8)
+  const int units = a.sched[H_NUNITS], team = merge_team(a.sched[H_MAXCHUNKS]);
+  if (team == 1)
     merge_tasks<1>(a, units, acc_s, z_s);
-  else if (most <= 32)
+  else if (team == 2)
     merge_tasks<2>(a, units, acc_s, z_s);
   else
     merge_tasks<8>(a, units, acc_s, z_s);
@@ -951,8 +967,14 @@ cudaError_t latent_occupancy(int32_t heads, int* blocks_per_sm) {
                                                        (size_t)latent_smem_bytes(heads));
 }
 
-cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool merge,
-                          cudaEvent_t decode_done, cudaStream_t stream) {
+int latent_merge_blocks(int32_t heads, int32_t units, int32_t most_slots, int most) {
+  const int64_t teams = kMergeWarps / merge_team(most_slots);
+  const int64_t blocks = ((int64_t)units * heads * kMergeParts + teams - 1) / teams;
+  return (int)(blocks < most ? blocks : most);
+}
+
+cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, cudaEvent_t decode_done,
+                          cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kLatThreads);
@@ -969,7 +991,7 @@ cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, bool me
   if (decode_done && (e = cudaEventRecordWithFlags(decode_done, stream, cudaEventRecordExternal)) !=
                          cudaSuccess)
     return e;
-  if (!merge) return cudaSuccess;
+  if (merge_grid == 0) return cudaSuccess;
   cfg.gridDim = dim3(merge_grid);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
