@@ -156,7 +156,8 @@ typedef struct pkd_config {
  * num_kv_heads 1, 1 <= Hq <= 128, page size a multiple of 16; no other flag.
  * Plans (pkd_plan) cut the requests' tokens, laid end to end, into equal
  * stretches, one per CTA -- per CTA pair above 64 heads, a work item covering
- * up to 64; alpha < 0 selects 128 and min_chunk_tokens < 0 128.  Graphs replay
+ * up to 64; alpha < 0 selects 128, min_chunk_tokens < 0 128 (256 above
+ * 32 heads).  Graphs replay
  * with the batch they were captured with. */
 #define PKD_FLAG_LATENT 1024u
 

@@ -772,13 +772,19 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 // Merge of split requests: out = sum_i w_i o_i / sum_i w_i, w_i = exp(L_i -
 // max L), over a request's partial states.  A task is 128 dims of one
 // (request, head); a lane holds four of them, so a slot is one 512-byte read
-// of a warp.  1, 2 or 8 warps share a task, by the longest request's slots
-// (one warp reads a task's few slots in one round trip; a long request's 150
-// would take it twenty): warp w takes slots w, w + warps, ... eight loads at
+// of a warp.  Up to 8 warps share a task (one reads a task's few slots in one
+// round trip; a long request's 150 would take it twenty): warp w takes slots w, w + warps, ... eight loads at
 // a time, and the warps' sums are added in warp order.
 constexpr int kMergeDims = 128, kMergeWarps = 8, kMergeParts = kLatentDim / kMergeDims;
-__host__ __device__ constexpr int merge_team(int most_slots) {
-  return most_slots <= 8 ? 1 : most_slots <= 32 ? 2 : 8;
+// Warps per task: one per eight slots of the longest request (up to 8) while
+// all of them find room at once (three blocks to an SM).  Eight for every
+// request of more than 8 slots ran in two waves where tasks are many: 20
+// against 11 us (8 requests of 2,000 tokens, 64 heads, 16 slots each).
+__host__ __device__ constexpr int merge_team(int most_slots, int64_t tasks) {
+  int team = 1;
+  while (team < kMergeWarps && most_slots > 8 * team && tasks * team * 2 <= 152 * 3 * kMergeWarps)
+    team *= 2;
+  return team;
 }
 template <int kTeam>
 __device__ __forceinline__ void merge_tasks(const LatentArgs& a, int units,
@@ -877,11 +883,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const __
   __shared__ float z_s[kMergeWarps];
   pdl_launch_dependents();
   if (a.wait_epoch != 0) pdl_wait();   // the schedule came from another stream
-  const int units = a.sched[H_NUNITS], team = merge_team(a.sched[H_MAXCHUNKS]);
+  const int units = a.sched[H_NUNITS];
+  const int team = merge_team(a.sched[H_MAXCHUNKS], (int64_t)units * a.heads * kMergeParts);
   if (team == 1)
     merge_tasks<1>(a, units, acc_s, z_s);
   else if (team == 2)
     merge_tasks<2>(a, units, acc_s, z_s);
+  else if (team == 4)
+    merge_tasks<4>(a, units, acc_s, z_s);
   else
     merge_tasks<8>(a, units, acc_s, z_s);
 }
@@ -968,8 +977,9 @@ cudaError_t latent_occupancy(int32_t heads, int* blocks_per_sm) {
 }
 
 int latent_merge_blocks(int32_t heads, int32_t units, int32_t most_slots, int most) {
-  const int64_t teams = kMergeWarps / merge_team(most_slots);
-  const int64_t blocks = ((int64_t)units * heads * kMergeParts + teams - 1) / teams;
+  const int64_t tasks = (int64_t)units * heads * kMergeParts;
+  const int64_t teams = kMergeWarps / merge_team(most_slots, tasks);
+  const int64_t blocks = (tasks + teams - 1) / teams;
   return (int)(blocks < most ? blocks : most);
 }
 

@@ -524,7 +524,8 @@ int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   const int32_t blocks = latent_blocks(cfg.num_qo_heads);
   const int32_t nv = std::max(1, n_cta / blocks);
   const int64_t alpha = cfg.alpha < 0 ? kLatentAlpha : cfg.alpha;
-  const int64_t min_chunk = cfg.min_chunk_tokens < 0 ? kLatentMinChunk : cfg.min_chunk_tokens;
+  const int64_t min_chunk =
+      cfg.min_chunk_tokens < 0 ? latent_min_chunk(cfg.num_qo_heads) : cfg.min_chunk_tokens;
   const int64_t floor_c = ceil_div(std::max<int64_t>(min_chunk, 1), P) * P;
   int64_t span = std::max(alpha + floor_c, ceil_div(total + alpha * batch, nv));
   while (!cut_even(lens, span, alpha, P, floor_c, nv, &parts)) span += std::max<int64_t>(P, span / 64);
