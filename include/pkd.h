@@ -423,8 +423,9 @@ int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const fl
  *       before the call returns, all different: bf16 or (PKD_FLAG_KV_FP8)
  *       E4M3 [num_pages][2][P][Hkv][D] or (PKD_FLAG_HND)
  *       [num_pages][2][Hkv][P][D]; fp32 and int32 [num_pages][Hkv][P]
- *   indptr [batch + 1], indices, last_page_len [batch], seen [batch] : device
- *       int32, the table before the eviction; a page may stand in it once
+ *   indptr [batch + 1], indices [num_indices], last_page_len [batch],
+ *   seen [batch] : device int32, the table before the eviction; a page may
+ *       stand in it once (rows of pages that stand there twice are undefined)
  *   max_len : at least the longest request's tokens, at most 262,144
  *   d_workspace : pkd_evict_workspace_bytes(...) bytes, 16-byte aligned, the
  *       call's own until its kernels are done (NULL when that is 0)
@@ -436,8 +437,8 @@ int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const fl
  * Errors: INVALID_ARG, CAPACITY (max_len), WORKSPACE_TOO_SMALL, CUDA. */
 int pkd_evict_kv(int32_t layers, void *const *kv, float *const *weights,
                  int32_t *const *positions, const int32_t *indptr, const int32_t *indices,
-                 const int32_t *last_page_len, const int32_t *seen, int32_t batch,
-                 int32_t max_len, int32_t budget, int32_t sinks, int32_t recent,
+                 int32_t num_indices, const int32_t *last_page_len, const int32_t *seen,
+                 int32_t batch, int32_t max_len, int32_t budget, int32_t sinks, int32_t recent,
                  int32_t per_head, int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
                  int32_t head_dim, uint32_t flags, void *d_workspace, size_t workspace_bytes,
                  int32_t *err, void *stream);
@@ -456,15 +457,17 @@ size_t pkd_evict_workspace_bytes(int32_t layers, int32_t batch, int32_t max_len,
  * projection's output.  The inputs must not overlap the cache.
  *   latent_new, rope_new : device bf16, 16-byte aligned
  *   cache                : device bf16 [num_pages][P][576], 16-byte aligned
- * Two tokens with the same slot leave one of the two rows there.  Tokens
- * outside the table are skipped and flagged in *err as by pkd_append_kv.
+ *   indices              : device int32 [num_indices]
+ * No two tokens may have the same slot (the row would mix the two).  Tokens
+ * outside the table, or of a request whose pages pass num_indices, are skipped
+ * and flagged in *err as by pkd_append_kv.
  * Errors: INVALID_ARG, CUDA. */
 int pkd_append_latent(const void *latent_new, int64_t latent_stride, const void *rope_new,
                       int64_t rope_stride, const int32_t *batch_indices,
                       const int32_t *positions, int32_t n, const int32_t *indptr,
-                      const int32_t *indices, const int32_t *last_page_len, int32_t batch,
-                      void *cache, int32_t num_pages, int32_t page_size, int32_t *err,
-                      void *stream);
+                      const int32_t *indices, int32_t num_indices,
+                      const int32_t *last_page_len, int32_t batch, void *cache,
+                      int32_t num_pages, int32_t page_size, int32_t *err, void *stream);
 
 /* Self-test of the device-side bounded waits (failure detection without a
  * GPU fault; FlashInfer, in depth, "Failure modes in production": errors come

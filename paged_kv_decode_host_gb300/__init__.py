@@ -175,11 +175,11 @@ def load():
                                                 i32, i32, i32, i32, ctypes.c_uint32, vp, vp]),
     }
     i64 = ctypes.c_int64
-    sig["pkd_append_latent"] = (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i32, vp, vp, vp, i32, vp,
-                                               i32, i32, vp, vp])
+    sig["pkd_append_latent"] = (ctypes.c_int, [vp, i64, vp, i64, vp, vp, i32, vp, vp, i32, vp, i32,
+                                               vp, i32, i32, vp, vp])
     sig["pkd_accumulate_weights"] = (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp,
                                                     ctypes.c_float, u64, vp])
-    sig["pkd_evict_kv"] = (ctypes.c_int, [i32, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+    sig["pkd_evict_kv"] = (ctypes.c_int, [i32, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32,
                                           i32, i32, i32, i32, i32, u32, vp, sz, vp, vp])
     sig["pkd_evict_workspace_bytes"] = (sz, [i32] * 6)
     for name, (res, args) in sig.items():
@@ -1069,8 +1069,8 @@ def append_latent(latent_new, rope_new, batch_indices, positions, indptr, indice
     latent_new [n, 512], rope_new [n, 64]: bf16, last dimension contiguous,
     rows of any stride that is a multiple of 8 elements (they may be column
     ranges of one projection's output); cache: bf16 [pages, P, 576], written
-    in place, not overlapping the inputs.  The table arguments and err are
-    append_kv's."""
+    in place, not overlapping the inputs; no two tokens with the same slot.
+    The table arguments and err are append_kv's."""
     import torch
     bf, i32 = torch.bfloat16, torch.int32
     dev = cache.get_device()
@@ -1101,7 +1101,7 @@ def append_latent(latent_new, rope_new, batch_indices, positions, indptr, indice
         st = (load().pkd_append_latent if fast is None else fast.append_latent)(
             latent_new.data_ptr(), strides[0], rope_new.data_ptr(), strides[1],
             batch_indices.data_ptr(), positions.data_ptr(), n, indptr.data_ptr(),
-            indices.data_ptr(), last_page_len.data_ptr(), batch, cache.data_ptr(),
+            indices.data_ptr(), indices.numel(), last_page_len.data_ptr(), batch, cache.data_ptr(),
             cache.shape[0], cache.shape[1], _err_arg(err, dev), _stream_ptr(stream))
     if st:
         _check(st, "pkd_append_latent")
@@ -1118,7 +1118,7 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
     caches as for :func:`append_kv`, weights float32 and positions int32
     [pages, Hkv, P] as :meth:`BatchDecodeWithPagedKVCache.accumulate_weights`
     keeps them.  indptr / indices / last_page_len / seen: int32 CUDA tensors,
-    the table and the tokens seen; max_len: at least the longest request's
+    the table (a page stands in it once) and the tokens seen; max_len: at least the longest request's
     tokens (at most 262,144).  Tokens at positions below ``sinks`` and among
     the last ``recent`` always stay.  per_head: every KV head keeps its own
     tokens; else all keep the same, by the sum of their weights.  Slots are
@@ -1167,8 +1167,8 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
         if need and stream is not None:
             ws.record_stream(stream)
         args = [[t.data_ptr() for t in ts] for ts in (kv_caches, weights, positions)]
-        rest = (indptr.data_ptr(), indices.data_ptr(), last_page_len.data_ptr(), seen.data_ptr(),
-                batch, max_len, budget, sinks, recent, per_head, pages, P, hkv, D,
+        rest = (indptr.data_ptr(), indices.data_ptr(), indices.numel(), last_page_len.data_ptr(),
+                seen.data_ptr(), batch, max_len, budget, sinks, recent, per_head, pages, P, hkv, D,
                 (FLAG_HND if kv_layout == "HND" else 0) | (FLAG_KV_FP8 if fp8 else 0),
                 ws.data_ptr() if need else 0, need, _err_arg(err, dev), _stream_ptr(stream))
         if fast is not None:

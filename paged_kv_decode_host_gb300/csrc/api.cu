@@ -708,9 +708,11 @@ int pkd_append_kv_layers(int32_t layers, const void* const* k_new, const void* c
 int pkd_append_latent(const void* latent_new, int64_t latent_stride, const void* rope_new,
                       int64_t rope_stride, const int32_t* batch_indices, const int32_t* positions,
                       int32_t n, const int32_t* indptr, const int32_t* indices,
-                      const int32_t* last_page_len, int32_t batch, void* cache, int32_t num_pages,
-                      int32_t page_size, int32_t* err, void* stream) {
-  if (n < 0 || batch < 0 || num_pages < 1 || page_size < 1) return PKD_E_INVALID_ARG;
+                      int32_t num_indices, const int32_t* last_page_len, int32_t batch,
+                      void* cache, int32_t num_pages, int32_t page_size, int32_t* err,
+                      void* stream) {
+  if (n < 0 || batch < 0 || num_indices < 0 || num_pages < 1 || page_size < 1)
+    return PKD_E_INVALID_ARG;
   if (n == 0) return PKD_OK;
   if (!latent_new || !rope_new || !batch_indices || !positions || !indptr || !indices ||
       !last_page_len || !cache)
@@ -723,7 +725,7 @@ int pkd_append_latent(const void* latent_new, int64_t latent_stride, const void*
     return PKD_E_INVALID_ARG;
   if (launch_latent_append(latent_new, n > 1 ? latent_stride * 2 : 0, rope_new,
                            n > 1 ? rope_stride * 2 : 0, batch_indices, positions, n, indptr,
-                           indices, last_page_len, batch, cache, num_pages, page_size, err,
+                           indices, num_indices, last_page_len, batch, cache, num_pages, page_size, err,
                            static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return PKD_E_CUDA;
   return PKD_OK;
@@ -812,8 +814,8 @@ size_t pkd_evict_workspace_bytes(int32_t layers, int32_t batch, int32_t max_len,
 
 int pkd_evict_kv(int32_t layers, void* const* kv, float* const* weights,
                  int32_t* const* positions, const int32_t* indptr, const int32_t* indices,
-                 const int32_t* last_page_len, const int32_t* seen, int32_t batch,
-                 int32_t max_len, int32_t budget, int32_t sinks, int32_t recent, int32_t per_head,
+                 int32_t num_indices, const int32_t* last_page_len, const int32_t* seen,
+                 int32_t batch, int32_t max_len, int32_t budget, int32_t sinks, int32_t recent, int32_t per_head,
                  int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
                  uint32_t flags, void* d_workspace, size_t workspace_bytes, int32_t* err,
                  void* stream) {
@@ -821,7 +823,7 @@ int pkd_evict_kv(int32_t layers, void* const* kv, float* const* weights,
   const int st = check_evict(layers, batch, max_len, budget, per_head, num_kv_heads);
   if (st != PKD_OK) return st;
   const int elem = (flags & PKD_FLAG_KV_FP8) ? 1 : 2;
-  if (!kv || !weights || !positions || sinks < 0 || recent < 0 ||
+  if (!kv || !weights || !positions || num_indices < 0 || sinks < 0 || recent < 0 ||
       (int64_t)sinks + recent > budget || num_pages < 1 || page_size < 1 || head_dim < 1 ||
       ((int64_t)head_dim * elem) % 16 != 0 || (int64_t)head_dim * elem > 16384 ||
       (int64_t)head_dim * elem * num_kv_heads > 32768)
@@ -851,6 +853,7 @@ int pkd_evict_kv(int32_t layers, void* const* kv, float* const* weights,
   a.err = err;
   a.layers = layers;
   a.batch = batch;
+  a.num_indices = num_indices;
   a.num_pages = num_pages;
   a.page_size = page_size;
   a.hkv = num_kv_heads;

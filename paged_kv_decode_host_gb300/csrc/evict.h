@@ -35,7 +35,7 @@ constexpr int kEvictMaxTokens = 8 * kEvictBlockTokens;
 struct EvictArgs {
   const int32_t *indptr, *indices, *last, *seen;
   int32_t* err;
-  int32_t layers, batch, num_pages, page_size, hkv;
+  int32_t layers, batch, num_indices, num_pages, page_size, hkv;
   int32_t budget, sinks, recent, per_head;
   int32_t max_len;
   int64_t page_bytes, token_bytes, head_bytes;   // strides in the cache

@@ -154,7 +154,8 @@ __device__ __forceinline__ bool job_of(const EvictArgs& a, int job, bool tell, J
   j->layer = job / a.batch;
   const int p0 = a.indptr[j->req], p1 = a.indptr[j->req + 1], last = a.last[j->req];
   const int64_t len = p1 > p0 ? (int64_t)a.page_size * (p1 - p0 - 1) + last : 0;
-  const bool wrong = p0 < 0 || p1 <= p0 || last < 1 || last > a.page_size || len > a.max_len;
+  const bool wrong = p0 < 0 || p1 <= p0 || p1 > a.num_indices || last < 1 ||
+                     last > a.page_size || len > a.max_len;
   if (wrong && tell && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
   j->n = (int)len;
   j->pages = a.indices + p0;

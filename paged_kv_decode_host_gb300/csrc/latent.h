@@ -56,8 +56,8 @@ cudaError_t encode_latent_q_map(const void* q, int32_t batch, int32_t heads, CUt
 cudaError_t launch_latent_append(const void* latent, int64_t latent_stride, const void* rope,
                                  int64_t rope_stride, const int32_t* batch_indices,
                                  const int32_t* positions, int32_t n, const int32_t* indptr,
-                                 const int32_t* indices, const int32_t* last_page_len,
-                                 int32_t batch, void* cache, int32_t num_pages, int32_t page_size,
+                                 const int32_t* indices, int32_t num_indices,
+                                 const int32_t* last_page_len, int32_t batch, void* cache, int32_t num_pages, int32_t page_size,
                                  int32_t* err, cudaStream_t stream);
 
 }  // namespace pkd

@@ -919,8 +919,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(
     const uint8_t* __restrict__ latent, int64_t latent_stride, const uint8_t* __restrict__ rope,
     int64_t rope_stride, const int32_t* __restrict__ batch_indices,
     const int32_t* __restrict__ positions, int32_t n, const int32_t* __restrict__ indptr,
-    const int32_t* __restrict__ indices, const int32_t* __restrict__ last_page_len, int32_t batch,
-    uint8_t* __restrict__ cache, int32_t num_pages, int32_t page_size, int32_t* err) {
+    const int32_t* __restrict__ indices, int32_t num_indices,
+    const int32_t* __restrict__ last_page_len, int32_t batch, uint8_t* __restrict__ cache, int32_t num_pages, int32_t page_size, int32_t* err) {
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   if (i >= n) return;
@@ -937,7 +937,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(
   if (b >= 0 && b < batch) {
     const int p0 = indptr[b], p1 = indptr[b + 1], last = last_page_len[b];
     const int64_t len = (int64_t)page_size * (p1 - p0 - 1) + last;
-    if (p1 > p0 && last >= 1 && last <= page_size && pos >= 0 && pos < len) {
+    if (p0 >= 0 && p1 > p0 && p1 <= num_indices && last >= 1 && last <= page_size && pos >= 0 &&
+        pos < len) {
       const int pg = indices[p0 + pos / page_size];
       if (pg >= 0 && pg < num_pages) {
         page = pg;
@@ -1055,13 +1056,13 @@ cudaError_t encode_latent_q_map(const void* q, int32_t batch, int32_t heads, CUt
 cudaError_t launch_latent_append(const void* latent, int64_t latent_stride, const void* rope,
                                  int64_t rope_stride, const int32_t* batch_indices,
                                  const int32_t* positions, int32_t n, const int32_t* indptr,
-                                 const int32_t* indices, const int32_t* last_page_len,
-                                 int32_t batch, void* cache, int32_t num_pages, int32_t page_size,
+                                 const int32_t* indices, int32_t num_indices,
+                                 const int32_t* last_page_len, int32_t batch, void* cache, int32_t num_pages, int32_t page_size,
                                  int32_t* err, cudaStream_t stream) {
   const int64_t blocks = ((int64_t)n + kAppendWarps - 1) / kAppendWarps;
   latent_append_kernel<<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(
       static_cast<const uint8_t*>(latent), latent_stride, static_cast<const uint8_t*>(rope),
-      rope_stride, batch_indices, positions, n, indptr, indices, last_page_len, batch,
+      rope_stride, batch_indices, positions, n, indptr, indices, num_indices, last_page_len, batch,
       static_cast<uint8_t*>(cache), num_pages, page_size, err);
   return cudaGetLastError();
 }

@@ -193,12 +193,12 @@ typedef int (*accumulate_fn)(void *ctx, const void *q, const void *kv, const flo
 typedef int (*append_latent_fn)(const void *latent, int64_t latent_stride, const void *rope,
                                 int64_t rope_stride, const int32_t *batch_indices,
                                 const int32_t *positions, int32_t n, const int32_t *indptr,
-                                const int32_t *indices, const int32_t *last, int32_t batch,
-                                void *cache, int32_t num_pages, int32_t page_size, int32_t *err,
+                                const int32_t *indices, int32_t num_indices, const int32_t *last,
+                                int32_t batch, void *cache, int32_t num_pages, int32_t page_size, int32_t *err,
                                 void *stream);
 typedef int (*evict_fn)(int32_t layers, void *const *kv, float *const *weights,
                         int32_t *const *positions, const int32_t *indptr, const int32_t *indices,
-                        const int32_t *last, const int32_t *seen, int32_t batch, int32_t max_len,
+                        int32_t num_indices, const int32_t *last, const int32_t *seen, int32_t batch, int32_t max_len,
                         int32_t budget, int32_t sinks, int32_t recent, int32_t per_head,
                         int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
                         int32_t head_dim, uint32_t flags, void *workspace, size_t workspace_bytes,
@@ -236,15 +236,15 @@ static PyObject *accumulate(PyObject *self, PyObject *args) {
 static PyObject *append_latent(PyObject *self, PyObject *args) {
   unsigned long long lat, rope, bi, pos, ip, ix, la, cache, err, stream;
   long long ls, rs;
-  int n, batch, pages, page;
+  int n, nnz, batch, pages, page;
   (void)self;
-  if (!PyArg_ParseTuple(args, "KLKLKKiKKKiKiiKK", &lat, &ls, &rope, &rs, &bi, &pos, &n, &ip, &ix,
-                        &la, &batch, &cache, &pages, &page, &err, &stream))
+  if (!PyArg_ParseTuple(args, "KLKLKKiKKiKiKiiKK", &lat, &ls, &rope, &rs, &bi, &pos, &n, &ip, &ix,
+                        &nnz, &la, &batch, &cache, &pages, &page, &err, &stream))
     return NULL;
   if (g_append_latent == NULL) return PyLong_FromLong(NOT_HANDLED);
   return PyLong_FromLong(g_append_latent(
       ADDR(lat), (int64_t)ls, ADDR(rope), (int64_t)rs, (const int32_t *)ADDR(bi),
-      (const int32_t *)ADDR(pos), n, (const int32_t *)ADDR(ip), (const int32_t *)ADDR(ix),
+      (const int32_t *)ADDR(pos), n, (const int32_t *)ADDR(ip), (const int32_t *)ADDR(ix), nnz,
       (const int32_t *)ADDR(la), batch, ADDR(cache), pages, page, (int32_t *)ADDR(err),
       ADDR(stream)));
 }
@@ -267,11 +267,11 @@ static int addresses(PyObject *list, Py_ssize_t n, void **out) {
 static PyObject *evict(PyObject *self, PyObject *args) {
   PyObject *kv, *w, *p;
   unsigned long long ip, ix, la, seen, ws, err, stream, ws_bytes;
-  int batch, max_len, budget, sinks, recent, per_head, pages, page, hkv, dim;
+  int nnz, batch, max_len, budget, sinks, recent, per_head, pages, page, hkv, dim;
   unsigned int flags;
   void *kvs[MAX_LAYERS], *ws_[MAX_LAYERS], *ps[MAX_LAYERS];
   (void)self;
-  if (!PyArg_ParseTuple(args, "OOOKKKKiiiiiiiiiiIKKKK", &kv, &w, &p, &ip, &ix, &la, &seen, &batch,
+  if (!PyArg_ParseTuple(args, "OOOKKiKKiiiiiiiiiiIKKKK", &kv, &w, &p, &ip, &ix, &nnz, &la, &seen, &batch,
                         &max_len, &budget, &sinks, &recent, &per_head, &pages, &page, &hkv, &dim,
                         &flags, &ws, &ws_bytes, &err, &stream))
     return NULL;
@@ -281,7 +281,7 @@ static PyObject *evict(PyObject *self, PyObject *args) {
     return PyLong_FromLong(NOT_HANDLED);
   return PyLong_FromLong(g_evict(
       (int32_t)layers, kvs, (float *const *)ws_, (int32_t *const *)ps, (const int32_t *)ADDR(ip),
-      (const int32_t *)ADDR(ix), (const int32_t *)ADDR(la), (const int32_t *)ADDR(seen), batch,
+      (const int32_t *)ADDR(ix), nnz, (const int32_t *)ADDR(la), (const int32_t *)ADDR(seen), batch,
       max_len, budget, sinks, recent, per_head, pages, page, hkv, dim, (uint32_t)flags, ADDR(ws),
       (size_t)ws_bytes, (int32_t *)ADDR(err), ADDR(stream)));
 }

@@ -170,7 +170,8 @@ def evict_reference(kvs, weights, positions, t, lens, seen, budget, page, layout
             for h in range(heads if per_head else 1):
                 x = w[pg, h, sl].astype(np.float64)
                 for k in range(1, 1 if per_head else heads):
-                    x = x + w[pg, k, sl].astype(np.float64)
+                    with np.errstate(invalid="ignore"):   # inf - inf: a NaN weight
+                        x = x + w[pg, k, sl].astype(np.float64)
                 x = x.astype(np.float32).astype(np.float64)
                 nan = np.isnan(x)
                 x[nan] = -np.inf
@@ -316,6 +317,87 @@ def test_evict_refusals():
         pkd.evict_kv([kv, kv], [w, w.clone()], [p, p.clone()], *d, 40, max_len=100)
     with pytest.raises(ValueError):
         pkd.evict_kv([kv], [w], [p.float()], *d, 40, max_len=100)
+
+
+@gpu
+def test_evict_indices_shorter_than_the_table():
+    lens, budget = [100, 80], 40
+    t, kvs, ws, ps, seen = evict_case(2, 16, lens, budget, seed=6)
+    want = [[x.copy() for x in y] for y in (kvs, ws, ps)]
+    got = run_evict((t[0], t[1][:9], t[2]), kvs, ws, ps, seen, budget, torch.bfloat16, max_len=100)
+    evict_reference(*want, t, [100, 0], seen, budget, 16, "NHD", 0, 0, True)
+    same(got, want)
+    assert got[3] == pkd.DEV_ERR_BOUNDS
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """A pool of 5 GB whose last pages hold the requests."""
+    page, hkv, pages, lens, budget = 16, 8, 80_000, [100, 700], 60
+    kv = torch.empty(kv_shape(pages, page, hkv, "NHD"), dtype=torch.bfloat16, device="cuda")
+    assert kv.numel() * 2 > 1 << 32
+    counts = [7, 44]
+    indptr = np.array([0, 7, 51], np.int32)
+    ids = (pages - 1 - np.random.default_rng(0).permutation(51)).astype(np.int32)
+    last = np.array([4, 12], np.int32)
+    at = torch.from_numpy(ids).long().cuda()
+    kv[at] = torch.randn(51, 2, page, hkv, D, device="cuda").bfloat16()
+    w = torch.zeros(pages, hkv, page, device="cuda")
+    p = torch.zeros(pages, hkv, page, dtype=torch.int32, device="cuda")
+    dec = pkd.BatchDecodeWithPagedKVCache(hkv, hkv, D, page, max_batch=2, max_num_pages=51, num_pages=pages)
+    dec.plan(indptr, ids, last)
+    q = torch.randn(2, hkv, D, device="cuda").bfloat16()
+    _, lse = dec.run(q, kv)
+    d = [torch.from_numpy(x).cuda() for x in (indptr, ids, last)]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    dec.accumulate_weights(q, kv, lse, w, positions=p, new_tokens=n, seen=n)
+    for i in range(2):
+        k = keys_of(kv, "NHD", at[indptr[i]:indptr[i + 1]])[:lens[i]]
+        x = torch.einsum("hd,thd->ht", q[i].double(), k) / math.sqrt(D)
+        got = w[at[indptr[i]:indptr[i + 1]]].transpose(0, 1).reshape(hkv, -1)[:, :lens[i]]
+        near(got, torch.exp(x - lse[i].double()[:, None]))
+    raw = kv[at].view(torch.int16).cpu().numpy()
+    small = [[raw], [w[at].cpu().numpy()], [p[at].cpu().numpy()]]
+    pkd.evict_kv([kv], [w], [p], *d, n, budget, max_len=700, sinks=2, recent=10)
+    local = (indptr, np.arange(51, dtype=np.int32), last)
+    evict_reference(*small, local, lens, lens, budget, page, "NHD", 2, 10, True)
+    same(([kv[at].view(torch.int16).cpu().numpy()], [w[at].cpu().numpy()], [p[at].cpu().numpy()]), small)
+
+
+@gpu
+@pytest.mark.parametrize("n,budget", [(300, 295), (3000, 1500)])
+def test_accumulate_and_evict_in_a_graph(n, budget):
+    """Captured once, replayed on new inputs, against eager calls; on two streams at once."""
+    def state(seed):
+        s = Step(2, 4, [n, 40], 16, seed=seed)
+        s.pos = torch.full(s.per_slot, -1, dtype=torch.int32, device="cuda")
+        at = np.arange(n)
+        s.pos[s.t[1][s.t[0][0] + at // 16], :, at % 16] = torch.arange(n, dtype=torch.int32, device="cuda")[:, None]
+        s.d = [torch.from_numpy(x).cuda() for x in s.t[:3]]
+        s.seen = torch.tensor([n, 40], dtype=torch.int32, device="cuda")
+        s.new = torch.ones(2, dtype=torch.int32, device="cuda")
+        return s
+
+    def step(s, **kw):
+        s.dec.accumulate_weights(s.q, s.kv, s.lse, s.weights, positions=s.pos, new_tokens=s.new, seen=s.seen)
+        pkd.evict_kv([s.kv], [s.weights], [s.pos], *s.d, s.seen, budget, max_len=n, sinks=2, recent=20)
+
+    a, b, c = state(1), state(1), state(1)
+    step(b)                                  # warms up, too
+    g = torch.cuda.CUDAGraph()
+    keep = [x.clone() for x in (a.kv, a.weights, a.pos)]
+    with torch.cuda.graph(g):
+        step(a)
+    for x, y in zip((a.kv, a.weights, a.pos), keep):
+        x.copy_(y)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    g.replay()
+    with torch.cuda.stream(other):
+        step(c)
+    torch.cuda.synchronize()
+    for x in (a, c):
+        assert torch.equal(x.kv, b.kv) and torch.equal(x.weights, b.weights) and torch.equal(x.pos, b.pos)
 
 
 def test_evicted_table():

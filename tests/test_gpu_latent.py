@@ -194,6 +194,11 @@ def test_append_skips_and_flags():
     assert err.item() == pkd.DEV_ERR_BOUNDS
     assert int((cache != 0).any(-1).sum()) == 2
     assert cache[int(t[1][1]), 3].all() and cache[int(t[1][2]), 4].all()
+    err.zero_()
+    short = d[1][:2].clone()   # request 1's page is past the indices' end
+    pkd.append_latent(new[2:4, :512], new[2:4, 512:], rows[2:4], at[2:4], d[0], short, d[2],
+                      torch.zeros_like(cache), err=err)
+    assert err.item() == pkd.DEV_ERR_BOUNDS
     pkd.append_latent(new[:0, :512], new[:0, 512:], rows[:0], at[:0], *d, cache)
 
 
@@ -226,6 +231,117 @@ def test_other_stream_and_refusals():
     with pytest.raises(ValueError):
         pkd.append_latent(q[0, :, :512].t(), q[0, :, 512:], *[torch.zeros(16, device="cuda").int()] * 4,
                           torch.zeros(15, device="cuda").int(), cache)
+
+
+@gpu
+def test_graph_follows_later_plans():
+    """A step captured while no request was split replays under a plan that splits them, and back."""
+    page, heads = 16, 40
+    lens_a, lens_b = [100, 50, 7], [3000, 900, 5000]
+    t = table(lens_b, page, 11)
+    cache = torch.randn(t[3], page, ROW, device="cuda").bfloat16()
+    q = torch.randn(3, heads, ROW, device="cuda").bfloat16()
+    out = torch.zeros(3, heads, DIM, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(3, heads, device="cuda")
+    dec = pkd.BatchLatentDecodeWithPagedCache(heads, DIM, 64, page, scale=SCALE, max_batch=4,
+                                              max_num_pages=len(t[1]), num_pages=t[3])
+
+    def tables(lens):
+        counts = [-(-n // page) for n in lens]
+        indptr = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        ids = np.concatenate([t[1][t[0][i]:t[0][i] + c] for i, c in enumerate(counts)])
+        return indptr, ids, np.array([n - page * (c - 1) for n, c in zip(lens, counts)], np.int32)
+
+    dec.plan(*tables(lens_a))
+    assert dec.plan_info()["num_units"] == 0
+    graph = dec.capture([q], [cache], [out], [lse])
+    for lens in (lens_a, lens_b, lens_a):
+        dec.plan(*tables(lens))
+        graph.launch()
+        close((out, lse), reference(q, cache, lens, tables(lens), page), cache.abs().max().double())
+    assert dec.device_error() == 0
+    dec.plan(*[x[:k] for x, k in zip(tables(lens_a), (3, 99, 2))])
+    with pytest.raises(pkd.PkdError, match="STALE"):   # the queries' map is of three requests
+        graph.launch()
+
+
+@gpu
+def test_capture_with_host_buffers_and_torch_graph():
+    lens, page, heads = [70, 300], 16, 16
+    t, q, cache, dec = make(heads, lens, page, seed=12)
+    dec.plan(*t[:3])
+    ref = reference(q, cache, lens, t, page)
+    top = cache.abs().max().double()
+    out, lse = torch.empty(2, heads, DIM, dtype=torch.bfloat16, device="cuda"), torch.empty(2, heads, device="cuda")
+    hq, ho, hl = q.cpu().pin_memory(), out.cpu().pin_memory(), lse.cpu().pin_memory()
+    qd = torch.zeros_like(q)
+    graph = dec.capture([qd], [cache], [out], [lse], host_qs=[hq], host_outs=[ho], host_lses=[hl])
+    graph.launch()
+    torch.cuda.synchronize()
+    close((ho.cuda(), hl.cuda()), ref, top)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = dec.run(q, cache)
+    g.replay()
+    close(got, ref, top)
+
+
+@gpu
+def test_epoch_on_another_stream_and_empty_batch():
+    lens, page = [500, 33], 16
+    t, q, cache, dec = make(32, lens, page, seed=13)
+    upload = torch.cuda.Stream()
+    for _ in range(3):
+        epoch = dec.plan(*t[:3], stream=upload)
+        got = dec.run(q, cache, expect_epoch=epoch)   # waits for the schedule on the device
+    close(got, reference(q, cache, lens, t, page), cache.abs().max().double())
+    with pytest.raises(pkd.PkdError, match="STALE"):
+        dec.run(q, cache, expect_epoch=epoch - 1)
+    torch.cuda.synchronize()
+    dec.plan(np.zeros(1, np.int32), np.zeros(0, np.int32), np.zeros(0, np.int32))
+    out, lse = dec.run(q[:0], cache)
+    assert out.shape == (0, 32, DIM) and lse.shape == (0, 32) and dec.device_error() == 0
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """A pool of 5 GB whose last pages hold the request, appended there and read back."""
+    page, pages, heads, n = 64, 70_000, 16, 200
+    cache = torch.empty(pages, page, ROW, dtype=torch.bfloat16, device="cuda")
+    assert cache.numel() * 2 > 1 << 32
+    ids = np.array([pages - 1, pages - 3, pages - 2, pages - 4], np.int32)
+    t = (np.array([0, 4], np.int32), ids, np.array([n - 192], np.int32))
+    rows = torch.randn(n, ROW, device="cuda").bfloat16()
+    pkd.append_latent(rows[:, :512], rows[:, 512:], torch.zeros(n, device="cuda").int(),
+                      torch.arange(n, device="cuda").int(), *[torch.from_numpy(x).cuda() for x in t], cache)
+    assert torch.equal(cache[torch.from_numpy(ids).long().cuda()].reshape(-1, ROW)[:n], rows)
+    dec = pkd.BatchLatentDecodeWithPagedCache(heads, DIM, 64, page, scale=SCALE, max_batch=1,
+                                              max_num_pages=4, num_pages=pages)
+    dec.plan(*t)
+    q = torch.randn(1, heads, ROW, device="cuda").bfloat16()
+    close(dec.run(q, cache), reference(q, cache, [n], t, page), rows.abs().max().double())
+
+
+@gpu
+def test_two_contexts_at_once():
+    """Two contexts on two streams over one cache, many times over."""
+    lens, page = [2000, 100, 5000], 16
+    t, q, cache, a = make(64, lens, page, seed=14)
+    b = pkd.BatchLatentDecodeWithPagedCache(64, DIM, 64, page, scale=SCALE, max_batch=3,
+                                            max_num_pages=len(t[1]), num_pages=t[3], num_ctas=50)
+    ref = reference(q, cache, lens, t, page)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a.plan(*t[:3])
+    with torch.cuda.stream(s):
+        b.plan(*t[:3])
+    for _ in range(20):
+        x = a.run(q, cache)
+        with torch.cuda.stream(s):
+            y = b.run(q, cache)
+    torch.cuda.synchronize()
+    for got in (x, y):
+        close(got, ref, cache.abs().max().double())
 
 
 @pytest.mark.parametrize("heads", [16, 64, 128])
