@@ -40,6 +40,7 @@ struct pkd_ctx {
   size_t next_map = 0;
   int merge_grid = 0;
   int device = 0;
+  int sms = 1;   // of that device
   Layout layout{};
   uint8_t* ws = nullptr;
   size_t ws_bytes = 0;
@@ -463,6 +464,10 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
     return PKD_E_WORKSPACE_TOO_SMALL;
   }
   cudaGetDevice(&ctx->device);
+  if (cudaDeviceGetAttribute(&ctx->sms, cudaDevAttrMultiProcessorCount, ctx->device) != cudaSuccess) {
+    delete ctx;
+    return PKD_E_CUDA;
+  }
   ctx->merge_grid = merge_grid_for(ctx->n_cta);
   ctx->ws = static_cast<uint8_t*>(d_workspace);
   ctx->ws_bytes = workspace_bytes;
@@ -531,7 +536,8 @@ static int plan_and_publish(pkd_ctx* ctx, PlanFn plan_fn, void* stream, uint64_t
   // sees the whole schedule
   words[H_EPOCH] = epoch_word(ctx->epoch + 1);
   if (cudaMemcpyAsync(ctx->ws + (size_t)H_WORDS * 4, words + H_WORDS,
-                      ((size_t)L.page_list + (size_t)info.nnz + (size_t)info.batch - H_WORDS) * 4,
+                      ((size_t)request_words(L, info.nnz) +
+                       (size_t)kRequestWords * ((size_t)info.batch + 1) - H_WORDS) * 4,
                       cudaMemcpyHostToDevice, s) != cudaSuccess ||
       cudaMemcpyAsync(ctx->ws, words, (size_t)H_WORDS * 4, cudaMemcpyHostToDevice, s) !=
           cudaSuccess)
@@ -775,8 +781,6 @@ int pkd_accumulate_weights(pkd_ctx* ctx, const void* q, const void* kv, const fl
   a.positions = positions;
   a.new_tokens = new_tokens;
   a.seen = seen;
-  a.off_cta = ctx->layout.cta_indptr;
-  a.off_items = ctx->layout.items;
   a.off_pages = ctx->layout.page_list;
   const int64_t head = (int64_t)kHeadDim * elem;
   a.page_bytes = 2 * (int64_t)c.page_size * c.num_kv_heads * head;
@@ -785,10 +789,11 @@ int pkd_accumulate_weights(pkd_ctx* ctx, const void* q, const void* kv, const fl
   a.hq = c.num_qo_heads;
   a.hkv = c.num_kv_heads;
   a.page_size = c.page_size;
+  a.page_shift = page_shift_of(c.page_size);
   a.num_pages = c.num_pages;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kHeadDim) * (double)k_scale);
   a.wait_epoch = expect_epoch != 0 ? epoch_word(expect_epoch) : 0;
-  return launch_weights(a, ctx->kind.fp8, ctx->n_cta, static_cast<cudaStream_t>(stream)) ==
+  return launch_weights(a, ctx->kind.fp8, ctx->sms, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? PKD_OK
              : PKD_E_CUDA;

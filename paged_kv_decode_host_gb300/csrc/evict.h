@@ -19,13 +19,20 @@ struct WeightsArgs {
   int32_t* positions;         // int32 [num_pages][Hkv][P] or null
   const int32_t* new_tokens;  // [batch] or null
   const int32_t* seen;        // [batch] (with positions)
-  int64_t off_cta, off_items, off_pages;
+  int64_t off_pages;
   int64_t page_bytes, token_bytes, head_bytes;   // strides of K in the cache
-  int32_t hq, hkv, page_size, num_pages;
+  int32_t hq, hkv, page_size, page_shift, num_pages;   // page_shift: log2 of the size, or -1
   float scale_log2;
   int32_t wait_epoch;
 };
 cudaError_t launch_weights(const WeightsArgs& a, bool fp8, int grid, cudaStream_t stream);
+
+// log2 of a page size, -1 when it is no power of two
+inline int32_t page_shift_of(int32_t page_size) {
+  for (int32_t k = 0; k < 31; ++k)
+    if (page_size == 1 << k) return k;
+  return -1;
+}
 
 constexpr int kMaxEvictLayers = 128;
 // Longest request of an eviction: its keys lie in the shared memory of a

@@ -601,9 +601,7 @@ size_t evict_workspace_bytes(int layers, int batch, int hkv, int per_head, int m
 cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
   const EvictPlan p = plan_for(a.layers, a.batch, a.hkv, a.per_head, a.max_len, a.budget);
   a.splits = p.splits;
-  a.page_shift = -1;
-  for (int k = 0; k < 31; ++k)
-    if (a.page_size == 1 << k) a.page_shift = k;
+  a.page_shift = page_shift_of(a.page_size);
   if (!p.split) {
     if (p.cluster) return launch_choose<512, true, true>(a, p, stream);
     if (p.threads == 128) return launch_choose<128, false, true>(a, p, stream);

@@ -107,7 +107,7 @@ struct Layout {
   int64_t units;         // [max_items][2]
   int64_t merge_indptr;  // [max_items + 1]
   int64_t page_list;     // [max_num_pages]
-  int64_t words;         // schedule words (end of page_list and the lengths behind it)
+  int64_t words;         // schedule words (end of page_list and the requests behind it)
   int64_t max_items;
   int64_t max_slots;     // partial-state slots
   // byte offsets inside the device workspace
@@ -118,6 +118,15 @@ struct Layout {
 };
 
 inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+// Behind the page list's nnz words (rounded up to 4), plain plans hold an
+// entry per request, and one more with the total: 16-token tiles of the
+// requests before, index of the first page in the page list, tokens, 0.
+constexpr int kRequestWords = 4, kRequestTile = 16;
+__host__ __device__ inline int64_t request_words(int64_t page_list, int64_t nnz) {
+  return page_list + (nnz + 3) / 4 * 4;
+}
+inline int64_t request_words(const Layout& L, int64_t nnz) { return request_words(L.page_list, nnz); }
 
 // Upper bound on work items of one plan: a split request of length l gives
 // ceil(l / c) <= l / c + 1 chunks and every chunk candidate is at least
@@ -163,8 +172,8 @@ inline Layout make_layout(const pkd_config& c, int64_t n_cta) {
   L.units = L.items + L.max_items * kItemWords;
   L.merge_indptr = L.units + L.max_items * 2;
   L.page_list = align_up(L.merge_indptr + L.max_items + 1, 4);
-  // behind the page list: plain plans' request lengths, from word nnz on
-  L.words = L.page_list + c.max_num_pages + c.max_batch;
+  // behind the page list: plain plans' requests (RequestEntry)
+  L.words = request_words(L, c.max_num_pages) + (int64_t)kRequestWords * (c.max_batch + 1);
   size_t sched_bytes = (size_t)L.words * 4;
   L.err_byte = (size_t)align_up((int64_t)sched_bytes, 256);
   L.o_part_byte = L.err_byte + 256;

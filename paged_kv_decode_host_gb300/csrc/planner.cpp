@@ -173,6 +173,21 @@ int64_t lpt(const std::vector<Item>& items, int32_t n_cta, std::vector<int32_t>*
   return makespan;
 }
 
+// The requests' entries behind the page list.
+void write_requests(int32_t* words, const Layout& L, int64_t nnz, const std::vector<int64_t>& lens,
+                    const int32_t* indptr) {
+  int32_t* w = words + request_words(L, nnz);
+  int64_t tiles = 0;
+  for (size_t i = 0; i <= lens.size(); ++i, w += kRequestWords) {
+    const bool end = i == lens.size();
+    w[0] = (int32_t)std::min<int64_t>(tiles, 0x7fffffff);
+    w[1] = end ? 0 : indptr[i];
+    w[2] = end ? 0 : (int32_t)lens[i];
+    w[3] = 0;
+    if (!end) tiles += ceil_div(lens[i], kRequestTile);
+  }
+}
+
 struct Block {
   int32_t req_first, n_req, table_row;
 };
@@ -255,9 +270,8 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     // page ids go into the schedule verbatim (the kernel reads a table row's
     // pages at indptr[row] + t / P), range-checked in the same pass
     if (!copy_checked(indices, words + L.page_list, nnz, cfg.num_pages)) return PKD_E_BAD_TABLE;
-    if (!group_indptr)   // the requests' lengths, for kernels that ask where a request ends
-      for (int32_t i = 0; i < n_rows; ++i) words[L.page_list + nnz + i] = (int32_t)row_len[i];
   }
+  if (!group_indptr) write_requests(words, L, nnz, row_len, indptr);
 
   // ---- row blocks
   std::vector<Block>& blocks = sc.blocks;
@@ -519,8 +533,8 @@ int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     if (nnz > cfg.max_num_pages) return PKD_E_CAPACITY;
     if (indices == nullptr) return PKD_E_INVALID_ARG;
     if (!copy_checked(indices, words + L.page_list, nnz, cfg.num_pages)) return PKD_E_BAD_TABLE;
-    for (int32_t i = 0; i < batch; ++i) words[L.page_list + nnz + i] = (int32_t)lens[i];
   }
+  write_requests(words, L, nnz, lens, indptr);
   const int32_t blocks = latent_blocks(cfg.num_qo_heads);
   const int32_t nv = std::max(1, n_cta / blocks);
   const int64_t alpha = cfg.alpha < 0 ? kLatentAlpha : cfg.alpha;
