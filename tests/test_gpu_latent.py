@@ -203,6 +203,32 @@ def test_append_skips_and_flags():
 
 
 @gpu
+@pytest.mark.parametrize("n", [1, 3, 31, 2431, 2432, 2433, 6003])
+def test_append_many(n):
+    """Tokens of several requests in any order, some outside the table."""
+    page, lens = 16, [3000, 1, 4100]
+    t = table(lens, page, n)
+    d = [torch.from_numpy(x).cuda() for x in t[:3]]
+    gen = np.random.default_rng(n)
+    every = [(b, p) for b, m in enumerate(lens) for p in range(m)]
+    pick = gen.permutation(len(every))[:n]
+    rows = np.array([every[k][0] for k in pick], np.int32)
+    at = np.array([every[k][1] for k in pick], np.int32)
+    out = gen.random(n) < 0.1
+    rows[out], at[out] = gen.integers(-2, 5, out.sum()), 5000   # past every request's end
+    both = torch.randn(n, 584, device="cuda").bfloat16()
+    cache = torch.randn(t[3], page, ROW, device="cuda").bfloat16()
+    want = cache.clone()
+    for i in np.nonzero(~out)[0]:
+        want[int(t[1][t[0][rows[i]] + at[i] // page]), int(at[i] % page)] = both[i, 8:584]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkd.append_latent(both[:, 8:520], both[:, 520:584], torch.from_numpy(rows).cuda(),
+                      torch.from_numpy(at).cuda(), *d, cache, err=err)
+    assert torch.equal(cache, want)
+    assert err.item() == (pkd.DEV_ERR_BOUNDS if out.any() else 0)
+
+
+@gpu
 def test_other_stream_and_refusals():
     lens = [100]
     t, q, cache, dec = make(16, lens, 16, seed=8)
