@@ -351,7 +351,8 @@ def _fast():
                    ctypes.cast(lib.pkd_plan_cascade, ctypes.c_void_p).value,
                    ctypes.cast(lib.pkd_run_scaled, ctypes.c_void_p).value)
             m.init_ops(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-                lib.pkd_accumulate_weights, lib.pkd_append_latent, lib.pkd_evict_kv)])
+                lib.pkd_accumulate_weights, lib.pkd_append_latent, lib.pkd_evict_kv,
+                lib.pkd_evict_workspace_bytes)])
             _fast_plan = m
         except ImportError:
             _fast_plan = False
@@ -1155,13 +1156,14 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
                                  f"cuda:{dev}")
     batch = _table_args(dev, indptr, indices, last_page_len, seen=seen)
     per_head = 1 if per_head else 0
-    for name, v in (("max_len", max_len), ("budget", budget), ("sinks", sinks), ("recent", recent)):
-        if not -2**31 <= v < 2**31:
-            raise OverflowError(f"{name} must fit 32 bits")
     lib, fast = load(), _fast()
+    if fast is None:
+        for v in (max_len, budget, sinks, recent):
+            if not -2**31 <= v < 2**31:
+                raise OverflowError("max_len, budget, sinks and recent must fit 32 bits")
     with _On(dev):
         # (sizes out of range: 0 here, refused in the call itself)
-        need = 0 if max_len <= budget else lib.pkd_evict_workspace_bytes(
+        need = (lib.pkd_evict_workspace_bytes if fast is None else fast.evict_bytes)(
             layers, batch, max_len, budget, per_head, hkv)
         ws = torch.empty(need, dtype=torch.uint8, device=c0.device) if need else None
         if need and stream is not None:

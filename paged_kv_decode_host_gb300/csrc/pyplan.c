@@ -203,14 +203,18 @@ typedef int (*evict_fn)(int32_t layers, void *const *kv, float *const *weights,
                         int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
                         int32_t head_dim, uint32_t flags, void *workspace, size_t workspace_bytes,
                         int32_t *err, void *stream);
+typedef size_t (*evict_bytes_fn)(int32_t layers, int32_t batch, int32_t max_len, int32_t budget,
+                                 int32_t per_head, int32_t num_kv_heads);
+static evict_bytes_fn g_evict_bytes = NULL;
 static accumulate_fn g_accumulate = NULL;
 static append_latent_fn g_append_latent = NULL;
 static evict_fn g_evict = NULL;
 
 static PyObject *init_ops(PyObject *self, PyObject *args) {
-  unsigned long long a, b, c;
+  unsigned long long a, b, c, d;
   (void)self;
-  if (!PyArg_ParseTuple(args, "KKK", &a, &b, &c)) return NULL;
+  if (!PyArg_ParseTuple(args, "KKKK", &a, &b, &c, &d)) return NULL;
+  g_evict_bytes = (evict_bytes_fn)(uintptr_t)d;
   g_accumulate = (accumulate_fn)(uintptr_t)a;
   g_append_latent = (append_latent_fn)(uintptr_t)b;
   g_evict = (evict_fn)(uintptr_t)c;
@@ -247,6 +251,15 @@ static PyObject *append_latent(PyObject *self, PyObject *args) {
       (const int32_t *)ADDR(pos), n, (const int32_t *)ADDR(ip), (const int32_t *)ADDR(ix), nnz,
       (const int32_t *)ADDR(la), batch, ADDR(cache), pages, page, (int32_t *)ADDR(err),
       ADDR(stream)));
+}
+
+static PyObject *evict_bytes(PyObject *self, PyObject *args) {
+  int layers, batch, max_len, budget, per_head, hkv;
+  (void)self;
+  if (!PyArg_ParseTuple(args, "iiiiii", &layers, &batch, &max_len, &budget, &per_head, &hkv))
+    return NULL;
+  if (g_evict_bytes == NULL) return PyLong_FromLong(0);
+  return PyLong_FromSize_t(g_evict_bytes(layers, batch, max_len, budget, per_head, hkv));
 }
 
 #define MAX_LAYERS 128
@@ -288,7 +301,9 @@ static PyObject *evict(PyObject *self, PyObject *args) {
 
 static PyMethodDef methods[] = {
     {"init_ops", init_ops, METH_VARARGS,
-     "init_ops(accumulate_weights_address, append_latent_address, evict_address)"},
+     "init_ops(accumulate_weights_address, append_latent_address, evict_address, "
+     "evict_workspace_bytes_address)"},
+    {"evict_bytes", evict_bytes, METH_VARARGS, "pkd_evict_workspace_bytes -> bytes"},
     {"accumulate", accumulate, METH_VARARGS, "pkd_accumulate_weights -> status"},
     {"append_latent", append_latent, METH_VARARGS, "pkd_append_latent -> status"},
     {"evict", evict, METH_VARARGS, "pkd_evict_kv (lists of addresses per layer) -> status"},
