@@ -156,9 +156,8 @@ typedef struct pkd_config {
  * num_kv_heads 1, 1 <= Hq <= 128, page size a multiple of 16; no other flag.
  * Plans (pkd_plan) cut the requests' tokens, laid end to end, into equal
  * stretches, one per CTA -- per CTA pair above 64 heads, a work item covering
- * up to 64; alpha < 0 selects 128, min_chunk_tokens < 0 128 (256 above
- * 32 heads).  Graphs replay
- * with the batch they were captured with. */
+ * up to 64; alpha < 0 selects 128, min_chunk_tokens < 0 128 (256 above 32
+ * heads).  Graphs replay with the batch they were captured with. */
 #define PKD_FLAG_LATENT 1024u
 
 typedef struct pkd_ctx pkd_ctx;
@@ -408,9 +407,9 @@ int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const fl
  * its tokens' accumulated weights -- for 1 to 128 layers in one launch, each
  * with its own cache, weights and positions.
  * Per layer, request and KV head (per_head 1), or per layer and request by
- * the sum of the heads' weights, rounded to fp32 once (per_head 0; positions of
- * head 0 count), the
- * `budget` tokens of largest weight stay; tokens with position < sinks or
+ * the sum of the heads' weights (per_head 0: fp32 additions whose rounding
+ * errors are carried along, so the sum is within its last place; positions of
+ * head 0 count), the `budget` tokens of largest weight stay; tokens with position < sinks or
  * >= seen[b] - recent stay before all others (sinks + recent <= budget);
  * equal weights: the lower slot first; NaN counts as the lowest.  Slots are
  * closed up without keeping an order (attention does not depend on it): the

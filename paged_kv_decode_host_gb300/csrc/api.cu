@@ -19,6 +19,7 @@
 #include "append_layers.h"
 #include "evict.h"
 #include "pkd_internal.h"
+#include "plan_layout.h"
 
 using namespace pkd;
 
@@ -33,6 +34,7 @@ struct pkd_ctx {
   pkd_config cfg;
   int32_t n_cta = 0;
   DecodeKind kind{};   // which decode kernel (consumer, cache type, producer)
+  bool latent = false;   // a latent cache: its kernel instead
   int smem_bytes = 0;
   // page-tile maps by cache address (the map holds only the address and the
   // context's fixed shape), replaced round-robin
@@ -101,7 +103,7 @@ int check_config(const pkd_config* c) {
   if (c->max_batch < 0 || c->max_num_pages < 0 || c->num_pages < 1 || c->page_size < 1 ||
       c->num_ctas < 0)
     return PKD_E_INVALID_ARG;
-  if (c->flags & PKD_FLAG_LATENT) {
+  if (is_latent(*c)) {
     // every head reads the same rows; pages are read in 16-token tiles
     if (c->head_dim != kLatentDim || c->num_kv_heads != 1 || c->num_qo_heads < 1 ||
         c->num_qo_heads > kLatentMaxHeads || c->page_size % 16 != 0 || c->page_size > 1 << 20)
@@ -129,8 +131,7 @@ int check_config(const pkd_config* c) {
 // shape; with a null probe the check is skipped).
 DecodeKind kind_for(const pkd_config* c, const void* probe_address) {
   DecodeKind k;
-  if (c->flags & PKD_FLAG_LATENT) {
-    k.latent = true;
+  if (is_latent(*c)) {
     CUtensorMap m;
     k.tmap = probe_address == nullptr ||
              encode_latent_map(probe_address, c->num_pages, c->page_size, 0, &m) == cudaSuccess;
@@ -156,8 +157,8 @@ DecodeKind kind_for(const pkd_config* c, const void* probe_address) {
 }
 
 int resolve_ctas(const pkd_config* c, const DecodeKind& k, int32_t* n_cta, int* smem_bytes) {
-  *smem_bytes = k.latent ? latent_smem_bytes(c->num_qo_heads)
-                         : decode_smem_bytes(c->num_kv_heads, k);
+  const bool latent = is_latent(*c);
+  *smem_bytes = latent ? latent_smem_bytes(c->num_qo_heads) : decode_smem_bytes(c->num_kv_heads, k);
   if (c->num_ctas > 0) {
     *n_cta = c->num_ctas;
     return PKD_OK;
@@ -166,10 +167,10 @@ int resolve_ctas(const pkd_config* c, const DecodeKind& k, int32_t* n_cta, int* 
   if (cudaGetDevice(&dev) != cudaSuccess) return PKD_E_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PKD_E_CUDA;
-  if ((k.latent ? latent_prepare(c->num_qo_heads) : decode_prepare(k, *smem_bytes)) != cudaSuccess)
+  if ((latent ? latent_prepare(c->num_qo_heads) : decode_prepare(k, *smem_bytes)) != cudaSuccess)
     return PKD_E_CUDA;
-  if ((k.latent ? latent_occupancy(c->num_qo_heads, &per_sm)
-                : decode_occupancy(k, c->num_kv_heads, *smem_bytes, &per_sm)) != cudaSuccess)
+  if ((latent ? latent_occupancy(c->num_qo_heads, &per_sm)
+              : decode_occupancy(k, c->num_kv_heads, *smem_bytes, &per_sm)) != cudaSuccess)
     return PKD_E_CUDA;
   if (per_sm < 1) return PKD_E_UNSUPPORTED_SHAPE;
   *n_cta = sms * per_sm;
@@ -190,10 +191,10 @@ int kv_map_for(pkd_ctx* ctx, const void* kv, CUtensorMap* out, CUtensorMap* out_
   e.kv = kv;
   const pkd_config& c = ctx->cfg;
   const bool hnd = (c.flags & PKD_FLAG_HND) != 0;
-  if (ctx->kind.latent &&
+  if (ctx->latent &&
       encode_latent_map(kv, c.num_pages, c.page_size, 1, &e.map_dense) != cudaSuccess)
     return PKD_E_CUDA;
-  if ((ctx->kind.latent ? encode_latent_map(kv, c.num_pages, c.page_size, 0, &e.map)
+  if ((ctx->latent ? encode_latent_map(kv, c.num_pages, c.page_size, 0, &e.map)
                         : encode_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads,
                                         ctx->kind.fp8, hnd, ctx->kind.dense, &e.map)) !=
       cudaSuccess)
@@ -260,7 +261,7 @@ int launch_latent_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, fl
 int launch_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, float* lse,
                float k_scale, float v_scale, cudaStream_t stream, cudaEvent_t ev_before,
                cudaEvent_t ev_after, int32_t wait_epoch = 0) {
-  if (ctx->kind.latent)
+  if (ctx->latent)
     return launch_latent_run(ctx, q, kv, out, lse, k_scale, v_scale, stream, ev_before, ev_after,
                              wait_epoch);
   const pkd_config& c = ctx->cfg;
@@ -360,7 +361,7 @@ int pkd_schedule_layout(const pkd_config* cfg, int64_t off[6]) {
   int st = check_config(cfg);
   if (st != PKD_OK) return st;
   if (cfg->num_ctas < 1) return PKD_E_INVALID_ARG;
-  Layout L = make_layout(*cfg, cfg->num_ctas);
+  Layout L = plan_layout(*cfg, cfg->num_ctas);
   off[0] = L.cta_indptr;
   off[1] = L.items;
   off[2] = L.units;
@@ -379,7 +380,7 @@ int pkd_plan_host_shared(const pkd_config* cfg, const int32_t* group_indptr, int
   if (cfg->num_ctas < 1 || host_words == nullptr || !(cfg->flags & PKD_FLAG_SHARED_PREFIX))
     return PKD_E_INVALID_ARG;
   if (num_groups > 0 && group_indptr == nullptr) return PKD_E_INVALID_ARG;
-  Layout L = make_layout(*cfg, cfg->num_ctas);
+  Layout L = plan_layout(*cfg, cfg->num_ctas);
   if (max_words < (size_t)L.words) return PKD_E_INVALID_ARG;
   return plan_schedule_grouped(*cfg, cfg->num_ctas, L, group_indptr, num_groups, indptr, indices,
                                last_page_len, host_words, info);
@@ -394,7 +395,7 @@ int pkd_plan_host_cascade(const pkd_config* cfg, const int32_t* group_indptr,
   if (st != PKD_OK) return st;
   if (cfg->num_ctas < 2 || host_words == nullptr || !(cfg->flags & PKD_FLAG_CASCADE))
     return PKD_E_INVALID_ARG;
-  Layout L = make_layout(*cfg, cfg->num_ctas);
+  Layout L = plan_layout(*cfg, cfg->num_ctas);
   if (max_words < (size_t)L.words) return PKD_E_INVALID_ARG;
   return plan_schedule_cascade(*cfg, cfg->num_ctas, L, group_indptr, num_groups, p_indptr,
                                p_indices, p_last, s_indptr, s_indices, s_last, host_words, info);
@@ -418,7 +419,7 @@ int pkd_plan_host(const pkd_config* cfg, const int32_t* indptr, const int32_t* i
   if (st != PKD_OK) return st;
   if (cfg->num_ctas < 1 || host_words == nullptr || (cfg->flags & PKD_FLAG_CASCADE))
     return PKD_E_INVALID_ARG;
-  Layout L = make_layout(*cfg, cfg->num_ctas);
+  Layout L = plan_layout(*cfg, cfg->num_ctas);
   if (max_words < (size_t)L.words) return PKD_E_INVALID_ARG;
   return plan_schedule(*cfg, cfg->num_ctas, L, indptr, indices, last_page_len, batch,
                        host_words, info);
@@ -430,7 +431,7 @@ size_t pkd_workspace_bytes(const pkd_config* cfg) {
   int smem = 0;
   // the workspace layout does not depend on the producer
   if (resolve_ctas(cfg, kind_for(cfg, nullptr), &n_cta, &smem) != PKD_OK) return 0;
-  return make_layout(*cfg, n_cta).total_bytes;
+  return plan_layout(*cfg, n_cta).total_bytes;
 }
 
 int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
@@ -444,7 +445,9 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
   if (!ctx) return PKD_E_INVALID_ARG;
   ctx->cfg = *cfg;
   ctx->kind = kind_for(cfg, d_workspace);
-  if ((ctx->kind.dense || ctx->kind.cascade || ctx->kind.latent) && !ctx->kind.tmap) {   // the driver refused a map
+  ctx->latent = is_latent(*cfg);
+  // the driver refused a map
+  if ((ctx->kind.dense || ctx->kind.cascade || ctx->latent) && !ctx->kind.tmap) {
     delete ctx;
     return PKD_E_UNSUPPORTED_SHAPE;
   }
@@ -453,12 +456,12 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
     delete ctx;
     return st;
   }
-  if ((ctx->kind.latent ? latent_prepare(cfg->num_qo_heads)
+  if ((ctx->latent ? latent_prepare(cfg->num_qo_heads)
                         : decode_prepare(ctx->kind, ctx->smem_bytes)) != cudaSuccess) {
     delete ctx;
     return PKD_E_CUDA;
   }
-  ctx->layout = make_layout(*cfg, ctx->n_cta);
+  ctx->layout = plan_layout(*cfg, ctx->n_cta);
   if (workspace_bytes < ctx->layout.total_bytes) {
     delete ctx;
     return PKD_E_WORKSPACE_TOO_SMALL;
@@ -536,7 +539,7 @@ static int plan_and_publish(pkd_ctx* ctx, PlanFn plan_fn, void* stream, uint64_t
   // sees the whole schedule
   words[H_EPOCH] = epoch_word(ctx->epoch + 1);
   if (cudaMemcpyAsync(ctx->ws + (size_t)H_WORDS * 4, words + H_WORDS,
-                      ((size_t)request_words(L, info.nnz) +
+                      ((size_t)request_words(L.page_list, info.nnz) +
                        (size_t)kRequestWords * ((size_t)info.batch + 1) - H_WORDS) * 4,
                       cudaMemcpyHostToDevice, s) != cudaSuccess ||
       cudaMemcpyAsync(ctx->ws, words, (size_t)H_WORDS * 4, cudaMemcpyHostToDevice, s) !=
@@ -742,7 +745,7 @@ int pkd_accumulate_weights(pkd_ctx* ctx, const void* q, const void* kv, const fl
                            const int32_t* seen, float k_scale, uint64_t expect_epoch,
                            void* stream) {
   if (ctx == nullptr || !std::isfinite(k_scale)) return PKD_E_INVALID_ARG;
-  if (ctx->kind.block || ctx->kind.cascade || ctx->kind.latent) return PKD_E_INVALID_ARG;
+  if (ctx->kind.block || ctx->kind.cascade || ctx->latent) return PKD_E_INVALID_ARG;
   if (ctx->epoch == 0) return PKD_E_NO_PLAN;
   if (expect_epoch != 0 && expect_epoch != ctx->epoch) return PKD_E_STALE_PLAN;
   if (ctx->info.batch == 0) return PKD_OK;
@@ -820,10 +823,10 @@ size_t pkd_evict_workspace_bytes(int32_t layers, int32_t batch, int32_t max_len,
 int pkd_evict_kv(int32_t layers, void* const* kv, float* const* weights,
                  int32_t* const* positions, const int32_t* indptr, const int32_t* indices,
                  int32_t num_indices, const int32_t* last_page_len, const int32_t* seen,
-                 int32_t batch, int32_t max_len, int32_t budget, int32_t sinks, int32_t recent, int32_t per_head,
-                 int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
-                 uint32_t flags, void* d_workspace, size_t workspace_bytes, int32_t* err,
-                 void* stream) {
+                 int32_t batch, int32_t max_len, int32_t budget, int32_t sinks, int32_t recent,
+                 int32_t per_head, int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                 int32_t head_dim, uint32_t flags, void* d_workspace, size_t workspace_bytes,
+                 int32_t* err, void* stream) {
   if ((flags & ~(PKD_FLAG_HND | PKD_FLAG_KV_FP8)) != 0) return PKD_E_INVALID_ARG;
   const int st = check_evict(layers, batch, max_len, budget, per_head, num_kv_heads);
   if (st != PKD_OK) return st;
@@ -929,7 +932,7 @@ int pkd_graph_capture_io(pkd_ctx* ctx, int32_t layers, const void* const* q,
   }
   const pkd_config& c = ctx->cfg;
   const size_t rows = (size_t)ctx->info.batch * c.num_qo_heads;
-  const size_t q_bytes = rows * (ctx->kind.latent ? kLatentRow : c.head_dim) * 2;
+  const size_t q_bytes = rows * (ctx->latent ? kLatentRow : c.head_dim) * 2;
   const size_t out_bytes = rows * c.head_dim * 2, lse_bytes = rows * 4;
   const bool copy_in = q_host != nullptr && rows > 0;
   const bool copy_out = (out_host != nullptr || lse_host != nullptr) && rows > 0;
@@ -1037,7 +1040,7 @@ int pkd_graph_launch(pkd_graph* g, void* stream) {
   if (g == nullptr || g->exec == nullptr) return PKD_E_INVALID_ARG;
   // a dense-prefix (or cascade, or latent) graph's query maps cover the batch
   // it was captured with
-  if ((g->ctx->kind.dense || g->ctx->kind.cascade || g->ctx->kind.latent) &&
+  if ((g->ctx->kind.dense || g->ctx->kind.cascade || g->ctx->latent) &&
       g->ctx->info.batch != g->batch)
     return PKD_E_STALE_PLAN;
   if (cudaGraphLaunch(g->exec, static_cast<cudaStream_t>(stream)) != cudaSuccess)

@@ -54,7 +54,6 @@
 #include "pkd_internal.h"
 #include "prefix_tc_body.cuh"
 #include "sm103_ptx.cuh"
-#include "tensor_map.h"
 
 namespace pkd {
 namespace {
@@ -1401,6 +1400,8 @@ cudaError_t launch_decode(const DecodeKind& k, const DecodeArgs& a, int grid, in
 // {row, 128, D * E, P * row} (NHD) or {D * E, 128, P * D * E, P * row} (HND);
 // box {chunk, 16 tokens, all halves, all heads, one K or V page}, which lands
 // as [head][half][token][128 B] with the 128-byte swizzle in either layout.
+namespace {
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
@@ -1414,6 +1415,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return encode;
 }
+
+}  // namespace
 
 // The query map: dims (innermost first) {64 elements, 128-byte half, query
 // head within the group, KV head, request} with byte strides {128, 256,

@@ -24,6 +24,14 @@ __host__ __device__ constexpr int32_t latent_blocks(int32_t heads) {
   return (heads + latent_block_heads(heads) - 1) / latent_block_heads(heads);
 }
 
+// Latent plans: an item's fixed cost (its queries, its first tile, its
+// epilogue) in tokens, and the split floor: a part's state is 2 KB per head,
+// written and read back, so many heads pay for finer parts.  Measured with
+// floors of 128 / 256: one request of 517 tokens, 16 heads 5.0 / 5.8 us; one of
+// 8,000, 128 heads 15.8 / 11.8; 8 of up to 2,000, 64 heads 11.1 / 10.1.
+constexpr int kLatentAlpha = 128;
+inline int64_t latent_min_chunk(int32_t heads) { return heads <= 32 ? 128 : 256; }
+
 struct LatentArgs {
   const int32_t* sched;
   float* o_part;         // fp32 [slot][heads][512]

@@ -45,14 +45,16 @@
 // stops, waits (bounded) for its copies and products, frees tensor memory
 // and returns.
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <math_constants.h>
 #include <stdint.h>
+
+#include <mutex>
 
 #include "latent.h"
 #include "pkd_internal.h"
 #include "prefix_tc_body.cuh"
 #include "sm103_ptx.cuh"
-#include "tensor_map.h"
 
 namespace pkd {
 namespace {
@@ -991,6 +993,21 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(
   }
 }
 static_assert(kLatentDim * 2 / 16 == 64 && kLatentRope * 2 / 16 <= 32, "two pieces per lane");
+
+// The driver's tensor-map encoder (null when it has none), looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return encode;
+}
 
 }  // namespace
 

@@ -8,7 +8,6 @@
 #include <cuda.h>   // CUtensorMap (encoded through the runtime's driver entry point)
 #include <cuda_runtime_api.h>
 
-#include "latent.h"
 #include "pkd.h"
 
 namespace pkd {
@@ -29,13 +28,6 @@ __host__ __device__ constexpr int ring_depth(bool mma, bool block, bool fp8) {
 constexpr int kDefaultAlpha = 32;
 constexpr int kDefaultMinChunk = 256;
 constexpr int kMergeThreads = 256;
-// Latent contexts: an item's fixed cost (its queries, its first tile, its
-// epilogue) in tokens, and the split floor: a part's state is 2 KB per head,
-// written and read back, so many heads pay for finer parts.  Measured with
-// floors of 128 / 256: one request of 517 tokens, 16 heads 5.0 / 5.8 us; one of
-// 8,000, 128 heads 15.8 / 11.8; 8 of up to 2,000, 64 heads 11.1 / 10.1.
-constexpr int kLatentAlpha = 128;
-inline int64_t latent_min_chunk(int32_t heads) { return heads <= 32 ? 128 : 256; }
 
 // Schedule header words (first 32 int32 of the workspace; 19..31 are 0).
 enum HeaderWord {
@@ -107,7 +99,7 @@ struct Layout {
   int64_t units;         // [max_items][2]
   int64_t merge_indptr;  // [max_items + 1]
   int64_t page_list;     // [max_num_pages]
-  int64_t words;         // schedule words (end of page_list and the requests behind it)
+  int64_t words;         // schedule words (end of page_list)
   int64_t max_items;
   int64_t max_slots;     // partial-state slots
   // byte offsets inside the device workspace
@@ -118,15 +110,6 @@ struct Layout {
 };
 
 inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-
-// Behind the page list's nnz words (rounded up to 4), plain plans hold an
-// entry per request, and one more with the total: 16-token tiles of the
-// requests before, index of the first page in the page list, tokens, 0.
-constexpr int kRequestWords = 4, kRequestTile = 16;
-__host__ __device__ inline int64_t request_words(int64_t page_list, int64_t nnz) {
-  return page_list + (nnz + 3) / 4 * 4;
-}
-inline int64_t request_words(const Layout& L, int64_t nnz) { return request_words(L.page_list, nnz); }
 
 // Upper bound on work items of one plan: a split request of length l gives
 // ceil(l / c) <= l / c + 1 chunks and every chunk candidate is at least
@@ -155,9 +138,6 @@ inline Layout make_layout(const pkd_config& c, int64_t n_cta) {
   // items <= Hkv * blocks + 4 n_cta
   if (c.flags & PKD_FLAG_DENSE_PREFIX)
     L.max_items = (int64_t)c.num_kv_heads * c.max_batch + 4 * n_cta + 8;
-  // latent plans: an item per block of heads; a request's blocks share slots
-  if (c.flags & PKD_FLAG_LATENT)
-    L.max_items = (int64_t)latent_blocks(c.num_qo_heads) * c.max_batch + 4 * n_cta + 8;
   if (c.flags & PKD_FLAG_CASCADE) {
     // prefix items <= Hkv * blocks + 2 n_pre, suffix items <= batch + 2 n_suf
     // (chunks at least half the level's work bound); every request is a
@@ -172,8 +152,7 @@ inline Layout make_layout(const pkd_config& c, int64_t n_cta) {
   L.units = L.items + L.max_items * kItemWords;
   L.merge_indptr = L.units + L.max_items * 2;
   L.page_list = align_up(L.merge_indptr + L.max_items + 1, 4);
-  // behind the page list: plain plans' requests (RequestEntry)
-  L.words = request_words(L, c.max_num_pages) + (int64_t)kRequestWords * (c.max_batch + 1);
+  L.words = L.page_list + c.max_num_pages;
   size_t sched_bytes = (size_t)L.words * 4;
   L.err_byte = (size_t)align_up((int64_t)sched_bytes, 256);
   L.o_part_byte = L.err_byte + 256;
@@ -249,7 +228,6 @@ struct DecodeKind {
                        // (P % 16 == 0, tensor-core consumers); else one copy per token row
   bool dense = false;  // dense shared-prefix kernel (tcgen05, one KV head per item)
   bool cascade = false;  // cascade kernel: dense prefix role + decode role (page tiles)
-  bool latent = false;   // latent cache (latent.h)
 };
 int decode_smem_bytes(int hkv, const DecodeKind& k);
 int decode_threads(int hkv, const DecodeKind& k);
@@ -305,10 +283,6 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
                           const int32_t* group_indptr, int32_t n_rows, const int32_t* indptr,
                           const int32_t* indices, const int32_t* last, int32_t* words,
                           pkd_plan_info* info);
-// Plans of latent contexts (PKD_FLAG_LATENT); plan_schedule(_grouped) calls it.
-int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
-                         const int32_t* indptr, const int32_t* indices, const int32_t* last,
-                         int32_t batch, int32_t* words, pkd_plan_info* info);
 // Which format a shared-prefix step should take (pkd_advise_format).
 int advise_format(const pkd_config& cfg, int32_t n_cta, const int32_t* group_indptr,
                   int32_t n_groups, const int32_t* p_indptr, const int32_t* p_last,

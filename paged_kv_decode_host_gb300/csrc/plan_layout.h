@@ -1,0 +1,44 @@
+// The schedule layout of contexts and host plans: make_layout's, with room for
+// the requests' entries behind the page list and for the items of latent
+// plans; and the latent planner.
+#pragma once
+
+#include "latent.h"
+#include "pkd_internal.h"
+
+namespace pkd {
+
+// Behind the page list's nnz words (rounded up to 4), plain plans hold an
+// entry per request, and one more with the total: 16-token tiles of the
+// requests before, index of the first page in the page list, tokens, 0.
+constexpr int kRequestWords = 4, kRequestTile = 16;
+__host__ __device__ inline int64_t request_words(int64_t page_list, int64_t nnz) {
+  return page_list + (nnz + 3) / 4 * 4;
+}
+
+inline bool is_latent(const pkd_config& c) { return (c.flags & PKD_FLAG_LATENT) != 0; }
+
+inline Layout plan_layout(const pkd_config& c, int64_t n_cta) {
+  pkd_config room = c;
+  // latent plans: an item per block of heads (plans beyond the clamp are
+  // refused for want of items)
+  const int64_t rows = (int64_t)latent_blocks(c.num_qo_heads) * c.max_batch;
+  if (is_latent(c)) room.max_batch = (int32_t)(rows < 0x7fffffff ? rows : 0x7fffffff);
+  Layout L = make_layout(room, n_cta);
+  // what lies behind the schedule words moves along by whole 256 bytes
+  L.words = request_words(L.page_list, c.max_num_pages) +
+            (int64_t)kRequestWords * ((int64_t)c.max_batch + 1);
+  const size_t more = ((size_t)L.words * 4 + 255) / 256 * 256 - L.err_byte;
+  L.err_byte += more;
+  L.o_part_byte += more;
+  L.l_part_byte += more;
+  L.total_bytes += more;
+  return L;
+}
+
+// Plans of latent contexts (planner.cpp; plan_schedule_grouped calls it).
+int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
+                         const int32_t* indptr, const int32_t* indices, const int32_t* last,
+                         int32_t batch, int32_t* words, pkd_plan_info* info);
+
+}  // namespace pkd

@@ -34,6 +34,7 @@
 #include <vector>
 
 #include "pkd_internal.h"
+#include "plan_layout.h"
 
 namespace pkd {
 namespace {
@@ -176,7 +177,7 @@ int64_t lpt(const std::vector<Item>& items, int32_t n_cta, std::vector<int32_t>*
 // The requests' entries behind the page list.
 void write_requests(int32_t* words, const Layout& L, int64_t nnz, const std::vector<int64_t>& lens,
                     const int32_t* indptr) {
-  int32_t* w = words + request_words(L, nnz);
+  int32_t* w = words + request_words(L.page_list, nnz);
   int64_t tiles = 0;
   for (size_t i = 0; i <= lens.size(); ++i, w += kRequestWords) {
     const bool end = i == lens.size();
@@ -226,7 +227,7 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
                           const int32_t* group_indptr, int32_t n_rows, const int32_t* indptr,
                           const int32_t* indices, const int32_t* last, int32_t* words,
                           pkd_plan_info* info) {
-  if (cfg.flags & PKD_FLAG_LATENT)
+  if (is_latent(cfg))
     return group_indptr ? PKD_E_INVALID_ARG
                         : plan_schedule_latent(cfg, n_cta, L, indptr, indices, last, n_rows, words,
                                                info);

@@ -15,12 +15,13 @@
 // end (nothing is merged afterwards, so cutting costs nothing; the planner's
 // items, which the decode kernel walks, left a block up to half more than
 // the mean beside one long request, and most blocks idle for a few short
-// ones); a warp takes 16 tokens of one KV head at a time.  The scores are mma.sync m16n8k16 products with the tokens as the 16
-// rows and the group's heads as the 8 columns: K goes from global memory
-// straight into the A fragments, with no shared memory and for any layout or
-// page size, because the order of the contraction is free -- a lane takes 32
-// contiguous bytes of a row for four (bf16) or eight (E4M3) steps and the
-// queries are permuted alike.  (A tcgen05 product would have to stage K in
+// ones); a warp takes 16 tokens of one KV head at a time.  The scores are
+// mma.sync m16n8k16 products with the tokens as the 16 rows and the group's
+// heads as the 8 columns: K goes from global memory straight into the A
+// fragments, with no shared memory and for any layout or page size, because
+// the order of the contraction is free -- a lane takes 32 contiguous bytes of
+// a row for four (bf16) or eight (E4M3) steps and the queries are permuted
+// alike.  (A tcgen05 product would have to stage K in
 // shared memory to use 8 of its columns.)
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -30,6 +31,7 @@
 
 #include "evict.h"
 #include "pkd_internal.h"
+#include "plan_layout.h"
 #include "sm103_ptx.cuh"
 
 namespace pkd {
