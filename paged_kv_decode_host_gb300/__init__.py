@@ -37,7 +37,8 @@ import numpy as np
 __all__ = [
     "build", "load", "PkdError", "BatchDecodeWithPagedKVCache",
     "BatchLatentDecodeWithPagedCache", "merge_states", "append_kv",
-    "append_kv_layers", "append_latent", "evict_kv", "evicted_table", "plan_host", "plan_host_shared", "plan_host_cascade", "advise_format",
+    "append_kv_layers", "append_latent", "evict_kv", "evicted_table", "plan_host",
+    "plan_host_shared", "plan_host_cascade", "advise_format",
     "schedule_layout",
     "selftest_bounded_wait", "Graph",
     "STATUS",
@@ -412,6 +413,17 @@ def _table_args(dev, indptr, indices, last_page_len, **per_row):
         if t.numel() != batch:
             raise ValueError(f"{name} must have one entry per request")
     return batch
+
+
+def _empty_on(stream, shape, dtype, device):
+    """A tensor that kernels on `stream` (None: the current one) write first:
+    its memory is taken from that stream's, since a block of the current
+    stream's may still be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _err_arg(err, dev):
@@ -885,9 +897,9 @@ class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
         if self.batch is None:
             raise PkdError(-5, "run before plan")
         if out is None:
-            out = torch.empty((q.shape[0], self.hq, self.d), dtype=torch.bfloat16, device=q.device)
+            out = _empty_on(stream, (q.shape[0], self.hq, self.d), torch.bfloat16, q.device)
         if lse is None and return_lse:
-            lse = torch.empty((q.shape[0], self.hq), dtype=torch.float32, device=q.device)
+            lse = _empty_on(stream, (q.shape[0], self.hq), torch.float32, q.device)
         self._check_run_args(q, cache, out, lse)
         fast, lp = _fast(), lse.data_ptr() if lse is not None else 0
         with _On(q.get_device()):
@@ -1119,8 +1131,8 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
     caches as for :func:`append_kv`, weights float32 and positions int32
     [pages, Hkv, P] as :meth:`BatchDecodeWithPagedKVCache.accumulate_weights`
     keeps them.  indptr / indices / last_page_len / seen: int32 CUDA tensors,
-    the table (a page stands in it once) and the tokens seen; max_len: at least the longest request's
-    tokens (at most 262,144).  Tokens at positions below ``sinks`` and among
+    the table (a page stands in it once) and the tokens seen; max_len: at least
+    the longest request's tokens (at most 262,144).  Tokens at positions below ``sinks`` and among
     the last ``recent`` always stay.  per_head: every KV head keeps its own
     tokens; else all keep the same, by the sum of their weights.  Slots are
     closed up without keeping their order: afterwards the request's first
@@ -1165,9 +1177,7 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
         # (sizes out of range: 0 here, refused in the call itself)
         need = (lib.pkd_evict_workspace_bytes if fast is None else fast.evict_bytes)(
             layers, batch, max_len, budget, per_head, hkv)
-        ws = torch.empty(need, dtype=torch.uint8, device=c0.device) if need else None
-        if need and stream is not None:
-            ws.record_stream(stream)
+        ws = _empty_on(stream, need, torch.uint8, c0.device) if need else None
         args = [[t.data_ptr() for t in ts] for ts in (kv_caches, weights, positions)]
         rest = (indptr.data_ptr(), indices.data_ptr(), indices.numel(), last_page_len.data_ptr(),
                 seen.data_ptr(), batch, max_len, budget, sinks, recent, per_head, pages, P, hkv, D,

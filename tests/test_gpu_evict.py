@@ -483,3 +483,28 @@ def test_serving_loop_with_a_budget():
                     assert abs(got[s] - m[s][2]) <= 1e-3 * m[s][2] + 1e-6
         lens = [min(n, budget) for n in lens]
     assert dec.device_error() == 0
+
+
+@gpu
+def test_evict_workspace_belongs_to_the_calls_stream(monkeypatch):
+    """The bitmaps' memory comes from the stream that writes them: a block of the current
+    stream's may still be in use there."""
+    t, kvs, ws, ps, seen = evict_case(2, 16, [3000], 1500)
+    side, taken, empty = torch.cuda.Stream(), [], torch.empty
+
+    def spy(*a, **kw):
+        taken.append(torch.cuda.current_stream() == side)
+        return empty(*a, **kw)
+
+    gpu_state = ([to_gpu(x, torch.bfloat16) for x in kvs], [torch.from_numpy(x).cuda() for x in ws],
+                 [torch.from_numpy(x).cuda() for x in ps])
+    d = [torch.from_numpy(x).cuda() for x in t[:3]] + [torch.tensor(seen, dtype=torch.int32, device="cuda")]
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", spy)
+    pkd.evict_kv(*gpu_state, *d, 1500, max_len=3000, stream=side)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert taken == [True]
+    evict_reference(kvs, ws, ps, t, [3000], seen, 1500, 16, "NHD", 0, 0, True)
+    same(([x.view(torch.int16).cpu().numpy() for x in gpu_state[0]],
+          *[[x.cpu().numpy() for x in y] for y in gpu_state[1:]]), (kvs, ws, ps))
