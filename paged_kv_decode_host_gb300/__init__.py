@@ -894,13 +894,11 @@ class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
     def run(self, q, cache, out=None, lse=None, return_lse=True, expect_epoch=0, stream=None):
         """Attention for one layer.  Returns (out, lse) or out."""
         import torch
-        if self.batch is None:
-            raise PkdError(-5, "run before plan")
-        if out is None:
-            out = _empty_on(stream, (q.shape[0], self.hq, self.d), torch.bfloat16, q.device)
-        if lse is None and return_lse:
-            lse = _empty_on(stream, (q.shape[0], self.hq), torch.float32, q.device)
         self._check_run_args(q, cache, out, lse)
+        if out is None:
+            out = _empty_on(stream, self._run_shapes[3], torch.bfloat16, q.device)
+        if lse is None and return_lse:
+            lse = _empty_on(stream, self._run_shapes[4], torch.float32, q.device)
         fast, lp = _fast(), lse.data_ptr() if lse is not None else 0
         with _On(q.get_device()):
             s = _stream_ptr(stream)

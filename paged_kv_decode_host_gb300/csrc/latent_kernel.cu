@@ -938,14 +938,17 @@ const void* kernel_of(int32_t heads) {
 }
 
 // ---------------------------------------------------------------- append
-// kTokens new tokens a warp: their latent and rotary parts, read from rows of
-// any stride (they are often column ranges of one projection's output),
-// become one cache row each.  Bytes: a row read and written per token.  The
-// rows do not depend on the table, so they are fetched while it is read (three
-// dependent lookups); four tokens a warp keep enough rows on their way behind
-// those to fill the memory system, one spreads a step's few tokens.
+// A warp makes one cache row of a new token's latent and rotary parts, read
+// from rows of any stride (they are often column ranges of one projection's
+// output).  Bytes: a row read and written per token.  The rows do not depend
+// on the table, so they are fetched while it is read (three dependent
+// lookups).  Both sides are marked as streamed: a prompt's rows pass through
+// L2 once (32,767 tokens of three states in turn: 14.7 us, 5.1 TB/s, against
+// 16.8 us; the reads or the writes alone so marked change nothing; 131,072
+// tokens 47.2 us, 6.4 TB/s, against 51.4), and rows that lie in L2 are as fast
+// either way.  Two or four tokens a warp are no faster so, and slower for
+// some 5,000 tokens (5.5 against 4.2 us).
 constexpr int kAppendWarps = 8;
-template <int kTokens>
 __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(
     const uint8_t* __restrict__ latent, int64_t latent_stride, const uint8_t* __restrict__ rope,
     int64_t rope_stride, const int32_t* __restrict__ batch_indices,
@@ -954,43 +957,32 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(
     const int32_t* __restrict__ last_page_len, int32_t batch, uint8_t* __restrict__ cache,
     int32_t num_pages, int32_t page_size, int32_t* err) {
   const int lane = threadIdx.x & 31;
-  const int64_t i0 = ((int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) * kTokens;
-  if (i0 >= n) return;
+  const int64_t i = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  if (i >= n) return;
   constexpr int kLat16 = kLatentDim * 2 / 16, kRope16 = kLatentRope * 2 / 16;
-  uint4 v[kTokens][2], vr[kTokens];
-#pragma unroll
-  for (int j = 0; j < kTokens; ++j) {
-    const int64_t i = min(i0 + j, (int64_t)n - 1);
-    const uint4* src = reinterpret_cast<const uint4*>(latent + i * latent_stride);
-    v[j][0] = src[lane];
-    v[j][1] = src[32 + lane];
-    vr[j] = make_uint4(0, 0, 0, 0);
-    if (lane < kRope16) vr[j] = reinterpret_cast<const uint4*>(rope + i * rope_stride)[lane];
-  }
-  // lane j looks token j up
+  const uint4* src = reinterpret_cast<const uint4*>(latent + i * latent_stride);
+  const uint4 v0 = __ldcs(src + lane), v1 = __ldcs(src + 32 + lane);
+  uint4 vr = make_uint4(0, 0, 0, 0);
+  if (lane < kRope16) vr = __ldcs(reinterpret_cast<const uint4*>(rope + i * rope_stride) + lane);
   int64_t row = -1;   // the cache's row: page * page_size + slot
-  if (lane < kTokens && i0 + lane < n) {
-    const int b = batch_indices[i0 + lane], pos = positions[i0 + lane];
-    if (b >= 0 && b < batch) {
-      const int p0 = indptr[b], p1 = indptr[b + 1], last = last_page_len[b];
-      const int64_t len = (int64_t)page_size * (p1 - p0 - 1) + last;
-      if (p0 >= 0 && p1 > p0 && p1 <= num_indices && last >= 1 && last <= page_size && pos >= 0 &&
-          pos < len) {
-        const int pg = indices[p0 + pos / page_size];
-        if (pg >= 0 && pg < num_pages) row = (int64_t)pg * page_size + pos % page_size;
-      }
+  const int b = batch_indices[i], pos = positions[i];
+  if (b >= 0 && b < batch) {
+    const int p0 = indptr[b], p1 = indptr[b + 1], last = last_page_len[b];
+    const int64_t len = (int64_t)page_size * (p1 - p0 - 1) + last;
+    if (p0 >= 0 && p1 > p0 && p1 <= num_indices && last >= 1 && last <= page_size && pos >= 0 &&
+        pos < len) {
+      const int pg = indices[p0 + pos / page_size];
+      if (pg >= 0 && pg < num_pages) row = (int64_t)pg * page_size + pos % page_size;
     }
-    if (row < 0 && err != nullptr) atomicOr(err, PKD_DEV_ERR_BOUNDS);
   }
-#pragma unroll
-  for (int j = 0; j < kTokens; ++j) {
-    const int64_t to = __shfl_sync(kFull, row, j);
-    if (to < 0) continue;
-    uint4* dst = reinterpret_cast<uint4*>(cache + to * kLatentRow * 2);
-    dst[lane] = v[j][0];
-    dst[32 + lane] = v[j][1];
-    if (lane < kRope16) dst[kLat16 + lane] = vr[j];
+  if (row < 0) {
+    if (lane == 0 && err != nullptr) atomicOr(err, PKD_DEV_ERR_BOUNDS);
+    return;
   }
+  uint4* dst = reinterpret_cast<uint4*>(cache + row * kLatentRow * 2);
+  __stcs(dst + lane, v0);
+  __stcs(dst + 32 + lane, v1);
+  if (lane < kRope16) __stcs(dst + kLat16 + lane, vr);
 }
 static_assert(kLatentDim * 2 / 16 == 64 && kLatentRope * 2 / 16 <= 32, "two pieces per lane");
 
@@ -1109,13 +1101,11 @@ cudaError_t launch_latent_append(const void* latent, int64_t latent_stride, cons
                                  int64_t rope_stride, const int32_t* batch_indices,
                                  const int32_t* positions, int32_t n, const int32_t* indptr,
                                  const int32_t* indices, int32_t num_indices,
-                                 const int32_t* last_page_len, int32_t batch, void* cache, int32_t num_pages, int32_t page_size,
-                                 int32_t* err, cudaStream_t stream) {
-  // four tokens a warp once one each would give every SM two blocks
-  const int tokens = n >= 2 * 152 * kAppendWarps ? 4 : 1;
-  const int64_t per = (int64_t)tokens * kAppendWarps, blocks = (n + per - 1) / per;
-  (tokens == 4 ? latent_append_kernel<4> : latent_append_kernel<1>)<<<(unsigned)blocks,
-                                                                      kAppendWarps * 32, 0, stream>>>(
+                                 const int32_t* last_page_len, int32_t batch, void* cache,
+                                 int32_t num_pages, int32_t page_size, int32_t* err,
+                                 cudaStream_t stream) {
+  const int64_t blocks = ((int64_t)n + kAppendWarps - 1) / kAppendWarps;
+  latent_append_kernel<<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(
       static_cast<const uint8_t*>(latent), latent_stride, static_cast<const uint8_t*>(rope),
       rope_stride, batch_indices, positions, n, indptr, indices, num_indices, last_page_len, batch,
       static_cast<uint8_t*>(cache), num_pages, page_size, err);
