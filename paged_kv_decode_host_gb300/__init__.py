@@ -29,6 +29,7 @@ API (names follow the pages' plan / run / merge_states):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -378,40 +379,41 @@ def _stream_ptr(stream=None):
     return _current_raw_stream()
 
 
-class _On:
-    """Makes a tensor's device the current one for a call, when it is not."""
+_HERE = contextlib.nullcontext()
+_get_device = None
 
-    __slots__ = ("guard",)
 
-    def __init__(self, dev):
+def _on(dev):
+    """A context in which device `dev` is the current one."""
+    global _get_device
+    if _get_device is None:
         import torch
-        get = getattr(torch._C, "_cuda_getDevice", None)
-        self.guard = None if get is not None and get() == dev else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _table_args(dev, indptr, indices, last_page_len, **per_row):
-    """Checks of a device table (int32, contiguous, on device `dev`) and of
-    int32 tensors with one entry per request; returns the batch."""
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if _get_device() == dev:
+        return _HERE
     import torch
-    i32 = torch.int32
-    for name, t in (("indptr", indptr), ("indices", indices), ("last_page_len", last_page_len),
-                    *per_row.items()):
-        if t.dtype is not i32 or not t.is_contiguous() or t.get_device() != dev:
-            raise TypeError(f"{name} must be a contiguous int32 tensor on cuda:{dev}")
+    return torch.cuda.device(dev)
+
+
+def _table_args(i32, dev, indptr, indices, last_page_len, seen=None):
+    """Checks of a device table (int32, contiguous, on device `dev`) and of
+    the tokens seen per request; returns the batch."""
+    if not (indptr.dtype is i32 and indices.dtype is i32 and last_page_len.dtype is i32
+            and indptr.get_device() == dev and indices.get_device() == dev
+            and last_page_len.get_device() == dev and indptr.is_contiguous()
+            and indices.is_contiguous() and last_page_len.is_contiguous()
+            and (seen is None or (seen.dtype is i32 and seen.get_device() == dev
+                                  and seen.is_contiguous()))):
+        for name, t in (("indptr", indptr), ("indices", indices),
+                        ("last_page_len", last_page_len), ("seen", seen)):
+            if t is not None and (t.dtype is not i32 or not t.is_contiguous()
+                                  or t.get_device() != dev):
+                raise TypeError(f"{name} must be a contiguous int32 tensor on cuda:{dev}")
     batch = last_page_len.numel()
     if indptr.numel() != batch + 1:
         raise ValueError("indptr must have batch + 1 entries")
-    for name, t in per_row.items():
-        if t.numel() != batch:
-            raise ValueError(f"{name} must have one entry per request")
+    if seen is not None and seen.numel() != batch:
+        raise ValueError("seen must have one entry per request")
     return batch
 
 
@@ -751,6 +753,8 @@ class BatchDecodeWithPagedKVCache:
             raise ValueError("positions needs new_tokens and seen")
         self._check_run_args(q, kv_cache, q, None)
         dev = q.get_device()
+        if dev != self.workspace.get_device():
+            raise ValueError(f"q is on {q.device}, the plan on {self.workspace.device}")
         for name, t, dt, shape in (("lse", lse, f32, (B, self.hq)),
                                    ("weights", weights, f32, per_slot),
                                    ("positions", positions, i32, per_slot),
@@ -763,7 +767,7 @@ class BatchDecodeWithPagedKVCache:
                 raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)} on "
                                  f"{q.device}")
         fast = _fast()
-        with _On(dev):
+        with _on(dev):
             st = (self._lib.pkd_accumulate_weights if fast is None else fast.accumulate)(
                 self._hv, q.data_ptr(), kv_cache.data_ptr(), lse.data_ptr(), weights.data_ptr(),
                 positions.data_ptr() if positions is not None else 0,
@@ -876,8 +880,12 @@ class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
                                 torch.Size((B, self.hq, self.d)), torch.Size((B, self.hq)))
         _, qs, cs, os_, ls = self._run_shapes
         bf, dev = torch.bfloat16, q.get_device()
-        if dev < 0 or self.device.index not in (None, dev):
-            raise ValueError(f"q is on {q.device}, the plan on {self.device}")
+        if dev != self.workspace.get_device():
+            raise ValueError(f"q is on {q.device}, the plan on {self.workspace.device}")
+        if (q.dtype is bf and kv_cache.dtype is bf and q.shape == qs and kv_cache.shape == cs
+                and q.is_contiguous() and kv_cache.is_contiguous()
+                and kv_cache.get_device() == dev and out is None and lse is None):
+            return
         for name, t, dt, shape in (("q", q, bf, qs), ("cache", kv_cache, bf, cs),
                                    ("out", out, bf, os_), ("lse", lse, torch.float32, ls)):
             if t is None:
@@ -900,7 +908,7 @@ class BatchLatentDecodeWithPagedCache(BatchDecodeWithPagedKVCache):
         if lse is None and return_lse:
             lse = _empty_on(stream, self._run_shapes[4], torch.float32, q.device)
         fast, lp = _fast(), lse.data_ptr() if lse is not None else 0
-        with _On(q.get_device()):
+        with _on(q.get_device()):
             s = _stream_ptr(stream)
             st = _NOT_HANDLED if fast is None else fast.run(
                 self._hv, q.data_ptr(), cache.data_ptr(), out.data_ptr(), lp, self.scale, 1.0,
@@ -1106,9 +1114,9 @@ def append_latent(latent_new, rope_new, batch_indices, positions, indptr, indice
             raise TypeError(f"{name} must be a contiguous int32 tensor on cuda:{dev}")
     if positions.numel() != n:
         raise ValueError("batch_indices and positions need one entry per new token")
-    batch = _table_args(dev, indptr, indices, last_page_len)
+    batch = _table_args(i32, dev, indptr, indices, last_page_len)
     fast = _fast()
-    with _On(dev):
+    with _on(dev):
         st = (load().pkd_append_latent if fast is None else fast.append_latent)(
             latent_new.data_ptr(), strides[0], rope_new.data_ptr(), strides[1],
             batch_indices.data_ptr(), positions.data_ptr(), n, indptr.data_ptr(),
@@ -1156,27 +1164,30 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
     per_slot = torch.Size((pages, hkv, P))
     if dev < 0:
         raise TypeError("caches must be on the GPU")
+    args = []
     for name, ts, dt, size in (("kv_caches", kv_caches, dtype, shape),
                                ("weights", weights, f32, per_slot),
                                ("positions", positions, i32, per_slot)):
-        for l, t in enumerate(ts):
+        at = []
+        for t in ts:
             if t.dtype is not dt or t.shape != size or t.get_device() != dev or \
                     not t.is_contiguous():
-                raise ValueError(f"{name}[{l}] must be a contiguous {dt} tensor {list(size)} on "
-                                 f"cuda:{dev}")
-    batch = _table_args(dev, indptr, indices, last_page_len, seen=seen)
+                raise ValueError(f"{name}[{len(at)}] must be a contiguous {dt} tensor "
+                                 f"{list(size)} on cuda:{dev}")
+            at.append(t.data_ptr())
+        args.append(at)
+    batch = _table_args(i32, dev, indptr, indices, last_page_len, seen)
     per_head = 1 if per_head else 0
     lib, fast = load(), _fast()
     if fast is None:
         for v in (max_len, budget, sinks, recent):
             if not -2**31 <= v < 2**31:
                 raise OverflowError("max_len, budget, sinks and recent must fit 32 bits")
-    with _On(dev):
+    with _on(dev):
         # (sizes out of range: 0 here, refused in the call itself)
         need = (lib.pkd_evict_workspace_bytes if fast is None else fast.evict_bytes)(
             layers, batch, max_len, budget, per_head, hkv)
         ws = _empty_on(stream, need, torch.uint8, c0.device) if need else None
-        args = [[t.data_ptr() for t in ts] for ts in (kv_caches, weights, positions)]
         rest = (indptr.data_ptr(), indices.data_ptr(), indices.numel(), last_page_len.data_ptr(),
                 seen.data_ptr(), batch, max_len, budget, sinks, recent, per_head, pages, P, hkv, D,
                 (FLAG_HND if kv_layout == "HND" else 0) | (FLAG_KV_FP8 if fp8 else 0),
