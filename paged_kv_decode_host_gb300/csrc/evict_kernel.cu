@@ -300,14 +300,18 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   int bad = 0;
   for (int i = tid; i <= P.div(n - 1); i += kThreads)
     bad |= (unsigned)j.pages[i] >= (unsigned)a.num_pages ? 1 : 0;
+  const int words = (n + 31) / 32;
   if (__syncthreads_or(bad)) {
     if (tid == 0 && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+    if (!kMove && rank == 0)   // nothing to move: the slots below the budget stay
+      for (int w = tid; w < words; w += kThreads)
+        a.bitmaps[(int64_t)job * z.words + w] =
+            32 * w + 32 <= keep ? kFull : 32 * w < keep ? (1u << (keep - 32 * w)) - 1u : 0u;
     return;
   }
   const float* weights = a.weights[j.layer];
   const int32_t* positions = a.positions[j.layer];
   const int seen = a.seen[j.req];
-  const int words = (n + 31) / 32;
   const int w0 = min(words, rank * (z.share / 32)), w1 = min(words, w0 + z.share / 32);
   const int t0 = 32 * w0, t1 = min(n, 32 * w1);
 
@@ -522,13 +526,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   const int groups = a.per_head ? a.hkv : 1;
   const int split = (int)blockIdx.x / groups % a.splits;
   const int job = (int)blockIdx.x / (groups * a.splits) * groups + (int)blockIdx.x % groups;
-  pdl_wait();   // the bitmaps, and whatever came before them
+  // the table is older than the kernel before, which only reads it
   Job j;
-  if (!job_of(a, job, false, &j)) return;
-  int bad = 0;
-  for (int i = threadIdx.x; i <= (j.n - 1) / a.page_size; i += kMoveThreads)
-    bad |= (unsigned)j.pages[i] >= (unsigned)a.num_pages ? 1 : 0;
-  if (__syncthreads_or(bad)) return;   // flagged by the kernel before
+  const bool idle = !job_of(a, job, false, &j);
+  pdl_wait();   // the bitmaps
+  if (idle) return;
   const uint32_t* in = a.bitmaps + (int64_t)job * z.words;
   for (int w = threadIdx.x; 32 * w < j.n; w += kMoveThreads) kept[w] = in[w];
   __syncthreads();

@@ -65,7 +65,8 @@ cudaError_t launch_latent_append(const void* latent, int64_t latent_stride, cons
                                  int64_t rope_stride, const int32_t* batch_indices,
                                  const int32_t* positions, int32_t n, const int32_t* indptr,
                                  const int32_t* indices, int32_t num_indices,
-                                 const int32_t* last_page_len, int32_t batch, void* cache, int32_t num_pages, int32_t page_size,
-                                 int32_t* err, cudaStream_t stream);
+                                 const int32_t* last_page_len, int32_t batch, void* cache,
+                                 int32_t num_pages, int32_t page_size, int32_t* err,
+                                 cudaStream_t stream);
 
 }  // namespace pkd

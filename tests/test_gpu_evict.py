@@ -299,6 +299,20 @@ def test_evict_wrong_tables_are_left_alone():
 
 
 @gpu
+@pytest.mark.parametrize("lens,budget", [([1600, 2000, 1700], 901), ([20_000, 9000], 4000)])
+def test_evict_wrong_pages_of_long_requests(lens, budget):
+    """As above where the moves are a kernel of their own: nothing of the request with the wrong page."""
+    t, kvs, ws, ps, seen = evict_case(2, 16, lens, budget, seed=4)
+    bad = t[1].copy()
+    bad[t[0][1] - 1] = t[3]                         # request 0's last page
+    want = [[x.copy() for x in y] for y in (kvs, ws, ps)]
+    got = run_evict((t[0], bad, t[2]), kvs, ws, ps, seen, budget, torch.bfloat16, max_len=max(lens))
+    evict_reference(*want, t, [0] + lens[1:], seen, budget, 16, "NHD", 0, 0, True)
+    same(got, want)
+    assert got[3] == pkd.DEV_ERR_BOUNDS
+
+
+@gpu
 def test_evict_refusals():
     lens = [100]
     t, kvs, ws, ps, seen = evict_case(2, 16, lens, 40, layers=2)
