@@ -39,7 +39,10 @@ using dev::kFull;
 using dev::pdl_launch_dependents;
 using dev::pdl_wait;
 
-constexpr int kWindow = 256;   // pairs listed at a time
+// Pairs listed at a time.  128 / 256 / 512: 102 / 98 / 99 us (24 requests of up
+// to 4,609 tokens cut to 2,048, four layers), 91 / 92 / 112 (two of 65,539 to
+// half, two layers).
+constexpr int kWindow = 256;
 constexpr int kFew = 8;        // evictions taken by block-wide minima
 
 // fp32 order as unsigned order: NaN lowest, -0 equal to 0; kept-always above all
