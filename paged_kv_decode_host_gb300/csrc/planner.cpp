@@ -527,7 +527,8 @@ int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
       const int64_t n = (int64_t)indptr[i + 1] - indptr[i];
       if (n < 1 || last[i] < 1 || last[i] > P) return PKD_E_BAD_TABLE;
       lens[i] = P * (n - 1) + last[i];
-      if (lens[i] > 0x7fffffffLL) return PKD_E_CAPACITY;
+      // (the kernel counts tokens in 32 bits, up to a few tiles past the end)
+      if (lens[i] > 0x7fffffffLL - 1024) return PKD_E_CAPACITY;
       total += lens[i];
     }
     nnz = indptr[batch];

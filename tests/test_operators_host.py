@@ -33,6 +33,18 @@ def test_latent_configurations(lib):
     assert layout_status(lib, num_pages=0) == INVALID
 
 
+def test_latent_plan_keeps_token_counts_in_32_bits():
+    """A table that names one large page often: tokens past a request's end must count in 32 bits, too."""
+    import numpy as np
+    page = 1 << 20
+    cfg = pkd.make_config(16, 1, 512, page, 1, 2048, 1, num_ctas=8, flags=pkd.FLAG_LATENT)
+    table = lambda n, last: (np.array([0, n], np.int32), np.zeros(n, np.int32), np.array([last], np.int32))
+    for n, last in ((2048, page), (2048, page - 1), (2048, page - 1023)):
+        with pytest.raises(pkd.PkdError, match="CAPACITY"):
+            pkd.plan_host(cfg, *table(n, last))
+    pkd.plan_host(cfg, *table(2048, page - 1024 - 1))
+
+
 def evict_status(lib, **kw):
     a = dict(layers=2, kv=[256, 512], weights=[1024, 1088], positions=[2048, 2112], indptr=64, indices=64,
              num_indices=4, last=64, seen=64, batch=1, max_len=100, budget=10, sinks=1, recent=2,
