@@ -42,7 +42,9 @@ using namespace dev;
 // Warps of a block: a multiple of 1, 2, 4 and 8 heads (a warp keeps its head),
 // each with one 16-token tile under way.  Fewer warps with two to four tiles
 // each were no faster for bf16 (16 x 2: 79 against 76 us, 64 requests of up
-// to 8,192 tokens) and slower for E4M3 (16 x 3: 37 against 33 us, 64 of 2,048).
+// to 8,192 tokens) and slower for E4M3 (16 x 3: 37 against 33 us, 64 of
+// 2,048); 24 with two E4M3 tiles spill (25 against 20 us, 50,021 tokens and 16
+// short requests).
 constexpr int kWarps = 24;
 constexpr float kLog2e = 1.4426950408889634f;
 
