@@ -23,18 +23,18 @@
 // (1 KB, 128-byte swizzle), the 9 column chunks in two regions: 4-8 (with the
 // rotary key) and 0-3.  (Four regions shorten the wait for the last scores but
 // lengthen the producer's way more: 78 -> 79 us for 128 heads.)
-//  * warp 8 streams C: one TMA tensor copy per region and 16 tokens (10 and 8
+//  * a warp streams C: one TMA tensor copy per region and 16 tokens (10 and 8
 //    KB; a 5-D map of the cache gives the blocked order, so page tiles join
 //    to one operand however the pages are scattered; 36 copies of 2 KB a tile
 //    were bound by their issue, about 110 cycles a copy);
-//  * warp 9 issues the score products of a region as it lands, warp 10 the P.V
+//  * one issues the score products of a region as it lands, one the P.V
 //    products, whose regions are refilled one after the other; the whole warp
 //    runs the loop and one elected lane issues, with unrolled constant
 //    descriptor steps: 29 / 38 cycles per 64 x 16 / 64 x 64 product and 45 /
 //    54 with 128 rows, where a lone thread that forms descriptors in the loop
 //    takes 135 for any;
-//  * warps 0-7 are the softmax: a thread holds one token and a quarter of the
-//    block's heads.  The maxima run over tokens, that
+//  * warps 0-7 (0-15 from 32 heads on) are the softmax: a thread holds one
+//    token and 4 or 8 of the block's heads.  The maxima run over tokens, that
 //    is, across lanes and warps, so they are not formed per tile: every tile
 //    is only compared with the running base, and the exact maxima are taken
 //    when some score exceeds its head's base by more than 2^8 (always in an
@@ -77,9 +77,6 @@ constexpr int kRegions = 2;
 __host__ __device__ constexpr int region_first(int g) { return g == 0 ? 4 : 0; }
 __host__ __device__ constexpr int region_chunks(int g) { return g == 0 ? 5 : 4; }
 constexpr int kRegionPairs = kPairs / kRegions;
-constexpr int kSoftWarps = 8;
-constexpr int kWarpLoad = 8, kWarpScore = 9, kWarpOut = 10;
-constexpr int kLatThreads = 11 * 32;
 constexpr float kRaiseLog2 = 8.f;
 constexpr float kLowest = -3.0e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
@@ -99,7 +96,15 @@ constexpr int kP = kTile * 128;   // [token][64 heads] bf16, 128-byte rows
 template <int NH_>
 struct LatentShape {
   static constexpr int NH = NH_;
-  static constexpr int HH = NH / 2, QH = NH / 4;   // heads of a softmax warp, of a thread
+  // Softmax teams of four warps (a warp per 16 tokens), a team's heads and a
+  // thread's (half a warp each); the warps behind them load, score and
+  // multiply.  Four teams where a thread keeps four heads or more: the softmax
+  // is part of a 64-head tile's round (128 heads, 32 requests: 77.9 -> 72.6 us;
+  // 32 heads, 64 requests of 2,000 tokens: 38.2 -> 37.2).
+  static constexpr int kTeams = NH >= 32 ? 4 : 2, HH = NH / kTeams, QH = HH / 2;
+  static constexpr int kSoft = 4 * kTeams;
+  static constexpr int kLoad = kSoft, kScore = kSoft + 1, kOut = kSoft + 2;
+  static constexpr int kThreads = (kSoft + 3) * 32;
   static constexpr int kQChunk = NH * 128;
   static constexpr int kQ = kChunks * kQChunk;
   // P is kept as two bf16 values, the rounded weight and what the rounding
@@ -127,12 +132,12 @@ struct LatentSmem {
   uint64_t qfull, qfree;
   uint64_t sfull[2], sfree[2];
   uint64_t pfull, pvdone, ofree;
-  uint64_t xch[2];                   // per half of the heads: the four warps' exchanges
+  uint64_t xch[C::kTeams];           // a team's four warps' exchanges
   uint64_t fin;
   uint32_t tmem_base;
   int abort_flag;
-  int raise[2][2][4];                              // [phase parity][half][quadrant]
-  float top[2][2][4][C::HH];                       // column maxima / sums, likewise
+  int raise[2][C::kTeams][4];                      // [phase parity][team][quadrant]
+  float top[2][C::kTeams][4][C::HH];               // column maxima / sums, likewise
 };
 
 template <class C>
@@ -287,7 +292,7 @@ __device__ __forceinline__ LatentItem item_at(const LatentArgs& a, int it) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(kLatThreads, 1)
+__global__ void __launch_bounds__(C::kThreads, 1)
     latent_decode_kernel(const __grid_constant__ LatentArgs a) {
   extern __shared__ __align__(1024) uint8_t sC[];   // the swizzle repeats every 1024 bytes
   if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     pdl_wait();
     return;
   }
-  if (warp == kWarpLoad && lane < 3) {   // the first copies would wait for their maps
+  if (warp == C::kLoad && lane < 3) {   // the first copies would wait for their maps
     const CUtensorMap* map = lane < 2 ? &a.kv_map[lane] : &a.q_map;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
@@ -325,12 +330,12 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     mbar_init(&sh->qfree, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->sfull[b], 1);
-      mbar_init(&sh->sfree[b], kSoftWarps);
-      mbar_init(&sh->xch[b], 4);
+      mbar_init(&sh->sfree[b], C::kSoft);
     }
-    mbar_init(&sh->pfull, kSoftWarps);
+    for (int b = 0; b < C::kTeams; ++b) mbar_init(&sh->xch[b], 4);
+    mbar_init(&sh->pfull, C::kSoft);
     mbar_init(&sh->pvdone, 1);
-    mbar_init(&sh->ofree, kSoftWarps);
+    mbar_init(&sh->ofree, C::kSoft);
     mbar_init(&sh->fin, 2);
     sh->abort_flag = 0;
     fence_mbar_init();
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   // sets itself up
   LatentItem item0{};
   int page_a = 0, page_b = 0;
-  if (warp == kWarpLoad) {
+  if (warp == C::kLoad) {
     item0 = item_at(a, it0);
     const int boxes = (item0.te - item0.tb + 15) >> 4;
     const int32_t* pages = a.sched + a.off_pages + item0.page0;
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, sh->tmem_base, 0);
 
-  if (warp == kWarpLoad) {
+  if (warp == C::kLoad) {
     // ------------------------------------------------------------ producer
     // q and the cache are read before the previous kernel is waited for, as
     // the decode kernel does (the contract of pkd_run)
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp == kWarpScore) {
+  } else if (warp == C::kScore) {
     // -------------------------------------------------------- S^T products
     const bool me = elect_one();
     const uint32_t idesc = tc::mma_idesc(kTile, C::NH, 0);
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       if (!mbar_wait(&sh->fin, 0, nullptr)) atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp == kWarpOut) {
+  } else if (warp == C::kOut) {
     // -------------------------------------------------------- O^T products
     const bool me = elect_one();
     const uint32_t idesc = tc::mma_idesc(128, C::NP, 1) | (1u << 15);   // A and B MN-major
@@ -568,8 +573,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
   } else {
     // -------------------------------------------------- softmax + epilogue
     constexpr int HH = C::HH, QH = C::QH;
-    const int quad = warp & 3, half = warp >> 2;
-    // scores: this thread's token of the tile and its heads of the half
+    const int quad = warp & 3, team = warp >> 2;
+    // scores: this thread's token of the tile and its heads of the team
     const int row = 16 * quad + (lane & 15), hq = (lane >> 4) * QH;
     const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16);   // this quadrant's lanes
     // the column that a column-wise reduction leaves here, and whether this
@@ -579,20 +584,20 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     uint32_t xc = 0;                                            // exchanges so far
     int r = 0;
     bool ok = true, waited = false;
-    // the four warps of this half meet (bounded): what each wrote into the
+    // the four warps of this team meet (bounded): what each wrote into the
     // exchange arrays of this phase's parity is visible to all afterwards;
     // the other parity's arrays may be rewritten from here on
     auto meet = [&]() -> bool {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->xch[half]);
-      if (!tc_wait(&sh->xch[half], xc & 1u, abort_flag, a.err, lane)) return false;
+      if (lane == 0) mbar_arrive(&sh->xch[team]);
+      if (!tc_wait(&sh->xch[team], xc & 1u, abort_flag, a.err, lane)) return false;
       ++xc;
       return true;
     };
     for (int it = it0; it < it1 && ok; ++it) {
       const LatentItem w = item_at(a, it);
       // l: this token's sums.  base: lane j holds the base (log2 units) of the
-      // half's head j; every warp keeps its own copy
+      // team's head j; every warp keeps its own copy
       float l[QH], base = 0.f;
 #pragma unroll
       for (int j = 0; j < QH; ++j) l[j] = 0.f;
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         const bool live = row < w.te - t;
         tc_fence_after();
         uint32_t sv[QH];
-        tmem_ld_rows16<QH>(tq + C::kColS + C::NH * b + HH * half, sv);
+        tmem_ld_rows16<QH>(tq + C::kColS + C::NH * b + HH * team, sv);
         tc::tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
@@ -622,28 +627,28 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           y[j] = live ? fmaf(__uint_as_float(sv[j]), a.scale_log2, -m) : -CUDART_INF_F;
           over = fmaxf(over, y[j]);
         }
-        // the four warps of this half agree whether to raise their bases; an
+        // the four warps of this team agree whether to raise their bases; an
         // item's first tile always does, and brings its maxima along
         const int par = (int)(xc & 1u);
         if (first) {
           const float top = columns_over_lanes<QH>(y, lane, max_nan);
-          if (speaks) sh->top[par][half][quad][col] = top;
+          if (speaks) sh->top[par][team][quad][col] = top;
         } else {
           const bool want = __any_sync(kFull, over > kRaiseLog2);
-          if (lane == 0) sh->raise[par][half][quad] = want ? 1 : 0;
+          if (lane == 0) sh->raise[par][team][quad] = want ? 1 : 0;
         }
         if (!meet()) {
           ok = false;
           break;
         }
-        const bool up = first || (sh->raise[par][half][0] | sh->raise[par][half][1] |
-                                  sh->raise[par][half][2] | sh->raise[par][half][3]) != 0;
+        const bool up = first || (sh->raise[par][team][0] | sh->raise[par][team][1] |
+                                  sh->raise[par][team][2] | sh->raise[par][team][3]) != 0;
         if (up) {
           int at = par;
           if (!first) {
             at = (int)(xc & 1u);
             const float top = columns_over_lanes<QH>(y, lane, max_nan);
-            if (speaks) sh->top[at][half][quad][col] = top;
+            if (speaks) sh->top[at][team][quad][col] = top;
             if (!meet()) {
               ok = false;
               break;
@@ -653,8 +658,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           // weigh 0 (not -inf - -inf).  A lane per head, then all read.
           float rise = 0.f;
           if (lane < HH) {
-            const float top = max_nan(max_nan(sh->top[at][half][0][lane], sh->top[at][half][1][lane]),
-                                      max_nan(sh->top[at][half][2][lane], sh->top[at][half][3][lane]));
+            const float top = max_nan(max_nan(sh->top[at][team][0][lane], sh->top[at][team][1][lane]),
+                                      max_nan(sh->top[at][team][2][lane], sh->top[at][team][3][lane]));
             rise = max_nan(top, first ? kLowest : 0.f);
             base += rise;
           }
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 #pragma unroll
               for (int c = 0; c < HH; c += kPart) {
                 uint32_t o[kPart];
-                const uint32_t at_o = tq + C::kColO + C::NH * p + HH * half + c;
+                const uint32_t at_o = tq + C::kColO + C::NH * p + HH * team + c;
                 tmem_ldn<kPart>(at_o, o);
                 tc::tmem_wait_ld();
 #pragma unroll
@@ -699,7 +704,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
           pw[j / 2] = hi;
           pl[j / 2] = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
         }
-        const int h8 = HH * half + hq;   // the block's head, a multiple of QH
+        const int h8 = HH * team + hq;   // the block's head, a multiple of QH
         uint8_t* prow = sP + row * 128;
         auto put = [&](int h, const uint32_t (&w)[QH / 2]) {
           if constexpr (QH == 4) {
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
       const int par = (int)(xc & 1u);
       {
         const float z = columns_over_lanes<QH>(l, lane, [](float x, float y) { return x + y; });
-        if (speaks) sh->top[par][half][quad][col] = z;
+        if (speaks) sh->top[par][team][quad][col] = z;
       }
       if (!meet() || !tc_wait(&sh->pvdone, (uint32_t)((r - 1) & 1), abort_flag, a.err, lane)) {
         ok = false;
@@ -735,11 +740,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         pdl_wait();   // outputs and partial states may be in use by the previous kernel
         waited = true;
       }
-      const int h0 = C::NH * w.block + HH * half;
+      const int h0 = C::NH * w.block + HH * team;
       float inv_mine = 0.f;
       if (lane < HH) {
-        const float z = (sh->top[par][half][0][lane] + sh->top[par][half][1][lane]) +
-                        (sh->top[par][half][2][lane] + sh->top[par][half][3][lane]);
+        const float z = (sh->top[par][team][0][lane] + sh->top[par][team][1][lane]) +
+                        (sh->top[par][team][2][lane] + sh->top[par][team][3][lane]);
         inv_mine = z == 0.f ? 0.f : a.v_scale / z;   // 0: every score -inf, an empty state
         if (quad == 0 && h0 + lane < a.heads) {
           const float lse = (base + log2f(z)) * kLn2;
@@ -756,10 +761,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         uint32_t o[HH];
-        tmem_ldn<HH>(tq + C::kColO + C::NP * p + HH * half, o);
+        tmem_ldn<HH>(tq + C::kColO + C::NP * p + HH * team, o);
         if constexpr (C::kSplit) {
           uint32_t o2[HH];
-          tmem_ldn<HH>(tq + C::kColO + C::NP * p + C::NH + HH * half, o2);
+          tmem_ldn<HH>(tq + C::kColO + C::NP * p + C::NH + HH * team, o2);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < HH; ++j)
@@ -937,6 +942,14 @@ const void* kernel_of(int32_t heads) {
   }
 }
 
+int threads_of(int32_t heads) {
+  switch (latent_block_heads(heads)) {
+    case 16: return Shape16::kThreads;
+    case 32: return Shape32::kThreads;
+    default: return Shape64::kThreads;
+  }
+}
+
 // ---------------------------------------------------------------- append
 // A warp makes one cache row of a new token's latent and rotary parts, read
 // from rows of any stride (they are often column ranges of one projection's
@@ -1017,7 +1030,7 @@ cudaError_t latent_prepare(int32_t heads) {
 }
 
 cudaError_t latent_occupancy(int32_t heads, int* blocks_per_sm) {
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of(heads), kLatThreads,
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of(heads), threads_of(heads),
                                                        (size_t)latent_smem_bytes(heads));
 }
 
@@ -1032,7 +1045,7 @@ cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, cudaEve
                           cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kLatThreads);
+  cfg.blockDim = dim3(threads_of(a.heads));
   cfg.dynamicSmemBytes = (size_t)latent_smem_bytes(a.heads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
