@@ -598,9 +598,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const LatentItem w = item_at(a, it);
       // l: this token's sums.  base: lane j holds the base (log2 units) of the
       // team's head j; every warp keeps its own copy
-      float l[QH], base = 0.f;
+      float l[QH], m[QH], base = 0.f;   // m: the bases of this thread's heads
 #pragma unroll
-      for (int j = 0; j < QH; ++j) l[j] = 0.f;
+      for (int j = 0; j < QH; ++j) l[j] = m[j] = 0.f;
       for (int t = w.tb; t < w.te && ok; t += kTile, ++r) {
         const int b = r & 1;
         // P of the tile before has been read (its buffer is written below,
@@ -623,8 +623,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         float over = -CUDART_INF_F;
 #pragma unroll
         for (int j = 0; j < QH; ++j) {
-          const float m = __shfl_sync(kFull, base, hq + j);
-          y[j] = live ? fmaf(__uint_as_float(sv[j]), a.scale_log2, -m) : -CUDART_INF_F;
+          y[j] = live ? fmaf(__uint_as_float(sv[j]), a.scale_log2, -m[j]) : -CUDART_INF_F;
           over = fmaxf(over, y[j]);
         }
         // the four warps of this team agree whether to raise their bases; an
@@ -688,6 +687,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           for (int j = 0; j < QH; ++j) {
             const float up_j = __shfl_sync(kFull, rise, hq + j);
             if (!first) l[j] *= exp2f(-up_j);
+            m[j] += up_j;
             y[j] -= up_j;
           }
         }
@@ -696,8 +696,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         uint32_t pw[QH / 2], pl[QH / 2];
 #pragma unroll
         for (int j = 0; j < QH; j += 2) {
-          const float p0 = live ? fast_exp2(y[j]) : 0.f;
-          const float p1 = live ? fast_exp2(y[j + 1]) : 0.f;
+          const float p0 = fast_exp2(y[j]);   // 0 past the last token
+          const float p1 = fast_exp2(y[j + 1]);
           l[j] += p0;
           l[j + 1] += p1;
           const uint32_t hi = pack_bf16(p0, p1);
