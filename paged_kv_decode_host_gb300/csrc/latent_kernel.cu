@@ -117,10 +117,16 @@ struct LatentShape {
   static constexpr int NP = kSplit ? 2 * NH : NH;   // columns of an O^T product
   // A tile's copies leave when the products of the tile two before are done,
   // and the way from there to its scores is the longest part of a 64-head
-  // tile's round: fetching it into L2 a tile earlier takes 5 % off (128 heads,
-  // 32 requests: 81 -> 78 us).  Fewer heads are bound by HBM, where the extra
-  // requests only disturb (50 -> 53 us).
+  // tile's round.  Where two blocks of heads read the same rows, fetching them
+  // into L2 a tile earlier pays (128 heads, 32 requests: 75.5 -> 71.4 us); one
+  // block is nearer HBM's rate, which the extra requests disturb (64 heads, 32
+  // requests: 46.3 -> 47.7; 16 heads, 64 requests: 50 -> 53; but 40 heads,
+  // 100,003 tokens: 34.2 -> 33.8).
   static constexpr bool kPrefetch = NH == 64;
+  // What a round cannot go below is the shared memory's rate: the products read
+  // their operands at about 110 bytes a cycle (of 128), 147 KB for a 64-head
+  // tile's scores and 98 KB for its P.V, beside 74 KB of copies: 2,550 cycles
+  // of some 3,250.
   static constexpr uint32_t kColO = 0, kColS = kPairs * NP;
   static_assert(NH % 16 == 0 && NH <= 64 && kColS + 2 * NH <= 512, "shape");
 };
@@ -429,7 +435,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
         if (!ok) break;
         extra = 0;
-        if constexpr (C::kPrefetch) {
+        if (C::kPrefetch && a.blocks > 1) {
           // the next tile into L2 while its slots are in use (a lane per box
           // and region)
           const int next = kBoxes * (k + 1) + lane % kBoxes, g = lane / kBoxes;
