@@ -268,6 +268,7 @@ template <int kThreads, bool kCluster, bool kMove>
 __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   constexpr int kWarps = kThreads / 32;
+  pdl_wait();   // the launch alone overlaps the kernel before (98.1 -> 96.2 us, 92.2 -> 90.3)
   if (!kMove) pdl_launch_dependents();
   int blocks = 1, rank = 0;
   if constexpr (kCluster) {
@@ -586,13 +587,15 @@ cudaError_t launch_choose(const EvictArgs& a, const EvictPlan& p, cudaStream_t s
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.blocks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.blocks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kCluster ? 1 : 0;
+  cfg.numAttrs = kCluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, f, a);
 }
 
