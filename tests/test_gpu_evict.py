@@ -522,3 +522,51 @@ def test_evict_workspace_belongs_to_the_calls_stream(monkeypatch):
     evict_reference(kvs, ws, ps, t, [3000], seen, 1500, 16, "NHD", 0, 0, True)
     same(([x.view(torch.int16).cpu().numpy() for x in gpu_state[0]],
           *[[x.cpu().numpy() for x in y] for y in gpu_state[1:]]), (kvs, ws, ps))
+
+
+def late(target, right, cycles=400_000):
+    """A kernel that writes `right` over `target`, a while after the calls that follow were launched."""
+    wrong = torch.full_like(target, float("nan")) if target.is_floating_point() else torch.zeros_like(target)
+    target.copy_(wrong)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(cycles)
+    torch.mul(right, 1, out=target)
+
+
+@gpu
+def test_calls_wait_for_the_kernel_before():
+    """Weight sums, evictions and latent appends are launched early: what they read and write is the
+    kernel's before them until it has ended."""
+    n, budget = 3000, 1500
+    s = Step(2, 4, [n, 40], 16, seed=11)
+    lse, start = s.lse.clone(), s.weights.clone()
+    want = s.expected(start, [0, 0])
+    late(s.lse, lse)
+    near(s.dec.accumulate_weights(s.q, s.kv, s.lse, s.weights), want)
+    s.weights.copy_(start)
+    late(s.weights, start)
+    near(s.dec.accumulate_weights(s.q, s.kv, s.lse, s.weights), want)
+
+    t, kvs, ws, ps, seen = evict_case(2, 16, [n], budget, seed=5)
+    for few in (n - 3, budget):                    # one kernel, and two
+        g = [to_gpu(kvs[0], torch.bfloat16)], [torch.from_numpy(ws[0]).cuda()], [torch.from_numpy(ps[0]).cuda()]
+        d = [torch.from_numpy(x).cuda() for x in t[:3]] + [torch.tensor(seen, dtype=torch.int32, device="cuda")]
+        for target in (g[1][0], g[2][0], d[0]):
+            late(target, target.clone())
+            pkd.evict_kv(*g, *d, few, max_len=n)
+            ref = [[x.copy() for x in y] for y in (kvs, ws, ps)]
+            evict_reference(*ref, t, [n], seen, few, 16, "NHD", 0, 0, True)
+            same(([x.view(torch.int16).cpu().numpy() for x in g[0]],
+                  *[[x.cpu().numpy() for x in y] for y in g[1:]]), ref)
+            for x, y in zip((g[0][0].view(torch.int16), g[1][0], g[2][0]), (kvs[0], ws[0], ps[0])):
+                x.copy_(torch.from_numpy(y))
+
+    cache = torch.zeros(t[3], 16, 576, device="cuda").bfloat16()
+    new = torch.randn(1, 576, device="cuda").bfloat16()
+    row, at = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), n - 1, dtype=torch.int32, device="cuda")
+    slot = int(t[1][(n - 1) // 16]), (n - 1) % 16
+    for target in (new, at, cache):
+        late(target, target.clone())
+        pkd.append_latent(new[:, :512], new[:, 512:], row, at, *d[:3], cache)
+        assert torch.equal(cache[slot], new[0]) and cache.count_nonzero() == new.count_nonzero()
+        cache.zero_()
