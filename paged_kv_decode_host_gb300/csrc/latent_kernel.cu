@@ -619,19 +619,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const bool first = t == w.tb;
         const bool live = row < w.te - t;
         tc_fence_after();
-        uint32_t sv[QH];
-        tmem_ld_rows16<QH>(tq + C::kColS + C::NH * b + HH * team, sv);
-        tc::tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->sfree[b]);
-        float y[QH];   // scores over the base
+        float y[QH];   // scores over the base (log2 units)
+        auto read_scores = [&](bool over_base) {
+          uint32_t sv[QH];
+          tmem_ld_rows16<QH>(tq + C::kColS + C::NH * b + HH * team, sv);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < QH; ++j)
+            y[j] = live ? fmaf(__uint_as_float(sv[j]), a.scale_log2, over_base ? -m[j] : 0.f)
+                        : -CUDART_INF_F;
+        };
+        read_scores(true);   // (an item's first tile: over 0)
         float over = -CUDART_INF_F;
 #pragma unroll
-        for (int j = 0; j < QH; ++j) {
-          y[j] = live ? fmaf(__uint_as_float(sv[j]), a.scale_log2, -m[j]) : -CUDART_INF_F;
-          over = fmaxf(over, y[j]);
-        }
+        for (int j = 0; j < QH; ++j) over = fmaxf(over, y[j]);
         // the four warps of this team agree whether to raise their bases; an
         // item's first tile always does, and brings its maxima along
         const int par = (int)(xc & 1u);
@@ -652,6 +653,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           int at = par;
           if (!first) {
             at = (int)(xc & 1u);
+            // maxima of the scores themselves: over a base that lies far
+            // below, as after tiles of masked tokens, they are rounded away
+            read_scores(false);
             const float top = columns_over_lanes<QH>(y, lane, max_nan);
             if (speaks) sh->top[at][team][quad][col] = top;
             if (!meet()) {
@@ -659,14 +663,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               break;
             }
           }
-          // how far each base rises; it stays finite, so that scores of -inf
-          // weigh 0 (not -inf - -inf).  A lane per head, then all read.
+          // the new bases, and how far they rise.  A base stays finite, so that
+          // scores of -inf weigh 0 (not -inf - -inf).  A lane per head, then
+          // all read.
           float rise = 0.f;
           if (lane < HH) {
             const float top = max_nan(max_nan(sh->top[at][team][0][lane], sh->top[at][team][1][lane]),
                                       max_nan(sh->top[at][team][2][lane], sh->top[at][team][3][lane]));
-            rise = max_nan(top, first ? kLowest : 0.f);
-            base += rise;
+            const float raised = max_nan(top, first ? kLowest : base);
+            rise = raised - base;
+            base = raised;
           }
           __syncwarp();
           if (!first) {
@@ -691,10 +697,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < QH; ++j) {
-            const float up_j = __shfl_sync(kFull, rise, hq + j);
-            if (!first) l[j] *= exp2f(-up_j);
-            m[j] += up_j;
-            y[j] -= up_j;
+            const float now = __shfl_sync(kFull, base, hq + j);
+            if (!first) l[j] *= exp2f(m[j] - now);
+            m[j] = now;
+            y[j] -= now;
           }
         }
         // weights 2^y; this thread's part of a row of P, 16-byte pieces of 8
@@ -728,7 +734,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->pfull);
+        if (lane == 0) {
+          mbar_arrive(&sh->pfull);
+          // (the scores of the tile after next wait for this tile's P.V anyway)
+          mbar_arrive(&sh->sfree[b]);
+        }
       }
       if (!ok) break;
       // ---- epilogue: sums over the tokens in a fixed order
