@@ -430,8 +430,10 @@ int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const fl
  *       call's own until its kernels are done (NULL when that is 0)
  *   D * element bytes: a multiple of 16; Hkv * D * element bytes <= 32,768
  *   err     : device int32 word or NULL
- * A request whose table row is wrong, is longer than max_len or names a page
- * outside the pool is left as it is and PKD_DEV_ERR_BOUNDS is OR-ed into *err.
+ * A request whose table row is wrong, is longer than max_len or (over the
+ * budget) names a page outside the pool is left as it is and PKD_DEV_ERR_BOUNDS
+ * is OR-ed into *err, also where max_len is at most the budget: a kernel then
+ * only looks the rows over, and without err none is launched.
  * One or two kernels, stream-ordered, capturable, the same bits every run.
  * Errors: INVALID_ARG, CAPACITY (max_len), WORKSPACE_TOO_SMALL, CUDA. */
 int pkd_evict_kv(int32_t layers, void *const *kv, float *const *weights,

@@ -1144,7 +1144,8 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
     closed up without keeping their order: afterwards the request's first
     ``budget`` slots are its cache (:func:`evicted_table` gives the table).
     err: optional int32 CUDA tensor of one element, flagged for requests whose
-    table is wrong (they are left as they are)."""
+    table row is wrong or that are longer than max_len (they are left as they
+    are)."""
     import torch
     layers = len(kv_caches)
     if not 1 <= layers <= 128 or len(weights) != layers or len(positions) != layers:

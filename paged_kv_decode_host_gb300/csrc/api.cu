@@ -836,9 +836,11 @@ int pkd_evict_kv(int32_t layers, void* const* kv, float* const* weights,
       ((int64_t)head_dim * elem) % 16 != 0 || (int64_t)head_dim * elem > 16384 ||
       (int64_t)head_dim * elem * num_kv_heads > 32768)
     return PKD_E_INVALID_ARG;
-  if (batch == 0 || max_len <= budget) return PKD_OK;   // nothing is over the budget
+  // nothing is over the budget, and nobody asks for what is wrong in the table
+  if (batch == 0 || (max_len <= budget && err == nullptr)) return PKD_OK;
   if (!indptr || !indices || !last_page_len || !seen || !aligned(err, 4)) return PKD_E_INVALID_ARG;
-  const size_t need = evict_workspace_bytes(layers, batch, num_kv_heads, per_head, max_len, budget);
+  const size_t need =
+      max_len > budget ? evict_workspace_bytes(layers, batch, num_kv_heads, per_head, max_len, budget) : 0;
   if (need > 0 && (d_workspace == nullptr || !aligned(d_workspace, 16))) return PKD_E_INVALID_ARG;
   if (workspace_bytes < need) return PKD_E_WORKSPACE_TOO_SMALL;
   const bool hnd = (flags & PKD_FLAG_HND) != 0;

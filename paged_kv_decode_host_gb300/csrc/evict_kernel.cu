@@ -541,6 +541,16 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   move_pairs(a, sh, j, kept, before, split, a.splits);
 }
 
+// Where max_len is at most the budget nothing is cut; what is wrong is flagged
+// all the same, a thread per request.
+constexpr int kCheckThreads = 128;
+__global__ void __launch_bounds__(kCheckThreads) evict_check_kernel(const __grid_constant__ EvictArgs a) {
+  pdl_wait();
+  const int req = (int)(blockIdx.x * kCheckThreads + threadIdx.x);
+  Job j;
+  if (req < a.batch) job_of(a, req, true, &j);
+}
+
 constexpr int kSms = 152;
 
 struct EvictPlan {
@@ -599,6 +609,20 @@ cudaError_t launch_choose(const EvictArgs& a, const EvictPlan& p, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, f, a);
 }
 
+cudaError_t launch_check(EvictArgs& a, cudaStream_t stream) {
+  a.layers = a.per_head = 0;   // jobs are requests
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.batch + kCheckThreads - 1) / kCheckThreads));
+  cfg.blockDim = dim3(kCheckThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_check_kernel, a);
+}
+
 }  // namespace
 
 size_t evict_workspace_bytes(int layers, int batch, int hkv, int per_head, int max_len, int budget) {
@@ -607,6 +631,7 @@ size_t evict_workspace_bytes(int layers, int batch, int hkv, int per_head, int m
 }
 
 cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
+  if (a.max_len <= a.budget) return launch_check(a, stream);
   const EvictPlan p = plan_for(a.layers, a.batch, a.hkv, a.per_head, a.max_len, a.budget);
   a.splits = p.splits;
   a.page_shift = page_shift_of(a.page_size);
