@@ -537,10 +537,7 @@ int pkd_plan_host_cascade(const pkd_config *cfg, const int32_t *group_indptr,
  *   off[2] units[num_units][2] = {req, num_chunks}
  *   off[3] merge_indptr[num_units + 1]
  *   off[4] page_list[nnz]    (the CSR indices, unchanged)
- *   off[5] total words (the page list's capacity, rounded up to 4, then
- *          4 (max_batch + 1) words: plain plans put {16-token tiles before,
- *          first page's index, tokens, 0} of every request, and the total of
- *          tiles, behind the page list's nnz words, rounded up to 4)
+ *   off[5] total words
  * Header words 0..31 hold: magic, batch, Hq, Hkv, D, P, num_ctas,
  * num_items, num_units, num_slots, chunk, alpha, nnz, makespan (clamped to
  * int32), split floor, requests per block, the most chunks of any split

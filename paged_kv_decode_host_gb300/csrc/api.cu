@@ -431,7 +431,7 @@ size_t pkd_workspace_bytes(const pkd_config* cfg) {
   int smem = 0;
   // the workspace layout does not depend on the producer
   if (resolve_ctas(cfg, kind_for(cfg, nullptr), &n_cta, &smem) != PKD_OK) return 0;
-  return plan_layout(*cfg, n_cta).total_bytes;
+  return context_layout(*cfg, n_cta).total_bytes;
 }
 
 int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
@@ -461,7 +461,7 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
     delete ctx;
     return PKD_E_CUDA;
   }
-  ctx->layout = plan_layout(*cfg, ctx->n_cta);
+  ctx->layout = context_layout(*cfg, ctx->n_cta);
   if (workspace_bytes < ctx->layout.total_bytes) {
     delete ctx;
     return PKD_E_WORKSPACE_TOO_SMALL;
@@ -511,8 +511,8 @@ void pkd_destroy(pkd_ctx* ctx) {
 
 }  // extern "C"
 
-// Plan into the next staging buffer (plan_fn(words, info) runs the planner)
-// and publish it.
+// Plan into the next staging buffer (plan_fn(words, info, end) runs the
+// planner; it may write on behind the page list, up to *end) and publish it.
 template <typename PlanFn>
 static int plan_and_publish(pkd_ctx* ctx, PlanFn plan_fn, void* stream, uint64_t* epoch) {
   if (ctx == nullptr) return PKD_E_INVALID_ARG;
@@ -525,13 +525,14 @@ static int plan_and_publish(pkd_ctx* ctx, PlanFn plan_fn, void* stream, uint64_t
   int32_t* words = ctx->staging[k];
   pkd_plan_info info{};
   int st = PKD_OK;
+  int64_t end = 0;   // words to upload
   try {
-    st = plan_fn(words, &info);
+    st = plan_fn(words, &info, &end);
   } catch (...) {   // the planner's working arrays found no memory
     st = PKD_E_CAPACITY;
   }
   if (st != PKD_OK) return st;
-  const Layout& L = ctx->layout;
+  if (end == 0) end = ctx->layout.page_list + info.nnz;
   // two copies in stream order: first the body (cta queues, items, units,
   // merge map and the page list behind them, as laid out in the workspace),
   // then the header with the plan's epoch word, so that a kernel that sees
@@ -539,9 +540,7 @@ static int plan_and_publish(pkd_ctx* ctx, PlanFn plan_fn, void* stream, uint64_t
   // sees the whole schedule
   words[H_EPOCH] = epoch_word(ctx->epoch + 1);
   if (cudaMemcpyAsync(ctx->ws + (size_t)H_WORDS * 4, words + H_WORDS,
-                      ((size_t)request_words(L.page_list, info.nnz) +
-                       (size_t)kRequestWords * ((size_t)info.batch + 1) - H_WORDS) * 4,
-                      cudaMemcpyHostToDevice, s) != cudaSuccess ||
+                      ((size_t)end - H_WORDS) * 4, cudaMemcpyHostToDevice, s) != cudaSuccess ||
       cudaMemcpyAsync(ctx->ws, words, (size_t)H_WORDS * 4, cudaMemcpyHostToDevice, s) !=
           cudaSuccess)
     return PKD_E_CUDA;
@@ -563,9 +562,12 @@ int pkd_plan(pkd_ctx* ctx, const int32_t* indptr, const int32_t* indices,
   if (ctx == nullptr || ctx->kind.cascade) return PKD_E_INVALID_ARG;
   return plan_and_publish(
       ctx,
-      [&](int32_t* words, pkd_plan_info* info) {
-        return plan_schedule_grouped(ctx->cfg, ctx->n_cta, ctx->layout, nullptr, batch, indptr,
-                                     indices, last_page_len, words, info);
+      [&](int32_t* words, pkd_plan_info* info, int64_t* end) {
+        const int st = plan_schedule_grouped(ctx->cfg, ctx->n_cta, ctx->layout, nullptr, batch,
+                                             indptr, indices, last_page_len, words, info);
+        if (st == PKD_OK && has_requests(ctx->cfg))
+          *end = write_requests(ctx->layout, ctx->cfg.page_size, indptr, last_page_len, batch, words);
+        return st;
       },
       stream, epoch);
 }
@@ -577,7 +579,7 @@ int pkd_plan_shared(pkd_ctx* ctx, const int32_t* group_indptr, int32_t num_group
   if (num_groups > 0 && group_indptr == nullptr) return PKD_E_INVALID_ARG;
   return plan_and_publish(
       ctx,
-      [&](int32_t* words, pkd_plan_info* info) {
+      [&](int32_t* words, pkd_plan_info* info, int64_t*) {
         return plan_schedule_grouped(ctx->cfg, ctx->n_cta, ctx->layout, group_indptr, num_groups,
                                      indptr, indices, last_page_len, words, info);
       },
@@ -591,7 +593,7 @@ int pkd_plan_cascade(pkd_ctx* ctx, const int32_t* group_indptr, int32_t num_grou
   if (ctx == nullptr || !ctx->kind.cascade) return PKD_E_INVALID_ARG;
   return plan_and_publish(
       ctx,
-      [&](int32_t* words, pkd_plan_info* info) {
+      [&](int32_t* words, pkd_plan_info* info, int64_t*) {
         return plan_schedule_cascade(ctx->cfg, ctx->n_cta, ctx->layout, group_indptr, num_groups,
                                      p_indptr, p_indices, p_last, s_indptr, s_indices, s_last,
                                      words, info);

@@ -1,6 +1,6 @@
-// The schedule layout of contexts and host plans: make_layout's, with room for
-// the requests' entries behind the page list and for the items of latent
-// plans; and the latent planner.
+// The schedule layout of host plans (make_layout's, with room for the items of
+// latent plans) and of contexts (with room for the requests' entries behind
+// the page list, where they have them); and the latent planner.
 #pragma once
 
 #include "latent.h"
@@ -8,9 +8,11 @@
 
 namespace pkd {
 
-// Behind the page list's nnz words (rounded up to 4), plain plans hold an
-// entry per request, and one more with the total: 16-token tiles of the
-// requests before, index of the first page in the page list, tokens, 0.
+// The entries that pkd_accumulate_weights cuts its work from: behind the page
+// list's nnz words (rounded up to 4) one per request, and one more with the
+// total: 16-token tiles of the requests before, index of the first page in the
+// page list, tokens, 0.  Only contexts that can accumulate hold them; the
+// host plans and the other contexts do without.
 constexpr int kRequestWords = 4, kRequestTile = 16;
 __host__ __device__ inline int64_t request_words(int64_t page_list, int64_t nnz) {
   return page_list + (nnz + 3) / 4 * 4;
@@ -24,7 +26,17 @@ inline Layout plan_layout(const pkd_config& c, int64_t n_cta) {
   // refused for want of items)
   const int64_t rows = (int64_t)latent_blocks(c.num_qo_heads) * c.max_batch;
   if (is_latent(c)) room.max_batch = (int32_t)(rows < 0x7fffffff ? rows : 0x7fffffff);
-  Layout L = make_layout(room, n_cta);
+  return make_layout(room, n_cta);
+}
+
+inline bool has_requests(const pkd_config& c) {
+  return (c.flags & (PKD_FLAG_SHARED_PREFIX | PKD_FLAG_CASCADE | PKD_FLAG_LATENT)) == 0;
+}
+// The layout of a context's workspace and staging: plan_layout's offsets, then
+// the requests' entries where it has them.
+inline Layout context_layout(const pkd_config& c, int64_t n_cta) {
+  Layout L = plan_layout(c, n_cta);
+  if (!has_requests(c)) return L;
   // what lies behind the schedule words moves along by whole 256 bytes
   L.words = request_words(L.page_list, c.max_num_pages) +
             (int64_t)kRequestWords * ((int64_t)c.max_batch + 1);
@@ -35,6 +47,11 @@ inline Layout plan_layout(const pkd_config& c, int64_t n_cta) {
   L.total_bytes += more;
   return L;
 }
+
+// The entries of a table that a plan has accepted, behind the plan's words;
+// returns the words up to their end.
+int64_t write_requests(const Layout& L, int32_t page_size, const int32_t* indptr,
+                       const int32_t* last, int32_t batch, int32_t* words);
 
 // Plans of latent contexts (planner.cpp; plan_schedule_grouped calls it).
 int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,

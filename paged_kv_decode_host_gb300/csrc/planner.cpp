@@ -174,21 +174,6 @@ int64_t lpt(const std::vector<Item>& items, int32_t n_cta, std::vector<int32_t>*
   return makespan;
 }
 
-// The requests' entries behind the page list.
-void write_requests(int32_t* words, const Layout& L, int64_t nnz, const std::vector<int64_t>& lens,
-                    const int32_t* indptr) {
-  int32_t* w = words + request_words(L.page_list, nnz);
-  int64_t tiles = 0;
-  for (size_t i = 0; i <= lens.size(); ++i, w += kRequestWords) {
-    const bool end = i == lens.size();
-    w[0] = (int32_t)std::min<int64_t>(tiles, 0x7fffffff);
-    w[1] = end ? 0 : indptr[i];
-    w[2] = end ? 0 : (int32_t)lens[i];
-    w[3] = 0;
-    if (!end) tiles += ceil_div(lens[i], kRequestTile);
-  }
-}
-
 struct Block {
   int32_t req_first, n_req, table_row;
 };
@@ -272,7 +257,6 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     // pages at indptr[row] + t / P), range-checked in the same pass
     if (!copy_checked(indices, words + L.page_list, nnz, cfg.num_pages)) return PKD_E_BAD_TABLE;
   }
-  if (!group_indptr) write_requests(words, L, nnz, row_len, indptr);
 
   // ---- row blocks
   std::vector<Block>& blocks = sc.blocks;
@@ -453,6 +437,23 @@ int plan_schedule_grouped(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   return PKD_OK;
 }
 
+int64_t write_requests(const Layout& L, int32_t page_size, const int32_t* indptr,
+                       const int32_t* last, int32_t batch, int32_t* words) {
+  int32_t* w = words + request_words(L.page_list, batch > 0 ? indptr[batch] : 0);
+  int64_t tiles = 0;
+  for (int32_t i = 0; i < batch; ++i, w += kRequestWords) {
+    const int64_t len = (int64_t)page_size * (indptr[i + 1] - indptr[i] - 1) + last[i];
+    w[0] = (int32_t)std::min<int64_t>(tiles, 0x7fffffff);
+    w[1] = indptr[i];
+    w[2] = (int32_t)len;
+    w[3] = 0;
+    tiles += ceil_div(len, kRequestTile);
+  }
+  w[0] = (int32_t)std::min<int64_t>(tiles, 0x7fffffff);
+  w[1] = w[2] = w[3] = 0;
+  return w + kRequestWords - words;
+}
+
 // ---------------------------------------------------------------- latent
 //
 // Plans of latent contexts.  Their kernel's time is its tokens (about 27 ns
@@ -536,7 +537,6 @@ int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     if (indices == nullptr) return PKD_E_INVALID_ARG;
     if (!copy_checked(indices, words + L.page_list, nnz, cfg.num_pages)) return PKD_E_BAD_TABLE;
   }
-  write_requests(words, L, nnz, lens, indptr);
   const int32_t blocks = latent_blocks(cfg.num_qo_heads);
   const int32_t nv = std::max(1, n_cta / blocks);
   const int64_t alpha = cfg.alpha < 0 ? kLatentAlpha : cfg.alpha;
