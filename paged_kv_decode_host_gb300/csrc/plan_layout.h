@@ -21,12 +21,24 @@ __host__ __device__ inline int64_t request_words(int64_t page_list, int64_t nnz)
 inline bool is_latent(const pkd_config& c) { return (c.flags & PKD_FLAG_LATENT) != 0; }
 
 inline Layout plan_layout(const pkd_config& c, int64_t n_cta) {
-  pkd_config room = c;
+  if (!is_latent(c)) return make_layout(c, n_cta);
   // latent plans: an item per block of heads (plans beyond the clamp are
   // refused for want of items)
-  const int64_t rows = (int64_t)latent_blocks(c.num_qo_heads) * c.max_batch;
-  if (is_latent(c)) room.max_batch = (int32_t)(rows < 0x7fffffff ? rows : 0x7fffffff);
-  return make_layout(room, n_cta);
+  pkd_config room = c;
+  const int64_t blocks = latent_blocks(c.num_qo_heads), rows = blocks * c.max_batch;
+  room.max_batch = (int32_t)(rows < 0x7fffffff ? rows : 0x7fffffff);
+  Layout L = make_layout(room, n_cta);
+  // A plan cuts at most once between two neighbouring stretches, of n_cta /
+  // blocks in all, and k cuts leave a request in k + 1 <= 2 k parts; a part's
+  // slot is one for all blocks of heads.  (Slots by items, as other plans need
+  // them, were 2 to 11 times as many: 431 MB instead of 39 for 128 heads and
+  // batches of up to 512.)
+  const int64_t stretches = n_cta < blocks ? 1 : n_cta / blocks;
+  L.max_slots = 2 * (stretches - 1);
+  const size_t row = (size_t)L.max_slots * c.num_qo_heads * sizeof(float);
+  L.l_part_byte = (size_t)align_up((int64_t)(L.o_part_byte + row * c.head_dim), 256);
+  L.total_bytes = (size_t)align_up((int64_t)(L.l_part_byte + row), 256);
+  return L;
 }
 
 inline bool has_requests(const pkd_config& c) {
