@@ -85,6 +85,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
 // 45 to 54 cycles against 28 to 38, and two tiles of 128 tokens do not fit
 // shared memory beside the queries.)
 constexpr int kTile = 64, kBoxes = kTile / 16;
+static_assert(32 % kBoxes == 0, "a warp's 32 page ids are whole tiles'");
 constexpr int kStages = 2;
 // 8 tokens of a region: the stride of the products' 8-row groups
 __host__ __device__ constexpr int group_bytes(int g) { return region_chunks(g) * 1024; }
@@ -405,11 +406,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int nbox = min(kBoxes, (w.te - t + 15) >> 4);
         const int st = r % kStages;
         const uint32_t use = (uint32_t)(r / kStages);
-        // lane j copies box j of the tile
-        const int box = kBoxes * k + lane % kBoxes;
-        const int late = __shfl_sync(kFull, next_page, box & 31);
-        int page = __shfl_sync(kFull, my_page, box & 31);
-        if (box >= base + 32) page = late;
+        // lane j copies box j of the tile; a tile's boxes, and the next
+        // tile's once the window has moved on, lie in one window of 32
+        int page = __shfl_sync(kFull, my_page, (kBoxes * k + lane % kBoxes) & 31);
         if (kBoxes * (k + 1) >= base + 32) {
           base += 32;
           my_page = next_page;
@@ -439,9 +438,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           // the next tile into L2 while its slots are in use (a lane per box
           // and region)
           const int next = kBoxes * (k + 1) + lane % kBoxes, g = lane / kBoxes;
-          const int pa = __shfl_sync(kFull, my_page, next & 31);
-          const int pb = __shfl_sync(kFull, next_page, next & 31);
-          const int np = next >= base + 32 ? pb : pa;
+          const int np = __shfl_sync(kFull, my_page, next & 31);
           if (g < kRegions && next < boxes && (unsigned)np < (unsigned)a.num_pages)
             tensor_prefetch(&a.kv_map[g], region_first(g), (t + kTile + 16 * (lane % kBoxes)) % P / 8,
                             np);
