@@ -51,7 +51,8 @@ extern "C" {
 #define PKD_E_WORKSPACE_TOO_SMALL -4
 #define PKD_E_NO_PLAN -5            /* run before any plan                  */
 #define PKD_E_STALE_PLAN -6         /* run against another plan's epoch    */
-#define PKD_E_CAPACITY -7           /* batch or page count above capacity  */
+#define PKD_E_CAPACITY -7           /* batch or page count above capacity, or
+                                       no host memory for the planner      */
 #define PKD_E_CUDA -8               /* a CUDA runtime call failed          */
 #define PKD_E_DEVICE -9             /* the device reported an error word   */
 #define PKD_E_SCRATCH_LIMIT -10     /* needs more than the static scratch   */

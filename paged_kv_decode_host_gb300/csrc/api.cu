@@ -69,6 +69,17 @@ struct pkd_graph {
 
 namespace {
 
+// A planner's status; its working arrays may find no memory, and no exception
+// leaves a C entry point.
+template <typename F>
+int planned(F plan) {
+  try {
+    return plan();
+  } catch (...) {
+    return PKD_E_CAPACITY;
+  }
+}
+
 bool valid_group(int g) { return g == 1 || g == 2 || g == 4 || g == 8; }
 
 // The consumer flags exclude each other; the shared-prefix kernel exists for
@@ -382,8 +393,10 @@ int pkd_plan_host_shared(const pkd_config* cfg, const int32_t* group_indptr, int
   if (num_groups > 0 && group_indptr == nullptr) return PKD_E_INVALID_ARG;
   Layout L = plan_layout(*cfg, cfg->num_ctas);
   if (max_words < (size_t)L.words) return PKD_E_INVALID_ARG;
-  return plan_schedule_grouped(*cfg, cfg->num_ctas, L, group_indptr, num_groups, indptr, indices,
-                               last_page_len, host_words, info);
+  return planned([&] {
+    return plan_schedule_grouped(*cfg, cfg->num_ctas, L, group_indptr, num_groups, indptr, indices,
+                                 last_page_len, host_words, info);
+  });
 }
 
 int pkd_plan_host_cascade(const pkd_config* cfg, const int32_t* group_indptr,
@@ -397,8 +410,10 @@ int pkd_plan_host_cascade(const pkd_config* cfg, const int32_t* group_indptr,
     return PKD_E_INVALID_ARG;
   Layout L = plan_layout(*cfg, cfg->num_ctas);
   if (max_words < (size_t)L.words) return PKD_E_INVALID_ARG;
-  return plan_schedule_cascade(*cfg, cfg->num_ctas, L, group_indptr, num_groups, p_indptr,
-                               p_indices, p_last, s_indptr, s_indices, s_last, host_words, info);
+  return planned([&] {
+    return plan_schedule_cascade(*cfg, cfg->num_ctas, L, group_indptr, num_groups, p_indptr,
+                                 p_indices, p_last, s_indptr, s_indices, s_last, host_words, info);
+  });
 }
 
 int pkd_advise_format(const pkd_config* cfg, const int32_t* group_indptr, int32_t num_groups,
@@ -408,8 +423,10 @@ int pkd_advise_format(const pkd_config* cfg, const int32_t* group_indptr, int32_
   if (st != PKD_OK) return st;
   if (cfg->num_ctas < 2 || advice == nullptr || !(cfg->flags & PKD_FLAG_CASCADE))
     return PKD_E_INVALID_ARG;
-  return advise_format(*cfg, cfg->num_ctas, group_indptr, num_groups, p_indptr, p_last, s_indptr,
-                       s_last, advice);
+  return planned([&] {
+    return advise_format(*cfg, cfg->num_ctas, group_indptr, num_groups, p_indptr, p_last, s_indptr,
+                         s_last, advice);
+  });
 }
 
 int pkd_plan_host(const pkd_config* cfg, const int32_t* indptr, const int32_t* indices,
@@ -421,8 +438,10 @@ int pkd_plan_host(const pkd_config* cfg, const int32_t* indptr, const int32_t* i
     return PKD_E_INVALID_ARG;
   Layout L = plan_layout(*cfg, cfg->num_ctas);
   if (max_words < (size_t)L.words) return PKD_E_INVALID_ARG;
-  return plan_schedule(*cfg, cfg->num_ctas, L, indptr, indices, last_page_len, batch,
-                       host_words, info);
+  return planned([&] {
+    return plan_schedule(*cfg, cfg->num_ctas, L, indptr, indices, last_page_len, batch,
+                         host_words, info);
+  });
 }
 
 size_t pkd_workspace_bytes(const pkd_config* cfg) {
@@ -524,13 +543,8 @@ static int plan_and_publish(pkd_ctx* ctx, PlanFn plan_fn, void* stream, uint64_t
   }
   int32_t* words = ctx->staging[k];
   pkd_plan_info info{};
-  int st = PKD_OK;
   int64_t end = 0;   // words to upload
-  try {
-    st = plan_fn(words, &info, &end);
-  } catch (...) {   // the planner's working arrays found no memory
-    st = PKD_E_CAPACITY;
-  }
+  const int st = planned([&] { return plan_fn(words, &info, &end); });
   if (st != PKD_OK) return st;
   if (end == 0) end = ctx->layout.page_list + info.nnz;
   // two copies in stream order: first the body (cta queues, items, units,
