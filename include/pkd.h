@@ -158,7 +158,9 @@ typedef struct pkd_config {
  * Plans (pkd_plan) cut the requests' tokens, laid end to end, into equal
  * stretches, one per CTA -- per CTA pair above 64 heads, a work item covering
  * up to 64; alpha < 0 selects 128, min_chunk_tokens < 0 128 (256 above 32
- * heads).  Graphs replay with the batch they were captured with. */
+ * heads).  Graphs replay with the batch they were captured with; a call that
+ * the caller captured does no work under a later plan of more requests, and
+ * ORs PKD_DEV_ERR_BOUNDS into the device error word. */
 #define PKD_FLAG_LATENT 1024u
 
 typedef struct pkd_ctx pkd_ctx;
@@ -395,8 +397,9 @@ int pkd_append_kv_layers(int32_t layers, const void *const *k_new, const void *c
  * Slots behind a request's end and pages of no request keep their values.
  * A page has one owner: a plan that names a page twice is BAD_TABLE (a graph
  * replayed under a later plan relies on that plan being free of repeats).
- * expect_epoch as in pkd_run.  One kernel, stream-ordered, capturable, the
- * same bits every run.
+ * expect_epoch as in pkd_run.  One kernel, stream-ordered, capturable (under a
+ * later plan of more requests a captured call does no work and ORs
+ * PKD_DEV_ERR_BOUNDS into the device error word), the same bits every run.
  * Errors: INVALID_ARG, NO_PLAN, STALE_PLAN, BAD_TABLE, CAPACITY (no host
  * memory for the check), CUDA. */
 int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const float *lse,

@@ -247,6 +247,7 @@ int launch_latent_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, fl
   a.blocks = latent_blocks(c.num_qo_heads);
   a.page_size = c.page_size;
   a.num_pages = c.num_pages;
+  a.batch = ctx->info.batch;
   a.scale_log2 = (float)(1.4426950408889634 * (double)scale);
   a.v_scale = v_scale;
   a.wait_epoch = wait_epoch;
@@ -810,6 +811,7 @@ int pkd_accumulate_weights(pkd_ctx* ctx, const void* q, const void* kv, const fl
   a.page_size = c.page_size;
   a.page_shift = page_shift_of(c.page_size);
   a.num_pages = c.num_pages;
+  a.batch = ctx->info.batch;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)kHeadDim) * (double)k_scale);
   a.wait_epoch = expect_epoch != 0 ? epoch_word(expect_epoch) : 0;
   return launch_weights(a, ctx->kind.fp8, ctx->sms, static_cast<cudaStream_t>(stream)) ==

@@ -22,6 +22,7 @@ struct WeightsArgs {
   int64_t off_pages;
   int64_t page_bytes, token_bytes, head_bytes;   // strides of K in the cache
   int32_t hq, hkv, page_size, page_shift, num_pages;   // page_shift: log2 of the size, or -1
+  int32_t batch;              // requests of q, lse, new_tokens and seen
   float scale_log2;
   int32_t wait_epoch;
 };

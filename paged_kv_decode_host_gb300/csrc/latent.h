@@ -41,6 +41,7 @@ struct LatentArgs {
   float* lse;            // fp32 [batch][heads] or null
   int64_t off_cta, off_items, off_pages, off_units, off_merge;
   int32_t heads, blocks, page_size, num_pages;
+  int32_t batch;         // requests of q, out and lse
   float scale_log2, v_scale;
   int32_t wait_epoch;
   CUtensorMap kv_map[2]; // the cache, 16-token boxes of either column region

@@ -319,7 +319,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   pdl_launch_dependents();
   const int it0 = __shfl_sync(kFull, a.sched[a.off_cta + blockIdx.x], 0);
   const int it1 = __shfl_sync(kFull, a.sched[a.off_cta + blockIdx.x + 1], 0);
-  if (it0 >= it1) {
+  // a captured call, under a later plan of more requests than q and out have
+  const bool outgrown = __shfl_sync(kFull, a.sched[H_BATCH], 0) > a.batch;
+  if (it0 >= it1 || outgrown) {
+    if (outgrown && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
     pdl_wait();
     return;
   }
@@ -928,7 +931,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const __
   __shared__ float z_s[kMergeWarps];
   pdl_launch_dependents();
   if (a.wait_epoch != 0) pdl_wait();   // the schedule came from another stream
-  const int units = a.sched[H_NUNITS];
+  const int units = a.sched[H_BATCH] > a.batch ? 0 : a.sched[H_NUNITS];   // as the decode kernel
   const int team = merge_team(a.sched[H_MAXCHUNKS], (int64_t)units * a.heads * kMergeParts);
   if (team == 1)
     merge_tasks<1>(a, units, acc_s, z_s);

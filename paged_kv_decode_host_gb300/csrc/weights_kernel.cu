@@ -126,6 +126,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(const __grid_co
   auto in_page = [&](int t) { return shift >= 0 ? t & (P - 1) : t % P; };
   // this block's tiles of all requests', end to end: [lo, hi), even shares
   const int batch = a.sched[H_BATCH], nnz = a.sched[H_NNZ];
+  if (batch > a.batch) {   // a captured call, under a later plan of more requests
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+    pdl_wait();
+    return;
+  }
   const int4* requests = reinterpret_cast<const int4*>(a.sched + request_words(a.off_pages, nnz));
   const int64_t total = requests[batch].x;
   const int lo = (int)(total * blockIdx.x / gridDim.x), hi = (int)(total * (blockIdx.x + 1) / gridDim.x);
