@@ -294,9 +294,10 @@ int pkd_get_plan_info(const pkd_ctx *ctx, pkd_plan_info *info);
  * kernel on `stream`, with programmatic dependent launch: the decode kernel
  * may start while the previous kernel in the stream runs and reads q and
  * the KV cache at once, so a kernel that writes them ahead of it in the same
- * stream must not release its dependents before it completes (kernels
- * launched without the programmatic attribute, such as pkd_append_kv's,
- * never do), and q and kv must not alias the out / lse of an earlier run
+ * stream must not release its dependents before it completes (kernels that
+ * execute no griddepcontrol.launch_dependents never do: pkd_append_kv's,
+ * pkd_append_latent's, pkd_accumulate_weights' and the one of an eviction that
+ * moves rows execute none), and q and kv must not alias the out / lse of an earlier run
  * still in the stream; out, lse and the partial states are written only
  * after the previous kernel completes.
  * Errors: INVALID_ARG, NO_PLAN, STALE_PLAN, CUDA. */
@@ -415,7 +416,10 @@ int pkd_accumulate_weights(pkd_ctx *ctx, const void *q, const void *kv, const fl
  * errors are carried along, so the sum is within its last place; positions of
  * head 0 count), the `budget` tokens of largest weight stay; tokens with position < sinks or
  * >= seen[b] - recent stay before all others (sinks + recent <= budget);
- * equal weights: the lower slot first; NaN counts as the lowest.  Slots are
+ * equal weights: the lower slot first; NaN counts as the lowest.  Every
+ * token's position must have been written (pkd_accumulate_weights does so for
+ * the tokens it is told are new): a fill value of -1 is below sinks, even if
+ * that is 0, and such a token stays before all others.  Slots are
  * closed up without keeping an order (attention does not depend on it): the
  * i-th slot below `budget` whose token goes takes the i-th kept token from
  * the slots behind, its K and V rows, weight and position.  A request's first
@@ -448,9 +452,11 @@ int pkd_evict_kv(int32_t layers, void *const *kv, float *const *weights,
                  int32_t head_dim, uint32_t flags, void *d_workspace, size_t workspace_bytes,
                  int32_t *err, void *stream);
 
-/* Device workspace of pkd_evict_kv for these arguments: a bit per token and
- * job where few long requests are cut, else 0 (also for arguments that
- * pkd_evict_kv refuses). */
+/* Device workspace of pkd_evict_kv for these arguments: where a request may
+ * lose and keep 512 tokens or more (min(max_len - budget, budget) >= 512), a
+ * bit per token of max_len for every layer, request and (per_head) KV head --
+ * 134 MB for 32 layers x 64 requests x 8 heads and 65,536 tokens; else 0 (also
+ * for arguments that pkd_evict_kv refuses). */
 size_t pkd_evict_workspace_bytes(int32_t layers, int32_t batch, int32_t max_len, int32_t budget,
                                  int32_t per_head, int32_t num_kv_heads);
 

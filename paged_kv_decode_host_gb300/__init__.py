@@ -1139,7 +1139,8 @@ def evict_kv(kv_caches, weights, positions, indptr, indices, last_page_len, seen
     keeps them.  indptr / indices / last_page_len / seen: int32 CUDA tensors,
     the table (a page stands in it once) and the tokens seen; max_len: at least
     the longest request's tokens (at most 262,144).  Tokens at positions below ``sinks`` and among
-    the last ``recent`` always stay.  per_head: every KV head keeps its own
+    the last ``recent`` always stay, so every token's position must have been
+    written before (a fill value of -1 is below any ``sinks``).  per_head: every KV head keeps its own
     tokens; else all keep the same, by the sum of their weights.  Slots are
     closed up without keeping their order: afterwards the request's first
     ``budget`` slots are its cache (:func:`evicted_table` gives the table).

@@ -19,9 +19,10 @@
 // minima instead.  The kept tokens become a bitmap, whose running counts pair
 // holes and movers.  Jobs with more than 32,768 tokens, and calls of few jobs
 // with long requests, take a cluster of up to 8 blocks a job, whose digit
-// counts and bitmaps meet through distributed shared memory; calls of few
-// jobs also leave the moves to a second kernel over the whole GPU, which
-// reads the bitmaps.  A job's moves begin only when all its weights are read.
+// counts and bitmaps meet through distributed shared memory.  Where a job may
+// move 512 tokens or more, however many jobs there are, the moves are left to
+// a second kernel over the whole GPU, which reads the bitmaps from the
+// workspace.  A job's moves begin only when all its weights are read.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -517,7 +518,8 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   move_pairs(a, sh, j, kept, before, rank, blocks);
 }
 
-// The moves of a call with few jobs: a.splits blocks per job.
+// The moves of a call whose jobs may move 512 tokens or more: a.splits blocks
+// per job.
 constexpr int kMoveThreads = 512;
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];

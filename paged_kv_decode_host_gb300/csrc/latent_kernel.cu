@@ -38,7 +38,7 @@
 //    is, across lanes and warps, so they are not formed per tile: every tile
 //    is only compared with the running base, and the exact maxima are taken
 //    when some score exceeds its head's base by more than 2^8 (always in an
-//    item's first tile).  P is written as bf16, for up to 32 heads with the
+//    item's first tile), from the scores read again.  P is written as bf16, for up to 32 heads with the
 //    rounding's rest beside it, into shared memory; the sums that divide it
 //    are kept unrounded in fp32.
 // Every wait is bounded; on timeout the kernel sets the device error word,
@@ -124,10 +124,10 @@ struct LatentShape {
   // requests: 46.3 -> 47.7; 16 heads, 64 requests: 50 -> 53; but 40 heads,
   // 100,003 tokens: 34.2 -> 33.8).
   static constexpr bool kPrefetch = NH == 64;
-  // What a round cannot go below is the shared memory's rate: the products read
-  // their operands at about 110 bytes a cycle (of 128), 147 KB for a 64-head
-  // tile's scores and 98 KB for its P.V, beside 74 KB of copies: 2,550 cycles
-  // of some 3,250.
+  // What a round of products of one CTA cannot go below is the shared memory's
+  // rate: they read their operands at about 110 bytes a cycle (of 128), 147 KB
+  // for a 64-head tile's scores and 98 KB for its P.V, beside 74 KB of copies:
+  // 2,550 cycles of some 3,250.
   static constexpr uint32_t kColO = 0, kColS = kPairs * NP;
   static_assert(NH % 16 == 0 && NH <= 64 && kColS + 2 * NH <= 512, "shape");
 };
