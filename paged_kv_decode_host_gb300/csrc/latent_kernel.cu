@@ -38,9 +38,9 @@
 //    is, across lanes and warps, so they are not formed per tile: every tile
 //    is only compared with the running base, and the exact maxima are taken
 //    when some score exceeds its head's base by more than 2^8 (always in an
-//    item's first tile), from the scores read again.  P is written as bf16, for up to 32 heads with the
-//    rounding's rest beside it, into shared memory; the sums that divide it
-//    are kept unrounded in fp32.
+//    item's first tile), from the scores read again.  P is written as bf16,
+//    for up to 32 heads with the rounding's rest beside it, into shared
+//    memory; the sums that divide it are kept unrounded in fp32.
 // Every wait is bounded; on timeout the kernel sets the device error word,
 // stops, waits (bounded) for its copies and products, frees tensor memory
 // and returns.
