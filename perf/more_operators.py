@@ -110,7 +110,7 @@ def _lens(case):
 def _paths(case):
     """The accepted drafts of an accept case's requests, in order: fixed by its sizes."""
     r = random.Random("%d,%d" % (case["batch"], case["drafts"]))
-    most = min(case["drafts"], 8)
+    most = min(-(-case["drafts"] // 2), 8)
     return [sorted(r.sample(range(case["drafts"]), r.randint(-(-most // 2), most))) for _ in range(case["batch"])]
 
 
