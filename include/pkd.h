@@ -162,6 +162,15 @@ typedef struct pkd_config {
  * the caller captured does no work under a later plan of more requests, and
  * ORs PKD_DEV_ERR_BOUNDS into the device error word. */
 #define PKD_FLAG_LATENT 1024u
+/* Tree context: every request has one or more query tokens, the last ones of
+ * its cached tokens -- drafts to be verified, as a tree or a chain, or a piece
+ * of a prompt.  Plans are made with pkd_plan_tree, layers run with
+ * pkd_run_tree.  max_batch is the capacity in query tokens (and in requests);
+ * pkd_plan_info.batch counts query tokens.  bf16 cache, head_dim 128, page
+ * size a multiple of 16; combinable with PKD_FLAG_HND only.  alpha < 0 selects
+ * 256, min_chunk_tokens < 0 256.  Not for pkd_plan, pkd_run, pkd_graph_capture
+ * and pkd_accumulate_weights. */
+#define PKD_FLAG_TREE 2048u
 
 typedef struct pkd_ctx pkd_ctx;
 typedef struct pkd_graph pkd_graph;
@@ -311,6 +320,56 @@ int pkd_run(pkd_ctx *ctx, const void *q, const void *kv, void *out, float *lse,
  * Errors: as pkd_run; INVALID_ARG for a non-finite scale. */
 int pkd_run_scaled(pkd_ctx *ctx, const void *q, const void *kv, void *out, float *lse,
                    float k_scale, float v_scale, uint64_t expect_epoch, void *stream);
+
+/* Plan one step of a tree context.  Host arrays (int32) as for pkd_plan, the
+ * table after the append of the query tokens, and q_indptr[batch + 1]: request
+ * b's query tokens are rows q_indptr[b] .. q_indptr[b+1] - 1 of q, and the
+ * last n_b = q_indptr[b+1] - q_indptr[b] of its l_b cached tokens (0 <= n_b <=
+ * l_b; a request without query tokens only has its row in the table).
+ *   causal 1: each request's query tokens are a chain (token i sees those up
+ *             to itself); 0: the runs' masks say what they see
+ *   window    0, or w >= 1: a query sees only tokens less than w positions
+ *             before it (see pkd_run_tree)
+ * Errors: as pkd_plan; BAD_TABLE also for n_b outside its range. */
+int pkd_plan_tree(pkd_ctx *ctx, const int32_t *q_indptr, const int32_t *indptr,
+                  const int32_t *indices, const int32_t *last_page_len, int32_t batch,
+                  int32_t causal, int32_t window, void *stream, uint64_t *epoch);
+
+/* Attention of the planned query tokens over their requests' cached tokens.
+ * With c_b = l_b - n_b, query token i of request b (i = 0 .. n_b - 1) stands at
+ * position c_b + d_i, cached token t < c_b at position t, and cached token c_b
+ * + j, which is query token j, at c_b + d_j.  For every query head h
+ *     s = scale * q . k;  with a cap: s = cap * tanh(s / cap);
+ *     s = s - slopes[h] * (position of q - position of k)
+ * over the tokens t < c_b and the query tokens j of the same request that i
+ * sees (bit j % 32 of word j / 32 of its mask row, itself only if its own bit
+ * is set; in a causal plan j <= i), in a plan with a window only where the
+ * position of k is more than that of q less the window:
+ *     out = softmax(s) V,  lse = log sum exp(s)
+ * A query that sees nothing gets 0 and -inf.  What masked tokens hold, values
+ * that are not finite included, does not matter.
+ *   q          : device bf16 [rows][Hq][D], 16-byte aligned
+ *   rows       : rows of q, out and lse, at least the plan's query tokens; rows
+ *                behind those are not written
+ *   kv         : device bf16 [num_pages][2][P][Hkv][D] (PKD_FLAG_HND: [2][Hkv][P][D])
+ *   out, lse   : device bf16 [rows][Hq][D]; device fp32 [rows][Hq] or NULL
+ *   mask       : device uint32 [rows][mask_words], mask_words at least the most
+ *                n_b / 32 rounded up; NULL in a causal plan
+ *   depths     : device int32 [rows], d_i of every query token (below 0 counts
+ *                as 0); NULL: d_i = i.  Only slopes and windows use them; NULL
+ *                in a causal plan
+ *   slopes     : device fp32 [Hq] or NULL
+ *   scale      : finite, > 0; score_cap: 0 (none) or finite, > 0
+ * expect_epoch, launches and stream order as pkd_run.  A call that the caller
+ * captured replays under later plans that its rows and mask_words fit; under
+ * another it does no work and ORs PKD_DEV_ERR_BOUNDS into the device error
+ * word.  The same bits every run.
+ * Errors: as pkd_run; INVALID_ARG also for rows or mask_words below the plan's
+ * and a mask or depths given to a causal plan. */
+int pkd_run_tree(pkd_ctx *ctx, const void *q, int32_t rows, const void *kv, void *out, float *lse,
+                 const uint32_t *mask, int32_t mask_words, const int32_t *depths,
+                 const float *slopes, float scale, float score_cap, uint64_t expect_epoch,
+                 void *stream);
 
 /* merge_states: for each of n x heads rows,
  *   m = max(s_a, s_b), w_a = exp(s_a - m), w_b = exp(s_b - m),
@@ -480,6 +539,77 @@ int pkd_append_latent(const void *latent_new, int64_t latent_stride, const void 
                       const int32_t *last_page_len, int32_t batch, void *cache,
                       int32_t num_pages, int32_t page_size, int32_t *err, void *stream);
 
+/* New tokens' queries and keys normed per head and rotated by their positions,
+ * keys and values written into their page slots, in one kernel.  For every
+ * token and head of q and k, in fp32:
+ *     y = x / sqrt(mean(x^2) + eps) * w        (with a norm)
+ *     then for i < rotary_dim / 2 the pair (a, b) = (i, i + rotary_dim / 2), or
+ *     (2 i, 2 i + 1) with `interleaved`:
+ *         (y_a cos - y_b sin, y_b cos + y_a sin) * rope_scale,
+ *         angle = 2 pi * turns[i] / 2^64 * rope_positions[token][axes[i]]
+ *     (turns as integers modulo 2^64: exact modulo one turn at any position);
+ *     dims from rotary_dim on only get the norm.
+ * Queries go to q_out, keys and values to the token's slot (the slot rule, the
+ * table and *err are pkd_append_latent's); a bf16 cache holds v as given, an
+ * E4M3 cache (PKD_FLAG_KV_FP8) y / k_scale and v / v_scale, rounded to nearest,
+ * at most 448 in magnitude.  A token without a slot still has its query rotated.
+ *   q [n][Hq][D], k, v [n][Hkv][D] : device bf16; token and head strides in
+ *       ELEMENTS, multiples of 8 (the three may be column ranges of one
+ *       projection's output), 16-byte aligned.  Hq may be 0 (q, q_out NULL)
+ *   q_out          : device bf16, strides likewise; q itself with q's strides, or
+ *                    no memory that q, k or v has
+ *   q_norm, k_norm : device [D], bf16 or (norms_f32) fp32, or NULL (no norm)
+ *   turns, axes    : device uint64 and int32 [rotary_dim / 2]
+ *   rotary_dim     : 0 to D, a multiple of 16 (8 interleaved)
+ *   rope_positions : device int32 [n][num_axes], 1 <= num_axes <= 4; an axis
+ *                    outside counts as the nearest
+ *   batch_indices, positions : device int32 [n], as for pkd_append_kv
+ *   kv             : as for pkd_append_kv_ex, not overlapping the inputs
+ *   head_dim       : 64, 128 or 256; flags: PKD_FLAG_HND, PKD_FLAG_KV_FP8
+ *   k_scale, v_scale : finite, > 0; 1 for a bf16 cache
+ * No two tokens may have the same slot (its row would mix the two).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (head_dim), CUDA. */
+int pkd_rotate_append_kv(const void *q, int64_t q_token, int64_t q_head, void *q_out,
+                         int64_t out_token, int64_t out_head, const void *k, int64_t k_token,
+                         int64_t k_head, const void *v, int64_t v_token, int64_t v_head,
+                         const void *q_norm, const void *k_norm, int32_t norms_f32, float eps,
+                         const uint64_t *turns, const int32_t *axes, int32_t rotary_dim,
+                         int32_t interleaved, float rope_scale, const int32_t *rope_positions,
+                         int32_t num_axes, const int32_t *batch_indices,
+                         const int32_t *positions, int32_t n, const int32_t *indptr,
+                         const int32_t *indices, int32_t num_indices,
+                         const int32_t *last_page_len, int32_t batch, void *kv,
+                         int32_t num_pages, int32_t page_size, int32_t num_qo_heads,
+                         int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale,
+                         uint32_t flags, int32_t *err, void *stream);
+
+/* Move every request's accepted drafts to the front of its drafted tokens, in
+ * place, for 1 to 128 layers in one launch.  The last drafted[b] of request b's
+ * l_b cached tokens are this step's drafts; its row of `accepted` names, in
+ * increasing order, those that stay (0-based among the drafts; the first
+ * negative entry ends the row).  With c_b = l_b - drafted[b], slot c_b + i takes
+ * the K and V rows of slot c_b + accepted[b][i].  Slots behind the last one keep
+ * what they hold, and the caller's next table ends there.
+ *   kv       : HOST array of `layers` device pointers, all different, caches as
+ *              for pkd_append_kv_ex
+ *   accepted : device int32 [batch][width], 0 <= width <= 1024
+ *   drafted  : device int32 [batch]
+ *   indptr [batch + 1], indices [num_indices], last_page_len [batch] : device
+ *              int32, the table with the drafts; a page that accepted drafts
+ *              lie in stands there once
+ *   flags    : PKD_FLAG_HND, PKD_FLAG_KV_FP8
+ *   err      : device int32 word or NULL
+ * A request whose table row is wrong, whose drafts are more than its tokens,
+ * whose accepted ones do not increase or are not drafts, or that names a page
+ * outside the pool for one of them is left as it is and PKD_DEV_ERR_BOUNDS is
+ * OR-ed into *err.  One kernel, stream-ordered, capturable.
+ * Errors: INVALID_ARG, CUDA. */
+int pkd_accept_kv(int32_t layers, void *const *kv, const int32_t *accepted, int32_t width,
+                  const int32_t *drafted, const int32_t *indptr, const int32_t *indices,
+                  int32_t num_indices, const int32_t *last_page_len, int32_t batch,
+                  int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                  uint32_t flags, int32_t *err, void *stream);
+
 /* Self-test of the device-side bounded waits (failure detection without a
  * GPU fault; FlashInfer, in depth, "Failure modes in production": errors come
  * back as status, never as a hang).  Launches one small kernel on `stream`
@@ -531,6 +661,15 @@ int pkd_plan_host_cascade(const pkd_config *cfg, const int32_t *group_indptr,
                           const int32_t *s_last, int32_t *host_words, size_t max_words,
                           pkd_plan_info *info);
 
+/* pkd_plan_host for a tree plan (cfg->flags has PKD_FLAG_TREE; arguments as
+ * pkd_plan_tree).  Behind the page list (its length rounded up to 4) follow 4
+ * words per request: first query token, query tokens, cached tokens before
+ * them, first page in the page list. */
+int pkd_plan_host_tree(const pkd_config *cfg, const int32_t *q_indptr, const int32_t *indptr,
+                       const int32_t *indices, const int32_t *last_page_len, int32_t batch,
+                       int32_t causal, int32_t window, int32_t *host_words, size_t max_words,
+                       pkd_plan_info *info);
+
 /* Word offsets of the schedule arrays (see pkd_plan_host):
  *   off[0] cta_indptr[num_ctas + 1]
  *   off[1] items[num_items][8] = {req, tok_begin, tok_end, dst_slot,
@@ -543,8 +682,12 @@ int pkd_plan_host_cascade(const pkd_config *cfg, const int32_t *group_indptr,
  *          page_list; cascade plans: prefix items have slot stride -1 and
  *          dst_slot = their chunk index, request req + i writing slot
  *          merge_indptr[req + i] + dst_slot; the page list holds the prefix
- *          table's indices, then the suffix table's)
- *   off[2] units[num_units][2] = {req, num_chunks}
+ *          table's indices, then the suffix table's; tree plans: an item
+ *          covers one KV head of a block of 128 / g query tokens of request
+ *          req: first_page is the request's first, word 5 the block's number
+ *          in the request, word 7 the head, and the block's token i writes
+ *          slot dst_slot + i * slot_stride)
+ *   off[2] units[num_units][2] = {req (tree plans: query token), num_chunks}
  *   off[3] merge_indptr[num_units + 1]
  *   off[4] page_list[nnz]    (the CSR indices, unchanged)
  *   off[5] total words
@@ -553,7 +696,9 @@ int pkd_plan_host_cascade(const pkd_config *cfg, const int32_t *group_indptr,
  * int32), split floor, requests per block, the most chunks of any split
  * request, the max_batch and max_num_pages the offsets were laid out for,
  * (cascade plans) the CTAs of the prefix level and its chunk, the plan's
- * epoch word (in a context's workspace; 0 in host-only plans), then zeros.
+ * epoch word (in a context's workspace; 0 in host-only plans), (tree plans)
+ * the requests, causal, the window and the most query tokens of a request,
+ * then zeros.
  * Errors: INVALID_ARG. */
 int pkd_schedule_layout(const pkd_config *cfg, int64_t off[6]);
 

@@ -25,6 +25,10 @@ API (names follow the pages' plan / run / merge_states):
 * ``cascade=True`` contexts: ``plan_cascade(group_indptr, prefix, suffix)``
   plans a shared prefix and every request's own suffix together; ``run``
   returns attention over both, merged.
+* :class:`RotaryPositions`, :func:`rotate_append_kv`,
+  :class:`BatchTreeDecodeWithPagedKVCache`, :func:`accept_kv` (drafts.py) -- a
+  step with drafted tokens: rotated and appended, attended as trees or chains,
+  the accepted ones moved into place.
 * :func:`selftest_bounded_wait` -- the device-side bounded-wait self-test.
 """
 from __future__ import annotations
@@ -43,6 +47,8 @@ __all__ = [
     "schedule_layout",
     "selftest_bounded_wait", "Graph",
     "STATUS",
+    "RotaryPositions", "rotate_append_kv", "BatchTreeDecodeWithPagedKVCache", "tree_mask",
+    "plan_host_tree", "accept_kv", "accepted_table",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -69,6 +75,8 @@ EXPORTS = (
     "pkd_selftest_bounded_wait", "pkd_append_kv_layers", "pkd_static_scratch_last_error",
     "pkd_plan_cascade", "pkd_plan_host_cascade", "pkd_advise_format", "pkd_append_latent",
     "pkd_accumulate_weights", "pkd_evict_kv", "pkd_evict_workspace_bytes",
+    "pkd_plan_tree", "pkd_plan_host_tree", "pkd_run_tree", "pkd_rotate_append_kv",
+    "pkd_accept_kv",
 )
 
 
@@ -184,6 +192,16 @@ def load():
     sig["pkd_evict_kv"] = (ctypes.c_int, [i32, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32,
                                           i32, i32, i32, i32, i32, u32, vp, sz, vp, vp])
     sig["pkd_evict_workspace_bytes"] = (sz, [i32] * 6)
+    f32 = ctypes.c_float
+    sig["pkd_plan_tree"] = (ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, vp, ctypes.POINTER(u64)])
+    sig["pkd_plan_host_tree"] = (ctypes.c_int, [cfgp, vp, vp, vp, vp, i32, i32, i32, vp, sz,
+                                                ctypes.POINTER(PlanInfo)])
+    sig["pkd_run_tree"] = (ctypes.c_int, [vp, vp, i32, vp, vp, vp, vp, i32, vp, vp, f32, f32, u64, vp])
+    sig["pkd_rotate_append_kv"] = (ctypes.c_int, [vp, i64, i64] * 4 + [
+        vp, vp, i32, f32, vp, vp, i32, i32, f32, vp, i32, vp, vp, i32, vp, vp, i32, vp, i32, vp,
+        i32, i32, i32, i32, i32, f32, f32, u32, vp, vp])
+    sig["pkd_accept_kv"] = (ctypes.c_int, [i32, vp, vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, i32,
+                                           i32, u32, vp, vp])
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
         f.restype = res
@@ -229,6 +247,7 @@ FLAG_CHUNK_SEARCH = 64  # chunk = largest page multiple still giving >= N_CTA it
 FLAG_HND = 32           # cache layout [pages, 2, Hkv, P, D] instead of NHD [pages, 2, P, Hkv, D]
 FLAG_DENSE_PREFIX = 128  # shared prefix on tcgen05 tensor cores: 128-row tiles, one KV head per item
 FLAG_LATENT = 1024      # latent cache [pages, P, 576] shared by every query head
+FLAG_TREE = 2048        # query tokens of requests over their caches: trees, chains, prompts' pieces
 FLAG_CASCADE = 256      # both levels of a shared-prefix step in one plan, one launch, one merge
 
 
@@ -355,6 +374,8 @@ def _fast():
             m.init_ops(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.pkd_accumulate_weights, lib.pkd_append_latent, lib.pkd_evict_kv,
                 lib.pkd_evict_workspace_bytes)])
+            m.init_step(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.pkd_plan_tree, lib.pkd_run_tree, lib.pkd_rotate_append_kv, lib.pkd_accept_kv)])
             _fast_plan = m
         except ImportError:
             _fast_plan = False
@@ -1227,3 +1248,7 @@ def evicted_table(indptr, indices, last_page_len, page_size, budget):
     ids = indices[:used]
     return (np.concatenate([[0], np.cumsum(left)]).astype(np.int32), np.ascontiguousarray(ids[keep]),
             (now - page_size * (left - 1)).astype(np.int32), np.ascontiguousarray(ids[~keep]))
+
+
+from .drafts import (BatchTreeDecodeWithPagedKVCache, RotaryPositions,  # noqa: E402
+                     accept_kv, accepted_table, plan_host_tree, rotate_append_kv, tree_mask)

@@ -23,7 +23,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkd.so")
 SOURCES = ["planner.cpp", "api.cu", "decode_kernel.cu", "prefix_tc_kernel.cu",
            "merge_kernels.cu", "static_scratch.cu", "append_kernel.cu", "selftest.cu",
-           "latent_kernel.cu", "weights_kernel.cu", "evict_kernel.cu"]
+           "latent_kernel.cu", "weights_kernel.cu", "evict_kernel.cu", "plan_tree.cpp",
+           "tree_kernel.cu", "rotate_kernel.cu", "accept_kernel.cu", "api_step.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 PYPLAN = os.path.join(HERE, "_pkd_plan" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 

@@ -35,6 +35,7 @@ struct pkd_ctx {
   int32_t n_cta = 0;
   DecodeKind kind{};   // which decode kernel (consumer, cache type, producer)
   bool latent = false;   // a latent cache: its kernel instead
+  bool tree = false;     // drafted tokens: its kernel instead
   int smem_bytes = 0;
   // page-tile maps by cache address (the map holds only the address and the
   // context's fixed shape), replaced round-robin
@@ -88,8 +89,9 @@ bool valid_flags(uint32_t f) {
   const uint32_t known = PKD_FLAG_FMA_CONSUMER | PKD_FLAG_MMA_CONSUMER | PKD_FLAG_SHARED_PREFIX |
                          PKD_FLAG_KV_FP8 | PKD_FLAG_ROW_COPIES | PKD_FLAG_CHUNK_SEARCH |
                          PKD_FLAG_HND | PKD_FLAG_DENSE_PREFIX | PKD_FLAG_CASCADE |
-                         PKD_FLAG_LATENT;
+                         PKD_FLAG_LATENT | PKD_FLAG_TREE;
   if (f & ~known) return false;
+  if ((f & PKD_FLAG_TREE) && (f & ~(PKD_FLAG_TREE | PKD_FLAG_HND))) return false;
   // a latent cache has one layout, one type, a planner and a kernel of its own
   if ((f & PKD_FLAG_LATENT) && f != PKD_FLAG_LATENT) return false;
   // a cascade context runs both of its levels itself: bf16 page tiles,
@@ -126,8 +128,9 @@ int check_config(const pkd_config* c) {
   if (c->num_qo_heads < 1 || c->num_qo_heads % c->num_kv_heads != 0)
     return PKD_E_UNSUPPORTED_SHAPE;
   if (!valid_group(c->num_qo_heads / c->num_kv_heads)) return PKD_E_UNSUPPORTED_SHAPE;
-  // the dense-prefix kernel (and the cascade kernel) read 16-token page tiles
-  if ((c->flags & (PKD_FLAG_DENSE_PREFIX | PKD_FLAG_CASCADE)) && c->page_size % 16 != 0)
+  // the dense-prefix kernel (and the cascade and tree kernels) read 16-token page tiles
+  if ((c->flags & (PKD_FLAG_DENSE_PREFIX | PKD_FLAG_CASCADE | PKD_FLAG_TREE)) &&
+      c->page_size % 16 != 0)
     return PKD_E_UNSUPPORTED_SHAPE;
   // a page must fit the copy-size and tx-count limits of one stage
   if ((int64_t)c->page_size * c->num_kv_heads * kHeadDim * 2 * 2 > (int64_t)1 << 30)
@@ -153,7 +156,7 @@ DecodeKind kind_for(const pkd_config* c, const void* probe_address) {
   k.block = (c->flags & PKD_FLAG_SHARED_PREFIX) != 0;
   k.fp8 = (c->flags & PKD_FLAG_KV_FP8) != 0;
   k.tmap = k.mma && c->page_size % 16 == 0 && !(c->flags & PKD_FLAG_ROW_COPIES);
-  k.dense = (c->flags & PKD_FLAG_DENSE_PREFIX) != 0;
+  k.dense = (c->flags & (PKD_FLAG_DENSE_PREFIX | PKD_FLAG_TREE)) != 0;   // (one map for both)
   k.cascade = (c->flags & PKD_FLAG_CASCADE) != 0;
   if (k.tmap && probe_address != nullptr) {
     CUtensorMap m;
@@ -168,8 +171,10 @@ DecodeKind kind_for(const pkd_config* c, const void* probe_address) {
 }
 
 int resolve_ctas(const pkd_config* c, const DecodeKind& k, int32_t* n_cta, int* smem_bytes) {
-  const bool latent = is_latent(*c);
-  *smem_bytes = latent ? latent_smem_bytes(c->num_qo_heads) : decode_smem_bytes(c->num_kv_heads, k);
+  const bool latent = is_latent(*c), tree = is_tree(*c);
+  *smem_bytes = latent ? latent_smem_bytes(c->num_qo_heads)
+                : tree ? tree_smem_bytes()
+                       : decode_smem_bytes(c->num_kv_heads, k);
   if (c->num_ctas > 0) {
     *n_cta = c->num_ctas;
     return PKD_OK;
@@ -178,9 +183,12 @@ int resolve_ctas(const pkd_config* c, const DecodeKind& k, int32_t* n_cta, int* 
   if (cudaGetDevice(&dev) != cudaSuccess) return PKD_E_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PKD_E_CUDA;
-  if ((latent ? latent_prepare(c->num_qo_heads) : decode_prepare(k, *smem_bytes)) != cudaSuccess)
+  if ((latent ? latent_prepare(c->num_qo_heads)
+       : tree ? tree_prepare()
+              : decode_prepare(k, *smem_bytes)) != cudaSuccess)
     return PKD_E_CUDA;
   if ((latent ? latent_occupancy(c->num_qo_heads, &per_sm)
+       : tree ? tree_occupancy(&per_sm)
               : decode_occupancy(k, c->num_kv_heads, *smem_bytes, &per_sm)) != cudaSuccess)
     return PKD_E_CUDA;
   if (per_sm < 1) return PKD_E_UNSUPPORTED_SHAPE;
@@ -430,12 +438,29 @@ int pkd_advise_format(const pkd_config* cfg, const int32_t* group_indptr, int32_
   });
 }
 
+int pkd_plan_host_tree(const pkd_config* cfg, const int32_t* q_indptr, const int32_t* indptr,
+                       const int32_t* indices, const int32_t* last_page_len, int32_t batch,
+                       int32_t causal, int32_t window, int32_t* host_words, size_t max_words,
+                       pkd_plan_info* info) {
+  int st = check_config(cfg);
+  if (st != PKD_OK) return st;
+  if (cfg->num_ctas < 1 || host_words == nullptr || !is_tree(*cfg)) return PKD_E_INVALID_ARG;
+  Layout L = plan_layout(*cfg, cfg->num_ctas);
+  if (max_words < (size_t)L.words) return PKD_E_INVALID_ARG;
+  int64_t end = 0;
+  return planned([&] {
+    return plan_schedule_tree(*cfg, cfg->num_ctas, L, q_indptr, indptr, indices, last_page_len,
+                              batch, causal, window, host_words, info, &end);
+  });
+}
+
 int pkd_plan_host(const pkd_config* cfg, const int32_t* indptr, const int32_t* indices,
                   const int32_t* last_page_len, int32_t batch, int32_t* host_words,
                   size_t max_words, pkd_plan_info* info) {
   int st = check_config(cfg);
   if (st != PKD_OK) return st;
-  if (cfg->num_ctas < 1 || host_words == nullptr || (cfg->flags & PKD_FLAG_CASCADE))
+  if (cfg->num_ctas < 1 || host_words == nullptr ||
+      (cfg->flags & (PKD_FLAG_CASCADE | PKD_FLAG_TREE)))
     return PKD_E_INVALID_ARG;
   Layout L = plan_layout(*cfg, cfg->num_ctas);
   if (max_words < (size_t)L.words) return PKD_E_INVALID_ARG;
@@ -466,6 +491,7 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
   ctx->cfg = *cfg;
   ctx->kind = kind_for(cfg, d_workspace);
   ctx->latent = is_latent(*cfg);
+  ctx->tree = is_tree(*cfg);
   // the driver refused a map
   if ((ctx->kind.dense || ctx->kind.cascade || ctx->latent) && !ctx->kind.tmap) {
     delete ctx;
@@ -477,7 +503,8 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
     return st;
   }
   if ((ctx->latent ? latent_prepare(cfg->num_qo_heads)
-                        : decode_prepare(ctx->kind, ctx->smem_bytes)) != cudaSuccess) {
+       : ctx->tree ? tree_prepare()
+                   : decode_prepare(ctx->kind, ctx->smem_bytes)) != cudaSuccess) {
     delete ctx;
     return PKD_E_CUDA;
   }
@@ -574,7 +601,7 @@ extern "C" {
 
 int pkd_plan(pkd_ctx* ctx, const int32_t* indptr, const int32_t* indices,
              const int32_t* last_page_len, int32_t batch, void* stream, uint64_t* epoch) {
-  if (ctx == nullptr || ctx->kind.cascade) return PKD_E_INVALID_ARG;
+  if (ctx == nullptr || ctx->kind.cascade || ctx->tree) return PKD_E_INVALID_ARG;
   return plan_and_publish(
       ctx,
       [&](int32_t* words, pkd_plan_info* info, int64_t* end) {
@@ -616,6 +643,19 @@ int pkd_plan_cascade(pkd_ctx* ctx, const int32_t* group_indptr, int32_t num_grou
       stream, epoch);
 }
 
+int pkd_plan_tree(pkd_ctx* ctx, const int32_t* q_indptr, const int32_t* indptr,
+                  const int32_t* indices, const int32_t* last_page_len, int32_t batch,
+                  int32_t causal, int32_t window, void* stream, uint64_t* epoch) {
+  if (ctx == nullptr || !ctx->tree) return PKD_E_INVALID_ARG;
+  return plan_and_publish(
+      ctx,
+      [&](int32_t* words, pkd_plan_info* info, int64_t* end) {
+        return plan_schedule_tree(ctx->cfg, ctx->n_cta, ctx->layout, q_indptr, indptr, indices,
+                                  last_page_len, batch, causal, window, words, info, end);
+      },
+      stream, epoch);
+}
+
 int pkd_get_plan_info(const pkd_ctx* ctx, pkd_plan_info* info) {
   if (ctx == nullptr || info == nullptr) return PKD_E_INVALID_ARG;
   if (ctx->epoch == 0) return PKD_E_NO_PLAN;
@@ -631,7 +671,7 @@ int pkd_run(pkd_ctx* ctx, const void* q, const void* kv, void* out, float* lse,
 int pkd_run_scaled(pkd_ctx* ctx, const void* q, const void* kv, void* out, float* lse,
                    float k_scale, float v_scale, uint64_t expect_epoch, void* stream) {
   if (!std::isfinite(k_scale) || !std::isfinite(v_scale)) return PKD_E_INVALID_ARG;
-  if (ctx == nullptr) return PKD_E_INVALID_ARG;
+  if (ctx == nullptr || ctx->tree) return PKD_E_INVALID_ARG;
   if (ctx->epoch == 0) return PKD_E_NO_PLAN;
   if (expect_epoch != 0 && expect_epoch != ctx->epoch) return PKD_E_STALE_PLAN;
   if (ctx->info.batch > 0) {
@@ -641,6 +681,86 @@ int pkd_run_scaled(pkd_ctx* ctx, const void* q, const void* kv, void* out, float
   }
   return launch_run(ctx, q, kv, out, lse, k_scale, v_scale, static_cast<cudaStream_t>(stream),
                     nullptr, nullptr, expect_epoch != 0 ? epoch_word(expect_epoch) : 0);
+}
+
+int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void* out, float* lse,
+                 const uint32_t* mask, int32_t mask_words, const int32_t* depths,
+                 const float* slopes, float scale, float score_cap, uint64_t expect_epoch,
+                 void* stream) {
+  if (ctx == nullptr || !ctx->tree || !std::isfinite(scale) || !(scale > 0.f) ||
+      !std::isfinite(score_cap) || !(score_cap >= 0.f) || mask_words < 0)
+    return PKD_E_INVALID_ARG;
+  if (ctx->epoch == 0) return PKD_E_NO_PLAN;
+  if (expect_epoch != 0 && expect_epoch != ctx->epoch) return PKD_E_STALE_PLAN;
+  const int32_t* head = ctx->staging[ctx->next_staging ^ 1];   // the current plan's header
+  const bool causal = head[H_CAUSAL] != 0;
+  if (rows < ctx->info.batch || (causal && (mask != nullptr || depths != nullptr)))
+    return PKD_E_INVALID_ARG;
+  if (mask == nullptr) mask_words = 0;
+  if (!causal && head[H_MAXQ] > 32 * (int64_t)mask_words) return PKD_E_INVALID_ARG;
+  if (ctx->info.batch > 0) {
+    if (q == nullptr || kv == nullptr || out == nullptr) return PKD_E_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(mask, 4) || !aligned(depths, 4) || !aligned(slopes, 4))
+      return PKD_E_INVALID_ARG;
+  }
+  const pkd_config& c = ctx->cfg;
+  const bool hnd = (c.flags & PKD_FLAG_HND) != 0;
+  const double cap = score_cap, log2e = 1.4426950408889634;
+  TreeArgs a{};
+  a.sched = reinterpret_cast<const int32_t*>(ctx->ws);
+  a.o_part = reinterpret_cast<float*>(ctx->ws + ctx->layout.o_part_byte);
+  a.l_part = reinterpret_cast<float*>(ctx->ws + ctx->layout.l_part_byte);
+  a.err = reinterpret_cast<int32_t*>(ctx->ws + ctx->layout.err_byte);
+  a.q = static_cast<const uint16_t*>(q);
+  a.kv = static_cast<const uint16_t*>(kv);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.mask = mask;
+  a.depths = depths;
+  a.slopes = slopes;
+  a.off_cta = ctx->layout.cta_indptr;
+  a.off_items = ctx->layout.items;
+  a.off_pages = ctx->layout.page_list;
+  a.token_elems = hnd ? kHeadDim : (int64_t)kHeadDim * c.num_kv_heads;
+  a.head_elems = hnd ? (int64_t)kHeadDim * c.page_size : kHeadDim;
+  a.v_elems = (int64_t)kHeadDim * c.num_kv_heads * c.page_size;
+  a.page_elems = 2 * a.v_elems;
+  a.hq = c.num_qo_heads;
+  a.hkv = c.num_kv_heads;
+  a.page_size = c.page_size;
+  a.num_pages = c.num_pages;
+  a.mask_words = mask_words;
+  a.tokens = rows;
+  a.scale_log2 = (float)(score_cap > 0.f ? 2.0 * log2e * scale / cap : log2e * scale);
+  a.cap_log2 = (float)(log2e * cap);
+  a.wait_epoch = expect_epoch != 0 ? epoch_word(expect_epoch) : 0;
+  if (ctx->info.batch > 0) {
+    const int st = kv_map_for(ctx, kv, &a.kv_map);
+    if (st != PKD_OK) return st;
+    if (encode_q_map(q, rows, c.num_qo_heads, c.num_kv_heads, &a.q_map) != cudaSuccess)
+      return PKD_E_CUDA;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus cap_status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cap_status) != cudaSuccess) return PKD_E_CUDA;
+  if (launch_tree(a, ctx->n_cta, s) != cudaSuccess) return PKD_E_CUDA;
+  // a captured launch must do for later plans, whose splits are not known yet
+  if (ctx->info.num_units == 0 && cap_status == cudaStreamCaptureStatusNone) return PKD_OK;
+  MergeArgs m{};
+  m.sched = a.sched;
+  m.o_part = a.o_part;
+  m.l_part = a.l_part;
+  m.out = a.out;
+  m.lse = lse;
+  m.off_units = ctx->layout.units;
+  m.off_merge = ctx->layout.merge_indptr;
+  m.hq = c.num_qo_heads;
+  m.wait_epoch = a.wait_epoch;
+  m.rows = rows;
+  m.most = 32 * (int64_t)mask_words;
+  return launch_merge_tree(m, ctx->merge_grid, ctx->max_chunks, s) == cudaSuccess ? PKD_OK
+                                                                                  : PKD_E_CUDA;
 }
 
 int pkd_merge_states(const void* v_a, const float* s_a, const void* v_b, const float* s_b,
@@ -762,7 +882,7 @@ int pkd_accumulate_weights(pkd_ctx* ctx, const void* q, const void* kv, const fl
                            const int32_t* seen, float k_scale, uint64_t expect_epoch,
                            void* stream) {
   if (ctx == nullptr || !std::isfinite(k_scale)) return PKD_E_INVALID_ARG;
-  if (ctx->kind.block || ctx->kind.cascade || ctx->latent) return PKD_E_INVALID_ARG;
+  if (ctx->kind.block || ctx->kind.cascade || ctx->latent || ctx->tree) return PKD_E_INVALID_ARG;
   if (ctx->epoch == 0) return PKD_E_NO_PLAN;
   if (expect_epoch != 0 && expect_epoch != ctx->epoch) return PKD_E_STALE_PLAN;
   if (ctx->info.batch == 0) return PKD_OK;
@@ -937,7 +1057,7 @@ int pkd_graph_capture_io(pkd_ctx* ctx, int32_t layers, const void* const* q,
                          void* const* out_host, float* const* lse_host, uint32_t flags,
                          pkd_graph** graph) {
   if (ctx == nullptr || graph == nullptr || layers < 1 || q == nullptr || kv == nullptr ||
-      out == nullptr)
+      out == nullptr || ctx->tree)
     return PKD_E_INVALID_ARG;
   if (lse_host != nullptr && lse == nullptr) return PKD_E_INVALID_ARG;
   if ((flags & ~PKD_GRAPH_TIMING) != 0) return PKD_E_INVALID_ARG;

@@ -58,7 +58,9 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // resident at once.
 constexpr int kWarpSlots = 32;
 
-template <int kBatch, int kThreads = kMergeThreads>
+// kTree: the units are query tokens of a tree run, whose states may be empty
+// (lse -inf, out 0), all of a unit's too.
+template <int kBatch, int kThreads = kMergeThreads, bool kTree = false>
 __global__ void __launch_bounds__(kThreads) merge_partials_kernel(const MergeArgs a) {
   static_assert(kThreads >= kHeadDim && kThreads % 32 == 0, "a thread per output dim");
   constexpr int kWarps = kThreads / 32;
@@ -75,7 +77,9 @@ __global__ void __launch_bounds__(kThreads) merge_partials_kernel(const MergeArg
     pdl_wait();
     waited = true;
   }
-  const int n_units = a.sched[H_NUNITS];
+  int n_units = a.sched[H_NUNITS];
+  if constexpr (kTree)   // (the attention kernel has raised the error word)
+    if (a.sched[H_BATCH] > a.rows || (!a.sched[H_CAUSAL] && a.sched[H_MAXQ] > a.most)) n_units = 0;
   const int64_t tasks = (int64_t)n_units * a.hq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool warp_mode = tasks >= (int64_t)4 * gridDim.x;
@@ -97,6 +101,7 @@ __global__ void __launch_bounds__(kThreads) merge_partials_kernel(const MergeArg
     float m = l2;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if constexpr (kTree) m = m == -CUDART_INF_F ? 0.f : m;
     const float w_lane = lane < n ? exp2f(l2 - m) : 0.f;
     float z = w_lane;
 #pragma unroll
@@ -112,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) merge_partials_kernel(const MergeArg
       acc.z = fmaf(w, o.z, acc.z);
       acc.w = fmaf(w, o.w, acc.w);
     }
-    const float inv = 1.f / z;
+    const float inv = kTree && z == 0.f ? 0.f : 1.f / z;
     const int64_t qrow = (int64_t)req * a.hq + h;
     *reinterpret_cast<uint2*>(a.out + qrow * kHeadDim + 4 * lane) =
         make_uint2(f32_to_bf16_rne(acc.x * inv) | (f32_to_bf16_rne(acc.y * inv) << 16),
@@ -164,6 +169,7 @@ __global__ void __launch_bounds__(kThreads) merge_partials_kernel(const MergeArg
     float m = wm[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) m = fmaxf(m, wm[w]);
+    if constexpr (kTree) m = m == -CUDART_INF_F ? 0.f : m;
     // ---- pass 2: this warp's share of sum exp2(L - M) O and sum exp2(L - M)
     // slots w, w + kWarps, ... (in batches of kBatch: a batch's loads are all
     // issued before its terms are added, in the same order)
@@ -205,7 +211,10 @@ __global__ void __launch_bounds__(kThreads) merge_partials_kernel(const MergeArg
         zt += wz[w];
       }
       const int64_t qrow = (int64_t)req * a.hq + h;
-      a.out[qrow * kHeadDim + threadIdx.x] = (uint16_t)f32_to_bf16_rne(o / zt);
+      if constexpr (kTree)
+        a.out[qrow * kHeadDim + threadIdx.x] = (uint16_t)f32_to_bf16_rne(zt == 0.f ? 0.f : o / zt);
+      else
+        a.out[qrow * kHeadDim + threadIdx.x] = (uint16_t)f32_to_bf16_rne(o / zt);
       if (threadIdx.x == 0 && a.lse != nullptr) a.lse[qrow] = (m + log2f(zt)) * kLn2;
     }
     __syncthreads();
@@ -282,6 +291,22 @@ cudaError_t launch_merge_partials(const MergeArgs& a, int grid, int32_t max_chun
   if (batch_short && max_chunks <= 4 * (kMergeThreads / 32))
     return cudaLaunchKernelEx(&cfg, merge_partials_kernel<4>, a);
   return cudaLaunchKernelEx(&cfg, merge_partials_kernel<1>, a);
+}
+
+cudaError_t launch_merge_tree(const MergeArgs& a, int grid, int32_t max_chunks,
+                              cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (max_chunks > kLongUnit)
+    return cudaLaunchKernelEx(&cfg, merge_partials_kernel<8, kMergeThreads, true>, a);
+  return cudaLaunchKernelEx(&cfg, merge_partials_kernel<1, kMergeThreads, true>, a);
 }
 
 cudaError_t launch_merge_states(const void* v_a, const float* s_a, const void* v_b,

@@ -1,0 +1,203 @@
+// Plans of tree contexts: every request has one or more query tokens, the
+// last ones of its cached tokens.
+//
+// A row block is up to 128 / g of a request's query tokens (the 128 rows of a
+// tile per KV head) with the range of cached tokens that any of them may see:
+// a window leaves the tokens before it out, and in a chain the tokens behind a
+// block's last one.  The blocks' ranges are laid end to end and cut into equal
+// stretches, one per group of Hkv CTAs, which walk the same tokens at the same
+// time, one KV head each: a token's heads are neighbours in memory.  Cuts fall
+// on whole rounds of the kernel.  A block in several parts leaves a partial
+// state per query token and part, and each of its tokens is a unit of the
+// merge, as the requests of a split shared-prefix block are.
+#include <algorithm>
+#include <cstring>
+#include <vector>
+
+#include "pkd_internal.h"
+#include "plan_layout.h"
+#include "plan_parts.h"
+
+namespace pkd {
+namespace {
+
+struct RowBlock {
+  int32_t req, block, tokens, first;   // first: query token of its first row
+  int64_t lo;                          // first cached token, a multiple of 16
+};
+
+}  // namespace
+
+int plan_schedule_tree(const pkd_config& cfg, int32_t n_cta, const Layout& L,
+                       const int32_t* q_indptr, const int32_t* indptr, const int32_t* indices,
+                       const int32_t* last, int32_t batch, int32_t causal, int32_t window,
+                       int32_t* words, pkd_plan_info* info, int64_t* end) {
+  if (batch < 0 || n_cta < 1 || words == nullptr || window < 0 || (causal != 0 && causal != 1))
+    return PKD_E_INVALID_ARG;
+  if (batch > 0 && (q_indptr == nullptr || indptr == nullptr || last == nullptr))
+    return PKD_E_INVALID_ARG;
+  if (batch > cfg.max_batch) return PKD_E_CAPACITY;
+  const int64_t P = cfg.page_size;
+  const int32_t hkv = cfg.num_kv_heads;
+  const int32_t rows = kTreeRows / (cfg.num_qo_heads / hkv);
+  thread_local std::vector<RowBlock> blocks;
+  thread_local std::vector<int64_t> lens;
+  thread_local std::vector<PlanPart> parts;
+  thread_local std::vector<int32_t> first_slot, n_chunks, order;
+  blocks.clear();
+  lens.clear();
+  int64_t nnz = 0, total = 0;
+  int32_t tokens = 0, most = 0;
+  if (batch > 0) {
+    if (indptr[0] != 0 || q_indptr[0] != 0) return PKD_E_BAD_TABLE;
+    for (int32_t i = 0; i < batch; ++i) {
+      const int64_t pages = (int64_t)indptr[i + 1] - indptr[i];
+      const int64_t n = (int64_t)q_indptr[i + 1] - q_indptr[i];
+      if (pages < 1 || last[i] < 1 || last[i] > P || n < 0) return PKD_E_BAD_TABLE;
+      const int64_t len = P * (pages - 1) + last[i];
+      // (the kernel counts tokens in 32 bits, up to a round past the end)
+      if (len > 0x7fffffffLL - 1024) return PKD_E_CAPACITY;
+      if (n > len) return PKD_E_BAD_TABLE;
+      if (q_indptr[i + 1] > cfg.max_batch) return PKD_E_CAPACITY;
+      const int64_t context = len - n;
+      most = std::max(most, (int32_t)n);
+      for (int32_t b = 0; (int64_t)b * rows < n; ++b) {
+        const int64_t r0 = (int64_t)b * rows, r1 = std::min<int64_t>(n, r0 + rows);
+        const int64_t at = context + (causal ? r0 : 0);   // the least position of a row
+        const int64_t lo = window > 0 ? std::max<int64_t>(0, at - window + 1) / 16 * 16 : 0;
+        const int64_t hi = causal ? context + r1 : len;
+        blocks.push_back(RowBlock{i, b, (int32_t)(r1 - r0), (int32_t)(q_indptr[i] + r0), lo});
+        lens.push_back(hi - lo);
+        total += hi - lo;
+      }
+    }
+    tokens = q_indptr[batch];
+    nnz = indptr[batch];
+    if (nnz > cfg.max_num_pages) return PKD_E_CAPACITY;
+    if (indices == nullptr) return PKD_E_INVALID_ARG;
+    if (!copy_checked(indices, words + L.page_list, nnz, cfg.num_pages)) return PKD_E_BAD_TABLE;
+  }
+  const int32_t nv = std::max(1, n_cta / hkv);
+  const int64_t alpha = cfg.alpha < 0 ? kTreeAlpha : cfg.alpha;
+  const int64_t min_chunk = cfg.min_chunk_tokens < 0 ? kTreeMinChunk : cfg.min_chunk_tokens;
+  const int64_t floor_c = ceil_div(std::max<int64_t>(min_chunk, 1), kTreeRound) * kTreeRound;
+  int64_t span =
+      std::max(alpha + floor_c, ceil_div(total + alpha * (int64_t)blocks.size(), nv));
+  while (!cut_even(lens, span, alpha, kTreeRound, floor_c, nv, &parts))
+    span += std::max<int64_t>(kTreeRound, span / 64);
+
+  // reduction map: the tokens of a block in several parts, blocks of most
+  // parts first, a token's slots one after the other in part order
+  const int32_t n_blocks = (int32_t)blocks.size();
+  n_chunks.assign((size_t)n_blocks, 0);
+  first_slot.assign((size_t)n_blocks, -1);
+  for (const PlanPart& p : parts) ++n_chunks[p.req];
+  order.clear();
+  for (int32_t i = 0; i < n_blocks; ++i)
+    if (n_chunks[i] > 1) order.push_back(i);
+  std::stable_sort(order.begin(), order.end(),
+                   [&](int32_t x, int32_t y) { return n_chunks[x] > n_chunks[y]; });
+  const int64_t n_items = (int64_t)parts.size() * hkv;
+  int64_t n_slots = 0;
+  for (int32_t i : order) n_slots += (int64_t)n_chunks[i] * blocks[i].tokens;
+  if (n_items > L.max_items || n_slots > L.max_slots) return PKD_E_CAPACITY;
+  int32_t* unit_words = words + L.units;
+  int32_t* merge_indptr = words + L.merge_indptr;
+  int32_t n_units = 0;
+  merge_indptr[0] = 0;
+  for (int32_t i : order) {
+    first_slot[i] = merge_indptr[n_units];
+    for (int32_t t = 0; t < blocks[i].tokens; ++t, ++n_units) {
+      unit_words[2 * n_units] = blocks[i].first + t;
+      unit_words[2 * n_units + 1] = n_chunks[i];
+      merge_indptr[n_units + 1] = merge_indptr[n_units] + n_chunks[i];
+    }
+  }
+
+  // queues: the parts of stretch v, once per KV head, on CTAs v * Hkv + head
+  // (all on one CTA when there are fewer CTAs than heads)
+  int32_t* cta_indptr = words + L.cta_indptr;
+  int32_t* item_words = words + L.items;
+  int64_t at = 0, p0 = 0;
+  int32_t cta = 0;
+  cta_indptr[0] = 0;
+  while (p0 < (int64_t)parts.size()) {
+    int64_t p1 = p0;
+    while (p1 < (int64_t)parts.size() && parts[p1].cta == parts[p0].cta) ++p1;
+    const int32_t v = parts[p0].cta;
+    for (int32_t h = 0; h < hkv; ++h) {
+      const int32_t c = n_cta >= hkv ? v * hkv + h : 0;
+      while (cta < c) cta_indptr[++cta] = (int32_t)at;
+      for (int64_t k = p0; k < p1; ++k, ++at) {
+        const PlanPart& p = parts[k];
+        const RowBlock& b = blocks[p.req];
+        int32_t* w = item_words + at * kItemWords;
+        int32_t chunk = 0;   // parts of one block follow one another
+        for (int64_t q = k; q > 0 && parts[q - 1].req == p.req; --q) ++chunk;
+        w[0] = b.req;
+        w[1] = (int32_t)(b.lo + p.tok_begin);
+        w[2] = (int32_t)(b.lo + p.tok_end);
+        w[3] = first_slot[p.req] >= 0 ? first_slot[p.req] + chunk : -1;
+        w[4] = indptr[b.req];
+        w[5] = b.block;
+        w[6] = first_slot[p.req] >= 0 ? n_chunks[p.req] : 0;
+        w[7] = h;
+      }
+    }
+    p0 = p1;
+  }
+  while (cta < n_cta) cta_indptr[++cta] = (int32_t)at;
+
+  // the requests' entries: first query token, query tokens, tokens before
+  // them in the cache, first page in the page list
+  int32_t* r = words + request_words(L.page_list, nnz);
+  for (int32_t i = 0; i < batch; ++i, r += kRequestWords) {
+    r[0] = q_indptr[i];
+    r[1] = q_indptr[i + 1] - q_indptr[i];
+    r[2] = (int32_t)(P * (indptr[i + 1] - indptr[i] - 1) + last[i] - r[1]);
+    r[3] = indptr[i];
+  }
+  *end = r - words;
+
+  int32_t* h = words;
+  std::memset(h, 0, sizeof(int32_t) * H_WORDS);
+  h[H_MAGIC] = kMagic;
+  h[H_BATCH] = tokens;
+  h[H_HQ] = cfg.num_qo_heads;
+  h[H_HKV] = hkv;
+  h[H_D] = cfg.head_dim;
+  h[H_P] = cfg.page_size;
+  h[H_NCTA] = n_cta;
+  h[H_NITEMS] = (int32_t)n_items;
+  h[H_NUNITS] = n_units;
+  h[H_NSLOTS] = (int32_t)n_slots;
+  h[H_CHUNK] = (int32_t)std::min<int64_t>(span - alpha, 0x7fffffff);
+  h[H_ALPHA] = (int32_t)std::min<int64_t>(alpha, 0x7fffffff);
+  h[H_NNZ] = (int32_t)nnz;
+  h[H_MAKESPAN] = (int32_t)std::min<int64_t>(span, 0x7fffffff);
+  h[H_MINCHUNK] = (int32_t)std::min<int64_t>(floor_c, 0x7fffffff);
+  h[H_BLOCK] = rows;
+  h[H_MAXCHUNKS] = order.empty() ? 0 : n_chunks[order[0]];
+  h[H_MAXBATCH] = cfg.max_batch;
+  h[H_MAXPAGES] = cfg.max_num_pages;
+  h[H_REQUESTS] = batch;
+  h[H_CAUSAL] = causal;
+  h[H_WINDOW] = window;
+  h[H_MAXQ] = most;
+  if (info) {
+    *info = pkd_plan_info{};
+    info->batch = tokens;
+    info->num_ctas = n_cta;
+    info->chunk_tokens = h[H_CHUNK];
+    info->num_items = (int32_t)n_items;
+    info->num_units = n_units;
+    info->num_slots = (int32_t)n_slots;
+    info->total_tokens = total;
+    info->makespan = span;
+    info->nnz = (int32_t)nnz;
+    info->schedule_words = (int32_t)*end;
+  }
+  return PKD_OK;
+}
+
+}  // namespace pkd

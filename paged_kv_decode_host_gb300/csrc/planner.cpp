@@ -35,6 +35,7 @@
 
 #include "pkd_internal.h"
 #include "plan_layout.h"
+#include "plan_parts.h"
 
 namespace pkd {
 namespace {
@@ -46,8 +47,6 @@ struct Item {
   int32_t tok_begin;
   int32_t tok_end;
 };
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Largest multiple of P, at least floor_c (itself a multiple of P), whose
 // split gives >= n_cta items; floor_c when none does.  The item count only
@@ -76,20 +75,6 @@ int64_t search_chunk(const std::vector<int64_t>& lens, int64_t n_cta, int64_t P,
       hi = mid - 1;
   }
   return lo * P;
-}
-
-// Copy n page ids and check 0 <= id < num_pages, in one pass the compiler
-// can vectorise (no early exit).
-bool copy_checked(const int32_t* __restrict__ src, int32_t* __restrict__ dst, int64_t n,
-                  int32_t num_pages) {
-  int32_t lo = 0, hi = 0;
-  for (int64_t k = 0; k < n; ++k) {
-    const int32_t v = src[k];
-    dst[k] = v;
-    lo = v < lo ? v : lo;
-    hi = v > hi ? v : hi;
-  }
-  return lo >= 0 && hi < num_pages;
 }
 
 // LPT visiting order: descending cost, then request, then chunk.
@@ -468,47 +453,6 @@ int64_t write_requests(const Layout& L, int32_t page_size, const int32_t* indptr
 // quarter of the time (32 requests of 4,096 tokens).  A cut leaves at least
 // the split floor on both sides where it can; the stretch is the shortest of
 // a few per cent steps that fits.
-namespace {
-
-struct LatentPart {
-  int32_t req, tok_begin, tok_end, cta;   // cta: of the first block of heads
-};
-
-// Cut the requests into stretches of cost `span` for nv CTAs; false when they
-// do not fit.
-bool cut_even(const std::vector<int64_t>& lens, int64_t span, int64_t alpha, int64_t P,
-              int64_t floor_c, int32_t nv, std::vector<LatentPart>* parts) {
-  parts->clear();
-  int32_t v = 0;
-  int64_t cap = span;
-  for (size_t i = 0; i < lens.size(); ++i) {
-    int64_t pos = 0;
-    while (pos < lens[i]) {
-      if (v >= nv) return false;
-      const int64_t rem = lens[i] - pos;
-      int64_t take = 0;
-      if (rem + alpha <= cap) {
-        take = rem;
-      } else if (cap == span) {   // an empty CTA: as much as fits, but no short rest
-        take = (span - alpha) / P * P;
-        if (rem - take < floor_c) take = std::min(take, ceil_div(ceil_div(rem, 2), P) * P);
-      } else {
-        take = std::min((cap - alpha) / P * P, (rem - floor_c) / P * P);
-        if (take < floor_c) take = 0;
-      }
-      if (take > 0) parts->push_back(LatentPart{(int32_t)i, (int32_t)pos, (int32_t)(pos + take), v});
-      pos += take;
-      cap -= take + alpha;
-      if (pos < lens[i]) {   // this CTA is full
-        ++v;
-        cap = span;
-      }
-    }
-  }
-  return true;
-}
-
-}  // namespace
 
 int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
                          const int32_t* indptr, const int32_t* indices, const int32_t* last,
@@ -518,7 +462,7 @@ int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   if (batch > cfg.max_batch) return PKD_E_CAPACITY;
   const int64_t P = cfg.page_size;
   thread_local std::vector<int64_t> lens;
-  thread_local std::vector<LatentPart> parts;
+  thread_local std::vector<PlanPart> parts;
   thread_local std::vector<int32_t> first_slot, n_chunks, order;
   lens.resize((size_t)batch);
   int64_t nnz = 0, total = 0;
@@ -550,7 +494,7 @@ int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   // (all its blocks of heads share it); most parts first, as elsewhere
   n_chunks.assign((size_t)batch, 0);
   first_slot.assign((size_t)batch, -1);
-  for (const LatentPart& p : parts) ++n_chunks[p.req];
+  for (const PlanPart& p : parts) ++n_chunks[p.req];
   order.clear();
   for (int32_t i = 0; i < batch; ++i)
     if (n_chunks[i] > 1) order.push_back(i);
@@ -586,7 +530,7 @@ int plan_schedule_latent(const pkd_config& cfg, int32_t n_cta, const Layout& L,
       const int32_t c = n_cta >= blocks ? v * blocks + b : 0;
       while (cta < c) cta_indptr[++cta] = (int32_t)at;
       for (int64_t k = p0; k < p1; ++k, ++at) {
-        const LatentPart& p = parts[k];
+        const PlanPart& p = parts[k];
         int32_t* w = item_words + at * kItemWords;
         int32_t chunk = 0;   // parts of one request follow one another
         for (int64_t q = k; q > 0 && parts[q - 1].req == p.req; --q) ++chunk;

@@ -16,6 +16,10 @@
  * layer array), after init_ops; an integer that does not fit its C type raises
  * OverflowError.
  *
+ * plan_tree, run_tree, rotate_append, accept_kv: pkd_plan_tree (arrays as plan's),
+ * pkd_run_tree, pkd_rotate_append_kv and pkd_accept_kv (a list of addresses), after
+ * init_step.
+ *
  * status is the C ABI's return value, or NOT_HANDLED (1000) when an argument
  * is not a 1-D C-contiguous int32 buffer: the caller then takes its general
  * path, which converts or rejects the input with a proper message. */
@@ -299,7 +303,143 @@ static PyObject *evict(PyObject *self, PyObject *args) {
       (size_t)ws_bytes, (int32_t *)ADDR(err), ADDR(stream)));
 }
 
+typedef int (*plan_tree_fn)(void *ctx, const int32_t *q_indptr, const int32_t *indptr,
+                            const int32_t *indices, const int32_t *last, int32_t batch,
+                            int32_t causal, int32_t window, void *stream, uint64_t *epoch);
+typedef int (*run_tree_fn)(void *ctx, const void *q, int32_t rows, const void *kv, void *out,
+                           float *lse, const uint32_t *mask, int32_t mask_words,
+                           const int32_t *depths, const float *slopes, float scale,
+                           float score_cap, uint64_t expect_epoch, void *stream);
+typedef int (*rotate_fn)(const void *q, int64_t q_token, int64_t q_head, void *q_out,
+                         int64_t out_token, int64_t out_head, const void *k, int64_t k_token,
+                         int64_t k_head, const void *v, int64_t v_token, int64_t v_head,
+                         const void *q_norm, const void *k_norm, int32_t norms_f32, float eps,
+                         const uint64_t *turns, const int32_t *axes, int32_t rotary_dim,
+                         int32_t interleaved, float rope_scale, const int32_t *rope_positions,
+                         int32_t num_axes, const int32_t *batch_indices,
+                         const int32_t *positions, int32_t n, const int32_t *indptr,
+                         const int32_t *indices, int32_t num_indices, const int32_t *last,
+                         int32_t batch, void *kv, int32_t num_pages, int32_t page_size,
+                         int32_t hq, int32_t hkv, int32_t head_dim, float k_scale, float v_scale,
+                         uint32_t flags, int32_t *err, void *stream);
+typedef int (*accept_fn)(int32_t layers, void *const *kv, const int32_t *accepted, int32_t width,
+                         const int32_t *drafted, const int32_t *indptr, const int32_t *indices,
+                         int32_t num_indices, const int32_t *last, int32_t batch,
+                         int32_t num_pages, int32_t page_size, int32_t hkv, int32_t head_dim,
+                         uint32_t flags, int32_t *err, void *stream);
+static plan_tree_fn g_plan_tree = NULL;
+static run_tree_fn g_run_tree = NULL;
+static rotate_fn g_rotate = NULL;
+static accept_fn g_accept = NULL;
+
+static PyObject *init_step(PyObject *self, PyObject *args) {
+  unsigned long long a, b, c, d;
+  (void)self;
+  if (!PyArg_ParseTuple(args, "KKKK", &a, &b, &c, &d)) return NULL;
+  g_plan_tree = (plan_tree_fn)(uintptr_t)a;
+  g_run_tree = (run_tree_fn)(uintptr_t)b;
+  g_rotate = (rotate_fn)(uintptr_t)c;
+  g_accept = (accept_fn)(uintptr_t)d;
+  Py_RETURN_NONE;
+}
+
+static PyObject *plan_tree(PyObject *self, PyObject *args) {
+  unsigned long long ctx, stream;
+  int causal, window;
+  PyObject *objs[4];
+  Py_buffer v[4];   /* q_indptr, indptr, indices, last */
+  (void)self;
+  if (!PyArg_ParseTuple(args, "KOOOOiiK", &ctx, &objs[0], &objs[1], &objs[2], &objs[3], &causal,
+                        &window, &stream))
+    return NULL;
+  if (g_plan_tree == NULL) return Py_BuildValue("iK", NOT_HANDLED, 0ULL);
+  for (int k = 0; k < 4; ++k) {
+    if (!get_i32(objs[k], &v[k])) {
+      for (int j = 0; j < k; ++j) PyBuffer_Release(&v[j]);
+      return Py_BuildValue("iK", NOT_HANDLED, 0ULL);
+    }
+  }
+  const Py_ssize_t batch = v[3].shape[0];
+  int st;
+  uint64_t epoch = 0;
+  if (v[0].shape[0] != batch + 1 || v[1].shape[0] != batch + 1 || batch > INT32_MAX ||
+      (batch > 0 && v[2].shape[0] < ((const int32_t *)v[1].buf)[batch])) {
+    st = NOT_HANDLED;   /* the general path reports the shape error */
+  } else {
+    st = g_plan_tree((void *)(uintptr_t)ctx, (const int32_t *)v[0].buf, (const int32_t *)v[1].buf,
+                     v[2].shape[0] ? (const int32_t *)v[2].buf : NULL, (const int32_t *)v[3].buf,
+                     (int32_t)batch, causal, window, (void *)(uintptr_t)stream, &epoch);
+  }
+  for (int k = 0; k < 4; ++k) PyBuffer_Release(&v[k]);
+  return Py_BuildValue("iK", st, (unsigned long long)epoch);
+}
+
+static PyObject *run_tree(PyObject *self, PyObject *args) {
+  unsigned long long ctx, q, kv, out, lse, mask, depths, slopes, epoch, stream;
+  int rows, words;
+  float scale, cap;
+  (void)self;
+  if (!PyArg_ParseTuple(args, "KKiKKKKiKKffKK", &ctx, &q, &rows, &kv, &out, &lse, &mask, &words,
+                        &depths, &slopes, &scale, &cap, &epoch, &stream))
+    return NULL;
+  if (g_run_tree == NULL) return PyLong_FromLong(NOT_HANDLED);
+  return PyLong_FromLong(g_run_tree(ADDR(ctx), ADDR(q), rows, ADDR(kv), ADDR(out),
+                                    (float *)ADDR(lse), (const uint32_t *)ADDR(mask), words,
+                                    (const int32_t *)ADDR(depths), (const float *)ADDR(slopes),
+                                    scale, cap, (uint64_t)epoch, ADDR(stream)));
+}
+
+static PyObject *rotate_append(PyObject *self, PyObject *args) {
+  unsigned long long q, qo, k, v, qn, kn, turns, axes, rp, bi, pos, ip, ix, la, kv, err, stream;
+  long long qt, qh, ot, oh, kt, kh, vt, vh;
+  int f32, rotary, pairs, n_axes, n, nnz, batch, pages, page, hq, hkv, dim;
+  float eps, rs, ks, vs;
+  unsigned int flags;
+  (void)self;
+  if (!PyArg_ParseTuple(args, "KLLKLLKLLKLLKKifKKiifKiKKiKKiKiKiiiiiffIKK", &q, &qt, &qh, &qo, &ot,
+                        &oh, &k, &kt, &kh, &v, &vt, &vh, &qn, &kn, &f32, &eps, &turns, &axes,
+                        &rotary, &pairs, &rs, &rp, &n_axes, &bi, &pos, &n, &ip, &ix, &nnz, &la,
+                        &batch, &kv, &pages, &page, &hq, &hkv, &dim, &ks, &vs, &flags, &err,
+                        &stream))
+    return NULL;
+  if (g_rotate == NULL) return PyLong_FromLong(NOT_HANDLED);
+  return PyLong_FromLong(g_rotate(
+      ADDR(q), qt, qh, ADDR(qo), ot, oh, ADDR(k), kt, kh, ADDR(v), vt, vh, ADDR(qn), ADDR(kn), f32,
+      eps, (const uint64_t *)ADDR(turns), (const int32_t *)ADDR(axes), rotary, pairs, rs,
+      (const int32_t *)ADDR(rp), n_axes, (const int32_t *)ADDR(bi), (const int32_t *)ADDR(pos), n,
+      (const int32_t *)ADDR(ip), (const int32_t *)ADDR(ix), nnz, (const int32_t *)ADDR(la), batch,
+      ADDR(kv), pages, page, hq, hkv, dim, ks, vs, (uint32_t)flags, (int32_t *)ADDR(err),
+      ADDR(stream)));
+}
+
+static PyObject *accept_kv(PyObject *self, PyObject *args) {
+  PyObject *kv;
+  unsigned long long acc, dr, ip, ix, la, err, stream;
+  int width, nnz, batch, pages, page, hkv, dim;
+  unsigned int flags;
+  void *kvs[MAX_LAYERS];
+  (void)self;
+  if (!PyArg_ParseTuple(args, "OKiKKKiKiiiiiIKK", &kv, &acc, &width, &dr, &ip, &ix, &nnz, &la,
+                        &batch, &pages, &page, &hkv, &dim, &flags, &err, &stream))
+    return NULL;
+  const Py_ssize_t layers = PyList_Check(kv) ? PyList_GET_SIZE(kv) : 0;
+  if (g_accept == NULL || layers < 1 || layers > MAX_LAYERS || !addresses(kv, layers, kvs))
+    return PyLong_FromLong(NOT_HANDLED);
+  return PyLong_FromLong(g_accept((int32_t)layers, kvs, (const int32_t *)ADDR(acc), width,
+                                  (const int32_t *)ADDR(dr), (const int32_t *)ADDR(ip),
+                                  (const int32_t *)ADDR(ix), nnz, (const int32_t *)ADDR(la), batch,
+                                  pages, page, hkv, dim, (uint32_t)flags, (int32_t *)ADDR(err),
+                                  ADDR(stream)));
+}
+
 static PyMethodDef methods[] = {
+    {"init_step", init_step, METH_VARARGS,
+     "init_step(plan_tree_address, run_tree_address, rotate_append_address, accept_address)"},
+    {"plan_tree", plan_tree, METH_VARARGS,
+     "plan_tree(ctx, q_indptr, indptr, indices, last, causal, window, stream) -> (status, epoch)"},
+    {"run_tree", run_tree, METH_VARARGS, "pkd_run_tree -> status"},
+    {"rotate_append", rotate_append, METH_VARARGS, "pkd_rotate_append_kv -> status"},
+    {"accept_kv", accept_kv, METH_VARARGS, "pkd_accept_kv (a list of addresses) -> status"},
     {"init_ops", init_ops, METH_VARARGS,
      "init_ops(accumulate_weights_address, append_latent_address, evict_address, "
      "evict_workspace_bytes_address)"},

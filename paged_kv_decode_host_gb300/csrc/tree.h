@@ -1,0 +1,45 @@
+// Attention of drafted tokens over a paged cache (tree_kernel.cu): sizes,
+// arguments and launchers.
+#pragma once
+
+#include <stdint.h>
+
+#include <cuda.h>
+#include <cuda_runtime_api.h>
+
+namespace pkd {
+
+constexpr int kTreeRows = 128;       // query rows of a tile: 128 / g tokens x g heads of a KV head
+constexpr int kTreeRound = 128;      // tokens per round of the kernel; plans cut at multiples of it
+constexpr int kTreeAlpha = 256;      // an item's fixed cost in tokens
+constexpr int kTreeMinChunk = 256;   // split floor in tokens
+
+struct TreeArgs {
+  const int32_t* sched;
+  float* o_part;            // fp32 [slot][Hq][128]
+  float* l_part;            // fp32 [slot][Hq] (natural log)
+  int32_t* err;
+  const uint16_t* q;        // bf16 [tokens][Hq][128]
+  const uint16_t* kv;       // the cache
+  uint16_t* out;            // bf16 [tokens][Hq][128]
+  float* lse;               // fp32 [tokens][Hq] or null
+  const uint32_t* mask;     // [tokens][mask_words] or null
+  const int32_t* depths;    // [tokens] or null: the tokens' numbers in their request
+  const float* slopes;      // [Hq] or null
+  int64_t off_cta, off_items, off_pages;
+  int64_t page_elems, token_elems, head_elems, v_elems;   // strides in the cache
+  int32_t hq, hkv, page_size, num_pages, mask_words;
+  int32_t tokens;           // rows of q, out and lse
+  float scale_log2;         // scale * log2(e); with a cap: 2 scale / cap * log2(e)
+  float cap_log2;           // cap * log2(e), 0 without
+  int32_t wait_epoch;
+  CUtensorMap kv_map;       // 16-token boxes of one 128-byte half of a KV head
+  CUtensorMap q_map;        // boxes of a KV head's 128 query rows and one half
+};
+
+int tree_smem_bytes();
+cudaError_t tree_prepare();
+cudaError_t tree_occupancy(int* blocks_per_sm);
+cudaError_t launch_tree(const TreeArgs& a, int grid, cudaStream_t stream);
+
+}  // namespace pkd

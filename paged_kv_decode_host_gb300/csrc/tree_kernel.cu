@@ -1,0 +1,693 @@
+// Attention of drafted tokens over a paged cache for sm_103a.
+//
+// Request b has l_b cached tokens, the last n_b of which are drafted in this
+// step: a tree, or a chain.  With c_b = l_b - n_b, query token i (n_b of them)
+// stands at position c_b + depth_i, cached token t < c_b at t, draft j at c_b
+// + depth_j.  Per query head
+//     s = scale q.k;  s = cap tanh(s / cap);  s -= slope (pos_q - pos_k)
+// over the tokens t < c_b and the drafts whose bit is set in the query's mask
+// (a chain: j <= i), in a window only where pos_q - pos_k < window;
+//     out = softmax(s) V,  lse = log sum exp(s);  nothing seen: 0 and -inf.
+//
+// A work item is one KV head of up to 128 / g query tokens of a request over a
+// range of its cached tokens: the 128 query rows of a tile share every key and
+// value, so both products run on the tensor cores as in the dense
+// shared-prefix role (prefix_tc_body.cuh, whose roles, rings and tensor-memory
+// map this kernel has: warp 8 copies queries and K, warp 10 V, warp 9 issues
+// S = Q K^T, warp 11 O += P V, warps 0-7 the softmax, two per lane quadrant
+// with 64 of a round's 128 columns each).  What differs:
+//  * rounds that some row does not see whole (drafts, a window's edge, the
+//    range's end) get a 64-bit word per row of the columns that it sees, from
+//    the context's length, the window and 64 bits of the mask; other rounds
+//    (nearly all of a long context) pay for none of it;
+//  * masked scores are replaced, never added to, so what K holds there plays
+//    no part.  P is 0 there, and 0 x V is 0 only for finite V: a result that
+//    is not finite while some token that its row does not see has a value
+//    that is not is summed again over the tokens seen (redo_row);
+//  * rows that have seen nothing keep the base -inf and a sum of 0;
+//  * tanh(x) = 1 - 2 / (1 + e^2x): one exponential and one reciprocal, an
+//    absolute error of about 2^-22 (x cap); the hardware's tanh (2^-11) would
+//    show in the lse;
+//  * distances are subtracted as whole numbers before they meet the slope;
+//  * P is rounded to bf16 for the product (V's type, which the tensor cores
+//    want for both); the row's sum, and with it the lse, is that of the weights
+//    before it;
+//  * lane quadrants without a query row (fewer than 97 rows) only keep the
+//    barriers' count.
+// Every wait is bounded, as in the dense role.
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "plan_layout.h"
+#include "prefix_tc_body.cuh"
+#include "tree.h"
+
+namespace pkd {
+namespace {
+
+using namespace dev;
+using namespace tc;
+static_assert(kTreeRows == kDenseRows && kTreeRound == kRoundTok, "the dense role's tile");
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// the lowest x bits of 64
+__device__ __forceinline__ uint64_t low_bits(int x) {
+  return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One query row of an item.
+struct Row {
+  const uint32_t* mask;   // its words, null in a chain
+  int words;
+  const int32_t* depths;  // of its request's drafts, or null: their numbers
+  int ctx, drafts;        // cached tokens before the drafts, drafts
+  int i, depth;           // its token's number and depth
+  int window;             // 0: none
+  int first_seen;         // the window's first context token (or below 0)
+};
+
+__device__ __forceinline__ int depth_of(const Row& r, int j) {
+  return r.depths != nullptr ? max(__ldg(r.depths + j), 0) : j;
+}
+
+// Bits j0 .. j0 + 63 of the row's mask (j0 > -64), those outside it 0.
+__device__ __forceinline__ uint64_t mask_bits(const Row& r, int j0) {
+  const int w = j0 >> 5, s = j0 & 31;   // w may be -1 or -2
+  auto word = [&](int k) -> uint64_t { return k >= 0 && k < r.words ? __ldg(r.mask + k) : 0u; };
+  const uint64_t lo = word(w) | (word(w + 1) << 32);
+  return s == 0 ? lo : (lo >> s) | (word(w + 2) << (64 - s));
+}
+
+// The columns c of 64 whose token t0 + c, below te, the row sees.
+__device__ __forceinline__ uint64_t visible(const Row& r, int t0, int te) {
+  uint64_t vis = low_bits(r.ctx - t0) & ~low_bits(r.first_seen - t0);
+  const int j0 = t0 - r.ctx;
+  if (j0 > -64 && j0 < r.drafts) {
+    uint64_t own = r.mask != nullptr ? mask_bits(r, j0)
+                                     : low_bits(r.i + 1 - j0) & ~low_bits(-j0);
+    own &= low_bits(r.drafts - j0);
+    if (r.window > 0 && r.depth >= r.window)   // (deeper than the window: rare)
+      for (uint64_t m = own; m != 0; m &= m - 1) {
+        const int c = __ffsll((long long)m) - 1;
+        if (r.depth - depth_of(r, j0 + c) >= r.window) own &= ~(1ull << c);
+      }
+    vis |= own;
+  }
+  return vis & low_bits(te - t0);
+}
+
+__device__ __forceinline__ float capped(float s, float scale, float cap) {
+  return fmaf(-2.f * cap, fast_rcp(1.f + fast_exp2(s * scale)), cap);
+}
+
+__device__ __forceinline__ int64_t token_offset(const TreeArgs& a, int first_page, int head, int t) {
+  int page = a.sched[a.off_pages + first_page + t / a.page_size];
+  if ((unsigned)page >= (unsigned)a.num_pages) page = 0;   // (as the copies do)
+  return page * a.page_elems + (t % a.page_size) * a.token_elems + head * a.head_elems;
+}
+
+__device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+
+// O of 32 dims (from dim0) of one row, unnormalised, summed over the tokens
+// that the row sees, if one that it does not see has a value that is not
+// finite in these dims; else left as it is.  Slow, and only for caches that
+// hold such values.
+__device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uint16_t* q, int first_page,
+                                      int head, int tb, int te, int dim0, float base, float slope2,
+                                      uint32_t (&o)[32]) {
+  auto sees = [&](int t) { return (visible(r, t, te) & 1u) != 0; };
+  bool poisoned = false;
+  auto look = [&](int t) {
+    if (sees(t)) return;
+    const uint16_t* v = a.kv + token_offset(a, first_page, head, t) + a.v_elems + dim0;
+    for (int d = 0; d < 32; ++d) poisoned |= (v[d] & 0x7f80u) == 0x7f80u;
+  };
+  for (int t = tb; t < min(te, min(r.first_seen, r.ctx)) && !poisoned; ++t) look(t);
+  for (int t = max(tb, r.ctx); t < te && !poisoned; ++t) look(t);
+  if (!poisoned) return;
+  float acc[32];
+  for (int d = 0; d < 32; ++d) acc[d] = 0.f;
+  for (int t = tb; t < te; ++t) {
+    if (!sees(t)) continue;
+    const uint16_t* k = a.kv + token_offset(a, first_page, head, t);
+    float s = 0.f;
+    for (int d = 0; d < kHeadDim; ++d) s = fmaf(bf16_at(q + d), bf16_at(k + d), s);
+    s = a.cap_log2 != 0.f ? capped(s, a.scale_log2, a.cap_log2) : s * a.scale_log2;
+    const int64_t away = t < r.ctx ? (int64_t)r.ctx + r.depth - t : (int64_t)r.depth - depth_of(r, t - r.ctx);
+    s = fmaf(-slope2, (float)away, s);
+    const float p = fast_exp2(s - base);
+    for (int d = 0; d < 32; ++d) acc[d] = fmaf(p, bf16_at(k + a.v_elems + dim0 + d), acc[d]);
+  }
+  for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(acc[d]);
+}
+
+template <bool kCap, bool kSlopes>
+__global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
+  pdl_launch_dependents();
+  const bool chain = a.sched[H_CAUSAL] != 0;
+  // a captured launch under a later plan that its tensors do not fit
+  if (a.sched[H_BATCH] > a.tokens || (!chain && a.sched[H_MAXQ] > 32 * (int64_t)a.mask_words)) {
+    if (threadIdx.x == 0) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+    pdl_wait();
+    return;
+  }
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;
+  uint8_t* stages = smem + kQBytes;
+  TcSmem* sh = reinterpret_cast<TcSmem*>(stages + kTcStages * kStageBytes);
+  volatile int* abort_flag = &sh->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int it0 = a.sched[a.off_cta + blockIdx.x];
+  const int it1 = a.sched[a.off_cta + blockIdx.x + 1];
+  if (it0 >= it1) {
+    pdl_wait();
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTcStages; ++s) {
+      mbar_init(&sh->fullk[s], 1);
+      mbar_init(&sh->emptyk[s], 1);
+      mbar_init(&sh->fullv[s], 1);
+      mbar_init(&sh->emptyv[s], 1);
+    }
+    mbar_init(&sh->qfull, 1);
+    mbar_init(&sh->qfree, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh->sfull[b], 1);
+      mbar_init(&sh->sfree[b], kSoftmaxWarps);
+      mbar_init(&sh->pfull[b], kSoftmaxWarps);
+      mbar_init(&sh->pfree[b], 1);
+    }
+    mbar_init(&sh->ofree, kSoftmaxWarps);
+    for (int q = 0; q < 4; ++q) mbar_init(&sh->xch[q], 2);
+    mbar_init(&sh->fin, 2);
+    sh->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sh->tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const int P = a.page_size;
+  const int g = a.hq / a.hkv;
+  const int tile_tokens = kTreeRows / g;
+  const int32_t* requests = a.sched + request_words(a.off_pages, a.sched[H_NNZ]);
+
+  if (warp == kWarpK || warp == kWarpV) {
+    // ------------------------------------------- producers (queries, K; V)
+    const int c = warp == kWarpK ? 0 : 1;
+    uint64_t* full = c ? sh->fullv : sh->fullk;
+    uint64_t* empty = c ? sh->emptyv : sh->emptyk;
+    uint8_t* ring = stages + (size_t)c * kTcStages * kKvBytes;
+    const uint64_t policy = l2_evict_first_policy();
+    pdl_wait();   // q and the cache may come from the previous kernel
+    int st = 0, nq = 0;
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+      const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
+      const int tb = item[1], te = item[2], poff = item[4], head = item[7];
+      // the item's queries (the previous item's score MMAs must be done)
+      if (c == 0 && it > it0 &&
+          !tc_wait(&sh->qfree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane)) {
+        ok = false;
+        break;
+      }
+      if (c == 0 && lane == 0) {
+        const int row0 = requests[item[0] * kRequestWords] + item[5] * tile_tokens;
+        ++nq;
+        mbar_arrive_expect_tx(&sh->qfull, (uint32_t)kQBytes);
+        for (int h = 0; h < 2; ++h)
+          tensor_copy_g2s(sQ + h * (kQBytes / 2), &a.q_map, 0, h, 0, head, row0, &sh->qfull, policy);
+      }
+      __syncwarp();
+      // page ids of 32 tiles of 16 tokens at a time (tb is a multiple of 16)
+      const int ntiles = (te - tb + 15) >> 4;
+      int base = -32, my_page = 0;
+      for (int t = tb, k = 0; t < te; t += kRoundTok, ++st, ++k) {
+        const int n = min(kRoundTok, te - t);
+        const int nbox = (n + 15) >> 4;
+        const int tile0 = kRoundTiles * k;
+        if (tile0 + kRoundTiles > base + 32) {
+          base = tile0;
+          my_page = 0;
+          if (base + lane < ntiles) {
+            my_page = a.sched[a.off_pages + poff + (tb + 16 * (base + lane)) / P];
+            if ((unsigned)my_page >= (unsigned)a.num_pages) {
+              atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+              my_page = 0;
+            }
+          }
+        }
+        const int slot = st % kTcStages;
+        const uint32_t round = (uint32_t)(st / kTcStages);
+        if (round > 0 && !tc_wait(&empty[slot], (round - 1) & 1u, abort_flag, a.err, lane)) {
+          ok = false;
+          break;
+        }
+        // lane 2 j + h (lanes 0-15) copies half h of tile j
+        const int j = lane >> 1, h = lane & 1;
+        const int page = __shfl_sync(kFull, my_page, (tile0 + (j & 7) - base) & 31);
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(2 * nbox * kBoxBytes));
+        __syncwarp();
+        if (j < nbox)
+          tensor_copy_g2s(ring + (size_t)slot * kKvBytes + h * kHalfBytes + j * kBoxBytes,
+                          &a.kv_map, 0, (t + 16 * j) % P, h, head, 2 * page + c, &full[slot],
+                          policy);
+      }
+    }
+    // drain: the last phase of every slot, and the last queries
+    if (lane == 0) {
+      for (int s = 0; s < kTcStages; ++s)
+        if (st > s && !mbar_wait(&full[s], (uint32_t)(((st - 1 - s) / kTcStages) & 1), nullptr))
+          atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+      if (nq > 0 && !mbar_wait(&sh->qfull, (uint32_t)((nq - 1) & 1), nullptr))
+        atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+    }
+  } else if (warp == kWarpS) {
+    // ------------------------------------------- S = Q K^T (lane 0 issues)
+    const uint32_t q0 = smem_u32(sQ), st0 = smem_u32(stages);
+    int r = 0;
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+      const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
+      const int tb = item[1], te = item[2];
+      const int nr = rounds_of(tb, te);
+      if (!tc_wait(&sh->qfull, (uint32_t)((it - it0) & 1), abort_flag, a.err, lane)) {
+        ok = false;
+        break;
+      }
+      for (int k = 0; k < nr; ++k, ++r) {
+        const int slot = r % kTcStages, b = r & 1;
+        if (!tc_wait(&sh->fullk[slot], (uint32_t)((r / kTcStages) & 1), abort_flag, a.err, lane) ||
+            (r >= 2 &&
+             !tc_wait(&sh->sfree[b], (uint32_t)(((r >> 1) - 1) & 1), abort_flag, a.err, lane))) {
+          ok = false;
+          break;
+        }
+        const int n = min(kRoundTok, te - (tb + k * kRoundTok));
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t idesc_s = mma_idesc(kDenseRows, 16 * ((n + 15) >> 4), 0);
+          const uint32_t kbase = st0 + (uint32_t)(slot * kKvBytes);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss(tmem + kColS + kSCols * b,
+                   smem_desc(q0 + (kk >> 2) * (kQBytes / 2) + (kk & 3) * 32, 16, 1024),
+                   smem_desc(kbase + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024),
+                   idesc_s, kk > 0);
+          mma_commit(&sh->sfull[b]);
+          mma_commit(&sh->emptyk[slot]);
+          if (k == nr - 1) mma_commit(&sh->qfree);   // the item's last score MMA
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      mma_commit(&sh->fin);
+      if (!mbar_wait(&sh->fin, 0, nullptr)) atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp == kWarpPV) {
+    // --------------------------------------------- O += P V (lane 0 issues)
+    const uint32_t idesc_o = mma_idesc(kDenseRows, kHeadDim, 1);
+    int r = 0;
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+      const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
+      const int tb = item[1], te = item[2];
+      const int nr = rounds_of(tb, te);
+      for (int k = 0; k < nr; ++k, ++r) {
+        const int slot = r % kTcStages, b = r & 1;
+        if (!tc_wait(&sh->pfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane) ||
+            !tc_wait(&sh->fullv[slot], (uint32_t)((r / kTcStages) & 1), abort_flag, a.err, lane) ||
+            (k == 0 && it > it0 &&
+             !tc_wait(&sh->ofree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane))) {
+          ok = false;
+          break;
+        }
+        const int n = min(kRoundTok, te - (tb + k * kRoundTok));
+        const int nbox = (n + 15) >> 4;
+        uint8_t* vbase = stages + (size_t)(kTcStages + slot) * kKvBytes;
+        if (n & 15) {
+          // slots past the range's end in the last tile: P is 0 there, but
+          // 0 x NaN would poison O, so zero those V rows (both halves)
+          const int v0 = n & 15;
+          uint8_t* tile = vbase + (nbox - 1) * kBoxBytes;
+          for (int i = lane; i < 2 * (16 - v0) * 8; i += 32) {
+            const int h = i / ((16 - v0) * 8), rem = i % ((16 - v0) * 8);
+            const int row = v0 + rem / 8, chunk = rem % 8;
+            *reinterpret_cast<uint4*>(tile + h * kHalfBytes + row * 128 + chunk * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t vb = smem_u32(vbase);
+          for (int j = 0; j < nbox; ++j)
+            mma_ts(tmem + kColO, tmem + kColP + kPCols * b + 8 * j,
+                   smem_desc(vb + j * kBoxBytes, kHalfBytes, 1024), idesc_o, k > 0 || j > 0);
+          mma_commit(&sh->pfree[b]);
+          mma_commit(&sh->emptyv[slot]);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      mma_commit(&sh->fin);
+      if (!mbar_wait(&sh->fin, 0, nullptr)) atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------- softmax + epilogue
+    const int quad = warp & 3, half = warp >> 2;   // lane quadrant, score / O columns half
+    const int row = quad * 32 + lane;               // tile row = tensor-memory lane
+    const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);   // this quadrant's lanes
+    const int window = a.sched[H_WINDOW];
+    pdl_wait();   // outputs, mask and depths may belong to the previous kernel
+    int rho = 0;
+    uint32_t xc = 0;   // exchanges with the partner warp so far (the barrier's phase)
+    bool ok = true;
+    auto pv_wait = [&](int r) -> bool {
+      if (r < 0) return true;
+      return tc_wait(&sh->pfree[r & 1], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane);
+    };
+    // one float per row with the partner warp of this quadrant, through
+    // tensor-memory columns that both have read
+    auto exchange = [&](uint32_t mine, uint32_t theirs, float v, float* other) -> bool {
+      tmem_st1(tq + mine, __float_as_uint(v));
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->xch[quad]);
+      if (!tc_wait(&sh->xch[quad], xc & 1u, abort_flag, a.err, lane)) return false;
+      ++xc;
+      tc_fence_after();
+      *other = __uint_as_float(tmem_ld1(tq + theirs));
+      tmem_wait_ld();
+      return true;
+    };
+    for (int it = it0; it < it1 && ok; ++it) {
+      const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
+      const int tb = item[1], te = item[2], dst = item[3], first_page = item[4];
+      const int i0 = item[5] * tile_tokens, stride = item[6], head = item[7];
+      const int32_t* entry = requests + item[0] * kRequestWords;
+      const int q_first = entry[0], drafts = entry[1], ctx = entry[2];
+      const int nr = rounds_of(tb, te);
+      const int r0 = rho;
+      rho = r0 + nr;
+      const int n_tok = min(tile_tokens, drafts - i0);
+      if (quad * 32 >= n_tok * g) {
+        // no row of this quadrant: keep the barriers' count, in their order
+        for (int r = r0; r < rho && ok; ++r) {
+          ok = tc_wait(&sh->sfull[r & 1], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&sh->sfree[r & 1]);
+          ok = r < 2 || pv_wait(r - 2);
+          if (ok && lane == 0) mbar_arrive(&sh->pfull[r & 1]);
+        }
+        ok = ok && pv_wait(rho - 2) && pv_wait(rho - 1);
+        if (ok && lane == 0) mbar_arrive(&sh->ofree);
+        continue;
+      }
+      const int i = row / g, hq = head * g + row % g;
+      const bool valid = i < n_tok;
+      Row me;
+      me.ctx = ctx;
+      me.drafts = drafts;
+      me.i = i0 + i;
+      me.words = a.mask_words;
+      me.mask = chain || !valid ? nullptr : a.mask + (int64_t)(q_first + me.i) * a.mask_words;
+      me.depths = chain || a.depths == nullptr ? nullptr : a.depths + q_first;
+      me.depth = valid ? depth_of(me, me.i) : 0;
+      me.window = window;
+      // (64 bits: a depth may be any int32)
+      me.first_seen = window > 0 ? (int)max((int64_t)-1, min((int64_t)0x7fffffff,
+                                            (int64_t)ctx + me.depth - window + 1))
+                                 : -1;
+      // rounds below `reach` need the window's mask in some row of the warp
+      int reach = valid ? me.first_seen : -1;
+      if (window > 0) reach = __reduce_max_sync(kFull, reach);
+      const float slope2 = kSlopes && valid ? a.slopes[hq] * kLog2e : 0.f;
+      float m_used = -CUDART_INF_F, l = 0.f;   // l: this warp's half of the row sum
+      bool o_has = false;
+      for (int k = 0; k < nr && ok; ++k) {
+        const int r = r0 + k, b = r & 1;
+        const int t0 = tb + k * kRoundTok + 64 * half;   // token of this warp's first column
+        if (!tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t s_col = kColS + kSCols * b + 64 * half;
+        uint32_t sv[2][32];
+        tmem_ld32(tq + s_col, sv[0]);
+        tmem_ld32(tq + s_col + 32, sv[1]);
+        tmem_wait_ld();
+        if constexpr (kCap) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              sv[q][j] = __float_as_uint(capped(__uint_as_float(sv[q][j]), a.scale_log2, a.cap_log2));
+        }
+        if constexpr (kSlopes) {
+          const float d0 = (float)((int64_t)ctx + me.depth - t0);   // distance to the first column's token
+          const float sc = kCap ? 1.f : a.scale_log2;
+          if (me.depths != nullptr && t0 + 64 > ctx) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const int t = t0 + 32 * q + j;
+                const float d = t >= ctx && t < te ? (float)(me.depth - depth_of(me, t - ctx))
+                                                   : d0 - (float)(32 * q + j);
+                sv[q][j] = __float_as_uint(fmaf(-slope2, d, __uint_as_float(sv[q][j]) * sc));
+              }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                sv[q][j] = __float_as_uint(fmaf(-slope2, d0 - (float)(32 * q + j),
+                                                __uint_as_float(sv[q][j]) * sc));
+          }
+        }
+        if (t0 + 64 > ctx || t0 < reach || te - t0 < 64) {
+          const uint64_t vis = valid ? visible(me, t0, te) : 0ull;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t v = (uint32_t)(vis >> (32 * q));
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(v & (1u << j))) sv[q][j] = __float_as_uint(-CUDART_INF_F);
+          }
+        }
+        float mq[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mq[j & 3] = fmaxf(mq[j & 3], __uint_as_float(sv[q][j]));
+        const float m_half = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        float m_other;
+        if (!exchange(s_col, kColS + kSCols * b + 64 * (1 - half), m_half, &m_other)) {
+          ok = false;
+          break;
+        }
+        // both halves of S are read and exchanged: the buffer may be refilled
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->sfree[b]);
+        const float sc2 = kCap || kSlopes ? 1.f : a.scale_log2;   // (positive: the max is the max's)
+        const float mx = fmaxf(m_half, m_other) * sc2;
+        // P buffer b was read by the P.V MMAs of round r - 2
+        if (r >= 2 && !pv_wait(r - 2)) {
+          ok = false;
+          break;
+        }
+        // the base is raised, and O rescaled, only past 2^8 of growth (per row;
+        // the waits and tensor-memory accesses are the whole warp's)
+        const bool need = mx > m_used + kRescaleLog2;
+        if (__any_sync(kFull, need)) {
+          const float alpha = need ? exp2f(m_used - mx) : 1.f;   // 0 while m_used = -inf
+          if (o_has) {
+            if (!pv_wait(r - 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int cb = 0; cb < 64; cb += 32) {
+              uint32_t o[32];
+              tmem_ld32(tq + kColO + 64 * half + cb, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st32(tq + kColO + 64 * half + cb, o);
+            }
+            tmem_wait_st();
+          }
+          l *= alpha;
+          if (need) m_used = mx;
+        }
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        const float neg_m = m_used == -CUDART_INF_F ? 0.f : -m_used;   // nothing seen yet: weights 0
+        uint32_t pw[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const uint32_t* src = sv[j >> 4];
+          const int c = 2 * (j & 15);
+          const float p0 = fast_exp2(fmaf(__uint_as_float(src[c]), sc2, neg_m));
+          const float p1 = fast_exp2(fmaf(__uint_as_float(src[c + 1]), sc2, neg_m));
+          pw[j] = pack_bf16(p0, p1);
+          ps[j & 3] += p0;
+          ps[(j + 2) & 3] += p1;
+        }
+        tmem_st32(tq + kColP + kPCols * b + 32 * half, pw);
+        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->pfull[b]);
+        o_has = true;
+      }
+      if (!ok) break;
+      // ---- epilogue: the item's P.V MMAs done (rounds in order; lag <= 1)
+      const int rl = rho - 1;
+      if (!pv_wait(rl - 1) || !pv_wait(rl)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // the row sum of both halves, exchanged through the last round's P
+      // columns (read by its P.V MMAs already); added in half order
+      const uint32_t p_last = kColP + kPCols * (rl & 1);
+      float l_other;
+      if (!exchange(p_last + 32 * half, p_last + 32 * (1 - half), l, &l_other)) {
+        ok = false;
+        break;
+      }
+      const float lt = half == 0 ? l + l_other : l_other + l;
+      const int64_t q_row = (int64_t)(q_first + i0 + i) * a.hq + hq;
+      const int64_t p_row = ((int64_t)dst + (int64_t)i * stride) * a.hq + hq;   // its partial state
+      const float inv = 1.f / lt;
+      for (int cb = 64 * half; cb < 64 * half + 64; cb += 32) {
+        uint32_t o[32];
+        tmem_ld32(tq + kColO + cb, o);
+        tmem_wait_ld();
+        if (valid) {
+          bool odd = false;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) odd |= (o[j] & 0x7f800000u) == 0x7f800000u;
+          if (odd && lt != 0.f) {
+            uint32_t again[32];   // (only this rare call needs the values in memory)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) again[j] = o[j];
+            redo_row(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used, slope2, again);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = again[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            o[j] = lt == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
+          if (dst < 0) {
+            uint4* op = reinterpret_cast<uint4*>(a.out + q_row * kHeadDim + cb);
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              op[q4] = make_uint4(
+                  pack_bf16(__uint_as_float(o[8 * q4 + 0]), __uint_as_float(o[8 * q4 + 1])),
+                  pack_bf16(__uint_as_float(o[8 * q4 + 2]), __uint_as_float(o[8 * q4 + 3])),
+                  pack_bf16(__uint_as_float(o[8 * q4 + 4]), __uint_as_float(o[8 * q4 + 5])),
+                  pack_bf16(__uint_as_float(o[8 * q4 + 6]), __uint_as_float(o[8 * q4 + 7])));
+          } else {
+            uint4* op = reinterpret_cast<uint4*>(a.o_part + p_row * kHeadDim + cb);
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4)
+              op[q4] = make_uint4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->ofree);
+      if (valid && half == 0) {
+        const float lse = lt == 0.f ? -CUDART_INF_F : (m_used + log2f(lt)) * kLn2;
+        if (dst >= 0)
+          a.l_part[p_row] = lse;
+        else if (a.lse != nullptr)
+          a.lse[q_row] = lse;
+      }
+    }
+  }
+  // all roles done: tensor memory is no longer read or written
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+const void* kernel_of(bool cap, bool slopes) {
+  if (cap)
+    return slopes ? reinterpret_cast<const void*>(&tree_kernel<true, true>)
+                  : reinterpret_cast<const void*>(&tree_kernel<true, false>);
+  return slopes ? reinterpret_cast<const void*>(&tree_kernel<false, true>)
+                : reinterpret_cast<const void*>(&tree_kernel<false, false>);
+}
+
+}  // namespace
+
+int tree_smem_bytes() { return tc::smem_bytes(); }
+
+cudaError_t tree_prepare() {
+  for (int k = 0; k < 4; ++k) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel_of(k & 1, k & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem_bytes());
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t tree_occupancy(int* blocks_per_sm) {
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of(false, false),
+                                                       kTcThreads, (size_t)tree_smem_bytes());
+}
+
+cudaError_t launch_tree(const TreeArgs& a, int grid, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = (size_t)tree_smem_bytes();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {const_cast<TreeArgs*>(&a)};
+  return cudaLaunchKernelExC(&cfg, kernel_of(a.cap_log2 != 0.f, a.slopes != nullptr), args);
+}
+
+}  // namespace pkd

@@ -1,0 +1,236 @@
+"""Accepted drafts moved into place in every layer, and a whole step with drafts."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_decode_host_gb300 as pkd
+
+pytestmark = pytest.mark.gpu
+
+
+def table(lens, page, seed=0, spare=3):
+    counts = [-(-n // page) for n in lens]
+    indptr = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    pool = int(indptr[-1]) + spare
+    where = np.random.default_rng(seed).permutation(pool)[: indptr[-1]].astype(np.int32)
+    last = np.array([n - page * (c - 1) for n, c in zip(lens, counts)], np.int32)
+    return indptr, where, last, pool
+
+
+class Case:
+    def __init__(self, lens=(37, 16, 5), drafted=(9, 16, 5), paths=((1, 4, 7), (0, 1, 2, 3), ()), page=16, hkv=2, D=128,
+                 layout="NHD", kv="bf16", layers=3, width=None, seed=0):
+        self.__dict__.update(lens=lens, drafted=drafted, paths=paths, page=page, layout=layout)
+        self.indptr, self.indices, self.last, self.pool = table(lens, page, seed)
+        g = torch.Generator("cuda").manual_seed(seed)
+        shape = (self.pool, 2, page, hkv, D) if layout == "NHD" else (self.pool, 2, hkv, page, D)
+        dt = torch.float8_e4m3fn if kv == "e4m3" else torch.bfloat16
+        self.kvs = [torch.randn(shape, generator=g, device="cuda").to(dt) for _ in range(layers)]
+        width = max([len(p) for p in paths] + [1]) if width is None else width
+        self.accepted = torch.tensor([list(p) + [-1] * (width - len(p)) for p in paths], dtype=torch.int32, device="cuda")
+        self.d_drafted = torch.tensor(drafted, dtype=torch.int32, device="cuda")
+        self.tables = [torch.from_numpy(x).cuda() for x in (self.indptr, self.indices, self.last)]
+
+    def run(self, **kw):
+        return pkd.accept_kv(self.kvs, self.accepted, self.d_drafted, *self.tables, kv_layout=self.layout, **kw)
+
+    def expected(self, skip=()):
+        got = []
+        for kv in self.kvs:
+            new = kv.view(torch.uint8).cpu().clone()
+            rows = new if self.layout == "NHD" else new.transpose(2, 3)
+            old = rows.clone()
+            for b, path in enumerate(self.paths):
+                at = lambda t: (int(self.indices[self.indptr[b] + t // self.page]), t % self.page)
+                ctx = self.lens[b] - self.drafted[b]
+                for i, a in enumerate(path if b not in skip else ()):
+                    (pt, st), (pf, sf) = at(ctx + i), at(ctx + a)
+                    rows[pt, :, st] = old[pf, :, sf]
+            got.append(new)
+        return got
+
+    def check(self, skip=()):
+        want = self.expected(skip)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        assert self.run(err=err) is self.kvs
+        assert err.item() == (2 if skip else 0)
+        for kv, w in zip(self.kvs, want):
+            assert torch.equal(kv.view(torch.uint8).cpu(), w)
+
+
+@pytest.mark.parametrize("layout", ["NHD", "HND"])
+@pytest.mark.parametrize("page,kv,hkv,D", [(16, "bf16", 2, 128), (1, "bf16", 8, 128), (5, "e4m3", 3, 128),
+                                           (64, "e4m3", 1, 16), (7, "bf16", 8, 256), (16, "bf16", 1, 8)])
+def test_caches(layout, page, kv, hkv, D):
+    Case(page=page, kv=kv, hkv=hkv, D=D, layout=layout).check()
+
+
+@pytest.mark.parametrize("layers", [1, 2, 128])
+def test_layers(layers):
+    Case(layers=layers, hkv=1).check()
+
+
+@pytest.mark.parametrize("n,path", [(1, (0,)), (1, ()), (40, tuple(range(40))), (40, tuple(range(1, 40))),
+                                    (40, (39,)), (300, tuple(range(0, 300, 2))), (300, tuple(range(3, 300))),
+                                    (1024, tuple(range(1024)))])
+def test_paths(n, path):
+    Case(lens=(n + 21,), drafted=(n,), paths=(path,)).check()
+    Case(lens=(n,), drafted=(n,), paths=(path,), width=1024).check()
+
+
+def test_rows_that_are_wrong_are_left_as_they_are():
+    paths = ((1, 4, 7), (0, 2, 2), (3, 2), (0, 9), (2, 5), (1, 0, 3, 2, 5, 4, 7, 6), (1, 2))
+    c = Case(lens=(37, 30, 20, 33, 40, 8, 12), drafted=(9, 9, 9, 9, 9, 9, 3), paths=paths)
+    c.drafted = (9, 9, 9, 9, 9, 8, 3)
+    c.d_drafted[5] = 2       # more accepted than drafted, not increasing
+    c.check(skip=(1, 2, 3, 5))
+    d = Case(lens=(37, 30, 20), drafted=(9, 9, 9), paths=((1, 4), (1, 4), (1, 4)))
+    d.d_drafted[0], d.d_drafted[1] = 38, -1
+    d.check(skip=(0, 1))
+    e = Case(lens=(37, 30), drafted=(9, 9), paths=((1, 4), (1, 4)))
+    e.tables[1][int(e.indptr[2]) - 1] = e.pool     # the page that request 1's drafts lie in
+    e.check(skip=(1,))
+    f = Case(lens=(37, 30), drafted=(9, 9), paths=((1, 4), (1, 4)))
+    f.tables[1] = f.tables[1][:-1]
+    f.check(skip=(1,))
+    g = Case(lens=(37, 30), drafted=(9, 9), paths=((1, 4), (1, 4)))
+    g.tables[2][0] = 17
+    g.check(skip=(0,))
+
+
+def test_entries_behind_the_first_negative_one_do_not_count():
+    c = Case(lens=(37,), drafted=(9,), paths=((1, 4, -1, 6, 100),))
+    c.paths = ((1, 4),)
+    c.check()
+
+
+def test_streams_and_graphs():
+    c, d = Case(), Case()
+    c.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    d.run(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(x, y) for x, y in zip(c.kvs, d.kvs))
+    e = Case()
+    keep = [kv.clone() for kv in e.kvs]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        e.run()
+    for kv, k in zip(e.kvs, keep):
+        kv.copy_(k)
+    graph.replay()
+    assert all(torch.equal(x, y) for x, y in zip(c.kvs, e.kvs))
+
+
+def test_refusals():
+    c = Case()
+    for kw in (dict(kvs=[]), dict(kvs=c.kvs * 50), dict(kvs=[c.kvs[0], c.kvs[0]]), dict(kvs=[c.kvs[0], c.kvs[1][:-1]]),
+               dict(kvs=[c.kvs[0].float()]), dict(accepted=c.accepted.long()), dict(accepted=c.accepted[:2]),
+               dict(accepted=torch.zeros(3, 1025, dtype=torch.int32, device="cuda")), dict(d_drafted=c.d_drafted[:2]),
+               dict(layout="x")):
+        d = Case()
+        d.__dict__.update(kw)
+        with pytest.raises((ValueError, TypeError, pkd.PkdError)):
+            d.run()
+
+
+def attention(q, k, v, scale):
+    """[H, D] over [t, Hkv, D], in 64 bits."""
+    hkv = k.shape[1]
+    x = torch.einsum("hgd,thd->hgt", q.view(hkv, -1, q.shape[-1]), k) * scale
+    return torch.einsum("hgt,thd->hgd", torch.softmax(x, -1), v).reshape(q.shape)
+
+
+def test_three_steps_with_drafts():
+    """Rotate and append trees of drafts, attend, accept a path, and go on: every step's results and
+    the cache are those of the accepted tokens alone."""
+    hq, hkv, D, page, batch, layers = 8, 2, 128, 16, 3, 2
+    g = torch.Generator("cuda").manual_seed(7)
+    r = np.random.default_rng(7)
+    rope = pkd.RotaryPositions([10_000.0 ** (-i / 64) for i in range(64)])
+    freq = torch.tensor([10_000.0 ** (-i / 64) for i in range(64)], dtype=torch.float64, device="cuda")
+    pool, pages = 60, 20
+    ids = [list(map(int, x)) for x in r.permutation(pool).reshape(batch, pages)]
+    kvs = [torch.full((pool, 2, page, hkv, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(layers)]
+    dec = pkd.BatchTreeDecodeWithPagedKVCache(hq, hkv, D, page, max_tokens=200, max_num_pages=batch * pages, num_pages=pool)
+    kept = [[[] for _ in range(batch)] for _ in range(layers)]   # accepted tokens' (k, v), rotated, in 64 bits
+    w = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).bfloat16()
+
+    def turn(x, at):
+        x = x.double() / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6) * w.double()
+        a = at.double()[:, None, None] * freq
+        lo, hi = x[..., :64], x[..., 64:]
+        return torch.cat([lo * torch.cos(a) - hi * torch.sin(a), hi * torch.cos(a) + lo * torch.sin(a)], -1)
+
+    for step, drafts in enumerate(((40, 17, 1), (9, 12, 6), (1, 30, 8))):
+        ctx = [len(kept[0][b]) for b in range(batch)]
+        lens = [a + n for a, n in zip(ctx, drafts)]
+        counts = [-(-n // page) for n in lens]
+        indptr = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        indices = np.concatenate([ids[b][:counts[b]] for b in range(batch)]).astype(np.int32)
+        last = np.array([n - page * (c - 1) for n, c in zip(lens, counts)], np.int32)
+        tables = [torch.from_numpy(x).cuda() for x in (indptr, indices, last)]
+        q_indptr = np.concatenate([[0], np.cumsum(drafts)]).astype(np.int32)
+        parents = np.concatenate([[j - 1 if step == 0 else int(r.integers(-1, j)) for j in range(n)]
+                                  for n in drafts]).astype(np.int32)   # first the prompts: chains
+        mask, depths = pkd.tree_mask(q_indptr, parents)
+        n = int(q_indptr[-1])
+        rows = torch.from_numpy(np.repeat(np.arange(batch), drafts)).int().cuda()
+        places = torch.from_numpy(np.concatenate([np.arange(a, b) for a, b in zip(ctx, lens)])).int().cuda()
+        at = torch.from_numpy(np.repeat(ctx, drafts) + depths).int().cuda()
+        d_mask, d_depths = torch.from_numpy(mask).cuda(), torch.from_numpy(depths).cuda()
+        dec.plan(q_indptr, indptr, indices, last)
+        turned = []
+        for l in range(layers):
+            both = torch.randn(n, hq + 2 * hkv, D, generator=g, device="cuda").bfloat16()
+            q, k, v = both[:, :hq], both[:, hq:hq + hkv], both[:, hq + hkv:]
+            q_out, _ = pkd.rotate_append_kv(q, k, v, rope, rows, places, *tables, kvs[l], rope_positions=at,
+                                            q_norm=w, k_norm=w)
+            out, _ = dec.run(q_out, kvs[l], mask=d_mask, depths=d_depths)
+            eq, ek, ev = turn(q, at), turn(k, at), v.double()
+            turned.append((ek, ev))
+            for b in range(batch):
+                for i in range(drafts[b]):
+                    row = int(q_indptr[b]) + i
+                    own, j = [], i
+                    while j >= 0:
+                        own.append(j)
+                        j = int(parents[q_indptr[b] + j])
+                    own = [int(q_indptr[b]) + j for j in sorted(own)]
+                    ks = torch.stack([x for x, _ in kept[l][b]] + [ek[j] for j in own])
+                    vs = torch.stack([x for _, x in kept[l][b]] + [ev[j] for j in own])
+                    ref = attention(eq[row], ks, vs, D ** -0.5)
+                    # q and k rounded to bf16 (2^-8 each): a score moves by at most 2 * 2^-8 * 128 * 2^0
+                    # of |q||k| scale in the worst case; of random signs, a few per cent of a weight
+                    assert (out[row].double() - ref).abs().max() <= 0.06
+        paths = []
+        for b in range(batch):
+            i = int(r.integers(0, drafts[b])) if step else drafts[b] - 1
+            path = []
+            while i >= 0:
+                path.append(i)
+                i = int(parents[q_indptr[b] + i])
+            paths.append(sorted(path))
+        wide = max(map(len, paths))
+        accepted = torch.tensor([p + [-1] * (wide - len(p)) for p in paths], dtype=torch.int32, device="cuda")
+        drafted = torch.tensor(drafts, dtype=torch.int32, device="cuda")
+        pkd.accept_kv(kvs, accepted, drafted, *tables)
+        for l in range(layers):
+            for b, path in enumerate(paths):
+                kept[l][b] += [(turned[l][0][int(q_indptr[b]) + i], turned[l][1][int(q_indptr[b]) + i]) for i in path]
+        table2 = pkd.accepted_table(indptr, indices, last, page, np.array(drafts, np.int32),
+                                    np.array([len(p) for p in paths], np.int32))
+        for b in range(batch):
+            mine = table2[1][table2[0][b]:table2[0][b + 1]]
+            length = page * (len(mine) - 1) + int(table2[2][b])
+            assert length == len(kept[0][b]) and list(mine) == ids[b][:len(mine)]
+            for l in range(layers):
+                got = kvs[l][torch.from_numpy(mine).long().cuda()].double().transpose(0, 1).reshape(2, -1, hkv, D)[:, :length]
+                ks, vs = torch.stack([x for x, _ in kept[l][b]]), torch.stack([x for _, x in kept[l][b]])
+                assert torch.equal(got[1], vs)
+                assert ((got[0] - ks).abs() <= 2.0 ** -8 * ks.abs() + 2.0 ** -18 * 8).all()
+        assert dec.device_error() == 0

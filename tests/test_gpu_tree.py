@@ -1,0 +1,371 @@
+"""Attention of drafted tokens over a paged cache, against the formula in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_decode_host_gb300 as pkd
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+def table(lens, page, seed=0, spare=3):
+    counts = [-(-n // page) for n in lens]
+    indptr = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    pool = int(indptr[-1]) + spare
+    where = np.random.default_rng(seed).permutation(pool)[: indptr[-1]].astype(np.int32)
+    last = np.array([n - page * (c - 1) for n, c in zip(lens, counts)], np.int32)
+    return indptr, where, last, pool
+
+
+def trees(drafts, seed):
+    """Random parents of every request's drafts."""
+    r = np.random.default_rng(seed)
+    return np.concatenate([[int(r.integers(max(-1, j // 3 - 2), j)) for j in range(n)] for n in drafts]
+                          + [[]]).astype(np.int32)
+
+
+class Case:
+    def __init__(self, hq=8, hkv=2, page=16, layout="NHD", lens=(37, 16, 5), drafts=(4, 3, 5), causal=False,
+                 window=0, cap=0.0, slopes=False, seed=0, rows=None, depths=True, magnitude=1.0, **kw):
+        self.__dict__.update(hq=hq, hkv=hkv, page=page, layout=layout, lens=lens, drafts=drafts, causal=causal,
+                             window=window, cap=cap)
+        self.indptr, self.indices, self.last, self.pool = table(lens, page, seed)
+        self.q_indptr = np.concatenate([[0], np.cumsum(drafts)]).astype(np.int32)
+        self.tokens = int(self.q_indptr[-1])
+        g = torch.Generator("cuda").manual_seed(seed)
+        shape = (self.pool, 2, page, hkv, D) if layout == "NHD" else (self.pool, 2, hkv, page, D)
+        self.kv = torch.randn(shape, generator=g, device="cuda").bfloat16()
+        self.q = (magnitude * torch.randn(self.tokens if rows is None else rows, hq, D, generator=g,
+                                          device="cuda")).bfloat16()
+        self.mask = self.depths = self.slopes = None
+        if not causal:
+            mask, depth = pkd.tree_mask(self.q_indptr, trees(drafts, seed))
+            pad = len(self.q) - self.tokens
+            self.mask = torch.from_numpy(np.concatenate([mask, np.zeros((pad, mask.shape[1]), np.int32)])).cuda()
+            if depths:
+                self.depths = torch.from_numpy(np.concatenate([depth, np.zeros(pad, np.int32)])).cuda()
+        if slopes:
+            self.slopes = torch.tensor([2.0 ** (-8.0 * (i + 1) / hq) for i in range(hq)], device="cuda")
+        self.dec = pkd.BatchTreeDecodeWithPagedKVCache(
+            hq, hkv, D, page, max_tokens=max(1, self.tokens, len(lens)), max_num_pages=len(self.indices),
+            num_pages=self.pool, kv_layout=layout, **kw)
+        self.plan()
+
+    def plan(self, **kw):
+        return self.dec.plan(self.q_indptr, self.indptr, self.indices, self.last, causal=self.causal,
+                             window=self.window, **kw)
+
+    def run(self, **kw):
+        return self.dec.run(self.q, self.kv, mask=self.mask, depths=self.depths, score_cap=self.cap,
+                            slopes=self.slopes, **kw)
+
+    def sees(self, b):
+        """[n, l] which tokens every query token of request b sees, and how far away they are."""
+        n, length, first = self.drafts[b], self.lens[b], int(self.q_indptr[b])
+        ctx = length - n
+        depth = np.arange(n) if self.depths is None else self.depths[first:first + n].cpu().numpy().astype(np.int64)
+        depth = np.maximum(depth, 0)
+        at = np.concatenate([np.arange(ctx), ctx + depth])
+        away = (ctx + depth)[:, None] - at[None, :]
+        see = np.ones((n, length), bool)
+        if self.causal:
+            see[:, ctx:] = np.tril(np.ones((n, n), bool))
+        else:
+            words = self.mask[first:first + n].cpu().numpy().view(np.uint32)
+            for j in range(n):
+                see[:, ctx + j] = (words[:, j // 32] >> np.uint32(j % 32)) & 1
+        if self.window:
+            see &= away < self.window
+        return torch.from_numpy(see).cuda(), torch.from_numpy(away).cuda()
+
+    def reference(self):
+        outs, lses = [], []
+        for b, (n, length) in enumerate(zip(self.drafts, self.lens)):
+            if n == 0:
+                continue
+            mine = torch.from_numpy(self.indices[self.indptr[b]:self.indptr[b + 1]]).long().cuda()
+            kv = self.kv[mine].double()
+            kv = kv if self.layout == "NHD" else kv.transpose(2, 3)
+            k, v = (kv[:, c].reshape(-1, self.hkv, D)[:length] for c in (0, 1))
+            first = int(self.q_indptr[b])
+            q = self.q[first:first + n].double().view(n, self.hkv, -1, D)
+            x = torch.einsum("nhgd,thd->hgnt", q, k) / math.sqrt(D)
+            see, away = self.sees(b)
+            if self.cap:
+                x = self.cap * torch.tanh(x / self.cap)
+            if self.slopes is not None:
+                x = x - self.slopes.double().view(self.hkv, -1, 1, 1) * away
+            x = torch.where(see, x, -math.inf)
+            lse = torch.logsumexp(x, -1)
+            p = torch.where(see, torch.exp(x - torch.where(lse == -math.inf, 0.0, lse)[..., None]), 0.0)
+            # what is not seen does not matter, whatever it holds
+            out = torch.zeros(self.hkv, self.hq // self.hkv, n, D, dtype=torch.float64, device="cuda")
+            for i in range(n):
+                t = see[i].nonzero()[:, 0]
+                out[:, :, i] = torch.einsum("hgt,thd->hgd", p[:, :, i, t], v[t])
+            outs.append(out.permute(2, 0, 1, 3).reshape(n, -1, D))
+            lses.append(lse.permute(2, 0, 1).reshape(n, -1))
+        return torch.cat(outs), torch.cat(lses)
+
+    def check(self, got=None):
+        out, lse = self.run() if got is None else got
+        ro, rl = self.reference()
+        out, lse = out[:self.tokens], lse[:self.tokens]
+        assert self.dec.device_error() == 0
+        fine = torch.isfinite(rl)
+        assert torch.equal(torch.isfinite(lse), fine) and (lse[~fine] == -math.inf).all()
+        assert (out[~fine] == 0).all()
+        # P is rounded to bf16 (half a step: 2^-8 of itself) and the row's sum is not: that moves a
+        # weighted mean of values of magnitude at most top by at most 2^-8 top, its own rounding by
+        # 2^-8 |out|; scores in fp32 (below) move the weights by under 2^-12 of themselves
+        top = float(self.kv.float()[torch.isfinite(self.kv.float())].abs().max())
+        assert (out.double() - ro).abs().max() <= 1.1 * 2 ** -8 * (top + float(ro.abs().max()))
+        # lse: a score is an fp32 sum of 128 products, random errors of 2^-24 of its terms' partial
+        # sums (under 2^-24 * 128 * 6 * scale of the queries' magnitude, < 1e-4); the cap's tanh is
+        # off by under 2^-21 of the cap, a bias by 2^-24 of itself; sums of n weights by under 2^-24 n
+        tol = 2e-4 + self.cap * 2 ** -20 + 2 ** -21 * float(rl[fine].abs().max() if fine.any() else 0)
+        assert fine.sum() == 0 or (lse[fine].double() - rl[fine]).abs().max() <= tol
+
+
+GROUPS = [(1, 1), (2, 1), (8, 1), (3, 3), (12, 3), (8, 2), (8, 8), (32, 8), (64, 8)]
+
+
+@pytest.mark.parametrize("hq,hkv", GROUPS)
+@pytest.mark.parametrize("layout,page", [("NHD", 16), ("HND", 48)])
+def test_heads_and_layouts(hq, hkv, layout, page):
+    Case(hq=hq, hkv=hkv, layout=layout, page=page, lens=(37, 16, 5, 300), drafts=(4, 3, 5, 9), seed=hq).check()
+
+
+@pytest.mark.parametrize("lens,drafts", [
+    ((1,), (1,)), ((2,), (2,)), ((16,), (16,)), ((17,), (1,)), ((127,), (3,)), ((128,), (3,)), ((129,), (3,)),
+    ((130,), (130,)), ((191, 192, 193), (64, 64, 65)), ((255, 256, 257), (1, 1, 1)), ((640,), (33,)),
+    ((40, 7, 90), (0, 7, 3)), ((40, 7), (0, 0)), ((500, 3), (70, 3)), ((64, 64, 64), (63, 1, 64))])
+@pytest.mark.parametrize("causal", [False, True])
+def test_lengths(lens, drafts, causal):
+    c = Case(hq=8, hkv=2, lens=lens, drafts=drafts, causal=causal, seed=len(lens))
+    if c.tokens:
+        c.check()
+    else:
+        out, lse = c.run()
+        assert out.numel() == 0 and c.dec.device_error() == 0
+
+
+@pytest.mark.parametrize("kw", [dict(cap=30.0), dict(cap=2.0, magnitude=4.0), dict(slopes=True), dict(window=1),
+                                dict(window=50), dict(window=200), dict(window=3, depths=False), dict(window=10**9),
+                                dict(cap=50.0, window=130, slopes=True), dict(slopes=True, depths=False),
+                                dict(magnitude=8.0)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_score_shapes(kw, causal):
+    if causal and "depths" in kw:
+        kw = {k: v for k, v in kw.items() if k != "depths"}
+    Case(hq=8, hkv=2, lens=(37, 400, 5, 260), drafts=(4, 40, 5, 1), causal=causal, seed=3, **kw).check()
+
+
+@pytest.mark.parametrize("lens,drafts,causal", [((3000, 40, 1500), (12, 3, 40), False), ((5000,), (1,), False),
+                                                ((20_000, 30), (8, 8), False), ((2500, 600), (200, 70), True)])
+@pytest.mark.parametrize("kw", [dict(), dict(cap=20.0, window=1300), dict(slopes=True)])
+def test_split_requests(lens, drafts, causal, kw):
+    c = Case(hq=16, hkv=4, lens=lens, drafts=drafts, causal=causal, seed=5, min_chunk_tokens=128, alpha=0, **kw)
+    assert c.dec.plan_info()["num_units"] > 0
+    c.check()
+    few = Case(hq=16, hkv=4, lens=lens, drafts=drafts, causal=causal, seed=5, num_ctas=3, **kw)   # fewer CTAs than heads
+    few.check()
+
+
+def test_long_requests_with_many_parts():
+    c = Case(hq=2, hkv=1, lens=(30_000, 77), drafts=(5, 2), min_chunk_tokens=128, alpha=0, page=64)
+    assert c.dec.plan_info()["num_slots"] > 5 * 64   # past the merge's long units
+    c.check()
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_rows_that_see_nothing(split):
+    kw = dict(min_chunk_tokens=128, alpha=0) if split else dict(num_ctas=2)
+    c = Case(hq=4, hkv=1, lens=(300, 9), drafts=(300, 9), **kw)
+    assert (c.dec.plan_info()["num_units"] > 0) == split
+    c.mask[1] = 0
+    c.mask[303] = 0
+    c.mask[7:11] = 0
+    c.check()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("split", [False, True])
+def test_what_is_masked_may_hold_anything(bad, split):
+    kw = dict(min_chunk_tokens=128, alpha=0) if split else dict(num_ctas=2)
+    c = Case(hq=8, hkv=2, lens=(400, 21), drafts=(150, 5), window=0, seed=9, **kw)
+    used = set(c.indices.tolist())
+    for page in range(c.pool):
+        if page not in used:
+            c.kv[page] = bad                              # pages of no request
+    c.kv[int(c.indices[c.indptr[2] - 1]), :, c.last[1]:] = bad   # behind a request's end
+    for draft in (3, 60, 149):                             # drafts that few rows see
+        c.mask[:150, draft // 32] &= ~(1 << (draft % 32)) if draft % 32 != 31 else 0x7fffffff
+        page, slot = divmod(250 + draft, 16)
+        c.kv[int(c.indices[page]), :, slot] = bad
+    c.check()
+
+
+def test_values_that_are_seen_keep_what_they_hold():
+    c = Case(hq=4, hkv=1, lens=(300,), drafts=(40,), seed=2)
+    c.mask[:, :] = 0
+    c.mask[5, 0] = 1 << 7
+    page, slot = divmod(260 + 7, 16)
+    c.kv[int(c.indices[page]), 1, slot, 0, 33] = float("nan")
+    c.kv[int(c.indices[page]), 1, slot, 0, 70] = float("inf")
+    out, lse = c.run()
+    assert torch.isnan(out[5, :, 33]).all() and (out[5, :, 70] == float("inf")).all()
+    rest = torch.ones_like(out, dtype=torch.bool)
+    rest[5, :, 33] = rest[5, :, 70] = False
+    assert torch.isfinite(out[rest]).all() and torch.isfinite(lse).all()
+    c.kv[int(c.indices[page]), 1, slot, 0, 33] = c.kv[int(c.indices[page]), 1, slot, 0, 70] = 0.0
+    c.mask[5, 0] = 0   # (its other dims: as in the call where it sees the draft, within the bound)
+    ref = c.reference()[0]
+    keep = torch.ones(40, dtype=torch.bool)
+    keep[5] = False
+    good = out[keep].double()
+    top = float(c.kv.float().abs().max())
+    good[~torch.isfinite(good)] = 0
+    assert (good - ref[keep]).abs().max() <= 1.1 * 2 ** -8 * (top + float(ref.abs().max()))
+
+
+def test_scores_that_rise_along_the_cache():
+    """The base of the exponentials is raised in every round; the early tokens' weights vanish."""
+    c = Case(hq=8, hkv=2, lens=(1500,), drafts=(6,), seed=4, num_ctas=2)
+    c.q[:] = 1.0
+    for t in range(1500):
+        page, slot = divmod(t, 16)
+        c.kv[int(c.indices[page]), 0, slot] = 0.02 * t
+    c.check()
+    c.kv[:, 0] = -c.kv[:, 0]
+    c.check()
+
+
+def test_rows_behind_the_last_query_are_left_alone():
+    c = Case(lens=(300, 50), drafts=(7, 2), rows=20)
+    out = torch.full((20, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((20, 8), 7.0, device="cuda")
+    c.check(c.run(out=out, lse=lse))
+    assert (out[9:] == 7).all() and (lse[9:] == 7).all()
+    assert c.run(return_lse=False).shape == out.shape
+
+
+def test_same_bits_every_run_and_on_other_streams():
+    c = Case(hq=16, hkv=4, lens=(4000, 700), drafts=(20, 9), min_chunk_tokens=128, alpha=0)
+    out, lse = c.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        o, l = c.run(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_plan_on_another_stream_with_its_epoch():
+    c = Case(hq=16, hkv=4, lens=(4000, 700), drafts=(20, 9), min_chunk_tokens=128, alpha=0)
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        epoch = c.plan(stream=side)
+        c.check(c.run(expect_epoch=epoch))
+    with pytest.raises(pkd.PkdError, match="STALE"):
+        c.run(expect_epoch=epoch - 1)
+
+
+def test_captured_step_under_later_plans():
+    c = Case(hq=8, hkv=2, lens=(700, 90, 40), drafts=(12, 9, 4), min_chunk_tokens=128, alpha=0)
+    out = torch.zeros(25, 8, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(25, 8, device="cuda")
+    c.run(out=out, lse=lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(out=out, lse=lse)
+    out.zero_(), lse.zero_()
+    graph.replay()
+    c.check((out, lse))
+    # fewer tokens, other lengths, no split
+    full = c.lens, c.drafts, c.q_indptr, c.indptr, c.indices, c.last, c.tokens
+    c.lens, c.drafts = (100, 5), (3, 5)
+    c.indptr, c.indices, c.last = np.array([0, 7, 8], np.int32), c.indices[10:18].copy(), np.array([4, 5], np.int32)
+    c.q_indptr, c.tokens = np.array([0, 3, 8], np.int32), 8
+    mask, depth = pkd.tree_mask(c.q_indptr, trees(c.drafts, 1))
+    c.mask[:8], c.depths[:8] = torch.from_numpy(mask).cuda(), torch.from_numpy(depth).cuda()
+    c.plan()
+    out.fill_(3.0)
+    graph.replay()
+    c.check((out, lse))
+    assert (out[8:] == 3).all()
+    # more tokens than the captured call has rows: no work, and the error word says so
+    c.lens, c.drafts, c.q_indptr, c.indptr, c.indices, c.last, c.tokens = full
+    q, o = c.q[:6].clone(), torch.zeros(6, 8, D, dtype=torch.bfloat16, device="cuda")
+    c.dec.plan(np.array([0, 3, 6], np.int32), np.array([0, 3, 6], np.int32), c.indices[:6].copy(),
+               np.array([8, 8], np.int32))
+    graph2 = torch.cuda.CUDAGraph()
+    mask6 = c.mask[:6].clone()
+    c.dec.run(q, c.kv, mask=mask6, out=o)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph2):
+        c.dec.run(q, c.kv, mask=mask6, out=o)
+    c.plan()
+    o.fill_(5.0)
+    graph2.replay()
+    torch.cuda.synchronize()
+    assert (o == 5).all() and c.dec.device_error() == 2
+
+
+def test_pools_past_32_bits():
+    """Pages whose elements lie past 2^31."""
+    c = Case(hq=8, hkv=8, lens=(70, 40), drafts=(5, 3), window=60)
+    far = 70_000
+    kv = torch.zeros(far + c.pool, 2, 16, 8, D, dtype=torch.bfloat16, device="cuda")
+    kv[far:] = c.kv
+    dec = pkd.BatchTreeDecodeWithPagedKVCache(8, 8, D, 16, max_tokens=8, max_num_pages=len(c.indices),
+                                              num_pages=far + c.pool)
+    dec.plan(c.q_indptr, c.indptr, c.indices + far, c.last, window=60)
+    c.check(dec.run(c.q, kv, mask=c.mask, depths=c.depths))
+    assert dec.device_error() == 0
+
+
+def test_depths_of_any_size():
+    c = Case(lens=(300,), drafts=(6,), slopes=True, window=400, seed=6)
+    c.depths[:] = torch.tensor([0, 90, -5, 150, 2000, 10], dtype=torch.int32)
+    c.check()
+    c = Case(lens=(300,), drafts=(3,), window=7, seed=6)
+    c.depths[:] = torch.tensor([2 ** 31 - 1, 0, 3], dtype=torch.int32)
+    c.check()
+
+
+def test_refusals():
+    c = Case()
+    q, kv, mask = c.q, c.kv, c.mask
+    for kw in (dict(mask=None), dict(mask=mask[:-1]), dict(mask=mask.float()), dict(mask=mask, depths=c.depths.long()),
+               dict(mask=mask, slopes=torch.zeros(3, device="cuda")), dict(mask=mask, lse=torch.zeros(3, device="cuda")),
+               dict(mask=mask[:, :0])):
+        with pytest.raises((ValueError, pkd.PkdError)):
+            c.dec.run(q, kv, **kw)
+    for kw in (dict(scale=0.0), dict(scale=float("nan")), dict(score_cap=-1.0), dict(score_cap=float("inf"))):
+        with pytest.raises(pkd.PkdError, match="INVALID"):
+            c.dec.run(q, kv, mask=mask, **kw)
+    for args in ((q[:-1], kv), (q.float(), kv), (q, kv[:-1]), (q.transpose(0, 1), kv), (q.cpu(), kv)):
+        with pytest.raises((ValueError, pkd.PkdError)):
+            c.dec.run(*args, mask=mask)
+    c.dec.plan(c.q_indptr, c.indptr, c.indices, c.last, causal=True)
+    for kw in (dict(mask=mask), dict(depths=c.depths)):
+        with pytest.raises(ValueError):
+            c.dec.run(q, kv, **kw)
+    for call in (c.dec.plan_shared, c.dec.plan_cascade, c.dec.accumulate_weights, c.dec.capture):
+        with pytest.raises(pkd.PkdError):
+            call()
+    fresh = pkd.BatchTreeDecodeWithPagedKVCache(8, 2, D, 16, max_tokens=4, max_num_pages=4, num_pages=4)
+    with pytest.raises(pkd.PkdError, match="NO_PLAN"):
+        fresh.run(q, kv)
+    with pytest.raises(pkd.PkdError):
+        pkd.BatchTreeDecodeWithPagedKVCache(8, 2, 64, 16, max_tokens=4, max_num_pages=4, num_pages=4)
+    with pytest.raises(pkd.PkdError):
+        pkd.BatchTreeDecodeWithPagedKVCache(8, 2, D, 8, max_tokens=4, max_num_pages=4, num_pages=4)
+    with pytest.raises(ValueError):
+        pkd.BatchTreeDecodeWithPagedKVCache(8, 2, D, 16, max_tokens=4, max_num_pages=4, num_pages=4, kv_layout="x")
+    assert c.dec.device_error() == 0
