@@ -4,10 +4,13 @@ Each translation unit compiles in its own nvcc process (in parallel); the
 objects are linked into ``paged_kv_decode_host_gb300/libpkd.so``.  No CMake.
 Beside it, when the Python headers are installed, the host C compiler builds
 ``_pkd_plan``: the binding's argument-marshalling fast path for the per-step
-plan calls (the binding falls back to ctypes without it).
+plan calls (the binding falls back to ctypes without it), and the host C++
+compiler ``_pkd_step``, which takes the calls of a step with drafts on torch's
+tensors directly (likewise).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -27,6 +30,9 @@ SOURCES = ["planner.cpp", "api.cu", "decode_kernel.cu", "prefix_tc_kernel.cu",
            "tree_kernel.cu", "rotate_kernel.cu", "accept_kernel.cu", "api_step.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 PYPLAN = os.path.join(HERE, "_pkd_plan" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+PYSTEP = os.path.join(HERE, "_pkd_step" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 
 def _python_include():
@@ -50,6 +56,32 @@ def _build_fast_plan():
     return PYPLAN
 
 
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    d = spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+    return d if d and os.path.exists(os.path.join(d, "include", "ATen")) else None
+
+
+def _build_step():
+    """The binding on torch's tensors; None without Python headers, torch or a C++ compiler."""
+    inc, torch_dir = _python_include(), _torch_dir()
+    cxx = shutil.which("c++") or shutil.which("g++")
+    if inc is None or torch_dir is None or cxx is None:
+        return None
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    dirs = [INCLUDE, inc, os.path.join(torch_dir, "include"), cuda]
+    tmp = PYSTEP + f".tmp{os.getpid()}"
+    r = subprocess.run([cxx, "-O2", "-std=c++17", "-shared", "-fPIC", *[f"-I{d}" for d in dirs],
+                        os.path.join(CSRC, "pystep.cpp"), "-o", tmp,
+                        "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-ltorch_cpu",
+                        "-ltorch_python", "-lc10_cuda"], capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(f"_pkd_step not built (general path used):\n{r.stderr[-2000:]}\n")
+        return None
+    os.replace(tmp, PYSTEP)
+    return PYSTEP
+
+
 def _nvcc() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -66,6 +98,8 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     if _python_include() is not None and not os.path.exists(PYPLAN):
+        return True
+    if _python_include() is not None and _torch_dir() is not None and not os.path.exists(PYSTEP):
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "pkd.h")]
@@ -89,10 +123,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        fast = ex.submit(_build_fast_plan)
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 2) as ex:
+        fast, step = ex.submit(_build_fast_plan), ex.submit(_build_step)
         objs = list(ex.map(compile_one, SOURCES))
-        fast.result()
+        fast.result(), step.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, "-shared", "-o", tmp, *objs, *ARCH, "-Xcompiler", "-fPIC", "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)

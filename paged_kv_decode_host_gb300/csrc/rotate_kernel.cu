@@ -16,14 +16,17 @@
 // error under 2^-20: a result is then rounded to 2^-9 of itself or coarser.
 //
 // The work is moving bytes (24 KB a token of 32 + 2 x 8 heads).  A head is D /
-// 8 lanes of 16 bytes, so a warp holds 256 / D heads at a time and walks the
-// heads of one token; its lanes' sines and cosines stay in registers for all of
-// them.  Partners of the half-split form are R / 16 lanes away.  Few tokens are
-// spread over more warps, down to one group of heads each (a lane's 8 sincos
-// pairs are then computed once per group): measured at the entry of the launch.
-// The table is looked up by every warp that writes a key or a value, behind the
-// loads of its first heads.  A token without a slot is flagged and its key and
-// value skipped; its query is rotated all the same.
+// 16 lanes, each with the two 16-byte pieces that turn together (the half-split
+// form needs no exchange between lanes then), so a warp holds 512 / D heads at a
+// time and a block's warps share the heads of one token.  The block looks the
+// token's slot up and computes its sines and cosines once, into shared memory,
+// behind the loads of its first heads; they, and the norms' weights, are read
+// from there for every head, so that registers leave room for 32 warps an SM.
+// 16,088 tokens of 32 + 2 x 8 heads: 64.8 us, 6.1 TB/s; one piece a lane with
+// shuffles between partners took 78.8 (bound by instructions), sines in
+// registers 72 (too few warps).
+// A token without a slot is flagged and its key and value skipped; its query is
+// rotated all the same.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -36,8 +39,8 @@ namespace {
 
 using namespace dev;
 
-constexpr int kWarps = 4;     // per block
-constexpr int kAhead = 4;     // groups of heads whose loads are in flight per warp
+constexpr int kMostWarps = 4;   // per block
+constexpr int kAhead = 2;       // groups of heads whose loads a warp has in flight
 
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -69,136 +72,188 @@ __device__ __forceinline__ int64_t slot_of(const RotateArgs& a, int64_t i) {
   return page * a.page_bytes + (pos % a.page_size) * a.token_bytes;
 }
 
+// Four floats of shared memory, read where they are used: held in registers
+// for a whole token they cost half of the warps that an SM can have.
+__device__ __forceinline__ float4 lds4(const float* p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(smem_u32(p)));
+  return v;
+}
+
+// The two pieces of 8 values that a lane holds of a head.
+struct Pieces {
+  uint4 a, b;
+};
+
+__device__ __forceinline__ void unpack(const uint4& x, float* y) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[2 * e] = lo_f32(w[e]);
+    y[2 * e + 1] = hi_f32(w[e]);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float* y) {
+  return make_uint4(pair_bf16(y[0], y[1]), pair_bf16(y[2], y[3]), pair_bf16(y[4], y[5]),
+                    pair_bf16(y[6], y[7]));
+}
+__device__ __forceinline__ uint2 pack_e4m3(const float* y, float m) {
+  return make_uint2(pair_e4m3(y[0] * m, y[1] * m) | (pair_e4m3(y[2] * m, y[3] * m) << 16),
+                    pair_e4m3(y[4] * m, y[5] * m) | (pair_e4m3(y[6] * m, y[7] * m) << 16));
+}
+
 template <int D, bool kNorm, bool kPairs>
-__global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const __grid_constant__ RotateArgs a) {
-  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;   // lanes of a head, heads of a warp
-  const int lane = threadIdx.x & 31, sub = lane % kLanes;
-  const int heads = a.hq + 2 * a.hkv;
-  const int groups = (heads + kHeads - 1) / kHeads;
-  const int segments = (groups + a.segment - 1) / a.segment;
-  const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t i = task / segments;
+__global__ void __launch_bounds__(kMostWarps * 32, 8)
+    rotate_kernel(const __grid_constant__ RotateArgs a) {
+  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;   // lanes of a head, heads of a warp
+  __shared__ __align__(16) float cosines[D / 2], sines[D / 2];
+  __shared__ __align__(16) float norms[kNorm ? 2 : 1][kNorm ? D : 1];   // weights of queries, keys
+  __shared__ int64_t slot_shared;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes, own = lane / kLanes;
+  const int q_groups = (a.hq + kHeads - 1) / kHeads;
+  const int groups = q_groups + (2 * a.hkv + kHeads - 1) / kHeads;
+  const int64_t i = blockIdx.x / a.segments;
+  const int warps = blockDim.x >> 5;
+  // this warp's groups of heads: g0, g0 + stride, ...
+  const int stride = warps * a.segments, g0 = (int)(blockIdx.x % a.segments) * warps + warp;
   pdl_wait();   // (the launch alone overlaps the kernel before)
-  if (i >= a.n) return;
-  const int g0 = (int)(task % segments) * a.segment, g1 = min(groups, g0 + a.segment);
 
-  // this lane's 16 bytes of head h
-  auto source = [&](int h) -> const uint4* {
-    const uint16_t* p = h < a.hq ? a.q + i * a.q_token + h * a.q_head
-                        : h < a.hq + a.hkv ? a.k + i * a.k_token + (h - a.hq) * a.k_head
-                                           : a.v + i * a.v_token + (h - a.hq - a.hkv) * a.v_head;
-    return reinterpret_cast<const uint4*>(p + 8 * sub);
-  };
-  uint4 x[kAhead];
-  auto load = [&](int g) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = (g + u) * kHeads + lane / kLanes;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (g + u < g1 && h < heads) x[u] = __ldcs(source(h));
-    }
-  };
-  load(g0);
-  const bool writes = g1 * kHeads > a.hq;   // a key or value in this segment
-  const int64_t slot = writes ? slot_of(a, i) : -1;
-  if (writes && slot < 0 && lane == 0 && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
-
-  // cosines, and sines with the sign that this lane's values take them with
-  float c[8], s[8];
-  const bool turns = 8 * sub < a.rotary_dim;
+  // This lane's pieces: in the half-split form those of the dims 8 p and 8 p +
+  // R / 2, the lanes behind R share what does not turn; else piece p and D / 16
+  // behind it.
   const int half = a.rotary_dim >> 1;
-  const int partner = kPairs ? lane : 8 * sub < half ? lane + half / 8 : lane - half / 8;
-#pragma unroll
-  for (int e = 0; e < (kPairs ? 4 : 8); ++e) {
-    const int f = kPairs ? 4 * sub + e : 8 * sub < half ? 8 * sub + e : 8 * sub - half + e;
-    float cs = 1.f, sn = 0.f;
-    if (turns) {
-      const int axis = min(max(__ldg(a.axes + f), 0), a.num_axes - 1);
-      const int64_t p = __ldg(a.rope_positions + i * a.num_axes + axis);
-      const int32_t part = (int32_t)(((uint64_t)p * __ldg(a.turns + f)) >> 32);
-      __sincosf((float)part * (float)(6.283185307179586 / 4294967296.0), &sn, &cs);
-      cs *= a.rope_scale;
-      sn *= a.rope_scale;
-    }
-    if (kPairs) {
-      c[2 * e] = c[2 * e + 1] = cs;
-      s[2 * e] = -sn;
-      s[2 * e + 1] = sn;
-    } else {
-      c[e] = cs;
-      s[e] = 8 * sub < half ? -sn : sn;
-    }
+  int pa = sub, pb = sub + kLanes;
+  bool ta = 8 * pa < a.rotary_dim, tb = 8 * pb < a.rotary_dim;
+  if (!kPairs) {
+    ta = tb = 8 * sub < half;
+    pa = ta ? sub : half / 8 + sub;
+    pb = ta ? sub + half / 8 : sub + kLanes;
   }
-  float wq[8], wk[8];
-  if constexpr (kNorm) {
-    auto weights = [&](const void* p, float (&w)[8]) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        w[e] = p == nullptr ? 1.f
-               : a.norms_f32 ? __ldg(static_cast<const float*>(p) + 8 * sub + e)
-                             : lo_f32(__ldg(static_cast<const uint16_t*>(p) + 8 * sub + e));
-    };
-    weights(a.q_norm, wq);
-    weights(a.k_norm, wk);
-  }
+  const int ea = 8 * pa, eb = 8 * pb;   // first dims
 
-  for (int g = g0; g < g1; g += kAhead) {
-    if (g > g0) load(g);
+  Pieces x[kAhead];
+  auto load = [&](int g, Pieces& to) {
+    to.a = to.b = make_uint4(0, 0, 0, 0);
+    const uint16_t* p = nullptr;
+    if (g < q_groups) {
+      const int h = g * kHeads + own;
+      if (h < a.hq) p = a.q + i * a.q_token + h * a.q_head;
+    } else {
+      const int h = (g - q_groups) * kHeads + own;
+      if (h < a.hkv)
+        p = a.k + i * a.k_token + h * a.k_head;
+      else if (h < 2 * a.hkv)
+        p = a.v + i * a.v_token + (h - a.hkv) * a.v_head;
+    }
+    if (p != nullptr) {
+      to.a = __ldcs(reinterpret_cast<const uint4*>(p + ea));
+      to.b = __ldcs(reinterpret_cast<const uint4*>(p + eb));
+    }
+  };
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (g + u >= g1) break;
-      const int h = (g + u) * kHeads + lane / kLanes;   // (past the last head: nothing is written)
-      const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
-      const uint32_t raw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float y[8];
+  for (int u = 0; u < kAhead; ++u) load(g0 + u * stride, x[u]);
+  // the token's slot, cosines and sines, once per block
+  if (threadIdx.x == blockDim.x - 1) {
+    const int64_t at = slot_of(a, i);
+    if (at < 0 && a.err != nullptr) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+    slot_shared = at;
+  }
+  for (int f = threadIdx.x; f < a.rotary_dim >> 1; f += blockDim.x) {
+    const int axis = min(max(__ldg(a.axes + f), 0), a.num_axes - 1);
+    const int64_t p = __ldg(a.rope_positions + i * a.num_axes + axis);
+    const int32_t part = (int32_t)(((uint64_t)p * __ldg(a.turns + f)) >> 32);
+    float sn, cs;
+    __sincosf((float)part * (float)(6.283185307179586 / 4294967296.0), &sn, &cs);
+    cosines[f] = cs * a.rope_scale;
+    sines[f] = sn * a.rope_scale;
+  }
+  if constexpr (kNorm) {
+    for (int d = threadIdx.x; d < 2 * D; d += blockDim.x) {
+      const void* p = d < D ? a.q_norm : a.k_norm;
+      const int e = d < D ? d : d - D;
+      norms[d / D][e] = p == nullptr  ? 1.f
+                        : a.norms_f32 ? __ldg(static_cast<const float*>(p) + e)
+                                      : lo_f32(__ldg(static_cast<const uint16_t*>(p) + e));
+    }
+  }
+  __syncthreads();
+  const int64_t slot = slot_shared;
+  // the norm (`on`: this lane's head has one) and the rotation of a head's values
+  auto norm = [&](float (&y)[16], bool on, const float* weights) {
+    if constexpr (kNorm) {
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum = fmaf(y[e], y[e], sum);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      if (on) {
+        const float r = rsqrtf(sum * (1.f / D) + a.eps);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 w = lds4(weights + (e < 8 ? ea + e : eb + e - 8));
+          y[e] *= r * w.x;
+          y[e + 1] *= r * w.y;
+          y[e + 2] *= r * w.z;
+          y[e + 3] *= r * w.w;
+        }
+      }
+    }
+  };
+  auto turn = [&](float (&y)[16]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {   // pairs (ea + e, eb + e), or (2 e', 2 e' + 1) of either piece
+      if (!(kPairs && q == 1 ? tb : ta)) continue;
+      const int f = kPairs ? (q == 0 ? 4 * pa : 4 * pb) : ea + 4 * q;
+      const float4 c4 = lds4(cosines + f), s4 = lds4(sines + f);
+      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        y[2 * e] = lo_f32(raw[e]);
-        y[2 * e + 1] = hi_f32(raw[e]);
+        const int lo = kPairs ? 8 * q + 2 * e : 4 * q + e, hi = kPairs ? lo + 1 : lo + 8;
+        const float u = y[lo], v = y[hi];
+        y[lo] = fmaf(-v, s[e], u * c[e]);
+        y[hi] = fmaf(u, s[e], v * c[e]);
       }
-      if constexpr (kNorm) {
-        float sum = 0.f;
+    }
+  };
+
+  for (int g = g0; g < groups; g += kAhead * stride) {
+    if (g > g0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(y[e], y[e], sum);
+      for (int u = 0; u < kAhead; ++u) load(g + u * stride, x[u]);
+    }
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        if (is_q ? a.q_norm != nullptr : is_k && a.k_norm != nullptr) {
-          const float r = rsqrtf(sum * (1.f / D) + a.eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] * r * (is_q ? wq[e] : wk[e]);
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = g + u * stride;
+      if (at >= groups) break;
+      float y[16];
+      unpack(x[u].a, y);
+      unpack(x[u].b, y + 8);
+      const bool queries = at < q_groups;
+      const int h = (queries ? at : at - q_groups) * kHeads + own;
+      const bool is_k = !queries && h < a.hkv;
+      norm(y, queries ? a.q_norm != nullptr : is_k && a.k_norm != nullptr, norms[kNorm && !queries]);
+      if (queries) {
+        turn(y);
+        if (h < a.hq) {
+          uint16_t* p = a.q_out + i * a.out_token + h * a.out_head;
+          __stcs(reinterpret_cast<uint4*>(p + ea), pack(y));
+          __stcs(reinterpret_cast<uint4*>(p + eb), pack(y + 8));
         }
+        continue;
       }
-      float other[8];
-      if constexpr (kPairs) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) other[e] = y[e ^ 1];
+      if (is_k) turn(y);
+      if (h >= 2 * a.hkv || slot < 0) continue;
+      uint8_t* dst = a.kv + slot + (is_k ? h * a.head_bytes : a.v_bytes + (h - a.hkv) * a.head_bytes);
+      if (a.fp8) {
+        const float m = is_k ? a.k_mul : a.v_mul;
+        *reinterpret_cast<uint2*>(dst + ea) = pack_e4m3(y, m);
+        *reinterpret_cast<uint2*>(dst + eb) = pack_e4m3(y + 8, m);
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) other[e] = __shfl_sync(kFull, y[e], partner & 31);
-      }
-      if ((is_q || is_k) && turns) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = fmaf(other[e], s[e], y[e] * c[e]);
-      }
-      if (is_q) {
-        __stcs(reinterpret_cast<uint4*>(a.q_out + i * a.out_token + h * a.out_head + 8 * sub),
-               make_uint4(pair_bf16(y[0], y[1]), pair_bf16(y[2], y[3]), pair_bf16(y[4], y[5]),
-                          pair_bf16(y[6], y[7])));
-      } else if (h < heads && slot >= 0) {
-        uint8_t* dst = a.kv + slot + (is_k ? 0 : a.v_bytes) +
-                       (int64_t)(h - a.hq - (is_k ? 0 : a.hkv)) * a.head_bytes;
-        if (a.fp8) {
-          const float m = is_k ? a.k_mul : a.v_mul;
-          *reinterpret_cast<uint2*>(dst + 8 * sub) =
-              make_uint2(pair_e4m3(y[0] * m, y[1] * m) | (pair_e4m3(y[2] * m, y[3] * m) << 16),
-                         pair_e4m3(y[4] * m, y[5] * m) | (pair_e4m3(y[6] * m, y[7] * m) << 16));
-        } else {
-          // (a value's bits as they are, a NaN's too)
-          *reinterpret_cast<uint4*>(dst + 16 * sub) =
-              is_k ? make_uint4(pair_bf16(y[0], y[1]), pair_bf16(y[2], y[3]),
-                                pair_bf16(y[4], y[5]), pair_bf16(y[6], y[7]))
-                   : x[u];
-        }
+        // (a value's bits as they are, a NaN's too)
+        *reinterpret_cast<uint4*>(dst + 2 * ea) = is_k ? pack(y) : x[u].a;
+        *reinterpret_cast<uint4*>(dst + 2 * eb) = is_k ? pack(y + 8) : x[u].b;
       }
     }
   }
@@ -220,16 +275,20 @@ cudaError_t launch_rotate_append(RotateArgs& a, int head_dim, cudaStream_t strea
   const void* f = head_dim == 64    ? kernel_of<64>(norm, pairs)
                   : head_dim == 128 ? kernel_of<128>(norm, pairs)
                                     : kernel_of<256>(norm, pairs);
-  // as few segments a token as still make kWarpsWanted warps
-  constexpr int kWarpsWanted = 152 * 16;
-  const int groups = (a.hq + 2 * a.hkv + 256 / head_dim - 1) / (256 / head_dim);
-  const int wanted = (kWarpsWanted + a.n - 1) / a.n;
-  const int parts = wanted < groups ? wanted : groups;
-  a.segment = (groups + parts - 1) / parts;
-  const int64_t warps = (int64_t)a.n * ((groups + a.segment - 1) / a.segment);
+  // A block per token: 4 warps, and 2 where the tokens are many times the blocks
+  // that are resident anyway (16,088 tokens of 32 + 2 x 8 heads: 64.8 us with 2
+  // warps, 70.1 with 4; 1,152 of 64 + 2 x 8 with norms: 12.9 and 11.1; 64 of 32
+  // + 2 x 8: 3.1 and 2.6).  Tokens fewer than two per SM are shared by more
+  // blocks, down to a group of heads per warp.
+  constexpr int kManyTokens = 4096, kBlocksWanted = 304;
+  const int warps = a.n >= kManyTokens ? 2 : kMostWarps;
+  const int heads = 512 / head_dim;   // of a warp
+  const int groups = (a.hq + heads - 1) / heads + (2 * a.hkv + heads - 1) / heads;
+  const int most = (groups + warps - 1) / warps, wanted = (kBlocksWanted + a.n - 1) / a.n;
+  a.segments = wanted < most ? wanted : most;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((warps + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.gridDim = dim3((unsigned)((int64_t)a.n * a.segments));
+  cfg.blockDim = dim3(warps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

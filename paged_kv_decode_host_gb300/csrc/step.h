@@ -34,7 +34,7 @@ struct RotateArgs {
   float k_mul, v_mul;              // 1 / scale of an e4m3 cache
   int32_t fp8;
   int32_t* err;
-  int32_t segment;                 // head groups of a warp (the launcher's)
+  int32_t segments;                // blocks that share a token's heads (the launcher's)
 };
 cudaError_t launch_rotate_append(RotateArgs& a, int head_dim, cudaStream_t stream);
 

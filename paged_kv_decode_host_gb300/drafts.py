@@ -21,6 +21,23 @@ from . import (_NOT_HANDLED, FLAG_HND, FLAG_KV_FP8, FLAG_TREE, BatchDecodeWithPa
                _stream_ptr, _table_args, load, make_config, schedule_layout)
 
 MAX_AXES = 4
+_step_module = None   # the calls on tensors (module), False when not built
+
+
+def _step():
+    """The compiled calls on tensors, if built."""
+    global _step_module
+    if _step_module is None:
+        try:
+            import torch  # noqa: F401  (its libraries come first)
+            from . import _pkd_step as m
+            lib = load()
+            m.init(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.pkd_rotate_append_kv, lib.pkd_run_tree, lib.pkd_accept_kv)])
+            _step_module = m
+        except ImportError:
+            _step_module = False
+    return _step_module or None
 
 
 class RotaryPositions:
@@ -95,6 +112,18 @@ def rotate_append_kv(q, k_new, v_new, rope, batch_indices, positions, indptr, in
     448.  No two tokens may have the same slot.  kv_cache, the table, err and
     kv_layout as for :func:`append_kv`; a token outside the table still has its
     query rotated."""
+    if stream is None and q_out is None and kv_layout in ("NHD", "HND"):
+        m = _step()
+        if m is not None:
+            got = m.rotate_append(
+                q, k_new, v_new, None if rope is None else rope._args,
+                1 if rope is None else rope.num_axes, 0 if rope is None else rope._dev,
+                batch_indices, positions, indptr, indices, last_page_len, kv_cache, rope_positions,
+                q_norm, k_norm, eps, k_scale, v_scale, kv_layout == "HND", err)
+            if got is not NotImplemented:
+                if got[0]:
+                    _check(got[0], "pkd_rotate_append_kv")
+                return got[1], kv_cache
     import torch
     bf, i32 = torch.bfloat16, torch.int32
     dev = kv_cache.get_device()
@@ -261,6 +290,8 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
         self._kv_shape = torch.Size((num_pages, 2, page_size, num_kv_heads, head_dim)
                                     if kv_layout == "NHD" else
                                     (num_pages, 2, num_kv_heads, page_size, head_dim))
+        self._dev, self._scale = self.workspace.get_device(), head_dim ** -0.5
+        self._shape = tuple(self._kv_shape) + (num_qo_heads,)
 
     def plan(self, q_indptr, indptr, indices, last_page_len, *, causal=False, window=0,
              stream=None):
@@ -313,6 +344,16 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
         score_cap * tanh(score / score_cap).  slopes: float32 [Hq], then -= slope
         * (position of the query - position of the key).
         A query that sees nothing gets 0 and an lse of -inf."""
+        if stream is None and self.batch is not None:
+            m = _step()
+            if m is not None:
+                got = m.run_tree(self._hv, self._dev, self.batch, self.causal, self._shape, q, kv_cache,
+                                 mask, depths, slopes, self._scale if scale is None else scale,
+                                 score_cap, out, lse, return_lse, expect_epoch)
+                if got is not NotImplemented:
+                    if got[0]:
+                        _check(got[0], "pkd_run_tree")
+                    return got[1:] if return_lse else got[1]
         import torch
         if self.batch is None:
             raise PkdError(-5, "run before plan")
@@ -351,7 +392,7 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
                 mask.data_ptr() if mask is not None else 0, words,
                 depths.data_ptr() if depths is not None else 0,
                 slopes.data_ptr() if slopes is not None else 0,
-                self.d ** -0.5 if scale is None else scale, score_cap, expect_epoch,
+                self._scale if scale is None else scale, score_cap, expect_epoch,
                 _stream_ptr(stream))
         if st:
             _check(st, "pkd_run_tree")
@@ -383,6 +424,15 @@ def accept_kv(kv_caches, accepted, drafted, indptr, indices, last_page_len, *, e
     (:func:`accepted_table` gives the table).  err: optional int32 CUDA tensor
     of one element, flagged for requests whose rows are wrong (they are left as
     they are)."""
+    if stream is None and kv_layout in ("NHD", "HND"):
+        m = _step()
+        if m is not None:
+            st = m.accept_kv(kv_caches, accepted, drafted, indptr, indices, last_page_len,
+                             kv_layout == "HND", err)
+            if st is not NotImplemented:
+                if st:
+                    _check(st, "pkd_accept_kv")
+                return kv_caches
     import torch
     layers = len(kv_caches)
     if not 1 <= layers <= 128:

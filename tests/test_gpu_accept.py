@@ -145,9 +145,17 @@ def attention(q, k, v, scale):
     return torch.einsum("hgt,thd->hgd", torch.softmax(x, -1), v).reshape(q.shape)
 
 
-def test_three_steps_with_drafts():
+@pytest.mark.parametrize("path", ["tensors", "addresses", "ctypes"])
+def test_three_steps_with_drafts(path, monkeypatch):
     """Rotate and append trees of drafts, attend, accept a path, and go on: every step's results and
     the cache are those of the accepted tokens alone."""
+    from paged_kv_decode_host_gb300 import drafts as calls
+    if path != "tensors":
+        monkeypatch.setattr(calls, "_step", lambda: None)
+    else:
+        assert calls._step() is not None
+    if path == "ctypes":
+        monkeypatch.setattr(calls, "_fast", lambda: None)
     hq, hkv, D, page, batch, layers = 8, 2, 128, 16, 3, 2
     g = torch.Generator("cuda").manual_seed(7)
     r = np.random.default_rng(7)
