@@ -352,7 +352,7 @@ int pkd_plan_tree(pkd_ctx *ctx, const int32_t *q_indptr, const int32_t *indptr,
  *   rows       : rows of q, out and lse, at least the plan's query tokens; rows
  *                behind those are not written
  *   kv         : device bf16 [num_pages][2][P][Hkv][D] (PKD_FLAG_HND: [2][Hkv][P][D])
- *   out, lse   : device bf16 [rows][Hq][D]; device fp32 [rows][Hq] or NULL
+ *   out, lse   : device bf16 [rows][Hq][D], 32-byte aligned; device fp32 [rows][Hq] or NULL
  *   mask       : device uint32 [rows][mask_words], mask_words at least the most
  *                n_b / 32 rounded up; NULL in a causal plan
  *   depths     : device int32 [rows], d_i of every query token (below 0 counts
@@ -683,8 +683,8 @@ int pkd_plan_host_tree(const pkd_config *cfg, const int32_t *q_indptr, const int
  *          dst_slot = their chunk index, request req + i writing slot
  *          merge_indptr[req + i] + dst_slot; the page list holds the prefix
  *          table's indices, then the suffix table's; tree plans: an item
- *          covers one KV head of a block of 128 / g query tokens of request
- *          req: first_page is the request's first, word 5 the block's number
+ *          covers one KV head of a block of up to 128 / g query tokens of
+ *          request req: word 4 counts them, word 5 is the first one's number
  *          in the request, word 7 the head, and the block's token i writes
  *          slot dst_slot + i * slot_stride)
  *   off[2] units[num_units][2] = {req (tree plans: query token), num_chunks}

@@ -700,7 +700,7 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
   if (!causal && head[H_MAXQ] > 32 * (int64_t)mask_words) return PKD_E_INVALID_ARG;
   if (ctx->info.batch > 0) {
     if (q == nullptr || kv == nullptr || out == nullptr) return PKD_E_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 32) || !aligned(lse, 4) ||
         !aligned(mask, 4) || !aligned(depths, 4) || !aligned(slopes, 4))
       return PKD_E_INVALID_ARG;
   }
@@ -734,6 +734,19 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
   a.tokens = rows;
   a.scale_log2 = (float)(score_cap > 0.f ? 2.0 * log2e * scale / cap : log2e * scale);
   a.cap_log2 = (float)(log2e * cap);
+  if (score_cap > 0.f) {
+    // tanh(x) / x for |x| <= 1/2 as a polynomial of x^2, fitted for the least
+    // largest error (tanh within 4e-8, in fp32)
+    const double fit[5] = {1.0, -0.33333075046539307, 0.13324907422065735, -0.05299423262476921,
+                           0.017151299864053726};
+    const double x = scale / cap;
+    a.cap_bound = (float)(0.5 / x);
+    double c = log2e * cap * x;
+    for (int k = 0; k < 5; ++k, c *= x * x) {
+      a.cap_poly[k] = (float)(c * fit[k]);
+      if (!std::isfinite(a.cap_poly[k])) a.cap_bound = -1.f;   // (a scale past all reason: never)
+    }
+  }
   a.wait_epoch = expect_epoch != 0 ? epoch_word(expect_epoch) : 0;
   if (ctx->info.batch > 0) {
     const int st = kv_map_for(ctx, kv, &a.kv_map);

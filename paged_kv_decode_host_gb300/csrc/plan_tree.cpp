@@ -22,7 +22,7 @@ namespace pkd {
 namespace {
 
 struct RowBlock {
-  int32_t req, block, tokens, first;   // first: query token of its first row
+  int32_t req, begin, tokens, first;   // its tokens in the request; first: of all query tokens
   int64_t lo;                          // first cached token, a multiple of 16
 };
 
@@ -39,7 +39,7 @@ int plan_schedule_tree(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   if (batch > cfg.max_batch) return PKD_E_CAPACITY;
   const int64_t P = cfg.page_size;
   const int32_t hkv = cfg.num_kv_heads;
-  const int32_t rows = kTreeRows / (cfg.num_qo_heads / hkv);
+  const int32_t rows = kTreeRows / (cfg.num_qo_heads / hkv);   // tokens of a block
   thread_local std::vector<RowBlock> blocks;
   thread_local std::vector<int64_t> lens;
   thread_local std::vector<PlanPart> parts;
@@ -66,7 +66,7 @@ int plan_schedule_tree(const pkd_config& cfg, int32_t n_cta, const Layout& L,
         const int64_t at = context + (causal ? r0 : 0);   // the least position of a row
         const int64_t lo = window > 0 ? std::max<int64_t>(0, at - window + 1) / 16 * 16 : 0;
         const int64_t hi = causal ? context + r1 : len;
-        blocks.push_back(RowBlock{i, b, (int32_t)(r1 - r0), (int32_t)(q_indptr[i] + r0), lo});
+        blocks.push_back(RowBlock{i, (int32_t)r0, (int32_t)(r1 - r0), (int32_t)(q_indptr[i] + r0), lo});
         lens.push_back(hi - lo);
         total += hi - lo;
       }
@@ -138,8 +138,8 @@ int plan_schedule_tree(const pkd_config& cfg, int32_t n_cta, const Layout& L,
         w[1] = (int32_t)(b.lo + p.tok_begin);
         w[2] = (int32_t)(b.lo + p.tok_end);
         w[3] = first_slot[p.req] >= 0 ? first_slot[p.req] + chunk : -1;
-        w[4] = indptr[b.req];
-        w[5] = b.block;
+        w[4] = b.tokens;
+        w[5] = b.begin;
         w[6] = first_slot[p.req] >= 0 ? n_chunks[p.req] : 0;
         w[7] = h;
       }

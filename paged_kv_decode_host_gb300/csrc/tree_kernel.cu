@@ -50,6 +50,9 @@ using namespace dev;
 using namespace tc;
 static_assert(kTreeRows == kDenseRows && kTreeRound == kRoundTok, "the dense role's tile");
 
+// Caps up to here (in units of log2) keep the base 0: weights within 2^-90 ..
+// 2^90, sums of 2^31 of them below 2^122.
+constexpr float kFixedBase = 90.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -62,6 +65,12 @@ __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
 }
 
 // One query row of an item.
@@ -117,13 +126,13 @@ __device__ __forceinline__ int64_t token_offset(const TreeArgs& a, int first_pag
 
 __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
-// O of 32 dims (from dim0) of one row, unnormalised, summed over the tokens
+// O of 32 dims (from dim0) of one row, times inv, summed over the tokens
 // that the row sees, if one that it does not see has a value that is not
 // finite in these dims; else left as it is.  Slow, and only for caches that
 // hold such values.
 __device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uint16_t* q, int first_page,
-                                      int head, int tb, int te, int dim0, float base, float slope2,
-                                      uint32_t (&o)[32]) {
+                                      int head, int tb, int te, int dim0, float base, float inv,
+                                      float slope2, uint32_t (&o)[32]) {
   auto sees = [&](int t) { return (visible(r, t, te) & 1u) != 0; };
   bool poisoned = false;
   auto look = [&](int t) {
@@ -147,7 +156,125 @@ __device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uin
     const float p = fast_exp2(s - base);
     for (int d = 0; d < 32; ++d) acc[d] = fmaf(p, bf16_at(k + a.v_elems + dim0 + d), acc[d]);
   }
-  for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(acc[d]);
+  for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(acc[d] * inv);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// 32 bytes (a whole sector: the lanes of a warp write rows far apart)
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// What the softmax of a round needs of its row and item.
+struct Span {
+  int ctx, te;            // tokens before the drafts; the item's end
+  int reach;              // rounds that start below it need the window's mask in some row of the warp
+  float slope2;           // log2(e) * the head's slope
+  bool valid;             // a query row
+};
+
+// Largest of 32 values and `most`.
+__device__ __forceinline__ float max32(const uint32_t (&v)[32], float most) {
+  float m[4] = {most, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+  for (int j = 0; j < 32; j += 8)
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      m[u] = fmaxf(fmaxf(m[u], __uint_as_float(v[j + 2 * u])), __uint_as_float(v[j + 2 * u + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// 32 products of a row to capped scores, in units of log2.  At most half the
+// cap in magnitude, as nearly all are, they take tanh's polynomial on the FMA
+// units; the exponential and the reciprocal of the general form take three
+// times as long.
+__device__ __forceinline__ void cap32(const TreeArgs& a, uint32_t (&v)[32]) {
+  float lo[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 32; j += 4)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      lo[u] = fminf(fminf(lo[u], __uint_as_float(v[j + 2 * u])), __uint_as_float(v[j + 2 * u + 1]));
+  if (__any_sync(kFull, fmaxf(max32(v, 0.f), -fminf(lo[0], lo[1])) > a.cap_bound)) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      v[j] = __float_as_uint(capped(__uint_as_float(v[j]), a.scale_log2, a.cap_log2));
+  } else {
+    const float c0 = a.cap_poly[0], c1 = a.cap_poly[1], c2 = a.cap_poly[2], c3 = a.cap_poly[3], c4 = a.cap_poly[4];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float x = __uint_as_float(v[j]), y = x * x;
+      v[j] = __float_as_uint(x * fmaf(fmaf(fmaf(fmaf(c4, y, c3), y, c2), y, c1), y, c0));
+    }
+  }
+}
+
+// 32 scores of tokens t0 .. t0 + 31 where some are biased by other distances
+// than the place in the cache says (drafts), or masked: in units of log2 where
+// there is a cap or a slope, else as they are.  (v: capped already)
+template <bool kCap, bool kSlopes>
+__device__ __forceinline__ void shape32(const TreeArgs& a, const Row& me, const Span& sp, int t0,
+                                        uint32_t (&v)[32]) {
+  if constexpr (kSlopes) {
+    const float d0 = (float)((int64_t)sp.ctx + me.depth - t0);   // distance to the first one's token
+    const float sc = kCap ? 1.f : a.scale_log2;
+    const bool drafts = me.depths != nullptr && t0 + 32 > sp.ctx;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int t = t0 + j;
+      const float d = drafts && t >= sp.ctx && t < sp.te ? (float)(me.depth - depth_of(me, t - sp.ctx))
+                                                         : d0 - (float)j;
+      v[j] = __float_as_uint(fmaf(-sp.slope2, d, __uint_as_float(v[j]) * sc));
+    }
+  }
+  const uint32_t vis = sp.valid ? (uint32_t)visible(me, t0, sp.te) : 0u;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (!(vis & (1u << j))) v[j] = __float_as_uint(-CUDART_INF_F);
+}
+
+// Weights 2^(v sc + b + j step) of 32 scores: P in 16 words at p_addr, their
+// sum into ps.
+template <bool kStep>
+__device__ __forceinline__ void weights32(const uint32_t (&v)[32], float sc, float b, float step, uint32_t p_addr,
+                                          float (&ps)[4]) {
+  uint32_t pw[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float b0 = kStep ? fmaf(step, (float)(2 * j), b) : b;
+    const float b1 = kStep ? fmaf(step, (float)(2 * j + 1), b) : b;
+    const float p0 = fast_exp2(fmaf(__uint_as_float(v[2 * j]), sc, b0));
+    const float p1 = fast_exp2(fmaf(__uint_as_float(v[2 * j + 1]), sc, b1));
+    pw[j] = pack_bf16(p0, p1);
+    ps[j & 3] += p0;
+    ps[(j + 2) & 3] += p1;
+  }
+  tmem_st16(p_addr, pw);
 }
 
 template <bool kCap, bool kSlopes>
@@ -195,6 +322,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     sh->abort_flag = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == 32) {
+    prefetch_map(&a.q_map);
+    prefetch_map(&a.kv_map);
+  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sh->tmem_base)),
@@ -217,13 +348,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     uint64_t* full = c ? sh->fullv : sh->fullk;
     uint64_t* empty = c ? sh->emptyv : sh->emptyk;
     uint8_t* ring = stages + (size_t)c * kTcStages * kKvBytes;
-    const uint64_t policy = l2_evict_first_policy();
+    const uint64_t first = l2_evict_first_policy(), normal = l2_evict_normal_policy();
     pdl_wait();   // q and the cache may come from the previous kernel
     int st = 0, nq = 0;
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
       const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
-      const int tb = item[1], te = item[2], poff = item[4], head = item[7];
+      const int tb = item[1], te = item[2], head = item[7];
+      const int32_t* entry = requests + item[0] * kRequestWords;
+      const int poff = entry[3];
       // the item's queries (the previous item's score MMAs must be done)
       if (c == 0 && it > it0 &&
           !tc_wait(&sh->qfree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane)) {
@@ -231,13 +364,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         break;
       }
       if (c == 0 && lane == 0) {
-        const int row0 = requests[item[0] * kRequestWords] + item[5] * tile_tokens;
+        const int row0 = entry[0] + item[5];
         ++nq;
         mbar_arrive_expect_tx(&sh->qfull, (uint32_t)kQBytes);
         for (int h = 0; h < 2; ++h)
-          tensor_copy_g2s(sQ + h * (kQBytes / 2), &a.q_map, 0, h, 0, head, row0, &sh->qfull, policy);
+          tensor_copy_g2s(sQ + h * (kQBytes / 2), &a.q_map, 0, h, 0, head, row0, &sh->qfull, first);
       }
       __syncwarp();
+      // (more than one row block reads these tokens: they may stay in L2)
+      const uint64_t policy = entry[1] > tile_tokens ? normal : first;
       // page ids of 32 tiles of 16 tokens at a time (tb is a multiple of 16)
       const int ntiles = (te - tb + 15) >> 4;
       int base = -32, my_page = 0;
@@ -407,14 +542,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     };
     for (int it = it0; it < it1 && ok; ++it) {
       const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
-      const int tb = item[1], te = item[2], dst = item[3], first_page = item[4];
-      const int i0 = item[5] * tile_tokens, stride = item[6], head = item[7];
+      const int tb = item[1], te = item[2], dst = item[3], n_tok = item[4], i0 = item[5];
+      const int stride = item[6], head = item[7];
       const int32_t* entry = requests + item[0] * kRequestWords;
-      const int q_first = entry[0], drafts = entry[1], ctx = entry[2];
+      const int q_first = entry[0], drafts = entry[1], ctx = entry[2], first_page = entry[3];
       const int nr = rounds_of(tb, te);
       const int r0 = rho;
       rho = r0 + nr;
-      const int n_tok = min(tile_tokens, drafts - i0);
       if (quad * 32 >= n_tok * g) {
         // no row of this quadrant: keep the barriers' count, in their order
         for (int r = r0; r < rho && ok; ++r) {
@@ -443,10 +577,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       me.first_seen = window > 0 ? (int)max((int64_t)-1, min((int64_t)0x7fffffff,
                                             (int64_t)ctx + me.depth - window + 1))
                                  : -1;
-      // rounds below `reach` need the window's mask in some row of the warp
-      int reach = valid ? me.first_seen : -1;
-      if (window > 0) reach = __reduce_max_sync(kFull, reach);
-      const float slope2 = kSlopes && valid ? a.slopes[hq] * kLog2e : 0.f;
+      Span sp;
+      sp.ctx = ctx;
+      sp.te = te;
+      sp.reach = valid ? me.first_seen : -1;
+      if (window > 0) sp.reach = __reduce_max_sync(kFull, sp.reach);
+      sp.slope2 = kSlopes && valid ? a.slopes[hq] * kLog2e : 0.f;
+      sp.valid = valid;
       float m_used = -CUDART_INF_F, l = 0.f;   // l: this warp's half of the row sum
       bool o_has = false;
       for (int k = 0; k < nr && ok; ++k) {
@@ -458,75 +595,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         }
         tc_fence_after();
         const uint32_t s_col = kColS + kSCols * b + 64 * half;
+        // does some row of the warp not see all of its 64 columns?
+        const bool special = t0 + 64 > ctx || t0 < sp.reach || te - t0 < 64;
         uint32_t sv[2][32];
         tmem_ld32(tq + s_col, sv[0]);
         tmem_ld32(tq + s_col + 32, sv[1]);
         tmem_wait_ld();
+        float sc = a.scale_log2, step = 0.f, mx = -CUDART_INF_F;
         if constexpr (kCap) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              sv[q][j] = __float_as_uint(capped(__uint_as_float(sv[q][j]), a.scale_log2, a.cap_log2));
+          cap32(a, sv[0]);
+          cap32(a, sv[1]);
+          sc = 1.f;
         }
-        if constexpr (kSlopes) {
-          const float d0 = (float)((int64_t)ctx + me.depth - t0);   // distance to the first column's token
-          const float sc = kCap ? 1.f : a.scale_log2;
-          if (me.depths != nullptr && t0 + 64 > ctx) {
-#pragma unroll
+        if (special) {
+          shape32<kCap, kSlopes>(a, me, sp, t0, sv[0]);
+          shape32<kCap, kSlopes>(a, me, sp, t0 + 32, sv[1]);
+          if (kSlopes) sc = 1.f;
+        }
+        // Capped scores lie between -cap and cap: with the base 0 no weight or sum
+        // leaves fp32's (and bf16's) range, and the largest need not be known.
+        const bool fixed = kCap && !kSlopes && a.cap_log2 <= kFixedBase;
+        if (!fixed) {
+          if (kSlopes && !special) {
+            // the largest product of 32 and their largest bias bound their scores
+            step = sp.slope2;
+            const float far = -step * (float)((int64_t)ctx + me.depth - t0);
             for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const int t = t0 + 32 * q + j;
-                const float d = t >= ctx && t < te ? (float)(me.depth - depth_of(me, t - ctx))
-                                                   : d0 - (float)(32 * q + j);
-                sv[q][j] = __float_as_uint(fmaf(-slope2, d, __uint_as_float(sv[q][j]) * sc));
-              }
+              mx = fmaxf(mx, fmaf(max32(sv[q], -CUDART_INF_F), sc, far + fmaxf(step * (32 * q), step * (32 * q + 31))));
           } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                sv[q][j] = __float_as_uint(fmaf(-slope2, d0 - (float)(32 * q + j),
-                                                __uint_as_float(sv[q][j]) * sc));
+            mx = fmaxf(max32(sv[0], -CUDART_INF_F), max32(sv[1], -CUDART_INF_F)) * sc;   // (sc > 0)
           }
-        }
-        if (t0 + 64 > ctx || t0 < reach || te - t0 < 64) {
-          const uint64_t vis = valid ? visible(me, t0, te) : 0ull;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint32_t v = (uint32_t)(vis >> (32 * q));
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(v & (1u << j))) sv[q][j] = __float_as_uint(-CUDART_INF_F);
+          float m_other;
+          if (!exchange(s_col, kColS + kSCols * b + 64 * (1 - half), mx, &m_other)) {
+            ok = false;
+            break;
           }
+          mx = fmaxf(mx, m_other);
         }
-        float mq[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mq[j & 3] = fmaxf(mq[j & 3], __uint_as_float(sv[q][j]));
-        const float m_half = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-        float m_other;
-        if (!exchange(s_col, kColS + kSCols * b + 64 * (1 - half), m_half, &m_other)) {
-          ok = false;
-          break;
-        }
-        // both halves of S are read and exchanged: the buffer may be refilled
+        // this half of S is read (and exchanged): the buffer may be refilled
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->sfree[b]);
-        const float sc2 = kCap || kSlopes ? 1.f : a.scale_log2;   // (positive: the max is the max's)
-        const float mx = fmaxf(m_half, m_other) * sc2;
         // P buffer b was read by the P.V MMAs of round r - 2
         if (r >= 2 && !pv_wait(r - 2)) {
           ok = false;
           break;
         }
+        if (fixed) m_used = 0.f;
         // the base is raised, and O rescaled, only past 2^8 of growth (per row;
         // the waits and tensor-memory accesses are the whole warp's)
-        const bool need = mx > m_used + kRescaleLog2;
-        if (__any_sync(kFull, need)) {
+        const bool need = !fixed && mx > m_used + kRescaleLog2;
+        if (!fixed && __any_sync(kFull, need)) {
           const float alpha = need ? exp2f(m_used - mx) : 1.f;   // 0 while m_used = -inf
           if (o_has) {
             if (!pv_wait(r - 1)) {
@@ -534,14 +653,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
               break;
             }
             tc_fence_after();
-#pragma unroll
-            for (int cb = 0; cb < 64; cb += 32) {
-              uint32_t o[32];
-              tmem_ld32(tq + kColO + 64 * half + cb, o);
+#pragma unroll 1
+            for (int cb = 0; cb < 64; cb += 16) {
+              uint32_t o[16];
+              tmem_ld16(tq + kColO + 64 * half + cb, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st32(tq + kColO + 64 * half + cb, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st16(tq + kColO + 64 * half + cb, o);
             }
             tmem_wait_st();
           }
@@ -549,19 +668,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           if (need) m_used = mx;
         }
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
-        const float neg_m = m_used == -CUDART_INF_F ? 0.f : -m_used;   // nothing seen yet: weights 0
-        uint32_t pw[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint32_t* src = sv[j >> 4];
-          const int c = 2 * (j & 15);
-          const float p0 = fast_exp2(fmaf(__uint_as_float(src[c]), sc2, neg_m));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(src[c + 1]), sc2, neg_m));
-          pw[j] = pack_bf16(p0, p1);
-          ps[j & 3] += p0;
-          ps[(j + 2) & 3] += p1;
-        }
-        tmem_st32(tq + kColP + kPCols * b + 32 * half, pw);
+        float base = m_used == -CUDART_INF_F ? 0.f : -m_used;   // nothing seen yet: weights 0
+        if (kSlopes && !special) base -= sp.slope2 * (float)((int64_t)ctx + me.depth - t0);
+        const uint32_t p_col = tq + kColP + kPCols * b + 32 * half;
+        weights32<kSlopes>(sv[0], sc, base, step, p_col, ps);
+        weights32<kSlopes>(sv[1], sc, kSlopes ? fmaf(step, 32.f, base) : base, step, p_col + 16, ps);
         l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
         tmem_wait_st();
         tc_fence_before();
@@ -588,41 +699,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       const float lt = half == 0 ? l + l_other : l_other + l;
       const int64_t q_row = (int64_t)(q_first + i0 + i) * a.hq + hq;
       const int64_t p_row = ((int64_t)dst + (int64_t)i * stride) * a.hq + hq;   // its partial state
-      const float inv = 1.f / lt;
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll 1
       for (int cb = 64 * half; cb < 64 * half + 64; cb += 32) {
         uint32_t o[32];
         tmem_ld32(tq + kColO + cb, o);
         tmem_wait_ld();
-        if (valid) {
-          bool odd = false;
+        float odd = 0.f;   // NaN if a value is not finite
 #pragma unroll
-          for (int j = 0; j < 32; ++j) odd |= (o[j] & 0x7f800000u) == 0x7f800000u;
-          if (odd && lt != 0.f) {
-            uint32_t again[32];   // (only this rare call needs the values in memory)
+        for (int j = 0; j < 32; ++j) {
+          const float x = __uint_as_float(o[j]) * inv;
+          o[j] = __float_as_uint(x);
+          odd = fmaf(x, 0.f, odd);
+        }
+        if (valid && odd != odd) {
+          uint32_t again[32];   // (only this rare case needs the values in memory)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) again[j] = o[j];
-            redo_row(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used, slope2, again);
+          for (int j = 0; j < 32; ++j) again[j] = lt == 0.f ? 0u : o[j];
+          if (lt != 0.f)
+            redo_row(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used, inv, sp.slope2, again);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = again[j];
+          for (int j = 0; j < 32; ++j) o[j] = again[j];
+        }
+        if (valid && dst < 0) {
+          uint16_t* op = a.out + q_row * kHeadDim + cb;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              w[j] = pack_bf16(__uint_as_float(o[16 * q + 2 * j]), __uint_as_float(o[16 * q + 2 * j + 1]));
+            store32(op + 16 * q, w);
           }
+        } else if (valid) {
+          float* op = a.o_part + p_row * kHeadDim + cb;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            o[j] = lt == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
-          if (dst < 0) {
-            uint4* op = reinterpret_cast<uint4*>(a.out + q_row * kHeadDim + cb);
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4)
-              op[q4] = make_uint4(
-                  pack_bf16(__uint_as_float(o[8 * q4 + 0]), __uint_as_float(o[8 * q4 + 1])),
-                  pack_bf16(__uint_as_float(o[8 * q4 + 2]), __uint_as_float(o[8 * q4 + 3])),
-                  pack_bf16(__uint_as_float(o[8 * q4 + 4]), __uint_as_float(o[8 * q4 + 5])),
-                  pack_bf16(__uint_as_float(o[8 * q4 + 6]), __uint_as_float(o[8 * q4 + 7])));
-          } else {
-            uint4* op = reinterpret_cast<uint4*>(a.o_part + p_row * kHeadDim + cb);
-#pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4)
-              op[q4] = make_uint4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
-          }
+          for (int q = 0; q < 4; ++q) store32(op + 8 * q, o + 8 * q);
         }
         __syncwarp();
       }

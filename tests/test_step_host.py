@@ -71,9 +71,10 @@ def test_plans_cover_every_row_and_token_once(lib, hq, hkv, ctas, causal, window
                                         for b in range(batch)]
         ranges, slots = {}, {}
         for it, head in zip(s["items"], s["heads"]):
-            req, tb, te, dst, first, block, stride = it
+            req, tb, te, dst, tokens, first, stride = it
+            block = first // rows
             assert 0 <= req < batch and 0 <= head < hkv and tb < te <= lens[req] and tb % 16 == 0
-            assert first == t[0][req] and 0 <= block * rows < drafts[req]
+            assert first % rows == 0 and tokens == min(rows, drafts[req] - first) > 0
             ranges.setdefault((req, block, head), []).append((tb, te, dst, stride))
         units = {}
         for u, (token, chunks) in enumerate(s["units"]):
