@@ -740,7 +740,7 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
     const double fit[5] = {1.0, -0.33333075046539307, 0.13324907422065735, -0.05299423262476921,
                            0.017151299864053726};
     const double x = scale / cap;
-    a.cap_bound = (float)(0.5 / x);
+    a.cap_bound = (float)(0.25 / (x * x));
     double c = log2e * cap * x;
     for (int k = 0; k < 5; ++k, c *= x * x) {
       a.cap_poly[k] = (float)(c * fit[k]);

@@ -32,8 +32,8 @@ struct TreeArgs {
   int32_t tokens;           // rows of q, out and lse
   float scale_log2;         // scale * log2(e); with a cap: 2 scale / cap * log2(e)
   float cap_log2;           // cap * log2(e), 0 without
-  // for products of up to cap_bound: cap_log2 * tanh(scale / cap * x) = x times
-  // this polynomial of x^2
+  // for products whose square is up to cap_bound: cap_log2 * tanh(scale / cap * x)
+  // = x times this polynomial of x^2
   float cap_bound, cap_poly[5];
   int32_t wait_epoch;
   CUtensorMap kv_map;       // 16-token boxes of one 128-byte half of a KV head

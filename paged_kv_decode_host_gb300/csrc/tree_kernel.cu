@@ -198,6 +198,48 @@ struct Span {
   bool valid;             // a query row
 };
 
+// The order of an item's nr rounds: with slopes from the newest tokens to the
+// oldest, whose biases only fall (the other way the base was raised, and O
+// rescaled, in every round: 700 cycles of 3,000).
+template <bool kSlopes>
+__device__ __forceinline__ int round_at(int k, int nr) {
+  return kSlopes ? nr - 1 - k : k;
+}
+
+// Two fp32 operations an instruction: these softmaxes are bound by instruction
+// issue, and packed ones count once.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(uint32_t lo, uint32_t hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 // Largest of 32 values and `most`.
 __device__ __forceinline__ float max32(const uint32_t (&v)[32], float most) {
   float m[4] = {most, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
@@ -209,27 +251,44 @@ __device__ __forceinline__ float max32(const uint32_t (&v)[32], float most) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// 32 products of a row to capped scores, in units of log2.  At most half the
-// cap in magnitude, as nearly all are, they take tanh's polynomial on the FMA
-// units; the exponential and the reciprocal of the general form take three
-// times as long.
-__device__ __forceinline__ void cap32(const TreeArgs& a, uint32_t (&v)[32]) {
-  float lo[2] = {0.f, 0.f};
+// 64 products of a row (columns s_addr .. of its S) to capped scores, in units
+// of log2.  At most half the cap in magnitude, as nearly all are, they take
+// tanh's polynomial on the FMA units; where any in the warp is larger, all are
+// read again and take the exponential and the reciprocal, three times as long.
+__device__ __noinline__ void cap64_any(float scale, float cap, uint32_t s_addr, uint32_t (&v)[64]) {
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t x[16];
+    tmem_ld16(s_addr + c, x);
+    tmem_wait_ld();
 #pragma unroll
-  for (int j = 0; j < 32; j += 4)
+    for (int j = 0; j < 16; ++j) v[c + j] = __float_as_uint(capped(__uint_as_float(x[j]), scale, cap));
+  }
+}
+__device__ __forceinline__ void cap64(const TreeArgs& a, uint32_t s_addr, uint32_t (&v)[2][32]) {
+  F2 c[5];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      lo[u] = fminf(fminf(lo[u], __uint_as_float(v[j + 2 * u])), __uint_as_float(v[j + 2 * u + 1]));
-  if (__any_sync(kFull, fmaxf(max32(v, 0.f), -fminf(lo[0], lo[1])) > a.cap_bound)) {
+  for (int k = 0; k < 5; ++k) c[k] = f2(a.cap_poly[k], a.cap_poly[k]);
+  float most[2] = {0.f, 0.f};   // of the squares
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      v[j] = __float_as_uint(capped(__uint_as_float(v[j]), a.scale_log2, a.cap_log2));
-  } else {
-    const float c0 = a.cap_poly[0], c1 = a.cap_poly[1], c2 = a.cap_poly[2], c3 = a.cap_poly[3], c4 = a.cap_poly[4];
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const F2 x = f2(v[q][j], v[q][j + 1]), y = mul2(x, x);
+      float lo, hi;
+      split(y, lo, hi);
+      most[q] = fmaxf(fmaxf(most[q], lo), hi);
+      split(mul2(x, fma2(fma2(fma2(fma2(c[4], y, c[3]), y, c[2]), y, c[1]), y, c[0])), lo, hi);
+      v[q][j] = __float_as_uint(lo);
+      v[q][j + 1] = __float_as_uint(hi);
+    }
+  if (__any_sync(kFull, fmaxf(most[0], most[1]) > a.cap_bound)) {
+    uint32_t w[64];
+    cap64_any(a.scale_log2, a.cap_log2, s_addr, w);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const float x = __uint_as_float(v[j]), y = x * x;
-      v[j] = __float_as_uint(x * fmaf(fmaf(fmaf(fmaf(c4, y, c3), y, c2), y, c1), y, c0));
+      v[0][j] = w[j];
+      v[1][j] = w[32 + j];
     }
   }
 }
@@ -262,37 +321,45 @@ __device__ __forceinline__ void shape32(const TreeArgs& a, const Row& me, const 
 // sum into ps.
 template <bool kStep>
 __device__ __forceinline__ void weights32(const uint32_t (&v)[32], float sc, float b, float step, uint32_t p_addr,
-                                          float (&ps)[4]) {
+                                          F2 (&ps)[2]) {
   uint32_t pw[16];
+  const F2 sc2 = f2(sc, sc), b2 = f2(b, b), st2 = f2(step, step);
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const float b0 = kStep ? fmaf(step, (float)(2 * j), b) : b;
-    const float b1 = kStep ? fmaf(step, (float)(2 * j + 1), b) : b;
-    const float p0 = fast_exp2(fmaf(__uint_as_float(v[2 * j]), sc, b0));
-    const float p1 = fast_exp2(fmaf(__uint_as_float(v[2 * j + 1]), sc, b1));
+    const F2 at = kStep ? fma2(st2, f2((float)(2 * j), (float)(2 * j + 1)), b2) : b2;
+    float x0, x1;
+    split(fma2(f2(v[2 * j], v[2 * j + 1]), sc2, at), x0, x1);
+    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
     pw[j] = pack_bf16(p0, p1);
-    ps[j & 3] += p0;
-    ps[(j + 2) & 3] += p1;
+    ps[j & 1] = add2(ps[j & 1], f2(p0, p1));
   }
   tmem_st16(p_addr, pw);
 }
 
+struct TreeSmem {
+  float swap[2][2][kTreeRows];   // exchanges of the warps of a quadrant: place, half, row
+};
+constexpr int kSmemBytes = kQBytes + kTcStages * kStageBytes + (int)sizeof(TcSmem) + (int)sizeof(TreeSmem);
+static_assert(kSmemBytes <= 227 * 1024 && sizeof(TcSmem) % 4 == 0, "dynamic shared memory of one CTA");
+
 template <bool kCap, bool kSlopes>
 __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
   pdl_launch_dependents();
   const bool chain = a.sched[H_CAUSAL] != 0;
-  // a captured launch under a later plan that its tensors do not fit
-  if (a.sched[H_BATCH] > a.tokens || (!chain && a.sched[H_MAXQ] > 32 * (int64_t)a.mask_words)) {
+  // a captured launch under a later plan that its tensors do not fit (and, never
+  // seen, shared memory that the swizzle could not use)
+  if (a.sched[H_BATCH] > a.tokens || (!chain && a.sched[H_MAXQ] > 32 * (int64_t)a.mask_words) ||
+      (smem_u32(smem) & 1023) != 0) {
     if (threadIdx.x == 0) atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
     pdl_wait();
     return;
   }
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
   uint8_t* stages = smem + kQBytes;
   TcSmem* sh = reinterpret_cast<TcSmem*>(stages + kTcStages * kStageBytes);
+  TreeSmem* more = reinterpret_cast<TreeSmem*>(sh + 1);
   volatile int* abort_flag = &sh->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int it0 = a.sched[a.off_cta + blockIdx.x];
@@ -317,7 +384,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       mbar_init(&sh->pfree[b], 1);
     }
     mbar_init(&sh->ofree, kSoftmaxWarps);
-    for (int q = 0; q < 4; ++q) mbar_init(&sh->xch[q], 2);
     mbar_init(&sh->fin, 2);
     sh->abort_flag = 0;
     fence_mbar_init();
@@ -373,33 +439,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       __syncwarp();
       // (more than one row block reads these tokens: they may stay in L2)
       const uint64_t policy = entry[1] > tile_tokens ? normal : first;
-      // page ids of 32 tiles of 16 tokens at a time (tb is a multiple of 16)
-      const int ntiles = (te - tb + 15) >> 4;
-      int base = -32, my_page = 0;
-      for (int t = tb, k = 0; t < te; t += kRoundTok, ++st, ++k) {
-        const int n = min(kRoundTok, te - t);
-        const int nbox = (n + 15) >> 4;
-        const int tile0 = kRoundTiles * k;
-        if (tile0 + kRoundTiles > base + 32) {
-          base = tile0;
-          my_page = 0;
-          if (base + lane < ntiles) {
-            my_page = a.sched[a.off_pages + poff + (tb + 16 * (base + lane)) / P];
-            if ((unsigned)my_page >= (unsigned)a.num_pages) {
-              atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
-              my_page = 0;
-            }
-          }
+      // Lane 2 j + h (lanes 0-15) copies half h of the round's tile j (tb is a
+      // multiple of 16); the page ids of the round after are on their way.
+      const int j = lane >> 1, h = lane & 1;
+      const int nr = rounds_of(tb, te), ntiles = (te - tb + 15) >> 4;
+      auto page_of = [&](int k) -> int {
+        const int tile = kRoundTiles * round_at<kSlopes>(k, nr) + j;
+        return k < nr && lane < 16 && tile < ntiles ? a.sched[a.off_pages + poff + (tb + 16 * tile) / P] : 0;
+      };
+      int next = page_of(0);
+      for (int k = 0; k < nr; ++k, ++st) {
+        int page = next;
+        next = page_of(k + 1);
+        if ((unsigned)page >= (unsigned)a.num_pages) {
+          atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+          page = 0;
         }
+        const int t = tb + kRoundTok * round_at<kSlopes>(k, nr);
+        const int nbox = (min(kRoundTok, te - t) + 15) >> 4;
         const int slot = st % kTcStages;
         const uint32_t round = (uint32_t)(st / kTcStages);
         if (round > 0 && !tc_wait(&empty[slot], (round - 1) & 1u, abort_flag, a.err, lane)) {
           ok = false;
           break;
         }
-        // lane 2 j + h (lanes 0-15) copies half h of tile j
-        const int j = lane >> 1, h = lane & 1;
-        const int page = __shfl_sync(kFull, my_page, (tile0 + (j & 7) - base) & 31);
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(2 * nbox * kBoxBytes));
         __syncwarp();
         if (j < nbox)
@@ -437,7 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           ok = false;
           break;
         }
-        const int n = min(kRoundTok, te - (tb + k * kRoundTok));
+        const int n = min(kRoundTok, te - (tb + round_at<kSlopes>(k, nr) * kRoundTok));
         if (lane == 0) {
           tc_fence_after();
           const uint32_t idesc_s = mma_idesc(kDenseRows, 16 * ((n + 15) >> 4), 0);
@@ -477,7 +540,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           ok = false;
           break;
         }
-        const int n = min(kRoundTok, te - (tb + k * kRoundTok));
+        const int n = min(kRoundTok, te - (tb + round_at<kSlopes>(k, nr) * kRoundTok));
         const int nbox = (n + 15) >> 4;
         uint8_t* vbase = stages + (size_t)(kTcStages + slot) * kKvBytes;
         if (n & 15) {
@@ -519,25 +582,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     const int window = a.sched[H_WINDOW];
     pdl_wait();   // outputs, mask and depths may belong to the previous kernel
     int rho = 0;
-    uint32_t xc = 0;   // exchanges with the partner warp so far (the barrier's phase)
+    uint32_t swaps = 0;   // exchanges with the partner warp so far
     bool ok = true;
     auto pv_wait = [&](int r) -> bool {
       if (r < 0) return true;
       return tc_wait(&sh->pfree[r & 1], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane);
     };
-    // one float per row with the partner warp of this quadrant, through
-    // tensor-memory columns that both have read
-    auto exchange = [&](uint32_t mine, uint32_t theirs, float v, float* other) -> bool {
-      tmem_st1(tq + mine, __float_as_uint(v));
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->xch[quad]);
-      if (!tc_wait(&sh->xch[quad], xc & 1u, abort_flag, a.err, lane)) return false;
-      ++xc;
-      tc_fence_after();
-      *other = __uint_as_float(tmem_ld1(tq + theirs));
-      tmem_wait_ld();
+    // One float per row with the partner warp of this quadrant, through shared
+    // memory: two places in turn (the partner has read one before it comes to the
+    // next exchange, and that is over before this warp writes there again).  The
+    // two warps meet at a barrier of their own, in a third of an mbarrier's time.
+    // A warp whose wait ran out has raised the abort flag and arrives there once
+    // more (below): a partner that waits goes on, and stops at the flag.
+    auto exchange = [&](float v, float* other) -> bool {
+      if (*abort_flag) return false;
+      more->swap[swaps & 1u][half][row] = v;
+      asm volatile("barrier.sync %0, 64;" ::"r"(1 + quad) : "memory");
+      *other = more->swap[swaps & 1u][half ^ 1][row];
+      ++swaps;
       return true;
     };
     for (int it = it0; it < it1 && ok; ++it) {
@@ -588,8 +650,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       bool o_has = false;
       for (int k = 0; k < nr && ok; ++k) {
         const int r = r0 + k, b = r & 1;
-        const int t0 = tb + k * kRoundTok + 64 * half;   // token of this warp's first column
-        if (!tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
+        const int t0 = tb + round_at<kSlopes>(k, nr) * kRoundTok + 64 * half;   // token of this warp's first column
+        // (P buffer b was read by the P.V MMAs of round r - 2)
+        if ((r >= 2 && !pv_wait(r - 2)) ||
+            !tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
           ok = false;
           break;
         }
@@ -603,8 +667,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         tmem_wait_ld();
         float sc = a.scale_log2, step = 0.f, mx = -CUDART_INF_F;
         if constexpr (kCap) {
-          cap32(a, sv[0]);
-          cap32(a, sv[1]);
+          cap64(a, tq + s_col, sv);
           sc = 1.f;
         }
         if (special) {
@@ -626,7 +689,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
             mx = fmaxf(max32(sv[0], -CUDART_INF_F), max32(sv[1], -CUDART_INF_F)) * sc;   // (sc > 0)
           }
           float m_other;
-          if (!exchange(s_col, kColS + kSCols * b + 64 * (1 - half), mx, &m_other)) {
+          if (!exchange(mx, &m_other)) {
             ok = false;
             break;
           }
@@ -636,11 +699,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->sfree[b]);
-        // P buffer b was read by the P.V MMAs of round r - 2
-        if (r >= 2 && !pv_wait(r - 2)) {
-          ok = false;
-          break;
-        }
         if (fixed) m_used = 0.f;
         // the base is raised, and O rescaled, only past 2^8 of growth (per row;
         // the waits and tensor-memory accesses are the whole warp's)
@@ -667,13 +725,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           l *= alpha;
           if (need) m_used = mx;
         }
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        F2 ps[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
         float base = m_used == -CUDART_INF_F ? 0.f : -m_used;   // nothing seen yet: weights 0
         if (kSlopes && !special) base -= sp.slope2 * (float)((int64_t)ctx + me.depth - t0);
         const uint32_t p_col = tq + kColP + kPCols * b + 32 * half;
         weights32<kSlopes>(sv[0], sc, base, step, p_col, ps);
         weights32<kSlopes>(sv[1], sc, kSlopes ? fmaf(step, 32.f, base) : base, step, p_col + 16, ps);
-        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        float l0, l1;
+        split(add2(ps[0], ps[1]), l0, l1);
+        l += l0 + l1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -688,11 +748,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         break;
       }
       tc_fence_after();
-      // the row sum of both halves, exchanged through the last round's P
-      // columns (read by its P.V MMAs already); added in half order
-      const uint32_t p_last = kColP + kPCols * (rl & 1);
+      // the row sum of both halves, added in half order
       float l_other;
-      if (!exchange(p_last + 32 * half, p_last + 32 * (1 - half), l, &l_other)) {
+      if (!exchange(l, &l_other)) {
         ok = false;
         break;
       }
@@ -749,6 +807,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           a.lse[q_row] = lse;
       }
     }
+    if (!ok) asm volatile("barrier.arrive %0, 64;" ::"r"(1 + quad) : "memory");
   }
   // all roles done: tensor memory is no longer read or written
   tc_fence_before();
@@ -771,7 +830,7 @@ const void* kernel_of(bool cap, bool slopes) {
 
 }  // namespace
 
-int tree_smem_bytes() { return tc::smem_bytes(); }
+int tree_smem_bytes() { return kSmemBytes; }
 
 cudaError_t tree_prepare() {
   for (int k = 0; k < 4; ++k) {
