@@ -168,7 +168,7 @@ typedef struct pkd_config {
  * pkd_run_tree.  max_batch is the capacity in query tokens (and in requests);
  * pkd_plan_info.batch counts query tokens.  bf16 cache, head_dim 128, page
  * size a multiple of 16; combinable with PKD_FLAG_HND only.  alpha < 0 selects
- * 256, min_chunk_tokens < 0 256.  Not for pkd_plan, pkd_run, pkd_graph_capture
+ * 512, min_chunk_tokens < 0 128.  Not for pkd_plan, pkd_run, pkd_graph_capture
  * and pkd_accumulate_weights. */
 #define PKD_FLAG_TREE 2048u
 

@@ -735,14 +735,14 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
   a.scale_log2 = (float)(score_cap > 0.f ? 2.0 * log2e * scale / cap : log2e * scale);
   a.cap_log2 = (float)(log2e * cap);
   if (score_cap > 0.f) {
-    // tanh(x) / x for |x| <= 1/2 as a polynomial of x^2, fitted for the least
-    // largest error (tanh within 4e-8, in fp32)
-    const double fit[5] = {1.0, -0.33333075046539307, 0.13324907422065735, -0.05299423262476921,
-                           0.017151299864053726};
+    // tanh(x) / x for |x| <= 0.4 as a polynomial of x^2, fitted for the least
+    // largest error (tanh within 7e-8, in fp32)
+    const double fit[4] = {0.9999999043749117, -0.33331390193300425, 0.13271438197786756,
+                           -0.04757281035736614};
     const double x = scale / cap;
-    a.cap_bound = (float)(0.25 / (x * x));
+    a.cap_bound = (float)(0.16 / (x * x));
     double c = log2e * cap * x;
-    for (int k = 0; k < 5; ++k, c *= x * x) {
+    for (int k = 0; k < 4; ++k, c *= x * x) {
       a.cap_poly[k] = (float)(c * fit[k]);
       if (!std::isfinite(a.cap_poly[k])) a.cap_bound = -1.f;   // (a scale past all reason: never)
     }

@@ -11,8 +11,12 @@ namespace pkd {
 
 constexpr int kTreeRows = 128;       // query rows of a tile: 128 / g tokens x g heads of a KV head
 constexpr int kTreeRound = 128;      // tokens per round of the kernel; plans cut at multiples of it
-constexpr int kTreeAlpha = 256;      // an item's fixed cost in tokens
-constexpr int kTreeMinChunk = 256;   // split floor in tokens
+// An item's fixed cost and the split floor, in tokens.  Measured with 512 / 128,
+// 256 / 256 and 128 / 128: 24 ragged requests x 7 drafts with slopes 38.7, 44.1
+// and 43.6 us; 16 x 61 drafts of 64 heads 190, 197 and 199; one of 517 tokens
+// 10.1, 10.5 and 10.2.
+constexpr int kTreeAlpha = 512;
+constexpr int kTreeMinChunk = 128;
 
 struct TreeArgs {
   const int32_t* sched;
@@ -34,7 +38,7 @@ struct TreeArgs {
   float cap_log2;           // cap * log2(e), 0 without
   // for products whose square is up to cap_bound: cap_log2 * tanh(scale / cap * x)
   // = x times this polynomial of x^2
-  float cap_bound, cap_poly[5];
+  float cap_bound, cap_poly[4];
   int32_t wait_epoch;
   CUtensorMap kv_map;       // 16-token boxes of one 128-byte half of a KV head
   CUtensorMap q_map;        // boxes of a KV head's 128 query rows and one half

@@ -252,7 +252,7 @@ __device__ __forceinline__ float max32(const uint32_t (&v)[32], float most) {
 }
 
 // 64 products of a row (columns s_addr .. of its S) to capped scores, in units
-// of log2.  At most half the cap in magnitude, as nearly all are, they take
+// of log2.  At most 0.4 of the cap in magnitude, as nearly all are, they take
 // tanh's polynomial on the FMA units; where any in the warp is larger, all are
 // read again and take the exponential and the reciprocal, three times as long.
 __device__ __noinline__ void cap64_any(float scale, float cap, uint32_t s_addr, uint32_t (&v)[64]) {
@@ -266,9 +266,9 @@ __device__ __noinline__ void cap64_any(float scale, float cap, uint32_t s_addr, 
   }
 }
 __device__ __forceinline__ void cap64(const TreeArgs& a, uint32_t s_addr, uint32_t (&v)[2][32]) {
-  F2 c[5];
+  F2 c[4];
 #pragma unroll
-  for (int k = 0; k < 5; ++k) c[k] = f2(a.cap_poly[k], a.cap_poly[k]);
+  for (int k = 0; k < 4; ++k) c[k] = f2(a.cap_poly[k], a.cap_poly[k]);
   float most[2] = {0.f, 0.f};   // of the squares
 #pragma unroll
   for (int q = 0; q < 2; ++q)
@@ -278,7 +278,7 @@ __device__ __forceinline__ void cap64(const TreeArgs& a, uint32_t s_addr, uint32
       float lo, hi;
       split(y, lo, hi);
       most[q] = fmaxf(fmaxf(most[q], lo), hi);
-      split(mul2(x, fma2(fma2(fma2(fma2(c[4], y, c[3]), y, c[2]), y, c[1]), y, c[0])), lo, hi);
+      split(mul2(x, fma2(fma2(fma2(c[3], y, c[2]), y, c[1]), y, c[0])), lo, hi);
       v[q][j] = __float_as_uint(lo);
       v[q][j + 1] = __float_as_uint(hi);
     }
@@ -317,9 +317,9 @@ __device__ __forceinline__ void shape32(const TreeArgs& a, const Row& me, const 
     if (!(vis & (1u << j))) v[j] = __float_as_uint(-CUDART_INF_F);
 }
 
-// Weights 2^(v sc + b + j step) of 32 scores: P in 16 words at p_addr, their
-// sum into ps.
-template <bool kStep>
+// Weights 2^(v sc + b + j step) of 32 scores (plain: 2^v): P in 16 words at
+// p_addr, their sum into ps.
+template <bool kStep, bool kPlain = false>
 __device__ __forceinline__ void weights32(const uint32_t (&v)[32], float sc, float b, float step, uint32_t p_addr,
                                           F2 (&ps)[2]) {
   uint32_t pw[16];
@@ -328,7 +328,7 @@ __device__ __forceinline__ void weights32(const uint32_t (&v)[32], float sc, flo
   for (int j = 0; j < 16; ++j) {
     const F2 at = kStep ? fma2(st2, f2((float)(2 * j), (float)(2 * j + 1)), b2) : b2;
     float x0, x1;
-    split(fma2(f2(v[2 * j], v[2 * j + 1]), sc2, at), x0, x1);
+    split(kPlain ? f2(v[2 * j], v[2 * j + 1]) : fma2(f2(v[2 * j], v[2 * j + 1]), sc2, at), x0, x1);
     const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
     pw[j] = pack_bf16(p0, p1);
     ps[j & 1] = add2(ps[j & 1], f2(p0, p1));
@@ -729,8 +729,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         float base = m_used == -CUDART_INF_F ? 0.f : -m_used;   // nothing seen yet: weights 0
         if (kSlopes && !special) base -= sp.slope2 * (float)((int64_t)ctx + me.depth - t0);
         const uint32_t p_col = tq + kColP + kPCols * b + 32 * half;
-        weights32<kSlopes>(sv[0], sc, base, step, p_col, ps);
-        weights32<kSlopes>(sv[1], sc, kSlopes ? fmaf(step, 32.f, base) : base, step, p_col + 16, ps);
+        if (fixed) {
+          weights32<false, true>(sv[0], 1.f, 0.f, 0.f, p_col, ps);
+          weights32<false, true>(sv[1], 1.f, 0.f, 0.f, p_col + 16, ps);
+        } else {
+          weights32<kSlopes>(sv[0], sc, base, step, p_col, ps);
+          weights32<kSlopes>(sv[1], sc, kSlopes ? fmaf(step, 32.f, base) : base, step, p_col + 16, ps);
+        }
         float l0, l1;
         split(add2(ps[0], ps[1]), l0, l1);
         l += l0 + l1;

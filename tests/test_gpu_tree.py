@@ -183,7 +183,7 @@ def test_long_requests_with_many_parts():
 
 @pytest.mark.parametrize("split", [False, True])
 def test_rows_that_see_nothing(split):
-    kw = dict(min_chunk_tokens=128, alpha=0) if split else dict(num_ctas=2)
+    kw = dict(min_chunk_tokens=128, alpha=0) if split else dict(num_ctas=1)
     c = Case(hq=4, hkv=1, lens=(300, 9), drafts=(300, 9), **kw)
     assert (c.dec.plan_info()["num_units"] > 0) == split
     c.mask[1] = 0
@@ -195,7 +195,7 @@ def test_rows_that_see_nothing(split):
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("split", [False, True])
 def test_what_is_masked_may_hold_anything(bad, split):
-    kw = dict(min_chunk_tokens=128, alpha=0) if split else dict(num_ctas=2)
+    kw = dict(min_chunk_tokens=128, alpha=0) if split else dict(num_ctas=1)
     c = Case(hq=8, hkv=2, lens=(400, 21), drafts=(150, 5), window=0, seed=9, **kw)
     used = set(c.indices.tolist())
     for page in range(c.pool):
