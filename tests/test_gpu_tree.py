@@ -232,6 +232,44 @@ def test_values_that_are_seen_keep_what_they_hold():
     assert (good - ref[keep]).abs().max() <= 1.1 * 2 ** -8 * (top + float(ref.abs().max()))
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(slopes=True), dict(cap=30.0), dict(window=120), dict(window=300, slopes=True)])
+def test_odd_values_beside_masked_ones(kw):
+    """A context token that all rows see, in a round with drafts and with a window's edge, shows; tokens
+    before the window of every row, or of some, do not reach those that do not see them."""
+    c = Case(hq=8, hkv=2, lens=(700, 90), drafts=(30, 5), seed=8, **kw)
+    ctx, before = 670, c.reference()
+    def v(t):
+        page, slot = divmod(t, 16)
+        return c.kv[int(c.indices[page]), 1, slot]
+    edges = (3, ctx - c.window + 1, ctx - c.window + 2)   # before all rows' windows, or before deep rows' only
+    keep = {t: v(t).clone() for t in (ctx - 3,) + edges * bool(c.window)}
+    v(ctx - 3)[1, 17] = float("nan")
+    v(ctx - 3)[0, 5] = -float("inf")
+    out, lse = c.run()
+    assert torch.isnan(out[:30, 4:, 17]).all() and (out[:30, :4, 5] == -float("inf")).all()
+    out = out.clone()
+    out[:30, 4:, 17] = out[:30, :4, 5] = 0
+    assert torch.isfinite(out).all()
+    before[0][:30, 4:, 17] = before[0][:30, :4, 5] = 0
+    top = 6.0
+    assert (out.double() - before[0]).abs().max() <= 1.1 * 2 ** -8 * (top + float(before[0].abs().max()))
+    v(ctx - 3)[:] = keep[ctx - 3]
+    if not c.window:
+        return
+    for t in edges:
+        v(t)[:, :] = float("nan")
+    see, _ = c.sees(0)
+    bad = torch.stack([see[:, t] for t in edges]).any(0)
+    assert bad.any() and not bad.all()
+    out, lse = c.run()
+    for i in range(30):
+        assert torch.isnan(out[i]).all() if bad[i] else torch.isfinite(out[i]).all()
+    good = torch.cat([~bad, torch.ones(5, dtype=torch.bool, device="cuda")])
+    for t, x in keep.items():
+        v(t)[:] = x
+    assert (out[good].double() - c.reference()[0][good]).abs().max() <= 1.1 * 2 ** -8 * (top + 4.0)
+
+
 def test_scores_that_rise_along_the_cache():
     """The base of the exponentials is raised in every round; the early tokens' weights vanish."""
     c = Case(hq=8, hkv=2, lens=(1500,), drafts=(6,), seed=4, num_ctas=2)
