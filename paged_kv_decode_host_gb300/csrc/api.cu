@@ -698,12 +698,14 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
     return PKD_E_INVALID_ARG;
   if (mask == nullptr) mask_words = 0;
   if (!causal && head[H_MAXQ] > 32 * (int64_t)mask_words) return PKD_E_INVALID_ARG;
-  if (ctx->info.batch > 0) {
-    if (q == nullptr || kv == nullptr || out == nullptr) return PKD_E_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 32) || !aligned(lse, 4) ||
-        !aligned(mask, 4) || !aligned(depths, 4) || !aligned(slopes, 4))
-      return PKD_E_INVALID_ARG;
-  }
+  const bool given = q != nullptr && kv != nullptr && out != nullptr;
+  if (ctx->info.batch > 0 && !given) return PKD_E_INVALID_ARG;
+  if (given && (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 32) || !aligned(lse, 4) ||
+                !aligned(mask, 4) || !aligned(depths, 4) || !aligned(slopes, 4)))
+    return PKD_E_INVALID_ARG;
+  // (also where this plan has no query tokens: a captured launch runs under
+  // later ones.  Without tensors it does for none that has any.)
+  if (!given) rows = 0;
   const pkd_config& c = ctx->cfg;
   const bool hnd = (c.flags & PKD_FLAG_HND) != 0;
   const double cap = score_cap, log2e = 1.4426950408889634;
@@ -748,7 +750,7 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
     }
   }
   a.wait_epoch = expect_epoch != 0 ? epoch_word(expect_epoch) : 0;
-  if (ctx->info.batch > 0) {
+  if (rows > 0) {
     const int st = kv_map_for(ctx, kv, &a.kv_map);
     if (st != PKD_OK) return st;
     if (encode_q_map(q, rows, c.num_qo_heads, c.num_kv_heads, &a.q_map) != cudaSuccess)

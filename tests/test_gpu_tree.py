@@ -354,6 +354,31 @@ def test_captured_step_under_later_plans():
     assert (o == 5).all() and c.dec.device_error() == 2
 
 
+def test_captured_under_an_empty_plan():
+    # a step captured before any request has query tokens replays under later plans that have
+    c = Case(lens=(60, 700), drafts=(5, 12), rows=20)
+    none = np.zeros(3, np.int32)
+    c.dec.plan(none, c.indptr, c.indices, c.last)
+    out, lse = torch.zeros_like(c.q), torch.zeros(20, 8, device="cuda")
+    bare, bare_lse = torch.zeros_like(c.q), torch.zeros(20, 8, device="cuda")
+    graph, graph2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(out=out, lse=lse)
+    with torch.cuda.graph(graph2):   # (no mask: does for no tree)
+        c.dec.run(c.q, c.kv, out=bare, lse=bare_lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (lse == 0).all() and c.dec.device_error() == 0
+    c.plan()
+    graph.replay()
+    c.check((out, lse))
+    assert (out[17:] == 0).all()
+    graph2.replay()
+    torch.cuda.synchronize()
+    assert (bare == 0).all() and (bare_lse == 0).all()
+    assert c.dec.device_error() == pkd.DEV_ERR_BOUNDS
+
+
 def test_pools_past_32_bits():
     """Pages whose elements lie past 2^31."""
     c = Case(hq=8, hkv=8, lens=(70, 40), drafts=(5, 3), window=60)
