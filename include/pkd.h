@@ -359,7 +359,7 @@ int pkd_plan_tree(pkd_ctx *ctx, const int32_t *q_indptr, const int32_t *indptr,
  *                as 0); NULL: d_i = i.  Only slopes and windows use them; NULL
  *                in a causal plan
  *   slopes     : device fp32 [Hq] or NULL
- *   scale      : finite, > 0; score_cap: 0 (none) or finite, > 0
+ *   scale      : 2^-96 to 2^96; score_cap: 0 (none), or 2^-30 to 2^96
  * expect_epoch, launches and stream order as pkd_run.  A call that the caller
  * captured replays under later plans that its rows and mask_words fit; under
  * another it does no work and ORs PKD_DEV_ERR_BOUNDS into the device error

@@ -10,6 +10,7 @@
 // overwritten.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -687,8 +688,8 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
                  const uint32_t* mask, int32_t mask_words, const int32_t* depths,
                  const float* slopes, float scale, float score_cap, uint64_t expect_epoch,
                  void* stream) {
-  if (ctx == nullptr || !ctx->tree || !std::isfinite(scale) || !(scale > 0.f) ||
-      !std::isfinite(score_cap) || !(score_cap >= 0.f) || mask_words < 0)
+  if (ctx == nullptr || !ctx->tree || !(scale >= 0x1p-96f && scale <= 0x1p96f) ||
+      !(score_cap == 0.f || (score_cap >= 0x1p-30f && score_cap <= 0x1p96f)) || mask_words < 0)
     return PKD_E_INVALID_ARG;
   if (ctx->epoch == 0) return PKD_E_NO_PLAN;
   if (expect_epoch != 0 && expect_epoch != ctx->epoch) return PKD_E_STALE_PLAN;
@@ -734,19 +735,19 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
   a.num_pages = c.num_pages;
   a.mask_words = mask_words;
   a.tokens = rows;
-  a.scale_log2 = (float)(score_cap > 0.f ? 2.0 * log2e * scale / cap : log2e * scale);
-  a.cap_log2 = (float)(log2e * cap);
-  if (score_cap > 0.f) {
-    // tanh(x) / x for |x| <= 0.4 as a polynomial of x^2, fitted for the least
-    // largest error (tanh within 7e-8, in fp32)
-    const double fit[4] = {0.9999999043749117, -0.33331390193300425, 0.13271438197786756,
-                           -0.04757281035736614};
-    const double x = scale / cap;
-    a.cap_bound = (float)(0.16 / (x * x));
+  const double x = score_cap > 0.f ? scale / cap : 0.0;
+  const bool has_cap = x >= 0x1p-120;   // (a larger cap is past fp32 products' reach)
+  a.scale_log2 = (float)(has_cap ? 2.0 * log2e * x : log2e * scale);
+  a.cap_log2 = has_cap ? (float)(log2e * cap) : 0.f;
+  if (has_cap) {
+    const double fit[4] = {kTanhFit0, kTanhFit1, kTanhFit2, kTanhFit3};
+    a.cap_bound = (float)std::min(kTanhFitTo / (x * x), 1e38);
     double c = log2e * cap * x;
     for (int k = 0; k < 4; ++k, c *= x * x) {
       a.cap_poly[k] = (float)(c * fit[k]);
-      if (!std::isfinite(a.cap_poly[k])) a.cap_bound = -1.f;   // (a scale past all reason: never)
+      // (huge or tiny caps: coefficients that fp32 does not hold; every score
+      // takes the way that scales the product first)
+      if (!std::isnormal(a.cap_poly[k])) a.cap_bound = -1.f;
     }
   }
   a.wait_epoch = expect_epoch != 0 ? epoch_word(expect_epoch) : 0;

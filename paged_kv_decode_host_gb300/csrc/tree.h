@@ -18,6 +18,12 @@ constexpr int kTreeRound = 128;      // tokens per round of the kernel; plans cu
 constexpr int kTreeAlpha = 512;
 constexpr int kTreeMinChunk = 128;
 
+// tanh(x) / x for |x| <= 0.4 as a polynomial of x^2, fitted for the least largest
+// error (tanh within 7e-8, in fp32).
+constexpr float kTanhFit0 = 0.9999999043749117f, kTanhFit1 = -0.33331390193300425f,
+                kTanhFit2 = 0.13271438197786756f, kTanhFit3 = -0.04757281035736614f;
+constexpr float kTanhFitTo = 0.16f;   // of x^2
+
 struct TreeArgs {
   const int32_t* sched;
   float* o_part;            // fp32 [slot][Hq][128]

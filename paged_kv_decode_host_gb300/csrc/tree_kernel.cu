@@ -25,9 +25,9 @@
 //    is not finite while some token that its row does not see has a value
 //    that is not is summed again over the tokens seen (redo_row);
 //  * rows that have seen nothing keep the base -inf and a sum of 0;
-//  * tanh(x) = 1 - 2 / (1 + e^2x): one exponential and one reciprocal, an
-//    absolute error of about 2^-22 (x cap); the hardware's tanh (2^-11) would
-//    show in the lse;
+//  * tanh(x) is a polynomial up to 0.4, within 2^-23 of itself; past that 1 - 2
+//    / (1 + e^2x), an exponential and a reciprocal, within about 2^-22; the
+//    hardware's tanh (2^-11) would show in the lse;
 //  * distances are subtracted as whole numbers before they meet the slope;
 //  * P is rounded to bf16 for the product (V's type, which the tensor cores
 //    want for both); the row's sum, and with it the lse, is that of the weights
@@ -114,8 +114,14 @@ __device__ __forceinline__ uint64_t visible(const Row& r, int t0, int te) {
   return vis & low_bits(te - t0);
 }
 
+// cap tanh(s scale ln 2 / 2), scale = 2 log2(e) scale_of_the_scores / cap: the
+// exponential's error is 2^-22 of the cap, so small ones take the polynomial.
 __device__ __forceinline__ float capped(float s, float scale, float cap) {
-  return fmaf(-2.f * cap, fast_rcp(1.f + fast_exp2(s * scale)), cap);
+  const float u = s * scale, x = u * (0.5f * kLn2), y = x * x;
+  const float small =
+      cap * x * fmaf(fmaf(fmaf(kTanhFit3, y, kTanhFit2), y, kTanhFit1), y, kTanhFit0);
+  const float any = fmaf(-2.f * cap, fast_rcp(1.f + fast_exp2(u)), cap);
+  return y <= kTanhFitTo ? small : any;   // (NaN: any, a NaN)
 }
 
 __device__ __forceinline__ int64_t token_offset(const TreeArgs& a, int first_page, int head, int t) {

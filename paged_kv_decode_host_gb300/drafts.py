@@ -340,9 +340,10 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
         depths: int32 [rows], a query token's position behind the request's
         first l - n tokens, by default its number among the request's; for
         windows and slopes only, not in causal plans.
-        scale: of q . k, by default 1 / sqrt(128).  score_cap > 0: scores become
-        score_cap * tanh(score / score_cap).  slopes: float32 [Hq], then -= slope
-        * (position of the query - position of the key).
+        scale: of q . k, by default 1 / sqrt(128).  score_cap (0: none; 2^-30 to
+        2^96): scores become score_cap * tanh(score / score_cap).  slopes:
+        float32 [Hq], then -= slope * (position of the query - position of the
+        key).
         A query that sees nothing gets 0 and an lse of -inf."""
         if stream is None and self.batch is not None:
             m = _step()

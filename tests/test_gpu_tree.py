@@ -29,9 +29,9 @@ def trees(drafts, seed):
 
 class Case:
     def __init__(self, hq=8, hkv=2, page=16, layout="NHD", lens=(37, 16, 5), drafts=(4, 3, 5), causal=False,
-                 window=0, cap=0.0, slopes=False, seed=0, rows=None, depths=True, magnitude=1.0, **kw):
+                 window=0, cap=0.0, slopes=False, seed=0, rows=None, depths=True, magnitude=1.0, scale=None, **kw):
         self.__dict__.update(hq=hq, hkv=hkv, page=page, layout=layout, lens=lens, drafts=drafts, causal=causal,
-                             window=window, cap=cap)
+                             window=window, cap=cap, scale=scale)
         self.indptr, self.indices, self.last, self.pool = table(lens, page, seed)
         self.q_indptr = np.concatenate([[0], np.cumsum(drafts)]).astype(np.int32)
         self.tokens = int(self.q_indptr[-1])
@@ -60,7 +60,7 @@ class Case:
 
     def run(self, **kw):
         return self.dec.run(self.q, self.kv, mask=self.mask, depths=self.depths, score_cap=self.cap,
-                            slopes=self.slopes, **kw)
+                            slopes=self.slopes, scale=self.scale, **kw)
 
     def sees(self, b):
         """[n, l] which tokens every query token of request b sees, and how far away they are."""
@@ -92,7 +92,7 @@ class Case:
             k, v = (kv[:, c].reshape(-1, self.hkv, D)[:length] for c in (0, 1))
             first = int(self.q_indptr[b])
             q = self.q[first:first + n].double().view(n, self.hkv, -1, D)
-            x = torch.einsum("nhgd,thd->hgnt", q, k) / math.sqrt(D)
+            x = torch.einsum("nhgd,thd->hgnt", q, k) * (D ** -0.5 if self.scale is None else self.scale)
             see, away = self.sees(b)
             if self.cap:
                 x = self.cap * torch.tanh(x / self.cap)
@@ -377,6 +377,29 @@ def test_captured_under_an_empty_plan():
     torch.cuda.synchronize()
     assert (bare == 0).all() and (bare_lse == 0).all()
     assert c.dec.device_error() == pkd.DEV_ERR_BOUNDS
+
+
+@pytest.mark.parametrize("cap,scale,magnitude", [
+    (1e6, None, 1.0), (1e6, None, 1e4), (1e4, 1e-2, 1.0), (1e4, 1e-3, 1e3), (2.0 ** 96, 1.0, 1.0),
+    (2.0 ** 96, 2.0 ** -30, 2.0 ** 30), (2.0 ** -30, None, 1.0), (1e-3, 1e6, 1.0), (50.0, None, 40.0)])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_caps_of_any_size(cap, scale, magnitude, slopes):
+    c = Case(lens=(300, 40), drafts=(9, 5), cap=cap, scale=scale, magnitude=magnitude, slopes=slopes)
+    out, lse = c.run()
+    ro, rl = c.reference()
+    assert c.dec.device_error() == 0
+    # a score is an fp32 sum of 128 products and 6 more roundings, the cap's polynomial within 2^-23
+    # of itself and past 0.4 of the cap within 2^-21 of the score (2^-22 of the cap at least); the
+    # largest score is under cap and under 128 * 36 * scale * magnitude.  Sums: 300 * 2^-24.
+    scale = 128 ** -0.5 if scale is None else scale
+    most = min(cap, scale * float(torch.einsum("nhd,nhd->nh", c.q.double(), c.q.double()).max()) ** 0.5
+               * float(c.kv[:, 0].double().pow(2).sum(-1).max()) ** 0.5)
+    off = most * (128 * 2.0 ** -24 + 2.0 ** -20) + 300 * 2.0 ** -24 + 2.0 ** -23 * float(rl.abs().max())
+    assert (lse.double() - rl).abs().max() <= off
+    # weights move by e^(2 off), P by 2^-8
+    top = float(c.kv.float().abs().max())
+    assert (out.double() - ro).abs().max() <= 2 * top * (math.exp(min(2 * off, 20.0)) - 1) + \
+        1.1 * 2 ** -8 * (top + float(ro.abs().max()))
 
 
 def test_pools_past_32_bits():
