@@ -229,8 +229,14 @@ struct Span {
   int ctx, te;            // tokens before the drafts; the item's end
   int reach;              // rounds that start below it need the window's mask in some row of the warp
   float slope2;           // log2(e) * the head's slope
+  bool steep;             // some row's slope is too steep for the estimate of 32 biased scores' largest
   bool valid;             // a query row
 };
+
+// The largest of 32 biased scores is taken as the largest score's plus the
+// largest bias: up to 31 slopes above what it is, so that weights of 2^-62 at
+// worst stand for 1.  (Models' slopes are at most 1, 1.44 in log2.)
+constexpr float kSteepest = 2.f;
 
 // The order of an item's nr rounds: with slopes from the newest tokens to the
 // oldest, whose biases only fall (the other way the base was raised, and O
@@ -679,6 +685,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       sp.reach = valid ? me.first_seen : -1;
       if (window > 0) sp.reach = __reduce_max_sync(kFull, sp.reach);
       sp.slope2 = kSlopes && valid ? a.slopes[hq] * kLog2e : 0.f;
+      sp.steep = kSlopes && __any_sync(kFull, fabsf(sp.slope2) > kSteepest);
       sp.valid = valid;
       float m_used = -CUDART_INF_F, l = 0.f;   // l: this warp's half of the row sum
       bool o_has = false;
@@ -693,8 +700,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         }
         tc_fence_after();
         const uint32_t s_col = kColS + kSCols * b + 64 * half;
-        // does some row of the warp not see all of its 64 columns?
-        const bool special = t0 + 64 > ctx || t0 < sp.reach || te - t0 < 64;
+        // does some row of the warp not see all of its 64 columns (or want each
+        // score's own bias)?
+        const bool special = t0 + 64 > ctx || t0 < sp.reach || te - t0 < 64 || (kSlopes && sp.steep);
         uint32_t sv[2][32];
         tmem_ld32(tq + s_col, sv[0]);
         tmem_ld32(tq + s_col + 32, sv[1]);

@@ -402,6 +402,27 @@ def test_caps_of_any_size(cap, scale, magnitude, slopes):
         1.1 * 2 ** -8 * (top + float(ro.abs().max()))
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_steep_slopes(sign):
+    # a bias that changes by more than fp32's exponents hold from one token of a round to the next
+    # ones, scores against it, and drafts that see none of the newest tokens
+    c = Case(hq=4, hkv=2, lens=(256 + 3, 700), drafts=(3, 5), slopes=True, magnitude=0.0)
+    c.slopes = sign * torch.tensor([8.0, 2.0, 1.5, 40.0], device="cuda")
+    c.mask[:3] = 0
+    c.q[..., 0] = 30.0
+    score = torch.where(torch.arange(16, device="cuda") == (0 if sign > 0 else 15), 40.0, -40.0)
+    c.kv[:, 0, :, :, 0] = score[None, :, None]
+    out, lse = c.run()
+    ro, rl = c.reference()
+    # scores of 106 and biases of up to 28,000: exponents off by 2^-23 of those
+    off = 4 * 2.0 ** -24 * (106 + 40 * 700) + 2.0 ** -23 * float(rl.abs().max())
+    assert c.dec.device_error() == 0 and torch.isfinite(lse).all()
+    assert (lse.double() - rl).abs().max() <= off
+    top = float(c.kv[:, 1].float().abs().max())
+    assert (out.double() - ro).abs().max() <= 2 * top * (math.exp(2 * off) - 1) + \
+        1.1 * 2 ** -8 * (top + float(ro.abs().max()))
+
+
 def test_pools_past_32_bits():
     """Pages whose elements lie past 2^31."""
     c = Case(hq=8, hkv=8, lens=(70, 40), drafts=(5, 3), window=60)
