@@ -130,31 +130,38 @@ __device__ __forceinline__ int64_t token_offset(const TreeArgs& a, int first_pag
   return page * a.page_elems + (t % a.page_size) * a.token_elems + head * a.head_elems;
 }
 
-// O of 32 dims (from dim0) of one row, times inv, summed over the tokens
-// that the row sees, if one that it does not see has a value that is not
-// finite in these dims; else left as it is.  (A look at V before each product
+// out of 32 dims (from dim0) of one row, summed over the tokens that the row
+// sees with weights 2^(s - total), if one that it does not see has a value that
+// is not finite in these dims, or (wide: weights far above 1, whose sums pass
+// fp32's range for values past 2^(110 - cap in log2)) if all that it sees are
+// finite; else left as it is.  (A look at V before each product
 // took 5 to 10 % of a step of short requests; this is for caches that hold such
 // values, and takes about 3 us a token: 16 requests of 8,192 tokens x 16 drafts 41 ms.)
 __device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uint16_t* q, int first_page,
-                                      int head, int tb, int te, int dim0, float base, float inv,
+                                      int head, int tb, int te, int dim0, float total, bool wide,
                                       float slope2, uint32_t (&o)[32]) {
   auto sees = [&](int t) { return (visible(r, t, te) & 1u) != 0; };
   auto values = [&](int t) {
     return reinterpret_cast<const uint4*>(a.kv + token_offset(a, first_page, head, t) + a.v_elems + dim0);
   };
-  bool poisoned = false;
-  auto look = [&](int t) {
-    if (sees(t)) return;
+  auto finite = [&](int t) {
     const uint4* v = values(t);
+    bool all = true;
     for (int d = 0; d < 4; ++d) {
       const uint4 x = v[d];
       for (uint32_t w : {x.x, x.y, x.z, x.w})
-        poisoned |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+        all &= (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
     }
+    return all;
   };
-  for (int t = tb; t < min(te, min(r.first_seen, r.ctx)) && !poisoned; ++t) look(t);
-  for (int t = max(tb, r.ctx); t < te && !poisoned; ++t) look(t);
-  if (!poisoned) return;
+  bool again = false;   // a token that is not seen has a value that is not finite
+  for (int t = tb; t < min(te, min(r.first_seen, r.ctx)) && !again; ++t) again = !sees(t) && !finite(t);
+  for (int t = max(tb, r.ctx); t < te && !again; ++t) again = !sees(t) && !finite(t);
+  if (!again && wide) {
+    again = true;
+    for (int t = tb; t < te && again; ++t) again = !sees(t) || finite(t);
+  }
+  if (!again) return;
   float acc[32];
 #pragma unroll
   for (int d = 0; d < 32; ++d) acc[d] = 0.f;
@@ -176,7 +183,7 @@ __device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uin
     s = a.cap_log2 != 0.f ? capped(s, a.scale_log2, a.cap_log2) : s * a.scale_log2;
     const int64_t away = t < r.ctx ? (int64_t)r.ctx + r.depth - t : (int64_t)r.depth - depth_of(r, t - r.ctx);
     s = fmaf(-slope2, (float)away, s);
-    const float p = fast_exp2(s - base);
+    const float p = fast_exp2(s - total);
     const uint4* v = values(t);
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
@@ -190,7 +197,7 @@ __device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uin
     }
   }
 #pragma unroll
-  for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(acc[d] * inv);
+  for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(acc[d]);
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -821,8 +828,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           uint32_t again[32];   // (only this rare case needs the values in memory)
 #pragma unroll
           for (int j = 0; j < 32; ++j) again[j] = lt == 0.f ? 0u : o[j];
-          if (lt != 0.f)
-            redo_row(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used, inv, sp.slope2, again);
+          if (lt > 0.f)   // (a NaN: the scores')
+            redo_row(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used + log2f(lt),
+                     kCap && !kSlopes && a.cap_log2 <= kFixedBase, sp.slope2, again);
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = again[j];
         }

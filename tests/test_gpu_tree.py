@@ -423,6 +423,22 @@ def test_steep_slopes(sign):
         1.1 * 2 ** -8 * (top + float(ro.abs().max()))
 
 
+@pytest.mark.parametrize("lens,drafts", [((300, 40), (9, 5)), ((3000,), (4,))])
+def test_large_values_under_a_cap(lens, drafts):
+    # scores at the cap and values near bf16's largest: a weighted mean of them is finite
+    c = Case(lens=lens, drafts=drafts, cap=60.0, magnitude=60.0, seed=3)
+    c.kv[:, 1] *= 2.0 ** 100
+    out, lse = c.run()
+    ro, rl = c.reference()
+    assert c.dec.device_error() == 0 and torch.isfinite(out.float()).all()
+    # scores off by 60 * (128 * 2^-24 + 2^-20): weights by 2 e-3 of themselves at most; P by 2^-8
+    off = 60.0 * (128 * 2.0 ** -24 + 2.0 ** -20) + 3000 * 2.0 ** -24
+    top = float(c.kv[:, 1].float().abs().max())
+    assert (lse.double() - rl).abs().max() <= off
+    assert (out.double() - ro).abs().max() <= 2 * top * (math.exp(2 * off) - 1) + \
+        1.1 * 2 ** -8 * (top + float(ro.abs().max()))
+
+
 def test_pools_past_32_bits():
     """Pages whose elements lie past 2^31."""
     c = Case(hq=8, hkv=8, lens=(70, 40), drafts=(5, 3), window=60)
