@@ -215,6 +215,7 @@ int kv_map_for(pkd_ctx* ctx, const void* kv, CUtensorMap* out, CUtensorMap* out_
       encode_latent_map(kv, c.num_pages, c.page_size, 1, &e.map_dense) != cudaSuccess)
     return PKD_E_CUDA;
   if ((ctx->latent ? encode_latent_map(kv, c.num_pages, c.page_size, 0, &e.map)
+       : ctx->tree ? encode_tree_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads, hnd, &e.map)
                         : encode_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads,
                                         ctx->kind.fp8, hnd, ctx->kind.dense, &e.map)) !=
       cudaSuccess)
@@ -729,6 +730,9 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
   a.head_elems = hnd ? (int64_t)kHeadDim * c.page_size : kHeadDim;
   a.v_elems = (int64_t)kHeadDim * c.num_kv_heads * c.page_size;
   a.page_elems = 2 * a.v_elems;
+  // (the map's third and fourth coordinates, in halves and groups of 8 tokens)
+  a.head_half = hnd ? 0 : 2;
+  a.head_group = hnd ? c.page_size / 8 : 0;
   a.hq = c.num_qo_heads;
   a.hkv = c.num_kv_heads;
   a.page_size = c.page_size;

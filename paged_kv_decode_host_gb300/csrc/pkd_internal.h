@@ -256,6 +256,11 @@ cudaError_t launch_cascade(const DecodeKind& k, const CascadeArgs& a, int grid, 
 // kernel, which lays the halves of 64 tokens out as two 8 KB matrices).
 cudaError_t encode_kv_map(const void* kv, int32_t num_pages, int32_t page_size, int32_t hkv,
                           bool fp8, bool hnd, bool head_half_box, CUtensorMap* map);
+// The tree kernel's map of a bf16 cache: boxes of 16 tokens of one KV head as [2
+// groups of 8 tokens][half][8][128 bytes], so that both matrix products find a
+// fixed stride between groups (2 KB) and between halves (1 KB).
+cudaError_t encode_tree_kv_map(const void* kv, int32_t num_pages, int32_t page_size, int32_t hkv,
+                               bool hnd, CUtensorMap* map);
 // Encode the dense kernel's query map of q [batch][Hq][D] bf16.
 cudaError_t encode_q_map(const void* q, int32_t batch, int32_t hq, int32_t hkv,
                          CUtensorMap* map);

@@ -46,7 +46,8 @@ struct TreeArgs {
   // = x times this polynomial of x^2
   float cap_bound, cap_poly[4];
   int32_t wait_epoch;
-  CUtensorMap kv_map;       // 16-token boxes of one 128-byte half of a KV head
+  int32_t head_half, head_group;   // where a head starts in kv_map
+  CUtensorMap kv_map;       // boxes of 16 tokens of a KV head: [2 x 8 tokens][half][8][128 B]
   CUtensorMap q_map;        // boxes of a KV head's 128 query rows and one half
 };
 

@@ -53,6 +53,10 @@ static_assert(kTreeRows == kDenseRows && kTreeRound == kRoundTok, "the dense rol
 // Caps up to here (in units of log2) keep the base 0: weights within 2^-90 ..
 // 2^90, sums of 2^31 of them below 2^122.
 constexpr float kFixedBase = 90.f;
+// Staged K and V: tiles of 16 tokens, [2 x 8 tokens][half of the dims][8][128 B],
+// each one copy: a copy costs its warp 50 to 90 cycles, and two (one per half)
+// were what bounded rounds of wide trees (2,300 cycles: 1,400 of copies).
+constexpr int kTileBytes = 2 * kBoxBytes;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -461,6 +465,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     uint64_t* full = c ? sh->fullv : sh->fullk;
     uint64_t* empty = c ? sh->emptyv : sh->emptyk;
     uint8_t* ring = stages + (size_t)c * kTcStages * kKvBytes;
+    const int step_pages = kRoundTok / P, step_at = kRoundTok % P;
     const uint64_t first = l2_evict_first_policy(), normal = l2_evict_normal_policy();
     pdl_wait();   // q and the cache may come from the previous kernel
     int st = 0, nq = 0;
@@ -486,18 +491,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       __syncwarp();
       // (more than one row block reads these tokens: they may stay in L2)
       const uint64_t policy = entry[1] > tile_tokens ? normal : first;
-      // Lane 2 j + h (lanes 0-15) copies half h of the round's tile j (tb is a
-      // multiple of 16); the page ids of the round after are on their way.
-      const int j = lane >> 1, h = lane & 1;
+      // Lane j < 8 copies the round's tile j (tb is a multiple of 16); the page
+      // ids of the round after are on their way.  Where tile j of a round lies: page
+      // `at_page` of the request, token `at` of it, moved on by one round each time
+      // (a division takes as long as two copies).
       const int nr = rounds_of(tb, te), ntiles = (te - tb + 15) >> 4;
-      auto page_of = [&](int k) -> int {
-        const int tile = kRoundTiles * round_at<kSlopes>(k, nr) + j;
-        return k < nr && lane < 16 && tile < ntiles ? a.sched[a.off_pages + poff + (tb + 16 * tile) / P] : 0;
-      };
-      int next = page_of(0);
+      const int32_t* pages = a.sched + a.off_pages + poff;
+      const int j = lane & (kRoundTiles - 1);
+      int tile = kRoundTiles * round_at<kSlopes>(0, nr) + j;
+      int at_page = (tb + 16 * tile) / P, at = (tb + 16 * tile) % P;
+      int next = tile < ntiles ? pages[at_page] : 0, next_at = at;
       for (int k = 0; k < nr; ++k, ++st) {
         int page = next;
-        next = page_of(k + 1);
+        at = next_at;
+        if (k + 1 < nr) {
+          tile += kSlopes ? -kRoundTiles : kRoundTiles;
+          at_page += kSlopes ? -step_pages : step_pages;
+          next_at += kSlopes ? -step_at : step_at;
+          if (!kSlopes && next_at >= P) {
+            next_at -= P;
+            ++at_page;
+          }
+          if (kSlopes && next_at < 0) {
+            next_at += P;
+            --at_page;
+          }
+          next = tile < ntiles ? pages[at_page] : 0;
+        }
         if ((unsigned)page >= (unsigned)a.num_pages) {
           atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
           page = 0;
@@ -510,12 +530,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(2 * nbox * kBoxBytes));
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(nbox * kTileBytes));
         __syncwarp();
-        if (j < nbox)
-          tensor_copy_g2s(ring + (size_t)slot * kKvBytes + h * kHalfBytes + j * kBoxBytes,
-                          &a.kv_map, 0, (t + 16 * j) % P, h, head, 2 * page + c, &full[slot],
-                          policy);
+        if (lane < nbox)
+          tensor_copy_g2s(ring + (size_t)slot * kKvBytes + lane * kTileBytes, &a.kv_map, 0, 0,
+                          head * a.head_half, head * a.head_group + (at >> 3), 2 * page + c,
+                          &full[slot], policy);
       }
     }
     // drain: the last phase of every slot, and the last queries
@@ -555,7 +575,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           for (int kk = 0; kk < 8; ++kk)
             mma_ss(tmem + kColS + kSCols * b,
                    smem_desc(q0 + (kk >> 2) * (kQBytes / 2) + (kk & 3) * 32, 16, 1024),
-                   smem_desc(kbase + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024),
+                   smem_desc(kbase + (kk >> 2) * 1024 + (kk & 3) * 32, 16, 2048),
                    idesc_s, kk > 0);
           mma_commit(&sh->sfull[b]);
           mma_commit(&sh->emptyk[slot]);
@@ -594,11 +614,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           // slots past the range's end in the last tile: P is 0 there, but
           // 0 x NaN would poison O, so zero those V rows (both halves)
           const int v0 = n & 15;
-          uint8_t* tile = vbase + (nbox - 1) * kBoxBytes;
+          uint8_t* tile = vbase + (nbox - 1) * kTileBytes;
           for (int i = lane; i < 2 * (16 - v0) * 8; i += 32) {
             const int h = i / ((16 - v0) * 8), rem = i % ((16 - v0) * 8);
             const int row = v0 + rem / 8, chunk = rem % 8;
-            *reinterpret_cast<uint4*>(tile + h * kHalfBytes + row * 128 + chunk * 16) =
+            *reinterpret_cast<uint4*>(tile + (row >> 3) * 2048 + h * 1024 + (row & 7) * 128 + chunk * 16) =
                 make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -609,7 +629,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           const uint32_t vb = smem_u32(vbase);
           for (int j = 0; j < nbox; ++j)
             mma_ts(tmem + kColO, tmem + kColP + kPCols * b + 8 * j,
-                   smem_desc(vb + j * kBoxBytes, kHalfBytes, 1024), idesc_o, k > 0 || j > 0);
+                   smem_desc(vb + j * kTileBytes, 1024, 2048), idesc_o, k > 0 || j > 0);
           mma_commit(&sh->pfree[b]);
           mma_commit(&sh->emptyv[slot]);
         }
