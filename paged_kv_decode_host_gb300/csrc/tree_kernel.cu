@@ -71,6 +71,13 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
@@ -465,6 +472,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     uint64_t* full = c ? sh->fullv : sh->fullk;
     uint64_t* empty = c ? sh->emptyv : sh->emptyk;
     uint8_t* ring = stages + (size_t)c * kTcStages * kKvBytes;
+    const bool me = elect_one();
     const int step_pages = kRoundTok / P, step_at = kRoundTok % P;
     const uint64_t first = l2_evict_first_policy(), normal = l2_evict_normal_policy();
     pdl_wait();   // q and the cache may come from the previous kernel
@@ -481,9 +489,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         ok = false;
         break;
       }
-      if (c == 0 && lane == 0) {
+      if (c == 0) ++nq;
+      if (c == 0 && me) {
         const int row0 = entry[0] + item[5];
-        ++nq;
         mbar_arrive_expect_tx(&sh->qfull, (uint32_t)kQBytes);
         for (int h = 0; h < 2; ++h)
           tensor_copy_g2s(sQ + h * (kQBytes / 2), &a.q_map, 0, h, 0, head, row0, &sh->qfull, first);
@@ -530,12 +538,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(nbox * kTileBytes));
+        const int group = head * a.head_group + (at >> 3), row = 2 * page + c;
+        int groups[kRoundTiles], pages_of[kRoundTiles];
+#pragma unroll
+        for (int u = 0; u < kRoundTiles; ++u) {
+          groups[u] = __shfl_sync(kFull, group, u);
+          pages_of[u] = __shfl_sync(kFull, row, u);
+        }
+        if (me) {
+          mbar_arrive_expect_tx(&full[slot], (uint32_t)(nbox * kTileBytes));
+#pragma unroll
+          for (int u = 0; u < kRoundTiles; ++u)
+            if (u < nbox)
+              tensor_copy_g2s(ring + (size_t)slot * kKvBytes + u * kTileBytes, &a.kv_map, 0, 0,
+                              head * a.head_half, groups[u], pages_of[u], &full[slot], policy);
+        }
         __syncwarp();
-        if (lane < nbox)
-          tensor_copy_g2s(ring + (size_t)slot * kKvBytes + lane * kTileBytes, &a.kv_map, 0, 0,
-                          head * a.head_half, head * a.head_group + (at >> 3), 2 * page + c,
-                          &full[slot], policy);
       }
     }
     // drain: the last phase of every slot, and the last queries
@@ -548,7 +566,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     }
   } else if (warp == kWarpS) {
     // ------------------------------------------- S = Q K^T (lane 0 issues)
-    const uint32_t q0 = smem_u32(sQ), st0 = smem_u32(stages);
+    const bool me = elect_one();
+    const uint64_t q0 = smem_desc(smem_u32(sQ), 16, 1024), k0 = smem_desc(smem_u32(stages), 16, 2048);
     int r = 0;
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
@@ -568,15 +587,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           break;
         }
         const int n = min(kRoundTok, te - (tb + round_at<kSlopes>(k, nr) * kRoundTok));
-        if (lane == 0) {
+        const uint32_t idesc_s = mma_idesc(kDenseRows, 16 * ((n + 15) >> 4), 0);
+        if (me) {
           tc_fence_after();
-          const uint32_t idesc_s = mma_idesc(kDenseRows, 16 * ((n + 15) >> 4), 0);
-          const uint32_t kbase = st0 + (uint32_t)(slot * kKvBytes);
+          const uint64_t ks = k0 + (uint64_t)(slot * (kKvBytes >> 4));
+#pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ss(tmem + kColS + kSCols * b,
-                   smem_desc(q0 + (kk >> 2) * (kQBytes / 2) + (kk & 3) * 32, 16, 1024),
-                   smem_desc(kbase + (kk >> 2) * 1024 + (kk & 3) * 32, 16, 2048),
-                   idesc_s, kk > 0);
+            mma_ss(tmem + kColS + kSCols * b, q0 + (uint64_t)((kk >> 2) * (kQBytes / 2 >> 4) + (kk & 3) * 2),
+                   ks + (uint64_t)((kk >> 2) * (1024 >> 4) + (kk & 3) * 2), idesc_s, kk > 0);
           mma_commit(&sh->sfull[b]);
           mma_commit(&sh->emptyk[slot]);
           if (k == nr - 1) mma_commit(&sh->qfree);   // the item's last score MMA
@@ -584,14 +602,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         __syncwarp();
       }
     }
-    if (lane == 0) {
+    if (me) {
       mma_commit(&sh->fin);
       if (!mbar_wait(&sh->fin, 0, nullptr)) atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
     }
     __syncwarp();
   } else if (warp == kWarpPV) {
     // --------------------------------------------- O += P V (lane 0 issues)
+    const bool me = elect_one();
     const uint32_t idesc_o = mma_idesc(kDenseRows, kHeadDim, 1);
+    const uint64_t v0 = smem_desc(smem_u32(stages) + kTcStages * kKvBytes, 1024, 2048);
     int r = 0;
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
@@ -613,30 +633,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         if (n & 15) {
           // slots past the range's end in the last tile: P is 0 there, but
           // 0 x NaN would poison O, so zero those V rows (both halves)
-          const int v0 = n & 15;
+          const int past = n & 15;
           uint8_t* tile = vbase + (nbox - 1) * kTileBytes;
-          for (int i = lane; i < 2 * (16 - v0) * 8; i += 32) {
-            const int h = i / ((16 - v0) * 8), rem = i % ((16 - v0) * 8);
-            const int row = v0 + rem / 8, chunk = rem % 8;
+          for (int i = lane; i < 2 * (16 - past) * 8; i += 32) {
+            const int h = i / ((16 - past) * 8), rem = i % ((16 - past) * 8);
+            const int row = past + rem / 8, chunk = rem % 8;
             *reinterpret_cast<uint4*>(tile + (row >> 3) * 2048 + h * 1024 + (row & 7) * 128 + chunk * 16) =
                 make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0) {
+        if (me) {
           tc_fence_after();
-          const uint32_t vb = smem_u32(vbase);
-          for (int j = 0; j < nbox; ++j)
-            mma_ts(tmem + kColO, tmem + kColP + kPCols * b + 8 * j,
-                   smem_desc(vb + j * kTileBytes, 1024, 2048), idesc_o, k > 0 || j > 0);
+          const uint64_t vs = v0 + (uint64_t)(slot * (kKvBytes >> 4));
+#pragma unroll
+          for (int j = 0; j < kRoundTiles; ++j)
+            if (j < nbox)
+              mma_ts(tmem + kColO, tmem + kColP + kPCols * b + 8 * j, vs + (uint64_t)(j * (kTileBytes >> 4)),
+                     idesc_o, k > 0 || j > 0);
           mma_commit(&sh->pfree[b]);
           mma_commit(&sh->emptyv[slot]);
         }
         __syncwarp();
       }
     }
-    if (lane == 0) {
+    if (me) {
       mma_commit(&sh->fin);
       if (!mbar_wait(&sh->fin, 0, nullptr)) atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
     }
