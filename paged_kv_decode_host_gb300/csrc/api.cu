@@ -764,7 +764,7 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaStreamCaptureStatus cap_status = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(s, &cap_status) != cudaSuccess) return PKD_E_CUDA;
-  if (launch_tree(a, ctx->n_cta, s) != cudaSuccess) return PKD_E_CUDA;
+  if (launch_tree(a, ctx->n_cta, ctx->info.chunk_tokens, s) != cudaSuccess) return PKD_E_CUDA;
   // a captured launch must do for later plans, whose splits are not known yet
   if (ctx->info.num_units == 0 && cap_status == cudaStreamCaptureStatusNone) return PKD_OK;
   MergeArgs m{};

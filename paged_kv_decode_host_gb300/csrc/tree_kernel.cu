@@ -39,6 +39,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "plan_layout.h"
 #include "prefix_tc_body.cuh"
 #include "tree.h"
@@ -76,6 +78,20 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                : "=r"(p));
   return p != 0;
+}
+
+// tc_wait whose first tries are the whole warp's, with a vote at once: a branch
+// that the compiler knows to be uniform, and no look at the clock.
+__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err,
+                                       int lane) {
+  return tc_wait(bar, parity, abort_flag, err, lane);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err,
+                                          int lane) {
+#pragma unroll 1
+  for (int n = 0; n < 64; ++n)
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  return slow_wait(bar, parity, abort_flag, err, lane);
 }
 
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
@@ -394,13 +410,24 @@ __device__ __forceinline__ void weights32(const uint32_t (&v)[32], float sc, flo
   tmem_st16(p_addr, pw);
 }
 
+// How the softmax warps share the rounds.  Where a CTA has many: four warps take
+// the even ones, four the odd ones, so that the two of a scheduler are at
+// different places and one's exponentials run beside the other's copies and waits
+// (16 x 61 drafts of 64 heads 133 -> 124 us, capped pieces of prompts 128 -> 118).
+// Where it has few (kHalves): all eight take every round, a half of its columns
+// each, which is over sooner (a request of one round a CTA 9.7 -> 9.1 us).  With
+// slopes always so: the base moves on with every round of a start (39.5 -> 35.6).
+constexpr int kStreamRounds = 4;
+
 struct TreeSmem {
+  float base[kTreeRows];      // a row's exponent base, as the last round left it
   float swap[2][2][kTreeRows];   // exchanges of the warps of a quadrant: place, half, row
+  uint64_t ready[2][4];       // base written by the stream's warp of a quadrant
 };
 constexpr int kSmemBytes = kQBytes + kTcStages * kStageBytes + (int)sizeof(TcSmem) + (int)sizeof(TreeSmem);
 static_assert(kSmemBytes <= 227 * 1024 && sizeof(TcSmem) % 4 == 0, "dynamic shared memory of one CTA");
 
-template <bool kCap, bool kSlopes>
+template <bool kCap, bool kSlopes, bool kHalves>
 __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
@@ -437,9 +464,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     mbar_init(&sh->qfree, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->sfull[b], 1);
-      mbar_init(&sh->sfree[b], kSoftmaxWarps);
-      mbar_init(&sh->pfull[b], kSoftmaxWarps);
+      mbar_init(&sh->sfree[b], kHalves ? kSoftmaxWarps : kSoftmaxWarps / 2);
+      mbar_init(&sh->pfull[b], kHalves ? kSoftmaxWarps : kSoftmaxWarps / 2);
       mbar_init(&sh->pfree[b], 1);
+      for (int q = 0; q < 4; ++q) mbar_init(&more->ready[b][q], 1);
     }
     mbar_init(&sh->ofree, kSoftmaxWarps);
     mbar_init(&sh->fin, 2);
@@ -485,7 +513,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       const int poff = entry[3];
       // the item's queries (the previous item's score MMAs must be done)
       if (c == 0 && it > it0 &&
-          !tc_wait(&sh->qfree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane)) {
+          !warp_wait(&sh->qfree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane)) {
         ok = false;
         break;
       }
@@ -534,7 +562,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         const int nbox = (min(kRoundTok, te - t) + 15) >> 4;
         const int slot = st % kTcStages;
         const uint32_t round = (uint32_t)(st / kTcStages);
-        if (round > 0 && !tc_wait(&empty[slot], (round - 1) & 1u, abort_flag, a.err, lane)) {
+        if (round > 0 && !warp_wait(&empty[slot], (round - 1) & 1u, abort_flag, a.err, lane)) {
           ok = false;
           break;
         }
@@ -574,15 +602,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
       const int tb = item[1], te = item[2];
       const int nr = rounds_of(tb, te);
-      if (!tc_wait(&sh->qfull, (uint32_t)((it - it0) & 1), abort_flag, a.err, lane)) {
+      if (!warp_wait(&sh->qfull, (uint32_t)((it - it0) & 1), abort_flag, a.err, lane)) {
         ok = false;
         break;
       }
       for (int k = 0; k < nr; ++k, ++r) {
         const int slot = r % kTcStages, b = r & 1;
-        if (!tc_wait(&sh->fullk[slot], (uint32_t)((r / kTcStages) & 1), abort_flag, a.err, lane) ||
+        // (the wait that is over first, first: one that is over still takes its time)
+        if (!warp_wait(&sh->fullk[slot], (uint32_t)((r / kTcStages) & 1), abort_flag, a.err, lane) ||
             (r >= 2 &&
-             !tc_wait(&sh->sfree[b], (uint32_t)(((r >> 1) - 1) & 1), abort_flag, a.err, lane))) {
+             !warp_wait(&sh->sfree[b], (uint32_t)(((r >> 1) - 1) & 1), abort_flag, a.err, lane))) {
           ok = false;
           break;
         }
@@ -620,10 +649,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       const int nr = rounds_of(tb, te);
       for (int k = 0; k < nr; ++k, ++r) {
         const int slot = r % kTcStages, b = r & 1;
-        if (!tc_wait(&sh->pfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane) ||
-            !tc_wait(&sh->fullv[slot], (uint32_t)((r / kTcStages) & 1), abort_flag, a.err, lane) ||
+        if (!warp_wait(&sh->fullv[slot], (uint32_t)((r / kTcStages) & 1), abort_flag, a.err, lane) ||
             (k == 0 && it > it0 &&
-             !tc_wait(&sh->ofree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane))) {
+             !warp_wait(&sh->ofree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane))) {
           ok = false;
           break;
         }
@@ -643,6 +671,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           }
           fence_proxy_async_smem();
           __syncwarp();
+        }
+        if (!warp_wait(&sh->pfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
+          ok = false;
+          break;
         }
         if (me) {
           tc_fence_after();
@@ -665,17 +697,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     __syncwarp();
   } else {
     // ------------------------------------------------- softmax + epilogue
-    const int quad = warp & 3, half = warp >> 2;   // lane quadrant, score / O columns half
+    const int quad = warp & 3, stream = warp >> 2;   // lane quadrant; parity of its rounds
     const int row = quad * 32 + lane;               // tile row = tensor-memory lane
     const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);   // this quadrant's lanes
     const int window = a.sched[H_WINDOW];
     pdl_wait();   // outputs, mask and depths may belong to the previous kernel
     int rho = 0;
     uint32_t swaps = 0;   // exchanges with the partner warp so far
+    uint32_t seen = 0;    // bases that the partner warp has handed over in the items before
     bool ok = true;
     auto pv_wait = [&](int r) -> bool {
       if (r < 0) return true;
-      return tc_wait(&sh->pfree[r & 1], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane);
+      return warp_wait(&sh->pfree[r & 1], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane);
     };
     // One float per row with the partner warp of this quadrant, through shared
     // memory: two places in turn (the partner has read one before it comes to the
@@ -685,9 +718,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     // more (below): a partner that waits goes on, and stops at the flag.
     auto exchange = [&](float v, float* other) -> bool {
       if (*abort_flag) return false;
-      more->swap[swaps & 1u][half][row] = v;
+      more->swap[swaps & 1u][stream][row] = v;
       asm volatile("barrier.sync %0, 64;" ::"r"(1 + quad) : "memory");
-      *other = more->swap[swaps & 1u][half ^ 1][row];
+      *other = more->swap[swaps & 1u][stream ^ 1][row];
       ++swaps;
       return true;
     };
@@ -700,13 +733,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       const int nr = rounds_of(tb, te);
       const int r0 = rho;
       rho = r0 + nr;
+      // this warp's rounds k0, k0 + kBy, ... of the item
+      constexpr int kBy = kHalves ? 1 : 2;
+      const int k0 = kHalves ? 0 : (r0 ^ stream) & 1;
       if (quad * 32 >= n_tok * g) {
         // no row of this quadrant: keep the barriers' count, in their order
-        for (int r = r0; r < rho && ok; ++r) {
-          ok = tc_wait(&sh->sfull[r & 1], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane);
+        for (int r = r0 + k0; r < rho && ok; r += kBy) {
+          ok = warp_wait(&sh->sfull[r & 1], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane);
           if (!ok) break;
           if (lane == 0) mbar_arrive(&sh->sfree[r & 1]);
-          ok = r < 2 || pv_wait(r - 2);
+          ok = pv_wait(r - 2);
           if (ok && lane == 0) mbar_arrive(&sh->pfull[r & 1]);
         }
         ok = ok && pv_wait(rho - 2) && pv_wait(rho - 1);
@@ -736,97 +772,129 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       sp.slope2 = kSlopes && valid ? a.slopes[hq] * kLog2e : 0.f;
       sp.steep = kSlopes && __any_sync(kFull, fabsf(sp.slope2) > kSteepest);
       sp.valid = valid;
-      float m_used = -CUDART_INF_F, l = 0.f;   // l: this warp's half of the row sum
-      bool o_has = false;
-      for (int k = 0; k < nr && ok; ++k) {
-        const int r = r0 + k, b = r & 1;
-        const int t0 = tb + round_at<kSlopes>(k, nr) * kRoundTok + 64 * half;   // token of this warp's first column
-        // (P buffer b was read by the P.V MMAs of round r - 2)
-        if ((r >= 2 && !pv_wait(r - 2)) ||
-            !tc_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
+      // Capped scores lie between -cap and cap: with the base 0 no weight or sum
+      // leaves fp32's (and bf16's) range, and the largest need not be known.
+      const bool fixed = kCap && !kSlopes && a.cap_log2 <= kFixedBase;
+      // the row's base when this warp last saw it, and the sum of its weights under it
+      float m_used = fixed ? 0.f : -CUDART_INF_F, l = 0.f;
+      for (int k = k0; k < nr && ok; k += kBy) {
+        const int r = r0 + k, b = kHalves ? r & 1 : stream;
+        const uint32_t s_col = tq + kColS + kSCols * b, p_col = tq + kColP + kPCols * b;
+        if (!warp_wait(&sh->sfull[b], (uint32_t)((r >> 1) & 1), abort_flag, a.err, lane)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t s_col = kColS + kSCols * b + 64 * half;
-        // does some row of the warp not see all of its 64 columns (or want each
-        // score's own bias)?
-        const bool special = t0 + 64 > ctx || t0 < sp.reach || te - t0 < 64 || (kSlopes && sp.steep);
-        uint32_t sv[2][32];
-        tmem_ld32(tq + s_col, sv[0]);
-        tmem_ld32(tq + s_col + 32, sv[1]);
-        tmem_wait_ld();
-        float sc = a.scale_log2, step = 0.f, mx = -CUDART_INF_F;
-        if constexpr (kCap) {
-          cap64(a, tq + s_col, sv);
-          sc = 1.f;
-        }
-        if (special) {
-          shape32<kCap, kSlopes>(a, me, sp, t0, sv[0]);
-          shape32<kCap, kSlopes>(a, me, sp, t0 + 32, sv[1]);
-          if (kSlopes) sc = 1.f;
-        }
-        // Capped scores lie between -cap and cap: with the base 0 no weight or sum
-        // leaves fp32's (and bf16's) range, and the largest need not be known.
-        const bool fixed = kCap && !kSlopes && a.cap_log2 <= kFixedBase;
-        if (!fixed) {
-          if (kSlopes && !special) {
-            // the largest product of 32 and their largest bias bound their scores
+        // Halves: this warp's 64 columns, once.  Else 0-63 for their largest score,
+        // 64-127 for theirs and, once the base is known, their weights, then 0-63
+        // again for theirs: a lane's 128 scores do not fit its registers.  (A fixed
+        // base: 64-127, 0-63.)
+        const int last = kHalves ? 1 : 2;
+        float mx = -CUDART_INF_F;
+        F2 ps[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll 1
+        for (int pass = fixed || kHalves ? 1 : 0; pass <= last; ++pass) {
+          const int h = kHalves ? stream : pass & 1;
+          const int t0 = tb + round_at<kSlopes>(k, nr) * kRoundTok + 64 * h;   // token of the first column
+          // does some row of the warp not see all of the 64 columns (or want each
+          // score's own bias)?
+          const bool special = t0 + 64 > ctx || t0 < sp.reach || te - t0 < 64 || (kSlopes && sp.steep);
+          uint32_t sv[2][32];
+          tmem_ld32(s_col + 64 * h, sv[0]);
+          tmem_ld32(s_col + 64 * h + 32, sv[1]);
+          tmem_wait_ld();
+          float sc = a.scale_log2, step = 0.f;
+          if constexpr (kCap) {
+            cap64(a, s_col + 64 * h, sv);
+            sc = 1.f;
+          }
+          if (pass == last) {   // S is read: the buffer may be refilled
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->sfree[b]);
+          }
+          if (special) {
+            shape32<kCap, kSlopes>(a, me, sp, t0, sv[0]);
+            shape32<kCap, kSlopes>(a, me, sp, t0 + 32, sv[1]);
+            if (kSlopes) sc = 1.f;
+          } else if (kSlopes) {
             step = sp.slope2;
-            const float far = -step * (float)((int64_t)ctx + me.depth - t0);
-            for (int q = 0; q < 2; ++q)
-              mx = fmaxf(mx, fmaf(max32(sv[q], -CUDART_INF_F), sc, far + fmaxf(step * (32 * q), step * (32 * q + 31))));
-          } else {
-            mx = fmaxf(max32(sv[0], -CUDART_INF_F), max32(sv[1], -CUDART_INF_F)) * sc;   // (sc > 0)
           }
-          float m_other;
-          if (!exchange(mx, &m_other)) {
-            ok = false;
-            break;
+          const float far = kSlopes && !special ? -step * (float)((int64_t)ctx + me.depth - t0) : 0.f;
+          if (!fixed && pass < 2) {
+            if (kSlopes && !special) {
+              // the largest product of 32 and their largest bias bound their scores
+              for (int q = 0; q < 2; ++q)
+                mx = fmaxf(mx, fmaf(max32(sv[q], -CUDART_INF_F), sc, far + fmaxf(step * (32 * q), step * (32 * q + 31))));
+            } else {
+              mx = fmaxf(mx, fmaxf(max32(sv[0], -CUDART_INF_F), max32(sv[1], -CUDART_INF_F)) * sc);   // (sc > 0)
+            }
           }
-          mx = fmaxf(mx, m_other);
-        }
-        // this half of S is read (and exchanged): the buffer may be refilled
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->sfree[b]);
-        if (fixed) m_used = 0.f;
-        // the base is raised, and O rescaled, only past 2^8 of growth (per row;
-        // the waits and tensor-memory accesses are the whole warp's)
-        const bool need = !fixed && mx > m_used + kRescaleLog2;
-        if (!fixed && __any_sync(kFull, need)) {
-          const float alpha = need ? exp2f(m_used - mx) : 1.f;   // 0 while m_used = -inf
-          if (o_has) {
-            if (!pv_wait(r - 1)) {
+          if (pass == 0) continue;
+          if (pass == 1) {
+            // (P's buffer was read by the P.V products of round r - 2)
+            if (!pv_wait(r - 2)) {
               ok = false;
               break;
             }
-            tc_fence_after();
+            if (!fixed) {
+              // The base is raised, and O rescaled, only past 2^8 of growth (per row;
+              // the waits and tensor-memory accesses are the whole warp's).  Without
+              // halves it goes from round to round, that is, from stream to stream.
+              float m_old = m_used;
+              if (kHalves) {
+                float m_other;
+                if (!exchange(mx, &m_other)) {
+                  ok = false;
+                  break;
+                }
+                mx = fmaxf(mx, m_other);
+              } else if (k > 0) {
+                if (!warp_wait(&more->ready[stream ^ 1][quad], (seen + ((k - 1) >> 1)) & 1u, abort_flag, a.err, lane)) {
+                  ok = false;
+                  break;
+                }
+                m_old = more->base[row];
+              }
+              const bool need = mx > m_old + kRescaleLog2;
+              const float m_new = need ? mx : m_old;
+              if (!kHalves) {
+                more->base[row] = m_new;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&more->ready[stream][quad]);
+              }
+              if (m_new != m_used) l *= exp2f(m_used - m_new);   // (0 while m_used = -inf)
+              m_used = m_new;
+              if (k > 0 && __any_sync(kFull, need)) {
+                const float alpha = need ? exp2f(m_old - mx) : 1.f;
+                if (!pv_wait(r - 1)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
 #pragma unroll 1
-            for (int cb = 0; cb < 64; cb += 16) {
-              uint32_t o[16];
-              tmem_ld16(tq + kColO + 64 * half + cb, o);
-              tmem_wait_ld();
+                for (int cb = kHalves ? 64 * h : 0; cb < (kHalves ? 64 * h + 64 : kHeadDim); cb += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(tq + kColO + cb, o);
+                  tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st16(tq + kColO + 64 * half + cb, o);
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                  tmem_st16(tq + kColO + cb, o);
+                }
+                tmem_wait_st();
+              }
             }
-            tmem_wait_st();
           }
-          l *= alpha;
-          if (need) m_used = mx;
+          if (fixed) {
+            weights32<false, true>(sv[0], 1.f, 0.f, 0.f, p_col + 32 * h, ps);
+            weights32<false, true>(sv[1], 1.f, 0.f, 0.f, p_col + 32 * h + 16, ps);
+          } else {
+            const float base = (m_used == -CUDART_INF_F ? 0.f : -m_used) + far;   // nothing seen yet: weights 0
+            weights32<kSlopes>(sv[0], sc, base, step, p_col + 32 * h, ps);
+            weights32<kSlopes>(sv[1], sc, kSlopes ? fmaf(step, 32.f, base) : base, step, p_col + 32 * h + 16, ps);
+          }
         }
-        F2 ps[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-        float base = m_used == -CUDART_INF_F ? 0.f : -m_used;   // nothing seen yet: weights 0
-        if (kSlopes && !special) base -= sp.slope2 * (float)((int64_t)ctx + me.depth - t0);
-        const uint32_t p_col = tq + kColP + kPCols * b + 32 * half;
-        if (fixed) {
-          weights32<false, true>(sv[0], 1.f, 0.f, 0.f, p_col, ps);
-          weights32<false, true>(sv[1], 1.f, 0.f, 0.f, p_col + 16, ps);
-        } else {
-          weights32<kSlopes>(sv[0], sc, base, step, p_col, ps);
-          weights32<kSlopes>(sv[1], sc, kSlopes ? fmaf(step, 32.f, base) : base, step, p_col + 16, ps);
-        }
+        if (!ok) break;
         float l0, l1;
         split(add2(ps[0], ps[1]), l0, l1);
         l += l0 + l1;
@@ -834,9 +902,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->pfull[b]);
-        o_has = true;
       }
       if (!ok) break;
+      if (!kHalves && !fixed) seen += (uint32_t)((nr - (k0 ^ 1) + 1) >> 1);   // the partner's rounds
       // ---- epilogue: the item's P.V MMAs done (rounds in order; lag <= 1)
       const int rl = rho - 1;
       if (!pv_wait(rl - 1) || !pv_wait(rl)) {
@@ -844,18 +912,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         break;
       }
       tc_fence_after();
-      // the row sum of both halves, added in half order
-      float l_other;
+      // the row's base (it only rises) and its sum, of both warps' in their order
+      float m_other = m_used, l_other;
+      if (!kHalves && !exchange(m_used, &m_other)) {
+        ok = false;
+        break;
+      }
+      if (m_other > m_used) {
+        l *= exp2f(m_used - m_other);
+        m_used = m_other;
+      }
       if (!exchange(l, &l_other)) {
         ok = false;
         break;
       }
-      const float lt = half == 0 ? l + l_other : l_other + l;
+      const float lt = stream == 0 ? l + l_other : l_other + l;
       const int64_t q_row = (int64_t)(q_first + i0 + i) * a.hq + hq;
       const int64_t p_row = ((int64_t)dst + (int64_t)i * stride) * a.hq + hq;   // its partial state
       const float inv = lt == 0.f ? 0.f : 1.f / lt;
 #pragma unroll 1
-      for (int cb = 64 * half; cb < 64 * half + 64; cb += 32) {
+      for (int cb = 64 * stream; cb < 64 * stream + 64; cb += 32) {
         uint32_t o[32];
         tmem_ld32(tq + kColO + cb, o);
         tmem_wait_ld();
@@ -896,7 +972,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ofree);
-      if (valid && half == 0) {
+      if (valid && stream == 0) {
         const float lse = lt == 0.f ? -CUDART_INF_F : (m_used + log2f(lt)) * kLn2;
         if (dst >= 0)
           a.l_part[p_row] = lse;
@@ -917,12 +993,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
   }
 }
 
-const void* kernel_of(bool cap, bool slopes) {
-  if (cap)
-    return slopes ? reinterpret_cast<const void*>(&tree_kernel<true, true>)
-                  : reinterpret_cast<const void*>(&tree_kernel<true, false>);
-  return slopes ? reinterpret_cast<const void*>(&tree_kernel<false, true>)
-                : reinterpret_cast<const void*>(&tree_kernel<false, false>);
+const void* kernel_of(bool cap, bool slopes, bool halves) {
+  if (slopes)
+    return cap ? reinterpret_cast<const void*>(&tree_kernel<true, true, true>)
+               : reinterpret_cast<const void*>(&tree_kernel<false, true, true>);
+  if (halves)
+    return cap ? reinterpret_cast<const void*>(&tree_kernel<true, false, true>)
+               : reinterpret_cast<const void*>(&tree_kernel<false, false, true>);
+  return cap ? reinterpret_cast<const void*>(&tree_kernel<true, false, false>)
+             : reinterpret_cast<const void*>(&tree_kernel<false, false, false>);
 }
 
 }  // namespace
@@ -930,20 +1009,20 @@ const void* kernel_of(bool cap, bool slopes) {
 int tree_smem_bytes() { return kSmemBytes; }
 
 cudaError_t tree_prepare() {
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 8; ++k) {
     const cudaError_t e = cudaFuncSetAttribute(
-        kernel_of(k & 1, k & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem_bytes());
+        kernel_of(k & 1, k & 2, k & 4), cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem_bytes());
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 cudaError_t tree_occupancy(int* blocks_per_sm) {
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of(false, false),
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of(false, false, false),
                                                        kTcThreads, (size_t)tree_smem_bytes());
 }
 
-cudaError_t launch_tree(const TreeArgs& a, int grid, cudaStream_t stream) {
+cudaError_t launch_tree(const TreeArgs& a, int grid, int64_t most_tokens, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kTcThreads);
@@ -955,7 +1034,8 @@ cudaError_t launch_tree(const TreeArgs& a, int grid, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void* args[] = {const_cast<TreeArgs*>(&a)};
-  return cudaLaunchKernelExC(&cfg, kernel_of(a.cap_log2 != 0.f, a.slopes != nullptr), args);
+  return cudaLaunchKernelExC(
+      &cfg, kernel_of(a.cap_log2 != 0.f, a.slopes != nullptr, most_tokens < kStreamRounds * kTreeRound), args);
 }
 
 }  // namespace pkd
