@@ -40,46 +40,63 @@ struct RowBlock {
 // placed (the groups stay together), then the others in the requests' order
 // (longest first, all groups came to their short blocks, whose starts leave
 // gaps, at the same time: windows of 64 ragged requests 123.7 us, 118.3 so).
+//
+// Where L2 does not hold the tokens that blocks share, the blocks' staying
+// together is worth more than equal loads: then these blocks go in `pieces` of
+// equal length (the longest one's), none of them cut otherwise.
 struct Placer {
-  std::vector<int32_t> by_length, rest;
+  struct Unit {
+    int32_t block, begin;
+    int64_t len;
+  };
+  std::vector<Unit> units, rest;
   std::vector<std::pair<int64_t, int32_t>> load;   // a heap: least load, then least group
   std::vector<int64_t> room;
   std::vector<PlanPart> whole, cut, parts;
-
-  void order(const std::vector<int64_t>& lens) {
-    by_length.resize(lens.size());
-    for (size_t i = 0; i < lens.size(); ++i) by_length[i] = (int32_t)i;
-    std::stable_sort(by_length.begin(), by_length.end(),
-                     [&](int32_t x, int32_t y) { return lens[x] > lens[y]; });
-  }
   std::vector<char> shared;
-  bool place(const std::vector<int64_t>& lens, int64_t span, int64_t alpha, int64_t round,
-             int64_t floor_c, int32_t nv) {
+
+  // The blocks, those of a request's several in `pieces` each, longest first.
+  void divide(const std::vector<RowBlock>& blocks, const std::vector<int64_t>& lens, int64_t pieces,
+              int64_t round) {
+    units.clear();
+    for (size_t i = 0, end; i < blocks.size(); i = end) {
+      int64_t longest = 0;
+      for (end = i; end < blocks.size() && blocks[end].req == blocks[i].req; ++end)
+        longest = std::max(longest, lens[end]);
+      const int64_t by = shared[i] ? ceil_div(ceil_div(longest, pieces), round) * round : longest;
+      for (int64_t at = 0; at < longest; at += by)
+        for (size_t b = i; b < end; ++b)
+          if (at < lens[b]) units.push_back(Unit{(int32_t)b, (int32_t)at, std::min(by, lens[b] - at)});
+    }
+    std::stable_sort(units.begin(), units.end(), [](const Unit& x, const Unit& y) { return x.len > y.len; });
+  }
+  bool place(int64_t span, int64_t alpha, int64_t round, int64_t floor_c, int32_t nv, bool cuts) {
     load.clear();
     for (int32_t v = 0; v < nv; ++v) load.emplace_back(0, v);   // (a heap already)
     const auto later = std::greater<std::pair<int64_t, int32_t>>();
     whole.clear();
     cut.clear();
     rest.clear();
-    for (const int32_t i : by_length) {
-      if (load.front().first + lens[i] + alpha > span) {
-        rest.push_back(i);
+    for (const Unit& u : units) {
+      if (load.front().first + u.len + alpha > span) {
+        if (!cuts) return false;
+        rest.push_back(u);
         continue;
       }
       std::pop_heap(load.begin(), load.end(), later);
       std::pair<int64_t, int32_t>& to = load.back();
-      whole.push_back(PlanPart{i, 0, (int32_t)lens[i], to.second});
-      to.first += lens[i] + alpha;
+      whole.push_back(PlanPart{u.block, u.begin, (int32_t)(u.begin + u.len), to.second});
+      to.first += u.len + alpha;
       std::push_heap(load.begin(), load.end(), later);
     }
     room.assign((size_t)nv, span);
     for (const auto& l : load) room[l.second] -= l.first;
     int32_t v = 0;
-    for (const int32_t i : rest) {
-      int64_t pos = 0;
-      for (; pos < lens[i]; ++v) {
+    for (const Unit& u : rest) {
+      const int64_t end = u.begin + u.len;
+      for (int64_t pos = u.begin; pos < end; ++v) {
         if (v >= nv) return false;
-        const int64_t rem = lens[i] - pos, fits = (room[v] - alpha) / round * round;
+        const int64_t rem = end - pos, fits = (room[v] - alpha) / round * round;
         int64_t take = 0;
         if (rem + alpha <= room[v]) {
           take = rem;
@@ -90,10 +107,10 @@ struct Placer {
           take = std::min(fits, (rem - floor_c) / round * round);
           if (take < floor_c) take = 0;
         }
-        if (take > 0) cut.push_back(PlanPart{i, (int32_t)pos, (int32_t)(pos + take), v});
+        if (take > 0) cut.push_back(PlanPart{u.block, (int32_t)pos, (int32_t)(pos + take), v});
         pos += take;
         room[v] -= take + (take > 0 ? alpha : 0);
-        if (pos >= lens[i]) break;   // (this group may have room for the next one)
+        if (pos >= end) break;   // (this group may have room for the next one)
       }
     }
     parts = whole;
@@ -124,7 +141,7 @@ int plan_schedule_tree(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   thread_local std::vector<RowBlock> blocks;
   thread_local std::vector<int64_t> lens;
   thread_local std::vector<PlanPart> parts;
-  thread_local std::vector<int32_t> first_slot, n_chunks, chunk_of, order;
+  thread_local std::vector<int32_t> first_slot, n_chunks, chunk_of, by_place, order;
   blocks.clear();
   lens.clear();
   int64_t nnz = 0, total = 0;
@@ -165,26 +182,62 @@ int plan_schedule_tree(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   int64_t span =
       std::max(alpha + floor_c, ceil_div(total + alpha * (int64_t)blocks.size(), nv));
   thread_local Placer placer;
-  placer.order(lens);
   placer.shared.assign(blocks.size(), 0);
-  for (size_t i = 0; i < blocks.size(); ++i)
+  int64_t together = 0, distinct = 0;   // tokens of blocks that share them; those tokens
+  for (size_t i = 0; i < blocks.size(); ++i) {
     placer.shared[i] = q_indptr[blocks[i].req + 1] - q_indptr[blocks[i].req] > rows;
+    if (!placer.shared[i]) continue;
+    together += lens[i];
+    if (blocks[i].begin == 0) distinct += lens[i];
+  }
   const auto grow = [](int64_t s) { return s + std::max<int64_t>(kTreeRound, s / 64); };
+  const int64_t least = span;
   int64_t even = span;
   while (!cut_even(lens, even, alpha, kTreeRound, floor_c, nv, &parts)) even = grow(even);
-  while (span <= even && !placer.place(lens, span, alpha, kTreeRound, floor_c, nv)) span = grow(span);
-  if (span <= even)
+  placer.divide(blocks, lens, 1, kTreeRound);
+  while (span <= even && !placer.place(span, alpha, kTreeRound, floor_c, nv, true)) span = grow(span);
+  int64_t apart = together;   // of these tokens, those of blocks that do not stay together
+  if (span <= even) {
     parts = placer.parts;
-  else
+    apart = 0;
+    for (const Placer::Unit& u : placer.rest)
+      if (placer.shared[u.block]) apart += u.len;
+  } else {
     span = even;
+  }
+  if (2 * together > total && distinct * hkv * (2 * kHeadDim * 2) > kTreeSharedBytes) {
+    int64_t best = span + (int64_t)((double)span * kTreeSharedGain / 100 * apart / together);
+    int64_t several = 0, rows_of = 0;   // such blocks, their query tokens
+    for (size_t i = 0; i < blocks.size(); ++i)
+      if (placer.shared[i]) ++several, rows_of += blocks[i].tokens;
+    for (int64_t times = 1; times <= 6; ++times) {   // about so many for each group
+      const int64_t pieces = times * std::max<int64_t>(nv, several) / several;
+      const int64_t slots = pieces > 1 ? pieces * rows_of : 0;   // (blocks may have a piece less)
+      if (slots > L.max_slots) break;
+      placer.divide(blocks, lens, pieces, kTreeRound);
+      if ((int64_t)placer.units.size() * hkv > L.max_items) break;
+      int64_t s = least;
+      while (s < best && !placer.place(s, alpha, kTreeRound, floor_c, nv, false)) s = grow(s);
+      if (s >= best) continue;
+      best = span = s;
+      parts = placer.parts;
+    }
+  }
 
   // reduction map: the tokens of a block in several parts, blocks of most
   // parts first, a token's slots one after the other in part order
   const int32_t n_blocks = (int32_t)blocks.size();
   n_chunks.assign((size_t)n_blocks, 0);
   first_slot.assign((size_t)n_blocks, -1);
-  chunk_of.clear();   // (a block's parts stand in order)
-  for (const PlanPart& p : parts) chunk_of.push_back(n_chunks[p.req]++);
+  // (a block's slots in the order of its tokens, whatever groups have its parts)
+  chunk_of.assign(parts.size(), 0);
+  by_place.resize(parts.size());
+  for (size_t k = 0; k < parts.size(); ++k) by_place[k] = (int32_t)k;
+  std::sort(by_place.begin(), by_place.end(), [](int32_t x, int32_t y) {
+    return parts[x].req != parts[y].req ? parts[x].req < parts[y].req
+                                        : parts[x].tok_begin < parts[y].tok_begin;
+  });
+  for (const int32_t k : by_place) chunk_of[k] = n_chunks[parts[k].req]++;
   order.clear();
   for (int32_t i = 0; i < n_blocks; ++i)
     if (n_chunks[i] > 1) order.push_back(i);

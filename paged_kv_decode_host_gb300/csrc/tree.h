@@ -17,6 +17,13 @@ constexpr int kTreeRound = 128;      // tokens per round of the kernel; plans cu
 // 10.1, 10.5 and 10.2.
 constexpr int kTreeAlpha = 512;
 constexpr int kTreeMinChunk = 128;
+// Tokens that several row blocks read, in bytes, from which on L2 does not hold
+// them from one block to the next, and what it is worth, in percent of a plan's
+// span, that all such blocks stay together then.  Measured: 256 tokens behind
+// 100,000, 64 heads 900 -> 586 us, 32 heads 469 -> 304; 4 x 100 drafts behind
+// 30,000 302 -> 185; 2 x 200 behind 50,000 of 4 KV heads (184 MB) 224 as it is.
+constexpr int64_t kTreeSharedBytes = 192ll << 20;
+constexpr int kTreeSharedGain = 60;
 
 // tanh(x) / x for |x| <= 0.4 as a polynomial of x^2, fitted for the least largest
 // error (tanh within 7e-8, in fp32).

@@ -439,6 +439,15 @@ def test_large_values_under_a_cap(lens, drafts):
         1.1 * 2 ** -8 * (top + float(ro.abs().max()))
 
 
+@pytest.mark.parametrize("causal", [False, True])
+def test_blocks_in_pieces(causal):
+    # more than L2 holds, shared by a request's row blocks: cut alike, merged from many parts
+    c = Case(hq=8, hkv=1, page=64, lens=(400_000, 70), drafts=(40, 3), causal=causal)
+    info = c.dec.plan_info()
+    assert info["num_units"] == 40 and info["num_slots"] > 40 * 8
+    c.check()
+
+
 def test_pools_past_32_bits():
     """Pages whose elements lie past 2^31."""
     c = Case(hq=8, hkv=8, lens=(70, 40), drafts=(5, 3), window=60)

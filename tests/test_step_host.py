@@ -46,6 +46,54 @@ def test_configurations(lib):
         assert status(flags=pkd.FLAG_TREE | extra) == INVALID, extra
 
 
+def check_plan(cfg, hq, hkv, page, lens, drafts, causal, window):
+    batch, t = len(lens), table(lens, page)
+    q_indptr = np.concatenate([[0], np.cumsum(drafts)]).astype(np.int32)
+    w, info, off = pkd.plan_host_tree(cfg, q_indptr, *t, causal=causal, window=window)
+    s = pkd.decode_schedule(w, off, info)
+    rows = 128 // (hq // hkv)
+    assert info["batch"] == sum(drafts) and s["cta_indptr"][-1] == info["num_items"]
+    assert s["page_list"] == t[1].tolist()
+    at = (off[4] + (info["nnz"] + 3) // 4 * 4) - 0
+    entries = w[at:at + 4 * batch].reshape(batch, 4)
+    if batch:
+        assert entries.tolist() == [[int(q_indptr[b]), drafts[b], lens[b] - drafts[b], int(t[0][b])]
+                                    for b in range(batch)]
+    ranges, slots = {}, {}
+    for it, head in zip(s["items"], s["heads"]):
+        req, tb, te, dst, tokens, first, stride = it
+        block = first // rows
+        assert 0 <= req < batch and 0 <= head < hkv and tb < te <= lens[req] and tb % 16 == 0
+        assert first % rows == 0 and tokens == min(rows, drafts[req] - first) > 0
+        ranges.setdefault((req, block, head), []).append((tb, te, dst, stride))
+    units = {}
+    for u, (token, chunks) in enumerate(s["units"]):
+        assert s["merge_indptr"][u + 1] - s["merge_indptr"][u] == chunks
+        units[token] = (s["merge_indptr"][u], chunks)
+    assert (s["merge_indptr"][-1] if units else 0) == info["num_slots"]
+    for b, n in enumerate(drafts):
+        for block in range(-(-n // rows)):
+            ctx, r0, r1 = lens[b] - n, block * rows, min(n, block * rows + rows)
+            least = ctx + (r0 if causal else 0)
+            lo = max(0, least - window + 1) // 16 * 16 if window else 0
+            hi = ctx + r1 if causal else lens[b]
+            for head in range(hkv):
+                parts = sorted(ranges.pop((b, block, head)))
+                assert parts[0][0] == lo and parts[-1][1] == hi
+                assert all(x[1] == y[0] and (x[1] - lo) % 128 == 0 for x, y in zip(parts, parts[1:]))
+                for i in range(r0, r1):
+                    token = int(q_indptr[b]) + i
+                    if len(parts) == 1:
+                        assert parts[0][2] == -1 and token not in units
+                        continue
+                    first, chunks = units[token]
+                    assert chunks == len(parts)
+                    for k, (_, _, dst, stride) in enumerate(parts):
+                        assert stride == chunks and dst + (i - r0) * stride == first + k
+    assert not ranges
+    return s, info
+
+
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 1), (3, 3), (8, 2), (64, 8)])
 @pytest.mark.parametrize("ctas", [1, 3, 8, 152])
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (False, 33), (True, 33), (True, 1)])
@@ -59,48 +107,28 @@ def test_plans_cover_every_row_and_token_once(lib, hq, hkv, ctas, causal, window
         t = table(lens, 16)
         cfg = config(num_qo_heads=hq, num_kv_heads=hkv, num_ctas=ctas, max_batch=max(1, sum(drafts), batch),
                      max_num_pages=int(t[0][-1]), num_pages=2000, min_chunk_tokens=int(r.choice([1, 256])))
-        w, info, off = pkd.plan_host_tree(cfg, q_indptr, *t, causal=causal, window=window)
-        s = pkd.decode_schedule(w, off, info)
-        rows = 128 // (hq // hkv)
-        assert info["batch"] == sum(drafts) and s["cta_indptr"][-1] == info["num_items"]
-        assert s["page_list"] == t[1].tolist()
-        at = (off[4] + (info["nnz"] + 3) // 4 * 4) - 0
-        entries = w[at:at + 4 * batch].reshape(batch, 4)
-        if batch:
-            assert entries.tolist() == [[int(q_indptr[b]), drafts[b], lens[b] - drafts[b], int(t[0][b])]
-                                        for b in range(batch)]
-        ranges, slots = {}, {}
-        for it, head in zip(s["items"], s["heads"]):
-            req, tb, te, dst, tokens, first, stride = it
-            block = first // rows
-            assert 0 <= req < batch and 0 <= head < hkv and tb < te <= lens[req] and tb % 16 == 0
-            assert first % rows == 0 and tokens == min(rows, drafts[req] - first) > 0
-            ranges.setdefault((req, block, head), []).append((tb, te, dst, stride))
-        units = {}
-        for u, (token, chunks) in enumerate(s["units"]):
-            assert s["merge_indptr"][u + 1] - s["merge_indptr"][u] == chunks
-            units[token] = (s["merge_indptr"][u], chunks)
-        assert (s["merge_indptr"][-1] if units else 0) == info["num_slots"]
-        for b, n in enumerate(drafts):
-            for block in range(-(-n // rows)):
-                ctx, r0, r1 = lens[b] - n, block * rows, min(n, block * rows + rows)
-                least = ctx + (r0 if causal else 0)
-                lo = max(0, least - window + 1) // 16 * 16 if window else 0
-                hi = ctx + r1 if causal else lens[b]
-                for head in range(hkv):
-                    parts = sorted(ranges.pop((b, block, head)))
-                    assert parts[0][0] == lo and parts[-1][1] == hi
-                    assert all(x[1] == y[0] and (x[1] - lo) % 128 == 0 for x, y in zip(parts, parts[1:]))
-                    for i in range(r0, r1):
-                        token = int(q_indptr[b]) + i
-                        if len(parts) == 1:
-                            assert parts[0][2] == -1 and token not in units
-                            continue
-                        first, chunks = units[token]
-                        assert chunks == len(parts)
-                        for k, (_, _, dst, stride) in enumerate(parts):
-                            assert stride == chunks and dst + (i - r0) * stride == first + k
-        assert not ranges
+        check_plan(cfg, hq, hkv, 16, lens, drafts, causal, window)
+
+
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 15000)])
+def test_plans_that_keep_blocks_together(lib, causal, window):
+    """More tokens than L2 holds, shared by several row blocks: in pieces, all cut alike."""
+    page = 4096
+    for hq, hkv, lens, drafts in ((64, 8, [100_000], [256]), (32, 8, [100_000], [256]), (32, 8, [30_000] * 4, [100] * 4),
+                                  (32, 8, [60_000, 50_000, 3], [65, 70, 3]), (8, 1, [400_000, 500], [40, 1])):
+        cfg = config(num_qo_heads=hq, num_kv_heads=hkv, num_ctas=152, max_batch=sum(drafts), page_size=page,
+                     max_num_pages=200, num_pages=200)
+        s, info = check_plan(cfg, hq, hkv, page, lens, drafts, causal, window)
+        if not window and lens[0] > 16384:
+            cuts = {}
+            for req, tb, te, dst, tokens, first, stride in s["items"]:
+                if req == 0:
+                    cuts.setdefault(first, set()).add(tb)
+            assert len({frozenset(c) for c in cuts.values()}) == 1, "blocks of a request cut at different tokens"
+        # room for a plan with few tokens, too: no pieces that it cannot hold
+    tight = config(num_qo_heads=64, num_kv_heads=8, num_ctas=152, max_batch=256, page_size=page, max_num_pages=30,
+                   num_pages=30)
+    check_plan(tight, 64, 8, page, [100_000], [256], causal, window)
 
 
 def test_largest_plans_fit_their_slots(lib):
