@@ -360,10 +360,11 @@ int pkd_plan_tree(pkd_ctx *ctx, const int32_t *q_indptr, const int32_t *indptr,
  *                in a causal plan
  *   slopes     : device fp32 [Hq] or NULL
  *   scale      : 2^-96 to 2^96; score_cap: 0 (none), or 2^-30 to 2^96
- * expect_epoch, launches and stream order as pkd_run.  A call that the caller
- * captured replays under later plans that its rows and mask_words fit; under
- * another it does no work and ORs PKD_DEV_ERR_BOUNDS into the device error
- * word.  The same bits every run.
+ * expect_epoch, launches and stream order as pkd_run: the runs of a context
+ * share its workspace, so two of them, captured ones too, are ordered by a
+ * stream or an event.  A call that the caller captured replays under later
+ * plans that its rows and mask_words fit; under another it does no work and
+ * ORs PKD_DEV_ERR_BOUNDS into the device error word.  The same bits every run.
  * Errors: as pkd_run; INVALID_ARG also for rows or mask_words below the plan's
  * and a mask or depths given to a causal plan. */
 int pkd_run_tree(pkd_ctx *ctx, const void *q, int32_t rows, const void *kv, void *out, float *lse,

@@ -11,11 +11,13 @@
 //
 // A work item is one KV head of up to 128 / g query tokens of a request over a
 // range of its cached tokens: the 128 query rows of a tile share every key and
-// value, so both products run on the tensor cores as in the dense
-// shared-prefix role (prefix_tc_body.cuh, whose roles, rings and tensor-memory
-// map this kernel has: warp 8 copies queries and K, warp 10 V, warp 9 issues
-// S = Q K^T, warp 11 O += P V, warps 0-7 the softmax, two per lane quadrant
-// with 64 of a round's 128 columns each).  What differs:
+// value, so both products run on the tensor cores, in rounds of 128 tokens.  Per
+// CTA: warps 8 and 10 copy queries and K, and V, into rings of three rounds;
+// warp 9 issues S = Q K^T, two S buffers ahead of the softmax; warps 0-7 (two per
+// lane quadrant of tensor memory, a row per lane) turn S into P, in tensor memory;
+// warp 11 issues O += P V, whose accumulator stays there for the whole item.
+//  * S and P have two buffers each and O one: 512 columns of tensor memory.  Q
+//    (32 KB) and the rings (192 KB) fill the shared memory.
 //  * rounds that some row does not see whole (drafts, a window's edge, the
 //    range's end) get a 64-bit word per row of the columns that it sees, from
 //    the context's length, the window and 64 bits of the mask; other rounds
@@ -31,10 +33,21 @@
 //  * distances are subtracted as whole numbers before they meet the slope;
 //  * P is rounded to bf16 for the product (V's type, which the tensor cores
 //    want for both); the row's sum, and with it the lse, is that of the weights
-//    before it;
+//    before it.  Sums, bases and states between parts are fp32;
 //  * lane quadrants without a query row (fewer than 97 rows) only keep the
 //    barriers' count.
-// Every wait is bounded, as in the dense role.
+// What bounds it: with few rows per KV head memory (64 ragged requests up to 8,192
+// tokens x 16 drafts, 32 heads on 8: 1.06 GB in 160 us, 6.6 TB/s); with full tiles
+// the round, about 1,600 cycles for 1,024 of tensor products (16 requests x 61 drafts
+// of 64 heads: 155 GFLOP in 125 us, 1.24 PFLOP/s), in which the tensor cores wait for
+// the softmax; a capped score's polynomial adds 600.  On the way there: two copies
+// instead of one per 16 tokens 159 -> 141 us, a lone thread that forms descriptors
+// 500 cycles a round, waits that look at the clock at once 139 -> 131.  Tried and
+// slower: an O of its own for each stream of rounds; two tiles per item; weights
+// under the last base before the round's largest score is known (they mend too
+// often what they save); releasing S before its scores are capped.
+// Every wait is bounded, as in the dense shared-prefix role (prefix_tc_body.cuh),
+// whose instructions and barriers these are.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -825,7 +838,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
             if (kSlopes && !special) {
               // the largest product of 32 and their largest bias bound their scores
               for (int q = 0; q < 2; ++q)
-                mx = fmaxf(mx, fmaf(max32(sv[q], -CUDART_INF_F), sc, far + fmaxf(step * (32 * q), step * (32 * q + 31))));
+                mx = fmaxf(mx, fmaf(max32(sv[q], -CUDART_INF_F), sc,
+                                    far + fmaxf(step * (32 * q), step * (32 * q + 31))));
             } else {
               mx = fmaxf(mx, fmaxf(max32(sv[0], -CUDART_INF_F), max32(sv[1], -CUDART_INF_F)) * sc);   // (sc > 0)
             }
@@ -850,7 +864,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
                 }
                 mx = fmaxf(mx, m_other);
               } else if (k > 0) {
-                if (!warp_wait(&more->ready[stream ^ 1][quad], (seen + ((k - 1) >> 1)) & 1u, abort_flag, a.err, lane)) {
+                if (!warp_wait(&more->ready[stream ^ 1][quad], (seen + ((k - 1) >> 1)) & 1u, abort_flag,
+                               a.err, lane)) {
                   ok = false;
                   break;
                 }

@@ -269,7 +269,8 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
     the most query tokens of a plan (and requests).  bf16, layout NHD or HND,
     head_dim 128, page size a multiple of 16.  Capture a step with
     ``torch.cuda.graph`` around its runs: it replays under later plans of no
-    more query tokens than q has rows.
+    more query tokens than q has rows.  The runs of one context share its
+    workspace: order them, captured ones too, by a stream or an event.
     """
 
     def __init__(self, num_qo_heads, num_kv_heads, head_dim, page_size, *, max_tokens,
