@@ -68,6 +68,10 @@ static_assert(kTreeRows == kDenseRows && kTreeRound == kRoundTok, "the dense rol
 // Caps up to here (in units of log2) keep the base 0: weights within 2^-90 ..
 // 2^90, sums of 2^31 of them below 2^122.
 constexpr float kFixedBase = 90.f;
+// Tokens that every row of the warp sees, from which on a base of 0 costs no
+// precision (errors against 64 bits: 1.41 times those of a plain fp32 form from
+// some hundred tokens on, with either base; 1.51 for 6 to 15 with 0).
+constexpr int kFixedTokens = 384;
 // Staged K and V: tiles of 16 tokens, [2 x 8 tokens][half of the dims][8][128 B],
 // each one copy: a copy costs its warp 50 to 90 cycles, and two (one per half)
 // were what bounded rounds of wide trees (2,300 cycles: 1,400 of copies).
@@ -786,8 +790,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       sp.steep = kSlopes && __any_sync(kFull, fabsf(sp.slope2) > kSteepest);
       sp.valid = valid;
       // Capped scores lie between -cap and cap: with the base 0 no weight or sum
-      // leaves fp32's (and bf16's) range, and the largest need not be known.
-      const bool fixed = kCap && !kSlopes && a.cap_log2 <= kFixedBase;
+      // leaves fp32's (and bf16's) range, and the largest need not be known.  Not
+      // for rows that see few tokens: with their largest as the base the weights
+      // that count most are powers of 2, or near them, and lose little as P.
+      const bool fixed = kCap && !kSlopes && a.cap_log2 <= kFixedBase &&
+                         min(te, ctx) - max(tb, sp.reach) >= kFixedTokens;
       // the row's base when this warp last saw it, and the sum of its weights under it
       float m_used = fixed ? 0.f : -CUDART_INF_F, l = 0.f;
       for (int k = k0; k < nr && ok; k += kBy) {
@@ -963,7 +970,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           for (int j = 0; j < 32; ++j) again[j] = lt == 0.f ? 0u : o[j];
           if (lt > 0.f)   // (a NaN: the scores')
             redo_row(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used + log2f(lt),
-                     kCap && !kSlopes && a.cap_log2 <= kFixedBase, sp.slope2, again);
+                     fixed, sp.slope2, again);
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = again[j];
         }

@@ -448,6 +448,18 @@ def test_blocks_in_pieces(causal):
     c.check()
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(cap=50.0), dict(slopes=True), dict(cap=50.0, slopes=True),
+                                dict(cap=30.0, scale=1.0)])
+def test_rows_of_one_token_are_its_value(kw):
+    # one weight, 1: no rounding but the value's own
+    c = Case(lens=(40, 700, 2), drafts=(4, 90, 1), window=1, causal=True, **kw)
+    out, lse = c.run()
+    mine = [torch.from_numpy(c.indices[c.indptr[b]:c.indptr[b + 1]]).long().cuda() for b in range(3)]
+    v = torch.cat([c.kv[mine[b], 1].reshape(-1, 2, D)[c.lens[b] - c.drafts[b]:c.lens[b]] for b in range(3)])
+    assert torch.equal(out, v.repeat_interleave(4, 1)) and c.dec.device_error() == 0
+    c.check()
+
+
 def test_pools_past_32_bits():
     """Pages whose elements lie past 2^31."""
     c = Case(hq=8, hkv=8, lens=(70, 40), drafts=(5, 3), window=60)
