@@ -166,8 +166,8 @@ typedef struct pkd_config {
  * its cached tokens -- drafts to be verified, as a tree or a chain, or a piece
  * of a prompt.  Plans are made with pkd_plan_tree, layers run with
  * pkd_run_tree.  max_batch is the capacity in query tokens (and in requests);
- * pkd_plan_info.batch counts query tokens.  bf16 cache, head_dim 128, page
- * size a multiple of 16; combinable with PKD_FLAG_HND only.  alpha < 0 selects
+ * pkd_plan_info.batch counts query tokens.  head_dim 128, page size a multiple
+ * of 16; combinable with PKD_FLAG_HND and PKD_FLAG_KV_FP8 only.  alpha < 0 selects
  * 512, min_chunk_tokens < 0 128.  Not for pkd_plan, pkd_run, pkd_graph_capture
  * and pkd_accumulate_weights. */
 #define PKD_FLAG_TREE 2048u
@@ -351,7 +351,8 @@ int pkd_plan_tree(pkd_ctx *ctx, const int32_t *q_indptr, const int32_t *indptr,
  *   q          : device bf16 [rows][Hq][D], 16-byte aligned
  *   rows       : rows of q, out and lse, at least the plan's query tokens; rows
  *                behind those are not written
- *   kv         : device bf16 [num_pages][2][P][Hkv][D] (PKD_FLAG_HND: [2][Hkv][P][D])
+ *   kv         : device bf16 (PKD_FLAG_KV_FP8: E4M3) [num_pages][2][P][Hkv][D]
+ *                (PKD_FLAG_HND: [2][Hkv][P][D])
  *   out, lse   : device bf16 [rows][Hq][D], 32-byte aligned; device fp32 [rows][Hq] or NULL
  *   mask       : device uint32 [rows][mask_words], mask_words at least the most
  *                n_b / 32 rounded up; NULL in a causal plan
@@ -371,6 +372,15 @@ int pkd_run_tree(pkd_ctx *ctx, const void *q, int32_t rows, const void *kv, void
                  const uint32_t *mask, int32_t mask_words, const int32_t *depths,
                  const float *slopes, float scale, float score_cap, uint64_t expect_epoch,
                  void *stream);
+
+/* pkd_run_tree with the attended key k_scale * K and the value v_scale * V (an
+ * E4M3 cache's scales, one per tensor): finite, > 0, and scale * k_scale within
+ * scale's range. */
+int pkd_run_tree_scaled(pkd_ctx *ctx, const void *q, int32_t rows, const void *kv, void *out,
+                        float *lse, const uint32_t *mask, int32_t mask_words,
+                        const int32_t *depths, const float *slopes, float scale,
+                        float score_cap, float k_scale, float v_scale, uint64_t expect_epoch,
+                        void *stream);
 
 /* merge_states: for each of n x heads rows,
  *   m = max(s_a, s_b), w_a = exp(s_a - m), w_b = exp(s_b - m),

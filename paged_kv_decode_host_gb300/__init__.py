@@ -75,7 +75,8 @@ EXPORTS = (
     "pkd_selftest_bounded_wait", "pkd_append_kv_layers", "pkd_static_scratch_last_error",
     "pkd_plan_cascade", "pkd_plan_host_cascade", "pkd_advise_format", "pkd_append_latent",
     "pkd_accumulate_weights", "pkd_evict_kv", "pkd_evict_workspace_bytes",
-    "pkd_plan_tree", "pkd_plan_host_tree", "pkd_run_tree", "pkd_rotate_append_kv",
+    "pkd_plan_tree", "pkd_plan_host_tree", "pkd_run_tree", "pkd_run_tree_scaled",
+    "pkd_rotate_append_kv",
     "pkd_accept_kv",
 )
 
@@ -197,6 +198,8 @@ def load():
     sig["pkd_plan_host_tree"] = (ctypes.c_int, [cfgp, vp, vp, vp, vp, i32, i32, i32, vp, sz,
                                                 ctypes.POINTER(PlanInfo)])
     sig["pkd_run_tree"] = (ctypes.c_int, [vp, vp, i32, vp, vp, vp, vp, i32, vp, vp, f32, f32, u64, vp])
+    sig["pkd_run_tree_scaled"] = (ctypes.c_int, [vp, vp, i32, vp, vp, vp, vp, i32, vp, vp, f32, f32,
+                                                 f32, f32, u64, vp])
     sig["pkd_rotate_append_kv"] = (ctypes.c_int, [vp, i64, i64] * 4 + [
         vp, vp, i32, f32, vp, vp, i32, i32, f32, vp, i32, vp, vp, i32, vp, vp, i32, vp, i32, vp,
         i32, i32, i32, i32, i32, f32, f32, u32, vp, vp])
@@ -375,7 +378,8 @@ def _fast():
                 lib.pkd_accumulate_weights, lib.pkd_append_latent, lib.pkd_evict_kv,
                 lib.pkd_evict_workspace_bytes)])
             m.init_step(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-                lib.pkd_plan_tree, lib.pkd_run_tree, lib.pkd_rotate_append_kv, lib.pkd_accept_kv)])
+                lib.pkd_plan_tree, lib.pkd_run_tree_scaled, lib.pkd_rotate_append_kv,
+                lib.pkd_accept_kv)])
             _fast_plan = m
         except ImportError:
             _fast_plan = False

@@ -92,7 +92,7 @@ bool valid_flags(uint32_t f) {
                          PKD_FLAG_HND | PKD_FLAG_DENSE_PREFIX | PKD_FLAG_CASCADE |
                          PKD_FLAG_LATENT | PKD_FLAG_TREE;
   if (f & ~known) return false;
-  if ((f & PKD_FLAG_TREE) && (f & ~(PKD_FLAG_TREE | PKD_FLAG_HND))) return false;
+  if ((f & PKD_FLAG_TREE) && (f & ~(PKD_FLAG_TREE | PKD_FLAG_HND | PKD_FLAG_KV_FP8))) return false;
   // a latent cache has one layout, one type, a planner and a kernel of its own
   if ((f & PKD_FLAG_LATENT) && f != PKD_FLAG_LATENT) return false;
   // a cascade context runs both of its levels itself: bf16 page tiles,
@@ -185,7 +185,7 @@ int resolve_ctas(const pkd_config* c, const DecodeKind& k, int32_t* n_cta, int* 
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PKD_E_CUDA;
   if ((latent ? latent_prepare(c->num_qo_heads)
-       : tree ? tree_prepare()
+       : tree ? tree_prepare(k.fp8)
               : decode_prepare(k, *smem_bytes)) != cudaSuccess)
     return PKD_E_CUDA;
   if ((latent ? latent_occupancy(c->num_qo_heads, &per_sm)
@@ -215,9 +215,10 @@ int kv_map_for(pkd_ctx* ctx, const void* kv, CUtensorMap* out, CUtensorMap* out_
       encode_latent_map(kv, c.num_pages, c.page_size, 1, &e.map_dense) != cudaSuccess)
     return PKD_E_CUDA;
   if ((ctx->latent ? encode_latent_map(kv, c.num_pages, c.page_size, 0, &e.map)
-       : ctx->tree ? encode_tree_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads, hnd, &e.map)
+       : ctx->tree && !ctx->kind.fp8
+           ? encode_tree_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads, hnd, &e.map)
                         : encode_kv_map(kv, c.num_pages, c.page_size, c.num_kv_heads,
-                                        ctx->kind.fp8, hnd, ctx->kind.dense, &e.map)) !=
+                                        ctx->kind.fp8, hnd, ctx->kind.dense || ctx->tree, &e.map)) !=
       cudaSuccess)
     return PKD_E_CUDA;
   if (ctx->kind.cascade &&
@@ -505,7 +506,7 @@ int pkd_create(const pkd_config* cfg, void* d_workspace, size_t workspace_bytes,
     return st;
   }
   if ((ctx->latent ? latent_prepare(cfg->num_qo_heads)
-       : ctx->tree ? tree_prepare()
+       : ctx->tree ? tree_prepare(ctx->kind.fp8)
                    : decode_prepare(ctx->kind, ctx->smem_bytes)) != cudaSuccess) {
     delete ctx;
     return PKD_E_CUDA;
@@ -689,7 +690,18 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
                  const uint32_t* mask, int32_t mask_words, const int32_t* depths,
                  const float* slopes, float scale, float score_cap, uint64_t expect_epoch,
                  void* stream) {
-  if (ctx == nullptr || !ctx->tree || !(scale >= 0x1p-96f && scale <= 0x1p96f) ||
+  return pkd_run_tree_scaled(ctx, q, rows, kv, out, lse, mask, mask_words, depths, slopes, scale,
+                             score_cap, 1.f, 1.f, expect_epoch, stream);
+}
+
+int pkd_run_tree_scaled(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void* out,
+                        float* lse, const uint32_t* mask, int32_t mask_words,
+                        const int32_t* depths, const float* slopes, float of_scores,
+                        float score_cap, float k_scale, float v_scale, uint64_t expect_epoch,
+                        void* stream) {
+  const double scale = (double)of_scores * k_scale;
+  if (ctx == nullptr || !ctx->tree || !(of_scores > 0.f) || !(k_scale > 0.f) ||
+      !(scale >= 0x1p-96 && scale <= 0x1p96) || !(v_scale > 0.f) || !std::isfinite(v_scale) ||
       !(score_cap == 0.f || (score_cap >= 0x1p-30f && score_cap <= 0x1p96f)) || mask_words < 0)
     return PKD_E_INVALID_ARG;
   if (ctx->epoch == 0) return PKD_E_NO_PLAN;
@@ -717,7 +729,7 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
   a.l_part = reinterpret_cast<float*>(ctx->ws + ctx->layout.l_part_byte);
   a.err = reinterpret_cast<int32_t*>(ctx->ws + ctx->layout.err_byte);
   a.q = static_cast<const uint16_t*>(q);
-  a.kv = static_cast<const uint16_t*>(kv);
+  a.kv = kv;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.mask = mask;
@@ -730,7 +742,9 @@ int pkd_run_tree(pkd_ctx* ctx, const void* q, int32_t rows, const void* kv, void
   a.head_elems = hnd ? (int64_t)kHeadDim * c.page_size : kHeadDim;
   a.v_elems = (int64_t)kHeadDim * c.num_kv_heads * c.page_size;
   a.page_elems = 2 * a.v_elems;
-  // (the map's third and fourth coordinates, in halves and groups of 8 tokens)
+  a.v_scale = v_scale;
+  a.fp8 = ctx->kind.fp8 ? 1 : 0;
+  // (a bf16 map's third and fourth coordinates, in halves and groups of 8 tokens)
   a.head_half = hnd ? 0 : 2;
   a.head_group = hnd ? c.page_size / 8 : 0;
   a.hq = c.num_qo_heads;

@@ -191,7 +191,7 @@ int plan_schedule_tree(const pkd_config& cfg, int32_t n_cta, const Layout& L,
     if (blocks[i].begin == 0) distinct += lens[i];
   }
   const auto grow = [](int64_t s) { return s + std::max<int64_t>(kTreeRound, s / 64); };
-  const int64_t least = span;
+  const int64_t least = span, token_bytes = 2 * kHeadDim * ((cfg.flags & PKD_FLAG_KV_FP8) ? 1 : 2);
   int64_t even = span;
   while (!cut_even(lens, even, alpha, kTreeRound, floor_c, nv, &parts)) even = grow(even);
   placer.divide(blocks, lens, 1, kTreeRound);
@@ -205,7 +205,7 @@ int plan_schedule_tree(const pkd_config& cfg, int32_t n_cta, const Layout& L,
   } else {
     span = even;
   }
-  if (2 * together > total && distinct * hkv * (2 * kHeadDim * 2) > kTreeSharedBytes) {
+  if (2 * together > total && distinct * hkv * token_bytes > kTreeSharedBytes) {
     int64_t best = span + (int64_t)((double)span * kTreeSharedGain / 100 * apart / together);
     int64_t several = 0, rows_of = 0;   // such blocks, their query tokens
     for (size_t i = 0; i < blocks.size(); ++i)

@@ -17,7 +17,7 @@
  * OverflowError.
  *
  * plan_tree, run_tree, rotate_append, accept_kv: pkd_plan_tree (arrays as plan's),
- * pkd_run_tree, pkd_rotate_append_kv and pkd_accept_kv (a list of addresses), after
+ * pkd_run_tree_scaled, pkd_rotate_append_kv and pkd_accept_kv (a list of addresses), after
  * init_step.
  *
  * status is the C ABI's return value, or NOT_HANDLED (1000) when an argument
@@ -309,7 +309,8 @@ typedef int (*plan_tree_fn)(void *ctx, const int32_t *q_indptr, const int32_t *i
 typedef int (*run_tree_fn)(void *ctx, const void *q, int32_t rows, const void *kv, void *out,
                            float *lse, const uint32_t *mask, int32_t mask_words,
                            const int32_t *depths, const float *slopes, float scale,
-                           float score_cap, uint64_t expect_epoch, void *stream);
+                           float score_cap, float k_scale, float v_scale, uint64_t expect_epoch,
+                           void *stream);
 typedef int (*rotate_fn)(const void *q, int64_t q_token, int64_t q_head, void *q_out,
                          int64_t out_token, int64_t out_head, const void *k, int64_t k_token,
                          int64_t k_head, const void *v, int64_t v_token, int64_t v_head,
@@ -377,16 +378,16 @@ static PyObject *plan_tree(PyObject *self, PyObject *args) {
 static PyObject *run_tree(PyObject *self, PyObject *args) {
   unsigned long long ctx, q, kv, out, lse, mask, depths, slopes, epoch, stream;
   int rows, words;
-  float scale, cap;
+  float scale, cap, ks, vs;
   (void)self;
-  if (!PyArg_ParseTuple(args, "KKiKKKKiKKffKK", &ctx, &q, &rows, &kv, &out, &lse, &mask, &words,
-                        &depths, &slopes, &scale, &cap, &epoch, &stream))
+  if (!PyArg_ParseTuple(args, "KKiKKKKiKKffffKK", &ctx, &q, &rows, &kv, &out, &lse, &mask, &words,
+                        &depths, &slopes, &scale, &cap, &ks, &vs, &epoch, &stream))
     return NULL;
   if (g_run_tree == NULL) return PyLong_FromLong(NOT_HANDLED);
   return PyLong_FromLong(g_run_tree(ADDR(ctx), ADDR(q), rows, ADDR(kv), ADDR(out),
                                     (float *)ADDR(lse), (const uint32_t *)ADDR(mask), words,
                                     (const int32_t *)ADDR(depths), (const float *)ADDR(slopes),
-                                    scale, cap, (uint64_t)epoch, ADDR(stream)));
+                                    scale, cap, ks, vs, (uint64_t)epoch, ADDR(stream)));
 }
 
 static PyObject *rotate_append(PyObject *self, PyObject *args) {
@@ -437,7 +438,7 @@ static PyMethodDef methods[] = {
      "init_step(plan_tree_address, run_tree_address, rotate_append_address, accept_address)"},
     {"plan_tree", plan_tree, METH_VARARGS,
      "plan_tree(ctx, q_indptr, indptr, indices, last, causal, window, stream) -> (status, epoch)"},
-    {"run_tree", run_tree, METH_VARARGS, "pkd_run_tree -> status"},
+    {"run_tree", run_tree, METH_VARARGS, "pkd_run_tree_scaled -> status"},
     {"rotate_append", rotate_append, METH_VARARGS, "pkd_rotate_append_kv -> status"},
     {"accept_kv", accept_kv, METH_VARARGS, "pkd_accept_kv (a list of addresses) -> status"},
     {"init_ops", init_ops, METH_VARARGS,

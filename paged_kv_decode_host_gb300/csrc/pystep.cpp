@@ -1,5 +1,5 @@
 // The calls of drafts.py on tensors directly: pkd_rotate_append_kv,
-// pkd_run_tree and pkd_accept_kv with their arguments checked, outputs
+// pkd_run_tree_scaled and pkd_accept_kv with their arguments checked, outputs
 // allocated and addresses taken in C++ (a call's host time from 16-20 us to
 // about 5: these run once per layer, and an accept names every layer's cache).
 //
@@ -21,7 +21,7 @@
 namespace {
 
 decltype(&pkd_rotate_append_kv) g_rotate = nullptr;
-decltype(&pkd_run_tree) g_run_tree = nullptr;
+decltype(&pkd_run_tree_scaled) g_run_tree = nullptr;
 decltype(&pkd_accept_kv) g_accept = nullptr;
 
 constexpr int kLayers = 128;
@@ -158,10 +158,10 @@ PyObject* rotate_append(PyObject*, PyObject* const* a, Py_ssize_t count) try {
 }
 
 // run_tree(ctx, device, tokens, causal, kv_shape, q, kv, mask, depths, slopes, scale, score_cap, out,
-//          lse, return_lse, expect_epoch) -> (status, out, lse or None); kv_shape: the context's
+//          lse, return_lse, expect_epoch, k_scale, v_scale, fp8) -> (status, out, lse or None); kv_shape: the context's
 //          (pages, 2, P, Hkv, D) or (pages, 2, Hkv, P, D), then Hq
 PyObject* run_tree(PyObject*, PyObject* const* a, Py_ssize_t count) try {
-  if (g_run_tree == nullptr || count != 16) return other();
+  if (g_run_tree == nullptr || count != 19) return other();
   bool ok = true;
   const at::Tensor *q = tensor(a[5], ok), *kv = tensor(a[6], ok), *mask = tensor_or_none(a[7], ok),
                    *depths = tensor_or_none(a[8], ok), *slopes = tensor_or_none(a[9], ok),
@@ -172,6 +172,8 @@ PyObject* run_tree(PyObject*, PyObject* const* a, Py_ssize_t count) try {
   const double scale = PyFloat_AsDouble(a[10]), cap = PyFloat_AsDouble(a[11]);
   const long want_lse = PyLong_AsLong(a[14]);
   const unsigned long long epoch = PyLong_AsUnsignedLongLong(a[15]);
+  const double ks = PyFloat_AsDouble(a[16]), vs = PyFloat_AsDouble(a[17]);
+  const at::ScalarType kv_type = PyLong_AsLong(a[18]) ? at::kFloat8_e4m3fn : at::kBFloat16;
   int64_t shape[6];
   for (int i = 0; i < 6; ++i) shape[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a[4], i));
   if (PyErr_Occurred() || c10::cuda::current_device() != dev) return other();
@@ -181,7 +183,7 @@ PyObject* run_tree(PyObject*, PyObject* const* a, Py_ssize_t count) try {
   const int64_t q_shape[3] = {n, hq, dim};
   const at::IntArrayRef heads(q_shape, 2);
   if (n < tokens || n > INT32_MAX || words > INT32_MAX || !whole(*q, at::kBFloat16, dev) ||
-      !is_shape(*q, q_shape) || !whole(*kv, at::kBFloat16, dev) || !is_shape(*kv, at::IntArrayRef(shape, 5)) ||
+      !is_shape(*q, q_shape) || !whole(*kv, kv_type, dev) || !is_shape(*kv, at::IntArrayRef(shape, 5)) ||
       (mask && (!whole(*mask, at::kInt, dev) || mask->dim() != 2 || mask->size(0) != n)) ||
       (depths && (!whole(*depths, at::kInt, dev) || !is_shape(*depths, {n}))) ||
       (slopes && (!whole(*slopes, at::kFloat, dev) || !is_shape(*slopes, {hq}))) ||
@@ -199,7 +201,8 @@ PyObject* run_tree(PyObject*, PyObject* const* a, Py_ssize_t count) try {
                             l.defined() ? static_cast<float*>(l.data_ptr()) : nullptr,
                             static_cast<const uint32_t*>(address(mask)), (int32_t)words,
                             static_cast<const int32_t*>(address(depths)),
-                            static_cast<const float*>(address(slopes)), (float)scale, (float)cap, epoch,
+                            static_cast<const float*>(address(slopes)), (float)scale, (float)cap, (float)ks, (float)vs,
+                            epoch,
                             c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream());
   PyObject* po = out ? Py_NewRef(a[12]) : THPVariable_Wrap(std::move(o));
   PyObject* pl = lse ? Py_NewRef(a[13]) : l.defined() ? THPVariable_Wrap(std::move(l)) : Py_NewRef(Py_None);
@@ -272,7 +275,7 @@ PyMethodDef methods[] = {
     {"rotate_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&rotate_append)), METH_FASTCALL,
      "pkd_rotate_append_kv on tensors -> (status, q_out), or NotImplemented"},
     {"run_tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&run_tree)), METH_FASTCALL,
-     "pkd_run_tree on tensors -> (status, out, lse), or NotImplemented"},
+     "pkd_run_tree_scaled on tensors -> (status, out, lse), or NotImplemented"},
     {"accept_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&accept_kv)), METH_FASTCALL,
      "pkd_accept_kv on tensors -> status, or NotImplemented"},
     {nullptr, nullptr, 0, nullptr}};

@@ -37,7 +37,7 @@ struct TreeArgs {
   float* l_part;            // fp32 [slot][Hq] (natural log)
   int32_t* err;
   const uint16_t* q;        // bf16 [tokens][Hq][128]
-  const uint16_t* kv;       // the cache
+  const void* kv;           // the cache, bf16 or (fp8) e4m3
   uint16_t* out;            // bf16 [tokens][Hq][128]
   float* lse;               // fp32 [tokens][Hq] or null
   const uint32_t* mask;     // [tokens][mask_words] or null
@@ -52,6 +52,8 @@ struct TreeArgs {
   // for products whose square is up to cap_bound: cap_log2 * tanh(scale / cap * x)
   // = x times this polynomial of x^2
   float cap_bound, cap_poly[4];
+  float v_scale;            // of the values (that of the keys is in scale_log2)
+  int32_t fp8;
   int32_t wait_epoch;
   int32_t head_half, head_group;   // where a head starts in kv_map
   CUtensorMap kv_map;       // boxes of 16 tokens of a KV head: [2 x 8 tokens][half][8][128 B]
@@ -59,7 +61,7 @@ struct TreeArgs {
 };
 
 int tree_smem_bytes();
-cudaError_t tree_prepare();
+cudaError_t tree_prepare(bool fp8);
 cudaError_t tree_occupancy(int* blocks_per_sm);
 // most_tokens: of a CTA, as planned (any plan may run under either choice of kernel)
 cudaError_t launch_tree(const TreeArgs& a, int grid, int64_t most_tokens, cudaStream_t stream);

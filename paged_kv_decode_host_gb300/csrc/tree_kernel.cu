@@ -175,6 +175,39 @@ __device__ __forceinline__ int64_t token_offset(const TreeArgs& a, int first_pag
   return page * a.page_elems + (t % a.page_size) * a.token_elems + head * a.head_elems;
 }
 
+// Two e4m3 values (in 16 bits) to bf16 pairs, exact; a NaN stays one.
+__device__ __forceinline__ uint32_t widen2(uint32_t two) {
+  uint32_t h, r;
+  float lo, hi;
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(h) : "r"(two));
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 8 values from element `at` on.
+template <bool kFp8>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&f)[8]) {
+  uint32_t w[4];
+  if (kFp8) {
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + at);
+    w[0] = widen2(x.x);
+    w[1] = widen2(x.x >> 16);
+    w[2] = widen2(x.y);
+    w[3] = widen2(x.y >> 16);
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    f[2 * u] = __uint_as_float(w[u] << 16);
+    f[2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
+  }
+}
+
 // out of 32 dims (from dim0) of one row, summed over the tokens that the row
 // sees with weights 2^(s - total), if one that it does not see has a value that
 // is not finite in these dims, or (wide: weights far above 1, whose sums pass
@@ -182,22 +215,20 @@ __device__ __forceinline__ int64_t token_offset(const TreeArgs& a, int first_pag
 // finite; else left as it is.  (A look at V before each product
 // took 5 to 10 % of a step of short requests; this is for caches that hold such
 // values, and takes about 3 us a token: 16 requests of 8,192 tokens x 16 drafts 41 ms.)
+template <bool kFp8>
 __device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uint16_t* q, int first_page,
                                       int head, int tb, int te, int dim0, float total, bool wide,
                                       float slope2, uint32_t (&o)[32]) {
   auto sees = [&](int t) { return (visible(r, t, te) & 1u) != 0; };
-  auto values = [&](int t) {
-    return reinterpret_cast<const uint4*>(a.kv + token_offset(a, first_page, head, t) + a.v_elems + dim0);
-  };
   auto finite = [&](int t) {
-    const uint4* v = values(t);
-    bool all = true;
-    for (int d = 0; d < 4; ++d) {
-      const uint4 x = v[d];
-      for (uint32_t w : {x.x, x.y, x.z, x.w})
-        all &= (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u;
+    const int64_t at = token_offset(a, first_page, head, t) + a.v_elems + dim0;
+    float bad = 0.f;
+    for (int d = 0; d < 32; d += 8) {
+      float v[8];
+      load8<kFp8>(a.kv, at + d, v);
+      for (int u = 0; u < 8; ++u) bad = fmaf(v[u], 0.f, bad);
     }
-    return all;
+    return bad == 0.f;
   };
   bool again = false;   // a token that is not seen has a value that is not finite
   for (int t = tb; t < min(te, min(r.first_seen, r.ctx)) && !again; ++t) again = !sees(t) && !finite(t);
@@ -212,37 +243,30 @@ __device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uin
   for (int d = 0; d < 32; ++d) acc[d] = 0.f;
   for (int t = tb; t < te; ++t) {
     if (!sees(t)) continue;
-    const uint4* k = reinterpret_cast<const uint4*>(a.kv + token_offset(a, first_page, head, t));
-    const uint4* qr = reinterpret_cast<const uint4*>(q);
+    const int64_t at = token_offset(a, first_page, head, t);
     float s = 0.f;
 #pragma unroll 4
-    for (int d = 0; d < kHeadDim / 8; ++d) {
-      const uint4 x = k[d], y = qr[d];
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    for (int d = 0; d < kHeadDim; d += 8) {
+      float x[8], y[8];
+      load8<kFp8>(a.kv, at + d, x);
+      load8<false>(q, d, y);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        s = fmaf(__uint_as_float(xs[u] << 16), __uint_as_float(ys[u] << 16), s);
-        s = fmaf(__uint_as_float(xs[u] & 0xffff0000u), __uint_as_float(ys[u] & 0xffff0000u), s);
-      }
+      for (int u = 0; u < 8; ++u) s = fmaf(x[u], y[u], s);
     }
     s = a.cap_log2 != 0.f ? capped(s, a.scale_log2, a.cap_log2) : s * a.scale_log2;
     const int64_t away = t < r.ctx ? (int64_t)r.ctx + r.depth - t : (int64_t)r.depth - depth_of(r, t - r.ctx);
     s = fmaf(-slope2, (float)away, s);
     const float p = fast_exp2(s - total);
-    const uint4* v = values(t);
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const uint4 x = v[d];
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+    for (int d = 0; d < 32; d += 8) {
+      float v[8];
+      load8<kFp8>(a.kv, at + a.v_elems + dim0 + d, v);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        acc[8 * d + 2 * u] = fmaf(p, __uint_as_float(xs[u] << 16), acc[8 * d + 2 * u]);
-        acc[8 * d + 2 * u + 1] = fmaf(p, __uint_as_float(xs[u] & 0xffff0000u), acc[8 * d + 2 * u + 1]);
-      }
+      for (int u = 0; u < 8; ++u) acc[d + u] = fmaf(p, v[u], acc[d + u]);
     }
   }
 #pragma unroll
-  for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(acc[d]);
+  for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(acc[d] * a.v_scale);
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -437,16 +461,41 @@ __device__ __forceinline__ void weights32(const uint32_t (&v)[32], float sc, flo
 // slopes always so: the base moves on with every round of a start (39.5 -> 35.6).
 constexpr int kStreamRounds = 4;
 
+// An e4m3 cache: K and V arrive as they are, in tiles of 16 tokens [16][128 B] and
+// two rounds of each, and the producers' warps widen them to bf16 (exact) into rings
+// of two rounds: the same 192 KB.
+constexpr int kNarrowBytes = kRoundTok * kHeadDim;   // K or V of a round
+
+// One round's tiles from e4m3 (chunk c of 16 bytes of token t holds dims 16 (c ^ (t
+// & 7)) on, as the copy swizzles them) to bf16 as the products want them.  8 lanes
+// take a token; those of one half of its dims write their second piece first, so
+// that the 8 pieces written at a time lie in different banks.
+__device__ __forceinline__ void widen_round(const uint8_t* narrow, uint8_t* wide, int tiles, int lane) {
+#pragma unroll 4
+  for (int i = 0; i < 4 * tiles; ++i) {
+    const int t = 4 * i + (lane >> 3), x = t & 7, q = (lane & 7) ^ x;
+    const uint4 v = *reinterpret_cast<const uint4*>(narrow + t * kHeadDim + (lane & 7) * 16);
+    const uint4 lo = make_uint4(widen2(v.x), widen2(v.x >> 16), widen2(v.y), widen2(v.y >> 16));
+    const uint4 hi = make_uint4(widen2(v.z), widen2(v.z >> 16), widen2(v.w), widen2(v.w >> 16));
+    uint8_t* to = wide + (t >> 4) * kTileBytes + ((t >> 3) & 1) * 2048 + (q >> 2) * 1024 + x * 128;
+    const int piece = (q & 3) * 2, turn = q >> 2;
+    *reinterpret_cast<uint4*>(to + ((piece + turn) ^ x) * 16) = turn ? hi : lo;
+    *reinterpret_cast<uint4*>(to + ((piece + 1 - turn) ^ x) * 16) = turn ? lo : hi;
+  }
+}
+
 struct TreeSmem {
   float base[kTreeRows];      // a row's exponent base, as the last round left it
   float swap[2][2][kTreeRows];   // exchanges of the warps of a quadrant: place, half, row
   uint64_t ready[2][4];       // base written by the stream's warp of a quadrant
+  uint64_t narrow[2][2];      // K's, V's two rounds of an e4m3 cache landed
 };
 constexpr int kSmemBytes = kQBytes + kTcStages * kStageBytes + (int)sizeof(TcSmem) + (int)sizeof(TreeSmem);
 static_assert(kSmemBytes <= 227 * 1024 && sizeof(TcSmem) % 4 == 0, "dynamic shared memory of one CTA");
 
-template <bool kCap, bool kSlopes, bool kHalves>
+template <bool kCap, bool kSlopes, bool kHalves, bool kFp8>
 __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kStages = kFp8 ? 2 : kTcStages;   // rounds of K, and of V, that the products read
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
   pdl_launch_dependents();
@@ -472,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     return;
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kTcStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh->fullk[s], 1);
       mbar_init(&sh->emptyk[s], 1);
       mbar_init(&sh->fullv[s], 1);
@@ -486,6 +535,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       mbar_init(&sh->pfull[b], kHalves ? kSoftmaxWarps : kSoftmaxWarps / 2);
       mbar_init(&sh->pfree[b], 1);
       for (int q = 0; q < 4; ++q) mbar_init(&more->ready[b][q], 1);
+      for (int c = 0; c < 2; ++c) mbar_init(&more->narrow[c][b], 1);
     }
     mbar_init(&sh->ofree, kSoftmaxWarps);
     mbar_init(&sh->fin, 2);
@@ -517,18 +567,92 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     const int c = warp == kWarpK ? 0 : 1;
     uint64_t* full = c ? sh->fullv : sh->fullk;
     uint64_t* empty = c ? sh->emptyv : sh->emptyk;
-    uint8_t* ring = stages + (size_t)c * kTcStages * kKvBytes;
+    uint8_t* ring = stages + (size_t)c * kStages * kKvBytes;
     const bool me = elect_one();
     const int step_pages = kRoundTok / P, step_at = kRoundTok % P;
     const uint64_t first = l2_evict_first_policy(), normal = l2_evict_normal_policy();
-    pdl_wait();   // q and the cache may come from the previous kernel
-    int st = 0, nq = 0;
+    // The queue's rounds, one after the other: `next_it`, round `next_k` of it.  Lane j
+    // < 8 copies the round's tile j (its first token is a multiple of 16), which lies on
+    // page `at_page` of the request, from token `next_at` of it on; they move on by one
+    // round each time (a division takes as long as two copies), and the page ids
+    // (`next`) are on their way a round ahead.
+    int next_it = it0, next_k = 0, nr = 0, from = 0, to = 0, head = 0;
+    int tile = 0, ntiles = 0, at_page = 0, next_at = 0, next = 0;
+    const int32_t* pages = nullptr;
+    uint64_t policy = first;
+    auto enter = [&]() {
+      const int32_t* item = a.sched + a.off_items + (int64_t)next_it * kItemWords;
+      const int32_t* entry = requests + item[0] * kRequestWords;
+      from = item[1];
+      to = item[2];
+      head = item[7];
+      // (more than one row block reads these tokens: they may stay in L2)
+      policy = entry[1] > tile_tokens ? normal : first;
+      pages = a.sched + a.off_pages + entry[3];
+      nr = rounds_of(from, to);
+      ntiles = (to - from + 15) >> 4;
+      tile = kRoundTiles * round_at<kSlopes>(0, nr) + (lane & (kRoundTiles - 1));
+      at_page = (from + 16 * tile) / P;
+      next_at = (from + 16 * tile) % P;
+      next = tile < ntiles ? pages[at_page] : 0;
+    };
+    auto issue = [&](uint8_t* dst, uint64_t* bar) {
+      int page = next;
+      const int at = next_at;
+      const int nbox = (min(kRoundTok, to - from - kRoundTok * round_at<kSlopes>(next_k, nr)) + 15) >> 4;
+      if (next_k + 1 < nr) {
+        tile += kSlopes ? -kRoundTiles : kRoundTiles;
+        at_page += kSlopes ? -step_pages : step_pages;
+        next_at += kSlopes ? -step_at : step_at;
+        if (!kSlopes && next_at >= P) {
+          next_at -= P;
+          ++at_page;
+        }
+        if (kSlopes && next_at < 0) {
+          next_at += P;
+          --at_page;
+        }
+        next = tile < ntiles ? pages[at_page] : 0;
+      }
+      if ((unsigned)page >= (unsigned)a.num_pages) {
+        atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
+        page = 0;
+      }
+      const int place = kFp8 ? at : head * a.head_group + (at >> 3), row = 2 * page + c;
+      int places[kRoundTiles], rows[kRoundTiles];
+#pragma unroll
+      for (int u = 0; u < kRoundTiles; ++u) {
+        places[u] = __shfl_sync(kFull, place, u);
+        rows[u] = __shfl_sync(kFull, row, u);
+      }
+      constexpr int kBytes = kFp8 ? 16 * kHeadDim : kTileBytes;
+      if (me) {
+        mbar_arrive_expect_tx(bar, (uint32_t)(nbox * kBytes));
+#pragma unroll
+        for (int u = 0; u < kRoundTiles; ++u)
+          if (u < nbox) {
+            if (kFp8)
+              tensor_copy_g2s(dst + u * kBytes, &a.kv_map, 0, places[u], 0, head, rows[u], bar, policy);
+            else
+              tensor_copy_g2s(dst + u * kBytes, &a.kv_map, 0, 0, head * a.head_half, places[u], rows[u], bar, policy);
+          }
+      }
+      __syncwarp();
+      if (++next_k == nr) {
+        next_k = 0;
+        if (++next_it < it1) enter();
+      }
+    };
+    int st = 0, nq = 0, issued = 0;
     bool ok = true;
+    uint8_t* narrow = stages + 2 * kStages * kKvBytes + c * 2 * kNarrowBytes;   // (an e4m3 cache's)
+    enter();
+    pdl_wait();   // q and the cache may come from the previous kernel
+    for (; kFp8 && issued < 2 && next_it < it1; ++issued)
+      issue(narrow + issued * kNarrowBytes, &more->narrow[c][issued]);
     for (int it = it0; it < it1 && ok; ++it) {
       const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
-      const int tb = item[1], te = item[2], head = item[7];
-      const int32_t* entry = requests + item[0] * kRequestWords;
-      const int poff = entry[3];
+      const int tb = item[1], te = item[2], rounds = rounds_of(tb, te);
       // the item's queries (the previous item's score MMAs must be done)
       if (c == 0 && it > it0 &&
           !warp_wait(&sh->qfree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane)) {
@@ -537,75 +661,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       }
       if (c == 0) ++nq;
       if (c == 0 && me) {
-        const int row0 = entry[0] + item[5];
+        const int row0 = requests[item[0] * kRequestWords] + item[5];
         mbar_arrive_expect_tx(&sh->qfull, (uint32_t)kQBytes);
         for (int h = 0; h < 2; ++h)
-          tensor_copy_g2s(sQ + h * (kQBytes / 2), &a.q_map, 0, h, 0, head, row0, &sh->qfull, first);
+          tensor_copy_g2s(sQ + h * (kQBytes / 2), &a.q_map, 0, h, 0, item[7], row0, &sh->qfull, first);
       }
       __syncwarp();
-      // (more than one row block reads these tokens: they may stay in L2)
-      const uint64_t policy = entry[1] > tile_tokens ? normal : first;
-      // Lane j < 8 copies the round's tile j (tb is a multiple of 16); the page
-      // ids of the round after are on their way.  Where tile j of a round lies: page
-      // `at_page` of the request, token `at` of it, moved on by one round each time
-      // (a division takes as long as two copies).
-      const int nr = rounds_of(tb, te), ntiles = (te - tb + 15) >> 4;
-      const int32_t* pages = a.sched + a.off_pages + poff;
-      const int j = lane & (kRoundTiles - 1);
-      int tile = kRoundTiles * round_at<kSlopes>(0, nr) + j;
-      int at_page = (tb + 16 * tile) / P, at = (tb + 16 * tile) % P;
-      int next = tile < ntiles ? pages[at_page] : 0, next_at = at;
-      for (int k = 0; k < nr; ++k, ++st) {
-        int page = next;
-        at = next_at;
-        if (k + 1 < nr) {
-          tile += kSlopes ? -kRoundTiles : kRoundTiles;
-          at_page += kSlopes ? -step_pages : step_pages;
-          next_at += kSlopes ? -step_at : step_at;
-          if (!kSlopes && next_at >= P) {
-            next_at -= P;
-            ++at_page;
-          }
-          if (kSlopes && next_at < 0) {
-            next_at += P;
-            --at_page;
-          }
-          next = tile < ntiles ? pages[at_page] : 0;
-        }
-        if ((unsigned)page >= (unsigned)a.num_pages) {
-          atomicOr(a.err, PKD_DEV_ERR_BOUNDS);
-          page = 0;
-        }
-        const int t = tb + kRoundTok * round_at<kSlopes>(k, nr);
-        const int nbox = (min(kRoundTok, te - t) + 15) >> 4;
-        const int slot = st % kTcStages;
-        const uint32_t round = (uint32_t)(st / kTcStages);
+      for (int k = 0; k < rounds; ++k, ++st) {
+        const int slot = st % kStages;
+        const uint32_t round = (uint32_t)(st / kStages);
+        uint8_t* dst = ring + (size_t)slot * kKvBytes;
         if (round > 0 && !warp_wait(&empty[slot], (round - 1) & 1u, abort_flag, a.err, lane)) {
           ok = false;
           break;
         }
-        const int group = head * a.head_group + (at >> 3), row = 2 * page + c;
-        int groups[kRoundTiles], pages_of[kRoundTiles];
-#pragma unroll
-        for (int u = 0; u < kRoundTiles; ++u) {
-          groups[u] = __shfl_sync(kFull, group, u);
-          pages_of[u] = __shfl_sync(kFull, row, u);
+        if constexpr (kFp8) {
+          const int buf = st & 1;
+          if (!warp_wait(&more->narrow[c][buf], (uint32_t)((st >> 1) & 1), abort_flag, a.err, lane)) {
+            ok = false;
+            break;
+          }
+          const int tiles = (min(kRoundTok, te - tb - kRoundTok * round_at<kSlopes>(k, rounds)) + 15) >> 4;
+          widen_round(narrow + buf * kNarrowBytes, dst, tiles, lane);
+          fence_proxy_async_smem();   // before the products' reads, and the next copy here
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[slot]);
+          if (next_it < it1) {
+            issue(narrow + buf * kNarrowBytes, &more->narrow[c][buf]);
+            ++issued;
+          }
+        } else {
+          issue(dst, &full[slot]);
         }
-        if (me) {
-          mbar_arrive_expect_tx(&full[slot], (uint32_t)(nbox * kTileBytes));
-#pragma unroll
-          for (int u = 0; u < kRoundTiles; ++u)
-            if (u < nbox)
-              tensor_copy_g2s(ring + (size_t)slot * kKvBytes + u * kTileBytes, &a.kv_map, 0, 0,
-                              head * a.head_half, groups[u], pages_of[u], &full[slot], policy);
-        }
-        __syncwarp();
       }
     }
     // drain: the last phase of every slot, and the last queries
     if (lane == 0) {
-      for (int s = 0; s < kTcStages; ++s)
-        if (st > s && !mbar_wait(&full[s], (uint32_t)(((st - 1 - s) / kTcStages) & 1), nullptr))
+      for (int s = 0; !kFp8 && s < kStages; ++s)
+        if (st > s && !mbar_wait(&full[s], (uint32_t)(((st - 1 - s) / kStages) & 1), nullptr))
+          atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+      for (int s = st; kFp8 && s < issued; ++s)
+        if (!mbar_wait(&more->narrow[c][s & 1], (uint32_t)((s >> 1) & 1), nullptr))
           atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
       if (nq > 0 && !mbar_wait(&sh->qfull, (uint32_t)((nq - 1) & 1), nullptr))
         atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
@@ -625,9 +721,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         break;
       }
       for (int k = 0; k < nr; ++k, ++r) {
-        const int slot = r % kTcStages, b = r & 1;
+        const int slot = r % kStages, b = r & 1;
         // (the wait that is over first, first: one that is over still takes its time)
-        if (!warp_wait(&sh->fullk[slot], (uint32_t)((r / kTcStages) & 1), abort_flag, a.err, lane) ||
+        if (!warp_wait(&sh->fullk[slot], (uint32_t)((r / kStages) & 1), abort_flag, a.err, lane) ||
             (r >= 2 &&
              !warp_wait(&sh->sfree[b], (uint32_t)(((r >> 1) - 1) & 1), abort_flag, a.err, lane))) {
           ok = false;
@@ -658,7 +754,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
     // --------------------------------------------- O += P V (lane 0 issues)
     const bool me = elect_one();
     const uint32_t idesc_o = mma_idesc(kDenseRows, kHeadDim, 1);
-    const uint64_t v0 = smem_desc(smem_u32(stages) + kTcStages * kKvBytes, 1024, 2048);
+    const uint64_t v0 = smem_desc(smem_u32(stages) + kStages * kKvBytes, 1024, 2048);
     int r = 0;
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
@@ -666,8 +762,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       const int tb = item[1], te = item[2];
       const int nr = rounds_of(tb, te);
       for (int k = 0; k < nr; ++k, ++r) {
-        const int slot = r % kTcStages, b = r & 1;
-        if (!warp_wait(&sh->fullv[slot], (uint32_t)((r / kTcStages) & 1), abort_flag, a.err, lane) ||
+        const int slot = r % kStages, b = r & 1;
+        if (!warp_wait(&sh->fullv[slot], (uint32_t)((r / kStages) & 1), abort_flag, a.err, lane) ||
             (k == 0 && it > it0 &&
              !warp_wait(&sh->ofree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane))) {
           ok = false;
@@ -675,7 +771,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
         }
         const int n = min(kRoundTok, te - (tb + round_at<kSlopes>(k, nr) * kRoundTok));
         const int nbox = (n + 15) >> 4;
-        uint8_t* vbase = stages + (size_t)(kTcStages + slot) * kKvBytes;
+        uint8_t* vbase = stages + (size_t)(kStages + slot) * kKvBytes;
         if (n & 15) {
           // slots past the range's end in the last tile: P is 0 there, but
           // 0 x NaN would poison O, so zero those V rows (both halves)
@@ -952,7 +1048,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       const float lt = stream == 0 ? l + l_other : l_other + l;
       const int64_t q_row = (int64_t)(q_first + i0 + i) * a.hq + hq;
       const int64_t p_row = ((int64_t)dst + (int64_t)i * stride) * a.hq + hq;   // its partial state
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const float inv = lt == 0.f ? 0.f : a.v_scale / lt;
 #pragma unroll 1
       for (int cb = 64 * stream; cb < 64 * stream + 64; cb += 32) {
         uint32_t o[32];
@@ -970,8 +1066,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
 #pragma unroll
           for (int j = 0; j < 32; ++j) again[j] = lt == 0.f ? 0u : o[j];
           if (lt > 0.f)   // (a NaN: the scores')
-            redo_row(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used + log2f(lt),
-                     fixed, sp.slope2, again);
+            redo_row<kFp8>(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used + log2f(lt),
+                           fixed, sp.slope2, again);
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = again[j];
         }
@@ -1016,32 +1112,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
   }
 }
 
+template <bool kFp8>
 const void* kernel_of(bool cap, bool slopes, bool halves) {
   if (slopes)
-    return cap ? reinterpret_cast<const void*>(&tree_kernel<true, true, true>)
-               : reinterpret_cast<const void*>(&tree_kernel<false, true, true>);
+    return cap ? reinterpret_cast<const void*>(&tree_kernel<true, true, true, kFp8>)
+               : reinterpret_cast<const void*>(&tree_kernel<false, true, true, kFp8>);
   if (halves)
-    return cap ? reinterpret_cast<const void*>(&tree_kernel<true, false, true>)
-               : reinterpret_cast<const void*>(&tree_kernel<false, false, true>);
-  return cap ? reinterpret_cast<const void*>(&tree_kernel<true, false, false>)
-             : reinterpret_cast<const void*>(&tree_kernel<false, false, false>);
+    return cap ? reinterpret_cast<const void*>(&tree_kernel<true, false, true, kFp8>)
+               : reinterpret_cast<const void*>(&tree_kernel<false, false, true, kFp8>);
+  return cap ? reinterpret_cast<const void*>(&tree_kernel<true, false, false, kFp8>)
+             : reinterpret_cast<const void*>(&tree_kernel<false, false, false, kFp8>);
 }
 
 }  // namespace
 
 int tree_smem_bytes() { return kSmemBytes; }
 
-cudaError_t tree_prepare() {
+cudaError_t tree_prepare(bool fp8) {
   for (int k = 0; k < 8; ++k) {
     const cudaError_t e = cudaFuncSetAttribute(
-        kernel_of(k & 1, k & 2, k & 4), cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem_bytes());
+        fp8 ? kernel_of<true>(k & 1, k & 2, k & 4) : kernel_of<false>(k & 1, k & 2, k & 4), cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem_bytes());
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 cudaError_t tree_occupancy(int* blocks_per_sm) {
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of(false, false, false),
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of<false>(false, false, false),
                                                        kTcThreads, (size_t)tree_smem_bytes());
 }
 
@@ -1057,8 +1154,9 @@ cudaError_t launch_tree(const TreeArgs& a, int grid, int64_t most_tokens, cudaSt
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void* args[] = {const_cast<TreeArgs*>(&a)};
+  const bool cap = a.cap_log2 != 0.f, slopes = a.slopes != nullptr, halves = most_tokens < kStreamRounds * kTreeRound;
   return cudaLaunchKernelExC(
-      &cfg, kernel_of(a.cap_log2 != 0.f, a.slopes != nullptr, most_tokens < kStreamRounds * kTreeRound), args);
+      &cfg, a.fp8 ? kernel_of<true>(cap, slopes, halves) : kernel_of<false>(cap, slopes, halves), args);
 }
 
 }  // namespace pkd

@@ -33,7 +33,7 @@ def _step():
             from . import _pkd_step as m
             lib = load()
             m.init(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-                lib.pkd_rotate_append_kv, lib.pkd_run_tree, lib.pkd_accept_kv)])
+                lib.pkd_rotate_append_kv, lib.pkd_run_tree_scaled, lib.pkd_accept_kv)])
             _step_module = m
         except ImportError:
             _step_module = False
@@ -266,8 +266,8 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
     A request's query tokens are the last of its cached tokens: append their
     keys and values first (:func:`append_kv`, :func:`rotate_append_kv`), then
     ``plan`` over the table with them, then ``run`` once per layer.  max_tokens:
-    the most query tokens of a plan (and requests).  bf16, layout NHD or HND,
-    head_dim 128, page size a multiple of 16.  Capture a step with
+    the most query tokens of a plan (and requests).  The cache is bf16 or (kv_dtype
+    "e4m3") E4M3, layout NHD or HND, head_dim 128, page size a multiple of 16.  Capture a step with
     ``torch.cuda.graph`` around its runs: it replays under later plans of no
     more query tokens than q has rows.  The runs of one context share its
     workspace: order them, captured ones too, by a stream or an event.
@@ -275,19 +275,22 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
 
     def __init__(self, num_qo_heads, num_kv_heads, head_dim, page_size, *, max_tokens,
                  max_num_pages, num_pages, alpha=-1, min_chunk_tokens=-1, num_ctas=0,
-                 kv_layout="NHD", device=None):
+                 kv_layout="NHD", kv_dtype="bf16", device=None):
         import torch
+        if kv_dtype not in ("bf16", "e4m3"):
+            raise ValueError("kv_dtype must be 'bf16' or 'e4m3'")
         if kv_layout not in ("NHD", "HND"):
             raise ValueError("kv_layout must be 'NHD' [pages, 2, P, Hkv, D] or "
                              "'HND' [pages, 2, Hkv, P, D]")
-        self.kv_layout, self.kv_dtype = kv_layout, "bf16"
+        self.kv_layout, self.kv_dtype, self._fp8 = kv_layout, kv_dtype, kv_dtype == "e4m3"
         self.device = torch.device("cuda" if device is None else device)
         self.hq, self.hkv, self.d, self.p = num_qo_heads, num_kv_heads, head_dim, page_size
         self.num_pages = num_pages
         self.causal, self._most = False, 0
         self._create(make_config(num_qo_heads, num_kv_heads, head_dim, page_size, max_tokens,
                                  max_num_pages, num_pages, alpha, min_chunk_tokens, num_ctas,
-                                 FLAG_TREE | (FLAG_HND if kv_layout == "HND" else 0)))
+                                 FLAG_TREE | (FLAG_HND if kv_layout == "HND" else 0)
+                                 | (FLAG_KV_FP8 if self._fp8 else 0)))
         self._kv_shape = torch.Size((num_pages, 2, page_size, num_kv_heads, head_dim)
                                     if kv_layout == "NHD" else
                                     (num_pages, 2, num_kv_heads, page_size, head_dim))
@@ -328,7 +331,8 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
         return ep
 
     def run(self, q, kv_cache, *, mask=None, depths=None, scale=None, score_cap=0.0, slopes=None,
-            out=None, lse=None, return_lse=True, expect_epoch=0, stream=None):
+            out=None, lse=None, return_lse=True, expect_epoch=0, stream=None, k_scale=1.0,
+            v_scale=1.0):
         """Attention for one layer.  Returns (out, lse) or out.
 
         q [rows, Hq, 128], rows at least the planned query tokens (rows behind
@@ -345,13 +349,16 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
         2^96): scores become score_cap * tanh(score / score_cap).  slopes:
         float32 [Hq], then -= slope * (position of the query - position of the
         key).
+        k_scale, v_scale: the attended key is k_scale * K and the value v_scale *
+        V (an E4M3 cache needs them).
         A query that sees nothing gets 0 and an lse of -inf."""
         if stream is None and self.batch is not None:
             m = _step()
             if m is not None:
                 got = m.run_tree(self._hv, self._dev, self.batch, self.causal, self._shape, q, kv_cache,
                                  mask, depths, slopes, self._scale if scale is None else scale,
-                                 score_cap, out, lse, return_lse, expect_epoch)
+                                 score_cap, out, lse, return_lse, expect_epoch, k_scale, v_scale,
+                                 self._fp8)
                 if got is not NotImplemented:
                     if got[0]:
                         _check(got[0], "pkd_run_tree")
@@ -360,6 +367,8 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
         if self.batch is None:
             raise PkdError(-5, "run before plan")
         bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+        kv_dt = bf if not self._fp8 else \
+            torch.uint8 if kv_cache.dtype is torch.uint8 else torch.float8_e4m3fn
         dev, rows = q.get_device(), q.shape[0]
         if dev != self.workspace.get_device():
             raise ValueError(f"q is on {q.device}, the plan on {self.workspace.device}")
@@ -369,7 +378,7 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
         if mask is not None and mask.dim() != 2:
             raise ValueError("mask must be [rows, words]")
         words = mask.shape[1] if mask is not None else 0
-        for name, t, dt, want in (("q", q, bf, shape), ("kv_cache", kv_cache, bf, self._kv_shape),
+        for name, t, dt, want in (("q", q, bf, shape), ("kv_cache", kv_cache, kv_dt, self._kv_shape),
                                   ("out", out, bf, shape), ("lse", lse, f32, shape[:2]),
                                   ("mask", mask, i32, (rows, words)),
                                   ("depths", depths, i32, shape[:1]),
@@ -388,13 +397,13 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
             lse = _empty_on(stream, shape[:2], f32, q.device)
         fast = _fast()
         with _on(dev):
-            st = (self._lib.pkd_run_tree if fast is None else fast.run_tree)(
+            st = (self._lib.pkd_run_tree_scaled if fast is None else fast.run_tree)(
                 self._hv, q.data_ptr(), rows, kv_cache.data_ptr(), out.data_ptr(),
                 lse.data_ptr() if lse is not None else 0,
                 mask.data_ptr() if mask is not None else 0, words,
                 depths.data_ptr() if depths is not None else 0,
                 slopes.data_ptr() if slopes is not None else 0,
-                self._scale if scale is None else scale, score_cap, expect_epoch,
+                self._scale if scale is None else scale, score_cap, k_scale, v_scale, expect_epoch,
                 _stream_ptr(stream))
         if st:
             _check(st, "pkd_run_tree")

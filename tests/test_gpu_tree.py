@@ -27,17 +27,25 @@ def trees(drafts, seed):
                           + [[]]).astype(np.int32)
 
 
+KV_SCALES = torch.tensor([0.5, 0.25], dtype=torch.float64).view(1, 2, 1, 1, 1)
+
+
 class Case:
     def __init__(self, hq=8, hkv=2, page=16, layout="NHD", lens=(37, 16, 5), drafts=(4, 3, 5), causal=False,
-                 window=0, cap=0.0, slopes=False, seed=0, rows=None, depths=True, magnitude=1.0, scale=None, **kw):
+                 window=0, cap=0.0, slopes=False, seed=0, rows=None, depths=True, magnitude=1.0, scale=None, fp8=False, **kw):
         self.__dict__.update(hq=hq, hkv=hkv, page=page, layout=layout, lens=lens, drafts=drafts, causal=causal,
-                             window=window, cap=cap, scale=scale)
+                             window=window, cap=cap, scale=scale, fp8=fp8)
+        self.scales = dict(k_scale=0.5, v_scale=0.25) if fp8 else {}
         self.indptr, self.indices, self.last, self.pool = table(lens, page, seed)
         self.q_indptr = np.concatenate([[0], np.cumsum(drafts)]).astype(np.int32)
         self.tokens = int(self.q_indptr[-1])
         g = torch.Generator("cuda").manual_seed(seed)
         shape = (self.pool, 2, page, hkv, D) if layout == "NHD" else (self.pool, 2, hkv, page, D)
         self.kv = torch.randn(shape, generator=g, device="cuda").bfloat16()
+        if fp8:   # values of about 1 once scaled
+            self.kv[:, 0] *= 2
+            self.kv[:, 1] *= 4
+            self.kv = self.kv.to(torch.float8_e4m3fn)
         self.q = (magnitude * torch.randn(self.tokens if rows is None else rows, hq, D, generator=g,
                                           device="cuda")).bfloat16()
         self.mask = self.depths = self.slopes = None
@@ -51,7 +59,7 @@ class Case:
             self.slopes = torch.tensor([2.0 ** (-8.0 * (i + 1) / hq) for i in range(hq)], device="cuda")
         self.dec = pkd.BatchTreeDecodeWithPagedKVCache(
             hq, hkv, D, page, max_tokens=max(1, self.tokens, len(lens)), max_num_pages=len(self.indices),
-            num_pages=self.pool, kv_layout=layout, **kw)
+            num_pages=self.pool, kv_layout=layout, kv_dtype="e4m3" if fp8 else "bf16", **kw)
         self.plan()
 
     def plan(self, **kw):
@@ -60,7 +68,7 @@ class Case:
 
     def run(self, **kw):
         return self.dec.run(self.q, self.kv, mask=self.mask, depths=self.depths, score_cap=self.cap,
-                            slopes=self.slopes, scale=self.scale, **kw)
+                            slopes=self.slopes, scale=self.scale, **self.scales, **kw)
 
     def sees(self, b):
         """[n, l] which tokens every query token of request b sees, and how far away they are."""
@@ -87,7 +95,8 @@ class Case:
             if n == 0:
                 continue
             mine = torch.from_numpy(self.indices[self.indptr[b]:self.indptr[b + 1]]).long().cuda()
-            kv = self.kv[mine].double()
+            kv = (self.kv.view(torch.uint8)[mine].view(torch.float8_e4m3fn).double() * KV_SCALES.cuda() if self.fp8
+                  else self.kv[mine].double())
             kv = kv if self.layout == "NHD" else kv.transpose(2, 3)
             k, v = (kv[:, c].reshape(-1, self.hkv, D)[:length] for c in (0, 1))
             first = int(self.q_indptr[b])
@@ -121,7 +130,8 @@ class Case:
         # P is rounded to bf16 (half a step: 2^-8 of itself) and the row's sum is not: that moves a
         # weighted mean of values of magnitude at most top by at most 2^-8 top, its own rounding by
         # 2^-8 |out|; scores in fp32 (below) move the weights by under 2^-12 of themselves
-        top = float(self.kv.float()[torch.isfinite(self.kv.float())].abs().max())
+        kv = self.kv.float() * (KV_SCALES.float().cuda() if self.fp8 else 1.0)
+        top = float(kv[torch.isfinite(kv)].abs().max())
         assert (out.double() - ro).abs().max() <= 1.1 * 2 ** -8 * (top + float(ro.abs().max()))
         # lse: a score is an fp32 sum of 128 products, random errors of 2^-24 of its terms' partial
         # sums (under 2^-24 * 128 * 6 * scale of the queries' magnitude, < 1e-4); the cap's tanh is
@@ -458,6 +468,65 @@ def test_rows_of_one_token_are_its_value(kw):
     v = torch.cat([c.kv[mine[b], 1].reshape(-1, 2, D)[c.lens[b] - c.drafts[b]:c.lens[b]] for b in range(3)])
     assert torch.equal(out, v.repeat_interleave(4, 1)) and c.dec.device_error() == 0
     c.check()
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 1), (3, 3), (8, 2), (32, 8), (64, 8)])
+@pytest.mark.parametrize("layout,page", [("NHD", 16), ("HND", 48), ("NHD", 256)])
+def test_e4m3_heads_and_layouts(hq, hkv, layout, page):
+    Case(hq=hq, hkv=hkv, layout=layout, page=page, lens=(37, 16, 5, 300, 900), drafts=(4, 3, 5, 9, 70), seed=hq,
+         fp8=True).check()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(cap=30.0), dict(slopes=True), dict(cap=30.0, slopes=True),
+                                dict(window=1), dict(window=150), dict(cap=50.0, window=600)])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens,drafts", [((3000, 40, 1500), (12, 3, 40)), ((129, 2, 1, 640, 17), (1, 2, 1, 128, 16))])
+def test_e4m3_scores(kw, causal, lens, drafts):
+    Case(lens=lens, drafts=drafts, causal=causal, fp8=True, **kw).check()
+
+
+def test_e4m3_many_rounds_and_items():
+    Case(hq=32, hkv=8, lens=(20_000, 3, 9_000, 2_000), drafts=(70, 1, 33, 5), fp8=True).check()
+    Case(hq=8, hkv=2, lens=(700,) * 40, drafts=(20,) * 40, fp8=True, num_ctas=4).check()
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_e4m3_what_is_masked_may_hold_anything(split):
+    kw = dict(min_chunk_tokens=128, alpha=0) if split else {}
+    c = Case(lens=(700, 60), drafts=(12, 5), fp8=True, window=300, **kw)
+    see = [c.sees(b)[0].any(0).cpu() for b in range(2)]
+    raw = c.kv.view(torch.uint8)
+    for b in range(2):
+        for t in (~see[b]).nonzero()[:, 0].tolist() + list(range(c.lens[b], 16 * (-(-c.lens[b] // 16)))):
+            raw[int(c.indices[c.indptr[b] + t // 16]), :, t % 16] = 0x7F   # NaN
+    # and a draft that only itself sees
+    c.mask[3], c.mask[4:12, 0] = torch.tensor([8], device="cuda").int(), c.mask[4:12, 0] & ~8
+    raw[int(c.indices[c.indptr[0] + 691 // 16]), :, 691 % 16] = 0xFF
+    out, lse = c.run()
+    mine = [i for i in range(17) if i != 3]
+    ro, rl = c.reference()
+    assert torch.isnan(out[3]).all() and torch.isnan(lse[3]).all()
+    assert (out[mine].double() - ro[mine]).abs().max() <= 1.1 * 2 ** -8 * 8 and c.dec.device_error() == 0
+    assert (lse[mine].double() - rl[mine]).abs().max() <= 2e-4
+
+
+def test_e4m3_captured_and_as_bytes():
+    c = Case(lens=(700, 90, 40), drafts=(12, 9, 4), fp8=True)
+    want = c.run()
+    c.kv = c.kv.view(torch.uint8)
+    got = c.run()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(out=out, lse=lse)
+    graph.replay()
+    assert torch.equal(want[0], out) and torch.equal(want[1], lse)
+    with pytest.raises(ValueError):
+        c.dec.run(c.q, c.kv.bfloat16(), mask=c.mask)
+    for bad in (dict(k_scale=0.0), dict(v_scale=float("inf")), dict(k_scale=float("nan")), dict(v_scale=-1.0)):
+        with pytest.raises(pkd.PkdError, match="INVALID"):
+            c.dec.run(c.q, c.kv, mask=c.mask, **bad)
 
 
 def test_pools_past_32_bits():

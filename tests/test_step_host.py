@@ -37,12 +37,13 @@ def test_configurations(lib):
     off = (ctypes.c_int64 * 6)()
     status = lambda **kw: lib.pkd_schedule_layout(ctypes.byref(config(**kw)), off)
     for kw in (dict(), dict(num_qo_heads=64, num_kv_heads=8), dict(num_qo_heads=3, num_kv_heads=3),
-               dict(flags=pkd.FLAG_TREE | pkd.FLAG_HND), dict(page_size=48), dict(max_batch=0), dict(num_ctas=1)):
+               dict(flags=pkd.FLAG_TREE | pkd.FLAG_HND), dict(flags=pkd.FLAG_TREE | pkd.FLAG_KV_FP8),
+               dict(flags=pkd.FLAG_TREE | pkd.FLAG_HND | pkd.FLAG_KV_FP8), dict(page_size=48), dict(max_batch=0), dict(num_ctas=1)):
         assert status(**kw) == 0, kw
     for kw in (dict(head_dim=64), dict(page_size=8), dict(num_qo_heads=6), dict(num_qo_heads=7),
                dict(num_qo_heads=18, num_kv_heads=9)):
         assert status(**kw) == SHAPE, kw
-    for extra in (1, 2, 4, 8, 16, 64, 128, 256, 1024):
+    for extra in (1, 2, 4, 16, 64, 128, 256, 1024):
         assert status(flags=pkd.FLAG_TREE | extra) == INVALID, extra
 
 
@@ -251,3 +252,5 @@ def test_accept_refusals(lib):
 def test_tree_calls_without_a_context(lib):
     assert lib.pkd_plan_tree(None, None, None, None, None, 0, 0, 0, None, None) == INVALID
     assert lib.pkd_run_tree(None, None, 0, None, None, None, None, 0, None, None, 1.0, 0.0, 0, None) == INVALID
+    assert lib.pkd_run_tree_scaled(None, None, 0, None, None, None, None, 0, None, None, 1.0, 0.0, 1.0, 1.0, 0,
+                                   None) == INVALID
