@@ -189,7 +189,7 @@ int resolve_ctas(const pkd_config* c, const DecodeKind& k, int32_t* n_cta, int* 
               : decode_prepare(k, *smem_bytes)) != cudaSuccess)
     return PKD_E_CUDA;
   if ((latent ? latent_occupancy(c->num_qo_heads, &per_sm)
-       : tree ? tree_occupancy(&per_sm)
+       : tree ? tree_occupancy(k.fp8, &per_sm)
               : decode_occupancy(k, c->num_kv_heads, *smem_bytes, &per_sm)) != cudaSuccess)
     return PKD_E_CUDA;
   if (per_sm < 1) return PKD_E_UNSUPPORTED_SHAPE;

@@ -62,7 +62,7 @@ struct TreeArgs {
 
 int tree_smem_bytes();
 cudaError_t tree_prepare(bool fp8);
-cudaError_t tree_occupancy(int* blocks_per_sm);
+cudaError_t tree_occupancy(bool fp8, int* blocks_per_sm);
 // most_tokens: of a CTA, as planned (any plan may run under either choice of kernel)
 cudaError_t launch_tree(const TreeArgs& a, int grid, int64_t most_tokens, cudaStream_t stream);
 

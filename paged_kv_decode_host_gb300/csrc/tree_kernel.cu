@@ -465,22 +465,86 @@ constexpr int kStreamRounds = 4;
 // two rounds of each, and the producers' warps widen them to bf16 (exact) into rings
 // of two rounds: the same 192 KB.
 constexpr int kNarrowBytes = kRoundTok * kHeadDim;   // K or V of a round
+// Three warps widen K, three V: the producer and two of a fourth warpgroup (the
+// producers alone took 6,000 cycles a round).  128 registers each then, which spills a
+// few words.
+constexpr int kWideners = 3;
+constexpr int kThreadsFp8 = kTcThreads + 128;
 
-// One round's tiles from e4m3 (chunk c of 16 bytes of token t holds dims 16 (c ^ (t
-// & 7)) on, as the copy swizzles them) to bf16 as the products want them.  8 lanes
-// take a token; those of one half of its dims write their second piece first, so
-// that the 8 pieces written at a time lie in different banks.
-__device__ __forceinline__ void widen_round(const uint8_t* narrow, uint8_t* wide, int tiles, int lane) {
-#pragma unroll 4
-  for (int i = 0; i < 4 * tiles; ++i) {
-    const int t = 4 * i + (lane >> 3), x = t & 7, q = (lane & 7) ^ x;
-    const uint4 v = *reinterpret_cast<const uint4*>(narrow + t * kHeadDim + (lane & 7) * 16);
-    const uint4 lo = make_uint4(widen2(v.x), widen2(v.x >> 16), widen2(v.y), widen2(v.y >> 16));
-    const uint4 hi = make_uint4(widen2(v.z), widen2(v.z >> 16), widen2(v.w), widen2(v.w >> 16));
-    uint8_t* to = wide + (t >> 4) * kTileBytes + ((t >> 3) & 1) * 2048 + (q >> 2) * 1024 + x * 128;
-    const int piece = (q & 3) * 2, turn = q >> 2;
-    *reinterpret_cast<uint4*>(to + ((piece + turn) ^ x) * 16) = turn ? hi : lo;
-    *reinterpret_cast<uint4*>(to + ((piece + 1 - turn) ^ x) * 16) = turn ? lo : hi;
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// Four e4m3 values to two bf16 pairs where none is a NaN: exponent and mantissa under
+// bf16's exponent, times 2^120 (7 and 127 are the types' biases), subnormals too.
+// Integer operations and one product a pair: conversion instructions (half, float,
+// bf16) bound whole rounds, at 5,700 cycles.
+__device__ __forceinline__ uint2 widen4(uint32_t four) {
+  uint32_t r[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint32_t x = __byte_perm(four, 0u, u == 0 ? 0x1404 : 0x3424);   // the bytes on top of 16 bits each
+    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[u]) : "r"(y), "r"(0x7b807b80u));
+  }
+  return make_uint2(r[0], r[1]);
+}
+// some byte of w is 0x7f or 0xff: bit 7 of a byte
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+
+// Tiles first, first + step, ... of a round from e4m3 (chunk c of 16 bytes of token t
+// holds dims 16 (c ^ (t & 7)) on, as the copy swizzles them) to bf16 as the products
+// want them.  8 lanes take a token; those of one half of its dims write their second
+// piece first, so that the 8 pieces written at a time lie in different banks.  Bound by
+// integer operations (some 50 for 512 values), so the tiles are dealt out such that
+// each scheduler's warps have as many.  Not inlined: with this loop unrolled, twice, the
+// whole kernel waited for its instructions.
+__device__ __noinline__ void widen_round(const uint8_t* narrow, uint8_t* wide, int tiles, int first, int step,
+                                         int lane) {
+  uint32_t from[2], to[2][2];   // of tokens x and x + 4 of 8
+  bool turn[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int x = (lane >> 3) + 4 * u, q = (lane & 7) ^ x, piece = (q & 3) * 2;
+    turn[u] = q >= 4;
+    from[u] = smem_u32(narrow) + x * kHeadDim + (lane & 7) * 16;
+    const uint32_t row = smem_u32(wide) + (q >> 2) * 1024 + x * 128;
+    to[u][0] = row + ((piece + (q >> 2)) ^ x) * 16;
+    to[u][1] = row + ((piece + 1 - (q >> 2)) ^ x) * 16;
+  }
+#pragma unroll 1
+  for (int tile = first; tile < tiles; tile += step) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // 8 tokens
+      uint4 v[2];
+      uint32_t odd = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 x = lds16(from[u] + tile * 16 * kHeadDim + h * 8 * kHeadDim);
+        v[u] = turn[u] ? make_uint4(x.z, x.w, x.x, x.y) : x;   // the piece to write first
+        odd |= nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w);
+      }
+      const bool nan = __any_sync(kFull, (odd & 0x80808080u) != 0);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint2 w[4] = {widen4(v[u].x), widen4(v[u].y), widen4(v[u].z), widen4(v[u].w)};
+        if (nan) {
+          w[0] = make_uint2(widen2(v[u].x), widen2(v[u].x >> 16));
+          w[1] = make_uint2(widen2(v[u].y), widen2(v[u].y >> 16));
+          w[2] = make_uint2(widen2(v[u].z), widen2(v[u].z >> 16));
+          w[3] = make_uint2(widen2(v[u].w), widen2(v[u].w >> 16));
+        }
+        const uint32_t at = tile * kTileBytes + h * 2048;
+        sts16(to[u][0] + at, make_uint4(w[0].x, w[0].y, w[1].x, w[1].y));
+        sts16(to[u][1] + at, make_uint4(w[2].x, w[2].y, w[3].x, w[3].y));
+      }
+    }
   }
 }
 
@@ -488,13 +552,14 @@ struct TreeSmem {
   float base[kTreeRows];      // a row's exponent base, as the last round left it
   float swap[2][2][kTreeRows];   // exchanges of the warps of a quadrant: place, half, row
   uint64_t ready[2][4];       // base written by the stream's warp of a quadrant
-  uint64_t narrow[2][2];      // K's, V's two rounds of an e4m3 cache landed
+  uint64_t narrow[2][2];      // K's, V's two rounds of an e4m3 cache landed,
+  uint64_t widened[2][2];     // and read by the wideners beside the producer
 };
 constexpr int kSmemBytes = kQBytes + kTcStages * kStageBytes + (int)sizeof(TcSmem) + (int)sizeof(TreeSmem);
 static_assert(kSmemBytes <= 227 * 1024 && sizeof(TcSmem) % 4 == 0, "dynamic shared memory of one CTA");
 
 template <bool kCap, bool kSlopes, bool kHalves, bool kFp8>
-__global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int kStages = kFp8 ? 2 : kTcStages;   // rounds of K, and of V, that the products read
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!schedule_ready(a.sched + H_EPOCH, a.wait_epoch, a.err)) return;
@@ -522,9 +587,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh->fullk[s], 1);
+      mbar_init(&sh->fullk[s], kFp8 ? kWideners : 1);
       mbar_init(&sh->emptyk[s], 1);
-      mbar_init(&sh->fullv[s], 1);
+      mbar_init(&sh->fullv[s], kFp8 ? kWideners : 1);
       mbar_init(&sh->emptyv[s], 1);
     }
     mbar_init(&sh->qfull, 1);
@@ -535,7 +600,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
       mbar_init(&sh->pfull[b], kHalves ? kSoftmaxWarps : kSoftmaxWarps / 2);
       mbar_init(&sh->pfree[b], 1);
       for (int q = 0; q < 4; ++q) mbar_init(&more->ready[b][q], 1);
-      for (int c = 0; c < 2; ++c) mbar_init(&more->narrow[c][b], 1);
+      for (int c = 0; c < 2; ++c) {
+        mbar_init(&more->narrow[c][b], 1);
+        mbar_init(&more->widened[c][b], kWideners - 1);
+      }
     }
     mbar_init(&sh->ofree, kSoftmaxWarps);
     mbar_init(&sh->fin, 2);
@@ -682,11 +750,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
             break;
           }
           const int tiles = (min(kRoundTok, te - tb - kRoundTok * round_at<kSlopes>(k, rounds)) + 15) >> 4;
-          widen_round(narrow + buf * kNarrowBytes, dst, tiles, lane);
+          widen_round(narrow + buf * kNarrowBytes, dst, tiles, 1, 4, lane);
           fence_proxy_async_smem();   // before the products' reads, and the next copy here
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[slot]);
           if (next_it < it1) {
+            if (!warp_wait(&more->widened[c][buf], (uint32_t)((st >> 1) & 1), abort_flag, a.err, lane)) {
+              ok = false;
+              break;
+            }
             issue(narrow + buf * kNarrowBytes, &more->narrow[c][buf]);
             ++issued;
           }
@@ -705,6 +777,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_kernel(const __grid_consta
           atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
       if (nq > 0 && !mbar_wait(&sh->qfull, (uint32_t)((nq - 1) & 1), nullptr))
         atomicOr(a.err, PKD_DEV_ERR_TIMEOUT);
+    }
+  } else if (kFp8 && warp >= kTcThreads / 32) {
+    // ------------------------------------- more wideners (two of K, two of V)
+    // (odd warps have no producer beside them: half of the tiles, the others a quarter)
+    const int c = (warp - kTcThreads / 32) >> 1, tile0 = warp & 1 ? 0 : 3, step = warp & 1 ? 2 : 4;
+    uint64_t* full = c ? sh->fullv : sh->fullk;
+    uint64_t* empty = c ? sh->emptyv : sh->emptyk;
+    uint8_t* ring = stages + (size_t)c * kStages * kKvBytes;
+    const uint8_t* narrow = stages + 2 * kStages * kKvBytes + c * 2 * kNarrowBytes;
+    int st = 0;
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+      const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
+      const int tb = item[1], te = item[2], rounds = rounds_of(tb, te);
+      for (int k = 0; k < rounds; ++k, ++st) {
+        const int slot = st % kStages, buf = st & 1;
+        const uint32_t round = (uint32_t)(st / kStages);
+        if ((round > 0 && !warp_wait(&empty[slot], (round - 1) & 1u, abort_flag, a.err, lane)) ||
+            !warp_wait(&more->narrow[c][buf], (uint32_t)((st >> 1) & 1), abort_flag, a.err, lane)) {
+          ok = false;
+          break;
+        }
+        const int tiles = (min(kRoundTok, te - tb - kRoundTok * round_at<kSlopes>(k, rounds)) + 15) >> 4;
+        widen_round(narrow + buf * kNarrowBytes, ring + (size_t)slot * kKvBytes, tiles, tile0, step, lane);
+        fence_proxy_async_smem();   // before the products' reads, and the next copy there
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[slot]);
+        if (lane == 0) mbar_arrive(&more->widened[c][buf]);
+      }
     }
   } else if (warp == kWarpS) {
     // ------------------------------------------- S = Q K^T (lane 0 issues)
@@ -1130,22 +1231,23 @@ int tree_smem_bytes() { return kSmemBytes; }
 
 cudaError_t tree_prepare(bool fp8) {
   for (int k = 0; k < 8; ++k) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        fp8 ? kernel_of<true>(k & 1, k & 2, k & 4) : kernel_of<false>(k & 1, k & 2, k & 4), cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem_bytes());
+    const void* f = fp8 ? kernel_of<true>(k & 1, k & 2, k & 4) : kernel_of<false>(k & 1, k & 2, k & 4);
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem_bytes());
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-cudaError_t tree_occupancy(int* blocks_per_sm) {
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel_of<false>(false, false, false),
-                                                       kTcThreads, (size_t)tree_smem_bytes());
+cudaError_t tree_occupancy(bool fp8, int* blocks_per_sm) {
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+      blocks_per_sm, fp8 ? kernel_of<true>(false, false, false) : kernel_of<false>(false, false, false),
+      fp8 ? kThreadsFp8 : kTcThreads, (size_t)tree_smem_bytes());
 }
 
 cudaError_t launch_tree(const TreeArgs& a, int grid, int64_t most_tokens, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kTcThreads);
+  cfg.blockDim = dim3(a.fp8 ? kThreadsFp8 : kTcThreads);
   cfg.dynamicSmemBytes = (size_t)tree_smem_bytes();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1154,7 +1256,8 @@ cudaError_t launch_tree(const TreeArgs& a, int grid, int64_t most_tokens, cudaSt
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void* args[] = {const_cast<TreeArgs*>(&a)};
-  const bool cap = a.cap_log2 != 0.f, slopes = a.slopes != nullptr, halves = most_tokens < kStreamRounds * kTreeRound;
+  const bool cap = a.cap_log2 != 0.f, slopes = a.slopes != nullptr;
+  const bool halves = most_tokens < kStreamRounds * kTreeRound;
   return cudaLaunchKernelExC(
       &cfg, a.fp8 ? kernel_of<true>(cap, slopes, halves) : kernel_of<false>(cap, slopes, halves), args);
 }

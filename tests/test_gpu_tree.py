@@ -1,5 +1,7 @@
 """Attention of drafted tokens over a paged cache, against the formula in 64 bits."""
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -508,6 +510,28 @@ def test_e4m3_what_is_masked_may_hold_anything(split):
     assert torch.isnan(out[3]).all() and torch.isnan(lse[3]).all()
     assert (out[mine].double() - ro[mine]).abs().max() <= 1.1 * 2 ** -8 * 8 and c.dec.device_error() == 0
     assert (lse[mine].double() - rl[mine]).abs().max() <= 2e-4
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+def test_first_context_of_a_process(kv_dtype):
+    code = f"""
+import paged_kv_decode_host_gb300 as pkd
+d = pkd.BatchTreeDecodeWithPagedKVCache(8, 2, 128, 16, max_tokens=4, max_num_pages=4, num_pages=4, kv_dtype={kv_dtype!r})
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=120)
+
+
+def test_e4m3_every_value():
+    # a row of one token is that token's values, whatever they are
+    c = Case(hq=2, hkv=2, lens=(4,), drafts=(4,), window=1, causal=True, fp8=True)
+    raw = c.kv.view(torch.uint8)
+    page = int(c.indices[0])
+    raw[page, 0] = 0
+    raw[page, 1, :4] = torch.arange(1024, device="cuda").fmod(256).to(torch.uint8).view(4, 2, D)
+    out, lse = c.run()
+    want = (c.kv[page, 1, :4].float() * 0.25).bfloat16()
+    assert torch.equal(out.isnan(), want.isnan()) and int(want.isnan().sum()) == 8
+    assert torch.equal(out.nan_to_num(), want.nan_to_num()) and c.dec.device_error() == 0
 
 
 def test_e4m3_captured_and_as_bytes():
