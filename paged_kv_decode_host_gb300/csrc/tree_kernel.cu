@@ -505,7 +505,9 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return (w & 0x7f7f7f
 // integer operations (some 50 for 512 values), so the tiles are dealt out such that
 // each scheduler's warps have as many.  Not inlined: with this loop unrolled, twice, the
 // whole kernel waited for its instructions.
-__device__ __noinline__ void widen_round(const uint8_t* narrow, uint8_t* wide, int tiles, int first, int step,
+// Returns whether one of the values was a NaN (kNan: they stay NaNs).
+template <bool kNan>
+__device__ __noinline__ bool widen_tiles(const uint8_t* narrow, uint8_t* wide, int tiles, int first, int step,
                                          int lane) {
   uint32_t from[2], to[2][2];   // of tokens x and x + 4 of 8
   bool turn[2];
@@ -518,34 +520,37 @@ __device__ __noinline__ void widen_round(const uint8_t* narrow, uint8_t* wide, i
     to[u][0] = row + ((piece + (q >> 2)) ^ x) * 16;
     to[u][1] = row + ((piece + 1 - (q >> 2)) ^ x) * 16;
   }
+  uint32_t odd = 0;
 #pragma unroll 1
   for (int tile = first; tile < tiles; tile += step) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {   // 8 tokens
       uint4 v[2];
-      uint32_t odd = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint4 x = lds16(from[u] + tile * 16 * kHeadDim + h * 8 * kHeadDim);
         v[u] = turn[u] ? make_uint4(x.z, x.w, x.x, x.y) : x;   // the piece to write first
-        odd |= nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w);
+        if (!kNan) odd |= nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w);
       }
-      const bool nan = __any_sync(kFull, (odd & 0x80808080u) != 0);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        uint2 w[4] = {widen4(v[u].x), widen4(v[u].y), widen4(v[u].z), widen4(v[u].w)};
-        if (nan) {
-          w[0] = make_uint2(widen2(v[u].x), widen2(v[u].x >> 16));
-          w[1] = make_uint2(widen2(v[u].y), widen2(v[u].y >> 16));
-          w[2] = make_uint2(widen2(v[u].z), widen2(v[u].z >> 16));
-          w[3] = make_uint2(widen2(v[u].w), widen2(v[u].w >> 16));
-        }
+        const uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint2 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = kNan ? make_uint2(widen2(in[k]), widen2(in[k] >> 16)) : widen4(in[k]);
         const uint32_t at = tile * kTileBytes + h * 2048;
         sts16(to[u][0] + at, make_uint4(w[0].x, w[0].y, w[1].x, w[1].y));
         sts16(to[u][1] + at, make_uint4(w[2].x, w[2].y, w[3].x, w[3].y));
       }
     }
   }
+  return __any_sync(kFull, (odd & 0x80808080u) != 0);
+}
+__device__ __forceinline__ void widen_round(const uint8_t* narrow, uint8_t* wide, int tiles, int first, int step,
+                                            int lane) {
+  if (widen_tiles<false>(narrow, wide, tiles, first, step, lane))
+    widen_tiles<true>(narrow, wide, tiles, first, step, lane);
 }
 
 struct TreeSmem {
