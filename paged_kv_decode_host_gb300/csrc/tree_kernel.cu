@@ -465,9 +465,9 @@ constexpr int kStreamRounds = 4;
 // two rounds of each, and the producers' warps widen them to bf16 (exact) into rings
 // of two rounds: the same 192 KB.
 constexpr int kNarrowBytes = kRoundTok * kHeadDim;   // K or V of a round
-// Three warps widen K, three V: the producer and two of a fourth warpgroup (the
-// producers alone took 6,000 cycles a round).  128 registers each then, which spills a
-// few words.
+// Three warps widen K, three V: the producer and two of a fourth warpgroup (64 ragged
+// requests x 16 drafts 324 us with the producers alone, 212 so; 159 over bf16, 145 if
+// nothing were widened).  128 registers each then, which spills a few words.
 constexpr int kWideners = 3;
 constexpr int kThreadsFp8 = kTcThreads + 128;
 
@@ -484,7 +484,7 @@ __device__ __forceinline__ void sts16(uint32_t at, const uint4& v) {
 // Four e4m3 values to two bf16 pairs where none is a NaN: exponent and mantissa under
 // bf16's exponent, times 2^120 (7 and 127 are the types' biases), subnormals too.
 // Integer operations and one product a pair: conversion instructions (half, float,
-// bf16) bound whole rounds, at 5,700 cycles.
+// bf16) bound rounds at 5,700 cycles.
 __device__ __forceinline__ uint2 widen4(uint32_t four) {
   uint32_t r[2];
 #pragma unroll
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
     // page `at_page` of the request, from token `next_at` of it on; they move on by one
     // round each time (a division takes as long as two copies), and the page ids
     // (`next`) are on their way a round ahead.
-    int next_it = it0, next_k = 0, nr = 0, from = 0, to = 0, head = 0;
+    int next_it = it0, next_k = 0, nr = 0, from = 0, to = 0, head = 0, q_row = 0;
     int tile = 0, ntiles = 0, at_page = 0, next_at = 0, next = 0;
     const int32_t* pages = nullptr;
     uint64_t policy = first;
@@ -659,6 +659,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
       from = item[1];
       to = item[2];
       head = item[7];
+      q_row = entry[0] + item[5];
       // (more than one row block reads these tokens: they may stay in L2)
       policy = entry[1] > tile_tokens ? normal : first;
       pages = a.sched + a.off_pages + entry[3];
@@ -725,7 +726,8 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
       issue(narrow + issued * kNarrowBytes, &more->narrow[c][issued]);
     for (int it = it0; it < it1 && ok; ++it) {
       const int32_t* item = a.sched + a.off_items + (int64_t)it * kItemWords;
-      const int tb = item[1], te = item[2], rounds = rounds_of(tb, te);
+      // (without narrow rounds ahead, the queue's next round is this item's first)
+      const int tb = kFp8 ? item[1] : from, te = kFp8 ? item[2] : to, rounds = rounds_of(tb, te);
       // the item's queries (the previous item's score MMAs must be done)
       if (c == 0 && it > it0 &&
           !warp_wait(&sh->qfree, (uint32_t)((it - it0 - 1) & 1), abort_flag, a.err, lane)) {
@@ -734,10 +736,11 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
       }
       if (c == 0) ++nq;
       if (c == 0 && me) {
-        const int row0 = requests[item[0] * kRequestWords] + item[5];
+        const int row0 = kFp8 ? requests[item[0] * kRequestWords] + item[5] : q_row;
         mbar_arrive_expect_tx(&sh->qfull, (uint32_t)kQBytes);
         for (int h = 0; h < 2; ++h)
-          tensor_copy_g2s(sQ + h * (kQBytes / 2), &a.q_map, 0, h, 0, item[7], row0, &sh->qfull, first);
+          tensor_copy_g2s(sQ + h * (kQBytes / 2), &a.q_map, 0, h, 0, kFp8 ? item[7] : head, row0, &sh->qfull,
+                          first);
       }
       __syncwarp();
       for (int k = 0; k < rounds; ++k, ++st) {

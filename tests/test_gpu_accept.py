@@ -242,3 +242,67 @@ def test_three_steps_with_drafts(path, monkeypatch):
                 assert torch.equal(got[1], vs)
                 assert ((got[0] - ks).abs() <= 2.0 ** -8 * ks.abs() + 2.0 ** -18 * 8).all()
         assert dec.device_error() == 0
+
+
+def test_two_steps_over_an_e4m3_cache():
+    """Prompts appended to an E4M3 cache, trees of drafts over it, the accepted moved, and one more token:
+    every result is the attention over what the cache holds, and the cache holds the accepted rows."""
+    hq, hkv, D, page, pool = 8, 2, 128, 32, 12
+    g = torch.Generator("cuda").manual_seed(11)
+    rope = pkd.RotaryPositions([10_000.0 ** (-i / 64) for i in range(64)])
+    ids = [[7, 2, 9, 4], [0, 11, 5, 3]]
+    kv = torch.zeros(pool, 2, hkv, page, D, dtype=torch.float8_e4m3fn, device="cuda")
+    scales = dict(k_scale=2 ** -5, v_scale=2 ** -6)
+    dec = pkd.BatchTreeDecodeWithPagedKVCache(hq, hkv, D, page, max_tokens=100, max_num_pages=8, num_pages=pool,
+                                              kv_dtype="e4m3", kv_layout="HND")
+
+    def held(b, n):
+        x = kv.view(torch.uint8)[torch.tensor(ids[b], device="cuda")].view(torch.float8_e4m3fn).double()
+        x = x.transpose(2, 3).transpose(0, 1).reshape(2, -1, hkv, D)[:, :n]
+        return x[0] * scales["k_scale"], x[1] * scales["v_scale"]
+
+    def step(ctx, counts, parents):
+        lens = [a + n for a, n in zip(ctx, counts)]
+        pages = [-(-n // page) for n in lens]
+        indptr = np.concatenate([[0], np.cumsum(pages)]).astype(np.int32)
+        indices = np.concatenate([ids[b][:pages[b]] for b in range(2)]).astype(np.int32)
+        last = np.array([n - page * (c - 1) for n, c in zip(lens, pages)], np.int32)
+        tables = [torch.from_numpy(x).cuda() for x in (indptr, indices, last)]
+        q_indptr = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        mask, depths = (None, None) if parents is None else pkd.tree_mask(q_indptr, parents)
+        n = int(q_indptr[-1])
+        deep = np.concatenate([np.arange(c) for c in counts]) if parents is None else depths
+        rows = torch.from_numpy(np.repeat([0, 1], counts)).int().cuda()
+        places = torch.from_numpy(np.concatenate([np.arange(a, b) for a, b in zip(ctx, lens)])).int().cuda()
+        at = torch.from_numpy(np.repeat(ctx, counts) + deep).int().cuda()
+        both = torch.randn(n, hq + 2 * hkv, D, generator=g, device="cuda").bfloat16()
+        q, _ = pkd.rotate_append_kv(both[:, :hq], both[:, hq:hq + hkv], both[:, hq + hkv:], rope, rows, places, *tables,
+                                    kv, rope_positions=at, kv_layout="HND", **scales)
+        dec.plan(q_indptr, indptr, indices, last, causal=parents is None)
+        d_mask = None if mask is None else torch.from_numpy(mask).cuda()
+        out, lse = dec.run(q, kv, mask=d_mask, **scales)
+        for b in range(2):
+            k, v = (x.repeat_interleave(hq // hkv, 1) for x in held(b, lens[b]))
+            for i in range(counts[b]):
+                row = int(q_indptr[b]) + i
+                sees = [t < ctx[b] or (t - ctx[b] <= i if parents is None else
+                                       bool(int(mask[row, 0]) >> (t - ctx[b]) & 1)) for t in range(lens[b])]
+                x = torch.einsum("hd,thd->ht", q[row].double(), k[sees]) * D ** -0.5
+                ref = torch.einsum("ht,thd->hd", x.softmax(-1), v[sees])
+                # (P and the output in bf16, values up to 6)
+                assert (out[row].double() - ref).abs().max() <= 1.1 * 2 ** -8 * 12
+                assert (lse[row].double() - x.logsumexp(-1)).abs().max() <= 2e-4
+        assert dec.device_error() == 0
+        return tables, lens
+
+    step([0, 0], [50, 33], None)
+    drafts = [6, 9]
+    tables, lens = step([50, 33], drafts, np.array([-1, 0, 0, 2, 3, -1] + [-1, 0, 1, 0, 3, 4, 5, 6, -1], np.int32))
+    before = [held(b, lens[b]) for b in range(2)]
+    paths = [[0, 2, 3], [0, 3, 4, 6]]
+    pkd.accept_kv([kv], torch.tensor([paths[0] + [-1], paths[1]], dtype=torch.int32, device="cuda"),
+                  torch.tensor(drafts, dtype=torch.int32, device="cuda"), *tables, kv_layout="HND")
+    for b, ctx in enumerate((50, 33)):
+        now, rows = held(b, ctx + len(paths[b])), list(range(ctx)) + [ctx + j for j in paths[b]]
+        assert all(torch.equal(x, y[rows]) for x, y in zip(now, before[b]))
+    step([53, 37], [1, 1], None)
