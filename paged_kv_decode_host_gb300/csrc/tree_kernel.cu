@@ -381,7 +381,9 @@ __device__ __noinline__ void cap64_any(float scale, float cap, uint32_t s_addr, 
     for (int j = 0; j < 16; ++j) v[c + j] = __float_as_uint(capped(__uint_as_float(x[j]), scale, cap));
   }
 }
-__device__ __forceinline__ void cap64(const TreeArgs& a, uint32_t s_addr, uint32_t (&v)[2][32]) {
+// (counts: this row is one, and what it does not see is 0 here.  Columns that no
+// product wrote hold what was there before, and would decide otherwise every run.)
+__device__ __forceinline__ void cap64(const TreeArgs& a, bool counts, uint32_t s_addr, uint32_t (&v)[2][32]) {
   F2 c[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) c[k] = f2(a.cap_poly[k], a.cap_poly[k]);
@@ -398,7 +400,7 @@ __device__ __forceinline__ void cap64(const TreeArgs& a, uint32_t s_addr, uint32
       v[q][j] = __float_as_uint(lo);
       v[q][j + 1] = __float_as_uint(hi);
     }
-  if (__any_sync(kFull, fmaxf(most[0], most[1]) > a.cap_bound)) {
+  if (__any_sync(kFull, counts && fmaxf(most[0], most[1]) > a.cap_bound)) {
     uint32_t w[64];
     cap64_any(a.scale_log2, a.cap_log2, s_addr, w);
 #pragma unroll
@@ -407,6 +409,14 @@ __device__ __forceinline__ void cap64(const TreeArgs& a, uint32_t s_addr, uint32
       v[1][j] = w[32 + j];
     }
   }
+}
+
+// 0 for the products with tokens t0 .. t0 + 31 that the row does not see.
+__device__ __forceinline__ void hide32(const Row& me, const Span& sp, int t0, uint32_t (&v)[32]) {
+  const uint32_t vis = sp.valid ? (uint32_t)visible(me, t0, sp.te) : 0u;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (!(vis & (1u << j))) v[j] = 0u;
 }
 
 // 32 scores of tokens t0 .. t0 + 31 where some are biased by other distances
@@ -1031,7 +1041,11 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
           tmem_wait_ld();
           float sc = a.scale_log2, step = 0.f;
           if constexpr (kCap) {
-            cap64(a, s_col + 64 * h, sv);
+            if (special) {
+              hide32(me, sp, t0, sv[0]);
+              hide32(me, sp, t0 + 32, sv[1]);
+            }
+            cap64(a, valid, s_col + 64 * h, sv);
             sc = 1.f;
           }
           if (pass == last) {   // S is read: the buffer may be refilled

@@ -553,6 +553,27 @@ def test_e4m3_captured_and_as_bytes():
             c.dec.run(c.q, c.kv, mask=c.mask, **bad)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw", [dict(), dict(window=1), dict(slopes=True), dict(causal=True, window=130)])
+def test_same_bits_whatever_ran_before(kw, fp8):
+    # capped scores choose their way by their size: by those that count only, not by what other
+    # launches, or tokens and rows that nobody sees, left behind
+    c = Case(lens=(863, 21, 70), drafts=(40, 17, 5), cap=30.0, fp8=fp8, rows=70, **kw)
+    other = [Case(lens=(500, 900), drafts=(30, 60), magnitude=m, seed=3) for m in (30.0, 1.0)]
+    first = c.run()
+    for k in range(6):
+        other[k & 1].run()
+        if k == 3:   # rows behind the plan's, slots behind the requests' ends
+            c.q[62:] = 1e6
+            raw = c.kv.view(torch.uint8)
+            for b in range(3):
+                for t in range(c.lens[b], 16 * -(-c.lens[b] // 16)):
+                    raw[int(c.indices[c.indptr[b] + t // 16]), :, t % 16] = 0x7A   # 320, or 3e35
+        again = c.run()
+        assert torch.equal(first[0][:62], again[0][:62]) and torch.equal(first[1][:62], again[1][:62])
+    assert c.dec.device_error() == 0
+
+
 def test_pools_past_32_bits():
     """Pages whose elements lie past 2^31."""
     c = Case(hq=8, hkv=8, lens=(70, 40), drafts=(5, 3), window=60)
