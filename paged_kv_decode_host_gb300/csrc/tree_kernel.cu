@@ -381,8 +381,8 @@ __device__ __noinline__ void cap64_any(float scale, float cap, uint32_t s_addr, 
     for (int j = 0; j < 16; ++j) v[c + j] = __float_as_uint(capped(__uint_as_float(x[j]), scale, cap));
   }
 }
-// (counts: this row is one, and what it does not see is 0 here.  Columns that no
-// product wrote hold what was there before, and would decide otherwise every run.)
+// (counts: this row is one, and what no row of the run sees is 0 here: columns that
+// no product wrote hold what was there before, and would decide otherwise every run.)
 __device__ __forceinline__ void cap64(const TreeArgs& a, bool counts, uint32_t s_addr, uint32_t (&v)[2][32]) {
   F2 c[4];
 #pragma unroll
@@ -411,19 +411,18 @@ __device__ __forceinline__ void cap64(const TreeArgs& a, bool counts, uint32_t s
   }
 }
 
-// 0 for the products with tokens t0 .. t0 + 31 that the row does not see.
-__device__ __forceinline__ void hide32(const Row& me, const Span& sp, int t0, uint32_t (&v)[32]) {
-  const uint32_t vis = sp.valid ? (uint32_t)visible(me, t0, sp.te) : 0u;
+// `value` for those of 32 scores that the row does not see.
+__device__ __forceinline__ void hide32(uint32_t vis, float value, uint32_t (&v)[32]) {
 #pragma unroll
   for (int j = 0; j < 32; ++j)
-    if (!(vis & (1u << j))) v[j] = 0u;
+    if (!(vis & (1u << j))) v[j] = __float_as_uint(value);
 }
 
 // 32 scores of tokens t0 .. t0 + 31 where some are biased by other distances
 // than the place in the cache says (drafts), or masked: in units of log2 where
 // there is a cap or a slope, else as they are.  (v: capped already)
 template <bool kCap, bool kSlopes>
-__device__ __forceinline__ void shape32(const TreeArgs& a, const Row& me, const Span& sp, int t0,
+__device__ __forceinline__ void shape32(const TreeArgs& a, const Row& me, const Span& sp, int t0, uint32_t vis,
                                         uint32_t (&v)[32]) {
   if constexpr (kSlopes) {
     const float d0 = (float)((int64_t)sp.ctx + me.depth - t0);   // distance to the first one's token
@@ -437,10 +436,7 @@ __device__ __forceinline__ void shape32(const TreeArgs& a, const Row& me, const 
       v[j] = __float_as_uint(fmaf(-sp.slope2, d, __uint_as_float(v[j]) * sc));
     }
   }
-  const uint32_t vis = sp.valid ? (uint32_t)visible(me, t0, sp.te) : 0u;
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (!(vis & (1u << j))) v[j] = __float_as_uint(-CUDART_INF_F);
+  hide32(vis, -CUDART_INF_F, v);
 }
 
 // Weights 2^(v sc + b + j step) of 32 scores (plain: 2^v): P in 16 words at
@@ -1041,9 +1037,12 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
           tmem_wait_ld();
           float sc = a.scale_log2, step = 0.f;
           if constexpr (kCap) {
-            if (special) {
-              hide32(me, sp, t0, sv[0]);
-              hide32(me, sp, t0 + 32, sv[1]);
+            // (where some columns hold no token of this run, or one that no row sees;
+            // a draft that some rows do not see is this run's all the same)
+            if (te - t0 < 64 || t0 < sp.reach) {
+              const uint64_t live = valid ? visible(me, t0, te) : 0u;
+              hide32((uint32_t)live, 0.f, sv[0]);
+              hide32((uint32_t)(live >> 32), 0.f, sv[1]);
             }
             cap64(a, valid, s_col + 64 * h, sv);
             sc = 1.f;
@@ -1054,8 +1053,9 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
             if (lane == 0) mbar_arrive(&sh->sfree[b]);
           }
           if (special) {
-            shape32<kCap, kSlopes>(a, me, sp, t0, sv[0]);
-            shape32<kCap, kSlopes>(a, me, sp, t0 + 32, sv[1]);
+            const uint64_t vis = valid ? visible(me, t0, te) : 0u;
+            shape32<kCap, kSlopes>(a, me, sp, t0, (uint32_t)vis, sv[0]);
+            shape32<kCap, kSlopes>(a, me, sp, t0 + 32, (uint32_t)(vis >> 32), sv[1]);
             if (kSlopes) sc = 1.f;
           } else if (kSlopes) {
             step = sp.slope2;
