@@ -12,9 +12,9 @@ namespace pkd {
 constexpr int kTreeRows = 128;       // query rows of a tile: 128 / g tokens x g heads of a KV head
 constexpr int kTreeRound = 128;      // tokens per round of the kernel; plans cut at multiples of it
 // An item's fixed cost and the split floor, in tokens.  Measured with 512 / 128,
-// 256 / 256 and 128 / 128: 24 ragged requests x 7 drafts with slopes 38.7, 44.1
-// and 43.6 us; 16 x 61 drafts of 64 heads 190, 197 and 199; one of 517 tokens
-// 10.1, 10.5 and 10.2.
+// 256 / 128, 1024 / 128 and 768 / 256: 24 ragged requests x 7 drafts with slopes
+// 36.4, 38.3, 36.9 and 36.4 us; 16 x 61 drafts of 64 heads 123.6, 134.1, 123.5 and
+// 123.4; one of 517 tokens 9.1, 9.0, 9.0 and 9.8.
 constexpr int kTreeAlpha = 512;
 constexpr int kTreeMinChunk = 128;
 // Tokens that several row blocks read, in bytes, from which on L2 does not hold

@@ -574,6 +574,25 @@ def test_same_bits_whatever_ran_before(kw, fp8):
     assert c.dec.device_error() == 0
 
 
+def test_two_contexts_at_once():
+    # each on a stream of its own, one of them an E4M3 cache, with copies of the plans on the way
+    cases = [Case(lens=(3000, 700, 90), drafts=(40, 9, 3), cap=30.0, seed=1),
+             Case(lens=(2500, 60, 1200), drafts=(17, 5, 70), slopes=True, fp8=True, seed=2)]
+    want = [[x.clone() for x in c.run()] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for k in range(12):
+        for c, s, g in zip(cases, streams, got):
+            with torch.cuda.stream(s):
+                if k % 4 == 3:
+                    c.plan()
+                g.append(c.run())
+    torch.cuda.synchronize()
+    for c, w, g in zip(cases, want, got):
+        assert all(torch.equal(x, y) for one in g for x, y in zip(one, w)) and c.dec.device_error() == 0
+
+
 def test_pools_past_32_bits():
     """Pages whose elements lie past 2^31."""
     c = Case(hq=8, hkv=8, lens=(70, 40), drafts=(5, 3), window=60)
