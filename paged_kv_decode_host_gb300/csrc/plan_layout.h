@@ -28,14 +28,14 @@ inline bool is_tree(const pkd_config& c) { return (c.flags & PKD_FLAG_TREE) != 0
 // Tree plans: max_batch counts query tokens, and requests.  Items are row
 // blocks (at most one per token) cut at most once between two neighbouring
 // stretches, once per KV head; k cuts leave a block in k + 1 <= 2 k parts, and
-// a part has a slot per token of its block: twice as many are held, for plans
-// that cut blocks into pieces.  Merge units are tokens.
+// a part has a slot per token of its block (plans that cut blocks into pieces
+// use as many pieces as find room).  Merge units are tokens.
 inline Layout tree_layout(const pkd_config& c, int64_t n_cta) {
   const int64_t stretches = std::max<int64_t>(1, n_cta / c.num_kv_heads);
   const int64_t rows = kTreeRows / (c.num_qo_heads / c.num_kv_heads);
   Layout L{};
   L.max_items = (int64_t)c.num_kv_heads * (c.max_batch + stretches) + 8;
-  L.max_slots = 4 * (stretches - 1) * rows;
+  L.max_slots = 2 * (stretches - 1) * rows;
   L.cta_indptr = H_WORDS;
   L.items = align_up(L.cta_indptr + n_cta + 1, 8);
   L.units = L.items + L.max_items * kItemWords;
