@@ -39,11 +39,12 @@
 // What bounds it: with few rows per KV head memory (64 ragged requests up to 8,192
 // tokens x 16 drafts, 32 heads on 8: 1.06 GB in 160 us, 6.6 TB/s); with full tiles
 // the round, about 1,750 cycles for 1,024 of tensor products (16 requests x 61 drafts
-// of 64 heads: 155 GFLOP in 125 us, 1.24 PFLOP/s; 140 in a long row of calls, where
+// of 64 heads: 155 GFLOP in 123 us, 1.26 PFLOP/s; 141 in a long row of calls, where
 // the power limit takes the clock from 2,070 to 1,680 MHz), in which the tensor cores
-// wait for the softmax; a capped score's polynomial adds 700.  On the way there: two copies
-// instead of one per 16 tokens 159 -> 141 us, a lone thread that forms descriptors
-// 500 cycles a round, waits that look at the clock at once 139 -> 131.  Tried and
+// wait for the softmax; a capped score's polynomial adds 700.  On the way there: one
+// copy instead of two per 16 tokens 159 -> 141 us; descriptors stepped by constants,
+// by an elected thread, 900 cycles of issue a round less; waits whose first tries do
+// not look at the clock 139 -> 131.  Tried and
 // slower: an O of its own for each stream of rounds; two tiles per item; weights
 // under the last base before the round's largest score is known (they mend too
 // often what they save); releasing S before its scores are capped.
