@@ -473,7 +473,7 @@ constexpr int kStreamRounds = 4;
 // of two rounds: the same 192 KB.
 constexpr int kNarrowBytes = kRoundTok * kHeadDim;   // K or V of a round
 // Three warps widen K, three V: the producer and two of a fourth warpgroup (64 ragged
-// requests x 16 drafts 324 us with the producers alone, 212 so; 159 over bf16, 145 if
+// requests x 16 drafts 324 us with the producers alone, 175 so; 159 over bf16, 145 if
 // nothing were widened).  128 registers each then, which spills a few words.
 constexpr int kWideners = 3;
 constexpr int kThreadsFp8 = kTcThreads + 128;
@@ -488,33 +488,15 @@ __device__ __forceinline__ void sts16(uint32_t at, const uint4& v) {
                : "memory");
 }
 
-// Four e4m3 values to two bf16 pairs where none is a NaN: exponent and mantissa under
-// bf16's exponent, times 2^120 (7 and 127 are the types' biases), subnormals too.
-// Integer operations and one product a pair: conversion instructions (half, float,
-// bf16) bound rounds at 5,700 cycles.
-__device__ __forceinline__ uint2 widen4(uint32_t four) {
-  uint32_t r[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const uint32_t x = __byte_perm(four, 0u, u == 0 ? 0x1404 : 0x3424);   // the bytes on top of 16 bits each
-    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[u]) : "r"(y), "r"(0x7b807b80u));
-  }
-  return make_uint2(r[0], r[1]);
-}
-// some byte of w is 0x7f or 0xff: bit 7 of a byte
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
-
 // Tiles first, first + step, ... of a round from e4m3 (chunk c of 16 bytes of token t
 // holds dims 16 (c ^ (t & 7)) on, as the copy swizzles them) to bf16 as the products
 // want them.  8 lanes take a token; those of one half of its dims write their second
 // piece first, so that the 8 pieces written at a time lie in different banks.  Bound by
-// integer operations (some 50 for 512 values), so the tiles are dealt out such that
-// each scheduler's warps have as many.  Not inlined: with this loop unrolled, twice, the
-// whole kernel waited for its instructions.
-// Returns whether one of the values was a NaN (kNan: they stay NaNs).
-template <bool kNan>
-__device__ __noinline__ bool widen_tiles(const uint8_t* narrow, uint8_t* wide, int tiles, int first, int step,
+// the conversions, so the tiles are dealt out such that each scheduler's warps have as
+// many.  (Integer operations and a product by 2^120 were slower the more values they
+// took: 181 us with none, 193, 200, 207 and 212 with a quarter, half, three quarters and
+// all.)  Not inlined: unrolled in two places, the whole kernel waited for instructions.
+__device__ __noinline__ void widen_round(const uint8_t* narrow, uint8_t* wide, int tiles, int first, int step,
                                          int lane) {
   uint32_t from[2], to[2][2];   // of tokens x and x + 4 of 8
   bool turn[2];
@@ -527,37 +509,20 @@ __device__ __noinline__ bool widen_tiles(const uint8_t* narrow, uint8_t* wide, i
     to[u][0] = row + ((piece + (q >> 2)) ^ x) * 16;
     to[u][1] = row + ((piece + 1 - (q >> 2)) ^ x) * 16;
   }
-  uint32_t odd = 0;
 #pragma unroll 1
   for (int tile = first; tile < tiles; tile += step) {
+    uint4 v[4];   // tokens x, x + 4, x + 8, x + 12
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {   // 8 tokens
-      uint4 v[2];
+    for (int u = 0; u < 4; ++u) v[u] = lds16(from[u & 1] + tile * 16 * kHeadDim + (u >> 1) * 8 * kHeadDim);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint4 x = lds16(from[u] + tile * 16 * kHeadDim + h * 8 * kHeadDim);
-        v[u] = turn[u] ? make_uint4(x.z, x.w, x.x, x.y) : x;   // the piece to write first
-        if (!kNan) odd |= nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        uint2 w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = kNan ? make_uint2(widen2(in[k]), widen2(in[k] >> 16)) : widen4(in[k]);
-        const uint32_t at = tile * kTileBytes + h * 2048;
-        sts16(to[u][0] + at, make_uint4(w[0].x, w[0].y, w[1].x, w[1].y));
-        sts16(to[u][1] + at, make_uint4(w[2].x, w[2].y, w[3].x, w[3].y));
-      }
+    for (int u = 0; u < 4; ++u) {
+      const bool t = turn[u & 1];   // the piece to write first
+      const uint4 x = t ? make_uint4(v[u].z, v[u].w, v[u].x, v[u].y) : v[u];
+      const uint32_t at = tile * kTileBytes + (u >> 1) * 2048;
+      sts16(to[u & 1][0] + at, make_uint4(widen2(x.x), widen2(x.x >> 16), widen2(x.y), widen2(x.y >> 16)));
+      sts16(to[u & 1][1] + at, make_uint4(widen2(x.z), widen2(x.z >> 16), widen2(x.w), widen2(x.w >> 16)));
     }
   }
-  return __any_sync(kFull, (odd & 0x80808080u) != 0);
-}
-__device__ __forceinline__ void widen_round(const uint8_t* narrow, uint8_t* wide, int tiles, int first, int step,
-                                            int lane) {
-  if (widen_tiles<false>(narrow, wide, tiles, first, step, lane))
-    widen_tiles<true>(narrow, wide, tiles, first, step, lane);
 }
 
 struct TreeSmem {
