@@ -25,7 +25,7 @@
 //  * masked scores are replaced, never added to, so what K holds there plays
 //    no part.  P is 0 there, and 0 x V is 0 only for finite V: a result that
 //    is not finite while some token that its row does not see has a value
-//    that is not is summed again over the tokens seen (redo_row);
+//    that is not is summed again over the tokens seen (redo_rows);
 //  * rows that have seen nothing keep the base -inf and a sum of 0;
 //  * tanh(x) is a polynomial up to 0.4, within 2^-23 of itself; past that 1 - 2
 //    / (1 + e^2x), an exponential and a reciprocal, within about 2^-22; the
@@ -100,10 +100,19 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // tc_wait whose first tries are the whole warp's, with a vote at once: a branch
-// that the compiler knows to be uniform, and no look at the clock.
+// that the compiler knows to be uniform, and no look at the clock.  Behind the
+// abort flag stands a count that a recomputation (redo_rows) raises as it goes: a
+// wait that runs out while it rises is for that, however long it takes, and
+// starts over (the recomputation is a loop over its item's tokens, which ends).
 __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err,
                                        int lane) {
-  return tc_wait(bar, parity, abort_flag, err, lane);
+  for (;;) {
+    const int before = abort_flag[1];
+    if (__all_sync(kFull, mbar_wait(bar, parity, abort_flag))) return true;
+    if (__any_sync(kFull, *abort_flag != 0 || abort_flag[1] == before)) break;
+  }
+  if (lane == 0) raise_error(err, abort_flag, PKD_DEV_ERR_TIMEOUT);
+  return false;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err,
                                           int lane) {
@@ -209,65 +218,113 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&f)[8]) 
   }
 }
 
-// out of 32 dims (from dim0) of one row, summed over the tokens that the row
-// sees with weights 2^(s - total), if one that it does not see has a value that
-// is not finite in these dims, or (wide: weights far above 1, whose sums pass
-// fp32's range for values past 2^(110 - cap in log2)) if all that it sees are
-// finite; else left as it is.  (A look at V before each product
-// took 5 to 10 % of a step of short requests; this is for caches that hold such
-// values, and takes about 3 us a token: 16 requests of 8,192 tokens x 16 drafts 41 ms.)
+// Are the 64 values from element `at` on finite?
 template <bool kFp8>
-__device__ __noinline__ void redo_row(const TreeArgs& a, const Row& r, const uint16_t* q, int first_page,
-                                      int head, int tb, int te, int dim0, float total, bool wide,
-                                      float slope2, uint32_t (&o)[32]) {
-  auto sees = [&](int t) { return (visible(r, t, te) & 1u) != 0; };
-  auto finite = [&](int t) {
-    const int64_t at = token_offset(a, first_page, head, t) + a.v_elems + dim0;
-    float bad = 0.f;
-    for (int d = 0; d < 32; d += 8) {
-      float v[8];
-      load8<kFp8>(a.kv, at + d, v);
-      for (int u = 0; u < 8; ++u) bad = fmaf(v[u], 0.f, bad);
-    }
-    return bad == 0.f;
+__device__ __forceinline__ bool finite64(const void* p, int64_t at) {
+  float bad = 0.f;
+#pragma unroll
+  for (int d = 0; d < 64; d += 8) {
+    float v[8];
+    load8<kFp8>(p, at + d, v);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) bad = fmaf(v[u], 0.f, bad);
+  }
+  return bad == 0.f;
+}
+
+// What redo_rows takes and gives, in memory: its registers are the round's as well
+// (held there, sums and arguments took 2 to 3 % of wide trees).
+struct Redo {
+  Row row;
+  bool mine;              // this lane's row is one
+  const uint16_t* q;      // its query (any, where it is none)
+  int first_page, head, tb, te, dim0, lane;
+  float total, slope2;
+  volatile int* beats;    // slow_wait's count
+  float o[64];
+};
+
+// 64 dims (from dim0) of the warp's rows, one a lane, summed over the tokens that a row
+// sees with weights 2^(s - total), where a token that it does not see has a value that
+// is not finite in these dims, or where all that it sees are finite (weights above 1,
+// whose sums pass fp32's range); false for rows whose result stands.  Tokens go by 8
+// (on one page): all lanes read the same K and V.  (A look at V before each product
+// took 5 to 10 % of a step of short requests; this is for caches that hold such values,
+// and takes 1.4 us a token: 16 requests of 8,192 tokens x 16 drafts 10 ms, and 29 where
+// every token read the rows' queries anew.)
+template <bool kFp8>
+__device__ __noinline__ bool redo_rows(const TreeArgs& a, Redo& in) {
+  const Row& r = in.row;
+  const int tb = in.tb, te = in.te, lane = in.lane, head = in.head, first_page = in.first_page;
+  bool mine = in.mine;
+  const auto beat = [&](int t0) {
+    if (lane == 0 && (t0 - tb) % 1024 == 0) atomicAdd(const_cast<int*>(in.beats), 1);
   };
-  bool again = false;   // a token that is not seen has a value that is not finite
-  for (int t = tb; t < min(te, min(r.first_seen, r.ctx)) && !again; ++t) again = !sees(t) && !finite(t);
-  for (int t = max(tb, r.ctx); t < te && !again; ++t) again = !sees(t) && !finite(t);
-  if (!again && wide) {
-    again = true;
-    for (int t = tb; t < te && again; ++t) again = !sees(t) || finite(t);
+  bool hidden = false, shown = false;   // a value that is not finite: of a token not seen, of one that is
+  for (int t0 = tb; t0 < te; t0 += 32) {
+    beat(t0);
+    const int t = t0 + lane;
+    const uint32_t odd = __ballot_sync(
+        kFull, t < te && !finite64<kFp8>(a.kv, token_offset(a, first_page, head, t) + a.v_elems + in.dim0));
+    if (odd == 0) continue;
+    const uint32_t see = mine ? (uint32_t)visible(r, t0, te) : 0u;
+    hidden = hidden || (odd & ~see) != 0;
+    shown = shown || (odd & see) != 0;
   }
-  if (!again) return;
-  float acc[32];
+  mine = mine && (hidden || !shown);
+  if (!__any_sync(kFull, mine)) return false;
+  for (int d = 0; d < 64; ++d) in.o[d] = 0.f;
+  for (int t0 = tb; t0 < te; t0 += 8) {
+    beat(t0);
+    const uint32_t see = mine ? (uint32_t)visible(r, t0, te) & 0xffu : 0u;
+    if (!__any_sync(kFull, see != 0)) continue;
+    // (of 8 tokens the last may lie behind the range, on its last page: read, not used)
+    const int64_t at = token_offset(a, first_page, head, t0);
+    float s[8];
 #pragma unroll
-  for (int d = 0; d < 32; ++d) acc[d] = 0.f;
-  for (int t = tb; t < te; ++t) {
-    if (!sees(t)) continue;
-    const int64_t at = token_offset(a, first_page, head, t);
-    float s = 0.f;
-#pragma unroll 4
+    for (int j = 0; j < 8; ++j) s[j] = 0.f;
+#pragma unroll 1
     for (int d = 0; d < kHeadDim; d += 8) {
-      float x[8], y[8];
-      load8<kFp8>(a.kv, at + d, x);
-      load8<false>(q, d, y);
+      float y[8];
+      load8<false>(in.q, d, y);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s = fmaf(x[u], y[u], s);
+      for (int j = 0; j < 8; ++j) {
+        float x[8];
+        load8<kFp8>(a.kv, at + j * a.token_elems + d, x);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s[j] = fmaf(x[u], y[u], s[j]);
+      }
     }
-    s = a.cap_log2 != 0.f ? capped(s, a.scale_log2, a.cap_log2) : s * a.scale_log2;
-    const int64_t away = t < r.ctx ? (int64_t)r.ctx + r.depth - t : (int64_t)r.depth - depth_of(r, t - r.ctx);
-    s = fmaf(-slope2, (float)away, s);
-    const float p = fast_exp2(s - total);
 #pragma unroll
-    for (int d = 0; d < 32; d += 8) {
-      float v[8];
-      load8<kFp8>(a.kv, at + a.v_elems + dim0 + d, v);
+    for (int j = 0; j < 8; ++j) {
+      const int t = t0 + j;
+      const float x = a.cap_log2 != 0.f ? capped(s[j], a.scale_log2, a.cap_log2) : s[j] * a.scale_log2;
+      const int64_t away = t < r.ctx              ? (int64_t)r.ctx + r.depth - t
+                           : (see >> j & 1u) != 0 ? (int64_t)r.depth - depth_of(r, t - r.ctx)
+                                                  : 0;
+      s[j] = fast_exp2(fmaf(-in.slope2, (float)away, x) - in.total);
+    }
+    const int64_t v = at + a.v_elems + in.dim0;
+#pragma unroll 1
+    for (int d = 0; d < 64; d += 8) {
+      float sum[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) acc[d + u] = fmaf(p, v[u], acc[d + u]);
+      for (int u = 0; u < 8; ++u) sum[u] = in.o[d + u];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float x[8];
+        load8<kFp8>(a.kv, v + j * a.token_elems + d, x);
+        if ((see >> j & 1u) != 0) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) sum[u] = fmaf(s[j], x[u], sum[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) in.o[d + u] = sum[u];
     }
   }
-#pragma unroll
-  for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(acc[d] * a.v_scale);
+  for (int d = 0; d < 64; ++d) in.o[d] *= a.v_scale;
+  return mine;
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -531,6 +588,7 @@ struct TreeSmem {
   uint64_t ready[2][4];       // base written by the stream's warp of a quadrant
   uint64_t narrow[2][2];      // K's, V's two rounds of an e4m3 cache landed,
   uint64_t widened[2][2];     // and read by the wideners beside the producer
+  int stop[2];                // the abort flag, and the count of slow_wait
 };
 constexpr int kSmemBytes = kQBytes + kTcStages * kStageBytes + (int)sizeof(TcSmem) + (int)sizeof(TreeSmem);
 static_assert(kSmemBytes <= 227 * 1024 && sizeof(TcSmem) % 4 == 0, "dynamic shared memory of one CTA");
@@ -554,7 +612,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
   uint8_t* stages = smem + kQBytes;
   TcSmem* sh = reinterpret_cast<TcSmem*>(stages + kTcStages * kStageBytes);
   TreeSmem* more = reinterpret_cast<TreeSmem*>(sh + 1);
-  volatile int* abort_flag = &sh->abort_flag;
+  volatile int* abort_flag = more->stop;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int it0 = a.sched[a.off_cta + blockIdx.x];
   const int it1 = a.sched[a.off_cta + blockIdx.x + 1];
@@ -584,7 +642,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
     }
     mbar_init(&sh->ofree, kSoftmaxWarps);
     mbar_init(&sh->fin, 2);
-    sh->abort_flag = 0;
+    more->stop[0] = more->stop[1] = 0;
     fence_mbar_init();
   }
   if (threadIdx.x == 32) {
@@ -1138,29 +1196,9 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
       const int64_t q_row = (int64_t)(q_first + i0 + i) * a.hq + hq;
       const int64_t p_row = ((int64_t)dst + (int64_t)i * stride) * a.hq + hq;   // its partial state
       const float inv = lt == 0.f ? 0.f : a.v_scale / lt;
-#pragma unroll 1
-      for (int cb = 64 * stream; cb < 64 * stream + 64; cb += 32) {
-        uint32_t o[32];
-        tmem_ld32(tq + kColO + cb, o);
-        tmem_wait_ld();
-        float odd = 0.f;   // NaN if a value is not finite
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float x = __uint_as_float(o[j]) * inv;
-          o[j] = __float_as_uint(x);
-          odd = fmaf(x, 0.f, odd);
-        }
-        if (valid && odd != odd) {
-          uint32_t again[32];   // (only this rare case needs the values in memory)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) again[j] = lt == 0.f ? 0u : o[j];
-          if (lt > 0.f)   // (a NaN: the scores')
-            redo_row<kFp8>(a, me, a.q + q_row * kHeadDim, first_page, head, tb, te, cb, m_used + log2f(lt),
-                           fixed, sp.slope2, again);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = again[j];
-        }
-        if (valid && dst < 0) {
+      // 32 dims of the row's result from cb on
+      const auto store = [&](int cb, const uint32_t* o) {
+        if (dst < 0) {
           uint16_t* op = a.out + q_row * kHeadDim + cb;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -1170,16 +1208,44 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
               w[j] = pack_bf16(__uint_as_float(o[16 * q + 2 * j]), __uint_as_float(o[16 * q + 2 * j + 1]));
             store32(op + 16 * q, w);
           }
-        } else if (valid) {
+        } else {
           float* op = a.o_part + p_row * kHeadDim + cb;
 #pragma unroll
           for (int q = 0; q < 4; ++q) store32(op + 8 * q, o + 8 * q);
         }
+      };
+      bool odd = false;   // a value is not finite (a NaN sum: the scores')
+#pragma unroll 1
+      for (int cb = 64 * stream; cb < 64 * stream + 64; cb += 32) {
+        uint32_t o[32];
+        tmem_ld32(tq + kColO + cb, o);
+        tmem_wait_ld();
+        float bad = 0.f;   // NaN if a value is not finite
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float x = lt == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
+          o[j] = __float_as_uint(x);
+          bad = fmaf(x, 0.f, bad);
+        }
+        odd = odd || (bad != bad && lt > 0.f);
+        if (valid) store(cb, o);
         __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ofree);
+      if (__any_sync(kFull, valid && odd)) {
+        Redo in;
+        in.row = me;
+        in.mine = valid && odd;
+        in.q = a.q + (valid ? q_row * kHeadDim : 0);
+        in.first_page = first_page, in.head = head, in.tb = tb, in.te = te;
+        in.dim0 = 64 * stream, in.lane = lane;
+        in.total = m_used + log2f(lt), in.slope2 = sp.slope2;
+        in.beats = abort_flag + 1;
+        if (redo_rows<kFp8>(a, in))
+          for (int c = 0; c < 64; c += 32) store(64 * stream + c, reinterpret_cast<const uint32_t*>(in.o + c));
+      }
       if (valid && stream == 0) {
         const float lse = lt == 0.f ? -CUDART_INF_F : (m_used + log2f(lt)) * kLn2;
         if (dst >= 0)
