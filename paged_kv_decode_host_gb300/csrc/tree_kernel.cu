@@ -1195,7 +1195,8 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
       const float lt = stream == 0 ? l + l_other : l_other + l;
       const int64_t q_row = (int64_t)(q_first + i0 + i) * a.hq + hq;
       const int64_t p_row = ((int64_t)dst + (int64_t)i * stride) * a.hq + hq;   // its partial state
-      const float inv = lt == 0.f ? 0.f : a.v_scale / lt;
+      // (not v_scale / lt: with a fixed base the sum may lie near either end of fp32's range)
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
       // 32 dims of the row's result from cb on
       const auto store = [&](int cb, const uint32_t* o) {
         if (dst < 0) {
@@ -1223,7 +1224,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
         float bad = 0.f;   // NaN if a value is not finite
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float x = lt == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
+          const float x = lt == 0.f ? 0.f : __uint_as_float(o[j]) * inv * a.v_scale;
           o[j] = __float_as_uint(x);
           bad = fmaf(x, 0.f, bad);
         }

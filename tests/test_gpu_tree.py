@@ -683,3 +683,17 @@ def test_values_near_the_largest_that_is_finite():
     ro, _ = c.reference()
     top = float(c.kv[:, 1].float().abs().max())
     assert (out.double() - ro).abs().max() <= 1.1 * 2 ** -8 * (top + float(ro.abs().max()))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("power", [-100, -60, 30])
+def test_scales_of_values_of_any_size(power, fp8):
+    # scores at their cap: sums of weights about 2^97, by which a small scale alone would vanish; powers
+    # of two change no bit of the result but its exponent
+    c = Case(lens=(3000, 500), drafts=(4, 3), cap=60.0, magnitude=60.0, seed=3, fp8=fp8, num_ctas=2)
+    c.scales = dict(k_scale=1.0, v_scale=1.0)
+    out, lse = (x.clone() for x in c.run())
+    c.scales["v_scale"] = 2.0 ** power
+    small, same = c.run()
+    assert torch.equal(small.double(), out.double() * 2.0 ** power) and torch.equal(lse, same)
+    assert out.double().abs().max() > 0.1 and c.dec.device_error() == 0
