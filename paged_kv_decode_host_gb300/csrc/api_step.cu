@@ -22,6 +22,13 @@ bool good_strides(int64_t token, int64_t head, int32_t n, int32_t heads, int32_t
          (heads <= 1 || (head % 8 == 0 && head >= least && head <= most));
 }
 
+RotateArgs::Divisor divisor(float scale) {
+  int e;
+  std::frexp(scale, &e);
+  const float lift = std::ldexp(1.f, e < -126 ? 127 : 1 - e), by = scale * lift;
+  return {lift, by, 1.f / by};
+}
+
 bool good_scale(float s) { return std::isfinite(s) && s > 0.f && std::isfinite(1.f / s); }
 
 }  // namespace
@@ -112,8 +119,8 @@ int pkd_rotate_append_kv(const void* q, int64_t q_token, int64_t q_head, void* q
   a.page_size = page_size;
   a.hq = num_qo_heads;
   a.hkv = num_kv_heads;
-  a.k_mul = 1.f / k_scale;
-  a.v_mul = 1.f / v_scale;
+  a.k_div = divisor(k_scale);
+  a.v_div = divisor(v_scale);
   a.fp8 = fp8 ? 1 : 0;
   a.err = err;
   return launch_rotate_append(a, head_dim, static_cast<cudaStream_t>(stream)) == cudaSuccess

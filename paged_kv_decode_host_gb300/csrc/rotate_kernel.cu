@@ -99,9 +99,20 @@ __device__ __forceinline__ uint4 pack(const float* y) {
   return make_uint4(pair_bf16(y[0], y[1]), pair_bf16(y[2], y[3]), pair_bf16(y[4], y[5]),
                     pair_bf16(y[6], y[7]));
 }
-__device__ __forceinline__ uint2 pack_e4m3(const float* y, float m) {
-  return make_uint2(pair_e4m3(y[0] * m, y[1] * m) | (pair_e4m3(y[2] * m, y[3] * m) << 16),
-                    pair_e4m3(y[4] * m, y[5] * m) | (pair_e4m3(y[6] * m, y[7] * m) << 16));
+// y / scale, rounded as the division is (times a rounded 1 / scale alone, a quotient
+// between two codes takes the other one): a product, and its rest by the same inverse,
+// after Markstein's theorem (IBM J. Res. Dev. 34, 1990).  The power of two that takes
+// the scale near 1 is exact wherever the quotient is a code's; one past them all may be
+// infinite, and has no rest.
+__device__ __forceinline__ float quotient(float y, const RotateArgs::Divisor& d) {
+  const float x = y * d.lift, q = x * d.inv;
+  return fabsf(q) < 1024.f ? fmaf(-fmaf(q, d.by, -x), d.inv, q) : q;   // (-0 stays -0)
+}
+__device__ __forceinline__ uint2 pack_e4m3(const float* y, const RotateArgs::Divisor& d) {
+  uint32_t two[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) two[e] = pair_e4m3(quotient(y[2 * e], d), quotient(y[2 * e + 1], d));
+  return make_uint2(two[0] | (two[1] << 16), two[2] | (two[3] << 16));
 }
 
 template <int D, bool kNorm, bool kPairs>
@@ -247,9 +258,9 @@ __global__ void __launch_bounds__(kMostWarps * 32, 8)
       if (h >= 2 * a.hkv || slot < 0) continue;
       uint8_t* dst = a.kv + slot + (is_k ? h * a.head_bytes : a.v_bytes + (h - a.hkv) * a.head_bytes);
       if (a.fp8) {
-        const float m = is_k ? a.k_mul : a.v_mul;
-        *reinterpret_cast<uint2*>(dst + ea) = pack_e4m3(y, m);
-        *reinterpret_cast<uint2*>(dst + eb) = pack_e4m3(y + 8, m);
+        const RotateArgs::Divisor div = is_k ? a.k_div : a.v_div;
+        *reinterpret_cast<uint2*>(dst + ea) = pack_e4m3(y, div);
+        *reinterpret_cast<uint2*>(dst + eb) = pack_e4m3(y + 8, div);
       } else {
         // (a value's bits as they are, a NaN's too)
         *reinterpret_cast<uint4*>(dst + 2 * ea) = is_k ? pack(y) : x[u].a;

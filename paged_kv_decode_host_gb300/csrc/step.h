@@ -31,7 +31,10 @@ struct RotateArgs {
   uint8_t* kv;
   int64_t page_bytes, v_bytes, token_bytes, head_bytes;   // strides in the cache
   int32_t num_pages, page_size, hq, hkv;
-  float k_mul, v_mul;              // 1 / scale of an e4m3 cache
+  // an e4m3 cache's scales: a power of two (lift), scale * lift in [0.5, 2) and its inverse
+  struct Divisor {
+    float lift, by, inv;
+  } k_div, v_div;
   int32_t fp8;
   int32_t* err;
   int32_t segments;                // blocks that share a token's heads (the launcher's)

@@ -273,3 +273,28 @@ def test_refusals():
     for kw in (dict(axes=[0] * 7), dict(axes=[4] * 8), dict(axes=[-1] * 8), dict(scale=float("inf"))):
         with pytest.raises(ValueError):
             pkd.RotaryPositions([1.0] * 8, **kw)
+
+
+@pytest.mark.parametrize("scale", [0.03, 1.0 / 90.0, 0.7, 3.0, 1e-6, 2.0 ** 20, 3e-39, 3.3e38])
+@pytest.mark.parametrize("norms", [None, torch.bfloat16])
+def test_e4m3_codes_of_every_value(scale, norms):
+    """Every bf16 value as a value, and as a key that is not turned: the code next to the fp32
+    quotient."""
+    c = Case(hq=1, hkv=8, kv="e4m3", old=(5,), new=(64,), rotary=0, norms=norms, layout="HND")
+    values = torch.arange(-2 ** 15, 2 ** 15, device="cuda").to(torch.int16).view(torch.bfloat16).view(64, 8, 128)
+    c.v = values
+    if norms is None:
+        c.k, c.k_scale = values.flip(0).contiguous(), scale
+    c.v_scale = scale
+    _, cache = c.run()
+    page = torch.from_numpy(c.indices).cuda().long()[c.places.long() // c.page]
+    got = cache.view(torch.uint8).transpose(2, 3)[page, :, c.places.long() % c.page]
+
+    def code(x):   # (numpy's: torch on the GPU multiplies by 1 / scale instead)
+        with np.errstate(all="ignore"):
+            y = np.clip(x.float().cpu().numpy() / np.float32(scale), np.float32(-448), np.float32(448))
+        return torch.from_numpy(y).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+
+    for at, x in ((1, values),) + (((0, c.k),) if norms is None else ()):
+        number = ~x.isnan()
+        assert torch.equal(got[:, at][number], code(x)[number]) and ((got[:, at][~number] & 0x7f) == 0x7f).all()
