@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -21,6 +22,25 @@ from . import (_NOT_HANDLED, FLAG_HND, FLAG_KV_FP8, FLAG_TREE, BatchDecodeWithPa
                _stream_ptr, _table_args, load, make_config, schedule_layout)
 
 MAX_AXES = 4
+
+
+def _turns(freq):
+    """freq radians per position as turns times 2^64, modulo 2^64, rounded to nearest: in
+    integers (a double's 53 bits would be off by up to 2^-56 turns a position)."""
+    bits = 160 + max(0, max(math.frexp(x)[1] for x in freq))
+
+    def arctan(n):   # of 1 / n, times 2^bits
+        total, power, k = 0, (1 << bits) // n, 1
+        while power:
+            total += power // k if k % 4 == 1 else -(power // k)
+            power //= n * n
+            k += 2
+        return total
+
+    pi = Fraction(16 * arctan(5) - 4 * arctan(239), 1 << bits)   # Machin's formula
+    return np.array([round(Fraction(x) * 2 ** 63 / pi) % 2 ** 64 for x in freq], dtype=np.uint64)
+
+
 _step_module = None   # the calls on tensors (module), False when not built
 
 
@@ -65,8 +85,7 @@ class RotaryPositions:
         if not math.isfinite(scale):
             raise ValueError("scale must be finite")
         self.num_axes, self.scale = max(axes) + 1, float(scale)
-        turns = np.array([int(round(x / (2 * math.pi) * 2.0 ** 64)) % 2 ** 64 for x in freq],
-                         dtype=np.uint64)
+        turns = _turns(freq)
         device = torch.device("cuda" if device is None else device)
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         self.axes = torch.tensor(axes, dtype=torch.int32, device=device)

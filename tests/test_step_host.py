@@ -1,5 +1,6 @@
 """Tree plans, masks, tables and refusals of the calls around a step with drafts, without a GPU."""
 import ctypes
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -254,3 +255,14 @@ def test_tree_calls_without_a_context(lib):
     assert lib.pkd_run_tree(None, None, 0, None, None, None, None, 0, None, None, 1.0, 0.0, 0, None) == INVALID
     assert lib.pkd_run_tree_scaled(None, None, 0, None, None, None, None, 0, None, None, 1.0, 0.0, 1.0, 1.0, 0,
                                    None) == INVALID
+
+
+@pytest.mark.parametrize("freq", [[500_000.0 ** (-i / 64) for i in range(64)], [10_000.0 ** (-i / 32) / 7 for i in range(32)],
+                                  [1.0, -3.7, 0.0, 5e-324, 1e20, -1e30, 2.0 ** -80, 123456.789]])
+def test_turns_are_rounded_once(freq):
+    """Turns per position times 2^64: the nearest integers, so that position p is off by at most p / 2."""
+    pi = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+    rope = pkd.RotaryPositions(freq, interleaved=True, device="cpu")
+    for x, got in zip(freq, rope.turns.numpy().view(np.uint64)):
+        off = (Fraction(x) * 2 ** 63 / pi - int(got)) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= Fraction(1, 2)
