@@ -551,6 +551,10 @@ int pkd_append_latent(const void *latent_new, int64_t latent_stride, const void 
                       const int32_t *last_page_len, int32_t batch, void *cache,
                       int32_t num_pages, int32_t page_size, int32_t *err, void *stream);
 
+/* Counts changes of the arguments of pkd_rotate_append_kv, pkd_run_tree_scaled and
+ * pkd_accept_kv: a binding that was compiled for others says so when it is loaded. */
+#define PKD_STEP_ABI 1
+
 /* New tokens' queries and keys normed per head and rotated by their positions,
  * keys and values written into their page slots, in one kernel.  For every
  * token and head of q and k, in fp32:

@@ -16,6 +16,8 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <cstring>
+
 #include "pkd.h"
 
 namespace {
@@ -260,10 +262,17 @@ PyObject* accept_kv(PyObject*, PyObject* const* a, Py_ssize_t count) try {
   return other();
 }
 
-// init(rotate_append_address, run_tree_address, accept_address)
+// init(abi, torch_version, rotate_append_address, run_tree_address, accept_address); ImportError
+// where the module was built for other entry points or another torch
 PyObject* init(PyObject*, PyObject* args) {
+  int abi;
+  const char* torch;
   unsigned long long r, t, c;
-  if (!PyArg_ParseTuple(args, "KKK", &r, &t, &c)) return nullptr;
+  if (!PyArg_ParseTuple(args, "isKKK", &abi, &torch, &r, &t, &c)) return nullptr;
+  if (abi != PKD_STEP_ABI || std::strcmp(torch, PKD_TORCH) != 0) {
+    PyErr_SetString(PyExc_ImportError, "_pkd_step was built for another libpkd or torch");
+    return nullptr;
+  }
   g_rotate = reinterpret_cast<decltype(g_rotate)>((uintptr_t)r);
   g_run_tree = reinterpret_cast<decltype(g_run_tree)>((uintptr_t)t);
   g_accept = reinterpret_cast<decltype(g_accept)>((uintptr_t)c);
@@ -271,7 +280,7 @@ PyObject* init(PyObject*, PyObject* args) {
 }
 
 PyMethodDef methods[] = {
-    {"init", init, METH_VARARGS, "init(rotate_append_address, run_tree_address, accept_address)"},
+    {"init", init, METH_VARARGS, "init(abi, torch_version, rotate_append_address, run_tree_address, accept_address)"},
     {"rotate_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&rotate_append)), METH_FASTCALL,
      "pkd_rotate_append_kv on tensors -> (status, q_out), or NotImplemented"},
     {"run_tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&run_tree)), METH_FASTCALL,

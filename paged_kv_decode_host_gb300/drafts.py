@@ -22,6 +22,7 @@ from . import (_NOT_HANDLED, FLAG_HND, FLAG_KV_FP8, FLAG_TREE, BatchDecodeWithPa
                _stream_ptr, _table_args, load, make_config, schedule_layout)
 
 MAX_AXES = 4
+STEP_ABI = 1   # PKD_STEP_ABI of pkd.h
 
 
 def _turns(freq):
@@ -49,13 +50,14 @@ def _step():
     global _step_module
     if _step_module is None:
         try:
-            import torch  # noqa: F401  (its libraries come first)
+            import torch   # (its libraries come first)
             from . import _pkd_step as m
             lib = load()
-            m.init(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-                lib.pkd_rotate_append_kv, lib.pkd_run_tree_scaled, lib.pkd_accept_kv)])
+            m.init(STEP_ABI, torch.__version__.split("+")[0],
+                   *[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                       lib.pkd_rotate_append_kv, lib.pkd_run_tree_scaled, lib.pkd_accept_kv)])
             _step_module = m
-        except ImportError:
+        except (ImportError, TypeError):   # (TypeError: the init of an older one)
             _step_module = False
     return _step_module or None
 
