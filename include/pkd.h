@@ -606,8 +606,8 @@ int pkd_rotate_append_kv(const void *q, int64_t q_token, int64_t q_head, void *q
  * negative entry ends the row).  With c_b = l_b - drafted[b], slot c_b + i takes
  * the K and V rows of slot c_b + accepted[b][i].  Slots behind the last one keep
  * what they hold, and the caller's next table ends there.
- *   kv       : HOST array of `layers` device pointers, all different, caches as
- *              for pkd_append_kv_ex
+ *   kv       : HOST array of `layers` device pointers, caches as for
+ *              pkd_append_kv_ex that do not overlap
  *   accepted : device int32 [batch][width], 0 <= width <= 1024
  *   drafted  : device int32 [batch]
  *   indptr [batch + 1], indices [num_indices], last_page_len [batch] : device

@@ -3,6 +3,7 @@
 // accept_kernel.cu).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "pkd_internal.h"
@@ -141,13 +142,22 @@ int pkd_accept_kv(int32_t layers, void* const* kv, const int32_t* accepted, int3
       (int64_t)head_dim * elem * num_kv_heads > (1 << 24))
     return PKD_E_INVALID_ARG;
   AcceptArgs a{};
+  uintptr_t order[kMaxAcceptLayers];
   for (int32_t l = 0; l < layers; ++l) {
     if (!kv[l] || !aligned(kv[l], 16)) return PKD_E_INVALID_ARG;
-    for (int32_t m = 0; m < l; ++m)   // two layers on one cache would race
-      if (kv[m] == kv[l]) return PKD_E_INVALID_ARG;
     a.kv[l] = kv[l];
+    order[l] = (uintptr_t)kv[l];
   }
+  std::sort(order, order + layers);
+  if (std::adjacent_find(order, order + layers) != order + layers) return PKD_E_INVALID_ARG;
   if (batch == 0 || width == 0) return PKD_OK;
+  const int64_t head = (int64_t)head_dim * elem;
+  a.v_bytes = (int64_t)page_size * num_kv_heads * head;
+  a.page_bytes = 2 * a.v_bytes;
+  // two layers in one place would race (and a pool past the address space wraps around)
+  if (a.page_bytes > ((int64_t)1 << 56) / num_pages) return PKD_E_INVALID_ARG;
+  for (int32_t l = 1; l < layers; ++l)
+    if (order[l] - order[l - 1] < (uintptr_t)(num_pages * a.page_bytes)) return PKD_E_INVALID_ARG;
   if (!accepted || !drafted || !indptr || !indices || !last_page_len || !aligned(accepted, 4) ||
       !aligned(drafted, 4) || !aligned(err, 4))
     return PKD_E_INVALID_ARG;
@@ -162,9 +172,6 @@ int pkd_accept_kv(int32_t layers, void* const* kv, const int32_t* accepted, int3
   a.num_pages = num_pages;
   a.page_size = page_size;
   const bool hnd = (flags & PKD_FLAG_HND) != 0;
-  const int64_t head = (int64_t)head_dim * elem;
-  a.v_bytes = (int64_t)page_size * num_kv_heads * head;
-  a.page_bytes = 2 * a.v_bytes;
   a.token_bytes = hnd ? head : head * num_kv_heads;
   a.head_bytes = hnd ? head * page_size : head;
   a.hkv = num_kv_heads;

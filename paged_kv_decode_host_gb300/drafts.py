@@ -447,7 +447,8 @@ def accept_kv(kv_caches, accepted, drafted, indptr, indices, last_page_len, *, e
     """Move every request's accepted drafts to the front of its drafted tokens,
     in place; all layers in one launch.
 
-    kv_caches: a list of 1 to 128 caches as for :func:`append_kv`, of one shape.
+    kv_caches: a list of 1 to 128 caches as for :func:`append_kv`, of one shape, which do
+    not overlap.
     drafted [batch] int32: that many tokens at a request's end are drafts.
     accepted [batch, width] int32 (width up to 1024): the drafts that stay, in
     increasing order (0-based; the first negative entry ends a row).  indptr /

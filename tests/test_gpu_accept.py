@@ -306,3 +306,18 @@ def test_two_steps_over_an_e4m3_cache():
         now, rows = held(b, ctx + len(paths[b])), list(range(ctx)) + [ctx + j for j in paths[b]]
         assert all(torch.equal(x, y[rows]) for x, y in zip(now, before[b]))
     step([53, 37], [1, 1], None)
+
+
+def test_caches_beside_one_another_and_overlapping():
+    c = Case(layers=4)
+    pool = torch.stack(c.kvs)          # the layers of one allocation, one behind the other
+    c.kvs = list(pool)
+    c.check()
+    c.kvs = [pool[2], pool[0], pool[3]]
+    c.check()
+    flat = pool.flatten(0, 1)
+    c.kvs = [flat[:c.pool], flat[c.pool - 1:2 * c.pool - 1]]
+    keep = flat.clone()
+    with pytest.raises(pkd.PkdError, match="INVALID"):
+        c.run()
+    assert torch.equal(flat, keep)

@@ -266,3 +266,13 @@ def test_turns_are_rounded_once(freq):
     for x, got in zip(freq, rope.turns.numpy().view(np.uint64)):
         off = (Fraction(x) * 2 ** 63 / pi - int(got)) % 2 ** 64
         assert min(off, 2 ** 64 - off) <= Fraction(1, 2)
+
+
+def test_accept_refuses_caches_that_overlap(lib):
+    """(4 pages of 16 tokens, 2 heads and 128 values: 65,536 bytes for K and V in bf16.)"""
+    size = 4 * 2 * 16 * 2 * 128 * 2
+    for kv in ([1 << 20, (1 << 20) + 16], [1 << 20, (1 << 20) + size - 16], [(1 << 20) + size // 2, 1 << 20],
+               [1 << 20, 1 << 22, (1 << 20) + size // 2, 1 << 23]):
+        assert accept_status(lib, layers=len(kv), kv=kv) == INVALID, kv
+    assert accept_status(lib, kv=[1 << 20, (1 << 20) + size // 2 - 16], flags=pkd.FLAG_KV_FP8) == INVALID
+    assert accept_status(lib, kv=[16, 1 << 40], pages=2 ** 31 - 1, page=2 ** 31 - 1, hkv=1 << 16) == INVALID
