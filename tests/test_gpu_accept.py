@@ -321,3 +321,56 @@ def test_caches_beside_one_another_and_overlapping():
     with pytest.raises(pkd.PkdError, match="INVALID"):
         c.run()
     assert torch.equal(flat, keep)
+
+
+@pytest.mark.parametrize("ctas", [0, 8])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_queued_directly_behind_a_tree_run(ctas, fp8):
+    """The tree kernel and its merge let the next launch start early: the moves and appends that follow
+    on the same cache, with nothing between them, touch none of it before the run has read it, nor each
+    other's rows.  With 8 CTAs nothing is split (the tree kernel itself comes before the moves) and most
+    of the GPU is free for what starts early."""
+    hq, hkv, D, page, n, batch = 32, 8, 128, 16, 24, 6
+    lens = [4000 + 37 * b for b in range(batch)]
+    indptr, indices, last, pool = table(lens, page)
+    q_indptr = (np.arange(batch + 1) * n).astype(np.int32)
+    g = torch.Generator("cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    parents = np.random.default_rng(3).integers(-1, np.tile(np.maximum(np.arange(n), 0), batch)).astype(np.int32)
+    mask, depths = (torch.from_numpy(x).cuda() for x in pkd.tree_mask(q_indptr, parents))
+    dec = pkd.BatchTreeDecodeWithPagedKVCache(hq, hkv, D, page, max_tokens=batch * n, max_num_pages=len(indices),
+                                              num_pages=pool, num_ctas=ctas, kv_dtype="e4m3" if fp8 else "bf16")
+    dec.plan(q_indptr, indptr, indices, last)
+    assert (dec.plan_info()["num_units"] == 0) == (ctas == 8)
+    start = rnd(pool, 2, page, hkv, D)
+    start = start.to(torch.float8_e4m3fn) if fp8 else start
+    kv = torch.empty_like(start)
+    tables = [torch.from_numpy(x).cuda() for x in (indptr, indices, last)]
+    accepted = torch.tensor([[1, 2, 5, 9, 10, 17, 20, 23]] * batch, dtype=torch.int32, device="cuda")
+    drafted = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    rope = pkd.RotaryPositions([10_000.0 ** (-i / 64) for i in range(64)])
+    q, both = rnd(batch * n, hq, D), rnd(batch * n, hq + 2 * hkv, D)
+    rows = torch.arange(batch, device="cuda", dtype=torch.int32).repeat_interleave(n)
+    places = torch.tensor([x - n + i for x in lens for i in range(n)], dtype=torch.int32, device="cuda")
+    # new tokens take the places behind the 8 that stay, and the last 4 of those
+    m = torch.arange(batch * n, device="cuda").view(batch, n)[:, 4:].reshape(-1)
+    both, rows, places = both[m], rows[m].contiguous(), places[m].contiguous()
+
+    def step(wait):
+        kv.view(torch.uint8).copy_(start.view(torch.uint8))
+        wait()
+        out, lse = dec.run(q, kv, mask=mask, depths=depths)
+        wait()
+        pkd.accept_kv([kv], accepted, drafted, *tables)
+        wait()
+        turned, _ = pkd.rotate_append_kv(both[:, :hq], both[:, hq:hq + hkv], both[:, hq + hkv:], rope, rows, places,
+                                         *tables, kv)
+        wait()
+        return out, lse, turned, kv.view(torch.uint8).clone()
+
+    want = step(torch.cuda.synchronize)
+    for _ in range(25):
+        got = step(lambda: None)
+        for x, y in zip(want, got):
+            assert torch.equal(x, y)
+    assert dec.device_error() == 0
