@@ -159,11 +159,15 @@ __device__ __forceinline__ uint64_t visible(const Row& r, int t0, int te) {
     uint64_t own = r.mask != nullptr ? mask_bits(r, j0)
                                      : low_bits(r.i + 1 - j0) & ~low_bits(-j0);
     own &= low_bits(r.drafts - j0);
-    if (r.window > 0 && r.depth >= r.window)   // (deeper than the window: rare)
-      for (uint64_t m = own; m != 0; m &= m - 1) {
-        const int c = __ffsll((long long)m) - 1;
-        if (r.depth - depth_of(r, j0 + c) >= r.window) own &= ~(1ull << c);
-      }
+    if (r.window > 0 && r.depth >= r.window) {
+      if (r.depths == nullptr)   // draft j stands j behind the context
+        own &= ~low_bits(r.depth - r.window + 1 - j0);
+      else   // (a tree deeper than the window: rare)
+        for (uint64_t m = own; m != 0; m &= m - 1) {
+          const int c = __ffsll((long long)m) - 1;
+          if (r.depth - depth_of(r, j0 + c) >= r.window) own &= ~(1ull << c);
+        }
+    }
     vis |= own;
   }
   return vis & low_bits(te - t0);

@@ -697,3 +697,10 @@ def test_scales_of_values_of_any_size(power, fp8):
     small, same = c.run()
     assert torch.equal(small.double(), out.double() * 2.0 ** power) and torch.equal(lse, same)
     assert out.double().abs().max() > 0.1 and c.dec.device_error() == 0
+
+
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 127, 128, 129, 300, 900])
+@pytest.mark.parametrize("causal", [False, True])
+def test_windows_within_long_pieces(window, causal):
+    # rows whose window ends among the query tokens themselves, chains and trees of which depths say nothing
+    Case(hq=4, hkv=2, lens=(900, 640, 70), drafts=(700, 640, 70), causal=causal, depths=False, window=window).check()
