@@ -781,7 +781,7 @@ int pkd_run_tree_scaled(pkd_ctx* ctx, const void* q, int32_t rows, const void* k
   if (launch_tree(a, ctx->n_cta, ctx->info.chunk_tokens, s) != cudaSuccess) return PKD_E_CUDA;
   // a captured launch must do for later plans, whose splits are not known yet
   if (ctx->info.num_units == 0 && cap_status == cudaStreamCaptureStatusNone) return PKD_OK;
-  MergeArgs m{};
+  TreeMergeArgs m{};
   m.sched = a.sched;
   m.o_part = a.o_part;
   m.l_part = a.l_part;

@@ -1470,25 +1470,4 @@ cudaError_t encode_kv_map(const void* kv, int32_t num_pages, int32_t page_size, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t encode_tree_kv_map(const void* kv, int32_t num_pages, int32_t page_size, int32_t hkv,
-                               bool hnd, CUtensorMap* map) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (encode == nullptr) return cudaErrorNotSupported;
-  if (kv == nullptr || (uintptr_t)kv % 16 != 0 || page_size % 16 != 0 || num_pages < 1 ||
-      hkv < 1 || hkv > kMaxKvHeads)
-    return cudaErrorInvalidValue;
-  const cuuint64_t head = (cuuint64_t)kHeadDim * 2, row = hkv * head, groups = page_size / 8;
-  const cuuint64_t dims[5] = {64, 8, hnd ? 2 : 2 * (cuuint64_t)hkv, hnd ? hkv * groups : groups,
-                              2 * (cuuint64_t)num_pages};
-  const cuuint64_t token = hnd ? head : row;
-  const cuuint64_t strides[4] = {token, 128, 8 * token, (cuuint64_t)page_size * row};
-  const cuuint32_t box[5] = {64, 8, 2, 2, 1};
-  const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(kv), dims,
-                            strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace pkd

@@ -45,16 +45,14 @@
 // stops, waits (bounded) for its copies and products, frees tensor memory
 // and returns.
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <math_constants.h>
 #include <stdint.h>
-
-#include <mutex>
 
 #include "latent.h"
 #include "pkd_internal.h"
 #include "prefix_tc_body.cuh"
 #include "sm103_ptx.cuh"
+#include "tensor_map.h"
 
 namespace pkd {
 namespace {
@@ -1018,21 +1016,6 @@ __global__ void __launch_bounds__(kAppendWarps * 32) latent_append_kernel(
 }
 static_assert(kLatentDim * 2 / 16 == 64 && kLatentRope * 2 / 16 <= 32, "two pieces per lane");
 
-// The driver's tensor-map encoder (null when it has none), looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return encode;
-}
-
 }  // namespace
 
 int latent_smem_bytes(int32_t heads) {
@@ -1091,7 +1074,7 @@ cudaError_t launch_latent(const LatentArgs& a, int grid, int merge_grid, cudaEve
 // tokens][128 bytes] with the 128-byte swizzle.
 cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page_size, int region,
                               CUtensorMap* map) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   if (cache == nullptr || (uintptr_t)cache % 16 != 0 || page_size % 16 != 0 || num_pages < 1)
     return cudaErrorInvalidValue;
@@ -1113,7 +1096,7 @@ cudaError_t encode_latent_map(const void* cache, int32_t num_pages, int32_t page
 // heads, every chunk, 1}, which lands as [chunk][head][128 bytes] with the
 // 128-byte swizzle; heads past the last read as zeros.
 cudaError_t encode_latent_q_map(const void* q, int32_t batch, int32_t heads, CUtensorMap* map) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   if (q == nullptr || (uintptr_t)q % 16 != 0 || batch < 1 || heads < 1) return cudaErrorInvalidValue;
   const cuuint64_t row = (cuuint64_t)kLatentRow * 2;

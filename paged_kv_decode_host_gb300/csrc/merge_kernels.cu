@@ -10,7 +10,10 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "pkd_internal.h"
+#include "tree.h"
 
 namespace pkd {
 namespace {
@@ -61,7 +64,8 @@ constexpr int kWarpSlots = 32;
 // kTree: the units are query tokens of a tree run, whose states may be empty
 // (lse -inf, out 0), all of a unit's too.
 template <int kBatch, int kThreads = kMergeThreads, bool kTree = false>
-__global__ void __launch_bounds__(kThreads) merge_partials_kernel(const MergeArgs a) {
+__global__ void __launch_bounds__(kThreads) merge_partials_kernel(
+    const std::conditional_t<kTree, TreeMergeArgs, MergeArgs> a) {
   static_assert(kThreads >= kHeadDim && kThreads % 32 == 0, "a thread per output dim");
   constexpr int kWarps = kThreads / 32;
   __shared__ float wm[kWarps];
@@ -293,7 +297,7 @@ cudaError_t launch_merge_partials(const MergeArgs& a, int grid, int32_t max_chun
   return cudaLaunchKernelEx(&cfg, merge_partials_kernel<1>, a);
 }
 
-cudaError_t launch_merge_tree(const MergeArgs& a, int grid, int32_t max_chunks,
+cudaError_t launch_merge_tree(const TreeMergeArgs& a, int grid, int32_t max_chunks,
                               cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

@@ -29,7 +29,7 @@ constexpr int kDefaultAlpha = 32;
 constexpr int kDefaultMinChunk = 256;
 constexpr int kMergeThreads = 256;
 
-// Schedule header words (first 32 int32 of the workspace; those behind the last named are 0).
+// Schedule header words (first 32 int32 of the workspace; 19..31 are 0).
 enum HeaderWord {
   H_MAGIC = 0, H_BATCH, H_HQ, H_HKV, H_D, H_P, H_NCTA, H_NITEMS, H_NUNITS,
   H_NSLOTS, H_CHUNK, H_ALPHA, H_NNZ, H_MAKESPAN, H_MINCHUNK, H_BLOCK,
@@ -39,10 +39,6 @@ enum HeaderWord {
   H_NPRE,        // cascade plans: CTAs [0, H_NPRE) run the shared-prefix items
   H_PCHUNK,      // cascade plans: the shared-prefix level's chunk (tokens)
   H_EPOCH,       // the plan's epoch (epoch_word); the upload writes the header last
-  H_REQUESTS,    // tree plans: requests (H_BATCH counts their query tokens)
-  H_CAUSAL,      //   1: every request's tokens are a chain
-  H_WINDOW,      //   the sliding window, 0 without
-  H_MAXQ,        //   the most query tokens of a request
   H_WORDS = 32
 };
 
@@ -219,11 +215,6 @@ struct MergeArgs {
   int64_t off_units, off_merge;
   int32_t hq;
   int32_t wait_epoch = 0;   // nonzero: read the schedule only after the decode grid completes
-  // Tree runs: rows of out and the most query tokens of a request that the
-  // run's masks cover; a plan beyond either is not merged.  Their states may be
-  // empty (lse -inf).
-  int32_t rows = 0;
-  int64_t most = 0;
 };
 
 // Kernel launchers (decode_kernel.cu / merge_kernels.cu).
@@ -256,11 +247,6 @@ cudaError_t launch_cascade(const DecodeKind& k, const CascadeArgs& a, int grid, 
 // kernel, which lays the halves of 64 tokens out as two 8 KB matrices).
 cudaError_t encode_kv_map(const void* kv, int32_t num_pages, int32_t page_size, int32_t hkv,
                           bool fp8, bool hnd, bool head_half_box, CUtensorMap* map);
-// The tree kernel's map of a bf16 cache: boxes of 16 tokens of one KV head as [2
-// groups of 8 tokens][half][8][128 bytes], so that both matrix products find a
-// fixed stride between groups (2 KB) and between halves (1 KB).
-cudaError_t encode_tree_kv_map(const void* kv, int32_t num_pages, int32_t page_size, int32_t hkv,
-                               bool hnd, CUtensorMap* map);
 // Encode the dense kernel's query map of q [batch][Hq][D] bf16.
 cudaError_t encode_q_map(const void* q, int32_t batch, int32_t hq, int32_t hkv,
                          CUtensorMap* map);
@@ -276,9 +262,6 @@ constexpr int32_t kLongUnit = 64;
 // at most 32 slots load all their slots in one batch per warp (4 each).
 cudaError_t launch_merge_partials(const MergeArgs& a, int grid, int32_t max_chunks,
                                   cudaStream_t stream, bool batch_short = false);
-// The merge of a tree run.
-cudaError_t launch_merge_tree(const MergeArgs& a, int grid, int32_t max_chunks,
-                              cudaStream_t stream);
 cudaError_t launch_merge_states(const void* v_a, const float* s_a, const void* v_b,
                                 const float* s_b, void* v_out, float* s_out,
                                 int64_t rows, int head_dim, cudaStream_t stream);

@@ -7,7 +7,18 @@
 #include <cuda.h>
 #include <cuda_runtime_api.h>
 
+#include "pkd_internal.h"
+
 namespace pkd {
+
+// Header words of tree plans, behind those of all plans (the rest are 0).
+enum TreeHeaderWord {
+  H_REQUESTS = H_EPOCH + 1,   // requests (H_BATCH counts their query tokens)
+  H_CAUSAL,                   // 1: every request's tokens are a chain
+  H_WINDOW,                   // the sliding window, 0 without
+  H_MAXQ,                     // the most query tokens of a request
+};
+static_assert(H_MAXQ < H_WORDS, "header words");
 
 constexpr int kTreeRows = 128;       // query rows of a tile: 128 / g tokens x g heads of a KV head
 constexpr int kTreeRound = 128;      // tokens per round of the kernel; plans cut at multiples of it
@@ -59,6 +70,21 @@ struct TreeArgs {
   CUtensorMap kv_map;       // boxes of 16 tokens of a KV head: [2 x 8 tokens][half][8][128 B]
   CUtensorMap q_map;        // boxes of a KV head's 128 query rows and one half
 };
+
+// The merge of a tree run, whose states may be empty (lse -inf).  A plan of more
+// query tokens than out has rows, or of more in a request than the run's masks
+// cover, is not merged.
+struct TreeMergeArgs : MergeArgs {
+  int32_t rows = 0;
+  int64_t most = 0;
+};
+cudaError_t launch_merge_tree(const TreeMergeArgs& a, int grid, int32_t max_chunks, cudaStream_t stream);
+
+// The map of a bf16 cache: boxes of 16 tokens of one KV head as [2 groups of 8
+// tokens][half][8][128 bytes], so that both matrix products find a fixed stride
+// between groups (2 KB) and between halves (1 KB).
+cudaError_t encode_tree_kv_map(const void* kv, int32_t num_pages, int32_t page_size, int32_t hkv,
+                               bool hnd, CUtensorMap* map);
 
 int tree_smem_bytes();
 cudaError_t tree_prepare(bool fp8);

@@ -58,6 +58,7 @@
 
 #include "plan_layout.h"
 #include "prefix_tc_body.cuh"
+#include "tensor_map.h"
 #include "tree.h"
 
 namespace pkd {
@@ -368,7 +369,6 @@ struct Span {
   int reach;              // rounds that start below it need the window's mask in some row of the warp
   float slope2;           // log2(e) * the head's slope
   bool steep;             // some row's slope is too steep for the estimate of 32 biased scores' largest
-  bool valid;             // a query row
 };
 
 // The largest of 32 biased scores is taken as the largest score's plus the
@@ -1028,7 +1028,6 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTcThreads, 1) tree_kerne
       if (window > 0) sp.reach = __reduce_max_sync(kFull, sp.reach);
       sp.slope2 = kSlopes && valid ? a.slopes[hq] * kLog2e : 0.f;
       sp.steep = kSlopes && __any_sync(kFull, fabsf(sp.slope2) > kSteepest);
-      sp.valid = valid;
       // Capped scores lie between -cap and cap: with the base 0 no weight or sum
       // leaves fp32's (and bf16's) range, and the largest need not be known.  Not
       // for rows that see few tokens: with their largest as the base the weights
@@ -1285,6 +1284,27 @@ const void* kernel_of(bool cap, bool slopes, bool halves) {
 }
 
 }  // namespace
+
+cudaError_t encode_tree_kv_map(const void* kv, int32_t num_pages, int32_t page_size, int32_t hkv,
+                               bool hnd, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  if (kv == nullptr || (uintptr_t)kv % 16 != 0 || page_size % 16 != 0 || num_pages < 1 ||
+      hkv < 1 || hkv > kMaxKvHeads)
+    return cudaErrorInvalidValue;
+  const cuuint64_t head = (cuuint64_t)kHeadDim * 2, row = hkv * head, groups = page_size / 8;
+  const cuuint64_t dims[5] = {64, 8, hnd ? 2 : 2 * (cuuint64_t)hkv, hnd ? hkv * groups : groups,
+                              2 * (cuuint64_t)num_pages};
+  const cuuint64_t token = hnd ? head : row;
+  const cuuint64_t strides[4] = {token, 128, 8 * token, (cuuint64_t)page_size * row};
+  const cuuint32_t box[5] = {64, 8, 2, 2, 1};
+  const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(kv), dims,
+                            strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 int tree_smem_bytes() { return kSmemBytes; }
 
