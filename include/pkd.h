@@ -354,7 +354,8 @@ int pkd_plan_tree(pkd_ctx *ctx, const int32_t *q_indptr, const int32_t *indptr,
  *                behind those are not written
  *   kv         : device bf16 (PKD_FLAG_KV_FP8: E4M3) [num_pages][2][P][Hkv][D]
  *                (PKD_FLAG_HND: [2][Hkv][P][D])
- *   out, lse   : device bf16 [rows][Hq][D], 32-byte aligned; device fp32 [rows][Hq] or NULL
+ *   out, lse   : device bf16 [rows][Hq][D], 32-byte aligned, not overlapping q or kv; device
+ *                fp32 [rows][Hq] or NULL
  *   mask       : device uint32 [rows][mask_words], mask_words at least the most
  *                n_b / 32 rounded up; NULL in a causal plan
  *   depths     : device int32 [rows], d_i of every query token (below 0 counts
@@ -367,8 +368,8 @@ int pkd_plan_tree(pkd_ctx *ctx, const int32_t *q_indptr, const int32_t *indptr,
  * stream or an event.  A call that the caller captured replays under later
  * plans that its rows and mask_words fit; under another it does no work and
  * ORs PKD_DEV_ERR_BOUNDS into the device error word.  The same bits every run.
- * Errors: as pkd_run; INVALID_ARG also for rows or mask_words below the plan's
- * and a mask or depths given to a causal plan. */
+ * Errors: as pkd_run; INVALID_ARG also for rows or mask_words below the plan's,
+ * out over q, and a mask or depths given to a causal plan. */
 int pkd_run_tree(pkd_ctx *ctx, const void *q, int32_t rows, const void *kv, void *out, float *lse,
                  const uint32_t *mask, int32_t mask_words, const int32_t *depths,
                  const float *slopes, float scale, float score_cap, uint64_t expect_epoch,

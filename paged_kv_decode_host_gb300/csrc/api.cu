@@ -717,6 +717,11 @@ int pkd_run_tree_scaled(pkd_ctx* ctx, const void* q, int32_t rows, const void* k
   if (given && (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 32) || !aligned(lse, 4) ||
                 !aligned(mask, 4) || !aligned(depths, 4) || !aligned(slopes, 4)))
     return PKD_E_INVALID_ARG;
+  // (rows that are summed again read their queries after others' results are written)
+  const uintptr_t q_at = (uintptr_t)q, out_at = (uintptr_t)out;
+  if (given && (q_at > out_at ? q_at - out_at : out_at - q_at) <
+                   (uintptr_t)rows * (uintptr_t)ctx->cfg.num_qo_heads * kHeadDim * 2)
+    return PKD_E_INVALID_ARG;
   // (also where this plan has no query tokens: a captured launch runs under
   // later ones.  Without tensors it does for none that has any.)
   if (!given) rows = 0;

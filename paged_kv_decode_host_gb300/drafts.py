@@ -370,6 +370,7 @@ class BatchTreeDecodeWithPagedKVCache(BatchDecodeWithPagedKVCache):
         2^96): scores become score_cap * tanh(score / score_cap).  slopes:
         float32 [Hq], then -= slope * (position of the query - position of the
         key).
+        out: bf16, like q, by default a new tensor; not on q's memory.
         k_scale, v_scale: the attended key is k_scale * K and the value v_scale *
         V (an E4M3 cache needs them).
         A query that sees nothing gets 0 and an lse of -inf."""

@@ -704,3 +704,17 @@ def test_scales_of_values_of_any_size(power, fp8):
 def test_windows_within_long_pieces(window, causal):
     # rows whose window ends among the query tokens themselves, chains and trees of which depths say nothing
     Case(hq=4, hkv=2, lens=(900, 640, 70), drafts=(700, 640, 70), causal=causal, depths=False, window=window).check()
+
+
+def test_results_on_the_queries_are_refused():
+    # (a row that is summed again would read the results of its other dims as its query)
+    c = Case(lens=(70, 40), drafts=(5, 3))
+    both = torch.zeros(16, 8, D, dtype=torch.bfloat16, device="cuda")
+    both[:8] = c.q
+    want, lse = c.run()
+    got, _ = c.dec.run(both[:8], c.kv, mask=c.mask, depths=c.depths, out=both[8:])   # (beside one another)
+    assert torch.equal(got, want)
+    for q, out in ((both[:8], both[:8]), (both[:8], both[1:9]), (both[8:], both[7:15])):
+        with pytest.raises(pkd.PkdError, match="INVALID"):
+            c.dec.run(q, c.kv, mask=c.mask, depths=c.depths, out=out)
+    assert c.dec.device_error() == 0
