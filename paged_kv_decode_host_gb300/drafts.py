@@ -12,8 +12,8 @@ ones moved into place.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
-from fractions import Fraction
 
 import numpy as np
 
@@ -25,12 +25,10 @@ MAX_AXES = 4
 STEP_ABI = 1   # PKD_STEP_ABI of pkd.h
 
 
-def _turns(freq):
-    """freq radians per position as turns times 2^64, modulo 2^64, rounded to nearest: in
-    integers (a double's 53 bits would be off by up to 2^-56 turns a position)."""
-    bits = 160 + max(0, max(math.frexp(x)[1] for x in freq))
-
-    def arctan(n):   # of 1 / n, times 2^bits
+@functools.lru_cache(maxsize=8)
+def _pi(bits):
+    """pi times 2^bits, by Machin's formula."""
+    def arctan(n):   # of 1 / n
         total, power, k = 0, (1 << bits) // n, 1
         while power:
             total += power // k if k % 4 == 1 else -(power // k)
@@ -38,8 +36,19 @@ def _turns(freq):
             k += 2
         return total
 
-    pi = Fraction(16 * arctan(5) - 4 * arctan(239), 1 << bits)   # Machin's formula
-    return np.array([round(Fraction(x) * 2 ** 63 / pi) % 2 ** 64 for x in freq], dtype=np.uint64)
+    return 16 * arctan(5) - 4 * arctan(239)
+
+
+def _turns(freq):
+    """freq radians per position as turns times 2^64, modulo 2^64, rounded to nearest: in
+    integers (a double's 53 bits would be off by up to 2^-56 turns a position)."""
+    bits = 160 + max(0, max(math.frexp(x)[1] for x in freq))
+    pi, turns = _pi(bits), []
+    for x in freq:
+        over, under = x.as_integer_ratio()   # x / (2 pi) * 2^64 = x 2^(63 + bits) / pi
+        under *= 2 * pi
+        turns.append(((over << (64 + bits)) + (under >> 1)) // under % 2 ** 64)
+    return np.array(turns, dtype=np.uint64)
 
 
 _step_module = None   # the calls on tensors (module), False when not built
