@@ -11,9 +11,9 @@
 // walks the accepted tokens, kAhead loads ahead of their stores, so nothing but
 // its own column is ever at stake and no barrier is needed.  The slots are
 // looked up once per block.  What bounds it is the chain of look-ups before the
-// first row (about 3 us), then memory: 64 requests x 32 layers, 85 MB moved, 16.4
-// us, 5.2 TB/s; 2.7 us for one request.  Two and four layers a block took 16.4 and
-// 17.1 (3.2 and 4.3 for one request), 128 and 512 threads 16.9 and 22.2, 4 and 16
+// first row (about 3 us), then memory: 64 requests x 32 layers, 85 MB read and
+// written, 16.0 us, 5.3 TB/s (6.5 behind the look-ups); 2.7 us for one request.  Two
+// and four layers a block took 16.4 and 17.1 (3.2 and 4.3 for one request), 128 and 512 threads 16.9 and 22.2, 4 and 16
 // loads ahead 17.7 and 23.0; loads and stores that leave no line behind gave 0.6.
 #include <cuda_runtime.h>
 #include <stdint.h>

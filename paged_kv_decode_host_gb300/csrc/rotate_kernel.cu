@@ -9,10 +9,10 @@
 // Queries go to q_out (bf16), keys and values to the cache (bf16, or e4m3 of
 // x / k_scale and x / v_scale, saturated), each rounded once, from fp32.
 //
-// Angles: a frequency is held as turns per position times 2^64, so p times it
-// in 64-bit integers is the angle modulo one turn, off by at most p 2^-65
-// turns, at any position and sign; its upper 32 bits become the fraction of a
-// turn.  Sine and cosine of an angle in [-pi, pi] are the hardware's, absolute
+// Angles: a frequency is held as turns per position times 2^64, rounded to
+// nearest, so p times it in 64-bit integers is the angle modulo one turn, off by
+// at most p 2^-65 turns, at any position and sign; its upper 32 bits become the
+// fraction of a turn.  Sine and cosine of an angle in [-pi, pi] are the hardware's, absolute
 // error under 2^-20: a result is then rounded to 2^-9 of itself or coarser.
 //
 // The work is moving bytes (24 KB a token of 32 + 2 x 8 heads).  A head is D /

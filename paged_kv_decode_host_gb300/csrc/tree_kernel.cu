@@ -33,13 +33,16 @@
 //  * distances are subtracted as whole numbers before they meet the slope;
 //  * P is rounded to bf16 for the product (V's type, which the tensor cores
 //    want for both); the row's sum, and with it the lse, is that of the weights
-//    before it.  Sums, bases and states between parts are fp32;
+//    before it.  Beside the output's own rounding that makes errors up to 1.41
+//    times those of an fp32 P (measured 0.0019 to 0.0024 against 0.0017); a second
+//    product with the rest of P would want 128 more columns of tensor memory, whose
+//    512 are taken.  Sums, bases and states between parts are fp32;
 //  * lane quadrants without a query row (fewer than 97 rows) only keep the
 //    barriers' count.
 // What bounds it: with few rows per KV head memory (64 ragged requests up to 8,192
-// tokens x 16 drafts, 32 heads on 8: 1.06 GB in 160 us, 6.6 TB/s); with full tiles
+// tokens x 16 drafts, 32 heads on 8: 1.06 GB in 157 to 160 us, 6.6 TB/s); with full tiles
 // the round, about 1,750 cycles for 1,024 of tensor products (16 requests x 61 drafts
-// of 64 heads: 155 GFLOP in 123 us, 1.26 PFLOP/s; 141 in a long row of calls, where
+// of 64 heads: 155 GFLOP in 123 us, 1.26 PFLOP/s; 140 in a long row of calls, where
 // the power limit takes the clock from 2,070 to 1,680 MHz), in which the tensor cores
 // wait for the softmax; a capped score's polynomial adds 700.  On the way there: one
 // copy instead of two per 16 tokens 159 -> 141 us; descriptors stepped by constants,
@@ -49,7 +52,7 @@
 // under the last base before the round's largest score is known (they mend too
 // often what they save); releasing S before its scores are capped.
 // Every wait is bounded, as in the dense shared-prefix role (prefix_tc_body.cuh),
-// whose instructions and barriers these are.
+// whose instructions and barriers these are (but see slow_wait).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -534,7 +537,7 @@ constexpr int kStreamRounds = 4;
 // of two rounds: the same 192 KB.
 constexpr int kNarrowBytes = kRoundTok * kHeadDim;   // K or V of a round
 // Three warps widen K, three V: the producer and two of a fourth warpgroup (64 ragged
-// requests x 16 drafts 324 us with the producers alone, 175 so; 159 over bf16, 145 if
+// requests x 16 drafts 324 us with the producers alone, 175 so; 157 over bf16, 145 if
 // nothing were widened).  128 registers each then, which spills a few words.
 constexpr int kWideners = 3;
 constexpr int kThreadsFp8 = kTcThreads + 128;

@@ -73,7 +73,8 @@ def _step():
 
 class RotaryPositions:
     """The frequencies of a model's rotary positions, kept on the device as turns
-    per position in 64-bit integers (exact modulo one turn at any position).
+    per position, rounded to 64 bits behind the point (the product with a position is
+    exact modulo one turn: position p is off by at most p * 2^-65 turns).
 
     inv_freq: rotary_dim / 2 angles per position (radians), e.g. theta ** (-2 i /
     rotary_dim), with whatever scaling the model applies.  interleaved: pair i is
