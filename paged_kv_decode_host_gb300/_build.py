@@ -53,7 +53,7 @@ def _torch_dir():
 
 def _torch_version():
     try:
-        return importlib.metadata.version("torch").split("+")[0]
+        return importlib.metadata.version("torch")
     except importlib.metadata.PackageNotFoundError:
         return ""
 
@@ -79,7 +79,7 @@ def _step_command():
         return None
     dirs = [INCLUDE, inc, os.path.join(torch_dir, "include"), cuda]
     return [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", *[f"-I{d}" for d in dirs],
-            f'-DPKD_TORCH="{_torch_version()}"', os.path.join(CSRC, "pystep.cpp"),
+            f'-DPKD_TORCH="{_torch_version().split("+")[0]}"', os.path.join(CSRC, "pystep.cpp"),
             "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
             "-lc10_cuda"]
 
@@ -90,10 +90,10 @@ def _optional():
     for path, command in ((PYPLAN, _plan_command()), (PYSTEP, _step_command())):
         if command is None:
             continue
-        h = hashlib.sha256("\0".join([*command, sys.version, platform.machine()]).encode())
-        for f in (os.path.join(CSRC, "pyplan.c"), os.path.join(CSRC, "pystep.cpp"),
-                  os.path.join(INCLUDE, "pkd.h")):
-            with open(f, "rb") as src:
+        # (not where compilers and headers lie: another shell's PATH is no reason to build anew)
+        h = hashlib.sha256("\0".join([sys.version, platform.machine(), _torch_version()]).encode())
+        for f in ("csrc/pyplan.c", "csrc/pystep.cpp", "../include/pkd.h"):
+            with open(os.path.join(HERE, f), "rb") as src:
                 h.update(src.read())
         yield path, command, os.path.join(BUILD, os.path.basename(path) + ".key"), h.hexdigest()
 
